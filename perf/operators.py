@@ -263,7 +263,7 @@ def prepare(case, seed):
             s["ws"] = rkv.accum_rows_workspace(B, H * G, H, c["T"], pages, P, DEV)
         elif c["op"] == "evict":
             s["dst_cache"] = _handle(rkv, s["dst"], B, H, P, s["dst"]["pages"])
-            s["ws"] = rkv.evict_workspace(B, H, pages, P, DEV, in_place=False)
+            s["ws"] = rkv.evict_workspace(B, H, c["keep"], DEV, in_place=False)
     return s
 
 
