@@ -59,9 +59,11 @@ typedef enum {
 #define RKV_DEVERR_CAPACITY  0x2  /* seq_len (+ appended tokens) beyond max_pages * page_size */
 #define RKV_DEVERR_TIMEOUT   0x4  /* a bounded wait on an mbarrier ran out */
 #define RKV_DEVERR_SEQ_LEN   0x8  /* device seq_len differs from the held_len the host passed */
+#define RKV_DEVERR_TREE      0x10 /* a tree_len, path_len, row_len or node id out of range */
 
 #define RKV_HEAD_DIM 128
 #define RKV_MAX_BATCH 256
+#define RKV_MAX_TREE 256
 
 /* Result of the adaptive ratio split. */
 typedef struct {
@@ -369,6 +371,129 @@ rkv_status rkv_decode_sparq(const rkv_cache* cache, const rkv_bf16* q, int32_t H
  * a [B*Hkv] int32 record of the positions copied (256-byte padded), then per (b, g)
  * a [128][max_pages * page_size] bf16 block. */
 size_t rkv_sparq_keys_size(int32_t B, int32_t Hkv, int32_t max_pages, int32_t page_size);
+
+/* Bytes of workspace rkv_tree_attention needs. */
+size_t rkv_tree_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t max_pages,
+                               int32_t page_size);
+
+/*
+ * Attention of a tree of drafted tokens over the cache (speculative decoding's
+ * verification): every cached token and, through the mask, the drafted nodes a node
+ * descends from.  Per sequence b, node t < tree_len[b] and query head h of KV head g:
+ *   z_j   = scale * q[b][h][t] . k_j over the n = seq_len[b] cached tokens and the
+ *           nodes j < tree_len[b] whose bit j of row t is set (a node that is to see
+ *           itself sets its own bit);
+ *   out   = sum_j exp(z_j) v_j / sum_j exp(z_j),  lse = log sum_j exp(z_j).
+ * A row that sees nothing (an empty cache and an empty mask row) gets out = 0 and
+ * lse = -inf.  Rows t >= tree_len[b] of out and lse are left as they were.  The cache is
+ * read only: nothing is appended (rkv_tree_commit does that for the accepted path).
+ *   q         : device [B][Hq][T][128] bf16; 1 <= T <= RKV_MAX_TREE.
+ *   k_tree, v_tree : device [B][Hkv][T][128] bf16, the nodes' keys and values; rows
+ *               from tree_len[b] on may hold anything, the others must be finite.
+ *   tree_mask : device [B][T][ceil(T / 32)] uint32, bit j % 32 of word j / 32 of row t:
+ *               node t sees node j.  Any mask is allowed; bits j >= tree_len[b] are
+ *               ignored.
+ *   tree_len  : device [B] int32 in [0, T], or NULL for T everywhere.  A value outside
+ *               sets RKV_DEVERR_TREE and counts as 0.
+ *   out       : device [B][Hq][T][128] bf16.   lse : device [B][Hq][T] fp32 or NULL.
+ * Logits, maxima, sums and the output's accumulation are fp32; the softmax weights enter
+ * the product with V as bf16.  seq_len and tree_len are read on the device, so a captured
+ * call can be replayed as the cache grows.  Calls whose work may overlap need workspaces
+ * of their own.
+ */
+rkv_status rkv_tree_attention(const rkv_cache* cache, const rkv_bf16* q, const rkv_bf16* k_tree,
+                              const rkv_bf16* v_tree, const uint32_t* tree_mask, int32_t Hq, int32_t T,
+                              const int32_t* tree_len, float scale, rkv_bf16* out, float* lse,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The accepted path of a drafted tree joins the cache: for each sequence the keys and
+ * values of nodes path[b][0 .. path_len[b]) are appended in that order at positions
+ * seq_len[b], ..., the touched pages' Kmax/Kmin fold them in, and seq_len[b] +=
+ * path_len[b].  The same as gathering those rows and calling rkv_append_page_summary,
+ * with a count per sequence that only the device knows.  A path_len outside [0,
+ * path_stride] or a node outside [0, T) sets RKV_DEVERR_TREE, a sequence that would
+ * outgrow its pages RKV_DEVERR_CAPACITY; that sequence is left unchanged.
+ *   k_tree, v_tree : device [B][Hkv][T][128] bf16.
+ *   path      : device [B][path_stride] int32.    path_len : device [B] int32.
+ */
+rkv_status rkv_tree_commit(const rkv_cache* cache, const rkv_bf16* k_tree, const rkv_bf16* v_tree, int32_t T,
+                           const int32_t* path, int32_t path_stride, const int32_t* path_len, void* stream);
+
+/* Bytes of workspace rkv_decode_accum needs. */
+size_t rkv_accum_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_pages, int32_t page_size);
+
+/*
+ * One-token attention over the whole cache that keeps count of every position's weight.
+ * Per sequence b, KV head g and head h of its group, with n = seq_len[b]:
+ *   p_h,t = exp(scale * q_h . k_t - lse_h),  lse_h = log sum_{t < n} exp(scale * q_h . k_t)
+ *   out_h = sum_t p_h,t v_t,   acc[b][g][t] += sum_h p_h,t   for t < n.
+ * n = 0 gives out = 0, lse = -inf and leaves acc.  No append: call
+ * rkv_append_page_summary (or rkv_tree_commit) first.
+ *   q   : device [B][Hq][128] bf16.    out : device [B][Hq][128] bf16.
+ *   lse : device [B][Hq] fp32 or NULL.
+ *   acc : device [B][Hkv][acc_stride] fp32, acc_stride >= max_pages * page_size; entry t
+ *         belongs to cache position t.  Zero it when the cache is empty: appended tokens
+ *         then start at zero, and rkv_evict_accum keeps it so.
+ * Precision as rkv_tree_attention; every acc entry has one writer, in a fixed order.
+ */
+rkv_status rkv_decode_accum(const rkv_cache* cache, const rkv_bf16* q, int32_t Hq, float scale, rkv_bf16* out,
+                            float* lse, float* acc, int32_t acc_stride, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace rkv_accum_rows needs. */
+size_t rkv_accum_rows_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t max_pages,
+                                     int32_t page_size);
+
+/*
+ * The weights of query rows whose attention is already done (a prompt's, a chunk's, an
+ * accepted path's), added to the same sums.  The m = row_len[b] rows are the cache's last
+ * m positions, row i lying at position n - m + i and seeing t <= n - m + i:
+ *   acc[b][g][t] += sum over heads h of the group, rows i with t <= n - m + i of
+ *                   exp(scale * q_h,i . k_t - lse_h,i).
+ * Row i is row i of q and lse, or row row_ids[b][i] (the nodes of an accepted path).
+ * Reads K only.
+ *   q       : device [B][Hq][T][128] bf16, 1 <= T <= 2^20.
+ *   lse     : device [B][Hq][T] fp32, natural log, as the attention calls return it; a row
+ *             of -inf weighs nothing.
+ *   row_ids : device [B][ids_stride] int32 in [0, T), or NULL; an id outside sets
+ *             RKV_DEVERR_TREE and its row weighs nothing.
+ *   row_len : device [B] int32 in [0, min(n, T or ids_stride)], or NULL for T (ids_stride
+ *             with row_ids) everywhere; a value outside sets RKV_DEVERR_TREE and the
+ *             sequence is skipped.
+ *   acc     : as rkv_decode_accum's.
+ */
+rkv_status rkv_accum_rows(const rkv_cache* cache, const rkv_bf16* q, const float* lse, int32_t Hq, int32_t T,
+                          const int32_t* row_len, const int32_t* row_ids, int32_t ids_stride, float scale,
+                          float* acc, int32_t acc_stride, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* Bytes of workspace rkv_evict_accum needs; max_keep: the largest keep[b]; in_place:
+ * whether the call has no separate destination (nonzero). */
+size_t rkv_evict_workspace_size(int32_t B, int32_t Hkv, int32_t max_keep, int32_t in_place);
+
+/*
+ * Cuts the cache to its heaviest and its latest tokens.  Per sequence b and KV head g,
+ * with n = seq_len[b]: when n <= keep[b] everything is kept, else the last `recent`
+ * positions and, of the others, the keep[b] - recent of largest acc (ties: lower
+ * position; a NaN counts as the largest).  The kept rows of K and V move to positions
+ * 0 .. min(n, keep[b]) in their order, with their acc entries; the summaries are rebuilt,
+ * acc behind them is zeroed up to its stride, and seq_len[b] = min(n, keep[b]).
+ *   keep     : host [B], 1 <= keep[b] <= the destination's capacity.
+ *   recent   : 0 <= recent <= every keep[b].
+ *   kept_idx : device [B][Hkv][kept_stride >= max keep] int32, receives the kept
+ *              positions, ascending, in the first min(n, keep[b]) entries.
+ *   dst, dst_acc : the destination cache and its sums, or NULL for both: in place.  A
+ *              destination has the source's B, Hkv and page_size, its pages are none of
+ *              the source's, and dst_acc is not acc; the source is then left as it was.
+ *              In place, no page may belong to two sequences.
+ * Caches of more than 393216 tokens per sequence (max_pages * page_size) return
+ * RKV_ERR_UNSUPPORTED.
+ */
+rkv_status rkv_evict_accum(const rkv_cache* cache, float* acc, int32_t acc_stride, const int32_t* keep,
+                           int32_t recent, int32_t* kept_idx, int32_t kept_stride, const rkv_cache* dst,
+                           float* dst_acc, int32_t dst_acc_stride, void* workspace, size_t workspace_bytes,
+                           void* stream);
 
 /*
  * Exact-TopK recall of a page selection: a diagnostic, not a step of the method.

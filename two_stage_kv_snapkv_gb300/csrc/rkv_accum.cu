@@ -1,0 +1,559 @@
+// Accumulated attention weights of the cached tokens, and the eviction by them.
+//
+//   accum_rows   acc_t += sum over the group's heads and the given rows i of
+//                [t <= n - m + i] exp(scale q_i . k_t - lse_i): the m rows are the
+//                cache's last m positions, lse_i what their attention left behind.
+//   evict        keeps, per (sequence, KV head), the `recent` last tokens and the
+//                heaviest of the others, in order, in this or another cache.
+#include "rkv_flat.cuh"
+#include "rkv_internal.h"
+#include "rkv_select.cuh"
+
+namespace rkv {
+namespace {
+
+// ---------------------------------------------------------------------------
+// accum_rows: transposed logits, keys as the MMA's M and query rows as its N, so that a
+// key's sum over the rows is a private loop and a shuffle over four lanes.  Only K is
+// read, 4 KB for a 16-key chunk, and every position has one writer: no atomics, the
+// same sums in the same order every time.
+constexpr int kRwKeys = 16;
+constexpr int kRwWarps = 8;
+constexpr int kRwThreads = kRwWarps * 32;
+constexpr int kRwStages = 4;
+constexpr int kRwStageBytes = 4096;
+constexpr int kRwBlock = 64;  // query rows staged at a time
+constexpr int kRwSmem = 1024 + kRwWarps * kRwStages * kRwStageBytes + kRwBlock * 256;
+
+struct RowsParams {
+  CUtensorMap tmk;
+  const rkv_bf16* q;   // [B][Hq][T][128]
+  const float* lse;    // [B][Hq][T]
+  const int32_t* row_len;
+  const int32_t* row_ids;
+  const int32_t* page_table;
+  const int32_t* seq_len;
+  int32_t* err;
+  float* acc;
+  int B, Hq, Hkv, G, gshift, T, ids_stride, P, pshift, max_pages, num_phys, acc_stride, N;
+  float scale_log2;
+};
+
+// Rows of sequence b that are taken (0 when the count or the length is not usable).
+__device__ __forceinline__ int rows_of(const RowsParams& p, int b, int n) {
+  const int most = p.row_ids ? p.ids_stride : p.T;
+  const int m = p.row_len ? p.row_len[b] : most;
+  if (m < 0 || m > most || m > n) {
+    flag_error(p.err, RKV_DEVERR_TREE);
+    return 0;
+  }
+  return m;
+}
+__device__ __forceinline__ int rows_cache_len(const RowsParams& p, int b) {
+  const int n = p.seq_len[b];
+  if (n < 0 || n > p.max_pages * p.P) {
+    flag_error(p.err, RKV_DEVERR_CAPACITY);
+    return 0;
+  }
+  return n;
+}
+
+__global__ void __launch_bounds__(kRwThreads, 1) accum_rows_kernel(const __grid_constant__ RowsParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ FlatTable ft;
+  __shared__ uint64_t full_b[kRwWarps][kRwStages];
+  __shared__ float ls[kRwBlock];  // base-2 log-sum-exp of the staged rows, +inf: weighs nothing
+  __shared__ int last[kRwBlock];  // last position a staged row sees
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* base = align1024(smem);
+  uint8_t* ring = base + warp * kRwStages * kRwStageBytes;
+  uint8_t* qs = base + kRwWarps * kRwStages * kRwStageBytes;
+  if (lane == 0)
+    for (int s = 0; s < kRwStages; ++s) mbar_init(&full_b[warp][s], 1);
+  if (tid == 0) fence_mbar_init();
+  flat_build(
+      ft, p.B, [&](int b) { return rows_cache_len(p, b); }, [&](int b) { return rows_of(p, b, rows_cache_len(p, b)); },
+      [&](int n, int m) { return m > 0 ? (n + kRwKeys - 1) / kRwKeys : 0; }, [&](int) { return p.Hkv; });
+  const long long total = ft.base[p.B];
+  const int N = flat_ctas(total, p.N);
+  if (blockIdx.x >= N) return;
+  const long long x0 = flat_first(total, blockIdx.x, N), x1 = flat_first(total, blockIdx.x + 1, N);
+  int fetched = 0, used = 0;
+  bool dead = false;
+  uint32_t skipped = 0;
+  FlatRun r;
+  for (long long x = x0; flat_run(ft, p.B, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+    const int b = r.b, g = r.unit, n = ft.n[b], m = ft.t[b], rows = m * p.G;
+    auto fetch = [&](int c) {
+      const int s = fetched % kRwStages, t0 = c * kRwKeys;
+      const int phys = p.page_table[(size_t)b * p.max_pages + (t0 >> p.pshift)];
+      if (phys >= 0 && phys < p.num_phys) {
+        skipped &= ~(1u << s);
+        if (lane == 0) {
+          const int row = (phys * p.Hkv + g) * p.P + (t0 & (p.P - 1));
+          uint8_t* st = ring + s * kRwStageBytes;
+          mbar_arrive_expect_tx(&full_b[warp][s], kRwStageBytes);
+          tma_load_2d(st, &p.tmk, 0, row, &full_b[warp][s]);
+          tma_load_2d(st + 2048, &p.tmk, 64, row, &full_b[warp][s]);
+        }
+      } else {
+        skipped |= 1u << s;
+        if (lane == 0) {
+          flag_error(p.err, RKV_DEVERR_PAGE_ID);
+          mbar_arrive(&full_b[warp][s]);
+        }
+      }
+      ++fetched;
+    };
+    for (int blk = 0; blk < rows; blk += kRwBlock) {
+      const int live = min(kRwBlock, rows - blk);
+      int fc = r.lo + warp;
+      for (int s = 0; s < kRwStages && fc < r.hi && !dead; ++s, fc += kRwWarps) fetch(fc);
+      // the block's query rows (row = i G + head), swizzled as the boxes are
+      __syncthreads();
+      for (int e = tid; e < kRwBlock * 16; e += kRwThreads) {
+        const int row = e >> 4, piece = e & 15;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < live) {
+          const int i = (blk + row) >> p.gshift, h = (blk + row) & (p.G - 1);
+          const int id = p.row_ids ? p.row_ids[(size_t)b * p.ids_stride + i] : i;
+          const bool ok = id >= 0 && id < p.T;
+          const size_t at = ((size_t)b * p.Hq + g * p.G + h) * p.T + (ok ? id : 0);
+          if (ok) v = reinterpret_cast<const uint4*>(p.q + at * 128)[piece];
+          if (piece == 0) {
+            if (!ok) flag_error(p.err, RKV_DEVERR_TREE);
+            const float l = ok ? p.lse[at] * 1.4426950408889634f : INFINITY;
+            ls[row] = l == -INFINITY ? INFINITY : l;
+            last[row] = n - m + i;
+          }
+        } else if (piece == 0) {
+          ls[row] = INFINITY;
+          last[row] = -1;
+        }
+        *reinterpret_cast<uint4*>(qs + (piece >> 3) * (kRwBlock * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) = v;
+      }
+      __syncthreads();
+      const uint32_t qb = smem_u32(qs);
+      for (int c = r.lo + warp; c < r.hi; c += kRwWarps) {
+        const int s = used % kRwStages;
+        const bool late = !dead && !mbar_wait(&full_b[warp][s], (uint32_t)((used / kRwStages) & 1));
+        if (__any_sync(0xffffffffu, late)) {
+          if (lane == 0) flag_error(p.err, RKV_DEVERR_TIMEOUT);
+          dead = true;
+        }
+        if (dead) break;
+        const bool take = !((skipped >> s) & 1u);
+        uint32_t ka[8][4];
+        const uint32_t ks = smem_u32(ring + s * kRwStageBytes);
+        {
+          const int key = (((lane >> 3) & 1) << 3) + (lane & 7);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int piece = k * 2 + (lane >> 4);
+            ldsm_x4(ka[k][0], ka[k][1], ka[k][2], ka[k][3],
+                    ks + (piece >> 3) * 2048 + key * 128 + (((piece & 7) ^ (key & 7)) << 4));
+          }
+        }
+        ++used;
+        __syncwarp();  // every lane has read the stage
+        if (fc < r.hi) {
+          fetch(fc);
+          fc += kRwWarps;
+        }
+        if (!take) continue;
+        const int t0 = c * kRwKeys + (lane >> 2), t1 = t0 + 8;
+        float w0 = 0.f, w1 = 0.f;
+        const int rr = ((lane >> 4) << 3) + (lane & 7), sub = (lane >> 3) & 1;
+        for (int r16 = 0; r16 < live; r16 += 16) {
+          float z[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+          const int row = r16 + rr;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int piece = k * 2 + sub;
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4(b0, b1, b2, b3, qb + (piece >> 3) * (kRwBlock * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+            mma_16816(z[0], ka[k][0], ka[k][1], ka[k][2], ka[k][3], b0, b1);
+            mma_16816(z[1], ka[k][0], ka[k][1], ka[k][2], ka[k][3], b2, b3);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int q = r16 + h * 8 + (lane & 3) * 2 + e;
+              const float l = ls[q];
+              const int seen = last[q];
+              const float e0 = ex2_approx(fmaf(z[h][e], p.scale_log2, -l));
+              const float e1 = ex2_approx(fmaf(z[h][2 + e], p.scale_log2, -l));
+              w0 += t0 <= seen ? e0 : 0.f;
+              w1 += t1 <= seen ? e1 : 0.f;
+            }
+        }
+        w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
+        w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
+        w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
+        w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
+        if ((lane & 3) == 0) {
+          float* a = p.acc + ((size_t)b * p.Hkv + g) * p.acc_stride;
+          if (t0 < n) a[t0] += w0;
+          if (t1 < n) a[t1] += w1;
+        }
+      }
+      __syncthreads();  // the staged rows are free
+    }
+  }
+  if (dead)
+    for (int i = used; i < fetched; ++i) mbar_wait(&full_b[warp][i % kRwStages], (uint32_t)((i / kRwStages) & 1));
+}
+
+// ---------------------------------------------------------------------------
+// evict
+struct EvictParams {
+  rkv_cache src, dst;
+  int in_place;
+  const float* acc;
+  float* dst_acc;
+  int acc_stride, dst_acc_stride, recent, kept_stride, stage_stride;
+  int32_t* kept;        // [B][Hkv][kept_stride]
+  int32_t* count;       // [B] tokens kept (workspace)
+  rkv_bf16* stage_k;    // in place: [B][Hkv][stage_stride][128], else null
+  rkv_bf16* stage_v;
+  float* stage_acc;     // [B][Hkv][stage_stride]
+  int cgroup;
+  int32_t keep[RKV_MAX_BATCH];
+};
+
+__device__ __forceinline__ int evict_len(const EvictParams& p, int b) {
+  const int n = p.src.seq_len[b];
+  return n < 0 || n > p.src.max_pages * p.src.page_size ? 0 : n;
+}
+
+// Kept positions, ascending.  A cluster of C CTAs per unit, grid (C, B*Hkv).
+__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
+  extern __shared__ uint32_t skeys[];
+  __shared__ SelectSmem ss;
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int unit = blockIdx.y, b = unit / p.src.Hkv, tid = threadIdx.x;
+  const int n = evict_len(p, b), keep = p.keep[b];
+  int32_t* out = p.kept + (size_t)unit * p.kept_stride;
+  if (rank == 0 && tid == 0 && unit % p.src.Hkv == 0) {
+    if (n != p.src.seq_len[b]) flag_error(p.src.error_word, RKV_DEVERR_CAPACITY);
+    p.count[b] = min(n, keep);
+  }
+  if (n <= keep) {  // the same branch in every CTA of the cluster
+    for (int i = rank * kSelectThreads + tid; i < n; i += C * kSelectThreads) out[i] = i;
+    return;
+  }
+  const int recent = p.recent, Lp = n - recent, k = keep - recent;  // recent <= keep < n
+  if (rank == 0)
+    for (int i = tid; i < recent; i += kSelectThreads) out[k + i] = Lp + i;
+  if (k == 0) return;
+  const float* acc = p.acc + (size_t)unit * p.acc_stride;
+  // a NaN counts as the heaviest, and both zeros as one
+  cluster_select(Lp, k, [&](int t) {
+    const float v = acc[t];
+    return v != v ? __int_as_float(0x7fffffff) : v + 0.f;
+  }, out, skeys, ss);
+}
+
+// Row i of a unit's kept list in the source cache; null when its page id is out of range.
+__device__ __forceinline__ bool evict_source(const EvictParams& p, int b, int g, int t, size_t& row) {
+  const int P = p.src.page_size;
+  const int phys = p.src.page_table[(size_t)b * p.src.max_pages + t / P];
+  if (phys < 0 || phys >= p.src.num_phys_pages) {
+    flag_error(p.src.error_word, RKV_DEVERR_PAGE_ID);
+    return false;
+  }
+  row = (((size_t)phys * p.src.Hkv + g) * P + t % P) * 128;
+  return true;
+}
+
+// In place only: the rows that move, into the workspace, before any page is written.
+// grid (ceil(max keep / 64), Hkv, B), 256 threads: 16 rows x 16 pieces of 16 bytes.
+__global__ void __launch_bounds__(256) evict_stage_kernel(const __grid_constant__ EvictParams p) {
+  const int b = blockIdx.z, g = blockIdx.y, n = p.count[b];
+  const size_t unit = (size_t)b * p.src.Hkv + g;
+  const int piece = threadIdx.x & 15;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = blockIdx.x * 64 + j * 16 + (threadIdx.x >> 4);
+    if (i >= n) continue;
+    const int t = p.kept[unit * p.kept_stride + i];
+    if (t == i) continue;
+    const size_t to = unit * p.stage_stride + i;
+    size_t row;
+    if (evict_source(p, b, g, t, row)) {
+      reinterpret_cast<uint4*>(p.stage_k + to * 128)[piece] = reinterpret_cast<const uint4*>(p.src.k_pages + row)[piece];
+      reinterpret_cast<uint4*>(p.stage_v + to * 128)[piece] = reinterpret_cast<const uint4*>(p.src.v_pages + row)[piece];
+    }
+    if (piece == 0) p.stage_acc[to] = p.acc[unit * p.acc_stride + t];
+  }
+}
+
+// Kept rows into the destination's pages, their summaries, their weights (zero behind
+// them) and the new lengths.  grid (ceil(max keep / (cgroup P)), Hkv, B), 128 threads: a
+// CTA fills cgroup <= 8 consecutive pages; thread t moves 16-byte piece t % 16 of rows
+// t / 16, t / 16 + 8, ... and keeps their max / min, which a shuffle and a pass over the
+// four warps combine into the page's column of a [channel][8 pages] tile, so that with
+// groups of eight a channel's summaries go out as one 16-byte store.
+template <int kRows>  // rows per thread: page size / 8
+__global__ void __launch_bounds__(128) evict_compact_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int P = 8 * kRows;
+  __shared__ float red[2][4][128];
+  __shared__ int32_t idx[8 * P];
+  __shared__ __align__(16) uint16_t tile[2][128][8];
+  const int b = blockIdx.z, g = blockIdx.y, tid = threadIdx.x;
+  const int lane = tid & 31, warp = tid >> 5;
+  const size_t unit = (size_t)b * p.src.Hkv + g;
+  const int n = p.count[b];
+  const int pg0 = blockIdx.x * p.cgroup;
+  if (blockIdx.x == 0 && g == 0 && tid == 0) p.dst.seq_len[b] = n;
+  // the weights behind the kept ones start again at zero
+  for (int t = n + blockIdx.x * 128 + tid; t < p.dst_acc_stride; t += gridDim.x * 128)
+    p.dst_acc[unit * p.dst_acc_stride + t] = 0.f;
+  if (pg0 * P >= n) return;
+  const int npg = min(p.cgroup, (n + P - 1) / P - pg0);
+  const int r_end = min(p.cgroup * P, n - pg0 * P);
+  const int32_t* kept = p.kept + unit * p.kept_stride + (size_t)pg0 * P;
+  for (int r = tid; r < r_end; r += 128) {
+    const int t = kept[r], i = pg0 * P + r;
+    idx[r] = t;
+    if (!p.in_place)
+      p.dst_acc[unit * p.dst_acc_stride + i] = p.acc[unit * p.acc_stride + t];
+    else if (t != i)
+      p.dst_acc[unit * p.dst_acc_stride + i] = p.stage_acc[unit * p.stage_stride + i];
+  }
+  __syncthreads();
+  const int piece = tid & 15, rg = tid >> 4;
+  for (int q = 0; q < npg; ++q) {
+    const int pg = pg0 + q;
+    const int phys = p.dst.page_table[(size_t)b * p.dst.max_pages + pg];
+    const bool page_ok = phys >= 0 && phys < p.dst.num_phys_pages;
+    if (!page_ok && tid == 0) flag_error(p.dst.error_word, RKV_DEVERR_PAGE_ID);
+    const int cnt = min(P, n - pg * P);
+    const size_t dst0 = (((size_t)(page_ok ? phys : 0) * p.dst.Hkv + g) * P) * 128 + piece * 8;
+    uint4 kv[kRows], vv[kRows];
+    bool have[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int r = rg + 8 * j, i = pg * P + r;
+      have[j] = r < cnt;
+      kv[j] = make_uint4(0, 0, 0, 0);
+      vv[j] = make_uint4(0, 0, 0, 0);
+      if (!have[j]) continue;
+      const int t = idx[q * P + r];
+      if (p.in_place && t != i) {
+        const size_t row = (unit * p.stage_stride + i) * 128 + piece * 8;
+        kv[j] = *reinterpret_cast<const uint4*>(p.stage_k + row);
+        vv[j] = *reinterpret_cast<const uint4*>(p.stage_v + row);
+      } else {
+        size_t row;
+        have[j] = evict_source(p, b, g, t, row);
+        if (have[j]) {
+          kv[j] = *reinterpret_cast<const uint4*>(p.src.k_pages + row + piece * 8);
+          vv[j] = *reinterpret_cast<const uint4*>(p.src.v_pages + row + piece * 8);
+        }
+      }
+    }
+    float mx[8], mn[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      mx[e] = -INFINITY;
+      mn[e] = INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      if (!have[j]) continue;
+      const int r = rg + 8 * j;
+      if (page_ok) {
+        *reinterpret_cast<uint4*>(p.dst.k_pages + dst0 + (size_t)r * 128) = kv[j];
+        *reinterpret_cast<uint4*>(p.dst.v_pages + dst0 + (size_t)r * 128) = vv[j];
+      }
+      const uint32_t w4[4] = {kv[j].x, kv[j].y, kv[j].z, kv[j].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a0 = bf16_lo(w4[e]), a1 = bf16_hi(w4[e]);
+        mx[2 * e] = fmaxf(mx[2 * e], a0);
+        mx[2 * e + 1] = fmaxf(mx[2 * e + 1], a1);
+        mn[2 * e] = fminf(mn[2 * e], a0);
+        mn[2 * e + 1] = fminf(mn[2 * e + 1], a1);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {  // lanes l and l ^ 16 hold the same piece
+      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
+      mn[e] = fminf(mn[e], __shfl_xor_sync(0xffffffffu, mn[e], 16));
+    }
+    if (lane < 16) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        red[0][warp][piece * 8 + e] = mx[e];
+        red[1][warp][piece * 8 + e] = mn[e];
+      }
+    }
+    __syncthreads();
+    const float M = fmaxf(fmaxf(red[0][0][tid], red[0][1][tid]), fmaxf(red[0][2][tid], red[0][3][tid]));
+    const float m = fminf(fminf(red[1][0][tid], red[1][1][tid]), fminf(red[1][2][tid], red[1][3][tid]));
+    // the values came from bf16 bit patterns, so the top 16 bits are exact
+    tile[0][tid][q] = (uint16_t)(__float_as_uint(M) >> 16);
+    tile[1][tid][q] = (uint16_t)(__float_as_uint(m) >> 16);
+    __syncthreads();  // red is reused by the next page
+  }
+  const size_t row = (unit * 128 + tid) * p.dst.max_pages + pg0;
+  if (npg == 8) {  // cgroup == 8: 16-byte aligned (max_pages is a multiple of 8)
+    *reinterpret_cast<uint4*>(p.dst.kmax + row) = *reinterpret_cast<const uint4*>(&tile[0][tid][0]);
+    *reinterpret_cast<uint4*>(p.dst.kmin + row) = *reinterpret_cast<const uint4*>(&tile[1][tid][0]);
+  } else {
+    for (int q = 0; q < npg; ++q) {
+      p.dst.kmax[row + q] = tile[0][tid][q];
+      p.dst.kmin[row + q] = tile[1][tid][q];
+    }
+  }
+}
+
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+int log2_int(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+}  // namespace
+
+size_t accum_rows_ws_bytes(int, int, int, int, int, int) { return 256; }
+
+cudaError_t launch_accum_rows(const AccumRowsArgs& a, cudaStream_t s) {
+  const rkv_cache& c = a.cache;
+  RowsParams p;
+  if (!encode_rows_map(&p.tmk, c.k_pages, (uint64_t)c.num_phys_pages * c.Hkv * c.page_size, kRwKeys)) {
+    set_last_error("cuTensorMapEncodeTiled failed for the cache's pages");
+    return cudaErrorInvalidValue;
+  }
+  p.q = a.q;
+  p.lse = a.lse;
+  p.row_len = a.row_len;
+  p.row_ids = a.row_ids;
+  p.page_table = c.page_table;
+  p.seq_len = c.seq_len;
+  p.err = c.error_word;
+  p.acc = a.acc;
+  p.B = c.B;
+  p.Hq = a.Hq;
+  p.Hkv = c.Hkv;
+  p.G = a.Hq / c.Hkv;
+  p.gshift = log2_int(p.G);
+  p.T = a.T;
+  p.ids_stride = a.ids_stride;
+  p.P = c.page_size;
+  p.pshift = log2_int(c.page_size);
+  p.max_pages = c.max_pages;
+  p.num_phys = c.num_phys_pages;
+  p.acc_stride = a.acc_stride;
+  p.N = num_sms();
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  static SmemOptIn opt;
+  cudaError_t e = opt.raise(reinterpret_cast<const void*>(accum_rows_kernel), kRwSmem);
+  if (e != cudaSuccess) return e;
+  launch_begin(K_ACCUM_ROWS, s);
+  accum_rows_kernel<<<p.N, kRwThreads, kRwSmem, s>>>(p);
+  launch_end(K_ACCUM_ROWS, s);
+  return cudaGetLastError();
+}
+
+int evict_max_tokens() { return kSelectMaxCluster * kSelectSliceMax; }
+
+size_t evict_ws_bytes(int B, int Hkv, int max_keep, bool in_place) {
+  size_t n = align256((size_t)B * 4);
+  if (in_place) {
+    const size_t rows = (size_t)B * Hkv * max_keep;
+    n += 2 * align256(rows * 256) + align256(rows * 4);
+  }
+  return n;
+}
+
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
+  const rkv_cache& c = a.cache;
+  EvictParams p;
+  p.src = c;
+  p.dst = a.dst;
+  p.in_place = a.in_place;
+  p.acc = a.acc;
+  p.dst_acc = a.dst_acc;
+  p.acc_stride = a.acc_stride;
+  p.dst_acc_stride = a.dst_acc_stride;
+  p.recent = a.recent;
+  p.kept = a.kept_idx;
+  p.kept_stride = a.kept_stride;
+  int keep_max = 1;
+  for (int b = 0; b < c.B; ++b) {
+    p.keep[b] = a.keep[b];
+    keep_max = a.keep[b] > keep_max ? a.keep[b] : keep_max;
+  }
+  uint8_t* w = static_cast<uint8_t*>(a.ws);
+  p.count = reinterpret_cast<int32_t*>(w);
+  w += align256((size_t)c.B * 4);
+  p.stage_k = p.stage_v = nullptr;
+  p.stage_acc = nullptr;
+  p.stage_stride = keep_max;
+  const size_t rows = (size_t)c.B * c.Hkv * keep_max;
+  if (a.in_place) {
+    p.stage_k = reinterpret_cast<rkv_bf16*>(w);
+    w += align256(rows * 256);
+    p.stage_v = reinterpret_cast<rkv_bf16*>(w);
+    w += align256(rows * 256);
+    p.stage_acc = reinterpret_cast<float*>(w);
+  }
+  // select: about 4096 positions a CTA, clusters of up to 8 while the units leave SMs
+  // idle and of 2 once they cover them, wide enough for the slices to fit
+  const int units = c.B * c.Hkv, cap = c.max_pages * c.page_size;
+  int C = (cap + 4095) / 4096;
+  const int by_units = num_sms() / units > 2 ? num_sms() / units : 2;
+  const int by_smem = (cap + kSelectSliceMax - 1) / kSelectSliceMax;
+  C = C < by_units ? C : by_units;
+  C = C > by_smem ? C : by_smem;
+  C = C > kSelectMaxCluster ? kSelectMaxCluster : C;
+  static SmemOptIn opt;
+  cudaError_t e = opt.raise(reinterpret_cast<const void*>(evict_select_kernel), kSelectSliceMax * 4);
+  if (e != cudaSuccess) return e;
+  {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C, (unsigned)units, 1);
+    cfg.blockDim = dim3(kSelectThreads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)((cap + C - 1) / C) * 4;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    launch_begin(K_EVICT_SELECT, s);
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+    launch_end(K_EVICT_SELECT, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.in_place) {
+    launch_begin(K_EVICT_STAGE, s);
+    evict_stage_kernel<<<dim3((keep_max + 63) / 64, c.Hkv, c.B), 256, 0, s>>>(p);
+    launch_end(K_EVICT_STAGE, s);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const int P = c.page_size;
+  p.cgroup = 8;
+  while (p.cgroup > 1 && (long)((keep_max + p.cgroup * P - 1) / (p.cgroup * P)) * units < 16L * num_sms()) p.cgroup /= 2;
+  const dim3 grid((keep_max + p.cgroup * P - 1) / (p.cgroup * P), c.Hkv, c.B);
+  launch_begin(K_EVICT_COMPACT, s);
+  if (P == 16)
+    evict_compact_kernel<2><<<grid, 128, 0, s>>>(p);
+  else if (P == 32)
+    evict_compact_kernel<4><<<grid, 128, 0, s>>>(p);
+  else
+    evict_compact_kernel<8><<<grid, 128, 0, s>>>(p);
+  launch_end(K_EVICT_COMPACT, s);
+  return cudaGetLastError();
+}
+
+}  // namespace rkv

@@ -40,6 +40,7 @@ rkv_status fail(rkv_status s, const char* fmt, ...) {
   return s;
 }
 
+bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 rkv_status check_cache(const rkv_cache* c) {
@@ -128,7 +129,8 @@ const char* kernel_name(int kind) {
       "snap_colsum",  "snap_pool",    "snap_select",    "snap_compact", "hsa_score",
       "hsa_topk",     "hsa_attend",   "hsa_combine",    "hsa_step",     "recall",
       "chunk_gather", "sparq_score",  "sparq_topk",     "sparq_attend", "wait_selftest",
-      "sparq_keys_sync"};
+      "sparq_keys_sync", "attend_rows", "attend_combine", "attend_weigh", "tree_commit",
+      "accum_rows", "evict_select", "evict_stage", "evict_compact"};
   return (kind >= 0 && kind < K_NUM_KINDS) ? names[kind] : nullptr;
 }
 
@@ -605,6 +607,216 @@ rkv_status rkv_decode_step_host(const rkv_cache* cache, const void* host_in, flo
   if (st != RKV_OK) return st;
   e = cudaMemcpyAsync(host_out, out, (size_t)cache->B * Hq * RKV_HEAD_DIM * 4, cudaMemcpyDeviceToHost, s);
   return cuda_status(e, "rkv_decode_step_host output copy");
+}
+
+size_t rkv_tree_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t max_pages, int32_t page_size) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || max_pages < 1 || page_size < 1) return 0;
+  return rkv::attend_ws_bytes(B, Hq, Hkv, T, max_pages, page_size, false);
+}
+
+rkv_status rkv_tree_attention(const rkv_cache* cache, const rkv_bf16* q, const rkv_bf16* k_tree,
+                              const rkv_bf16* v_tree, const uint32_t* tree_mask, int32_t Hq, int32_t T,
+                              const int32_t* tree_len, float scale, rkv_bf16* out, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  const NvtxRange nvtx_range("rkv_tree_attention");
+  rkv_status st = check_cache(cache);
+  if (st != RKV_OK) return st;
+  if ((st = check_heads(Hq, cache->Hkv)) != RKV_OK) return st;
+  if (!q || !k_tree || !v_tree || !tree_mask || !out || !workspace)
+    return fail(RKV_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!al16(q) || !al16(k_tree) || !al16(v_tree) || !al16(out) || !al16(workspace))
+    return fail(RKV_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if (!al4(tree_mask) || !al4(tree_len) || !al4(lse))
+    return fail(RKV_ERR_INVALID_ARG, "tree_mask, tree_len and lse must be 4-byte aligned");
+  if (T < 1 || T > RKV_MAX_TREE) return fail(RKV_ERR_INVALID_ARG, "T=%d outside [1, %d]", T, RKV_MAX_TREE);
+  if ((long long)cache->B * Hq * T >= (1LL << 31)) return fail(RKV_ERR_UNSUPPORTED, "B * Hq * T above 2^31");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(RKV_ERR_INVALID_ARG, "scale must be positive");
+  const size_t need = rkv::attend_ws_bytes(cache->B, Hq, cache->Hkv, T, cache->max_pages, cache->page_size, false);
+  if (workspace_bytes < need)
+    return fail(RKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  rkv::AttendArgs a = {};
+  a.cache = *cache;
+  a.q = q;
+  a.Hq = Hq;
+  a.T = T;
+  a.k_tree = k_tree;
+  a.v_tree = v_tree;
+  a.mask = tree_mask;
+  a.tree_len = tree_len;
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.ws = workspace;
+  return cuda_status(rkv::launch_attend(a, static_cast<cudaStream_t>(stream)), "rkv_tree_attention launch");
+}
+
+rkv_status rkv_tree_commit(const rkv_cache* cache, const rkv_bf16* k_tree, const rkv_bf16* v_tree, int32_t T,
+                           const int32_t* path, int32_t path_stride, const int32_t* path_len, void* stream) {
+  const NvtxRange nvtx_range("rkv_tree_commit");
+  rkv_status st = check_cache(cache);
+  if (st != RKV_OK) return st;
+  if (!k_tree || !v_tree || !path || !path_len) return fail(RKV_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!al16(k_tree) || !al16(v_tree)) return fail(RKV_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if (!al4(path) || !al4(path_len)) return fail(RKV_ERR_INVALID_ARG, "path and path_len must be 4-byte aligned");
+  if (T < 1 || T > RKV_MAX_TREE) return fail(RKV_ERR_INVALID_ARG, "T=%d outside [1, %d]", T, RKV_MAX_TREE);
+  if (path_stride < 1 || path_stride > RKV_MAX_TREE)
+    return fail(RKV_ERR_INVALID_ARG, "path_stride=%d outside [1, %d]", path_stride, RKV_MAX_TREE);
+  rkv::CommitArgs a;
+  a.cache = *cache;
+  a.k_tree = k_tree;
+  a.v_tree = v_tree;
+  a.T = T;
+  a.path = path;
+  a.path_stride = path_stride;
+  a.path_len = path_len;
+  return cuda_status(rkv::launch_commit(a, static_cast<cudaStream_t>(stream)), "rkv_tree_commit launch");
+}
+
+// The sums of a cache's positions: one for every position it can hold.
+static rkv_status check_acc(const rkv_cache* c, const float* acc, int32_t acc_stride, const char* what) {
+  if (!acc) return fail(RKV_ERR_INVALID_ARG, "%s is NULL", what);
+  if (!al4(acc)) return fail(RKV_ERR_INVALID_ARG, "%s must be 4-byte aligned", what);
+  if (acc_stride < c->max_pages * c->page_size)
+    return fail(RKV_ERR_INVALID_ARG, "%s's stride %d is below the cache's %d positions", what, acc_stride,
+                c->max_pages * c->page_size);
+  return RKV_OK;
+}
+
+size_t rkv_accum_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_pages, int32_t page_size) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || max_pages < 1 || page_size < 1) return 0;
+  return rkv::attend_ws_bytes(B, Hq, Hkv, 1, max_pages, page_size, true);
+}
+
+rkv_status rkv_decode_accum(const rkv_cache* cache, const rkv_bf16* q, int32_t Hq, float scale, rkv_bf16* out,
+                            float* lse, float* acc, int32_t acc_stride, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  const NvtxRange nvtx_range("rkv_decode_accum");
+  rkv_status st = check_cache(cache);
+  if (st != RKV_OK) return st;
+  if ((st = check_heads(Hq, cache->Hkv)) != RKV_OK) return st;
+  if (!q || !out || !workspace) return fail(RKV_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!al16(q) || !al16(out) || !al16(workspace))
+    return fail(RKV_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if (!al4(lse)) return fail(RKV_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  if ((st = check_acc(cache, acc, acc_stride, "acc")) != RKV_OK) return st;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(RKV_ERR_INVALID_ARG, "scale must be positive");
+  const size_t need = rkv::attend_ws_bytes(cache->B, Hq, cache->Hkv, 1, cache->max_pages, cache->page_size, true);
+  if (workspace_bytes < need)
+    return fail(RKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  rkv::AttendArgs a = {};
+  a.cache = *cache;
+  a.q = q;
+  a.Hq = Hq;
+  a.T = 1;
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.acc = acc;
+  a.acc_stride = acc_stride;
+  a.ws = workspace;
+  return cuda_status(rkv::launch_attend(a, static_cast<cudaStream_t>(stream)), "rkv_decode_accum launch");
+}
+
+size_t rkv_accum_rows_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t max_pages,
+                                     int32_t page_size) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || max_pages < 1 || page_size < 1) return 0;
+  return rkv::accum_rows_ws_bytes(B, Hq, Hkv, T, max_pages, page_size);
+}
+
+rkv_status rkv_accum_rows(const rkv_cache* cache, const rkv_bf16* q, const float* lse, int32_t Hq, int32_t T,
+                          const int32_t* row_len, const int32_t* row_ids, int32_t ids_stride, float scale, float* acc,
+                          int32_t acc_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  const NvtxRange nvtx_range("rkv_accum_rows");
+  rkv_status st = check_cache(cache);
+  if (st != RKV_OK) return st;
+  if ((st = check_heads(Hq, cache->Hkv)) != RKV_OK) return st;
+  if (!q || !lse || !workspace) return fail(RKV_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!al16(q) || !al16(workspace)) return fail(RKV_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if (!al4(lse) || !al4(row_len) || !al4(row_ids))
+    return fail(RKV_ERR_INVALID_ARG, "lse, row_len and row_ids must be 4-byte aligned");
+  if (T < 1 || T > (1 << 20)) return fail(RKV_ERR_INVALID_ARG, "T=%d outside [1, 2^20]", T);
+  if (row_ids && (ids_stride < 1 || ids_stride > (1 << 20)))
+    return fail(RKV_ERR_INVALID_ARG, "ids_stride=%d outside [1, 2^20]", ids_stride);
+  if ((long long)cache->B * Hq * T >= (1LL << 31)) return fail(RKV_ERR_UNSUPPORTED, "B * Hq * T above 2^31");
+  if ((st = check_acc(cache, acc, acc_stride, "acc")) != RKV_OK) return st;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(RKV_ERR_INVALID_ARG, "scale must be positive");
+  const size_t need = rkv::accum_rows_ws_bytes(cache->B, Hq, cache->Hkv, T, cache->max_pages, cache->page_size);
+  if (workspace_bytes < need)
+    return fail(RKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  rkv::AccumRowsArgs a;
+  a.cache = *cache;
+  a.q = q;
+  a.lse = lse;
+  a.Hq = Hq;
+  a.T = T;
+  a.row_len = row_len;
+  a.row_ids = row_ids;
+  a.ids_stride = ids_stride;
+  a.scale = scale;
+  a.acc = acc;
+  a.acc_stride = acc_stride;
+  a.ws = workspace;
+  return cuda_status(rkv::launch_accum_rows(a, static_cast<cudaStream_t>(stream)), "rkv_accum_rows launch");
+}
+
+size_t rkv_evict_workspace_size(int32_t B, int32_t Hkv, int32_t max_keep, int32_t in_place) {
+  if (B < 1 || Hkv < 1 || max_keep < 1) return 0;
+  return rkv::evict_ws_bytes(B, Hkv, max_keep, in_place != 0);
+}
+
+rkv_status rkv_evict_accum(const rkv_cache* cache, float* acc, int32_t acc_stride, const int32_t* keep, int32_t recent,
+                           int32_t* kept_idx, int32_t kept_stride, const rkv_cache* dst, float* dst_acc,
+                           int32_t dst_acc_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  const NvtxRange nvtx_range("rkv_evict_accum");
+  rkv_status st = check_cache(cache);
+  if (st != RKV_OK) return st;
+  if (!keep || !kept_idx || !workspace) return fail(RKV_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!al4(kept_idx)) return fail(RKV_ERR_INVALID_ARG, "kept_idx must be 4-byte aligned");
+  if (!al16(workspace)) return fail(RKV_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if ((st = check_acc(cache, acc, acc_stride, "acc")) != RKV_OK) return st;
+  const bool in_place = dst == nullptr;
+  if (in_place != (dst_acc == nullptr))
+    return fail(RKV_ERR_INVALID_ARG, "dst and dst_acc must both be given, or neither (in place)");
+  const rkv_cache* to = in_place ? cache : dst;
+  if (!in_place) {
+    if ((st = check_cache(dst)) != RKV_OK) return st;
+    if (dst->B != cache->B || dst->Hkv != cache->Hkv || dst->page_size != cache->page_size)
+      return fail(RKV_ERR_INVALID_ARG, "dst differs from the cache in B, Hkv or page_size");
+    if ((st = check_acc(dst, dst_acc, dst_acc_stride, "dst_acc")) != RKV_OK) return st;
+    if (dst_acc == acc || dst->page_table == cache->page_table || dst->seq_len == cache->seq_len ||
+        dst->kmax == cache->kmax || dst->kmin == cache->kmin)
+      return fail(RKV_ERR_INVALID_ARG, "dst shares storage with the cache (pass NULL to evict in place)");
+  }
+  if ((long long)cache->B * cache->Hkv > 65535) return fail(RKV_ERR_UNSUPPORTED, "B * Hkv above 65535");
+  if (cache->max_pages * cache->page_size > rkv::evict_max_tokens())
+    return fail(RKV_ERR_UNSUPPORTED, "eviction supports caches of at most %d tokens per sequence",
+                rkv::evict_max_tokens());
+  if (recent < 0) return fail(RKV_ERR_INVALID_ARG, "recent=%d", recent);
+  const int cap = to->max_pages * to->page_size;
+  int max_keep = 1;
+  for (int b = 0; b < cache->B; ++b) {
+    if (keep[b] < 1 || keep[b] > cap) return fail(RKV_ERR_INVALID_ARG, "keep[%d]=%d outside [1, %d]", b, keep[b], cap);
+    if (keep[b] < recent) return fail(RKV_ERR_INVALID_ARG, "keep[%d]=%d below recent=%d", b, keep[b], recent);
+    if (keep[b] > kept_stride) return fail(RKV_ERR_INVALID_ARG, "kept_stride=%d < keep[%d]=%d", kept_stride, b, keep[b]);
+    max_keep = keep[b] > max_keep ? keep[b] : max_keep;
+  }
+  const size_t need = rkv::evict_ws_bytes(cache->B, cache->Hkv, max_keep, in_place);
+  if (workspace_bytes < need)
+    return fail(RKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  rkv::EvictArgs a;
+  a.cache = *cache;
+  a.dst = *to;
+  a.in_place = in_place;
+  a.acc = acc;
+  a.acc_stride = acc_stride;
+  a.dst_acc = in_place ? acc : dst_acc;
+  a.dst_acc_stride = in_place ? acc_stride : dst_acc_stride;
+  a.keep = keep;
+  a.recent = recent;
+  a.kept_idx = kept_idx;
+  a.kept_stride = kept_stride;
+  a.ws = workspace;
+  return cuda_status(rkv::launch_evict(a, static_cast<cudaStream_t>(stream)), "rkv_evict_accum launch");
 }
 
 rkv_status rkv_exact_topk_recall(const rkv_cache* cache, const rkv_bf16* q, int32_t Hq, const int32_t* sel_pages,

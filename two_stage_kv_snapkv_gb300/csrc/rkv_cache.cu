@@ -6,6 +6,8 @@
 // decode equals a rebuild of the summaries, bit for bit).  Min and max of bf16
 // values are exact, so folding new tokens into a page's stored summary, or
 // recomputing the page from its tokens, is bit-identical to any rebuild order.
+#include <cooperative_groups.h>
+
 #include "rkv_device.cuh"
 #include "rkv_internal.h"
 
@@ -172,10 +174,80 @@ __global__ void append_advance_kernel(const __grid_constant__ AppendParams p) {
   if (n >= 0 && n + p.n_new <= p.max_pages * p.P) p.seq_len[b] = n + p.n_new;
 }
 
+// Accepted path of a drafted tree: rows path[b][0 .. len) of the tree's keys and values
+// go to positions n, n + 1, ..., the touched pages' summaries fold them in, and the
+// length moves on.  A few kilobytes per sequence: launch latency bounds it, so it is one
+// launch, a cluster of up to eight CTAs per sequence that share its KV heads, and the
+// cluster barrier puts the new length behind every CTA's reading of the old one.
+struct CommitParams {
+  AppendParams a;  // k_new / v_new: the tree's, n_new: its nodes T
+  const int32_t* path;
+  const int32_t* path_len;
+  int path_stride;
+};
+
+__global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant__ CommitParams cp) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ int s_bad;
+  const AppendParams& p = cp.a;
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int b = blockIdx.y, tid = threadIdx.x, T = p.n_new;
+  const int n = p.seq_len[b], m = cp.path_len[b];
+  const int32_t* path = cp.path + (size_t)b * cp.path_stride;
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  int bad = 0;
+  if (m < 0 || m > cp.path_stride) {
+    bad = RKV_DEVERR_TREE;
+  } else {
+    for (int i = tid; i < m; i += 256)
+      if (path[i] < 0 || path[i] >= T) bad = RKV_DEVERR_TREE;
+    if (n < 0 || (long long)n + m > (long long)p.max_pages * p.P) bad |= RKV_DEVERR_CAPACITY;
+  }
+  if (bad) atomicOr(&s_bad, bad);
+  __syncthreads();
+  bad = s_bad;
+  if (bad && rank == 0 && tid == 0) flag_error(p.err, bad);
+  if (!bad && m > 0) {
+    const int32_t* ptab = p.page_table + (size_t)b * p.max_pages;
+    const int end = n + m, first = n / p.P, pages = (end - 1) / p.P - first + 1;
+    for (int g = rank; g < p.Hkv; g += C) {
+      const size_t src0 = ((size_t)b * p.Hkv + g) * T * 128;
+      for (int e = tid; e < m * 16; e += 256) {
+        const int i = e >> 4, piece = e & 15, pos = n + i, phys = ptab[pos / p.P];
+        if (!phys_ok(p, phys)) continue;
+        const size_t dst = (((size_t)phys * p.Hkv + g) * p.P + pos % p.P) * 128, src = src0 + (size_t)path[i] * 128;
+        reinterpret_cast<uint4*>(p.k_pages + dst)[piece] = reinterpret_cast<const uint4*>(p.k_new + src)[piece];
+        reinterpret_cast<uint4*>(p.v_pages + dst)[piece] = reinterpret_cast<const uint4*>(p.v_new + src)[piece];
+      }
+      for (int e = tid; e < pages * 128; e += 256) {
+        const int pg = first + (e >> 7), c = e & 127;
+        if (!phys_ok(p, ptab[pg])) continue;
+        const size_t at = ((size_t)(b * p.Hkv + g) * 128 + c) * p.max_pages + pg;
+        const int s0 = max(n, pg * p.P), s1 = min(end, (pg + 1) * p.P);
+        float mx = -INFINITY, mn = INFINITY;
+        if (s0 > pg * p.P) {  // the page held tokens before: its summary is of them
+          mx = bf16_f(p.kmax[at]);
+          mn = bf16_f(p.kmin[at]);
+        }
+        for (int t = s0; t < s1; ++t) {
+          const float x = bf16_f(p.k_new[src0 + (size_t)path[t - n] * 128 + c]);
+          mx = fmaxf(mx, x);
+          mn = fminf(mn, x);
+        }
+        p.kmax[at] = (rkv_bf16)(__float_as_uint(mx) >> 16);
+        p.kmin[at] = (rkv_bf16)(__float_as_uint(mn) >> 16);
+      }
+    }
+  }
+  cluster.sync();  // every CTA has read the old length
+  if (rank == 0 && tid == 0 && !bad) p.seq_len[b] = n + m;
+}
+
 }  // namespace
 
-cudaError_t launch_append(const rkv_cache& c, const rkv_bf16* k_new, const rkv_bf16* v_new, int n_new,
-                          cudaStream_t s) {
+static AppendParams append_params(const rkv_cache& c, const rkv_bf16* k_new, const rkv_bf16* v_new, int n_new) {
   AppendParams p;
   p.k_pages = c.k_pages;
   p.v_pages = c.v_pages;
@@ -192,6 +264,12 @@ cudaError_t launch_append(const rkv_cache& c, const rkv_bf16* k_new, const rkv_b
   p.max_pages = c.max_pages;
   p.num_phys = c.num_phys_pages;
   p.n_new = n_new;
+  return p;
+}
+
+cudaError_t launch_append(const rkv_cache& c, const rkv_bf16* k_new, const rkv_bf16* v_new, int n_new,
+                          cudaStream_t s) {
+  const AppendParams p = append_params(c, k_new, v_new, n_new);
   if (n_new <= 16) {
     launch_begin(K_APPEND_SMALL, s);
     append_small_kernel<<<c.B, 256, 0, s>>>(p);
@@ -206,6 +284,31 @@ cudaError_t launch_append(const rkv_cache& c, const rkv_bf16* k_new, const rkv_b
     launch_end(K_APPEND_ADVANCE, s);
   }
   return cudaGetLastError();
+}
+
+cudaError_t launch_commit(const CommitArgs& a, cudaStream_t s) {
+  CommitParams p;
+  p.a = append_params(a.cache, a.k_tree, a.v_tree, a.T);
+  p.path = a.path;
+  p.path_len = a.path_len;
+  p.path_stride = a.path_stride;
+  int C = 1;
+  while (C < 8 && 2 * C <= a.cache.Hkv) C *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C, a.cache.B);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  launch_begin(K_TREE_COMMIT, s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_commit_kernel, p);
+  launch_end(K_TREE_COMMIT, s);
+  return e;
 }
 
 }  // namespace rkv

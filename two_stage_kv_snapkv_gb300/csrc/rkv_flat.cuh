@@ -1,0 +1,101 @@
+// A flat split of ragged units over a grid, from lengths that only the device knows.
+//
+// Every sequence b holds `per_unit(b)` pieces of work (key chunks, token blocks) for each
+// of its `units(b)` units (KV heads, row tiles).  All units' pieces in order (b major)
+// form one line of `total` pieces and CTA i of N takes [i total / N, (i + 1) total / N):
+// the grid is sized without the lengths, and no CTA carries more than one piece above
+// the mean.  Each CTA rebuilds the table (one load a sequence and a warp scan, measured
+// well under a microsecond).
+#pragma once
+
+#include "rkv_device.cuh"
+
+namespace rkv {
+
+struct FlatTable {
+  long long base[RKV_MAX_BATCH + 1];  // pieces before sequence b
+  int n[RKV_MAX_BATCH];               // tokens of sequence b (0 when its length is not usable)
+  int t[RKV_MAX_BATCH];               // query rows (nodes) of sequence b
+  int per[RKV_MAX_BATCH];             // pieces of each of its units
+  int units[RKV_MAX_BATCH];           // its units
+};
+
+// len(b) -> tokens, rows(b) -> nodes, per(n, t) -> pieces a unit, units(t) -> units.
+// Called by every thread of the block (at least 32); ends with a block barrier.
+template <class Len, class Rows, class Per, class Units>
+__device__ __forceinline__ void flat_build(FlatTable& ft, int B, Len len, Rows rows, Per per, Units units) {
+  const int tid = threadIdx.x;
+  for (int b = tid; b < B; b += blockDim.x) {
+    ft.n[b] = len(b);
+    ft.t[b] = rows(b);
+    ft.per[b] = per(ft.n[b], ft.t[b]);
+    ft.units[b] = units(ft.t[b]);
+  }
+  __syncthreads();
+  if (tid < 32) {
+    constexpr int kEach = RKV_MAX_BATCH / 32;
+    long long s = 0;
+    for (int j = 0; j < kEach; ++j) {
+      const int b = tid * kEach + j;
+      if (b < B) s += (long long)ft.per[b] * ft.units[b];
+    }
+    long long incl = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (tid >= o) incl += y;
+    }
+    long long at = incl - s;
+    for (int j = 0; j < kEach; ++j) {
+      const int b = tid * kEach + j;
+      if (b < B) {
+        ft.base[b] = at;
+        at += (long long)ft.per[b] * ft.units[b];
+        if (b == B - 1) ft.base[B] = at;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// CTAs that take part: no more than there are pieces, so that no share is empty and every
+// CTA between a unit's first and last holds a part of it.
+__device__ __forceinline__ int flat_ctas(long long total, int N) { return (int)min((long long)N, total); }
+__device__ __forceinline__ long long flat_first(long long total, int i, int N) { return total * i / N; }
+// The CTA whose share holds piece x.
+__device__ __forceinline__ int flat_cta(long long x, long long total, int N) {
+  return (int)(((x + 1) * N - 1) / total);
+}
+// The sequence that holds piece x (0 <= x < base[B]).
+__device__ __forceinline__ int flat_seq(const FlatTable& ft, int B, long long x) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (ft.base[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Walks the pieces of a share a run at a time: a run is the share's part of one unit.
+struct FlatRun {
+  int b, unit;           // sequence, unit inside it
+  int lo, hi;            // the run's pieces of the unit
+  int whole;             // the run is the whole unit
+  int first;             // the run starts the share
+  long long x;           // the run's first piece
+};
+__device__ __forceinline__ bool flat_run(const FlatTable& ft, int B, long long x, long long x0, long long x1, FlatRun& r) {
+  if (x >= x1) return false;
+  r.b = flat_seq(ft, B, x);
+  const int per = ft.per[r.b];
+  const long long off = x - ft.base[r.b];
+  r.unit = (int)(off / per);
+  r.lo = (int)(off - (long long)r.unit * per);
+  r.hi = (int)min((long long)per, r.lo + (x1 - x));
+  r.whole = r.lo == 0 && r.hi == per;
+  r.first = x == x0;
+  r.x = x;
+  return true;
+}
+
+}  // namespace rkv

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "rkv.h"
 
 namespace rkv {
@@ -33,6 +35,14 @@ enum KernelKind {
   K_SPARQ_ATTEND,
   K_WAIT_SELFTEST,
   K_SPARQ_KEYS_SYNC,
+  K_ATTEND_ROWS,
+  K_ATTEND_COMBINE,
+  K_ATTEND_WEIGH,
+  K_TREE_COMMIT,
+  K_ACCUM_ROWS,
+  K_EVICT_SELECT,
+  K_EVICT_STAGE,
+  K_EVICT_COMPACT,
   K_NUM_KINDS
 };
 const char* kernel_name(int kind);
@@ -41,6 +51,22 @@ const char* kernel_name(int kind);
 void launch_begin(int kind, cudaStream_t stream);
 void launch_end(int kind, cudaStream_t stream);
 int num_sms();
+// SMs a workspace is laid out for (a grid never has more CTAs per SM slot than this).
+constexpr int kMaxSms = 256;
+// Raises a kernel's dynamic shared memory limit, once for each device it runs on.
+struct SmemOptIn {
+  std::atomic<uint64_t> done{0};
+  cudaError_t raise(const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+};
 // Sets the message rkv_last_error() returns on this thread.
 void set_last_error(const char* msg);
 
@@ -121,6 +147,69 @@ size_t sparq_keys_bytes(int B, int Hkv, int max_pages, int page_size);
 cudaError_t launch_sparq(const DecodeArgs& a, cudaStream_t s);
 bool decode_fused_ok(const rkv_cache& c);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
+
+// --------------------------------------------------------------- dense rows: tree and weights
+struct AttendArgs {
+  rkv_cache cache;
+  const rkv_bf16* q;  // [B][Hq][T][128]
+  int Hq, T;
+  const rkv_bf16* k_tree;  // [B][Hkv][T][128] (mask given)
+  const rkv_bf16* v_tree;
+  const uint32_t* mask;     // [B][T][ceil(T/32)], null: the cache alone
+  const int32_t* tree_len;  // device [B] or null
+  float scale;
+  rkv_bf16* out;
+  float* lse;  // may be null
+  float* acc;  // [B][Hkv][acc_stride] (T == 1, no mask) or null
+  int acc_stride;
+  void* ws;
+};
+size_t attend_ws_bytes(int B, int Hq, int Hkv, int T, int max_pages, int page_size, bool weights);
+cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s);
+
+struct CommitArgs {
+  rkv_cache cache;
+  const rkv_bf16* k_tree;
+  const rkv_bf16* v_tree;
+  int T;
+  const int32_t* path;  // device [B][path_stride]
+  int path_stride;
+  const int32_t* path_len;  // device [B]
+};
+cudaError_t launch_commit(const CommitArgs& a, cudaStream_t s);
+
+struct AccumRowsArgs {
+  rkv_cache cache;
+  const rkv_bf16* q;  // [B][Hq][T][128]
+  const float* lse;   // [B][Hq][T]
+  int Hq, T;
+  const int32_t* row_len;  // device [B] or null
+  const int32_t* row_ids;  // device [B][ids_stride] or null
+  int ids_stride;
+  float scale;
+  float* acc;
+  int acc_stride;
+  void* ws;
+};
+size_t accum_rows_ws_bytes(int B, int Hq, int Hkv, int T, int max_pages, int page_size);
+cudaError_t launch_accum_rows(const AccumRowsArgs& a, cudaStream_t s);
+
+struct EvictArgs {
+  rkv_cache cache, dst;
+  bool in_place;
+  const float* acc;
+  int acc_stride;
+  float* dst_acc;
+  int dst_acc_stride;
+  const int32_t* keep;  // host [B]
+  int recent;
+  int32_t* kept_idx;
+  int kept_stride;
+  void* ws;
+};
+int evict_max_tokens();
+size_t evict_ws_bytes(int B, int Hkv, int max_keep, bool in_place);
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 
 // --------------------------------------------------------------- diagnostics
 struct RecallArgs {

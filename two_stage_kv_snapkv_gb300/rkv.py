@@ -27,8 +27,10 @@ DEVERR_PAGE_ID = 0x1
 DEVERR_CAPACITY = 0x2
 DEVERR_TIMEOUT = 0x4
 DEVERR_SEQ_LEN = 0x8
+DEVERR_TREE = 0x10
 HEAD_DIM = 128
 MAX_BATCH = 256
+MAX_TREE = 256
 
 
 class RkvError(RuntimeError):
@@ -104,6 +106,25 @@ _lib.rkv_decode_sparq.argtypes = [ctypes.POINTER(RkvCacheStruct), _vp, _i32, _i3
 _lib.rkv_sparq_keys_size.argtypes = [_i32, _i32, _i32, _i32]
 _lib.rkv_sparq_keys_size.restype = _sz
 _lib.rkv_decode_sparq.restype = _i32
+_cachep = ctypes.POINTER(RkvCacheStruct)
+_lib.rkv_tree_workspace_size.argtypes = [_i32] * 6
+_lib.rkv_tree_workspace_size.restype = _sz
+_lib.rkv_tree_attention.argtypes = [_cachep, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _f32, _vp, _vp, _vp, _sz, _vp]
+_lib.rkv_tree_attention.restype = _i32
+_lib.rkv_tree_commit.argtypes = [_cachep, _vp, _vp, _i32, _vp, _i32, _vp, _vp]
+_lib.rkv_tree_commit.restype = _i32
+_lib.rkv_accum_workspace_size.argtypes = [_i32] * 5
+_lib.rkv_accum_workspace_size.restype = _sz
+_lib.rkv_decode_accum.argtypes = [_cachep, _vp, _i32, _f32, _vp, _vp, _vp, _i32, _vp, _sz, _vp]
+_lib.rkv_decode_accum.restype = _i32
+_lib.rkv_accum_rows_workspace_size.argtypes = [_i32] * 6
+_lib.rkv_accum_rows_workspace_size.restype = _sz
+_lib.rkv_accum_rows.argtypes = [_cachep, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _f32, _vp, _i32, _vp, _sz, _vp]
+_lib.rkv_accum_rows.restype = _i32
+_lib.rkv_evict_workspace_size.argtypes = [_i32] * 4
+_lib.rkv_evict_workspace_size.restype = _sz
+_lib.rkv_evict_accum.argtypes = [_cachep, _vp, _i32, _i32p, _i32, _vp, _i32, _cachep, _vp, _i32, _vp, _sz, _vp]
+_lib.rkv_evict_accum.restype = _i32
 _lib.rkv_exact_topk_recall.argtypes = [ctypes.POINTER(RkvCacheStruct), _vp, _i32, _vp, _i32, _i32p, _f32, _vp, _vp,
                                        _vp]
 _lib.rkv_exact_topk_recall.restype = _i32
@@ -130,7 +151,9 @@ EXPORTED = ["rkv_split_ratio", "rkv_split_ratio_mt", "rkv_prefill_workspace_size
             "rkv_prefill_chunk_workspace_size", "rkv_prefill_chunk", "rkv_append_page_summary",
             "rkv_decode_workspace_size", "rkv_decode_hsa", "rkv_decode_hsa_noalloc", "rkv_decode_step",
             "rkv_decode_path", "rkv_step_host_staging_size", "rkv_decode_step_host", "rkv_sparq_workspace_size", "rkv_decode_sparq", "rkv_sparq_keys_size",
-            "rkv_exact_topk_recall", "rkv_selftest_bounded_wait", "rkv_get_device_status", "rkv_last_error",
+            "rkv_tree_workspace_size", "rkv_tree_attention", "rkv_tree_commit", "rkv_accum_workspace_size",
+            "rkv_decode_accum", "rkv_accum_rows_workspace_size", "rkv_accum_rows", "rkv_evict_workspace_size",
+            "rkv_evict_accum", "rkv_exact_topk_recall", "rkv_selftest_bounded_wait", "rkv_get_device_status", "rkv_last_error",
             "rkv_launch_count", "rkv_profile_enable", "rkv_profile_accumulate", "rkv_profile_release",
             "rkv_profile_reset", "rkv_profile_read"]
 
@@ -375,6 +398,180 @@ def rkv_decode_sparq(cache: PagedCache, q: torch.Tensor, k1: Sequence[int], k_to
     _check(_lib.rkv_decode_sparq(ctypes.byref(cache.struct), _ptr(q), Hq, _host_i32(k1), _host_i32(k_tokens), scale,
                                  _ptr(out), _ptr(sel_channels), _ptr(sel_tokens), stride, _ptr(keys_t), kt_bytes,
                                  _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+# ------------------------------------------------------------------ tree decoding, accumulated weights
+def _want(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype, device) -> None:
+    if t is None:
+        return
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: expected {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _want_acc(acc: torch.Tensor, name: str, cache: "PagedCache", device) -> None:
+    if acc.dim() != 3:
+        raise ValueError(f"{name}: expected [B, Hkv, positions], got {list(acc.shape)}")
+    _want(acc, name, (cache.B, cache.Hkv, acc.shape[2]), torch.float32, device)
+
+
+def _want_ws(workspace: torch.Tensor, device) -> None:
+    if workspace.dtype != torch.uint8 or workspace.device != device:
+        raise ValueError(f"workspace: expected torch.uint8 on {device}, got {workspace.dtype} on {workspace.device}")
+
+
+def _call_on(device, stream, fn, *args) -> None:
+    """fn(*args, stream) with the tensors' device current (its current stream when none is given)."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)))
+
+
+def tree_workspace(B: int, Hq: int, Hkv: int, T: int, max_pages: int, page_size: int, device="cuda") -> torch.Tensor:
+    n = _lib.rkv_tree_workspace_size(B, Hq, Hkv, T, max_pages, page_size)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def rkv_tree_attention(cache: PagedCache, q: torch.Tensor, k_tree: torch.Tensor, v_tree: torch.Tensor,
+                       tree_mask: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                       tree_len: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of T drafted nodes ([B, Hq, T, 128] q, [B, Hkv, T, 128] k_tree / v_tree)
+    over the cache and, through tree_mask ([B, T, ceil(T/32)] int32 bit words), each other.
+    out is bf16 [B, Hq, T, 128], lse fp32 [B, Hq, T], tree_len int32 [B] on the device."""
+    if q.dim() != 4:
+        raise ValueError(f"q: expected [B, Hq, T, {HEAD_DIM}], got {list(q.shape)}")
+    B, Hq, T, d = q.shape
+    dev = cache.k_pages.device
+    bf16 = torch.bfloat16
+    _want(q, "q", (cache.B, Hq, T, HEAD_DIM), bf16, dev)
+    _want(k_tree, "k_tree", (B, cache.Hkv, T, HEAD_DIM), bf16, dev)
+    _want(v_tree, "v_tree", (B, cache.Hkv, T, HEAD_DIM), bf16, dev)
+    _want(tree_mask, "tree_mask", (B, T, (T + 31) // 32), torch.int32, dev)
+    _want(out, "out", (B, Hq, T, HEAD_DIM), bf16, dev)
+    _want(lse, "lse", (B, Hq, T), torch.float32, dev)
+    _want(tree_len, "tree_len", (B,), torch.int32, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if workspace is None:
+        workspace = tree_workspace(B, Hq, cache.Hkv, T, cache.max_pages, cache.page_size, dev)
+    _want_ws(workspace, dev)
+    _call_on(dev, stream, _lib.rkv_tree_attention, ctypes.byref(cache.struct), _ptr(q), _ptr(k_tree), _ptr(v_tree),
+             _ptr(tree_mask), Hq, T, _ptr(tree_len), scale, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel())
+
+
+def rkv_tree_commit(cache: PagedCache, k_tree: torch.Tensor, v_tree: torch.Tensor, path: torch.Tensor,
+                    path_len: torch.Tensor, stream=None):
+    """Append the accepted nodes path[b, :path_len[b]] (int32, on the device) of the tree
+    to the cache and fold them into the page summaries."""
+    if k_tree.dim() != 4 or path.dim() != 2:
+        raise ValueError("k_tree: expected [B, Hkv, T, 128]; path: expected [B, nodes]")
+    T = k_tree.shape[2]
+    dev = cache.k_pages.device
+    _want(k_tree, "k_tree", (cache.B, cache.Hkv, T, HEAD_DIM), torch.bfloat16, dev)
+    _want(v_tree, "v_tree", (cache.B, cache.Hkv, T, HEAD_DIM), torch.bfloat16, dev)
+    _want(path, "path", (cache.B, path.shape[1]), torch.int32, dev)
+    _want(path_len, "path_len", (cache.B,), torch.int32, dev)
+    _call_on(dev, stream, _lib.rkv_tree_commit, ctypes.byref(cache.struct), _ptr(k_tree), _ptr(v_tree), T, _ptr(path),
+             path.shape[1], _ptr(path_len))
+
+
+def accum_workspace(B: int, Hq: int, Hkv: int, max_pages: int, page_size: int, device="cuda") -> torch.Tensor:
+    n = _lib.rkv_accum_workspace_size(B, Hq, Hkv, max_pages, page_size)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def accum_sums(cache: "PagedCache") -> torch.Tensor:
+    """Zeroed sums for rkv_decode_accum, rkv_accum_rows and rkv_evict_accum on this cache."""
+    return torch.zeros((cache.B, cache.Hkv, cache.max_pages * cache.page_size), dtype=torch.float32,
+                       device=cache.k_pages.device)
+
+
+def rkv_decode_accum(cache: PagedCache, q: torch.Tensor, out: torch.Tensor, acc: torch.Tensor,
+                     lse: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """One-token attention over the whole cache (q, out: bf16 [B, Hq, 128]) that adds every
+    position's weight, summed over the group's heads, to acc (accum_sums)."""
+    if q.dim() != 3:
+        raise ValueError(f"q: expected [B, Hq, {HEAD_DIM}], got {list(q.shape)}")
+    B, Hq, d = q.shape
+    dev = cache.k_pages.device
+    _want(q, "q", (cache.B, Hq, HEAD_DIM), torch.bfloat16, dev)
+    _want(out, "out", (B, Hq, HEAD_DIM), torch.bfloat16, dev)
+    _want(lse, "lse", (B, Hq), torch.float32, dev)
+    _want_acc(acc, "acc", cache, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if workspace is None:
+        workspace = accum_workspace(B, Hq, cache.Hkv, cache.max_pages, cache.page_size, dev)
+    _want_ws(workspace, dev)
+    _call_on(dev, stream, _lib.rkv_decode_accum, ctypes.byref(cache.struct), _ptr(q), Hq, scale, _ptr(out), _ptr(lse),
+             _ptr(acc), acc.shape[2], _ptr(workspace), workspace.numel())
+
+
+def accum_rows_workspace(B: int, Hq: int, Hkv: int, T: int, max_pages: int, page_size: int,
+                         device="cuda") -> torch.Tensor:
+    n = _lib.rkv_accum_rows_workspace_size(B, Hq, Hkv, T, max_pages, page_size)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def rkv_accum_rows(cache: PagedCache, q: torch.Tensor, lse: torch.Tensor, acc: torch.Tensor,
+                   row_len: Optional[torch.Tensor] = None, row_ids: Optional[torch.Tensor] = None,
+                   scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Add to acc the weights of query rows whose attention is done (q bf16 [B, Hq, T, 128],
+    their lse fp32 [B, Hq, T]): row i, or row row_ids[b, i], stands at position
+    seq_len[b] - row_len[b] + i of the cache."""
+    if q.dim() != 4:
+        raise ValueError(f"q: expected [B, Hq, T, {HEAD_DIM}], got {list(q.shape)}")
+    B, Hq, T, d = q.shape
+    dev = cache.k_pages.device
+    _want(q, "q", (cache.B, Hq, T, HEAD_DIM), torch.bfloat16, dev)
+    _want(lse, "lse", (B, Hq, T), torch.float32, dev)
+    _want(row_len, "row_len", (B,), torch.int32, dev)
+    if row_ids is not None and row_ids.dim() != 2:
+        raise ValueError(f"row_ids: expected [B, rows], got {list(row_ids.shape)}")
+    ids = row_ids.shape[1] if row_ids is not None else 0
+    _want(row_ids, "row_ids", (B, ids), torch.int32, dev)
+    _want_acc(acc, "acc", cache, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if workspace is None:
+        workspace = accum_rows_workspace(B, Hq, cache.Hkv, T, cache.max_pages, cache.page_size, dev)
+    _want_ws(workspace, dev)
+    _call_on(dev, stream, _lib.rkv_accum_rows, ctypes.byref(cache.struct), _ptr(q), _ptr(lse), Hq, T, _ptr(row_len),
+             _ptr(row_ids), ids, scale, _ptr(acc), acc.shape[2], _ptr(workspace), workspace.numel())
+
+
+def evict_workspace(B: int, Hkv: int, max_keep: int, device="cuda", in_place: bool = True) -> torch.Tensor:
+    n = _lib.rkv_evict_workspace_size(B, Hkv, max_keep, 1 if in_place else 0)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def rkv_evict_accum(cache: PagedCache, acc: torch.Tensor, keep: Sequence[int], recent: int, kept_idx: torch.Tensor,
+                    dst: Optional[PagedCache] = None, dst_acc: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None):
+    """Cut every sequence to its keep[b] tokens: the `recent` last and the heaviest by acc
+    of the others, per KV head; in place, or into dst and dst_acc.  kept_idx (int32
+    [B, Hkv, >= max(keep)]) receives the kept positions, ascending."""
+    dev = cache.k_pages.device
+    if len(keep) != cache.B:
+        raise ValueError(f"keep: expected {cache.B} values, got {len(keep)}")
+    if kept_idx.dim() != 3:
+        raise ValueError(f"kept_idx: expected [B, Hkv, tokens], got {list(kept_idx.shape)}")
+    _want(kept_idx, "kept_idx", (cache.B, cache.Hkv, kept_idx.shape[2]), torch.int32, dev)
+    _want_acc(acc, "acc", cache, dev)
+    if dst is not None and dst.k_pages.device != dev:
+        raise ValueError("dst lies on another device")
+    if dst_acc is not None:
+        _want_acc(dst_acc, "dst_acc", cache if dst is None else dst, dev)
+    if workspace is None:
+        workspace = evict_workspace(cache.B, cache.Hkv, max(1, max(int(x) for x in keep)), dev,
+                                    in_place=dst is None)
+    _want_ws(workspace, dev)
+    _call_on(dev, stream, _lib.rkv_evict_accum, ctypes.byref(cache.struct), _ptr(acc), acc.shape[2], _host_i32(keep),
+             int(recent), _ptr(kept_idx), kept_idx.shape[2], ctypes.byref(dst.struct) if dst is not None else None,
+             _ptr(dst_acc), dst_acc.shape[2] if dst_acc is not None else 0, _ptr(workspace), workspace.numel())
 
 
 def rkv_exact_topk_recall(cache: PagedCache, q: torch.Tensor, sel_pages: torch.Tensor, k_tokens: Sequence[int],
