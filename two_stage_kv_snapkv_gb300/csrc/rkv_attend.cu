@@ -34,8 +34,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWeighTokens = 1024;                // tokens of a weighing block
 
 struct AttendParams {
-  CUtensorMap tmk, tmv;    // the page pools as [rows][128] bf16, 16-row x 64-channel boxes
-  CUtensorMap tmkt, tmvt;  // the tree's keys and values, the same boxes (T > 0 nodes given)
+  CUtensorMap tmk, tmv;    // the page pools as [rows][128] bf16, 16-row x 64-channel boxes (the tiled
+                           // kernel: a page's rows)
+  CUtensorMap tmkt, tmvt;  // the tree's keys and values, the same boxes (the tiled kernel: 128 rows)
   const rkv_bf16* q;       // [B][Hq][T][128]
   const uint32_t* mask;    // [B][T][words], null: no tree
   const int32_t* page_table;
@@ -44,8 +45,8 @@ struct AttendParams {
   int32_t* err;
   rkv_bf16* out;            // [B][Hq][T][128]
   float* lse;               // [B][Hq][T], may be null
-  float* part_o;            // [2 N][16][128]
-  float2* part_ml;          // [2 N][16]
+  float* part_o;            // [2 N][tile rows][128]
+  float2* part_ml;          // [2 N][tile rows]
   float2* row_ml;           // [B][Hkv][G]: final (m, l) of a one-token step, for the weights
   float* z;                 // [B][Hkv][G][zstride] base-2 scaled logits of a one-token step, or null
   float* acc;               // [B][Hkv][acc_stride]
@@ -70,11 +71,12 @@ __device__ __forceinline__ int checked_nodes(const AttendParams& p, int b) {
   return t;
 }
 
-__device__ __forceinline__ void build_rows_table(const AttendParams& p, FlatTable& ft) {
+template <int kRows, int kKeys>
+__device__ __forceinline__ void build_table(const AttendParams& p, FlatTable& ft) {
   flat_build(
       ft, p.B, [&](int b) { return checked_len(p, b); }, [&](int b) { return checked_nodes(p, b); },
-      [&](int n, int t) { return (n + kArKeys - 1) / kArKeys + (p.mask ? (t + kArKeys - 1) / kArKeys : 0); },
-      [&](int t) { return p.Hkv * ((t * p.G + kArRows - 1) / kArRows); });
+      [&](int n, int t) { return (n + kKeys - 1) / kKeys + (p.mask ? (t + kKeys - 1) / kKeys : 0); },
+      [&](int t) { return p.Hkv * ((t * p.G + kRows - 1) / kRows); });
 }
 
 // Rows 16 rt .. of unit (b, g): node and head of row r.
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(kArThreads, 1) attend_rows_kernel(const __grid
   if (lane == 0)
     for (int s = 0; s < kArStages; ++s) mbar_init(&full_b[warp][s], 1);
   if (tid == 0) fence_mbar_init();
-  build_rows_table(p, ft);
+  build_table<kArRows, kArKeys>(p, ft);
   grid_launch_dependents();
   const long long total = ft.base[p.B];
   const int N = flat_ctas(total, p.N);
@@ -361,84 +363,596 @@ __device__ __forceinline__ size_t part_slot(long long ux, long long total, int c
   return 2 * (size_t)c + (flat_first(total, c, N) >= ux ? 0 : 1);
 }
 
-// Joins the parts of the split units.  One CTA of 128 threads per (row tile x KV head,
-// sequence), thread = channel; it reads the parts (L2 resident) once.
-__global__ void __launch_bounds__(128) attend_combine_kernel(const __grid_constant__ AttendParams p) {
-  __shared__ FlatTable ft;
-  grid_dependency_wait();
-  build_rows_table(p, ft);
+// Final (m, l) of one row of a split unit: the lanes of a warp take the parts c0 .. c1.
+template <int kRows>
+__device__ __forceinline__ float2 join_ml(const AttendParams& p, long long ux, long long total, int N, int c0, int c1,
+                                          int row, int lane) {
+  float M = kNoMax;
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_ml[part_slot(ux, total, c, N) * kRows + row].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.f;
+  for (int c = c0 + lane; c <= c1; c += 32) {
+    const float2 ml = p.part_ml[part_slot(ux, total, c, N) * kRows + row];
+    L += ml.y * ex2_approx(ml.x - M);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  return make_float2(M, L);
+}
+
+// Joins the parts of the split units: one warp a row, four channels a lane, eight parts'
+// loads in flight.  grid (ceil(rows of a sequence / 8), B), 256 threads.
+template <int kRows, int kKeys>
+__device__ __forceinline__ void combine_row(const AttendParams& p, const FlatTable& ft, int b, int idx, int lane) {
   const long long total = ft.base[p.B];
   const int N = flat_ctas(total, p.N);
-  const int d = threadIdx.x;
-  const int b = blockIdx.y;
-  for (int unit = blockIdx.x; unit < ft.units[b]; unit += gridDim.x) {
-    const int g = unit % p.Hkv, rt = unit / p.Hkv;
-    const int live = min(kArRows, ft.t[b] * p.G - rt * kArRows);
-    const int per = ft.per[b];
-    if (per == 0) {  // nothing to see: no token cached and no tree
-      for (int r = 0; r < live; ++r) {
-        const size_t orow = out_row(p, b, g, rt * kArRows + r);
-        p.out[orow * 128 + d] = 0;
-        if (d == 0 && p.lse) p.lse[orow] = -INFINITY;
-      }
-      continue;
-    }
-    const long long ux = ft.base[b] + (long long)unit * per;
-    const int c0 = flat_cta(ux, total, N), c1 = flat_cta(ux + per - 1, total, N);
-    if (c0 == c1) continue;  // final already
-    for (int r = 0; r < live; ++r) {
-      float M = kNoMax;
-      for (int c = c0; c <= c1; ++c) M = fmaxf(M, p.part_ml[part_slot(ux, total, c, N) * kArRows + r].x);
-      float L = 0.f, o = 0.f;
-      for (int c = c0; c <= c1; ++c) {
-        const size_t at = part_slot(ux, total, c, N) * kArRows + r;
-        const float2 ml = p.part_ml[at];
-        const float f = ex2_approx(ml.x - M);
-        L += ml.y * f;
-        o += p.part_o[at * 128 + d] * f;
-      }
-      const size_t orow = out_row(p, b, g, rt * kArRows + r);
-      const __nv_bfloat16 v = __float2bfloat16_rn(L > 0.f ? o / L : 0.f);
-      p.out[orow * 128 + d] = *reinterpret_cast<const rkv_bf16*>(&v);
-      if (d == 0) {
-        if (p.lse) p.lse[orow] = lse_of(M, L);
-        if (p.z) p.row_ml[((size_t)b * p.Hkv + g) * p.G + r] = make_float2(M, L);
+  const int t = ft.t[b], per = ft.per[b];
+  const int rows = t * p.G;  // query rows of a unit's KV head
+  if (idx >= rows * p.Hkv) return;
+  const int g = idx / rows, r = idx - g * rows, rt = r / kRows, row = r % kRows;
+  const size_t orow = out_row(p, b, g, r);
+  uint2* out = reinterpret_cast<uint2*>(p.out + orow * 128) + lane;
+  if (per == 0) {  // nothing to see: no token cached and no tree
+    *out = make_uint2(0u, 0u);
+    if (lane == 0 && p.lse) p.lse[orow] = -INFINITY;
+    return;
+  }
+  const long long ux = ft.base[b] + (long long)(rt * p.Hkv + g) * per;
+  const int c0 = flat_cta(ux, total, N), c1 = flat_cta(ux + per - 1, total, N);
+  if (c0 == c1) return;  // final already
+  const float2 ml = join_ml<kRows>(p, ux, total, N, c0, c1, row, lane);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0; c <= c1; c += 8) {
+    float4 v[8];
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f[j] = 0.f;
+      v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c + j <= c1) {
+        const size_t at = part_slot(ux, total, c + j, N) * kRows + row;
+        f[j] = p.part_ml[at].x;
+        v[j] = reinterpret_cast<const float4*>(p.part_o + at * 128)[lane];
       }
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j <= c1) {
+        const float w = ex2_approx(f[j] - ml.x);
+        o.x += v[j].x * w;
+        o.y += v[j].y * w;
+        o.z += v[j].z * w;
+        o.w += v[j].w * w;
+      }
+  }
+  const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
+  *out = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (lane == 0 && p.lse) p.lse[orow] = lse_of(ml.x, ml.y);
+}
+
+template <int kRows, int kKeys>
+__global__ void __launch_bounds__(256) attend_combine_kernel(const __grid_constant__ AttendParams p) {
+  __shared__ FlatTable ft;
+  build_table<kRows, kKeys>(p, ft);  // lengths only: they were final before the parts' kernel began
+  grid_dependency_wait();
+  combine_row<kRows, kKeys>(p, ft, blockIdx.y, blockIdx.x * 8 + (threadIdx.x >> 5), threadIdx.x & 31);
+}
+
+// The end of a one-token step: the first CTAs join the rows as attend_combine does, the
+// others add the weights, acc_j += sum_h 2^(z_hj - m_h) / l_h, over blocks of
+// kWeighTokens tokens of a (sequence, KV head), four tokens a thread; each block joins its
+// heads' (m, l) for itself.  The logits were written a moment ago and mostly lie in L2.
+__global__ void __launch_bounds__(256) attend_weigh_kernel(const __grid_constant__ AttendParams p) {
+  __shared__ FlatTable ft;
+  __shared__ float lse2[8];
+  __shared__ long long wbase[RKV_MAX_BATCH + 1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  build_table<kArRows, kArKeys>(p, ft);
+  flat_scan(wbase, p.B, [&](int b) { return (long long)p.Hkv * ((ft.n[b] + kWeighTokens - 1) / kWeighTokens); });
+  grid_dependency_wait();
+  const int joins = p.B * ((p.Hq + 7) / 8);
+  if ((int)blockIdx.x < joins) {
+    const int per_b = (p.Hq + 7) / 8;
+    combine_row<kArRows, kArKeys>(p, ft, blockIdx.x / per_b, (blockIdx.x % per_b) * 8 + warp, lane);
+    return;
+  }
+  const long long total = ft.base[p.B];
+  const int N = flat_ctas(total, p.N);
+  for (long long x = blockIdx.x - joins; x < wbase[p.B]; x += gridDim.x - joins) {
+    int b = 0, hi = p.B - 1;
+    while (b < hi) {
+      const int mid = (b + hi + 1) >> 1;
+      if (wbase[mid] <= x) b = mid; else hi = mid - 1;
+    }
+    const int n = ft.n[b], blocks = (n + kWeighTokens - 1) / kWeighTokens;
+    const int g = (int)((x - wbase[b]) / blocks), blk = (int)((x - wbase[b]) % blocks);
+    const size_t unit = (size_t)b * p.Hkv + g;
+    if (warp < p.G) {
+      const long long ux = ft.base[b] + (long long)g * ft.per[b];
+      const int c0 = flat_cta(ux, total, N), c1 = flat_cta(ux + ft.per[b] - 1, total, N);
+      const float2 ml = c0 == c1 ? p.row_ml[unit * p.G + warp]
+                                 : join_ml<kArRows>(p, ux, total, N, c0, c1, warp, lane);
+      if (lane == 0) lse2[warp] = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;  // nothing read: weighs nothing
+    }
+    __syncthreads();
+    const int t = blk * kWeighTokens + tid * 4;
+    if (t < n) {
+      float w[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int h = 0; h < p.G; ++h) {
+        const float base = lse2[h];
+        const float4 z = *reinterpret_cast<const float4*>(p.z + (unit * p.G + h) * p.zstride + t);
+        w[0] += ex2_approx(z.x - base);
+        w[1] += ex2_approx(z.y - base);
+        w[2] += ex2_approx(z.z - base);
+        w[3] += ex2_approx(z.w - base);
+      }
+      float* a = p.acc + unit * p.acc_stride + t;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (t + e < n) a[e] += w[e];
+    }
+    __syncthreads();  // lse2 is free
   }
 }
 
-// The weights of a one-token step: acc_j += sum_h 2^(z_hj - m_h) / l_h.  Blocks of
-// kWeighTokens tokens of a (sequence, KV head), 256 threads with four tokens each; the
-// logits were written a moment ago and mostly still lie in L2.
-__global__ void __launch_bounds__(256) attend_weigh_kernel(const __grid_constant__ AttendParams p) {
+// ---------------------------------------------------------------------------
+// attend_tiles: 17 query rows and more, on the fifth-generation tensor cores.
+//
+// Two row slots of 128 rows work in turn on 128-key tiles: while a slot's four warps turn
+// its logits into weights, the tensor cores run the other slot's products.
+//   S = Q K^T   128 x 128 x 128, both operands in shared memory, S in TMEM;
+//   P           bf16, written back over S's columns (thread = row = TMEM lane);
+//   O += P V    128 x 128 x 128, P from TMEM, V from shared memory, O in TMEM.
+// kWide: a unit's tile is 256 rows, the slots hold different rows and both use every key
+// tile, so the cache is read once for 256 rows.  Otherwise the tile is 128 rows and the
+// slots take alternate key tiles of the same rows, each with its own maximum, sum and O,
+// and join them at the end of a run.  K and V of a key tile are 64 KB, 128 keys x 128
+// channels x 256 rows x 4 = 16.8 MFLOP: at the card's rates the bytes take 1.4 us of an
+// SM's share and the products 1.1 us, so the wide form sits near both roofs and the narrow
+// one on the bytes alone.
+//   warps 0-3, 4-7: softmax of slot 0, 1;  warp 8: TMA;  warp 9: MMA issue.
+// The running maximum that the weights refer to moves only when a row's new maximum is
+// above it by more than 8 (base 2): weights then stay below 2^8 and O is rescaled, a TMEM
+// round trip of 64 KB, a few times a run instead of every tile.
+// Ring entries are 32 KB, a tile's K or V; order and phases are the same formula on the TMA
+// and the MMA side.  Every wait is bounded; one that runs out flags RKV_DEVERR_TIMEOUT and
+// stops every role.
+constexpr int kAtKeys = 128;
+constexpr int kAtThreads = 320;
+constexpr int kAtEntry = 128 * 256;
+constexpr float kAtSlack = 8.f;
+template <bool kWide>
+struct TileShape {
+  static constexpr int kRows = kWide ? 256 : 128;
+  static constexpr int kQBytes = kRows * 256;
+  static constexpr int kEntries = kWide ? 4 : 5;
+  static constexpr int kSmem = 1024 + kQBytes + kEntries * kAtEntry;
+};
+
+template <bool kWide>
+__global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __grid_constant__ AttendParams p) {
+  using Sh = TileShape<kWide>;
+  constexpr int E = Sh::kEntries, R = Sh::kRows;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ FlatTable ft;
-  grid_dependency_wait();
-  flat_build(
-      ft, p.B, [&](int b) { return checked_len(p, b); }, [&](int) { return 1; },
-      [&](int n, int) { return (n + kWeighTokens - 1) / kWeighTokens; }, [&](int) { return p.Hkv; });
-  const long long total = ft.base[p.B];
-  for (long long x = blockIdx.x; x < total; x += gridDim.x) {
-    const int b = flat_seq(ft, p.B, x);
-    const long long off = x - ft.base[b];
-    const int g = (int)(off / ft.per[b]), blk = (int)(off % ft.per[b]);
-    const size_t unit = (size_t)b * p.Hkv + g;
-    const int t = blk * kWeighTokens + threadIdx.x * 4, n = ft.n[b];
-    if (t >= n) continue;
-    float w[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int h = 0; h < p.G; ++h) {
-      const float2 ml = p.row_ml[unit * p.G + h];
-      const float base = ml.x + log2f(ml.y);
-      const float4 z = *reinterpret_cast<const float4*>(p.z + (unit * p.G + h) * p.zstride + t);
-      w[0] += ex2_approx(z.x - base);
-      w[1] += ex2_approx(z.y - base);
-      w[2] += ex2_approx(z.z - base);
-      w[3] += ex2_approx(z.w - base);
+  __shared__ uint64_t full_b[E], empty_b[E], s_b[2], p_b[2], o_b[2], q_b[2], ml_b;
+  __shared__ uint32_t groups[E];   // a K entry's 16-key groups that were loaded (page ids in range)
+  __shared__ uint32_t sgroups[2];  // the same for the tile whose logits a slot holds
+  __shared__ float2 ml_s[2][128];
+  __shared__ uint32_t tmem_base;
+  __shared__ volatile int abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* qs = align1024(smem);
+  uint8_t* ring = qs + Sh::kQBytes;
+  if (tid == 0) {
+    for (int e = 0; e < E; ++e) {
+      mbar_init(&full_b[e], 1);
+      mbar_init(&empty_b[e], 1);
     }
-    float* a = p.acc + unit * p.acc_stride + t;
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_b[s], 2);    // the issuing thread and its commit
+      mbar_init(&p_b[s], 128);
+      mbar_init(&o_b[s], 1);
+      mbar_init(&q_b[s], kWide ? 128 : 256);
+    }
+    mbar_init(&ml_b, 256);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  build_table<R, kAtKeys>(p, ft);  // ends with a block barrier
+  tc_fence_after();
+  grid_launch_dependents();
+  const uint32_t tmem = tmem_base;
+  const long long total = ft.base[p.B];
+  const int N = flat_ctas(total, p.N);
+  const bool works = (int)blockIdx.x < N;
+  const long long x0 = works ? flat_first(total, blockIdx.x, N) : 0, x1 = works ? flat_first(total, blockIdx.x + 1, N) : 0;
+  auto give_up = [&]() {
+    flag_error(p.err, RKV_DEVERR_TIMEOUT);
+    abort_flag = 1;
+  };
+  int loaded = 0;  // ring entries filled (warp 8) or used (warp 9)
+  FlatRun r;
+
+  if (warp == 8) {
+    bool ok = true;
+    for (long long x = x0; ok && flat_run(ft, p.B, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+      const int b = r.b, g = r.unit % p.Hkv, n = ft.n[b], nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
+      const int box = p.P * 128, lanes = 256 / p.P;  // bytes of a box; boxes of a whole tile
+      auto page_of = [&](int tile) {                 // this lane's physical page of a cache tile, -1: none
+        const int pg = tile * (kAtKeys >> p.pshift) + (lane >> 1);
+        if (tile >= nc || lane >= lanes || pg * p.P >= n) return -1;
+        const int phys = p.page_table[(size_t)b * p.max_pages + pg];
+        if (phys >= 0 && phys < p.num_phys) return phys;
+        flag_error(p.err, RKV_DEVERR_PAGE_ID);
+        return -1;
+      };
+      auto issue = [&](int tile, int phys, bool v) {
+        const int e = loaded % E;
+        if (loaded >= E && !mbar_wait(&empty_b[e], (uint32_t)((loaded / E - 1) & 1))) give_up();
+        if (__any_sync(0xffffffffu, abort_flag)) return false;
+        uint8_t* st = ring + e * kAtEntry;
+        if (tile < nc) {
+          const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0);
+          const uint32_t bytes = __popc(have) * box;
+          if (lane == 0) {
+            if (!v) {  // even lanes carry the pages; a page is P / 16 groups
+              uint32_t gr = 0;
+              for (int l = 0; l < lanes; l += 2)
+                if ((have >> l) & 1u) gr |= ((1u << (p.P >> 4)) - 1u) << ((l >> 1) * (p.P >> 4));
+              groups[e] = gr;
+            }
+            if (bytes) mbar_arrive_expect_tx(&full_b[e], bytes);
+            else mbar_arrive(&full_b[e]);
+          }
+          __syncwarp();
+          if (phys >= 0)
+            tma_load_2d(st + (lane & 1) * (kAtEntry / 2) + (lane >> 1) * box, v ? &p.tmv : &p.tmk, (lane & 1) * 64,
+                        (phys * p.Hkv + g) * p.P, &full_b[e]);
+        } else if (lane == 0) {
+          const int row = (b * p.Hkv + g) * p.T + (tile - nc) * kAtKeys;
+          groups[e] = 0xffu;
+          mbar_arrive_expect_tx(&full_b[e], kAtEntry);
+          tma_load_2d(st, v ? &p.tmvt : &p.tmkt, 0, row, &full_b[e]);
+          tma_load_2d(st + kAtEntry / 2, v ? &p.tmvt : &p.tmkt, 64, row, &full_b[e]);
+        }
+        ++loaded;
+        return true;
+      };
+      int cur = page_of(r.lo), next = nt > 1 ? page_of(r.lo + 1) : -1;
+      ok = issue(r.lo, cur, false);
+      for (int i = 0; ok && i < nt; ++i) {
+        const int after = i + 2 < nt ? page_of(r.lo + i + 2) : -1;
+        if (!kWide && i + 1 < nt) ok = issue(r.lo + i + 1, next, false);
+        ok = ok && issue(r.lo + i, cur, true);
+        if (kWide && i + 1 < nt) ok = ok && issue(r.lo + i + 1, next, false);
+        cur = next;
+        next = after;
+      }
+    }
+  } else if (warp == 9) {
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128), idesc_o = idesc_s | kIdescBNMajor;
+    const uint32_t q32 = smem_u32(qs), ring32 = smem_u32(ring);
+    int seen_p[2] = {0, 0}, runs[2] = {0, 0};
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int phase) {
+      if (!mbar_wait(bar, (uint32_t)(phase & 1))) give_up();
+      return !__any_sync(0xffffffffu, abort_flag);
+    };
+    // S of `slot` from the K entry e (its copy has landed)
+    auto mma_s = [&](int slot, int e, bool release) {
+      if (lane == 0) {
+        tc_fence_after();
+        sgroups[slot] = groups[e];
+        const uint32_t qa = q32 + (kWide ? slot * (128 * 256) : 0), ka = ring32 + e * kAtEntry;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (t + e < n) a[e] += w[e];
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t off = (k >> 2) * (kAtEntry / 2) + (k & 3) * 32;
+          tc_mma_bf16(tmem + slot * 256, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off), idesc_s, k > 0);
+        }
+        if (release) tc_commit(&empty_b[e]);
+        tc_commit(&s_b[slot]);
+        mbar_arrive(&s_b[slot]);
+      }
+      __syncwarp();
+    };
+    auto mma_o = [&](int slot, int e, bool first, bool last, bool release) {
+      if (lane == 0) {
+        tc_fence_after();
+        const uint32_t va = ring32 + e * kAtEntry;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc_mma_bf16_ts(tmem + slot * 256 + 128, tmem + slot * 256 + k * 8,
+                         sw128_nmajor_desc(va + k * 2048, kAtEntry / 2), idesc_o, (first && k == 0) ? 0u : 1u);
+        if (release) tc_commit(&empty_b[e]);
+        if (last) tc_commit(&o_b[slot]);
+      }
+      __syncwarp();
+    };
+    for (long long x = x0; ok && flat_run(ft, p.B, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+      const int b = r.b, n = ft.n[b], nodes = ft.t[b], nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
+      const bool two = kWide && nodes * p.G - (r.unit / p.Hkv) * R > 128;  // slot 1 has rows
+      // keys of a tile that may hold anything (behind the end, on a bad page) have weight 0,
+      // and 0 x NaN is not 0: their V rows are cleared first
+      auto clean_v = [&](int tile, int e, uint32_t gr) {
+        const int left = tile < nc ? n - tile * kAtKeys : nodes - (tile - nc) * kAtKeys;
+        if (left >= kAtKeys && gr == 0xffu) return;
+        for (int i = lane; i < 128 * 16; i += 32) {
+          const int row = i >> 4;
+          if (row < left && ((gr >> (row >> 4)) & 1u)) continue;
+          *reinterpret_cast<uint4*>(ring + e * kAtEntry + ((i >> 3) & 1) * (kAtEntry / 2) + row * 128 + (i & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
+      auto take = [&]() {  // the next ring entry, landed
+        const int e = loaded % E;
+        ok = wait(&full_b[e], loaded / E);
+        ++loaded;
+        return e;
+      };
+      ok = wait(&q_b[0], runs[0]++);
+      if (kWide && ok) ok = wait(&q_b[1], runs[1]++);
+      if (!ok) break;
+      if (kWide) {
+        int ek = take();
+        if (!ok) break;
+        uint32_t gr = groups[ek];
+        mma_s(0, ek, !two);
+        if (two) mma_s(1, ek, true);
+        for (int i = 0; i < nt; ++i) {
+          const int ev = take();
+          if (!ok) break;
+          clean_v(r.lo + i, ev, gr);
+          const bool last = i + 1 == nt;
+          if (!(ok = wait(&p_b[0], seen_p[0]++))) break;
+          mma_o(0, ev, i == 0, last, !two);
+          if (last && !two && lane == 0) tc_commit(&o_b[1]);  // keeps an idle slot in step
+          int en = 0;
+          if (!last) {
+            en = take();
+            if (!ok) break;
+            gr = groups[en];
+            mma_s(0, en, !two);
+          }
+          if (two) {
+            if (!(ok = wait(&p_b[1], seen_p[1]++))) break;
+            mma_o(1, ev, i == 0, last, true);
+            if (!last) mma_s(1, en, true);
+          }
+        }
+      } else {
+        uint32_t gr[2];
+        const int e0 = take();
+        if (!ok) break;
+        gr[0] = groups[e0];
+        mma_s(0, e0, true);
+        for (int i = 0; i < nt; ++i) {
+          // order of the entries: K_0, then K_(i+1) and V_i for every i
+          const int slot = i & 1;
+          int en = 0;
+          uint32_t gn = 0;
+          if (i + 1 < nt) {
+            en = take();
+            if (!ok) break;
+            gn = groups[en];
+            if (i == 0) mma_s(1, en, true);
+          }
+          // tile i + 1's logits go where tile i - 1's weights lay: its product was issued before
+          if (i + 1 < nt && i > 0) mma_s(slot ^ 1, en, true);
+          const int ev = take();
+          if (!ok) break;
+          clean_v(r.lo + i, ev, gr[slot]);
+          if (i + 1 < nt) gr[slot ^ 1] = gn;
+          if (!(ok = wait(&p_b[slot], seen_p[slot]++))) break;
+          mma_o(slot, ev, i < 2, i + 2 >= nt, true);
+        }
+      }
+    }
+    // the last entries' releases land before the CTA may exit
+    if (ok)
+      for (int i = loaded > E ? loaded - E : 0; i < loaded; ++i) mbar_wait(&empty_b[i % E], (uint32_t)((i / E) & 1));
+  } else {
+    const int slot = warp >> 2, row = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), mine = lanes + slot * 256;
+    const float sl = p.scale_log2;
+    int seen_s = 0, run = 0, done[2] = {0, 0};
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int phase) {
+      const bool late = !mbar_wait(bar, (uint32_t)(phase & 1));
+      if (late) give_up();
+      return !__any_sync(0xffffffffu, late || abort_flag);  // warp-uniform: the TMEM accesses are .aligned
+    };
+    for (long long x = x0; ok && flat_run(ft, p.B, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+      const int b = r.b, g = r.unit % p.Hkv, rt = r.unit / p.Hkv;
+      const int n = ft.n[b], nodes = ft.t[b], rows = nodes * p.G, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
+      const bool idle = kWide && slot == 1 && rows - rt * R <= 128;
+      // the query rows, swizzled as TMA would store them (eight rows of 16 pieces at a time)
+      {
+        constexpr int kPer = kWide ? 128 : 64;  // rows this slot's warps load
+        const int q0 = kWide ? 0 : slot * 64;
+        uint8_t* dst = qs + (kWide ? slot * (128 * 256) : 0);
+        const int piece = row & 15;
+        for (int i = q0 + (row >> 4); i < q0 + kPer; i += 8) {
+          const int rr = rt * R + (kWide ? slot * 128 : 0) + i;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (rr < rows) v = reinterpret_cast<const uint4*>(p.q + out_row(p, b, g, rr) * 128)[piece];
+          *reinterpret_cast<uint4*>(dst + (piece >> 3) * (128 * 128) + i * 128 + (((piece & 7) ^ (i & 7)) << 4)) = v;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&q_b[kWide ? slot : 0]);
+      }
+      const int my = rt * R + (kWide ? slot * 128 : 0) + row;  // this thread's query row
+      float m = kNoMax, l = 0.f;
+      if (!idle) {
+        for (int i = kWide ? 0 : slot; i < nt; i += kWide ? 1 : 2) {
+          if (!(ok = wait(&s_b[slot], seen_s++))) break;
+          tc_fence_after();
+          const int tile = r.lo + i;
+          const uint32_t gr = sgroups[slot];
+          const int left = tile < nc ? n - tile * kAtKeys : nodes - (tile - nc) * kAtKeys;
+          const bool all = tile < nc && left >= kAtKeys && gr == 0xffu;
+          uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+          if (!all) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int k = left - w * 32;
+              see[w] = k >= 32 ? ~0u : (k <= 0 ? 0u : (1u << k) - 1u);
+              if (!((gr >> (2 * w)) & 1u)) see[w] &= 0xffff0000u;
+              if (!((gr >> (2 * w + 1)) & 1u)) see[w] &= 0x0000ffffu;
+            }
+            if (tile >= nc) {
+              const int w0 = (tile - nc) * 4;
+              const uint32_t* mk = p.mask + ((size_t)b * p.T + (my < rows ? my >> p.gshift : 0)) * p.words + w0;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) see[w] &= w0 + w < p.words ? mk[w] : 0u;
+            }
+          }
+          uint32_t v[4][32];
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tc_ld32_wait(mine + c * 32, v[c]);
+            if (!all) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((see[c] >> j) & 1u)) v[c][j] = 0xff800000u;  // -inf
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(v[c][j]));
+          }
+          mx *= sl;  // sl > 0
+          const bool first = i < (kWide ? 1 : 2);
+          if (first) {
+            m = fmaxf(kNoMax, mx);
+          } else if (__any_sync(0xffffffffu, mx > m + kAtSlack)) {
+            // this slot's earlier products are complete: its logits were issued after them
+            const float to = fmaxf(m, mx), f = ex2_approx(m - to);
+            m = to;
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tc_ld32_wait(mine + 128 + c * 32, o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tc_st32_wait(mine + 128 + c * 32, o);
+            }
+          }
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int cc = c * 2 + (j >> 4), jj = (j & 15) * 2;
+              const float a0 = ex2_approx(fmaf(__uint_as_float(v[cc][jj]), sl, -m));
+              const float a1 = ex2_approx(fmaf(__uint_as_float(v[cc][jj + 1]), sl, -m));
+              s0 += a0;
+              s1 += a1;
+              // bf16 weights (off by at most 2^-8 of each, as V is); their sum stays unrounded
+              pk[j] = pack_bf16x2(a0, a1);
+            }
+            tc_st32_wait(mine + c * 32, pk);
+          }
+          l += s0 + s1;
+          tc_fence_before();
+          mbar_arrive(&p_b[slot]);
+        }
+      }
+      if (!ok) break;
+      // the run's end: out = O / l (whole unit) or the part (m, l, O)
+      const bool has[2] = {true, kWide ? true : nt > 1};
+      float f0 = 1.f, f1 = 0.f;
+      if (kWide) {
+        if (!(ok = wait(&o_b[slot], done[slot]++))) break;
+      } else {
+        ml_s[slot][row] = make_float2(m, l);
+        mbar_arrive(&ml_b);
+        if (!(ok = wait(&ml_b, run))) break;
+        if (!(ok = wait(&o_b[0], done[0]++))) break;
+        if (has[1] && !(ok = wait(&o_b[1], done[1]++))) break;
+        const float2 a = ml_s[0][row], c = has[1] ? ml_s[1][row] : make_float2(kNoMax, 0.f);
+        m = fmaxf(a.x, c.x);
+        f0 = ex2_approx(a.x - m);
+        f1 = ex2_approx(c.x - m);
+        l = a.y * f0 + c.y * f1;
+      }
+      ++run;
+      tc_fence_after();
+      if (!idle) {
+        const bool live = my < rows;
+        const float inv = r.whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+        const size_t orow = live ? out_row(p, b, g, my) : 0;
+        const size_t prow = (2 * (size_t)blockIdx.x + (r.first ? 0 : 1)) * R + (kWide ? slot * 128 : 0) + row;
+        // kWide: all 128 channels of this slot's row; else 64 channels of both slots' O
+        constexpr int kChunks = kWide ? 4 : 2;
+#pragma unroll 1
+        for (int cc = 0; cc < kChunks; ++cc) {
+          const int c = kWide ? cc : slot * 2 + cc;
+          uint32_t o[32];
+          tc_ld32_wait(kWide ? mine + 128 + c * 32 : lanes + 128 + c * 32, o);
+          if (!kWide) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
+            if (has[1]) {
+              uint32_t o1[32];
+              tc_ld32_wait(lanes + 256 + 128 + c * 32, o1);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j])));
+            }
+          }
+          if (!live) continue;
+          if (r.whole) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16x2(__uint_as_float(o[j * 8 + 2 * e]) * inv, __uint_as_float(o[j * 8 + 2 * e + 1]) * inv);
+              reinterpret_cast<uint4*>(p.out + orow * 128 + c * 32)[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              reinterpret_cast<uint4*>(p.part_o + prow * 128 + c * 32)[j] =
+                  make_uint4(o[j * 4], o[j * 4 + 1], o[j * 4 + 2], o[j * 4 + 3]);
+          }
+        }
+        if (live && (kWide || slot == 0)) {
+          if (!r.whole) p.part_ml[prow] = make_float2(m, l);
+          else if (p.lse) p.lse[orow] = lse_of(m, l);
+        }
+        tc_fence_before();  // O is read before the next run's queries let its products start
+      }
+    }
+  }
+
+  // teardown: after a timeout, wait (bounded) for the copies and products still in flight
+  tc_fence_before();
+  __syncthreads();
+  if (abort_flag) {
+    if (warp == 8 && lane == 0)
+      for (int i = loaded > E ? loaded - E : 0; i < loaded; ++i) mbar_wait(&full_b[i % E], (uint32_t)((i / E) & 1));
+    if (warp == 9 && lane == 0) {  // everything issued before this commit has completed when it arrives
+      tc_commit(&o_b[0]);
+      const uint64_t t0 = global_ns();
+      while (global_ns() - t0 < 1000000ull) {
+      }
+    }
+    __syncthreads();
+  }
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -467,15 +981,21 @@ int log2_int(int x) {
   return s;
 }
 
+// How many rows of a unit share a pass over the cache: 16 (mma.sync), 128 or 256 (tcgen05).
+int tile_rows(int T, int G) { return T * G <= kArRows ? kArRows : (T * G <= 128 ? 128 : 256); }
+
 cudaError_t fill_params(const AttendArgs& a, AttendParams& p) {
+  const int rows = tile_rows(a.T, a.Hq / a.cache.Hkv);
+  const uint32_t box = rows == kArRows ? kArKeys : (uint32_t)a.cache.page_size;
+  const uint32_t tbox = rows == kArRows ? kArKeys : kAtKeys;
   const rkv_cache& c = a.cache;
-  const uint64_t rows = (uint64_t)c.num_phys_pages * c.Hkv * c.page_size;
-  bool ok = encode_rows_map(&p.tmk, c.k_pages, rows, kArKeys) && encode_rows_map(&p.tmv, c.v_pages, rows, kArKeys);
+  const uint64_t prows = (uint64_t)c.num_phys_pages * c.Hkv * c.page_size;
+  bool ok = encode_rows_map(&p.tmk, c.k_pages, prows, box) && encode_rows_map(&p.tmv, c.v_pages, prows, box);
   p.tmkt = p.tmk;
   p.tmvt = p.tmv;
   if (a.mask) {
     const uint64_t trows = (uint64_t)c.B * c.Hkv * a.T;
-    ok = ok && encode_rows_map(&p.tmkt, a.k_tree, trows, kArKeys) && encode_rows_map(&p.tmvt, a.v_tree, trows, kArKeys);
+    ok = ok && encode_rows_map(&p.tmkt, a.k_tree, trows, tbox) && encode_rows_map(&p.tmvt, a.v_tree, trows, tbox);
   }
   if (!ok) {
     set_last_error("cuTensorMapEncodeTiled failed for the cache's pages or the tree");
@@ -511,9 +1031,8 @@ cudaError_t fill_params(const AttendArgs& a, AttendParams& p) {
 }  // namespace
 
 size_t attend_ws_bytes(int B, int Hq, int Hkv, int T, int max_pages, int page_size, bool weights) {
-  (void)Hkv;
-  (void)T;
-  size_t n = align256((size_t)2 * kMaxSms * kArRows * 128 * 4) + align256((size_t)2 * kMaxSms * kArRows * 8);
+  const size_t rows = (size_t)2 * kMaxSms * tile_rows(T, Hq / Hkv > 0 ? Hq / Hkv : 1);
+  size_t n = align256(rows * 128 * 4) + align256(rows * 8);
   if (weights) n += align256((size_t)B * Hq * 8) + align256((size_t)B * Hq * max_pages * page_size * 4);
   return n;
 }
@@ -524,11 +1043,13 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
   cudaError_t e = fill_params(a, p);
   if (e != cudaSuccess) return e;
   if (p.N > kMaxSms) p.N = kMaxSms;
+  const int tile = tile_rows(a.T, p.G);
+  const size_t rows = (size_t)2 * kMaxSms * tile;
   uint8_t* w = static_cast<uint8_t*>(a.ws);
   p.part_o = reinterpret_cast<float*>(w);
-  w += align256((size_t)2 * kMaxSms * kArRows * 128 * 4);
+  w += align256(rows * 128 * 4);
   p.part_ml = reinterpret_cast<float2*>(w);
-  w += align256((size_t)2 * kMaxSms * kArRows * 8);
+  w += align256(rows * 8);
   p.row_ml = nullptr;
   p.z = nullptr;
   if (a.acc) {
@@ -536,18 +1057,37 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
     w += align256((size_t)c.B * a.Hq * 8);
     p.z = reinterpret_cast<float*>(w);
   }
+  const dim3 jgrid((a.Hq * a.T + 7) / 8, c.B);
+  if (tile > kArRows) {
+    const bool wide = tile == 256;
+    static SmemOptIn opt[2];
+    const int smem = wide ? TileShape<true>::kSmem : TileShape<false>::kSmem;
+    const void* f = wide ? reinterpret_cast<const void*>(attend_tiles_kernel<true>)
+                         : reinterpret_cast<const void*>(attend_tiles_kernel<false>);
+    if ((e = opt[wide].raise(f, smem)) != cudaSuccess) return e;
+    launch_begin(K_ATTEND_TILES, s);
+    if (wide)
+      attend_tiles_kernel<true><<<p.N, kAtThreads, smem, s>>>(p);
+    else
+      attend_tiles_kernel<false><<<p.N, kAtThreads, smem, s>>>(p);
+    launch_end(K_ATTEND_TILES, s);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return wide ? launch_dependent(attend_combine_kernel<256, kAtKeys>, jgrid, 256, K_ATTEND_COMBINE, s, p)
+                : launch_dependent(attend_combine_kernel<128, kAtKeys>, jgrid, 256, K_ATTEND_COMBINE, s, p);
+  }
   static SmemOptIn opt;
   if ((e = opt.raise(reinterpret_cast<const void*>(attend_rows_kernel), kArSmem)) != cudaSuccess) return e;
   launch_begin(K_ATTEND_ROWS, s);
   attend_rows_kernel<<<p.N, kArThreads, kArSmem, s>>>(p);
   launch_end(K_ATTEND_ROWS, s);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int units = c.Hkv * ((a.T * p.G + kArRows - 1) / kArRows);
-  e = launch_dependent(attend_combine_kernel, dim3(units < 65536 ? units : 65535, c.B), 128, K_ATTEND_COMBINE, s, p);
-  if (e != cudaSuccess || !a.acc) return e;
+  if (!a.acc)
+    return launch_dependent(attend_combine_kernel<kArRows, kArKeys>, jgrid, 256, K_ATTEND_COMBINE, s, p);
+  const int joins = c.B * ((a.Hq + 7) / 8);
   const long long blocks = (long long)c.B * c.Hkv * ((p.zstride + kWeighTokens - 1) / kWeighTokens);
   const long long most = 8LL * p.N;
-  return launch_dependent(attend_weigh_kernel, dim3((unsigned)(blocks < most ? blocks : most)), 256, K_ATTEND_WEIGH, s, p);
+  return launch_dependent(attend_weigh_kernel, dim3(joins + (unsigned)(blocks < most ? blocks : most)), 256,
+                          K_ATTEND_WEIGH, s, p);
 }
 
 }  // namespace rkv

@@ -225,6 +225,30 @@ __device__ __forceinline__ void tc_ld32_wait(uint32_t taddr, uint32_t (&r)[32]) 
       : "memory");
 }
 
+// This thread's TMEM lane: 32 packed columns written, with the wait in the same statement.
+__device__ __forceinline__ void tc_st32_wait(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n"
+      "tcgen05.wait::st.sync.aligned;\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem], bf16 in, fp32 accumulate; A: row = lane, two K elements
+// to a column.
+__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Shared-memory matrix descriptor of a K-major bf16 operand stored as TMA writes it with
 // 128-byte swizzle: rows of 128 B (64 elements of K), 8-row groups 1024 B apart, the
 // atom 1024-byte aligned.  Fields: start address >> 4 (bits 0-13), leading byte offset
@@ -235,6 +259,15 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t saddr) {
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
+// The same for an operand whose rows run along K (N contiguous: V's [key][channel] as the
+// B of P V): 64 elements of N to a 128-byte row, 8 rows of K to a 1024-byte group.  The
+// leading offset steps from 64 elements of N to the next 64, the stride offset from 8
+// rows of K to the next 8; a K step of 16 is a +2048 B start address.
+__device__ __forceinline__ uint64_t sw128_nmajor_desc(uint32_t saddr, uint32_t n_block_bytes) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(n_block_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+constexpr uint32_t kIdescBNMajor = 1u << 16;  // B runs along N in memory
 // Instruction descriptor of kind::f16 with bf16 A and B, fp32 D, both K-major:
 // D format (bits 4-5) = 1 (f32), A format (7-9) = 1 (bf16), B format (10-12) = 1 (bf16),
 // N >> 3 (17-22), M >> 4 (24-28).

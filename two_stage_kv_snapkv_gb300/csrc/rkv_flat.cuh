@@ -20,6 +20,35 @@ struct FlatTable {
   int units[RKV_MAX_BATCH];           // its units
 };
 
+// base[b] = sum of size(0 .. b - 1), base[B] the total: the first warp's scan; ends with a
+// block barrier.
+template <class Size>
+__device__ __forceinline__ void flat_scan(long long* base, int B, Size size) {
+  const int lane = threadIdx.x;
+  if (lane < 32) {
+    const int each = (B + 31) / 32;
+    long long s = 0;
+    for (int j = 0; j < each; ++j)
+      if (lane * each + j < B) s += size(lane * each + j);
+    long long incl = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    long long at = incl - s;
+    for (int j = 0; j < each; ++j) {
+      const int b = lane * each + j;
+      if (b < B) {
+        base[b] = at;
+        at += size(b);
+        if (b == B - 1) base[B] = at;
+      }
+    }
+  }
+  __syncthreads();
+}
+
 // len(b) -> tokens, rows(b) -> nodes, per(n, t) -> pieces a unit, units(t) -> units.
 // Called by every thread of the block (at least 32); ends with a block barrier.
 template <class Len, class Rows, class Per, class Units>
@@ -32,30 +61,7 @@ __device__ __forceinline__ void flat_build(FlatTable& ft, int B, Len len, Rows r
     ft.units[b] = units(ft.t[b]);
   }
   __syncthreads();
-  if (tid < 32) {
-    constexpr int kEach = RKV_MAX_BATCH / 32;
-    long long s = 0;
-    for (int j = 0; j < kEach; ++j) {
-      const int b = tid * kEach + j;
-      if (b < B) s += (long long)ft.per[b] * ft.units[b];
-    }
-    long long incl = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (tid >= o) incl += y;
-    }
-    long long at = incl - s;
-    for (int j = 0; j < kEach; ++j) {
-      const int b = tid * kEach + j;
-      if (b < B) {
-        ft.base[b] = at;
-        at += (long long)ft.per[b] * ft.units[b];
-        if (b == B - 1) ft.base[B] = at;
-      }
-    }
-  }
-  __syncthreads();
+  flat_scan(ft.base, B, [&](int b) { return (long long)ft.per[b] * ft.units[b]; });
 }
 
 // CTAs that take part: no more than there are pieces, so that no share is empty and every
