@@ -26,7 +26,8 @@ constexpr int kRwBlock = 64;  // query rows staged at a time
 constexpr int kRwSmem = 1024 + kRwWarps * kRwStages * kRwStageBytes + kRwBlock * 256;
 
 struct RowsParams {
-  CUtensorMap tmk;
+  CUtensorMap tmk;     // the key pool as [rows][128] bf16, 128-byte swizzled boxes of 64 channels
+  CUtensorMap tmq;     // q the same, boxes of nq rows (accum_tiles)
   const rkv_bf16* q;   // [B][Hq][T][128]
   const float* lse;    // [B][Hq][T]
   const int32_t* row_len;
@@ -35,7 +36,8 @@ struct RowsParams {
   const int32_t* seq_len;
   int32_t* err;
   float* acc;
-  int B, Hq, Hkv, G, gshift, T, ids_stride, P, pshift, max_pages, num_phys, acc_stride, N;
+  float* part;         // accum_tiles: [2 N][256] sums of the units' parts
+  int B, Hq, Hkv, G, gshift, T, ids_stride, P, pshift, max_pages, num_phys, acc_stride, N, nq;
   float scale_log2;
 };
 
@@ -203,6 +205,352 @@ __global__ void __launch_bounds__(kRwThreads, 1) accum_rows_kernel(const __grid_
   }
   if (dead)
     for (int i = used; i < fetched; ++i) mbar_wait(&full_b[warp][i % kRwStages], (uint32_t)((i / kRwStages) & 1));
+}
+
+// ---------------------------------------------------------------------------
+// accum_tiles: many rows (a prompt's or a chunk's), on the fifth-generation tensor cores.
+//
+// S^T = K Q^T with the keys on the TMEM lanes: a thread owns a key, and its sum over the
+// rows is a private loop over columns, as in the window scoring of the prefill.  A unit is
+// 256 keys of a KV head (two 128-key MMAs share each query tile of nq rows, so that a tile
+// read from L2 feeds twice the products); its pieces are the (head, row tile) pairs that
+// see it, and all units' pieces form one line that is split evenly over the SMs: the
+// causal triangle needs no balancing of its own.  A unit split between CTAs leaves its
+// parts in the workspace and accum_join adds them in order.
+// Per piece 2 x 128 x nq x 128 multiply-adds and 256 nq exponentials; at nq = 128 the
+// products take 1024 clocks of an SM and the exponentials as many at 32 a clock: two
+// accumulators a key tile keep both busy.
+//   warps 0-15: sums (warps 4 w .. 4 w + 3: key tile w / 2, column half w % 2);
+//   warp 16: TMA;  warp 17: MMA issue;  warp 18: the rows' log-sum-exps.
+constexpr int kAmKeys = 256;
+constexpr int kAmThreads = 19 * 32;
+constexpr int kAmLse = 4;
+constexpr int kAmSmem = 1024 + 2 * 65536 + 2 * 32768;
+
+struct TilesTable {
+  long long base[RKV_MAX_BATCH + 1];
+  int n[RKV_MAX_BATCH], m[RKV_MAX_BATCH];
+};
+
+// The units of one KV head: n tokens, m rows at positions c0 = n - m ...; unit j (keys
+// 256 j ...) is seen by row tiles f(j) .. RT - 1 of every head.
+struct HeadShape {
+  int RT, J0, jz, units, G;
+  __device__ __forceinline__ HeadShape(int n, int m, int nq, int G_) : G(G_) {
+    RT = (m + nq - 1) / nq;
+    const int c0 = n - m;
+    J0 = (c0 + 127) / 128;  // nq < 128 means one row tile: f is 0 throughout
+    if (RT == 1) J0 = 1 << 28;
+    jz = J0 / 2 + 1;        // the first unit that some row tile does not see
+    units = m > 0 ? (n + kAmKeys - 1) / kAmKeys : 0;
+  }
+  __device__ __forceinline__ int first(int j) const { return max(0, 2 * j - J0); }
+  __device__ __forceinline__ int pieces(int j) const { return G * (RT - first(j)); }
+  __device__ __forceinline__ long long before(int j) const {  // pieces of units 0 .. j - 1
+    long long c = (long long)j * RT;
+    if (j > jz) c -= (long long)(j - jz) * (jz + j - 1) - (long long)J0 * (j - jz);
+    return c * G;
+  }
+};
+
+struct TilesRun {
+  int b, g, j, lo, hi, f, width;  // pieces lo .. hi of unit j; width = row tiles of a head that see it
+  long long x, ux;                // the run's first piece, the unit's first piece
+  int whole, first;
+};
+
+__device__ __forceinline__ bool tiles_run(const RowsParams& p, const TilesTable& tt, int nq, long long x, long long x0,
+                                          long long x1, TilesRun& r) {
+  if (x >= x1) return false;
+  int lo = 0, hi = p.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tt.base[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  r.b = lo;
+  const HeadShape h(tt.n[lo], tt.m[lo], nq, p.G);
+  const long long each = h.before(h.units), off = x - tt.base[lo];
+  r.g = (int)(off / each);
+  const long long in = off - r.g * each;
+  int a = 0, z = h.units - 1;
+  while (a < z) {
+    const int mid = (a + z + 1) >> 1;
+    if (h.before(mid) <= in) a = mid; else z = mid - 1;
+  }
+  r.j = a;
+  r.f = h.first(a);
+  r.width = h.RT - r.f;
+  const int count = h.pieces(a);
+  r.lo = (int)(in - h.before(a));
+  r.hi = (int)min((long long)count, r.lo + (x1 - x));
+  r.whole = r.lo == 0 && r.hi == count;
+  r.first = x == x0;
+  r.x = x;
+  r.ux = x - r.lo;
+  return true;
+}
+
+__device__ __forceinline__ void tiles_table(const RowsParams& p, TilesTable& tt) {
+  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+    const int n = rows_cache_len(p, b);
+    tt.n[b] = n;
+    tt.m[b] = rows_of(p, b, n);
+  }
+  __syncthreads();
+  flat_scan(tt.base, p.B, [&](int b) {
+    const HeadShape h(tt.n[b], tt.m[b], p.nq, p.G);
+    return p.Hkv * h.before(h.units);
+  });
+}
+
+__global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid_constant__ RowsParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ TilesTable tt;
+  __shared__ uint64_t kfull[2], kempty[2], qfull[2], qempty[2], sfull[2], sempty[2], lfull[kAmLse], lempty[kAmLse], hsum;
+  __shared__ __align__(16) float ls[kAmLse][128];
+  __shared__ float half_s[2][128];
+  __shared__ uint32_t tmem_base;
+  __shared__ volatile int abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* ks = align1024(smem);
+  uint8_t* qs = ks + 2 * 65536;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&kfull[i], 1);
+      mbar_init(&kempty[i], 1);
+      mbar_init(&qfull[i], 1);
+      mbar_init(&qempty[i], 1);
+      mbar_init(&sfull[i], 1);
+      mbar_init(&sempty[i], 512);
+    }
+    for (int i = 0; i < kAmLse; ++i) {
+      mbar_init(&lfull[i], 32);
+      mbar_init(&lempty[i], 512);
+    }
+    mbar_init(&hsum, 512);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 17) {
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  tiles_table(p, tt);
+  tc_fence_after();
+  grid_launch_dependents();
+  const uint32_t tmem = tmem_base;
+  const int nq = p.nq;
+  const long long total = tt.base[p.B];
+  const int N = flat_ctas(total, p.N);
+  const bool works = (int)blockIdx.x < N;
+  const long long x0 = works ? flat_first(total, blockIdx.x, N) : 0, x1 = works ? flat_first(total, blockIdx.x + 1, N) : 0;
+  auto wait = [&](uint64_t* bar, int phase) {
+    const bool late = !mbar_wait(bar, (uint32_t)(phase & 1));
+    if (late) {
+      flag_error(p.err, RKV_DEVERR_TIMEOUT);
+      abort_flag = 1;
+    }
+    return !__any_sync(0xffffffffu, late || abort_flag);
+  };
+  TilesRun r;
+  int units = 0, tiles = 0;  // units and query tiles loaded (16), used (17), read (others)
+  bool ok = true;
+
+  if (warp == 16) {
+    for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+      const int n = tt.n[r.b], s = units & 1;
+      // the unit's keys: one box of a page a lane
+      const int pg = r.j * (kAmKeys >> p.pshift) + (lane >> 1);
+      int phys = -1;
+      if (lane < 2 * (kAmKeys >> p.pshift) && pg * p.P < n) {
+        phys = p.page_table[(size_t)r.b * p.max_pages + pg];
+        if (phys < 0 || phys >= p.num_phys) {
+          flag_error(p.err, RKV_DEVERR_PAGE_ID);
+          phys = -1;
+        }
+      }
+      if (units >= 2 && !(ok = wait(&kempty[s], units / 2 - 1))) break;
+      const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0);
+      if (lane == 0) {
+        if (have) mbar_arrive_expect_tx(&kfull[s], __popc(have) * p.P * 128);
+        else mbar_arrive(&kfull[s]);
+      }
+      __syncwarp();
+      if (phys >= 0) {
+        const int row = (lane >> 1) * p.P;  // of the unit's 256
+        tma_load_2d(ks + s * 65536 + (row >> 7) * 32768 + (lane & 1) * 16384 + (row & 127) * 128, &p.tmk, (lane & 1) * 64,
+                    (phys * p.Hkv + r.g) * p.P, &kfull[s]);
+      }
+      ++units;
+      for (int o = r.lo; o < r.hi; ++o) {
+        const int t = tiles & 1, h = o / r.width, rt = r.f + o - h * r.width;
+        if (tiles >= 2 && !(ok = wait(&qempty[t], tiles / 2 - 1))) break;
+        if (lane == 0) {
+          const int row = (r.b * p.Hq + r.g * p.G + h) * p.T + rt * nq;
+          mbar_arrive_expect_tx(&qfull[t], nq * 256);
+          tma_load_2d(qs + t * 32768, &p.tmq, 0, row, &qfull[t]);
+          tma_load_2d(qs + t * 32768 + 16384, &p.tmq, 64, row, &qfull[t]);
+        }
+        __syncwarp();
+        ++tiles;
+      }
+    }
+  } else if (warp == 17) {
+    const uint32_t idesc = idesc_bf16_f32(128, nq), k32 = smem_u32(ks), q32 = smem_u32(qs);
+    for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+      const int s = units & 1;
+      if (!(ok = wait(&kfull[s], units / 2))) break;
+      ++units;
+      for (int o = r.lo; o < r.hi; ++o) {
+        const int t = tiles & 1;
+        if (!(ok = wait(&qfull[t], tiles / 2))) break;
+        if (tiles >= 2 && !(ok = wait(&sempty[t], tiles / 2 - 1))) break;
+        if (lane == 0) {
+          tc_fence_after();
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+              tc_mma_bf16(tmem + t * 256 + w * 128, sw128_kmajor_desc(k32 + s * 65536 + w * 32768 + off),
+                          sw128_kmajor_desc(q32 + t * 32768 + off), idesc, k > 0);
+            }
+          tc_commit(&qempty[t]);
+          if (o + 1 == r.hi) tc_commit(&kempty[s]);
+          tc_commit(&sfull[t]);
+        }
+        __syncwarp();
+        ++tiles;
+      }
+    }
+    if (ok) {  // the last releases land before the CTA may exit
+      for (int i = max(0, tiles - 2); i < tiles; ++i) mbar_wait(&qempty[i & 1], (uint32_t)((i / 2) & 1));
+      for (int i = max(0, units - 2); i < units; ++i) mbar_wait(&kempty[i & 1], (uint32_t)((i / 2) & 1));
+    }
+  } else if (warp == 18) {
+    for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+      const int m = tt.m[r.b];
+      for (int o = r.lo; o < r.hi; ++o) {
+        const int l = tiles % kAmLse, h = o / r.width, i0 = (r.f + o - h * r.width) * nq;
+        const float* src = p.lse + ((size_t)r.b * p.Hq + r.g * p.G + h) * p.T + i0;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = lane + 32 * e < min(nq, m - i0) ? src[lane + 32 * e] : -INFINITY;
+        if (tiles >= kAmLse && !(ok = wait(&lempty[l], tiles / kAmLse - 1))) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          ls[l][lane + 32 * e] = v[e] == -INFINITY ? INFINITY : v[e] * 1.4426950408889634f;
+        mbar_arrive(&lfull[l]);
+        ++tiles;
+      }
+    }
+  } else {
+    const int wg = warp >> 2, kt = wg >> 1, half = wg & 1, key = kt * 128 + (tid & 127);
+    const int cols = nq >> 1, c0 = half * cols;  // this warp's columns
+    const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kt * 128 + c0;
+    const float sl = p.scale_log2;
+    for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+      const int n = tt.n[r.b], m = tt.m[r.b], t = r.j * kAmKeys + key;
+      float sum = 0.f;
+      for (int o = r.lo; o < r.hi; ++o) {
+        const int buf = tiles & 1, l = tiles % kAmLse, h = o / r.width, i0 = (r.f + o - h * r.width) * nq;
+        if (!(ok = wait(&lfull[l], tiles / kAmLse))) break;
+        if (!(ok = wait(&sfull[buf], tiles / 2))) break;
+        tc_fence_after();
+        // the columns this key's sum takes: rows i >= t - (n - m) (causal) and i < m
+        const int jmin = t - (n - m) - i0, jmax = m - i0;
+        const bool all = __all_sync(0xffffffffu, jmin <= c0 && jmax >= c0 + cols);
+        float s0 = 0.f, s1 = 0.f;
+        for (int c = 0; c < cols; c += 32) {
+          uint32_t v[32];
+          tc_ld32_wait(mine + buf * 256 + c, v);
+          const float* lp = &ls[l][c0 + c];
+          if (all) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float4 a = *reinterpret_cast<const float4*>(lp + j);
+              s0 += ex2_approx(fmaf(__uint_as_float(v[j]), sl, -a.x));
+              s1 += ex2_approx(fmaf(__uint_as_float(v[j + 1]), sl, -a.y));
+              s0 += ex2_approx(fmaf(__uint_as_float(v[j + 2]), sl, -a.z));
+              s1 += ex2_approx(fmaf(__uint_as_float(v[j + 3]), sl, -a.w));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int col = c0 + c + j;
+              const float e = ex2_approx(fmaf(__uint_as_float(v[j]), sl, -lp[j]));
+              s0 += col >= jmin && col < jmax ? e : 0.f;
+            }
+          }
+        }
+        sum += s0 + s1;  // tile by tile: a sum of thousands of rows keeps its small terms
+        tc_fence_before();
+        mbar_arrive(&sempty[buf]);
+        mbar_arrive(&lempty[l]);
+        ++tiles;
+      }
+      if (!ok) break;
+      // the two halves of the columns meet
+      if (half) half_s[kt][tid & 127] = sum;
+      mbar_arrive(&hsum);
+      if (!(ok = wait(&hsum, 2 * units))) break;
+      if (!half) {
+        sum += half_s[kt][tid & 127];
+        if (r.whole) {
+          if (t < n) {
+            const int phys = p.page_table[(size_t)r.b * p.max_pages + (t >> p.pshift)];
+            if (phys >= 0 && phys < p.num_phys) p.acc[((size_t)r.b * p.Hkv + r.g) * p.acc_stride + t] += sum;
+          }
+        } else {
+          p.part[(2 * (size_t)blockIdx.x + (r.first ? 0 : 1)) * kAmKeys + key] = sum;
+        }
+      }
+      mbar_arrive(&hsum);  // half_s is free
+      if (!(ok = wait(&hsum, 2 * units + 1))) break;
+      ++units;
+    }
+  }
+
+  // teardown: after a timeout, wait (bounded) for the copies and products still in flight
+  tc_fence_before();
+  __syncthreads();
+  if (abort_flag) {
+    if (warp == 16 && lane == 0) {
+      for (int i = max(0, tiles - 2); i < tiles; ++i) mbar_wait(&qfull[i & 1], (uint32_t)((i / 2) & 1));
+      for (int i = max(0, units - 2); i < units; ++i) mbar_wait(&kfull[i & 1], (uint32_t)((i / 2) & 1));
+    }
+    if (warp == 17 && lane == 0 && tiles > 0) mbar_wait(&sfull[(tiles - 1) & 1], (uint32_t)(((tiles - 1) / 2) & 1));
+    __syncthreads();
+  }
+  if (warp == 17) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Adds the parts of the units that were split between CTAs, in the CTAs' order.  grid N,
+// 256 threads (keys): CTA c joins the unit that starts in c's share and ends behind it.
+__global__ void __launch_bounds__(kAmKeys) accum_join_kernel(const __grid_constant__ RowsParams p) {
+  __shared__ TilesTable tt;
+  tiles_table(p, tt);
+  grid_dependency_wait();
+  const long long total = tt.base[p.B];
+  const int N = flat_ctas(total, p.N), c = blockIdx.x;
+  if (c >= N) return;
+  const long long x0 = flat_first(total, c, N), x1 = flat_first(total, c + 1, N);
+  TilesRun r;
+  tiles_run(p, tt, p.nq, x1 - 1, x0, total, r);
+  const long long end = r.x + (r.hi - r.lo);  // the unit's end
+  if (r.ux < x0 || end <= x1) return;
+  const int last = flat_cta(end - 1, total, N), t = r.j * kAmKeys + threadIdx.x;
+  float sum = 0.f;
+  for (int i = c; i <= last; ++i)
+    sum += p.part[(2 * (size_t)i + (flat_first(total, i, N) >= r.ux ? 0 : 1)) * kAmKeys + threadIdx.x];
+  if (t < tt.n[r.b]) {
+    const int phys = p.page_table[(size_t)r.b * p.max_pages + (t >> p.pshift)];
+    if (phys >= 0 && phys < p.num_phys) p.acc[((size_t)r.b * p.Hkv + r.g) * p.acc_stride + t] += sum;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -412,23 +760,22 @@ __global__ void __launch_bounds__(128) evict_compact_kernel(const __grid_constan
   }
 }
 
-inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-int log2_int(int x) {
-  int s = 0;
-  while ((1 << s) < x) ++s;
-  return s;
-}
-
 }  // namespace
 
-size_t accum_rows_ws_bytes(int, int, int, int, int, int) { return 256; }
+size_t accum_rows_ws_bytes(int, int, int, int, int, int) { return (size_t)2 * kMaxSms * kAmKeys * 4; }
 
 cudaError_t launch_accum_rows(const AccumRowsArgs& a, cudaStream_t s) {
   const rkv_cache& c = a.cache;
   RowsParams p;
-  if (!encode_rows_map(&p.tmk, c.k_pages, (uint64_t)c.num_phys_pages * c.Hkv * c.page_size, kRwKeys)) {
-    set_last_error("cuTensorMapEncodeTiled failed for the cache's pages");
+  // up to 64 rows of a KV head are one staged block of accum_rows; rows picked by id are
+  // gathered, which only accum_rows does
+  const bool tiles = !a.row_ids && (long long)a.T * (a.Hq / c.Hkv) > kRwBlock;
+  p.nq = a.T > 64 ? 128 : 64;
+  bool ok = encode_rows_map(&p.tmk, c.k_pages, (uint64_t)c.num_phys_pages * c.Hkv * c.page_size,
+                            tiles ? (uint32_t)c.page_size : (uint32_t)kRwKeys);
+  if (tiles) ok = ok && encode_rows_map(&p.tmq, a.q, (uint64_t)c.B * a.Hq * a.T, (uint32_t)p.nq);
+  if (!ok) {
+    set_last_error("cuTensorMapEncodeTiled failed for the cache's pages or the queries");
     return cudaErrorInvalidValue;
   }
   p.q = a.q;
@@ -453,9 +800,20 @@ cudaError_t launch_accum_rows(const AccumRowsArgs& a, cudaStream_t s) {
   p.acc_stride = a.acc_stride;
   p.N = num_sms();
   p.scale_log2 = a.scale * 1.4426950408889634f;
+  if (p.N > kMaxSms) p.N = kMaxSms;
+  p.part = static_cast<float*>(a.ws);
+  cudaError_t e;
+  if (tiles) {
+    static SmemOptIn opt;
+    if ((e = opt.raise(reinterpret_cast<const void*>(accum_tiles_kernel), kAmSmem)) != cudaSuccess) return e;
+    launch_begin(K_ACCUM_TILES, s);
+    accum_tiles_kernel<<<p.N, kAmThreads, kAmSmem, s>>>(p);
+    launch_end(K_ACCUM_TILES, s);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_dependent(accum_join_kernel, dim3(p.N), kAmKeys, K_ACCUM_JOIN, s, p);
+  }
   static SmemOptIn opt;
-  cudaError_t e = opt.raise(reinterpret_cast<const void*>(accum_rows_kernel), kRwSmem);
-  if (e != cudaSuccess) return e;
+  if ((e = opt.raise(reinterpret_cast<const void*>(accum_rows_kernel), kRwSmem)) != cudaSuccess) return e;
   launch_begin(K_ACCUM_ROWS, s);
   accum_rows_kernel<<<p.N, kRwThreads, kRwSmem, s>>>(p);
   launch_end(K_ACCUM_ROWS, s);

@@ -956,31 +956,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
   }
 }
 
-inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-template <class K, class P>
-cudaError_t launch_dependent(K kernel, dim3 grid, int threads, int kind, cudaStream_t s, const P& p) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  launch_begin(kind, s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
-  launch_end(kind, s);
-  return e;
-}
-
-int log2_int(int x) {
-  int s = 0;
-  while ((1 << s) < x) ++s;
-  return s;
-}
-
 // How many rows of a unit share a pass over the cache: 16 (mma.sync), 128 or 256 (tcgen05).
 int tile_rows(int T, int G) { return T * G <= kArRows ? kArRows : (T * G <= 128 ? 128 : 256); }
 

@@ -1386,7 +1386,6 @@ __global__ void __launch_bounds__(kThreads) sparq_attend_kernel(const __grid_con
   }
 }
 
-inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // A [rows][128] bf16 page pool as a 2-D tensor map with 16-row x 64-channel boxes.
 bool encode_pool_map(CUtensorMap* m, const rkv_bf16* base, uint64_t rows) {

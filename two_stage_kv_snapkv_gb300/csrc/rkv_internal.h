@@ -41,6 +41,8 @@ enum KernelKind {
   K_ATTEND_WEIGH,
   K_TREE_COMMIT,
   K_ACCUM_ROWS,
+  K_ACCUM_TILES,
+  K_ACCUM_JOIN,
   K_EVICT_SELECT,
   K_EVICT_STAGE,
   K_EVICT_COMPACT,
@@ -68,6 +70,31 @@ struct SmemOptIn {
     return e;
   }
 };
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+inline int log2_int(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+// A launch that may start while the kernel before it on `s` ends (it must wait for it with
+// griddepcontrol.wait before reading what that kernel wrote).
+template <class Params>
+cudaError_t launch_dependent(void (*kernel)(Params), dim3 grid, int threads, int kind, cudaStream_t s,
+                             const Params& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  launch_begin(kind, s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  launch_end(kind, s);
+  return e;
+}
 // Sets the message rkv_last_error() returns on this thread.
 void set_last_error(const char* msg);
 

@@ -596,8 +596,6 @@ __global__ void __launch_bounds__(128) snap_compact_kernel(const __grid_constant
   }
 }
 
-inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 }  // namespace
 
 size_t prefill_ws_bytes(int B, int Hq, int Hkv, int w, int Lmax) {
