@@ -20,9 +20,9 @@ namespace {
 constexpr int kRwKeys = 16;
 constexpr int kRwWarps = 8;
 constexpr int kRwThreads = kRwWarps * 32;
-constexpr int kRwStages = 4;
+constexpr int kRwStages = 6;
 constexpr int kRwStageBytes = 4096;
-constexpr int kRwBlock = 64;  // query rows staged at a time
+constexpr int kRwBlock = 64;  // query rows staged at a time, at most
 constexpr int kRwSmem = 1024 + kRwWarps * kRwStages * kRwStageBytes + kRwBlock * 256;
 
 struct RowsParams {
@@ -60,12 +60,15 @@ __device__ __forceinline__ int rows_cache_len(const RowsParams& p, int b) {
   return n;
 }
 
+// kR16: 16-row groups of a block; the block's rows stay in registers as B fragments.
+template <int kR16>
 __global__ void __launch_bounds__(kRwThreads, 1) accum_rows_kernel(const __grid_constant__ RowsParams p) {
+  constexpr int kBlock = kR16 * 16;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ FlatTable ft;
   __shared__ uint64_t full_b[kRwWarps][kRwStages];
-  __shared__ float ls[kRwBlock];  // base-2 log-sum-exp of the staged rows, +inf: weighs nothing
-  __shared__ int last[kRwBlock];  // last position a staged row sees
+  __shared__ float ls[kBlock];  // base-2 log-sum-exp of the staged rows, +inf: weighs nothing
+  __shared__ int last[kBlock];  // last position a staged row sees
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* base = align1024(smem);
   uint8_t* ring = base + warp * kRwStages * kRwStageBytes;
@@ -86,9 +89,16 @@ __global__ void __launch_bounds__(kRwThreads, 1) accum_rows_kernel(const __grid_
   FlatRun r;
   for (long long x = x0; flat_run(ft, p.B, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
     const int b = r.b, g = r.unit, n = ft.n[b], m = ft.t[b], rows = m * p.G;
+    int ids = -1, ids_at = 0;  // page ids of this warp's chunks ids_at + 8 lane
+    auto load_ids = [&](int c) {
+      ids_at = c;
+      const int mine = c + lane * kRwWarps;
+      ids = mine < r.hi ? p.page_table[(size_t)b * p.max_pages + ((mine * kRwKeys) >> p.pshift)] : -1;
+    };
     auto fetch = [&](int c) {
       const int s = fetched % kRwStages, t0 = c * kRwKeys;
-      const int phys = p.page_table[(size_t)b * p.max_pages + (t0 >> p.pshift)];
+      if (c >= ids_at + 32 * kRwWarps) load_ids(c);
+      const int phys = __shfl_sync(0xffffffffu, ids, (c - ids_at) / kRwWarps);
       if (phys >= 0 && phys < p.num_phys) {
         skipped &= ~(1u << s);
         if (lane == 0) {
@@ -107,13 +117,13 @@ __global__ void __launch_bounds__(kRwThreads, 1) accum_rows_kernel(const __grid_
       }
       ++fetched;
     };
-    for (int blk = 0; blk < rows; blk += kRwBlock) {
-      const int live = min(kRwBlock, rows - blk);
+    for (int blk = 0; blk < rows; blk += kBlock) {
+      const int live = min(kBlock, rows - blk);
       int fc = r.lo + warp;
+      load_ids(fc);
       for (int s = 0; s < kRwStages && fc < r.hi && !dead; ++s, fc += kRwWarps) fetch(fc);
       // the block's query rows (row = i G + head), swizzled as the boxes are
-      __syncthreads();
-      for (int e = tid; e < kRwBlock * 16; e += kRwThreads) {
+      for (int e = tid; e < kBlock * 16; e += kRwThreads) {
         const int row = e >> 4, piece = e & 15;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (row < live) {
@@ -132,12 +142,40 @@ __global__ void __launch_bounds__(kRwThreads, 1) accum_rows_kernel(const __grid_
           ls[row] = INFINITY;
           last[row] = -1;
         }
-        *reinterpret_cast<uint4*>(qs + (piece >> 3) * (kRwBlock * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) = v;
+        *reinterpret_cast<uint4*>(qs + (piece >> 3) * (kBlock * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) = v;
       }
       __syncthreads();
-      const uint32_t qb = smem_u32(qs);
+      uint32_t qf[kR16][8][4];
+      float lr[kR16][4];
+      {
+        const uint32_t qb = smem_u32(qs);
+        const int rr = ((lane >> 4) << 3) + (lane & 7), sub = (lane >> 3) & 1;
+#pragma unroll
+        for (int q = 0; q < kR16; ++q) {
+          const int row = q * 16 + rr;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int piece = k * 2 + sub;
+            ldsm_x4(qf[q][k][0], qf[q][k][1], qf[q][k][2], qf[q][k][3],
+                    qb + (piece >> 3) * (kBlock * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) lr[q][e] = ls[q * 16 + (e >> 1) * 8 + (lane & 3) * 2 + (e & 1)];
+        }
+      }
+      // the sums of the next chunk's positions, loaded a chunk ahead of their use
+      float* const sums = p.acc + ((size_t)b * p.Hkv + g) * p.acc_stride + (lane >> 2);
+      const bool adds = (lane & 3) == 0;
+      auto sum_at = [&](int c, int o) {
+        const int t = c * kRwKeys + o;
+        return adds && c < r.hi && t + (lane >> 2) < n ? sums[t] : 0.f;
+      };
+      float next0 = sum_at(r.lo + warp, 0), next1 = sum_at(r.lo + warp, 8);
       for (int c = r.lo + warp; c < r.hi; c += kRwWarps) {
         const int s = used % kRwStages;
+        const float old0 = next0, old1 = next1;
+        next0 = sum_at(c + kRwWarps, 0);
+        next1 = sum_at(c + kRwWarps, 8);
         const bool late = !dead && !mbar_wait(&full_b[warp][s], (uint32_t)((used / kRwStages) & 1));
         if (__any_sync(0xffffffffu, late)) {
           if (lane == 0) flag_error(p.err, RKV_DEVERR_TIMEOUT);
@@ -145,15 +183,24 @@ __global__ void __launch_bounds__(kRwThreads, 1) accum_rows_kernel(const __grid_
         }
         if (dead) break;
         const bool take = !((skipped >> s) & 1u);
-        uint32_t ka[8][4];
         const uint32_t ks = smem_u32(ring + s * kRwStageBytes);
+        float z[kR16][2][4];
+#pragma unroll
+        for (int q = 0; q < kR16; ++q)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[q][e >> 2][e & 3] = 0.f;
         {
           const int key = (((lane >> 3) & 1) << 3) + (lane & 7);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int piece = k * 2 + (lane >> 4);
-            ldsm_x4(ka[k][0], ka[k][1], ka[k][2], ka[k][3],
-                    ks + (piece >> 3) * 2048 + key * 128 + (((piece & 7) ^ (key & 7)) << 4));
+            uint32_t a0, a1, a2, a3;
+            ldsm_x4(a0, a1, a2, a3, ks + (piece >> 3) * 2048 + key * 128 + (((piece & 7) ^ (key & 7)) << 4));
+#pragma unroll
+            for (int q = 0; q < kR16; ++q) {
+              mma_16816(z[q][0], a0, a1, a2, a3, qf[q][k][0], qf[q][k][1]);
+              mma_16816(z[q][1], a0, a1, a2, a3, qf[q][k][2], qf[q][k][3]);
+            }
           }
         }
         ++used;
@@ -165,39 +212,29 @@ __global__ void __launch_bounds__(kRwThreads, 1) accum_rows_kernel(const __grid_
         if (!take) continue;
         const int t0 = c * kRwKeys + (lane >> 2), t1 = t0 + 8;
         float w0 = 0.f, w1 = 0.f;
-        const int rr = ((lane >> 4) << 3) + (lane & 7), sub = (lane >> 3) & 1;
-        for (int r16 = 0; r16 < live; r16 += 16) {
-          float z[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-          const int row = r16 + rr;
+        const bool all = (c + 1) * kRwKeys <= n - m + 1;  // every row sees the whole chunk
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int piece = k * 2 + sub;
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4(b0, b1, b2, b3, qb + (piece >> 3) * (kRwBlock * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
-            mma_16816(z[0], ka[k][0], ka[k][1], ka[k][2], ka[k][3], b0, b1);
-            mma_16816(z[1], ka[k][0], ka[k][1], ka[k][2], ka[k][3], b2, b3);
-          }
+        for (int q = 0; q < kR16; ++q)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int q = r16 + h * 8 + (lane & 3) * 2 + e;
-              const float l = ls[q];
-              const int seen = last[q];
-              const float e0 = ex2_approx(fmaf(z[h][e], p.scale_log2, -l));
-              const float e1 = ex2_approx(fmaf(z[h][2 + e], p.scale_log2, -l));
+          for (int e = 0; e < 4; ++e) {
+            const float e0 = ex2_approx(fmaf(z[q][e >> 1][e & 1], p.scale_log2, -lr[q][e]));
+            const float e1 = ex2_approx(fmaf(z[q][e >> 1][2 + (e & 1)], p.scale_log2, -lr[q][e]));
+            if (all) {
+              w0 += e0;
+              w1 += e1;
+            } else {
+              const int seen = last[q * 16 + (e >> 1) * 8 + (lane & 3) * 2 + (e & 1)];
               w0 += t0 <= seen ? e0 : 0.f;
               w1 += t1 <= seen ? e1 : 0.f;
             }
-        }
+          }
         w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
         w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
         w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
         w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
-        if ((lane & 3) == 0) {
-          float* a = p.acc + ((size_t)b * p.Hkv + g) * p.acc_stride;
-          if (t0 < n) a[t0] += w0;
-          if (t1 < n) a[t1] += w1;
+        if (adds) {
+          if (t0 < n) sums[c * kRwKeys] = old0 + w0;
+          if (t1 < n) sums[c * kRwKeys + 8] = old1 + w1;
         }
       }
       __syncthreads();  // the staged rows are free
@@ -224,8 +261,8 @@ __global__ void __launch_bounds__(kRwThreads, 1) accum_rows_kernel(const __grid_
 //   warp 16: TMA;  warp 17: MMA issue;  warp 18: the rows' log-sum-exps.
 constexpr int kAmKeys = 256;
 constexpr int kAmThreads = 19 * 32;
-constexpr int kAmLse = 4;
-constexpr int kAmSmem = 1024 + 2 * 65536 + 2 * 32768;
+constexpr int kAmQ = 4;  // query tiles in the ring
+constexpr int kAmSmem = 1024 + 6 * 32768;
 
 struct TilesTable {
   long long base[RKV_MAX_BATCH + 1];
@@ -303,29 +340,36 @@ __device__ __forceinline__ void tiles_table(const RowsParams& p, TilesTable& tt)
   });
 }
 
+// kQRows (nq): 128 with one unit's keys (64 KB) resident and four 32 KB query tiles in
+// flight, a unit then having many pieces; 64 (T <= 64: a piece per head) with two units'
+// keys and four 16 KB tiles.
+template <int kQRows>
 __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid_constant__ RowsParams p) {
+  constexpr int KS = kQRows == 128 ? 1 : 2, QB = kQRows * 256;
+  static_assert(KS * 65536 + kAmQ * QB == 6 * 32768, "the rings fill the shared memory");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ TilesTable tt;
-  __shared__ uint64_t kfull[2], kempty[2], qfull[2], qempty[2], sfull[2], sempty[2], lfull[kAmLse], lempty[kAmLse], hsum;
-  __shared__ __align__(16) float ls[kAmLse][128];
+  __shared__ uint64_t kfull[KS], kempty[KS], qfull[kAmQ], qempty[kAmQ], sfull[2], sempty[2], lfull[2], hsum;
+  __shared__ __align__(16) float ls[2][128];
   __shared__ float half_s[2][128];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* ks = align1024(smem);
-  uint8_t* qs = ks + 2 * 65536;
+  uint8_t* qs = ks + KS * 65536;
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < KS; ++i) {
       mbar_init(&kfull[i], 1);
       mbar_init(&kempty[i], 1);
+    }
+    for (int i = 0; i < kAmQ; ++i) {
       mbar_init(&qfull[i], 1);
       mbar_init(&qempty[i], 1);
-      mbar_init(&sfull[i], 1);
-      mbar_init(&sempty[i], 512);
     }
-    for (int i = 0; i < kAmLse; ++i) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull[i], 2);  // the issuing thread and its commit
+      mbar_init(&sempty[i], 512);
       mbar_init(&lfull[i], 32);
-      mbar_init(&lempty[i], 512);
     }
     mbar_init(&hsum, 512);
     abort_flag = 0;
@@ -340,18 +384,19 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
   tc_fence_after();
   grid_launch_dependents();
   const uint32_t tmem = tmem_base;
-  const int nq = p.nq;
+  constexpr int nq = kQRows;
   const long long total = tt.base[p.B];
   const int N = flat_ctas(total, p.N);
   const bool works = (int)blockIdx.x < N;
   const long long x0 = works ? flat_first(total, blockIdx.x, N) : 0, x1 = works ? flat_first(total, blockIdx.x + 1, N) : 0;
   auto wait = [&](uint64_t* bar, int phase) {
-    const bool late = !mbar_wait(bar, (uint32_t)(phase & 1));
-    if (late) {
+    const bool late = !mbar_wait_role(bar, (uint32_t)(phase & 1), &abort_flag);
+    if (__any_sync(0xffffffffu, late)) {
       flag_error(p.err, RKV_DEVERR_TIMEOUT);
       abort_flag = 1;
+      return false;
     }
-    return !__any_sync(0xffffffffu, late || abort_flag);
+    return true;
   };
   TilesRun r;
   int units = 0, tiles = 0;  // units and query tiles loaded (16), used (17), read (others)
@@ -359,7 +404,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
 
   if (warp == 16) {
     for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
-      const int n = tt.n[r.b], s = units & 1;
+      const int n = tt.n[r.b], s = units % KS;
       // the unit's keys: one box of a page a lane
       const int pg = r.j * (kAmKeys >> p.pshift) + (lane >> 1);
       int phys = -1;
@@ -370,7 +415,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
           phys = -1;
         }
       }
-      if (units >= 2 && !(ok = wait(&kempty[s], units / 2 - 1))) break;
+      if (units >= KS && !(ok = wait(&kempty[s], units / KS - 1))) break;
       const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0);
       if (lane == 0) {
         if (have) mbar_arrive_expect_tx(&kfull[s], __popc(have) * p.P * 128);
@@ -383,103 +428,132 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
                     (phys * p.Hkv + r.g) * p.P, &kfull[s]);
       }
       ++units;
+      int h = r.lo / r.width, rt = r.f + r.lo - h * r.width;
       for (int o = r.lo; o < r.hi; ++o) {
-        const int t = tiles & 1, h = o / r.width, rt = r.f + o - h * r.width;
-        if (tiles >= 2 && !(ok = wait(&qempty[t], tiles / 2 - 1))) break;
+        const int t = tiles % kAmQ;
+        if (tiles >= kAmQ && !(ok = wait(&qempty[t], tiles / kAmQ - 1))) break;
         if (lane == 0) {
           const int row = (r.b * p.Hq + r.g * p.G + h) * p.T + rt * nq;
           mbar_arrive_expect_tx(&qfull[t], nq * 256);
-          tma_load_2d(qs + t * 32768, &p.tmq, 0, row, &qfull[t]);
-          tma_load_2d(qs + t * 32768 + 16384, &p.tmq, 64, row, &qfull[t]);
+          tma_load_2d(qs + t * QB, &p.tmq, 0, row, &qfull[t]);
+          tma_load_2d(qs + t * QB + QB / 2, &p.tmq, 64, row, &qfull[t]);
         }
         __syncwarp();
         ++tiles;
+        if (++rt == r.f + r.width) {
+          rt = r.f;
+          ++h;
+        }
       }
     }
   } else if (warp == 17) {
     const uint32_t idesc = idesc_bf16_f32(128, nq), k32 = smem_u32(ks), q32 = smem_u32(qs);
     for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
-      const int s = units & 1;
-      if (!(ok = wait(&kfull[s], units / 2))) break;
+      const int s = units % KS;
+      if (!(ok = wait(&kfull[s], units / KS))) break;
       ++units;
       for (int o = r.lo; o < r.hi; ++o) {
-        const int t = tiles & 1;
-        if (!(ok = wait(&qfull[t], tiles / 2))) break;
-        if (tiles >= 2 && !(ok = wait(&sempty[t], tiles / 2 - 1))) break;
+        const int t = tiles % kAmQ, d = tiles & 1;
+        if (!(ok = wait(&qfull[t], tiles / kAmQ))) break;
+        // the rows' log-sum-exps are written after the buffer's last reading, so this wait
+        // covers the logits' buffer too
+        if (!(ok = wait(&lfull[d], tiles / 2))) break;
         if (lane == 0) {
           tc_fence_after();
 #pragma unroll
           for (int w = 0; w < 2; ++w)
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-              tc_mma_bf16(tmem + t * 256 + w * 128, sw128_kmajor_desc(k32 + s * 65536 + w * 32768 + off),
-                          sw128_kmajor_desc(q32 + t * 32768 + off), idesc, k > 0);
+              const uint32_t in = (k & 3) * 32;
+              tc_mma_bf16(tmem + d * 256 + w * 128,
+                          sw128_kmajor_desc(k32 + s * 65536 + w * 32768 + (k >> 2) * 16384 + in),
+                          sw128_kmajor_desc(q32 + t * QB + (k >> 2) * (QB / 2) + in), idesc, k > 0);
             }
           tc_commit(&qempty[t]);
           if (o + 1 == r.hi) tc_commit(&kempty[s]);
-          tc_commit(&sfull[t]);
+          tc_commit(&sfull[d]);
+          mbar_arrive(&sfull[d]);
         }
         __syncwarp();
         ++tiles;
       }
     }
     if (ok) {  // the last releases land before the CTA may exit
-      for (int i = max(0, tiles - 2); i < tiles; ++i) mbar_wait(&qempty[i & 1], (uint32_t)((i / 2) & 1));
-      for (int i = max(0, units - 2); i < units; ++i) mbar_wait(&kempty[i & 1], (uint32_t)((i / 2) & 1));
+      for (int i = max(0, tiles - kAmQ); i < tiles; ++i) mbar_wait(&qempty[i % kAmQ], (uint32_t)((i / kAmQ) & 1));
+      for (int i = max(0, units - KS); i < units; ++i) mbar_wait(&kempty[i % KS], (uint32_t)((i / KS) & 1));
     }
   } else if (warp == 18) {
     for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
       const int m = tt.m[r.b];
+      int h = r.lo / r.width, rt = r.f + r.lo - h * r.width;
       for (int o = r.lo; o < r.hi; ++o) {
-        const int l = tiles % kAmLse, h = o / r.width, i0 = (r.f + o - h * r.width) * nq;
+        const int d = tiles & 1, i0 = rt * nq;
         const float* src = p.lse + ((size_t)r.b * p.Hq + r.g * p.G + h) * p.T + i0;
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = lane + 32 * e < min(nq, m - i0) ? src[lane + 32 * e] : -INFINITY;
-        if (tiles >= kAmLse && !(ok = wait(&lempty[l], tiles / kAmLse - 1))) break;
+        if (tiles >= 2 && !(ok = wait(&sempty[d], tiles / 2 - 1))) break;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          ls[l][lane + 32 * e] = v[e] == -INFINITY ? INFINITY : v[e] * 1.4426950408889634f;
-        mbar_arrive(&lfull[l]);
+          ls[d][lane + 32 * e] = v[e] == -INFINITY ? -INFINITY : v[e] * -1.4426950408889634f;  // negated: an addend
+        mbar_arrive(&lfull[d]);
         ++tiles;
+        if (++rt == r.f + r.width) {
+          rt = r.f;
+          ++h;
+        }
       }
     }
   } else {
     const int wg = warp >> 2, kt = wg >> 1, half = wg & 1, key = kt * 128 + (tid & 127);
-    const int cols = nq >> 1, c0 = half * cols;  // this warp's columns
+    constexpr int cols = nq >> 1;
+    const int c0 = half * cols;  // this warp's columns
     const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kt * 128 + c0;
     const float sl = p.scale_log2;
     for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
       const int n = tt.n[r.b], m = tt.m[r.b], t = r.j * kAmKeys + key;
       float sum = 0.f;
+      int rt = r.f + r.lo % r.width;
       for (int o = r.lo; o < r.hi; ++o) {
-        const int buf = tiles & 1, l = tiles % kAmLse, h = o / r.width, i0 = (r.f + o - h * r.width) * nq;
-        if (!(ok = wait(&lfull[l], tiles / kAmLse))) break;
+        const int buf = tiles & 1, i0 = rt * nq;
+        if (++rt == r.f + r.width) rt = r.f;
         if (!(ok = wait(&sfull[buf], tiles / 2))) break;
         tc_fence_after();
+        uint32_t va[2][32];
+        tc_ld32(mine + buf * 256, va[0]);
+        if (cols > 32) tc_ld32(mine + buf * 256 + 32, va[1]);
         // the columns this key's sum takes: rows i >= t - (n - m) (causal) and i < m
         const int jmin = t - (n - m) - i0, jmax = m - i0;
         const bool all = __all_sync(0xffffffffu, jmin <= c0 && jmax >= c0 + cols);
         float s0 = 0.f, s1 = 0.f;
+        tc_ld_wait();
+#pragma unroll
         for (int c = 0; c < cols; c += 32) {
-          uint32_t v[32];
-          tc_ld32_wait(mine + buf * 256 + c, v);
-          const float* lp = &ls[l][c0 + c];
+          uint32_t(&v)[32] = va[c / 32];
+          tc_ld_done(v);
+          const float* lp = &ls[buf][c0 + c];
           if (all) {
+            const float2 sl2 = make_float2(sl, sl);
+            float2 e2 = make_float2(s0, s1), f2 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
               const float4 a = *reinterpret_cast<const float4*>(lp + j);
-              s0 += ex2_approx(fmaf(__uint_as_float(v[j]), sl, -a.x));
-              s1 += ex2_approx(fmaf(__uint_as_float(v[j + 1]), sl, -a.y));
-              s0 += ex2_approx(fmaf(__uint_as_float(v[j + 2]), sl, -a.z));
-              s1 += ex2_approx(fmaf(__uint_as_float(v[j + 3]), sl, -a.w));
+              float2 x = fma2(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sl2, make_float2(a.x, a.y));
+              float2 y = fma2(make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), sl2, make_float2(a.z, a.w));
+              x.x = ex2_approx(x.x);
+              x.y = ex2_approx(x.y);
+              y.x = ex2_approx(y.x);
+              y.y = ex2_approx(y.y);
+              e2 = add2(e2, x);
+              f2 = add2(f2, y);
             }
+            s0 = e2.x + f2.x;
+            s1 = e2.y + f2.y;
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const int col = c0 + c + j;
-              const float e = ex2_approx(fmaf(__uint_as_float(v[j]), sl, -lp[j]));
+              const float e = ex2_approx(fmaf(__uint_as_float(v[j]), sl, lp[j]));
               s0 += col >= jmin && col < jmax ? e : 0.f;
             }
           }
@@ -487,7 +561,6 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
         sum += s0 + s1;  // tile by tile: a sum of thousands of rows keeps its small terms
         tc_fence_before();
         mbar_arrive(&sempty[buf]);
-        mbar_arrive(&lempty[l]);
         ++tiles;
       }
       if (!ok) break;
@@ -517,8 +590,8 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
   __syncthreads();
   if (abort_flag) {
     if (warp == 16 && lane == 0) {
-      for (int i = max(0, tiles - 2); i < tiles; ++i) mbar_wait(&qfull[i & 1], (uint32_t)((i / 2) & 1));
-      for (int i = max(0, units - 2); i < units; ++i) mbar_wait(&kfull[i & 1], (uint32_t)((i / 2) & 1));
+      for (int i = max(0, tiles - kAmQ); i < tiles; ++i) mbar_wait(&qfull[i % kAmQ], (uint32_t)((i / kAmQ) & 1));
+      for (int i = max(0, units - KS); i < units; ++i) mbar_wait(&kfull[i % KS], (uint32_t)((i / KS) & 1));
     }
     if (warp == 17 && lane == 0 && tiles > 0) mbar_wait(&sfull[(tiles - 1) & 1], (uint32_t)(((tiles - 1) / 2) & 1));
     __syncthreads();
@@ -804,18 +877,22 @@ cudaError_t launch_accum_rows(const AccumRowsArgs& a, cudaStream_t s) {
   p.part = static_cast<float*>(a.ws);
   cudaError_t e;
   if (tiles) {
-    static SmemOptIn opt;
-    if ((e = opt.raise(reinterpret_cast<const void*>(accum_tiles_kernel), kAmSmem)) != cudaSuccess) return e;
+    static SmemOptIn opt[2];
+    void (*kernel)(RowsParams) = p.nq == 128 ? accum_tiles_kernel<128> : accum_tiles_kernel<64>;
+    if ((e = opt[p.nq == 128].raise(reinterpret_cast<const void*>(kernel), kAmSmem)) != cudaSuccess) return e;
     launch_begin(K_ACCUM_TILES, s);
-    accum_tiles_kernel<<<p.N, kAmThreads, kAmSmem, s>>>(p);
+    kernel<<<p.N, kAmThreads, kAmSmem, s>>>(p);
     launch_end(K_ACCUM_TILES, s);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return launch_dependent(accum_join_kernel, dim3(p.N), kAmKeys, K_ACCUM_JOIN, s, p);
   }
-  static SmemOptIn opt;
-  if ((e = opt.raise(reinterpret_cast<const void*>(accum_rows_kernel), kRwSmem)) != cudaSuccess) return e;
+  const long long most = (long long)(a.row_ids ? a.ids_stride : a.T) * p.G;
+  void (*kernel)(RowsParams) = most <= 16 ? accum_rows_kernel<1> : (most <= 32 ? accum_rows_kernel<2> : accum_rows_kernel<4>);
+  static SmemOptIn opt[3];
+  if ((e = opt[most <= 16 ? 0 : (most <= 32 ? 1 : 2)].raise(reinterpret_cast<const void*>(kernel), kRwSmem)) != cudaSuccess)
+    return e;
   launch_begin(K_ACCUM_ROWS, s);
-  accum_rows_kernel<<<p.N, kRwThreads, kRwSmem, s>>>(p);
+  kernel<<<p.N, kRwThreads, kRwSmem, s>>>(p);
   launch_end(K_ACCUM_ROWS, s);
   return cudaGetLastError();
 }

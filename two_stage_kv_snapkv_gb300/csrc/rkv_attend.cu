@@ -119,6 +119,10 @@ __global__ void __launch_bounds__(kArThreads, 1) attend_rows_kernel(const __grid
     }
   };
   settle();
+  // page ids of the run's next 32 chunks of this warp, one a lane: a load per 32 chunks
+  // instead of one, with its latency, in front of every copy
+  int ids = 0, ids_at = -1;  // ids: for chunks ids_at + 8 lane of the fetch run
+  long long ids_x = -1;
   int fetched = 0, used = 0;
   bool dead = false;
   // the stages of this ring that hold no copy: a page id out of range (its keys are skipped)
@@ -132,7 +136,13 @@ __global__ void __launch_bounds__(kArThreads, 1) attend_rows_kernel(const __grid
     int row;
     if (fc < nc) {
       const int t0 = fc * kArKeys;
-      const int phys = p.page_table[(size_t)fr.b * p.max_pages + (t0 >> p.pshift)];
+      if (ids_x != fr.x || fc >= ids_at + 32 * kArWarps) {
+        ids_x = fr.x;
+        ids_at = fc;
+        const int c = fc + lane * kArWarps;
+        ids = c < min(fr.hi, nc) ? p.page_table[(size_t)fr.b * p.max_pages + ((c * kArKeys) >> p.pshift)] : -1;
+      }
+      const int phys = __shfl_sync(0xffffffffu, ids, (fc - ids_at) / kArWarps);
       ok = phys >= 0 && phys < p.num_phys;
       row = (phys * p.Hkv + g) * p.P + (t0 & (p.P - 1));
     } else {
@@ -358,31 +368,36 @@ __global__ void __launch_bounds__(kArThreads, 1) attend_rows_kernel(const __grid
     for (int i = used; i < fetched; ++i) mbar_wait(&full_b[warp][i % kArStages], (uint32_t)((i / kArStages) & 1));
 }
 
-// Slot of CTA c's part of the unit whose chunks start at ux.
-__device__ __forceinline__ size_t part_slot(long long ux, long long total, int c, int N) {
-  return 2 * (size_t)c + (flat_first(total, c, N) >= ux ? 0 : 1);
-}
+// Where the parts of a split unit lie: CTA c's at slot 2 c, but the first CTA's at 2 c + 1
+// when its share began before the unit.
+struct PartSlots {
+  int c0, c1, late;
+  __device__ __forceinline__ PartSlots(long long ux, int per, long long total, int N)
+      : c0(flat_cta(ux, total, N)), c1(flat_cta(ux + per - 1, total, N)), late(flat_first(total, c0, N) < ux) {}
+  __device__ __forceinline__ size_t operator[](int c) const { return 2 * (size_t)c + (c == c0 ? late : 0); }
+};
 
-// Final (m, l) of one row of a split unit: the lanes of a warp take the parts c0 .. c1.
+// Final (m, l) of one row of a split unit: the lanes of a warp take its parts.
 template <int kRows>
-__device__ __forceinline__ float2 join_ml(const AttendParams& p, long long ux, long long total, int N, int c0, int c1,
-                                          int row, int lane) {
-  float M = kNoMax;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_ml[part_slot(ux, total, c, N) * kRows + row].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f;
-  for (int c = c0 + lane; c <= c1; c += 32) {
-    const float2 ml = p.part_ml[part_slot(ux, total, c, N) * kRows + row];
-    L += ml.y * ex2_approx(ml.x - M);
+__device__ __forceinline__ float2 join_ml(const AttendParams& p, const PartSlots& ps, int row, int lane) {
+  float M = kNoMax, L = 0.f;
+  for (int c = ps.c0 + lane; c <= ps.c1; c += 32) {
+    const float2 ml = p.part_ml[ps[c] * kRows + row];
+    const float to = fmaxf(M, ml.x);
+    L = L * ex2_approx(M - to) + ml.y * ex2_approx(ml.x - to);
+    M = to;
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  for (int o = 16; o; o >>= 1) {
+    const float m = __shfl_xor_sync(0xffffffffu, M, o), l = __shfl_xor_sync(0xffffffffu, L, o), to = fmaxf(M, m);
+    L = L * ex2_approx(M - to) + l * ex2_approx(m - to);
+    M = to;
+  }
   return make_float2(M, L);
 }
 
 // Joins the parts of the split units: one warp a row, four channels a lane, eight parts'
-// loads in flight.  grid (ceil(rows of a sequence / 8), B), 256 threads.
+// loads in flight.  256 threads, eight rows of the line of all rows at a time.
 template <int kRows, int kKeys>
 __device__ __forceinline__ void combine_row(const AttendParams& p, const FlatTable& ft, int b, int idx, int lane) {
   const long long total = ft.base[p.B];
@@ -398,37 +413,45 @@ __device__ __forceinline__ void combine_row(const AttendParams& p, const FlatTab
     if (lane == 0 && p.lse) p.lse[orow] = -INFINITY;
     return;
   }
-  const long long ux = ft.base[b] + (long long)(rt * p.Hkv + g) * per;
-  const int c0 = flat_cta(ux, total, N), c1 = flat_cta(ux + per - 1, total, N);
-  if (c0 == c1) return;  // final already
-  const float2 ml = join_ml<kRows>(p, ux, total, N, c0, c1, row, lane);
+  const PartSlots ps(ft.base[b] + (long long)(rt * p.Hkv + g) * per, per, total, N);
+  if (ps.c0 == ps.c1) return;  // final already
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = c0; c <= c1; c += 8) {
+  float M = kNoMax, L = 0.f;
+  for (int c = ps.c0; c <= ps.c1; c += 8) {
     float4 v[8];
-    float f[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      f[j] = 0.f;
-      v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c + j <= c1) {
-        const size_t at = part_slot(ux, total, c + j, N) * kRows + row;
-        f[j] = p.part_ml[at].x;
-        v[j] = reinterpret_cast<const float4*>(p.part_o + at * 128)[lane];
-      }
-    }
+    float2 ml[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (c + j <= c1) {
-        const float w = ex2_approx(f[j] - ml.x);
+      if (c + j <= ps.c1) {
+        const size_t at = ps[c + j] * kRows + row;
+        ml[j] = p.part_ml[at];
+        v[j] = reinterpret_cast<const float4*>(p.part_o + at * 128)[lane];
+      }
+    float to = M;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j <= ps.c1) to = fmaxf(to, ml[j].x);
+    const float f = ex2_approx(M - to);
+    M = to;
+    L *= f;
+    o.x *= f;
+    o.y *= f;
+    o.z *= f;
+    o.w *= f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j <= ps.c1) {
+        const float w = ex2_approx(ml[j].x - M);
+        L += ml[j].y * w;
         o.x += v[j].x * w;
         o.y += v[j].y * w;
         o.z += v[j].z * w;
         o.w += v[j].w * w;
       }
   }
-  const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
   *out = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (lane == 0 && p.lse) p.lse[orow] = lse_of(ml.x, ml.y);
+  if (lane == 0 && p.lse) p.lse[orow] = lse_of(M, L);
 }
 
 template <int kRows, int kKeys>
@@ -436,7 +459,9 @@ __global__ void __launch_bounds__(256) attend_combine_kernel(const __grid_consta
   __shared__ FlatTable ft;
   build_table<kRows, kKeys>(p, ft);  // lengths only: they were final before the parts' kernel began
   grid_dependency_wait();
-  combine_row<kRows, kKeys>(p, ft, blockIdx.y, blockIdx.x * 8 + (threadIdx.x >> 5), threadIdx.x & 31);
+  const long long each = (long long)p.Hq * p.T, rows = each * p.B;
+  for (long long x = blockIdx.x * 8 + (threadIdx.x >> 5); x < rows; x += gridDim.x * 8)
+    combine_row<kRows, kKeys>(p, ft, (int)(x / each), (int)(x % each), threadIdx.x & 31);
 }
 
 // The end of a one-token step: the first CTAs join the rows as attend_combine does, the
@@ -469,10 +494,8 @@ __global__ void __launch_bounds__(256) attend_weigh_kernel(const __grid_constant
     const int g = (int)((x - wbase[b]) / blocks), blk = (int)((x - wbase[b]) % blocks);
     const size_t unit = (size_t)b * p.Hkv + g;
     if (warp < p.G) {
-      const long long ux = ft.base[b] + (long long)g * ft.per[b];
-      const int c0 = flat_cta(ux, total, N), c1 = flat_cta(ux + ft.per[b] - 1, total, N);
-      const float2 ml = c0 == c1 ? p.row_ml[unit * p.G + warp]
-                                 : join_ml<kArRows>(p, ux, total, N, c0, c1, warp, lane);
+      const PartSlots ps(ft.base[b] + (long long)g * ft.per[b], ft.per[b], total, N);
+      const float2 ml = ps.c0 == ps.c1 ? p.row_ml[unit * p.G + warp] : join_ml<kArRows>(p, ps, warp, lane);
       if (lane == 0) lse2[warp] = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;  // nothing read: weighs nothing
     }
     __syncthreads();
@@ -585,18 +608,24 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
     for (long long x = x0; ok && flat_run(ft, p.B, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
       const int b = r.b, g = r.unit % p.Hkv, n = ft.n[b], nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
       const int box = p.P * 128, lanes = 256 / p.P;  // bytes of a box; boxes of a whole tile
-      auto page_of = [&](int tile) {                 // this lane's physical page of a cache tile, -1: none
+      // this lane's page id of a cache tile, -1: none; loaded two tiles ahead and judged only
+      // when it is used, so that the load's latency stays off the ring
+      auto page_of = [&](int tile) {
         const int pg = tile * (kAtKeys >> p.pshift) + (lane >> 1);
-        if (tile >= nc || lane >= lanes || pg * p.P >= n) return -1;
-        const int phys = p.page_table[(size_t)b * p.max_pages + pg];
-        if (phys >= 0 && phys < p.num_phys) return phys;
-        flag_error(p.err, RKV_DEVERR_PAGE_ID);
-        return -1;
+        return tile < nc && lane < lanes && pg * p.P < n ? p.page_table[(size_t)b * p.max_pages + pg] : -1;
       };
       auto issue = [&](int tile, int phys, bool v) {
         const int e = loaded % E;
-        if (loaded >= E && !mbar_wait(&empty_b[e], (uint32_t)((loaded / E - 1) & 1))) give_up();
-        if (__any_sync(0xffffffffu, abort_flag)) return false;
+        const int pg = tile * (kAtKeys >> p.pshift) + (lane >> 1);
+        if (phys < 0 || phys >= p.num_phys) {
+          if (tile < nc && lane < lanes && pg * p.P < n) flag_error(p.err, RKV_DEVERR_PAGE_ID);
+          phys = -1;
+        }
+        const bool late = loaded >= E && !mbar_wait_role(&empty_b[e], (uint32_t)((loaded / E - 1) & 1), &abort_flag);
+        if (__any_sync(0xffffffffu, late)) {
+          give_up();
+          return false;
+        }
         uint8_t* st = ring + e * kAtEntry;
         if (tile < nc) {
           const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0);
@@ -642,8 +671,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
     int seen_p[2] = {0, 0}, runs[2] = {0, 0};
     bool ok = true;
     auto wait = [&](uint64_t* bar, int phase) {
-      if (!mbar_wait(bar, (uint32_t)(phase & 1))) give_up();
-      return !__any_sync(0xffffffffu, abort_flag);
+      const bool late = !mbar_wait_role(bar, (uint32_t)(phase & 1), &abort_flag);
+      if (__any_sync(0xffffffffu, late)) {
+        give_up();
+        return false;
+      }
+      return true;
     };
     // S of `slot` from the K entry e (its copy has landed)
     auto mma_s = [&](int slot, int e, bool release) {
@@ -766,9 +799,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
     int seen_s = 0, run = 0, done[2] = {0, 0};
     bool ok = true;
     auto wait = [&](uint64_t* bar, int phase) {
-      const bool late = !mbar_wait(bar, (uint32_t)(phase & 1));
-      if (late) give_up();
-      return !__any_sync(0xffffffffu, late || abort_flag);  // warp-uniform: the TMEM accesses are .aligned
+      const bool late = !mbar_wait_role(bar, (uint32_t)(phase & 1), &abort_flag);
+      if (__any_sync(0xffffffffu, late)) {  // warp-uniform: the TMEM accesses are .aligned
+        give_up();
+        return false;
+      }
+      return true;
     };
     for (long long x = x0; ok && flat_run(ft, p.B, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
       const int b = r.b, g = r.unit % p.Hkv, rt = r.unit / p.Hkv;
@@ -780,11 +816,17 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
         const int q0 = kWide ? 0 : slot * 64;
         uint8_t* dst = qs + (kWide ? slot * (128 * 256) : 0);
         const int piece = row & 15;
-        for (int i = q0 + (row >> 4); i < q0 + kPer; i += 8) {
-          const int rr = rt * R + (kWide ? slot * 128 : 0) + i;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (rr < rows) v = reinterpret_cast<const uint4*>(p.q + out_row(p, b, g, rr) * 128)[piece];
-          *reinterpret_cast<uint4*>(dst + (piece >> 3) * (128 * 128) + i * 128 + (((piece & 7) ^ (i & 7)) << 4)) = v;
+        uint4 v[kPer / 8];  // all loads in flight together
+#pragma unroll
+        for (int j = 0; j < kPer / 8; ++j) {
+          const int rr = rt * R + (kWide ? slot * 128 : 0) + q0 + (row >> 4) + j * 8;
+          v[j] = make_uint4(0, 0, 0, 0);
+          if (rr < rows) v[j] = reinterpret_cast<const uint4*>(p.q + out_row(p, b, g, rr) * 128)[piece];
+        }
+#pragma unroll
+        for (int j = 0; j < kPer / 8; ++j) {
+          const int i = q0 + (row >> 4) + j * 8;
+          *reinterpret_cast<uint4*>(dst + (piece >> 3) * (128 * 128) + i * 128 + (((piece & 7) ^ (i & 7)) << 4)) = v[j];
         }
         fence_proxy_async_smem();
         mbar_arrive(&q_b[kWide ? slot : 0]);
@@ -816,19 +858,25 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
             }
           }
           uint32_t v[4][32];
-          float mx = -INFINITY;
+          float mx = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tc_ld32(mine + c * 32, v[c]);
+          tc_ld_wait();
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            tc_ld32_wait(mine + c * 32, v[c]);
+            tc_ld_done(v[c]);
             if (!all) {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 if (!((see[c] >> j) & 1u)) v[c][j] = 0xff800000u;  // -inf
             }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(v[c][j]));
+            for (int j = 0; j < 32; j += 4) {
+              mx = max3(mx, __uint_as_float(v[c][j]), __uint_as_float(v[c][j + 1]));
+              mx1 = max3(mx1, __uint_as_float(v[c][j + 2]), __uint_as_float(v[c][j + 3]));
+            }
           }
-          mx *= sl;  // sl > 0
+          mx = fmaxf(mx, mx1) * sl;  // sl > 0
           const bool first = i < (kWide ? 1 : 2);
           if (first) {
             m = fmaxf(kNoMax, mx);
@@ -846,23 +894,25 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
               tc_st32_wait(mine + 128 + c * 32, o);
             }
           }
-          float s0 = 0.f, s1 = 0.f;
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 sl2 = make_float2(sl, sl), m2 = make_float2(-m, -m);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t pk[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const int cc = c * 2 + (j >> 4), jj = (j & 15) * 2;
-              const float a0 = ex2_approx(fmaf(__uint_as_float(v[cc][jj]), sl, -m));
-              const float a1 = ex2_approx(fmaf(__uint_as_float(v[cc][jj + 1]), sl, -m));
-              s0 += a0;
-              s1 += a1;
+              float2 a = fma2(make_float2(__uint_as_float(v[cc][jj]), __uint_as_float(v[cc][jj + 1])), sl2, m2);
+              a.x = ex2_approx(a.x);
+              a.y = ex2_approx(a.y);
+              sum[j & 1] = add2(sum[j & 1], a);
               // bf16 weights (off by at most 2^-8 of each, as V is); their sum stays unrounded
-              pk[j] = pack_bf16x2(a0, a1);
+              pk[j] = pack_bf16x2(a.x, a.y);
             }
-            tc_st32_wait(mine + c * 32, pk);
+            tc_st32(mine + c * 32, pk);
           }
-          l += s0 + s1;
+          tc_st_wait();
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tc_fence_before();
           mbar_arrive(&p_b[slot]);
         }
@@ -1032,7 +1082,8 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
     w += align256((size_t)c.B * a.Hq * 8);
     p.z = reinterpret_cast<float*>(w);
   }
-  const dim3 jgrid((a.Hq * a.T + 7) / 8, c.B);
+  const long long jrows = ((long long)c.B * a.Hq * a.T + 7) / 8, jmost = 6LL * p.N;
+  const dim3 jgrid((unsigned)(jrows < jmost ? jrows : jmost));
   if (tile > kArRows) {
     const bool wide = tile == 256;
     static SmemOptIn opt[2];

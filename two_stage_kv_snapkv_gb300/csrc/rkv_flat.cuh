@@ -67,9 +67,15 @@ __device__ __forceinline__ void flat_build(FlatTable& ft, int B, Len len, Rows r
 // CTAs that take part: no more than there are pieces, so that no share is empty and every
 // CTA between a unit's first and last holds a part of it.
 __device__ __forceinline__ int flat_ctas(long long total, int N) { return (int)min((long long)N, total); }
-__device__ __forceinline__ long long flat_first(long long total, int i, int N) { return total * i / N; }
+// 32-bit divisions where the operands allow it: a 64-bit one costs about a hundred
+// instructions.  N is at most kMaxSms + 1 < 2^10.
+__device__ __forceinline__ long long flat_first(long long total, int i, int N) {
+  if (total < (1 << 20)) return (uint32_t)total * (uint32_t)i / (uint32_t)N;
+  return total * i / N;
+}
 // The CTA whose share holds piece x.
 __device__ __forceinline__ int flat_cta(long long x, long long total, int N) {
+  if (total < (1 << 20)) return (int)(((uint32_t)(x + 1) * (uint32_t)N - 1) / (uint32_t)total);
   return (int)(((x + 1) * N - 1) / total);
 }
 // The sequence that holds piece x (0 <= x < base[B]).
@@ -95,7 +101,7 @@ __device__ __forceinline__ bool flat_run(const FlatTable& ft, int B, long long x
   r.b = flat_seq(ft, B, x);
   const int per = ft.per[r.b];
   const long long off = x - ft.base[r.b];
-  r.unit = (int)(off / per);
+  r.unit = off < (1LL << 31) ? (int)((uint32_t)off / (uint32_t)per) : (int)(off / per);
   r.lo = (int)(off - (long long)r.unit * per);
   r.hi = (int)min((long long)per, r.lo + (x1 - x));
   r.whole = r.lo == 0 && r.hi == per;

@@ -401,31 +401,40 @@ def rkv_decode_sparq(cache: PagedCache, q: torch.Tensor, k1: Sequence[int], k_to
 
 
 # ------------------------------------------------------------------ tree decoding, accumulated weights
-def _want(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype, device) -> None:
+def _arg(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype, device) -> Optional[int]:
+    """The address of a tensor that must have this shape, type and device and be contiguous
+    (None stays None)."""
     if t is None:
-        return
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name}: expected {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors passed to librkv must be contiguous")
+    return t.data_ptr()
 
 
-def _want_acc(acc: torch.Tensor, name: str, cache: "PagedCache", device) -> None:
-    if acc.dim() != 3:
-        raise ValueError(f"{name}: expected [B, Hkv, positions], got {list(acc.shape)}")
-    _want(acc, name, (cache.B, cache.Hkv, acc.shape[2]), torch.float32, device)
+def _acc_arg(acc: torch.Tensor, name: str, cache: "PagedCache", device) -> int:
+    if acc is None or acc.dim() != 3:
+        raise ValueError(f"{name}: expected [B, Hkv, positions]")
+    return _arg(acc, name, (cache.B, cache.Hkv, acc.shape[2]), torch.float32, device)
 
 
-def _want_ws(workspace: torch.Tensor, device) -> None:
-    if workspace.dtype != torch.uint8 or workspace.device != device:
-        raise ValueError(f"workspace: expected torch.uint8 on {device}, got {workspace.dtype} on {workspace.device}")
+def _ws_arg(workspace: torch.Tensor, device) -> int:
+    if workspace.dtype != torch.uint8:
+        raise ValueError(f"workspace: expected torch.uint8, got {workspace.dtype}")
+    return _arg(workspace, "workspace", workspace.shape, torch.uint8, device)
 
 
 def _call_on(device, stream, fn, *args) -> None:
     """fn(*args, stream) with the tensors' device current (its current stream when none is given)."""
     if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
+        raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)))
+            status = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream)
+    if status != RKV_OK:
+        _check(status)
 
 
 def tree_workspace(B: int, Hq: int, Hkv: int, T: int, max_pages: int, page_size: int, device="cuda") -> torch.Tensor:
@@ -445,20 +454,16 @@ def rkv_tree_attention(cache: PagedCache, q: torch.Tensor, k_tree: torch.Tensor,
     B, Hq, T, d = q.shape
     dev = cache.k_pages.device
     bf16 = torch.bfloat16
-    _want(q, "q", (cache.B, Hq, T, HEAD_DIM), bf16, dev)
-    _want(k_tree, "k_tree", (B, cache.Hkv, T, HEAD_DIM), bf16, dev)
-    _want(v_tree, "v_tree", (B, cache.Hkv, T, HEAD_DIM), bf16, dev)
-    _want(tree_mask, "tree_mask", (B, T, (T + 31) // 32), torch.int32, dev)
-    _want(out, "out", (B, Hq, T, HEAD_DIM), bf16, dev)
-    _want(lse, "lse", (B, Hq, T), torch.float32, dev)
-    _want(tree_len, "tree_len", (B,), torch.int32, dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    args = (_arg(q, "q", (cache.B, Hq, T, HEAD_DIM), bf16, dev),
+            _arg(k_tree, "k_tree", (B, cache.Hkv, T, HEAD_DIM), bf16, dev),
+            _arg(v_tree, "v_tree", (B, cache.Hkv, T, HEAD_DIM), bf16, dev),
+            _arg(tree_mask, "tree_mask", (B, T, (T + 31) // 32), torch.int32, dev), Hq, T,
+            _arg(tree_len, "tree_len", (B,), torch.int32, dev), 1.0 / math.sqrt(d) if scale is None else scale,
+            _arg(out, "out", (B, Hq, T, HEAD_DIM), bf16, dev), _arg(lse, "lse", (B, Hq, T), torch.float32, dev))
     if workspace is None:
         workspace = tree_workspace(B, Hq, cache.Hkv, T, cache.max_pages, cache.page_size, dev)
-    _want_ws(workspace, dev)
-    _call_on(dev, stream, _lib.rkv_tree_attention, ctypes.byref(cache.struct), _ptr(q), _ptr(k_tree), _ptr(v_tree),
-             _ptr(tree_mask), Hq, T, _ptr(tree_len), scale, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel())
+    _call_on(dev, stream, _lib.rkv_tree_attention, ctypes.byref(cache.struct), *args, _ws_arg(workspace, dev),
+             workspace.numel())
 
 
 def rkv_tree_commit(cache: PagedCache, k_tree: torch.Tensor, v_tree: torch.Tensor, path: torch.Tensor,
@@ -469,12 +474,11 @@ def rkv_tree_commit(cache: PagedCache, k_tree: torch.Tensor, v_tree: torch.Tenso
         raise ValueError("k_tree: expected [B, Hkv, T, 128]; path: expected [B, nodes]")
     T = k_tree.shape[2]
     dev = cache.k_pages.device
-    _want(k_tree, "k_tree", (cache.B, cache.Hkv, T, HEAD_DIM), torch.bfloat16, dev)
-    _want(v_tree, "v_tree", (cache.B, cache.Hkv, T, HEAD_DIM), torch.bfloat16, dev)
-    _want(path, "path", (cache.B, path.shape[1]), torch.int32, dev)
-    _want(path_len, "path_len", (cache.B,), torch.int32, dev)
-    _call_on(dev, stream, _lib.rkv_tree_commit, ctypes.byref(cache.struct), _ptr(k_tree), _ptr(v_tree), T, _ptr(path),
-             path.shape[1], _ptr(path_len))
+    shape = (cache.B, cache.Hkv, T, HEAD_DIM)
+    args = (_arg(k_tree, "k_tree", shape, torch.bfloat16, dev), _arg(v_tree, "v_tree", shape, torch.bfloat16, dev), T,
+            _arg(path, "path", (cache.B, path.shape[1]), torch.int32, dev), path.shape[1],
+            _arg(path_len, "path_len", (cache.B,), torch.int32, dev))
+    _call_on(dev, stream, _lib.rkv_tree_commit, ctypes.byref(cache.struct), *args)
 
 
 def accum_workspace(B: int, Hq: int, Hkv: int, max_pages: int, page_size: int, device="cuda") -> torch.Tensor:
@@ -497,17 +501,13 @@ def rkv_decode_accum(cache: PagedCache, q: torch.Tensor, out: torch.Tensor, acc:
         raise ValueError(f"q: expected [B, Hq, {HEAD_DIM}], got {list(q.shape)}")
     B, Hq, d = q.shape
     dev = cache.k_pages.device
-    _want(q, "q", (cache.B, Hq, HEAD_DIM), torch.bfloat16, dev)
-    _want(out, "out", (B, Hq, HEAD_DIM), torch.bfloat16, dev)
-    _want(lse, "lse", (B, Hq), torch.float32, dev)
-    _want_acc(acc, "acc", cache, dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    args = (_arg(q, "q", (cache.B, Hq, HEAD_DIM), torch.bfloat16, dev), Hq, 1.0 / math.sqrt(d) if scale is None else scale,
+            _arg(out, "out", (B, Hq, HEAD_DIM), torch.bfloat16, dev), _arg(lse, "lse", (B, Hq), torch.float32, dev),
+            _acc_arg(acc, "acc", cache, dev), acc.shape[2])
     if workspace is None:
         workspace = accum_workspace(B, Hq, cache.Hkv, cache.max_pages, cache.page_size, dev)
-    _want_ws(workspace, dev)
-    _call_on(dev, stream, _lib.rkv_decode_accum, ctypes.byref(cache.struct), _ptr(q), Hq, scale, _ptr(out), _ptr(lse),
-             _ptr(acc), acc.shape[2], _ptr(workspace), workspace.numel())
+    _call_on(dev, stream, _lib.rkv_decode_accum, ctypes.byref(cache.struct), *args, _ws_arg(workspace, dev),
+             workspace.numel())
 
 
 def accum_rows_workspace(B: int, Hq: int, Hkv: int, T: int, max_pages: int, page_size: int,
@@ -526,21 +526,17 @@ def rkv_accum_rows(cache: PagedCache, q: torch.Tensor, lse: torch.Tensor, acc: t
         raise ValueError(f"q: expected [B, Hq, T, {HEAD_DIM}], got {list(q.shape)}")
     B, Hq, T, d = q.shape
     dev = cache.k_pages.device
-    _want(q, "q", (cache.B, Hq, T, HEAD_DIM), torch.bfloat16, dev)
-    _want(lse, "lse", (B, Hq, T), torch.float32, dev)
-    _want(row_len, "row_len", (B,), torch.int32, dev)
     if row_ids is not None and row_ids.dim() != 2:
         raise ValueError(f"row_ids: expected [B, rows], got {list(row_ids.shape)}")
     ids = row_ids.shape[1] if row_ids is not None else 0
-    _want(row_ids, "row_ids", (B, ids), torch.int32, dev)
-    _want_acc(acc, "acc", cache, dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    args = (_arg(q, "q", (cache.B, Hq, T, HEAD_DIM), torch.bfloat16, dev),
+            _arg(lse, "lse", (B, Hq, T), torch.float32, dev), Hq, T, _arg(row_len, "row_len", (B,), torch.int32, dev),
+            _arg(row_ids, "row_ids", (B, ids), torch.int32, dev), ids, 1.0 / math.sqrt(d) if scale is None else scale,
+            _acc_arg(acc, "acc", cache, dev), acc.shape[2])
     if workspace is None:
         workspace = accum_rows_workspace(B, Hq, cache.Hkv, T, cache.max_pages, cache.page_size, dev)
-    _want_ws(workspace, dev)
-    _call_on(dev, stream, _lib.rkv_accum_rows, ctypes.byref(cache.struct), _ptr(q), _ptr(lse), Hq, T, _ptr(row_len),
-             _ptr(row_ids), ids, scale, _ptr(acc), acc.shape[2], _ptr(workspace), workspace.numel())
+    _call_on(dev, stream, _lib.rkv_accum_rows, ctypes.byref(cache.struct), *args, _ws_arg(workspace, dev),
+             workspace.numel())
 
 
 def evict_workspace(B: int, Hkv: int, max_keep: int, device="cuda", in_place: bool = True) -> torch.Tensor:
@@ -559,19 +555,16 @@ def rkv_evict_accum(cache: PagedCache, acc: torch.Tensor, keep: Sequence[int], r
         raise ValueError(f"keep: expected {cache.B} values, got {len(keep)}")
     if kept_idx.dim() != 3:
         raise ValueError(f"kept_idx: expected [B, Hkv, tokens], got {list(kept_idx.shape)}")
-    _want(kept_idx, "kept_idx", (cache.B, cache.Hkv, kept_idx.shape[2]), torch.int32, dev)
-    _want_acc(acc, "acc", cache, dev)
     if dst is not None and dst.k_pages.device != dev:
         raise ValueError("dst lies on another device")
-    if dst_acc is not None:
-        _want_acc(dst_acc, "dst_acc", cache if dst is None else dst, dev)
+    kept = _arg(kept_idx, "kept_idx", (cache.B, cache.Hkv, kept_idx.shape[2]), torch.int32, dev)
+    sums = _acc_arg(acc, "acc", cache, dev)
+    to = _acc_arg(dst_acc, "dst_acc", cache, dev) if dst_acc is not None else None
     if workspace is None:
-        workspace = evict_workspace(cache.B, cache.Hkv, max(1, max(int(x) for x in keep)), dev,
-                                    in_place=dst is None)
-    _want_ws(workspace, dev)
-    _call_on(dev, stream, _lib.rkv_evict_accum, ctypes.byref(cache.struct), _ptr(acc), acc.shape[2], _host_i32(keep),
-             int(recent), _ptr(kept_idx), kept_idx.shape[2], ctypes.byref(dst.struct) if dst is not None else None,
-             _ptr(dst_acc), dst_acc.shape[2] if dst_acc is not None else 0, _ptr(workspace), workspace.numel())
+        workspace = evict_workspace(cache.B, cache.Hkv, max(1, max(int(x) for x in keep)), dev, in_place=dst is None)
+    _call_on(dev, stream, _lib.rkv_evict_accum, ctypes.byref(cache.struct), sums, acc.shape[2], _host_i32(keep),
+             int(recent), kept, kept_idx.shape[2], ctypes.byref(dst.struct) if dst is not None else None, to,
+             dst_acc.shape[2] if dst_acc is not None else 0, _ws_arg(workspace, dev), workspace.numel())
 
 
 def rkv_exact_topk_recall(cache: PagedCache, q: torch.Tensor, sel_pages: torch.Tensor, k_tokens: Sequence[int],
