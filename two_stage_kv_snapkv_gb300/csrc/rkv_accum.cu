@@ -447,7 +447,9 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
       }
     }
   } else if (warp == 17) {
-    const uint32_t idesc = idesc_bf16_f32(128, nq), k32 = smem_u32(ks), q32 = smem_u32(qs);
+    constexpr uint32_t idesc = idesc_bf16_f32(128, nq);
+    const bool lead = elect_lane();
+    const uint32_t klo = sw128_kmajor_lo(smem_u32(ks)), qlo = sw128_kmajor_lo(smem_u32(qs));
     for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
       const int s = units % KS;
       if (!(ok = wait(&kfull[s], units / KS))) break;
@@ -458,22 +460,22 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
         // the rows' log-sum-exps are written after the buffer's last reading, so this wait
         // covers the logits' buffer too
         if (!(ok = wait(&lfull[d], tiles / 2))) break;
-        if (lane == 0) {
-          tc_fence_after();
+        tc_fence_after();
+        const uint32_t q = qlo + t * (QB >> 4);
 #pragma unroll
-          for (int w = 0; w < 2; ++w)
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t to = tmem + d * 256 + w * 128, key = klo + s * (65536 >> 4) + w * (32768 >> 4);
+          tc_mma_ss<false>(lead, to, key, q, idesc);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t in = (k & 3) * 32;
-              tc_mma_bf16(tmem + d * 256 + w * 128,
-                          sw128_kmajor_desc(k32 + s * 65536 + w * 32768 + (k >> 2) * 16384 + in),
-                          sw128_kmajor_desc(q32 + t * QB + (k >> 2) * (QB / 2) + in), idesc, k > 0);
-            }
-          tc_commit(&qempty[t]);
-          if (o + 1 == r.hi) tc_commit(&kempty[s]);
-          tc_commit(&sfull[d]);
-          mbar_arrive(&sfull[d]);
+          for (int k = 1; k < 8; ++k) {
+            const uint32_t in = (k & 3) * 32;
+            tc_mma_ss<true>(lead, to, key + (((k >> 2) * 16384 + in) >> 4), q + (((k >> 2) * (QB / 2) + in) >> 4), idesc);
+          }
         }
+        tc_commit_if(lead, &qempty[t]);
+        tc_commit_if(lead && o + 1 == r.hi, &kempty[s]);
+        tc_commit_if(lead, &sfull[d]);
+        if (lead) mbar_arrive(&sfull[d]);
         __syncwarp();
         ++tiles;
       }

@@ -678,35 +678,32 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
       }
       return true;
     };
+    const bool lead = elect_lane();
+    const uint32_t qlo = sw128_kmajor_lo(q32), klo = sw128_kmajor_lo(ring32), vlo = sw128_nmajor_lo(ring32, kAtEntry / 2);
     // S of `slot` from the K entry e (its copy has landed)
     auto mma_s = [&](int slot, int e, bool release) {
-      if (lane == 0) {
-        tc_fence_after();
-        sgroups[slot] = groups[e];
-        const uint32_t qa = q32 + (kWide ? slot * (128 * 256) : 0), ka = ring32 + e * kAtEntry;
+      tc_fence_after();
+      if (lead) sgroups[slot] = groups[e];
+      const uint32_t d = tmem + slot * 256, qa = qlo + (kWide ? slot * (128 * 256 >> 4) : 0), ka = klo + e * (kAtEntry >> 4);
+      tc_mma_ss<false>(lead, d, qa, ka, idesc_s);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t off = (k >> 2) * (kAtEntry / 2) + (k & 3) * 32;
-          tc_mma_bf16(tmem + slot * 256, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off), idesc_s, k > 0);
-        }
-        if (release) tc_commit(&empty_b[e]);
-        tc_commit(&s_b[slot]);
-        mbar_arrive(&s_b[slot]);
+      for (int k = 1; k < 8; ++k) {
+        const uint32_t off = ((k >> 2) * (kAtEntry / 2) + (k & 3) * 32) >> 4;
+        tc_mma_ss<true>(lead, d, qa + off, ka + off, idesc_s);
       }
+      tc_commit_if(lead && release, &empty_b[e]);
+      tc_commit_if(lead, &s_b[slot]);
+      if (lead) mbar_arrive(&s_b[slot]);
       __syncwarp();
     };
     auto mma_o = [&](int slot, int e, bool first, bool last, bool release) {
-      if (lane == 0) {
-        tc_fence_after();
-        const uint32_t va = ring32 + e * kAtEntry;
+      tc_fence_after();
+      const uint32_t d = tmem + slot * 256 + 128, pa = tmem + slot * 256, va = vlo + e * (kAtEntry >> 4);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc_mma_bf16_ts(tmem + slot * 256 + 128, tmem + slot * 256 + k * 8,
-                         sw128_nmajor_desc(va + k * 2048, kAtEntry / 2), idesc_o, (first && k == 0) ? 0u : 1u);
-        if (release) tc_commit(&empty_b[e]);
-        if (last) tc_commit(&o_b[slot]);
-      }
-      __syncwarp();
+      for (int k = 0; k < 8; ++k)
+        tc_mma_ts(lead, d, pa + k * 8, va + (k * 2048 >> 4), idesc_o, (first && k == 0) ? 0u : 1u);
+      tc_commit_if(lead && release, &empty_b[e]);
+      tc_commit_if(lead && last, &o_b[slot]);
     };
     for (long long x = x0; ok && flat_run(ft, p.B, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
       const int b = r.b, n = ft.n[b], nodes = ft.t[b], nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
@@ -747,7 +744,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
           const bool last = i + 1 == nt;
           if (!(ok = wait(&p_b[0], seen_p[0]++))) break;
           mma_o(0, ev, i == 0, last, !two);
-          if (last && !two && lane == 0) tc_commit(&o_b[1]);  // keeps an idle slot in step
+          if (kWide) tc_commit_if(lead && last && !two, &o_b[1]);  // keeps an idle slot in step
           int en = 0;
           if (!last) {
             en = take();

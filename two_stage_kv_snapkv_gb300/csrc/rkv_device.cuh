@@ -303,17 +303,6 @@ __device__ __forceinline__ void tc_st32_wait(uint32_t taddr, const uint32_t (&r)
   tc_st32(taddr, r);
   tc_st_wait();
 }
-// D[tmem] (+)= A[tmem] * B[smem], bf16 in, fp32 accumulate; A: row = lane, two K elements
-// to a column.
-__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // Shared-memory matrix descriptor of a K-major bf16 operand stored as TMA writes it with
 // 128-byte swizzle: rows of 128 B (64 elements of K), 8-row groups 1024 B apart, the
 // atom 1024-byte aligned.  Fields: start address >> 4 (bits 0-13), leading byte offset
@@ -324,13 +313,51 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t saddr) {
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-// The same for an operand whose rows run along K (N contiguous: V's [key][channel] as the
-// B of P V): 64 elements of N to a 128-byte row, 8 rows of K to a 1024-byte group.  The
-// leading offset steps from 64 elements of N to the next 64, the stride offset from 8
-// rows of K to the next 8; a K step of 16 is a +2048 B start address.
-__device__ __forceinline__ uint64_t sw128_nmajor_desc(uint32_t saddr, uint32_t n_block_bytes) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(n_block_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// The two halves of such a descriptor.  The high one is the same for every operand here;
+// the low one moves with the address, so a step along K is one 32-bit addition.
+// kmajor: as above.  nmajor: an operand whose rows run along K (N contiguous: V's
+// [key][channel] as the B of P V), 64 elements of N to a 128-byte row, 8 rows of K to a
+// 1024-byte group; the leading offset steps from 64 elements of N to the next 64 and a K
+// step of 16 is +2048 B.
+constexpr uint32_t kSw128DescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t sw128_kmajor_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | (1u << 16); }
+__device__ __forceinline__ uint32_t sw128_nmajor_lo(uint32_t saddr, uint32_t n_block_bytes) {
+  return ((saddr >> 4) & 0x3FFFu) | ((n_block_bytes >> 4) << 16);
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// tc_mma_bf16 from descriptor halves, A in shared memory (ss) or in TMEM (ts: row = lane,
+// two K elements to a column).  Called by a whole warp, issued where `issue` holds: the
+// operands then stay in uniform registers.  (Issued from one lane's branch with 64-bit
+// descriptors built per instruction, an MMA cost 115 clocks of issue against 64 of work.)
+template <bool kAccumulate>
+__device__ __forceinline__ void tc_mma_ss(bool issue, uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 q, %0, 0;\n setp.ne.b32 p, %6, 0;\n"
+      " mov.b64 x, {%2, %4};\n mov.b64 y, {%3, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%1], x, y, %5, p;\n}\n" ::"r"((uint32_t)issue),
+      "r"(d_tmem), "r"(alo), "r"(blo), "r"(kSw128DescHi), "r"(idesc), "n"(kAccumulate ? 1 : 0)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(bool issue, uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 y;\n setp.ne.b32 q, %0, 0;\n setp.ne.b32 p, %6, 0;\n"
+      " mov.b64 y, {%3, %4};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], y, %5, p;\n}\n" ::"r"((uint32_t)issue),
+      "r"(d_tmem), "r"(a_tmem), "r"(blo), "r"(kSw128DescHi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_if(bool issue, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n}\n" ::"r"((uint32_t)issue),
+      "r"(smem_u32(bar))
+      : "memory");
 }
 constexpr uint32_t kIdescBNMajor = 1u << 16;  // B runs along N in memory
 // Instruction descriptor of kind::f16 with bf16 A and B, fp32 D, both K-major:
