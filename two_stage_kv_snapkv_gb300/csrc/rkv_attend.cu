@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(256) attend_weigh_kernel(const __grid_constant
 // channels x 256 rows x 4 = 16.8 MFLOP: at the card's rates the bytes take 1.4 us of an
 // SM's share and the products 1.1 us, so the wide form sits near both roofs and the narrow
 // one on the bytes alone.
-//   warps 0-3, 4-7: softmax of slot 0, 1;  warp 8: TMA;  warp 9: MMA issue.
+//   warps 0-3, 4-7: softmax of slot 0, 1;  warp 8: TMA;  warp 9: MMA issue;  10, 11: idle.
 // The running maximum that the weights refer to moves only when a row's new maximum is
 // above it by more than 8 (base 2): weights then stay below 2^8 and O is rescaled, a TMEM
 // round trip of 64 KB, a few times a run instead of every tile.
@@ -542,32 +542,81 @@ __global__ void __launch_bounds__(256) attend_weigh_kernel(const __grid_constant
 // and the MMA side.  Every wait is bounded; one that runs out flags RKV_DEVERR_TIMEOUT and
 // stops every role.
 constexpr int kAtKeys = 128;
-constexpr int kAtThreads = 320;
+constexpr int kAtThreads = 384;
+// Registers: 384 threads start with 168 each; the softmax warps take 208 and the third
+// warpgroup (TMA, MMA, two idle warps) keeps 88: 256 x 208 + 128 x 88 = 384 x 168.
+constexpr int kAtSoftRegs = 208, kAtIssueRegs = 88;
+static_assert(256 * kAtSoftRegs + 128 * kAtIssueRegs == 384 * 168, "the split must be what the block was launched with");
 constexpr int kAtEntry = 128 * 256;
 constexpr float kAtSlack = 8.f;
 template <bool kWide>
 struct TileShape {
   static constexpr int kRows = kWide ? 256 : 128;
   static constexpr int kQBytes = kRows * 256;
-  static constexpr int kEntries = kWide ? 4 : 5;
-  static constexpr int kSmem = 1024 + kQBytes + kEntries * kAtEntry;
+  static constexpr int kEntries = 5;
+  // Everything lies in dynamic shared memory, whose start is aligned to 1024 bytes: queries
+  // and ring fill 224 of the 227 KB in the wide form, with no room for a rounding.
+  struct Shared {
+    uint8_t q[kQBytes];
+    uint8_t ring[kEntries * kAtEntry];
+    long long base[RKV_MAX_BATCH + 1];
+    uint64_t full[kEntries], empty[kEntries], s[2], p[2], o[2], qf[2], out[2], ml;
+    uint32_t groups[kEntries];  // a K entry's 16-key groups that were loaded (page ids in range)
+    uint32_t sgroups[2];        // the same for the tile whose logits a slot holds
+    uint32_t tmem_base;
+    int abort_flag;
+    float2 ml_s[kWide ? 1 : 2][kWide ? 1 : 128];
+  };
+  static constexpr int kSmem = sizeof(Shared);
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
+
+// The tiled kernel's table: only the line's offsets; a run's lengths are read again.
+struct SlimRun : FlatRun {
+  int n, t;
+};
+template <int kRows, int kKeys>
+__device__ __forceinline__ int pieces_of(const AttendParams& p, int n, int t) {
+  (void)p;
+  return (n + kKeys - 1) / kKeys + (p.mask ? (t + kKeys - 1) / kKeys : 0);
+}
+template <int kRows, int kKeys>
+__device__ __forceinline__ bool slim_run(const AttendParams& p, const long long* base, long long x, long long x0,
+                                         long long x1, SlimRun& r) {
+  if (x >= x1) return false;
+  int lo = 0, hi = p.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (base[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  r.b = lo;
+  r.n = checked_len(p, lo);
+  r.t = checked_nodes(p, lo);
+  const int per = pieces_of<kRows, kKeys>(p, r.n, r.t);
+  const long long off = x - base[lo];
+  r.unit = off < (1LL << 31) ? (int)((uint32_t)off / (uint32_t)per) : (int)(off / per);
+  r.lo = (int)(off - (long long)r.unit * per);
+  r.hi = (int)min((long long)per, r.lo + (x1 - x));
+  r.whole = r.lo == 0 && r.hi == per;
+  r.first = x == x0;
+  r.x = x;
+  return true;
+}
 
 template <bool kWide>
 __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __grid_constant__ AttendParams p) {
   using Sh = TileShape<kWide>;
   constexpr int E = Sh::kEntries, R = Sh::kRows;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ FlatTable ft;
-  __shared__ uint64_t full_b[E], empty_b[E], s_b[2], p_b[2], o_b[2], q_b[2], ml_b;
-  __shared__ uint32_t groups[E];   // a K entry's 16-key groups that were loaded (page ids in range)
-  __shared__ uint32_t sgroups[2];  // the same for the tile whose logits a slot holds
-  __shared__ float2 ml_s[2][128];
-  __shared__ uint32_t tmem_base;
-  __shared__ volatile int abort_flag;
+  extern __shared__ __align__(1024) uint8_t dyn_smem[];
+  typename Sh::Shared& sh = *reinterpret_cast<typename Sh::Shared*>(dyn_smem);
+  uint64_t *const full_b = sh.full, *const empty_b = sh.empty, *const s_b = sh.s, *const p_b = sh.p, *const o_b = sh.o,
+                  *const q_b = sh.qf;
+  uint64_t* const ml_b = &sh.ml;
+  uint32_t *const groups = sh.groups, *const sgroups = sh.sgroups;
+  volatile int& abort_flag = *const_cast<volatile int*>(&sh.abort_flag);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint8_t* qs = align1024(smem);
-  uint8_t* ring = qs + Sh::kQBytes;
+  uint8_t* const qs = sh.q;
+  uint8_t* const ring = sh.ring;
   if (tid == 0) {
     for (int e = 0; e < E; ++e) {
       mbar_init(&full_b[e], 1);
@@ -578,21 +627,25 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
       mbar_init(&p_b[s], 128);
       mbar_init(&o_b[s], 1);
       mbar_init(&q_b[s], kWide ? 128 : 256);
+      mbar_init(&sh.out[s], kWide ? 128 : 256);
     }
-    mbar_init(&ml_b, 256);
+    mbar_init(ml_b, 256);
     abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 9) {
-    tmem_alloc(&tmem_base, 512);
+    tmem_alloc(&sh.tmem_base, 512);
     tmem_relinquish();
   }
   tc_fence_before();
-  build_table<R, kAtKeys>(p, ft);  // ends with a block barrier
+  flat_scan(sh.base, p.B, [&](int b) {  // ends with a block barrier
+    const int t = checked_nodes(p, b);
+    return (long long)pieces_of<R, kAtKeys>(p, checked_len(p, b), t) * p.Hkv * ((t * p.G + R - 1) / R);
+  });
   tc_fence_after();
   grid_launch_dependents();
-  const uint32_t tmem = tmem_base;
-  const long long total = ft.base[p.B];
+  const uint32_t tmem = sh.tmem_base;
+  const long long total = sh.base[p.B];
   const int N = flat_ctas(total, p.N);
   const bool works = (int)blockIdx.x < N;
   const long long x0 = works ? flat_first(total, blockIdx.x, N) : 0, x1 = works ? flat_first(total, blockIdx.x + 1, N) : 0;
@@ -601,195 +654,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
     abort_flag = 1;
   };
   int loaded = 0;  // ring entries filled (warp 8) or used (warp 9)
-  FlatRun r;
+  SlimRun r;
 
-  if (warp == 8) {
-    bool ok = true;
-    for (long long x = x0; ok && flat_run(ft, p.B, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
-      const int b = r.b, g = r.unit % p.Hkv, n = ft.n[b], nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
-      const int box = p.P * 128, lanes = 256 / p.P;  // bytes of a box; boxes of a whole tile
-      // this lane's page id of a cache tile, -1: none; loaded two tiles ahead and judged only
-      // when it is used, so that the load's latency stays off the ring
-      auto page_of = [&](int tile) {
-        const int pg = tile * (kAtKeys >> p.pshift) + (lane >> 1);
-        return tile < nc && lane < lanes && pg * p.P < n ? p.page_table[(size_t)b * p.max_pages + pg] : -1;
-      };
-      auto issue = [&](int tile, int phys, bool v) {
-        const int e = loaded % E;
-        const int pg = tile * (kAtKeys >> p.pshift) + (lane >> 1);
-        if (phys < 0 || phys >= p.num_phys) {
-          if (tile < nc && lane < lanes && pg * p.P < n) flag_error(p.err, RKV_DEVERR_PAGE_ID);
-          phys = -1;
-        }
-        const bool late = loaded >= E && !mbar_wait_role(&empty_b[e], (uint32_t)((loaded / E - 1) & 1), &abort_flag);
-        if (__any_sync(0xffffffffu, late)) {
-          give_up();
-          return false;
-        }
-        uint8_t* st = ring + e * kAtEntry;
-        if (tile < nc) {
-          const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0);
-          const uint32_t bytes = __popc(have) * box;
-          if (lane == 0) {
-            if (!v) {  // even lanes carry the pages; a page is P / 16 groups
-              uint32_t gr = 0;
-              for (int l = 0; l < lanes; l += 2)
-                if ((have >> l) & 1u) gr |= ((1u << (p.P >> 4)) - 1u) << ((l >> 1) * (p.P >> 4));
-              groups[e] = gr;
-            }
-            if (bytes) mbar_arrive_expect_tx(&full_b[e], bytes);
-            else mbar_arrive(&full_b[e]);
-          }
-          __syncwarp();
-          if (phys >= 0)
-            tma_load_2d(st + (lane & 1) * (kAtEntry / 2) + (lane >> 1) * box, v ? &p.tmv : &p.tmk, (lane & 1) * 64,
-                        (phys * p.Hkv + g) * p.P, &full_b[e]);
-        } else if (lane == 0) {
-          const int row = (b * p.Hkv + g) * p.T + (tile - nc) * kAtKeys;
-          groups[e] = 0xffu;
-          mbar_arrive_expect_tx(&full_b[e], kAtEntry);
-          tma_load_2d(st, v ? &p.tmvt : &p.tmkt, 0, row, &full_b[e]);
-          tma_load_2d(st + kAtEntry / 2, v ? &p.tmvt : &p.tmkt, 64, row, &full_b[e]);
-        }
-        ++loaded;
-        return true;
-      };
-      int cur = page_of(r.lo), next = nt > 1 ? page_of(r.lo + 1) : -1;
-      ok = issue(r.lo, cur, false);
-      for (int i = 0; ok && i < nt; ++i) {
-        const int after = i + 2 < nt ? page_of(r.lo + i + 2) : -1;
-        if (!kWide && i + 1 < nt) ok = issue(r.lo + i + 1, next, false);
-        ok = ok && issue(r.lo + i, cur, true);
-        if (kWide && i + 1 < nt) ok = ok && issue(r.lo + i + 1, next, false);
-        cur = next;
-        next = after;
-      }
-    }
-  } else if (warp == 9) {
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128), idesc_o = idesc_s | kIdescBNMajor;
-    const uint32_t q32 = smem_u32(qs), ring32 = smem_u32(ring);
-    int seen_p[2] = {0, 0}, runs[2] = {0, 0};
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, int phase) {
-      const bool late = !mbar_wait_role(bar, (uint32_t)(phase & 1), &abort_flag);
-      if (__any_sync(0xffffffffu, late)) {
-        give_up();
-        return false;
-      }
-      return true;
-    };
-    const bool lead = elect_lane();
-    const uint32_t qlo = sw128_kmajor_lo(q32), klo = sw128_kmajor_lo(ring32), vlo = sw128_nmajor_lo(ring32, kAtEntry / 2);
-    // S of `slot` from the K entry e (its copy has landed)
-    auto mma_s = [&](int slot, int e, bool release) {
-      tc_fence_after();
-      if (lead) sgroups[slot] = groups[e];
-      const uint32_t d = tmem + slot * 256, qa = qlo + (kWide ? slot * (128 * 256 >> 4) : 0), ka = klo + e * (kAtEntry >> 4);
-      tc_mma_ss<false>(lead, d, qa, ka, idesc_s);
-#pragma unroll
-      for (int k = 1; k < 8; ++k) {
-        const uint32_t off = ((k >> 2) * (kAtEntry / 2) + (k & 3) * 32) >> 4;
-        tc_mma_ss<true>(lead, d, qa + off, ka + off, idesc_s);
-      }
-      tc_commit_if(lead && release, &empty_b[e]);
-      tc_commit_if(lead, &s_b[slot]);
-      if (lead) mbar_arrive(&s_b[slot]);
-      __syncwarp();
-    };
-    auto mma_o = [&](int slot, int e, bool first, bool last, bool release) {
-      tc_fence_after();
-      const uint32_t d = tmem + slot * 256 + 128, pa = tmem + slot * 256, va = vlo + e * (kAtEntry >> 4);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        tc_mma_ts(lead, d, pa + k * 8, va + (k * 2048 >> 4), idesc_o, (first && k == 0) ? 0u : 1u);
-      tc_commit_if(lead && release, &empty_b[e]);
-      tc_commit_if(lead && last, &o_b[slot]);
-    };
-    for (long long x = x0; ok && flat_run(ft, p.B, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
-      const int b = r.b, n = ft.n[b], nodes = ft.t[b], nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
-      const bool two = kWide && nodes * p.G - (r.unit / p.Hkv) * R > 128;  // slot 1 has rows
-      // keys of a tile that may hold anything (behind the end, on a bad page) have weight 0,
-      // and 0 x NaN is not 0: their V rows are cleared first
-      auto clean_v = [&](int tile, int e, uint32_t gr) {
-        const int left = tile < nc ? n - tile * kAtKeys : nodes - (tile - nc) * kAtKeys;
-        if (left >= kAtKeys && gr == 0xffu) return;
-        for (int i = lane; i < 128 * 16; i += 32) {
-          const int row = i >> 4;
-          if (row < left && ((gr >> (row >> 4)) & 1u)) continue;
-          *reinterpret_cast<uint4*>(ring + e * kAtEntry + ((i >> 3) & 1) * (kAtEntry / 2) + row * 128 + (i & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      };
-      auto take = [&]() {  // the next ring entry, landed
-        const int e = loaded % E;
-        ok = wait(&full_b[e], loaded / E);
-        ++loaded;
-        return e;
-      };
-      ok = wait(&q_b[0], runs[0]++);
-      if (kWide && ok) ok = wait(&q_b[1], runs[1]++);
-      if (!ok) break;
-      if (kWide) {
-        int ek = take();
-        if (!ok) break;
-        uint32_t gr = groups[ek];
-        mma_s(0, ek, !two);
-        if (two) mma_s(1, ek, true);
-        for (int i = 0; i < nt; ++i) {
-          const int ev = take();
-          if (!ok) break;
-          clean_v(r.lo + i, ev, gr);
-          const bool last = i + 1 == nt;
-          if (!(ok = wait(&p_b[0], seen_p[0]++))) break;
-          mma_o(0, ev, i == 0, last, !two);
-          if (kWide) tc_commit_if(lead && last && !two, &o_b[1]);  // keeps an idle slot in step
-          int en = 0;
-          if (!last) {
-            en = take();
-            if (!ok) break;
-            gr = groups[en];
-            mma_s(0, en, !two);
-          }
-          if (two) {
-            if (!(ok = wait(&p_b[1], seen_p[1]++))) break;
-            mma_o(1, ev, i == 0, last, true);
-            if (!last) mma_s(1, en, true);
-          }
-        }
-      } else {
-        uint32_t gr[2];
-        const int e0 = take();
-        if (!ok) break;
-        gr[0] = groups[e0];
-        mma_s(0, e0, true);
-        for (int i = 0; i < nt; ++i) {
-          // order of the entries: K_0, then K_(i+1) and V_i for every i
-          const int slot = i & 1;
-          int en = 0;
-          uint32_t gn = 0;
-          if (i + 1 < nt) {
-            en = take();
-            if (!ok) break;
-            gn = groups[en];
-            if (i == 0) mma_s(1, en, true);
-          }
-          // tile i + 1's logits go where tile i - 1's weights lay: its product was issued before
-          if (i + 1 < nt && i > 0) mma_s(slot ^ 1, en, true);
-          const int ev = take();
-          if (!ok) break;
-          clean_v(r.lo + i, ev, gr[slot]);
-          if (i + 1 < nt) gr[slot ^ 1] = gn;
-          if (!(ok = wait(&p_b[slot], seen_p[slot]++))) break;
-          mma_o(slot, ev, i < 2, i + 2 >= nt, true);
-        }
-      }
-    }
-    // the last entries' releases land before the CTA may exit
-    if (ok)
-      for (int i = loaded > E ? loaded - E : 0; i < loaded; ++i) mbar_wait(&empty_b[i % E], (uint32_t)((i / E) & 1));
-  } else {
+  if (warp < 8) {
+    setmaxnreg_inc<kAtSoftRegs>();
     const int slot = warp >> 2, row = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), mine = lanes + slot * 256;
     const float sl = p.scale_log2;
@@ -803,11 +671,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
       }
       return true;
     };
-    for (long long x = x0; ok && flat_run(ft, p.B, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+    for (long long x = x0; ok && slim_run<R, kAtKeys>(p, sh.base, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
       const int b = r.b, g = r.unit % p.Hkv, rt = r.unit / p.Hkv;
-      const int n = ft.n[b], nodes = ft.t[b], rows = nodes * p.G, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
+      const int n = r.n, nodes = r.t, rows = nodes * p.G, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
       const bool idle = kWide && slot == 1 && rows - rt * R <= 128;
-      // the query rows, swizzled as TMA would store them (eight rows of 16 pieces at a time)
+      // the query rows, swizzled as TMA would store them, over the last run's staged outputs
+      if (run > 0 && !(ok = wait(&sh.out[kWide ? slot : 0], run - 1))) break;
       {
         constexpr int kPer = kWide ? 128 : 64;  // rows this slot's warps load
         const int q0 = kWide ? 0 : slot * 64;
@@ -921,12 +790,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
       if (kWide) {
         if (!(ok = wait(&o_b[slot], done[slot]++))) break;
       } else {
-        ml_s[slot][row] = make_float2(m, l);
-        mbar_arrive(&ml_b);
-        if (!(ok = wait(&ml_b, run))) break;
+        sh.ml_s[slot][row] = make_float2(m, l);
+        mbar_arrive(ml_b);
+        if (!(ok = wait(ml_b, run))) break;
         if (!(ok = wait(&o_b[0], done[0]++))) break;
         if (has[1] && !(ok = wait(&o_b[1], done[1]++))) break;
-        const float2 a = ml_s[0][row], c = has[1] ? ml_s[1][row] : make_float2(kNoMax, 0.f);
+        const float2 a = sh.ml_s[0][row], c = has[1] ? sh.ml_s[1][row] : make_float2(kNoMax, 0.f);
         m = fmaxf(a.x, c.x);
         f0 = ex2_approx(a.x - m);
         f1 = ex2_approx(c.x - m);
@@ -939,8 +808,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
         const float inv = r.whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
         const size_t orow = live ? out_row(p, b, g, my) : 0;
         const size_t prow = (2 * (size_t)blockIdx.x + (r.first ? 0 : 1)) * R + (kWide ? slot * 128 : 0) + row;
-        // kWide: all 128 channels of this slot's row; else 64 channels of both slots' O
+        // kWide: all 128 channels of this slot's row; else 64 channels of both slots' O.  32
+        // channels of the warp's 32 rows at a time go through the query tile's memory (its
+        // products are done), so that the stores are whole 128-byte (bf16: 64-byte) pieces
+        // of rows and not 16 bytes of 32 rows each.
         constexpr int kChunks = kWide ? 4 : 2;
+        uint8_t* const stage = qs + slot * (kWide ? 32768 : 16384) + (warp & 3) * 4096;
+        const int row0 = rt * R + (kWide ? slot * 128 : 0) + (warp & 3) * 32;  // the warp's first query row
+        const size_t prow0 = prow - lane;
 #pragma unroll 1
         for (int cc = 0; cc < kChunks; ++cc) {
           const int c = kWide ? cc : slot * 2 + cc;
@@ -957,7 +832,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
                 o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j])));
             }
           }
-          if (!live) continue;
+          __syncwarp();  // the staged piece before this one is read
           if (r.whole) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -965,13 +840,28 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 w[e] = pack_bf16x2(__uint_as_float(o[j * 8 + 2 * e]) * inv, __uint_as_float(o[j * 8 + 2 * e + 1]) * inv);
-              reinterpret_cast<uint4*>(p.out + orow * 128 + c * 32)[j] = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int i = k * 8 + (lane >> 2), j = lane & 3;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + i * 64 + ((j ^ ((i >> 1) & 3)) << 4));
+              if (row0 + i < rows)
+                reinterpret_cast<uint4*>(p.out + out_row(p, b, g, row0 + i) * 128 + c * 32)[j] = v;
             }
           } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              reinterpret_cast<uint4*>(p.part_o + prow * 128 + c * 32)[j] =
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
                   make_uint4(o[j * 4], o[j * 4 + 1], o[j * 4 + 2], o[j * 4 + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int i = k * 4 + (lane >> 3), j = lane & 7;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + i * 128 + ((j ^ (i & 7)) << 4));
+              if (row0 + i < rows) reinterpret_cast<uint4*>(p.part_o + (prow0 + i) * 128 + c * 32)[j] = v;
+            }
           }
         }
         if (live && (kWide || slot == 0)) {
@@ -980,7 +870,197 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
         }
         tc_fence_before();  // O is read before the next run's queries let its products start
       }
+      mbar_arrive(&sh.out[kWide ? slot : 0]);  // this thread has read what it staged
     }
+  } else {
+    setmaxnreg_dec<kAtIssueRegs>();
+    if (warp == 8) {
+    bool ok = true;
+    for (long long x = x0; ok && slim_run<R, kAtKeys>(p, sh.base, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+      const int b = r.b, g = r.unit % p.Hkv, n = r.n, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
+      const int box = p.P * 128, lanes = 256 / p.P;  // bytes of a box; boxes of a whole tile
+      // this lane's page id of a cache tile, -1: none; loaded two tiles ahead and judged only
+      // when it is used, so that the load's latency stays off the ring
+      auto page_of = [&](int tile) {
+        const int pg = tile * (kAtKeys >> p.pshift) + (lane >> 1);
+        return tile < nc && lane < lanes && pg * p.P < n ? p.page_table[(size_t)b * p.max_pages + pg] : -1;
+      };
+      auto issue = [&](int tile, int phys, bool v) {
+        const int e = loaded % E;
+        const int pg = tile * (kAtKeys >> p.pshift) + (lane >> 1);
+        if (phys < 0 || phys >= p.num_phys) {
+          if (tile < nc && lane < lanes && pg * p.P < n) flag_error(p.err, RKV_DEVERR_PAGE_ID);
+          phys = -1;
+        }
+        const bool late = loaded >= E && !mbar_wait_role(&empty_b[e], (uint32_t)((loaded / E - 1) & 1), &abort_flag);
+        if (__any_sync(0xffffffffu, late)) {
+          give_up();
+          return false;
+        }
+        uint8_t* st = ring + e * kAtEntry;
+        if (tile < nc) {
+          const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0);
+          const uint32_t bytes = __popc(have) * box;
+          if (lane == 0) {
+            if (!v) {  // even lanes carry the pages; a page is P / 16 groups
+              uint32_t gr = 0;
+              for (int l = 0; l < lanes; l += 2)
+                if ((have >> l) & 1u) gr |= ((1u << (p.P >> 4)) - 1u) << ((l >> 1) * (p.P >> 4));
+              groups[e] = gr;
+            }
+            if (bytes) mbar_arrive_expect_tx(&full_b[e], bytes);
+            else mbar_arrive(&full_b[e]);
+          }
+          __syncwarp();
+          if (phys >= 0)
+            tma_load_2d(st + (lane & 1) * (kAtEntry / 2) + (lane >> 1) * box, v ? &p.tmv : &p.tmk, (lane & 1) * 64,
+                        (phys * p.Hkv + g) * p.P, &full_b[e]);
+        } else if (lane == 0) {
+          const int row = (b * p.Hkv + g) * p.T + (tile - nc) * kAtKeys;
+          groups[e] = 0xffu;
+          mbar_arrive_expect_tx(&full_b[e], kAtEntry);
+          tma_load_2d(st, v ? &p.tmvt : &p.tmkt, 0, row, &full_b[e]);
+          tma_load_2d(st + kAtEntry / 2, v ? &p.tmvt : &p.tmkt, 64, row, &full_b[e]);
+        }
+        ++loaded;
+        return true;
+      };
+      int cur = page_of(r.lo), next = nt > 1 ? page_of(r.lo + 1) : -1;
+      ok = issue(r.lo, cur, false);
+      for (int i = 0; ok && i < nt; ++i) {
+        const int after = i + 2 < nt ? page_of(r.lo + i + 2) : -1;
+        if (!kWide && i + 1 < nt) ok = issue(r.lo + i + 1, next, false);
+        ok = ok && issue(r.lo + i, cur, true);
+        if (kWide && i + 1 < nt) ok = ok && issue(r.lo + i + 1, next, false);
+        cur = next;
+        next = after;
+      }
+    }
+  } else if (warp == 9) {
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128), idesc_o = idesc_s | kIdescBNMajor;
+    const uint32_t q32 = smem_u32(qs), ring32 = smem_u32(ring);
+    int seen_p[2] = {0, 0}, runs[2] = {0, 0};
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int phase) {
+      const bool late = !mbar_wait_role(bar, (uint32_t)(phase & 1), &abort_flag);
+      if (__any_sync(0xffffffffu, late)) {
+        give_up();
+        return false;
+      }
+      return true;
+    };
+    const bool lead = elect_lane();
+    const uint32_t qlo = sw128_kmajor_lo(q32), klo = sw128_kmajor_lo(ring32), vlo = sw128_nmajor_lo(ring32, kAtEntry / 2);
+    // S of `slot` from the K entry e (its copy has landed)
+    auto mma_s = [&](int slot, int e, bool release) {
+      tc_fence_after();
+      if (lead) sgroups[slot] = groups[e];
+      const uint32_t d = tmem + slot * 256, qa = qlo + (kWide ? slot * (128 * 256 >> 4) : 0), ka = klo + e * (kAtEntry >> 4);
+      tc_mma_ss<false>(lead, d, qa, ka, idesc_s);
+#pragma unroll
+      for (int k = 1; k < 8; ++k) {
+        const uint32_t off = ((k >> 2) * (kAtEntry / 2) + (k & 3) * 32) >> 4;
+        tc_mma_ss<true>(lead, d, qa + off, ka + off, idesc_s);
+      }
+      tc_commit_if(lead && release, &empty_b[e]);
+      tc_commit_if(lead, &s_b[slot]);
+      if (lead) mbar_arrive(&s_b[slot]);
+      __syncwarp();
+    };
+    auto mma_o = [&](int slot, int e, bool first, bool last, bool release) {
+      tc_fence_after();
+      const uint32_t d = tmem + slot * 256 + 128, pa = tmem + slot * 256, va = vlo + e * (kAtEntry >> 4);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        tc_mma_ts(lead, d, pa + k * 8, va + (k * 2048 >> 4), idesc_o, (first && k == 0) ? 0u : 1u);
+      tc_commit_if(lead && release, &empty_b[e]);
+      tc_commit_if(lead && last, &o_b[slot]);
+    };
+    for (long long x = x0; ok && slim_run<R, kAtKeys>(p, sh.base, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+      const int n = r.n, nodes = r.t, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
+      const bool two = kWide && nodes * p.G - (r.unit / p.Hkv) * R > 128;  // slot 1 has rows
+      // keys of a tile that may hold anything (behind the end, on a bad page) have weight 0,
+      // and 0 x NaN is not 0: their V rows are cleared first
+      auto clean_v = [&](int tile, int e, uint32_t gr) {
+        const int left = tile < nc ? n - tile * kAtKeys : nodes - (tile - nc) * kAtKeys;
+        if (left >= kAtKeys && gr == 0xffu) return;
+        for (int i = lane; i < 128 * 16; i += 32) {
+          const int row = i >> 4;
+          if (row < left && ((gr >> (row >> 4)) & 1u)) continue;
+          *reinterpret_cast<uint4*>(ring + e * kAtEntry + ((i >> 3) & 1) * (kAtEntry / 2) + row * 128 + (i & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
+      auto take = [&]() {  // the next ring entry, landed
+        const int e = loaded % E;
+        ok = wait(&full_b[e], loaded / E);
+        ++loaded;
+        return e;
+      };
+      ok = wait(&q_b[0], runs[0]++);
+      if (kWide && ok) ok = wait(&q_b[1], runs[1]++);
+      if (!ok) break;
+      if (kWide) {
+        int ek = take();
+        if (!ok) break;
+        uint32_t gr = groups[ek];
+        mma_s(0, ek, !two);
+        if (two) mma_s(1, ek, true);
+        for (int i = 0; i < nt; ++i) {
+          const int ev = take();
+          if (!ok) break;
+          clean_v(r.lo + i, ev, gr);
+          const bool last = i + 1 == nt;
+          if (!(ok = wait(&p_b[0], seen_p[0]++))) break;
+          mma_o(0, ev, i == 0, last, !two);
+          if (kWide) tc_commit_if(lead && last && !two, &o_b[1]);  // keeps an idle slot in step
+          int en = 0;
+          if (!last) {
+            en = take();
+            if (!ok) break;
+            gr = groups[en];
+            mma_s(0, en, !two);
+          }
+          if (two) {
+            if (!(ok = wait(&p_b[1], seen_p[1]++))) break;
+            mma_o(1, ev, i == 0, last, true);
+            if (!last) mma_s(1, en, true);
+          }
+        }
+      } else {
+        uint32_t gr[2];
+        const int e0 = take();
+        if (!ok) break;
+        gr[0] = groups[e0];
+        mma_s(0, e0, true);
+        for (int i = 0; i < nt; ++i) {
+          // order of the entries: K_0, then K_(i+1) and V_i for every i
+          const int slot = i & 1;
+          int en = 0;
+          uint32_t gn = 0;
+          if (i + 1 < nt) {
+            en = take();
+            if (!ok) break;
+            gn = groups[en];
+            if (i == 0) mma_s(1, en, true);
+          }
+          // tile i + 1's logits go where tile i - 1's weights lay: its product was issued before
+          if (i + 1 < nt && i > 0) mma_s(slot ^ 1, en, true);
+          const int ev = take();
+          if (!ok) break;
+          clean_v(r.lo + i, ev, gr[slot]);
+          if (i + 1 < nt) gr[slot ^ 1] = gn;
+          if (!(ok = wait(&p_b[slot], seen_p[slot]++))) break;
+          mma_o(slot, ev, i < 2, i + 2 >= nt, true);
+        }
+      }
+    }
+    // the last entries' releases land before the CTA may exit
+    if (ok)
+      for (int i = loaded > E ? loaded - E : 0; i < loaded; ++i) mbar_wait(&empty_b[i % E], (uint32_t)((i / E) & 1));
+  }
   }
 
   // teardown: after a timeout, wait (bounded) for the copies and products still in flight
