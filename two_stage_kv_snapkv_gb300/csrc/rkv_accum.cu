@@ -403,12 +403,13 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
   bool ok = true;
 
   if (warp == 16) {
+    const bool lead = elect_lane();
     for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
       const int n = tt.n[r.b], s = units % KS;
-      // the unit's keys: one box of a page a lane
-      const int pg = r.j * (kAmKeys >> p.pshift) + (lane >> 1);
+      // the unit's keys, a page a lane
+      const int pages = kAmKeys >> p.pshift, pg = r.j * pages + lane;
       int phys = -1;
-      if (lane < 2 * (kAmKeys >> p.pshift) && pg * p.P < n) {
+      if (lane < pages && pg * p.P < n) {
         phys = p.page_table[(size_t)r.b * p.max_pages + pg];
         if (phys < 0 || phys >= p.num_phys) {
           flag_error(p.err, RKV_DEVERR_PAGE_ID);
@@ -416,29 +417,30 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
         }
       }
       if (units >= KS && !(ok = wait(&kempty[s], units / KS - 1))) break;
-      const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0);
-      if (lane == 0) {
-        if (have) mbar_arrive_expect_tx(&kfull[s], __popc(have) * p.P * 128);
+      const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0), bar = smem_u32(&kfull[s]);
+      if (lead) {
+        if (have) mbar_arrive_expect_tx(&kfull[s], __popc(have) * p.P * 256);
         else mbar_arrive(&kfull[s]);
       }
       __syncwarp();
-      if (phys >= 0) {
-        const int row = (lane >> 1) * p.P;  // of the unit's 256
-        tma_load_2d(ks + s * 65536 + (row >> 7) * 32768 + (lane & 1) * 16384 + (row & 127) * 128, &p.tmk, (lane & 1) * 64,
-                    (phys * p.Hkv + r.g) * p.P, &kfull[s]);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int ph = __shfl_sync(0xffffffffu, phys, j), row = j * p.P;  // of the unit's 256
+        const bool go = lead && ((have >> j) & 1u);
+        const uint32_t to = smem_u32(ks) + s * 65536 + (row >> 7) * 32768 + (row & 127) * 128;
+        tma_load_2d_if(go, to, &p.tmk, 0, (ph * p.Hkv + r.g) * p.P, bar);
+        tma_load_2d_if(go, to + 16384, &p.tmk, 64, (ph * p.Hkv + r.g) * p.P, bar);
       }
       ++units;
       int h = r.lo / r.width, rt = r.f + r.lo - h * r.width;
       for (int o = r.lo; o < r.hi; ++o) {
         const int t = tiles % kAmQ;
         if (tiles >= kAmQ && !(ok = wait(&qempty[t], tiles / kAmQ - 1))) break;
-        if (lane == 0) {
-          const int row = (r.b * p.Hq + r.g * p.G + h) * p.T + rt * nq;
-          mbar_arrive_expect_tx(&qfull[t], nq * 256);
-          tma_load_2d(qs + t * QB, &p.tmq, 0, row, &qfull[t]);
-          tma_load_2d(qs + t * QB + QB / 2, &p.tmq, 64, row, &qfull[t]);
-        }
+        const int row = (r.b * p.Hq + r.g * p.G + h) * p.T + rt * nq;
+        if (lead) mbar_arrive_expect_tx(&qfull[t], nq * 256);
         __syncwarp();
+        tma_load_2d_if(lead, smem_u32(qs) + t * QB, &p.tmq, 0, row, smem_u32(&qfull[t]));
+        tma_load_2d_if(lead, smem_u32(qs) + t * QB + QB / 2, &p.tmq, 64, row, smem_u32(&qfull[t]));
         ++tiles;
         if (++rt == r.f + r.width) {
           rt = r.f;

@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(256) attend_weigh_kernel(const __grid_constant
 // channels x 256 rows x 4 = 16.8 MFLOP: at the card's rates the bytes take 1.4 us of an
 // SM's share and the products 1.1 us, so the wide form sits near both roofs and the narrow
 // one on the bytes alone.
-//   warps 0-3, 4-7: softmax of slot 0, 1;  warp 8: TMA;  warp 9: MMA issue;  10, 11: idle.
+//   warps 0-3, 4-7: softmax of slot 0, 1;  warps 8, 10: TMA of K, V;  warp 9: MMA issue;  11: idle.
 // The running maximum that the weights refer to moves only when a row's new maximum is
 // above it by more than 8 (base 2): weights then stay below 2^8 and O is rescaled, a TMEM
 // round trip of 64 KB, a few times a run instead of every tile.
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(256) attend_weigh_kernel(const __grid_constant
 constexpr int kAtKeys = 128;
 constexpr int kAtThreads = 384;
 // Registers: 384 threads start with 168 each; the softmax warps take 208 and the third
-// warpgroup (TMA, MMA, two idle warps) keeps 88: 256 x 208 + 128 x 88 = 384 x 168.
+// warpgroup (TMA, MMA, an idle warp) keeps 88: 256 x 208 + 128 x 88 = 384 x 168.
 constexpr int kAtSoftRegs = 208, kAtIssueRegs = 88;
 static_assert(256 * kAtSoftRegs + 128 * kAtIssueRegs == 384 * 168, "the split must be what the block was launched with");
 constexpr int kAtEntry = 128 * 256;
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
     flag_error(p.err, RKV_DEVERR_TIMEOUT);
     abort_flag = 1;
   };
-  int loaded = 0;  // ring entries filled (warp 8) or used (warp 9)
+  int loaded = 0;  // one past the last ring entry filled (warps 8, 10) or used (warp 9)
   SlimRun r;
 
   if (warp < 8) {
@@ -874,67 +874,77 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
     }
   } else {
     setmaxnreg_dec<kAtIssueRegs>();
-    if (warp == 8) {
+    if (warp == 8 || warp == 10) {
+    // warp 8 fetches K, warp 10 V; entry of K_i / V_i among a run's 2 nt entries:
+    // wide K_i 2 i, V_i 2 i + 1; narrow K_0, then K_(i+1) and V_i for every i
+    const bool v = warp == 10;
+    const CUtensorMap* map = v ? &p.tmv : &p.tmk;
+    const CUtensorMap* tmap = v ? &p.tmvt : &p.tmkt;
+    const bool lead = elect_lane();
+    const uint32_t ring32 = smem_u32(ring);
+    const int pages = kAtKeys >> p.pshift, box = p.P * 128;  // pages of a tile, bytes of a box
+    int before = 0;                                          // entries of the runs before
     bool ok = true;
     for (long long x = x0; ok && slim_run<R, kAtKeys>(p, sh.base, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
       const int b = r.b, g = r.unit % p.Hkv, n = r.n, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
-      const int box = p.P * 128, lanes = 256 / p.P;  // bytes of a box; boxes of a whole tile
-      // this lane's page id of a cache tile, -1: none; loaded two tiles ahead and judged only
+      // lane j: page id of the tile's page j, -1: none; loaded a tile ahead and judged only
       // when it is used, so that the load's latency stays off the ring
       auto page_of = [&](int tile) {
-        const int pg = tile * (kAtKeys >> p.pshift) + (lane >> 1);
-        return tile < nc && lane < lanes && pg * p.P < n ? p.page_table[(size_t)b * p.max_pages + pg] : -1;
+        const int pg = tile * pages + lane;
+        return tile < nc && lane < pages && pg * p.P < n ? p.page_table[(size_t)b * p.max_pages + pg] : -1;
       };
-      auto issue = [&](int tile, int phys, bool v) {
-        const int e = loaded % E;
-        const int pg = tile * (kAtKeys >> p.pshift) + (lane >> 1);
-        if (phys < 0 || phys >= p.num_phys) {
-          if (tile < nc && lane < lanes && pg * p.P < n) flag_error(p.err, RKV_DEVERR_PAGE_ID);
-          phys = -1;
-        }
-        const bool late = loaded >= E && !mbar_wait_role(&empty_b[e], (uint32_t)((loaded / E - 1) & 1), &abort_flag);
+      int next = page_of(r.lo);
+      for (int i = 0; i < nt; ++i) {
+        const int tile = r.lo + i;
+        int phys = next;
+        next = i + 1 < nt ? page_of(tile + 1) : -1;
+        const int at = before + (kWide ? 2 * i + v : (v ? (i + 1 < nt ? 2 * i + 2 : 2 * nt - 1) : (i > 0 ? 2 * i - 1 : 0)));
+        const int e = at % E;
+        const bool late = at >= E && !mbar_wait_role(&empty_b[e], (uint32_t)((at / E - 1) & 1), &abort_flag);
         if (__any_sync(0xffffffffu, late)) {
           give_up();
-          return false;
+          ok = false;
+          break;
         }
-        uint8_t* st = ring + e * kAtEntry;
+        const uint32_t st = ring32 + e * kAtEntry, bar = smem_u32(&full_b[e]);
         if (tile < nc) {
+          if (phys < 0 || phys >= p.num_phys) {
+            if (lane < pages && (tile * pages + lane) * p.P < n) flag_error(p.err, RKV_DEVERR_PAGE_ID);
+            phys = -1;
+          }
           const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0);
-          const uint32_t bytes = __popc(have) * box;
-          if (lane == 0) {
-            if (!v) {  // even lanes carry the pages; a page is P / 16 groups
-              uint32_t gr = 0;
-              for (int l = 0; l < lanes; l += 2)
-                if ((have >> l) & 1u) gr |= ((1u << (p.P >> 4)) - 1u) << ((l >> 1) * (p.P >> 4));
+          if (lead) {
+            if (!v) {
+              uint32_t gr = 0;  // a page is P / 16 groups
+              for (int j = 0; j < pages; ++j)
+                if ((have >> j) & 1u) gr |= ((1u << (p.P >> 4)) - 1u) << (j * (p.P >> 4));
               groups[e] = gr;
             }
-            if (bytes) mbar_arrive_expect_tx(&full_b[e], bytes);
+            if (have) mbar_arrive_expect_tx(&full_b[e], __popc(have) * 2 * box);
             else mbar_arrive(&full_b[e]);
           }
           __syncwarp();
-          if (phys >= 0)
-            tma_load_2d(st + (lane & 1) * (kAtEntry / 2) + (lane >> 1) * box, v ? &p.tmv : &p.tmk, (lane & 1) * 64,
-                        (phys * p.Hkv + g) * p.P, &full_b[e]);
-        } else if (lane == 0) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int ph = __shfl_sync(0xffffffffu, phys, j);
+            const bool go = lead && j < pages && ((have >> j) & 1u);
+            const int row = (ph * p.Hkv + g) * p.P;
+            tma_load_2d_if(go, st + j * box, map, 0, row, bar);
+            tma_load_2d_if(go, st + kAtEntry / 2 + j * box, map, 64, row, bar);
+          }
+        } else {
           const int row = (b * p.Hkv + g) * p.T + (tile - nc) * kAtKeys;
-          groups[e] = 0xffu;
-          mbar_arrive_expect_tx(&full_b[e], kAtEntry);
-          tma_load_2d(st, v ? &p.tmvt : &p.tmkt, 0, row, &full_b[e]);
-          tma_load_2d(st + kAtEntry / 2, v ? &p.tmvt : &p.tmkt, 64, row, &full_b[e]);
+          if (lead) {
+            if (!v) groups[e] = 0xffu;
+            mbar_arrive_expect_tx(&full_b[e], kAtEntry);
+          }
+          __syncwarp();
+          tma_load_2d_if(lead, st, tmap, 0, row, bar);
+          tma_load_2d_if(lead, st + kAtEntry / 2, tmap, 64, row, bar);
         }
-        ++loaded;
-        return true;
-      };
-      int cur = page_of(r.lo), next = nt > 1 ? page_of(r.lo + 1) : -1;
-      ok = issue(r.lo, cur, false);
-      for (int i = 0; ok && i < nt; ++i) {
-        const int after = i + 2 < nt ? page_of(r.lo + i + 2) : -1;
-        if (!kWide && i + 1 < nt) ok = issue(r.lo + i + 1, next, false);
-        ok = ok && issue(r.lo + i, cur, true);
-        if (kWide && i + 1 < nt) ok = ok && issue(r.lo + i + 1, next, false);
-        cur = next;
-        next = after;
+        loaded = at + 1;
       }
+      before += 2 * nt;
     }
   } else if (warp == 9) {
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128), idesc_o = idesc_s | kIdescBNMajor;
@@ -1067,7 +1077,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
   tc_fence_before();
   __syncthreads();
   if (abort_flag) {
-    if (warp == 8 && lane == 0)
+    if ((warp == 8 || warp == 10) && lane == 0)
       for (int i = loaded > E ? loaded - E : 0; i < loaded; ++i) mbar_wait(&full_b[i % E], (uint32_t)((i / E) & 1));
     if (warp == 9 && lane == 0) {  // everything issued before this commit has completed when it arrives
       tc_commit(&o_b[0]);
