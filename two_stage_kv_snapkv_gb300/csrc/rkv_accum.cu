@@ -38,7 +38,7 @@ struct RowsParams {
   float* acc;
   float* part;         // accum_tiles: [2 N][256] sums of the units' parts
   int B, Hq, Hkv, G, gshift, T, ids_stride, P, pshift, max_pages, num_phys, acc_stride, N, nq;
-  float scale_log2;
+  float scale, scale_log2;
 };
 
 // Rows of sequence b that are taken (0 when the count or the length is not usable).
@@ -254,15 +254,21 @@ __global__ void __launch_bounds__(kRwThreads, 1) accum_rows_kernel(const __grid_
 // see it, and all units' pieces form one line that is split evenly over the SMs: the
 // causal triangle needs no balancing of its own.  A unit split between CTAs leaves its
 // parts in the workspace and accum_join adds them in order.
-// Per piece 2 x 128 x nq x 128 multiply-adds and 256 nq exponentials; at nq = 128 the
-// products take 1024 clocks of an SM and the exponentials as many at 32 a clock: two
+// The log-sum-exps come off inside the product: a 17th group of 16 channels holds 1, 1, 1
+// for every key and, for row i, -lse_i / scale as three bf16 terms (24 bits), so the
+// accumulator is (z - lse) / scale and the sum a product, an exponential and an addition
+// per cell.  (Read from shared memory instead, 16 loads a warp and tile, the sums took
+// twice as long while the products, which use all of its bandwidth, ran.)
+// Per piece 2 x 128 x nq x 144 multiply-adds and 256 nq exponentials; at nq = 128 the
+// products take 1152 clocks of an SM and the exponentials 1024 at 32 a clock: two
 // accumulators a key tile keep both busy.
 //   warps 0-15: sums (warps 4 w .. 4 w + 3: key tile w / 2, column half w % 2);
-//   warp 16: TMA;  warp 17: MMA issue;  warp 18: the rows' log-sum-exps.
+//   warp 16: TMA;  warp 17: MMA issue;  warps 18, 19: the rows' log-sum-exps.
 constexpr int kAmKeys = 256;
-constexpr int kAmThreads = 19 * 32;
-constexpr int kAmQ = 4;  // query tiles in the ring
-constexpr int kAmSmem = 1024 + 6 * 32768;
+constexpr int kAmThreads = 640;
+constexpr int kAmQ = 4;           // query tiles in the ring
+constexpr int kAmExtra = 128 * 32;  // 128 rows x 16 channels of the extra product
+constexpr int kAmSmem = 1024 + 6 * 32768 + (1 + kAmQ) * kAmExtra;
 
 struct TilesTable {
   long long base[RKV_MAX_BATCH + 1];
@@ -349,14 +355,22 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
   static_assert(KS * 65536 + kAmQ * QB == 6 * 32768, "the rings fill the shared memory");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ TilesTable tt;
-  __shared__ uint64_t kfull[KS], kempty[KS], qfull[kAmQ], qempty[kAmQ], sfull[2], sempty[2], lfull[2], hsum;
-  __shared__ __align__(16) float ls[2][128];
+  __shared__ uint64_t kfull[KS], kempty[KS], qfull[kAmQ], qempty[kAmQ], lfull[kAmQ];
+  __shared__ uint64_t sfull[2][2], sempty[2][2], hsum;  // [buffer][key tile]
   __shared__ float half_s[2][128];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* ks = align1024(smem);
   uint8_t* qs = ks + KS * 65536;
+  uint8_t* ones = ks + 6 * 32768;        // the extra channels of every key
+  uint8_t* bias = ones + kAmExtra;       // and of the rows of the query tiles in the ring
+  for (int i = tid; i < (1 + kAmQ) * kAmExtra / 16; i += kAmThreads) {
+    // rows of 8 to a core matrix, the two core matrices of a row 128 bytes apart
+    const bool one = i < kAmExtra / 16 && ((i >> 3) & 1) == 0;
+    reinterpret_cast<uint4*>(ones)[i] = one ? make_uint4(0x3f803f80u, 0x00003f80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
   if (tid == 0) {
     for (int i = 0; i < KS; ++i) {
       mbar_init(&kfull[i], 1);
@@ -365,11 +379,11 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
     for (int i = 0; i < kAmQ; ++i) {
       mbar_init(&qfull[i], 1);
       mbar_init(&qempty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sfull[i], 2);  // the issuing thread and its commit
-      mbar_init(&sempty[i], 512);
       mbar_init(&lfull[i], 32);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sfull[i >> 1][i & 1], 1);
+      mbar_init(&sempty[i >> 1][i & 1], 256);
     }
     mbar_init(&hsum, 512);
     abort_flag = 0;
@@ -402,7 +416,80 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
   int units = 0, tiles = 0;  // units and query tiles loaded (16), used (17), read (others)
   bool ok = true;
 
-  if (warp == 16) {
+  if (warp < 16) {
+    const int wg = warp >> 2, kt = wg >> 1, half = wg & 1, key = kt * 128 + (tid & 127);
+    constexpr int cols = nq >> 1;
+    const int c0 = half * cols;  // this warp's columns
+    const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kt * 128 + c0;
+    const float sl = p.scale_log2;
+    for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+      const int n = tt.n[r.b], m = tt.m[r.b], t = r.j * kAmKeys + key;
+      float sum = 0.f;
+      int rt = r.f + r.lo % r.width;
+      for (int o = r.lo; o < r.hi; ++o) {
+        const int buf = tiles & 1, i0 = rt * nq;
+        if (++rt == r.f + r.width) rt = r.f;
+        if (!(ok = wait(&sfull[buf][kt], tiles / 2))) break;
+        tc_fence_after();
+        uint32_t va[2][32];
+        tc_ld32(mine + buf * 256, va[0]);
+        if (cols > 32) tc_ld32(mine + buf * 256 + 32, va[1]);
+        // the columns this key's sum takes: rows i >= t - (n - m) (causal) and i < m
+        const int jmin = t - (n - m) - i0, jmax = m - i0;
+        const bool all = __all_sync(0xffffffffu, jmin <= c0 && jmax >= c0 + cols);
+        float s0 = 0.f, s1 = 0.f;
+        tc_ld_wait();
+#pragma unroll
+        for (int c = 0; c < cols; c += 32) {
+          uint32_t(&v)[32] = va[c / 32];
+          tc_ld_done(v);
+          if (all) {
+            float u0 = 0.f, u1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {  // scalar on purpose: the packed product measured half as fast
+              s0 += ex2_approx(__uint_as_float(v[j]) * sl);
+              s1 += ex2_approx(__uint_as_float(v[j + 1]) * sl);
+              u0 += ex2_approx(__uint_as_float(v[j + 2]) * sl);
+              u1 += ex2_approx(__uint_as_float(v[j + 3]) * sl);
+            }
+            s0 += u0;
+            s1 += u1;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int col = c0 + c + j;
+              const float e = ex2_approx(__uint_as_float(v[j]) * sl);
+              s0 += col >= jmin && col < jmax ? e : 0.f;
+            }
+          }
+        }
+        sum += s0 + s1;  // tile by tile: a sum of thousands of rows keeps its small terms
+        tc_fence_before();
+        mbar_arrive(&sempty[buf][kt]);
+        ++tiles;
+      }
+      if (!ok) break;
+      // the two halves of the columns meet
+      if (half) half_s[kt][tid & 127] = sum;
+      mbar_arrive(&hsum);
+      if (!(ok = wait(&hsum, 2 * units))) break;
+      if (!half) {
+        sum += half_s[kt][tid & 127];
+        if (r.whole) {
+          if (t < n) {
+            const int phys = p.page_table[(size_t)r.b * p.max_pages + (t >> p.pshift)];
+            if (phys >= 0 && phys < p.num_phys) p.acc[((size_t)r.b * p.Hkv + r.g) * p.acc_stride + t] += sum;
+          }
+        } else {
+          p.part[(2 * (size_t)blockIdx.x + (r.first ? 0 : 1)) * kAmKeys + key] = sum;
+        }
+      }
+      mbar_arrive(&hsum);  // half_s is free
+      if (!(ok = wait(&hsum, 2 * units + 1))) break;
+      ++units;
+    }
+  } else {
+    if (warp == 16) {
     const bool lead = elect_lane();
     for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
       const int n = tt.n[r.b], s = units % KS;
@@ -452,6 +539,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
     constexpr uint32_t idesc = idesc_bf16_f32(128, nq);
     const bool lead = elect_lane();
     const uint32_t klo = sw128_kmajor_lo(smem_u32(ks)), qlo = sw128_kmajor_lo(smem_u32(qs));
+    const uint32_t onelo = plain_kmajor_lo(smem_u32(ones)), biaslo = plain_kmajor_lo(smem_u32(bias));
     for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
       const int s = units % KS;
       if (!(ok = wait(&kfull[s], units / KS))) break;
@@ -459,13 +547,12 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
       for (int o = r.lo; o < r.hi; ++o) {
         const int t = tiles % kAmQ, d = tiles & 1;
         if (!(ok = wait(&qfull[t], tiles / kAmQ))) break;
-        // the rows' log-sum-exps are written after the buffer's last reading, so this wait
-        // covers the logits' buffer too
-        if (!(ok = wait(&lfull[d], tiles / 2))) break;
-        tc_fence_after();
+        if (!(ok = wait(&lfull[t], tiles / kAmQ))) break;
         const uint32_t q = qlo + t * (QB >> 4);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
+          if (tiles >= 2 && !(ok = wait(&sempty[d][w], tiles / 2 - 1))) break;
+          tc_fence_after();
           const uint32_t to = tmem + d * 256 + w * 128, key = klo + s * (65536 >> 4) + w * (32768 >> 4);
           tc_mma_ss<false>(lead, to, key, q, idesc);
 #pragma unroll
@@ -473,11 +560,12 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
             const uint32_t in = (k & 3) * 32;
             tc_mma_ss<true>(lead, to, key + (((k >> 2) * 16384 + in) >> 4), q + (((k >> 2) * (QB / 2) + in) >> 4), idesc);
           }
+          tc_mma_ss<true, kPlainDescHi>(lead, to, onelo, biaslo + t * (kAmExtra >> 4), idesc);
+          tc_commit_if(lead, &sfull[d][w]);
         }
+        if (!ok) break;
         tc_commit_if(lead, &qempty[t]);
         tc_commit_if(lead && o + 1 == r.hi, &kempty[s]);
-        tc_commit_if(lead, &sfull[d]);
-        if (lead) mbar_arrive(&sfull[d]);
         __syncwarp();
         ++tiles;
       }
@@ -486,106 +574,57 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
       for (int i = max(0, tiles - kAmQ); i < tiles; ++i) mbar_wait(&qempty[i % kAmQ], (uint32_t)((i / kAmQ) & 1));
       for (int i = max(0, units - KS); i < units; ++i) mbar_wait(&kempty[i % KS], (uint32_t)((i / KS) & 1));
     }
-  } else if (warp == 18) {
+  } else {
+    // two warps take the query tiles in turn; a tile's log-sum-exps are loaded while the
+    // one before it (of this warp) is still being written
+    const float inv = 1.f / p.scale;
+    int before = 0;  // tiles of the runs before
     for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
       const int m = tt.m[r.b];
-      int h = r.lo / r.width, rt = r.f + r.lo - h * r.width;
-      for (int o = r.lo; o < r.hi; ++o) {
-        const int d = tiles & 1, i0 = rt * nq;
+      int o = r.lo + ((before + warp) & 1);  // warp 18 takes the even tiles of the CTA
+      int h = o / r.width, rt = r.f + o - h * r.width;
+      auto load = [&](float(&v)[4]) {
+        const int i0 = rt * nq;
         const float* src = p.lse + ((size_t)r.b * p.Hq + r.g * p.G + h) * p.T + i0;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = lane + 32 * e < min(nq, m - i0) ? src[lane + 32 * e] : -INFINITY;
-        if (tiles >= 2 && !(ok = wait(&sempty[d], tiles / 2 - 1))) break;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          ls[d][lane + 32 * e] = v[e] == -INFINITY ? -INFINITY : v[e] * -1.4426950408889634f;  // negated: an addend
-        mbar_arrive(&lfull[d]);
-        ++tiles;
-        if (++rt == r.f + r.width) {
-          rt = r.f;
+          v[e] = o < r.hi && lane + 32 * e < min(nq, m - i0) ? src[lane + 32 * e] : -INFINITY;
+      };
+      float next[4];
+      load(next);
+      while (o < r.hi) {
+        const int tile = before + o - r.lo, t = tile % kAmQ;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = next[e];
+        o += 2;
+        rt += 2;
+        while (rt >= r.f + r.width) {
+          rt -= r.width;
           ++h;
         }
+        load(next);
+        // -lse / scale in three bf16 terms (a row that weighs nothing: a huge negative one)
+        uint2 w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float a = v[e] == -INFINITY ? -1e30f : -v[e] * inv;
+          a = a > 1e30f ? 1e30f : (a < -1e30f ? -1e30f : a);  // a NaN stays one
+          const float hi = __bfloat162float(__float2bfloat16_rn(a)), r1 = a - hi;
+          const float mid = __bfloat162float(__float2bfloat16_rn(r1));
+          w[e] = make_uint2(pack_bf16x2(hi, mid), pack_bf16x2(r1 - mid, 0.f));
+        }
+        if (tile >= kAmQ && !(ok = wait(&qempty[t], tile / kAmQ - 1))) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = lane + 32 * e;
+          if (row < nq) *reinterpret_cast<uint2*>(bias + t * kAmExtra + (row >> 3) * 256 + (row & 7) * 16) = w[e];
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&lfull[t]);
       }
+      before += r.hi - r.lo;
     }
-  } else {
-    const int wg = warp >> 2, kt = wg >> 1, half = wg & 1, key = kt * 128 + (tid & 127);
-    constexpr int cols = nq >> 1;
-    const int c0 = half * cols;  // this warp's columns
-    const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kt * 128 + c0;
-    const float sl = p.scale_log2;
-    for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
-      const int n = tt.n[r.b], m = tt.m[r.b], t = r.j * kAmKeys + key;
-      float sum = 0.f;
-      int rt = r.f + r.lo % r.width;
-      for (int o = r.lo; o < r.hi; ++o) {
-        const int buf = tiles & 1, i0 = rt * nq;
-        if (++rt == r.f + r.width) rt = r.f;
-        if (!(ok = wait(&sfull[buf], tiles / 2))) break;
-        tc_fence_after();
-        uint32_t va[2][32];
-        tc_ld32(mine + buf * 256, va[0]);
-        if (cols > 32) tc_ld32(mine + buf * 256 + 32, va[1]);
-        // the columns this key's sum takes: rows i >= t - (n - m) (causal) and i < m
-        const int jmin = t - (n - m) - i0, jmax = m - i0;
-        const bool all = __all_sync(0xffffffffu, jmin <= c0 && jmax >= c0 + cols);
-        float s0 = 0.f, s1 = 0.f;
-        tc_ld_wait();
-#pragma unroll
-        for (int c = 0; c < cols; c += 32) {
-          uint32_t(&v)[32] = va[c / 32];
-          tc_ld_done(v);
-          const float* lp = &ls[buf][c0 + c];
-          if (all) {
-            const float2 sl2 = make_float2(sl, sl);
-            float2 e2 = make_float2(s0, s1), f2 = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 a = *reinterpret_cast<const float4*>(lp + j);
-              float2 x = fma2(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sl2, make_float2(a.x, a.y));
-              float2 y = fma2(make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), sl2, make_float2(a.z, a.w));
-              x.x = ex2_approx(x.x);
-              x.y = ex2_approx(x.y);
-              y.x = ex2_approx(y.x);
-              y.y = ex2_approx(y.y);
-              e2 = add2(e2, x);
-              f2 = add2(f2, y);
-            }
-            s0 = e2.x + f2.x;
-            s1 = e2.y + f2.y;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int col = c0 + c + j;
-              const float e = ex2_approx(fmaf(__uint_as_float(v[j]), sl, lp[j]));
-              s0 += col >= jmin && col < jmax ? e : 0.f;
-            }
-          }
-        }
-        sum += s0 + s1;  // tile by tile: a sum of thousands of rows keeps its small terms
-        tc_fence_before();
-        mbar_arrive(&sempty[buf]);
-        ++tiles;
-      }
-      if (!ok) break;
-      // the two halves of the columns meet
-      if (half) half_s[kt][tid & 127] = sum;
-      mbar_arrive(&hsum);
-      if (!(ok = wait(&hsum, 2 * units))) break;
-      if (!half) {
-        sum += half_s[kt][tid & 127];
-        if (r.whole) {
-          if (t < n) {
-            const int phys = p.page_table[(size_t)r.b * p.max_pages + (t >> p.pshift)];
-            if (phys >= 0 && phys < p.num_phys) p.acc[((size_t)r.b * p.Hkv + r.g) * p.acc_stride + t] += sum;
-          }
-        } else {
-          p.part[(2 * (size_t)blockIdx.x + (r.first ? 0 : 1)) * kAmKeys + key] = sum;
-        }
-      }
-      mbar_arrive(&hsum);  // half_s is free
-      if (!(ok = wait(&hsum, 2 * units + 1))) break;
-      ++units;
     }
   }
 
@@ -597,7 +636,8 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
       for (int i = max(0, tiles - kAmQ); i < tiles; ++i) mbar_wait(&qfull[i % kAmQ], (uint32_t)((i / kAmQ) & 1));
       for (int i = max(0, units - KS); i < units; ++i) mbar_wait(&kfull[i % KS], (uint32_t)((i / KS) & 1));
     }
-    if (warp == 17 && lane == 0 && tiles > 0) mbar_wait(&sfull[(tiles - 1) & 1], (uint32_t)(((tiles - 1) / 2) & 1));
+    if (warp == 17 && lane == 0 && tiles > 0)
+      mbar_wait(&sfull[(tiles - 1) & 1][1], (uint32_t)(((tiles - 1) / 2) & 1));
     __syncthreads();
   }
   if (warp == 17) {
@@ -876,6 +916,7 @@ cudaError_t launch_accum_rows(const AccumRowsArgs& a, cudaStream_t s) {
   p.num_phys = c.num_phys_pages;
   p.acc_stride = a.acc_stride;
   p.N = num_sms();
+  p.scale = a.scale;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   if (p.N > kMaxSms) p.N = kMaxSms;
   p.part = static_cast<float*>(a.ws);

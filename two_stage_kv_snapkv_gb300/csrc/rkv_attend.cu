@@ -760,25 +760,24 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
               tc_st32_wait(mine + 128 + c * 32, o);
             }
           }
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          const float2 sl2 = make_float2(sl, sl), m2 = make_float2(-m, -m);
+          float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t pk[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const int cc = c * 2 + (j >> 4), jj = (j & 15) * 2;
-              float2 a = fma2(make_float2(__uint_as_float(v[cc][jj]), __uint_as_float(v[cc][jj + 1])), sl2, m2);
-              a.x = ex2_approx(a.x);
-              a.y = ex2_approx(a.y);
-              sum[j & 1] = add2(sum[j & 1], a);
+              const float ax = ex2_approx(fmaf(__uint_as_float(v[cc][jj]), sl, -m));
+              const float ay = ex2_approx(fmaf(__uint_as_float(v[cc][jj + 1]), sl, -m));
+              (j & 1 ? u0 : s0) += ax;
+              (j & 1 ? u1 : s1) += ay;
               // bf16 weights (off by at most 2^-8 of each, as V is); their sum stays unrounded
-              pk[j] = pack_bf16x2(a.x, a.y);
+              pk[j] = pack_bf16x2(ax, ay);
             }
             tc_st32(mine + c * 32, pk);
           }
           tc_st_wait();
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          l += (s0 + s1) + (u0 + u1);
           tc_fence_before();
           mbar_arrive(&p_b[slot]);
         }

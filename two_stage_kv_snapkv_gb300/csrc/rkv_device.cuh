@@ -187,23 +187,6 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// Two fp32 lanes in one instruction (half the issue slots of two; the same roundings).
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
-      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n"
-      " mov.b64 {%0, %1}, w;\n}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -336,6 +319,11 @@ __device__ __forceinline__ uint32_t sw128_kmajor_lo(uint32_t saddr) { return ((s
 __device__ __forceinline__ uint32_t sw128_nmajor_lo(uint32_t saddr, uint32_t n_block_bytes) {
   return ((saddr >> 4) & 0x3FFFu) | ((n_block_bytes >> 4) << 16);
 }
+// A K-major operand without swizzle, 16 elements of K deep: 8 x 16-byte core matrices of 128
+// bytes, the two along K one behind the other (leading offset 128), groups of 8 rows 256
+// bytes apart.
+constexpr uint32_t kPlainDescHi = (256 >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t plain_kmajor_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | ((128u >> 4) << 16); }
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_lane() {
   uint32_t p;
@@ -346,13 +334,13 @@ __device__ __forceinline__ bool elect_lane() {
 // two K elements to a column).  Called by a whole warp, issued where `issue` holds: the
 // operands then stay in uniform registers.  (Issued from one lane's branch with 64-bit
 // descriptors built per instruction, an MMA cost 115 clocks of issue against 64 of work.)
-template <bool kAccumulate>
+template <bool kAccumulate, uint32_t kDescHi = kSw128DescHi>
 __device__ __forceinline__ void tc_mma_ss(bool issue, uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc) {
   asm volatile(
       "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 q, %0, 0;\n setp.ne.b32 p, %6, 0;\n"
       " mov.b64 x, {%2, %4};\n mov.b64 y, {%3, %4};\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%1], x, y, %5, p;\n}\n" ::"r"((uint32_t)issue),
-      "r"(d_tmem), "r"(alo), "r"(blo), "r"(kSw128DescHi), "r"(idesc), "n"(kAccumulate ? 1 : 0)
+      "r"(d_tmem), "r"(alo), "r"(blo), "r"(kDescHi), "r"(idesc), "n"(kAccumulate ? 1 : 0)
       : "memory");
 }
 __device__ __forceinline__ void tc_mma_ts(bool issue, uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc,
