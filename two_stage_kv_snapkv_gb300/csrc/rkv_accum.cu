@@ -18,12 +18,9 @@ namespace {
 // read, 4 KB for a 16-key chunk, and every position has one writer: no atomics, the
 // same sums in the same order every time.
 constexpr int kRwKeys = 16;
-constexpr int kRwWarps = 8;
-constexpr int kRwThreads = kRwWarps * 32;
-constexpr int kRwStages = 6;
 constexpr int kRwStageBytes = 4096;
 constexpr int kRwBlock = 64;  // query rows staged at a time, at most
-constexpr int kRwSmem = 1024 + kRwWarps * kRwStages * kRwStageBytes + kRwBlock * 256;
+constexpr int kRwSmem = 1024 + 48 * kRwStageBytes + kRwBlock * 256;
 
 struct RowsParams {
   CUtensorMap tmk;     // the key pool as [rows][128] bf16, 128-byte swizzled boxes of 64 channels
@@ -61,9 +58,18 @@ __device__ __forceinline__ int rows_cache_len(const RowsParams& p, int b) {
 }
 
 // kR16: 16-row groups of a block; the block's rows stay in registers as B fragments.
+// Up to two groups leave room for 16 warps with three stages each, which hide the chain
+// of a chunk (load, product, exponential, sum) better than eight warps with six.
 template <int kR16>
-__global__ void __launch_bounds__(kRwThreads, 1) accum_rows_kernel(const __grid_constant__ RowsParams p) {
+struct RowsShape {
+  static constexpr int kWarps = kR16 <= 2 ? 16 : 8;
+  static constexpr int kStages = 48 / kWarps;
+};
+template <int kR16>
+__global__ void __launch_bounds__(RowsShape<kR16>::kWarps * 32, 1)
+    accum_rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr int kBlock = kR16 * 16;
+  constexpr int kRwWarps = RowsShape<kR16>::kWarps, kRwStages = RowsShape<kR16>::kStages, kRwThreads = kRwWarps * 32;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ FlatTable ft;
   __shared__ uint64_t full_b[kRwWarps][kRwStages];
@@ -937,7 +943,7 @@ cudaError_t launch_accum_rows(const AccumRowsArgs& a, cudaStream_t s) {
   if ((e = opt[most <= 16 ? 0 : (most <= 32 ? 1 : 2)].raise(reinterpret_cast<const void*>(kernel), kRwSmem)) != cudaSuccess)
     return e;
   launch_begin(K_ACCUM_ROWS, s);
-  kernel<<<p.N, kRwThreads, kRwSmem, s>>>(p);
+  kernel<<<p.N, most <= 32 ? RowsShape<2>::kWarps * 32 : RowsShape<4>::kWarps * 32, kRwSmem, s>>>(p);
   launch_end(K_ACCUM_ROWS, s);
   return cudaGetLastError();
 }

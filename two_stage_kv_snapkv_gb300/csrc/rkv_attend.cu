@@ -31,7 +31,7 @@ constexpr int kArMergeFloats = kArWarps * kArMergeRows * 128;
 constexpr int kArSmem = 1024 + kArWarps * kArStages * kArStageBytes + kArMergeFloats * 4;
 constexpr float kNoMax = -1e30f;                  // running maximum of a row that saw nothing
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWeighTokens = 1024;                // tokens of a weighing block
+constexpr int kWeighTokens = 2048;                // tokens of a weighing block, eight a thread
 
 struct AttendParams {
   CUtensorMap tmk, tmv;    // the page pools as [rows][128] bf16, 16-row x 64-channel boxes (the tiled
@@ -396,7 +396,7 @@ __device__ __forceinline__ float2 join_ml(const AttendParams& p, const PartSlots
   return make_float2(M, L);
 }
 
-// Joins the parts of the split units: one warp a row, four channels a lane, eight parts'
+// Joins the parts of the split units: one warp a row, four channels a lane, four parts'
 // loads in flight.  256 threads, eight rows of the line of all rows at a time.
 template <int kRows, int kKeys>
 __device__ __forceinline__ void combine_row(const AttendParams& p, const FlatTable& ft, int b, int idx, int lane) {
@@ -417,20 +417,18 @@ __device__ __forceinline__ void combine_row(const AttendParams& p, const FlatTab
   if (ps.c0 == ps.c1) return;  // final already
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = kNoMax, L = 0.f;
-  for (int c = ps.c0; c <= ps.c1; c += 8) {
-    float4 v[8];
-    float2 ml[8];
+  for (int c = ps.c0; c <= ps.c1; c += 4) {
+    float4 v[4];
+    float2 ml[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j <= ps.c1) {
-        const size_t at = ps[c + j] * kRows + row;
-        ml[j] = p.part_ml[at];
-        v[j] = reinterpret_cast<const float4*>(p.part_o + at * 128)[lane];
-      }
-    float to = M;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j <= ps.c1) to = fmaxf(to, ml[j].x);
+    for (int j = 0; j < 4; ++j) {
+      const bool in = c + j <= ps.c1;
+      const size_t at = ps[in ? c + j : c] * kRows + row;  // behind the last part: the first again, unweighted
+      ml[j] = p.part_ml[at];
+      v[j] = reinterpret_cast<const float4*>(p.part_o + at * 128)[lane];
+      if (!in) ml[j] = make_float2(kNoMax, 0.f);
+    }
+    const float to = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
     const float f = ex2_approx(M - to);
     M = to;
     L *= f;
@@ -439,15 +437,14 @@ __device__ __forceinline__ void combine_row(const AttendParams& p, const FlatTab
     o.z *= f;
     o.w *= f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j <= ps.c1) {
-        const float w = ex2_approx(ml[j].x - M);
-        L += ml[j].y * w;
-        o.x += v[j].x * w;
-        o.y += v[j].y * w;
-        o.z += v[j].z * w;
-        o.w += v[j].w * w;
-      }
+    for (int j = 0; j < 4; ++j) {
+      const float w = c + j <= ps.c1 ? ex2_approx(ml[j].x - M) : 0.f;
+      L += ml[j].y * w;
+      o.x += v[j].x * w;
+      o.y += v[j].y * w;
+      o.z += v[j].z * w;
+      o.w += v[j].w * w;
+    }
   }
   const float inv = L > 0.f ? 1.f / L : 0.f;
   *out = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -455,7 +452,7 @@ __device__ __forceinline__ void combine_row(const AttendParams& p, const FlatTab
 }
 
 template <int kRows, int kKeys>
-__global__ void __launch_bounds__(256) attend_combine_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(256, 4) attend_combine_kernel(const __grid_constant__ AttendParams p) {
   __shared__ FlatTable ft;
   build_table<kRows, kKeys>(p, ft);  // lengths only: they were final before the parts' kernel began
   grid_dependency_wait();
@@ -466,9 +463,9 @@ __global__ void __launch_bounds__(256) attend_combine_kernel(const __grid_consta
 
 // The end of a one-token step: the first CTAs join the rows as attend_combine does, the
 // others add the weights, acc_j += sum_h 2^(z_hj - m_h) / l_h, over blocks of
-// kWeighTokens tokens of a (sequence, KV head), four tokens a thread; each block joins its
+// kWeighTokens tokens of a (sequence, KV head), eight tokens a thread; each block joins its
 // heads' (m, l) for itself.  The logits were written a moment ago and mostly lie in L2.
-__global__ void __launch_bounds__(256) attend_weigh_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(256, 4) attend_weigh_kernel(const __grid_constant__ AttendParams p) {
   __shared__ FlatTable ft;
   __shared__ float lse2[8];
   __shared__ long long wbase[RKV_MAX_BATCH + 1];
@@ -499,21 +496,31 @@ __global__ void __launch_bounds__(256) attend_weigh_kernel(const __grid_constant
       if (lane == 0) lse2[warp] = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;  // nothing read: weighs nothing
     }
     __syncthreads();
-    const int t = blk * kWeighTokens + tid * 4;
-    if (t < n) {
-      float w[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int h = 0; h < p.G; ++h) {
-        const float base = lse2[h];
-        const float4 z = *reinterpret_cast<const float4*>(p.z + (unit * p.G + h) * p.zstride + t);
-        w[0] += ex2_approx(z.x - base);
-        w[1] += ex2_approx(z.y - base);
-        w[2] += ex2_approx(z.z - base);
-        w[3] += ex2_approx(z.w - base);
-      }
-      float* a = p.acc + unit * p.acc_stride + t;
+    // two quads of tokens a thread; positions behind n hold -inf up to the chunk's end and
+    // are not read beyond it
+    const int t[2] = {blk * kWeighTokens + tid * 4, blk * kWeighTokens + kWeighTokens / 2 + tid * 4};
+    float4 w[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    const float* zu = p.z + unit * p.G * p.zstride;
+#pragma unroll 4
+    for (int h = 0; h < p.G; ++h) {
+      const float base = lse2[h];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (t + e < n) a[e] += w[e];
+      for (int q = 0; q < 2; ++q)
+        if (t[q] < n) {
+          const float4 z = *reinterpret_cast<const float4*>(zu + (size_t)h * p.zstride + t[q]);
+          w[q].x += ex2_approx(z.x - base);
+          w[q].y += ex2_approx(z.y - base);
+          w[q].z += ex2_approx(z.z - base);
+          w[q].w += ex2_approx(z.w - base);
+        }
+    }
+    float* a = p.acc + unit * p.acc_stride;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float e[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t[q] + i < n) a[t[q] + i] += e[i];
     }
     __syncthreads();  // lse2 is free
   }
@@ -1168,7 +1175,7 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
     w += align256((size_t)c.B * a.Hq * 8);
     p.z = reinterpret_cast<float*>(w);
   }
-  const long long jrows = ((long long)c.B * a.Hq * a.T + 7) / 8, jmost = 6LL * p.N;
+  const long long jrows = ((long long)c.B * a.Hq * a.T + 7) / 8, jmost = 8LL * p.N;
   const dim3 jgrid((unsigned)(jrows < jmost ? jrows : jmost));
   if (tile > kArRows) {
     const bool wide = tile == 256;
