@@ -94,19 +94,21 @@ def _check_tree(out, lse, K, V, q, kt, vt, sees, nodes, scale=None):
     ([130], 1, 8, 16, 256, [256], "random"),
     ([4099], 4, 4, 16, 17, [17], "tree"),
 ])
-def test_tree_attention(rkv, lens, Hkv, G, P, T, nodes, kind):
+@pytest.mark.parametrize("room", [0, 40000])
+def test_tree_attention(rkv, lens, Hkv, G, P, T, nodes, kind, room):
+    # the room a cache has left decides which kernel takes a short one
     live = nodes or [T] * len(lens)
-    cache, K, V, q, kt, vt, sees, _ = _tree_case(rkv, lens, Hkv, G, P, T, live, kind)
+    cache, K, V, q, kt, vt, sees, _ = _tree_case(rkv, lens, Hkv, G, P, T, live, kind, room=room)
     out, lse = _run_tree(rkv, cache, q, kt, vt, sees, nodes)
     assert _status(rkv, cache) == 0
     _check_tree(out, lse, K, V, q, kt, vt, sees, live)
 
 
-@pytest.mark.parametrize("T,G", [(3, 4), (40, 4)])
-def test_tree_attention_large_logits_and_scale(rkv, T, G):
+@pytest.mark.parametrize("T,G,room", [(3, 4, 0), (3, 4, 40000), (40, 4, 0)])
+def test_tree_attention_large_logits_and_scale(rkv, T, G, room):
     # keys far from the mean: the running maximum moves late in the cache, by hundreds
     lens, nodes = [777], [T]
-    cache, K, V, q, kt, vt, sees, _ = _tree_case(rkv, lens, 1, G, 16, T, nodes, "tree", seed=5)
+    cache, K, V, q, kt, vt, sees, _ = _tree_case(rkv, lens, 1, G, 16, T, nodes, "tree", seed=5, room=room)
     K[0][:, 700] *= 40
     K[0][:, 5] *= 20
     C.put_rows(cache, 0, K[0], V[0])
@@ -114,10 +116,10 @@ def test_tree_attention_large_logits_and_scale(rkv, T, G):
     _check_tree(out, lse, K, V, q, kt, vt, sees, nodes, 0.3)
 
 
-@pytest.mark.parametrize("T,G", [(2, 4), (24, 4)])
-def test_tree_attention_bad_lengths_and_pages_are_flagged(rkv, T, G):
+@pytest.mark.parametrize("T,G,room", [(2, 4, 0), (2, 4, 40000), (24, 4, 0)])
+def test_tree_attention_bad_lengths_and_pages_are_flagged(rkv, T, G, room):
     lens, nodes = [300, 40], [T, T]
-    cache, K, V, q, kt, vt, sees, _ = _tree_case(rkv, lens, 1, G, 16, T, nodes, "tree", seed=6)
+    cache, K, V, q, kt, vt, sees, _ = _tree_case(rkv, lens, 1, G, 16, T, nodes, "tree", seed=6, room=room)
     out, lse = _run_tree(rkv, cache, q, kt, vt, sees, [T + 1, T])
     assert _status(rkv, cache) == rkv.DEVERR_TREE
     assert (out[0].cpu() == 7).all()
@@ -165,9 +167,10 @@ def _check_decode(out, lse, got_acc, acc0, K, V, q, steps=1):
 
 @pytest.mark.parametrize("lens,Hkv,G,P", [
     ([0], 1, 1, 16), ([1], 2, 8, 16), ([0, 5, 16], 1, 4, 16), ([17, 1000, 31], 2, 2, 32), ([64, 63, 129], 1, 8, 64),
-    ([2563], 8, 4, 16), ([6000, 0], 1, 1, 16), ([40] * 70, 4, 4, 16)])
-def test_decode_accum(rkv, lens, Hkv, G, P):
-    cache, K, V = C.make_cache(rkv, lens, Hkv, P, seed=11)
+    ([2563], 8, 4, 16), ([6000, 0], 1, 1, 16), ([40] * 70, 4, 4, 16), ([100, 7, 300], 30, 2, 16)])
+@pytest.mark.parametrize("room", [0, 20000])
+def test_decode_accum(rkv, lens, Hkv, G, P, room):
+    cache, K, V = C.make_cache(rkv, lens, Hkv, P, seed=11, room=room)
     g = C.gen(12)
     B = len(lens)
     q = C.randn(g, B, Hkv * G, D)
@@ -186,8 +189,9 @@ def test_decode_accum(rkv, lens, Hkv, G, P):
         assert torch.equal(acc[b, :, n:].cpu(), acc0[b, :, n:])
 
 
-def test_decode_accum_skips_a_bad_page(rkv):
-    cache, K, V = C.make_cache(rkv, [100, 50], 1, 16, seed=13)
+@pytest.mark.parametrize("room", [0, 20000])
+def test_decode_accum_skips_a_bad_page(rkv, room):
+    cache, K, V = C.make_cache(rkv, [100, 50], 1, 16, seed=13, room=room)
     q = C.randn(C.gen(14), 2, 4, D)
     acc = rkv.accum_sums(cache)
     out = torch.empty(2, 4, D, dtype=torch.bfloat16, device="cuda")

@@ -129,7 +129,7 @@ const char* kernel_name(int kind) {
       "snap_colsum",  "snap_pool",    "snap_select",    "snap_compact", "hsa_score",
       "hsa_topk",     "hsa_attend",   "hsa_combine",    "hsa_step",     "recall",
       "chunk_gather", "sparq_score",  "sparq_topk",     "sparq_attend", "wait_selftest",
-      "sparq_keys_sync", "attend_rows", "attend_tiles", "attend_combine", "attend_weigh", "tree_commit",
+      "sparq_keys_sync", "attend_rows", "attend_tiles", "attend_units", "attend_combine", "attend_weigh", "tree_commit",
       "accum_rows", "accum_tiles", "accum_join", "evict_select", "evict_stage", "evict_compact"};
   return (kind >= 0 && kind < K_NUM_KINDS) ? names[kind] : nullptr;
 }

@@ -14,6 +14,8 @@
 // keep HBM busy), its own running maximum, sum and fp32 output, and meet once per run.  A
 // run that is a whole unit is final; the parts of a split unit go to the workspace and
 // attend_combine joins them.
+#include <cooperative_groups.h>
+
 #include "rkv_flat.cuh"
 #include "rkv_internal.h"
 
@@ -51,6 +53,7 @@ struct AttendParams {
   float* z;                 // [B][Hkv][G][zstride] base-2 scaled logits of a one-token step, or null
   float* acc;               // [B][Hkv][acc_stride]
   int B, Hq, Hkv, G, gshift, T, words, P, pshift, max_pages, num_phys, zstride, acc_stride, N;
+  int row_tiles;            // attend_units: 16-row tiles of a KV head
   float scale_log2;
 };
 
@@ -85,6 +88,143 @@ __device__ __forceinline__ size_t out_row(const AttendParams& p, int b, int g, i
 }
 
 __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY; }
+
+// A warp's share of a 16-row tile: the queries as A fragments (eight steps of 16
+// channels), the running maximum, sum and fp32 output of fragment rows r0 = lane / 4 and
+// r1 = r0 + 8 of the tile.
+struct RowTile {
+  uint32_t qa[8][4];
+  float o[16][4];
+  float m0, m1, l0, l1;
+  int b, r0, r1, rows, nc, n, nodes;  // rows: live query rows of the KV head; nc: cache chunks
+
+  __device__ __forceinline__ void start(const AttendParams& p, int b_, int g, int rt, int n_, int nodes_) {
+    const int lane = threadIdx.x & 31;
+    b = b_;
+    n = n_;
+    nodes = nodes_;
+    rows = nodes * p.G;
+    nc = (n + kArKeys - 1) / kArKeys;
+    r0 = rt * kArRows + (lane >> 2);
+    r1 = r0 + 8;
+    const uint32_t* q0 = reinterpret_cast<const uint32_t*>(p.q + out_row(p, b, g, r0) * 128);
+    const uint32_t* q1 = reinterpret_cast<const uint32_t*>(p.q + out_row(p, b, g, r1) * 128);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      qa[k][0] = r0 < rows ? q0[k * 8 + (lane & 3)] : 0u;
+      qa[k][1] = r1 < rows ? q1[k * 8 + (lane & 3)] : 0u;
+      qa[k][2] = r0 < rows ? q0[k * 8 + 4 + (lane & 3)] : 0u;
+      qa[k][3] = r1 < rows ? q1[k * 8 + 4 + (lane & 3)] : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+    m0 = m1 = kNoMax;
+    l0 = l1 = 0.f;
+  }
+
+  // One chunk, K and V in st (its copy has landed).  save(z, col): base-2 logits of row r0
+  // at columns col, col + 1 of the chunk, -inf where masked.
+  template <class Save>
+  __device__ __forceinline__ void step(const AttendParams& p, uint8_t* st, int c, Save save) {
+    const int lane = threadIdx.x & 31, qc = (lane & 3) * 2;
+    const int left = c < nc ? n - c * kArKeys : nodes - (c - nc) * kArKeys;  // keys of the chunk from here on
+    if (left < kArKeys) {  // what lies behind the last key may be anything: 0 x NaN is not 0
+      for (int i = lane; i < 2 * (kArKeys - left) * 8; i += 32) {
+        const int half = i & 1, rest = i >> 1;
+        *reinterpret_cast<uint4*>(st + 4096 + half * 2048 + (left + (rest >> 3)) * 128 + (rest & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+    const uint32_t ks = smem_u32(st), vs = ks + 4096;
+    float z[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    {
+      const int key = ((lane >> 4) << 3) + (lane & 7), sub = (lane >> 3) & 1;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int piece = k * 2 + sub;
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4(b0, b1, b2, b3, ks + (piece >> 3) * 2048 + key * 128 + (((piece & 7) ^ (key & 7)) << 4));
+        mma_16816(z[0], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b0, b1);
+        mma_16816(z[1], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b2, b3);
+      }
+    }
+    // base-2 logits; masked ones -inf
+    uint32_t see0 = left >= kArKeys ? 0xffffu : (1u << left) - 1u, see1 = see0;
+    if (c >= nc) {
+      const int j0 = (c - nc) * kArKeys;
+      const uint32_t* mk = p.mask + (size_t)b * p.T * p.words + (j0 >> 5);
+      see0 &= r0 < rows ? mk[(size_t)(r0 >> p.gshift) * p.words] >> (j0 & 31) : 0u;
+      see1 &= r1 < rows ? mk[(size_t)(r1 >> p.gshift) * p.words] >> (j0 & 31) : 0u;
+    }
+    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = h * 8 + qc + e;
+        z[h][e] = (see0 >> col) & 1u ? z[h][e] * p.scale_log2 : -INFINITY;
+        z[h][2 + e] = (see1 >> col) & 1u ? z[h][2 + e] * p.scale_log2 : -INFINITY;
+        mx0 = fmaxf(mx0, z[h][e]);
+        mx1 = fmaxf(mx1, z[h][2 + e]);
+      }
+    save(make_float2(z[0][0], z[0][1]), qc);
+    save(make_float2(z[1][0], z[1][1]), qc + 8);
+    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+    const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+    const float f0 = ex2_approx(m0 - n0), f1 = ex2_approx(m1 - n1);
+    m0 = n0;
+    m1 = n1;
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        z[h][e] = ex2_approx(z[h][e] - n0);
+        z[h][2 + e] = ex2_approx(z[h][2 + e] - n1);
+        s0 += z[h][e];
+        s1 += z[h][2 + e];
+      }
+    l0 = l0 * f0 + s0;  // this thread's columns; the four lanes of a row add up at the end
+    l1 = l1 * f1 + s1;
+    if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        o[j][0] *= f0;
+        o[j][1] *= f0;
+        o[j][2] *= f1;
+        o[j][3] *= f1;
+      }
+    }
+    // The weights enter the second product as bf16 (off by at most 2^-9 of each, as
+    // the values they multiply and the output are); their sum stays unrounded.
+    const uint32_t a0 = pack_bf16x2(z[0][0], z[0][1]), a1 = pack_bf16x2(z[0][2], z[0][3]);
+    const uint32_t a2 = pack_bf16x2(z[1][0], z[1][1]), a3 = pack_bf16x2(z[1][2], z[1][3]);
+    const int key = (((lane >> 3) & 1) << 3) + (lane & 7);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int piece = j * 2 + (lane >> 4);
+      uint32_t b0, b1, b2, b3;
+      ldsm_x4_t(b0, b1, b2, b3, vs + (piece >> 3) * 2048 + key * 128 + (((piece & 7) ^ (key & 7)) << 4));
+      mma_16816(o[2 * j], a0, a1, a2, a3, b0, b1);
+      mma_16816(o[2 * j + 1], a0, a1, a2, a3, b2, b3);
+    }
+  }
+
+  // The four lanes of a row add their sums up.
+  __device__ __forceinline__ void finish() {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+  }
+};
 
 __global__ void __launch_bounds__(kArThreads, 1) attend_rows_kernel(const __grid_constant__ AttendParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -176,31 +316,12 @@ __global__ void __launch_bounds__(kArThreads, 1) attend_rows_kernel(const __grid
 
   const int qr = lane >> 2, qc = (lane & 3) * 2;  // fragment row and column pair
   FlatRun cr;
+  RowTile tile;
   for (long long x = x0; flat_run(ft, p.B, x, x0, x1, cr); x = cr.x + (cr.hi - cr.lo)) {
     const int b = cr.b, g = cr.unit % p.Hkv, rt = cr.unit / p.Hkv;
-    const int n = ft.n[b], nodes = ft.t[b], rows = nodes * p.G;
-    const int nc = (n + kArKeys - 1) / kArKeys;
-    const int r0 = rt * kArRows + qr, r1 = r0 + 8;
-    // the tile's queries as A fragments, eight steps of 16 channels
-    uint32_t qa[8][4];
-    {
-      const uint32_t* q0 = reinterpret_cast<const uint32_t*>(p.q + out_row(p, b, g, r0) * 128);
-      const uint32_t* q1 = reinterpret_cast<const uint32_t*>(p.q + out_row(p, b, g, r1) * 128);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        qa[k][0] = r0 < rows ? q0[k * 8 + (lane & 3)] : 0u;
-        qa[k][1] = r1 < rows ? q1[k * 8 + (lane & 3)] : 0u;
-        qa[k][2] = r0 < rows ? q0[k * 8 + 4 + (lane & 3)] : 0u;
-        qa[k][3] = r1 < rows ? q1[k * 8 + 4 + (lane & 3)] : 0u;
-      }
-    }
-    float o[16][4];
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    float m0 = kNoMax, m1 = kNoMax, l0 = 0.f, l1 = 0.f;
-
+    tile.start(p, b, g, rt, ft.n[b], ft.t[b]);
+    const int rows = tile.rows;
+    float* const zu = p.z + ((size_t)(b * p.Hkv + g) * p.G) * p.zstride;
     for (int c = cr.lo + warp; c < cr.hi; c += kArWarps) {
       const int s = used % kArStages;
       const bool late = !dead && !mbar_wait(&full_b[warp][s], (uint32_t)((used / kArStages) & 1));
@@ -208,118 +329,26 @@ __global__ void __launch_bounds__(kArThreads, 1) attend_rows_kernel(const __grid
         if (lane == 0) flag_error(p.err, RKV_DEVERR_TIMEOUT);
         dead = true;
       }
-      const bool take = !dead && !((skipped >> s) & 1u);
-      const int left = c < nc ? n - c * kArKeys : nodes - (c - nc) * kArKeys;  // keys of the chunk from here on
-      if (take) {
-        uint8_t* st = ring + s * kArStageBytes;
-        if (left < kArKeys) {  // what lies behind the last key may be anything: 0 x NaN is not 0
-          for (int i = lane; i < 2 * (kArKeys - left) * 8; i += 32) {
-            const int half = i & 1, rest = i >> 1;
-            *reinterpret_cast<uint4*>(st + 4096 + half * 2048 + (left + (rest >> 3)) * 128 + (rest & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        const uint32_t ks = smem_u32(st), vs = ks + 4096;
-        float z[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        {
-          const int key = ((lane >> 4) << 3) + (lane & 7), sub = (lane >> 3) & 1;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int piece = k * 2 + sub;
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4(b0, b1, b2, b3, ks + (piece >> 3) * 2048 + key * 128 + (((piece & 7) ^ (key & 7)) << 4));
-            mma_16816(z[0], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b0, b1);
-            mma_16816(z[1], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b2, b3);
-          }
-        }
-        // base-2 logits; masked ones -inf
-        uint32_t see0 = left >= kArKeys ? 0xffffu : (1u << left) - 1u, see1 = see0;
-        if (c >= nc) {
-          const int j0 = (c - nc) * kArKeys;
-          const uint32_t* mk = p.mask + (size_t)b * p.T * p.words + (j0 >> 5);
-          see0 &= r0 < rows ? mk[(size_t)(r0 >> p.gshift) * p.words] >> (j0 & 31) : 0u;
-          see1 &= r1 < rows ? mk[(size_t)(r1 >> p.gshift) * p.words] >> (j0 & 31) : 0u;
-        }
-        float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int col = h * 8 + qc + e;
-            z[h][e] = (see0 >> col) & 1u ? z[h][e] * p.scale_log2 : -INFINITY;
-            z[h][2 + e] = (see1 >> col) & 1u ? z[h][2 + e] * p.scale_log2 : -INFINITY;
-            mx0 = fmaxf(mx0, z[h][e]);
-            mx1 = fmaxf(mx1, z[h][2 + e]);
-          }
-        if (p.z) {  // the logits, for the weights (positions behind n hold -inf)
-          const size_t zb = ((size_t)(b * p.Hkv + g) * p.G) * p.zstride + (size_t)c * kArKeys + qc;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (r0 < rows)
-              *reinterpret_cast<float2*>(p.z + zb + (size_t)r0 * p.zstride + h * 8) = make_float2(z[h][0], z[h][1]);
-        }
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-        const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-        const float f0 = ex2_approx(m0 - n0), f1 = ex2_approx(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            z[h][e] = ex2_approx(z[h][e] - n0);
-            z[h][2 + e] = ex2_approx(z[h][2 + e] - n1);
-            s0 += z[h][e];
-            s1 += z[h][2 + e];
-          }
-        l0 = l0 * f0 + s0;  // this thread's columns; the four lanes of a row add up at the end
-        l1 = l1 * f1 + s1;
-        if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            o[j][0] *= f0;
-            o[j][1] *= f0;
-            o[j][2] *= f1;
-            o[j][3] *= f1;
-          }
-        }
-        // The weights enter the second product as bf16 (off by at most 2^-9 of each, as
-        // the values they multiply and the output are); their sum stays unrounded.
-        const uint32_t a0 = pack_bf16x2(z[0][0], z[0][1]), a1 = pack_bf16x2(z[0][2], z[0][3]);
-        const uint32_t a2 = pack_bf16x2(z[1][0], z[1][1]), a3 = pack_bf16x2(z[1][2], z[1][3]);
-        const int key = (((lane >> 3) & 1) << 3) + (lane & 7);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int piece = j * 2 + (lane >> 4);
-          uint32_t b0, b1, b2, b3;
-          ldsm_x4_t(b0, b1, b2, b3, vs + (piece >> 3) * 2048 + key * 128 + (((piece & 7) ^ (key & 7)) << 4));
-          mma_16816(o[2 * j], a0, a1, a2, a3, b0, b1);
-          mma_16816(o[2 * j + 1], a0, a1, a2, a3, b2, b3);
-        }
+      if (!dead && !((skipped >> s) & 1u)) {
+        tile.step(p, ring + s * kArStageBytes, c, [&](float2 z, int col) {
+          if (p.z && tile.r0 < rows)
+            *reinterpret_cast<float2*>(zu + (size_t)tile.r0 * p.zstride + (size_t)c * kArKeys + col) = z;
+        });
       } else if (p.z) {  // nothing was read: the positions weigh nothing
         for (int i = lane; i < rows * kArKeys; i += 32)
-          p.z[((size_t)(b * p.Hkv + g) * p.G + i / kArKeys) * p.zstride + (size_t)c * kArKeys + i % kArKeys] = -INFINITY;
+          zu[(size_t)(i / kArKeys) * p.zstride + (size_t)c * kArKeys + i % kArKeys] = -INFINITY;
       }
       ++used;
       __syncwarp();  // every lane has read the stage
       if (!dead) fetch();
     }
 
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    tile.finish();
     if ((lane & 3) == 0) {
-      wm[warp][qr] = m0;
-      wl[warp][qr] = l0;
-      wm[warp][qr + 8] = m1;
-      wl[warp][qr + 8] = l1;
+      wm[warp][qr] = tile.m0;
+      wl[warp][qr] = tile.l0;
+      wm[warp][qr + 8] = tile.m1;
+      wl[warp][qr + 8] = tile.l1;
     }
     // the warps meet, four rows at a time: thread = (row, two channels)
     const int live = min(kArRows, rows - rt * kArRows);
@@ -331,7 +360,7 @@ __global__ void __launch_bounds__(kArThreads, 1) attend_rows_kernel(const __grid
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           *reinterpret_cast<float2*>(merge + (warp * kArMergeRows + (qr & 3)) * 128 + j * 8 + qc) =
-              make_float2(o[j][(quarter >> 1) * 2], o[j][(quarter >> 1) * 2 + 1]);
+              make_float2(tile.o[j][(quarter >> 1) * 2], tile.o[j][(quarter >> 1) * 2 + 1]);
       }
       __syncthreads();
       const int sub = tid >> 6, d = (tid & 63) * 2, row = quarter * kArMergeRows + sub, r = rt * kArRows + row;
@@ -366,6 +395,214 @@ __global__ void __launch_bounds__(kArThreads, 1) attend_rows_kernel(const __grid
   // after a timeout: wait (bounded) for what this warp still has in flight
   if (dead)
     for (int i = used; i < fetched; ++i) mbar_wait(&full_b[warp][i % kArStages], (uint32_t)((i / kArStages) & 1));
+}
+
+// ---------------------------------------------------------------------------
+// attend_units: the same tile for small caches, where launches and latencies count: one
+// cluster of C CTAs per (sequence, KV head, row tile), each with an equal part of the
+// unit's chunks, two stages a warp.  The parts meet through distributed shared memory, so
+// there is one launch and no workspace; with weights, the logits stay in shared memory
+// until the log-sum-exps are known.  kWarps 8 for clusters of four and eight, 4 (three CTAs
+// an SM) for smaller ones.
+constexpr int kAuStages = 2;
+constexpr int kMaxUnitTokens = 1536 + kArKeys;  // tokens of a CTA whose logits it keeps
+template <int kWarps>
+struct UnitsShape {
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kRing = kWarps * kAuStages * kArStageBytes;  // then the warps' outputs
+  static constexpr int kPart = kArRows * 128 * 4;                   // the CTA's output
+  static_assert(kWarps * kArRows * 128 * 4 <= kRing, "the warps' outputs take the ring's place");
+  static constexpr int smem(int z_tokens, int G) { return 1024 + kRing + kPart + z_tokens * G * 4; }
+};
+
+template <int kWarps>
+__global__ void __launch_bounds__(UnitsShape<kWarps>::kThreads) attend_units_kernel(const __grid_constant__ AttendParams p) {
+  using Sh = UnitsShape<kWarps>;
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full_b[kWarps][kAuStages];
+  __shared__ float wm[kWarps][kArRows], wl[kWarps][kArRows];
+  __shared__ float2 part_ml[kArRows];  // this CTA's (m, l), read by the cluster
+  __shared__ float lse2[8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  uint8_t* base = align1024(smem);
+  uint8_t* ring = base + warp * kAuStages * kArStageBytes;
+  float* merge = reinterpret_cast<float*>(base);
+  float* part_o = reinterpret_cast<float*>(base + Sh::kRing);
+  float* zs = part_o + kArRows * 128;  // [G][tokens of this CTA]
+  const int units = p.Hkv * p.row_tiles, b = blockIdx.y / units, unit = blockIdx.y % units;
+  const int g = unit % p.Hkv, rt = unit / p.Hkv;
+  if (lane == 0)
+    for (int s = 0; s < kAuStages; ++s) mbar_init(&full_b[warp][s], 1);
+  if (tid == 0) fence_mbar_init();
+  __syncwarp();
+  const int n = checked_len(p, b), nodes = checked_nodes(p, b);
+  const int live = min(kArRows, nodes * p.G - rt * kArRows);
+  if (live <= 0) return;  // the same in every CTA of the cluster
+  const int nc = (n + kArKeys - 1) / kArKeys, chunks = nc + (p.mask ? (nodes + kArKeys - 1) / kArKeys : 0);
+  const int lo = (int)((long long)chunks * rank / C), hi = (int)((long long)chunks * (rank + 1) / C);
+  int ids = -1, ids_at = lo + warp;
+  auto load_ids = [&](int c) {
+    ids_at = c;
+    const int mine = c + lane * kWarps;
+    ids = mine < min(hi, nc) ? p.page_table[(size_t)b * p.max_pages + ((mine * kArKeys) >> p.pshift)] : -1;
+  };
+  load_ids(lo + warp);
+  int fetched = 0, used = 0;
+  bool dead = false;
+  uint32_t skipped = 0;
+  auto fetch = [&](int c) {
+    const int s = fetched % kAuStages;
+    bool ok = true;
+    int row;
+    if (c < nc) {
+      if (c >= ids_at + 32 * kWarps) load_ids(c);
+      const int phys = __shfl_sync(0xffffffffu, ids, (c - ids_at) / kWarps);
+      ok = phys >= 0 && phys < p.num_phys;
+      row = (phys * p.Hkv + g) * p.P + ((c * kArKeys) & (p.P - 1));
+    } else {
+      row = (b * p.Hkv + g) * p.T + (c - nc) * kArKeys;
+    }
+    if (ok) {
+      skipped &= ~(1u << s);
+      if (lane == 0) {
+        const CUtensorMap* mk = c < nc ? &p.tmk : &p.tmkt;
+        const CUtensorMap* mv = c < nc ? &p.tmv : &p.tmvt;
+        uint8_t* st = ring + s * kArStageBytes;
+        uint64_t* bar = &full_b[warp][s];
+        mbar_arrive_expect_tx(bar, kArStageBytes);
+        tma_load_2d(st, mk, 0, row, bar);
+        tma_load_2d(st + 2048, mk, 64, row, bar);
+        tma_load_2d(st + 4096, mv, 0, row, bar);
+        tma_load_2d(st + 6144, mv, 64, row, bar);
+      }
+    } else {
+      skipped |= 1u << s;
+      if (lane == 0) {
+        flag_error(p.err, RKV_DEVERR_PAGE_ID);
+        mbar_arrive(&full_b[warp][s]);
+      }
+    }
+    ++fetched;
+  };
+  int fc = lo + warp;
+  for (int s = 0; s < kAuStages && fc < hi; ++s, fc += kWarps) fetch(fc);
+  RowTile tile;
+  tile.start(p, b, g, rt, n, nodes);
+  const int tokens = (hi - lo) * kArKeys;
+  for (int c = lo + warp; c < hi; c += kWarps) {
+    const int s = used % kAuStages;
+    const bool late = !dead && !mbar_wait(&full_b[warp][s], (uint32_t)((used / kAuStages) & 1));
+    if (__any_sync(0xffffffffu, late)) {
+      if (lane == 0) flag_error(p.err, RKV_DEVERR_TIMEOUT);
+      dead = true;
+    }
+    if (!dead && !((skipped >> s) & 1u)) {
+      tile.step(p, ring + s * kArStageBytes, c, [&](float2 z, int col) {
+        if (p.acc && tile.r0 < p.G) *reinterpret_cast<float2*>(zs + tile.r0 * tokens + (c - lo) * kArKeys + col) = z;
+      });
+    } else if (p.acc) {
+      for (int i = lane; i < p.G * kArKeys; i += 32)
+        zs[(i / kArKeys) * tokens + (c - lo) * kArKeys + i % kArKeys] = -INFINITY;
+    }
+    ++used;
+    __syncwarp();
+    if (fc < hi && !dead) {
+      fetch(fc);
+      fc += kWarps;
+    }
+  }
+  if (dead)
+    for (int i = used; i < fetched; ++i) mbar_wait(&full_b[warp][i % kAuStages], (uint32_t)((i / kAuStages) & 1));
+  tile.finish();
+  const int qr = lane >> 2, qc = (lane & 3) * 2;
+  if ((lane & 3) == 0) {
+    wm[warp][qr] = tile.m0;
+    wl[warp][qr] = tile.l0;
+    wm[warp][qr + 8] = tile.m1;
+    wl[warp][qr + 8] = tile.l1;
+  }
+  __syncthreads();  // every warp is done with its ring: the outputs take its place
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+    if (half * 8 < live) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        *reinterpret_cast<float2*>(merge + (warp * kArRows + half * 8 + qr) * 128 + j * 8 + qc) =
+            make_float2(tile.o[j][half * 2], tile.o[j][half * 2 + 1]);
+    }
+  __syncthreads();
+  for (int i = tid; i < live * 64; i += Sh::kThreads) {
+    const int row = i >> 6, d = (i & 63) * 2;
+    float M = kNoMax, L = 0.f, ax = 0.f, ay = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w][row]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = ex2_approx(wm[w][row] - M);
+      const float2 v = *reinterpret_cast<const float2*>(merge + (w * kArRows + row) * 128 + d);
+      L += wl[w][row] * f;
+      ax += v.x * f;
+      ay += v.y * f;
+    }
+    *reinterpret_cast<float2*>(part_o + row * 128 + d) = make_float2(ax, ay);
+    if (d == 0) part_ml[row] = make_float2(M, L);
+  }
+  cluster.sync();  // every CTA's part is in place
+  // rows of the output in turn over the cluster: thread = (row, two channels), eight parts'
+  // reads in flight
+  for (int i = tid; i < live * 64; i += Sh::kThreads) {
+    const int row = i >> 6, d = (i & 63) * 2;
+    if (row % C != rank) continue;
+    float2 ml[8], v[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < C) {
+        ml[c] = *cluster.map_shared_rank(&part_ml[row], c);
+        v[c] = *cluster.map_shared_rank(reinterpret_cast<float2*>(part_o + row * 128 + d), c);
+      }
+    float M = kNoMax, L = 0.f, ax = 0.f, ay = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < C) M = fmaxf(M, ml[c].x);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < C) {
+        const float f = ex2_approx(ml[c].x - M);
+        L += ml[c].y * f;
+        ax += v[c].x * f;
+        ay += v[c].y * f;
+      }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const size_t orow = out_row(p, b, g, rt * kArRows + row);
+    *reinterpret_cast<uint32_t*>(p.out + orow * 128 + d) = pack_bf16x2(ax * inv, ay * inv);
+    if (d == 0 && p.lse) p.lse[orow] = lse_of(M, L);
+  }
+  if (p.acc) {  // one token: its rows are the group's heads
+    {
+      for (int h = warp; h < p.G; h += kWarps) {
+        float2 ml = lane < C ? *cluster.map_shared_rank(&part_ml[h], lane) : make_float2(kNoMax, 0.f);
+        float M = ml.x;
+#pragma unroll
+        for (int o = 4; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float L = ml.y * ex2_approx(ml.x - M);
+#pragma unroll
+        for (int o = 4; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (lane == 0) lse2[h] = L > 0.f ? M + log2f(L) : INFINITY;  // nothing read: weighs nothing
+      }
+    }
+    __syncthreads();
+    float* a = p.acc + ((size_t)b * p.Hkv + g) * p.acc_stride + (size_t)lo * kArKeys;
+    for (int t = tid; t < tokens; t += Sh::kThreads) {
+      if (lo * kArKeys + t >= n) break;
+      float w = 0.f;
+      for (int h = 0; h < p.G; ++h) w += ex2_approx(zs[h * tokens + t] - lse2[h]);
+      a[t] += w;
+    }
+  }
+  cluster.sync();  // no CTA leaves while another still reads its shared memory
 }
 
 // Where the parts of a split unit lie: CTA c's at slot 2 c, but the first CTA's at 2 c + 1
@@ -1102,8 +1339,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
 // How many rows of a unit share a pass over the cache: 16 (mma.sync), 128 or 256 (tcgen05).
 int tile_rows(int T, int G) { return T * G <= kArRows ? kArRows : (T * G <= 128 ? 128 : 256); }
 
-cudaError_t fill_params(const AttendArgs& a, AttendParams& p) {
-  const int rows = tile_rows(a.T, a.Hq / a.cache.Hkv);
+cudaError_t fill_params(const AttendArgs& a, AttendParams& p, int rows) {
   const uint32_t box = rows == kArRows ? kArKeys : (uint32_t)a.cache.page_size;
   const uint32_t tbox = rows == kArRows ? kArKeys : kAtKeys;
   const rkv_cache& c = a.cache;
@@ -1141,6 +1377,11 @@ cudaError_t fill_params(const AttendArgs& a, AttendParams& p) {
   p.max_pages = c.max_pages;
   p.num_phys = c.num_phys_pages;
   p.zstride = c.max_pages * c.page_size;
+  p.z = nullptr;
+  p.row_ml = nullptr;
+  p.part_o = nullptr;
+  p.part_ml = nullptr;
+  p.row_tiles = 0;
   p.N = num_sms();
   p.scale_log2 = a.scale * 1.4426950408889634f;
   return cudaSuccess;
@@ -1155,12 +1396,60 @@ size_t attend_ws_bytes(int B, int Hq, int Hkv, int T, int max_pages, int page_si
   return n;
 }
 
+// Whether attend_units takes the call, with clusters of how many CTAs (0: it does not).
+// The host knows the caches' capacity, not their lengths.  One wave of clusters (a CTA an
+// SM; with four warps three) against the line split over all SMs plus the join, one token,
+// 8 KV heads, us: 1 x 515 tokens 7.3 (C = 8) against 11.3, 1 x 2563 10.0 against 12.1, 1 x
+// 8192 16.5 against 15.1; 4 x 4096 16.4 (C = 4) against 20.5; 16 x 600 13.1 (C = 2, four
+// warps) against 16.8, 16 x 4000 57.4 against 55.5; 64 x 300 25.4 (C = 1) against 32.4, 64
+// x 2000 110 against 99.  Two row tiles, 2 KV heads, 515 tokens: 9.4 against 11.3 on the
+// tensor-core tiles; 32 units of four row tiles no longer gain.
+int units_cluster(const AttendArgs& a) {
+  const rkv_cache& c = a.cache;
+  const int tiles = (a.T * (a.Hq / c.Hkv) + kArRows - 1) / kArRows, cap = c.max_pages * c.page_size;
+  const long long units = (long long)c.B * c.Hkv * tiles;
+  if (units > 65535 || (tiles > 1 && units > 8)) return 0;
+  const int C = units <= 9 ? 8 : (units <= 36 ? 4 : (units <= 300 ? 2 : 1));
+  return cap <= C * (C == 8 ? 1024 : (C == 4 ? 1536 : 512)) ? C : 0;
+}
+
+cudaError_t launch_units(const AttendArgs& a, AttendParams& p, int C, cudaStream_t s) {
+  const rkv_cache& c = a.cache;
+  p.row_tiles = (a.T * p.G + kArRows - 1) / kArRows;
+  const int cap = (c.max_pages * c.page_size) / kArKeys + (a.mask ? (a.T + kArKeys - 1) / kArKeys : 0);
+  const int z_tokens = a.acc ? (cap + C - 1) / C * kArKeys : 0;
+  const bool four = C <= 2;
+  const int smem = four ? UnitsShape<4>::smem(z_tokens, p.G) : UnitsShape<8>::smem(z_tokens, p.G);
+  void (*kernel)(AttendParams) = four ? attend_units_kernel<4> : attend_units_kernel<8>;
+  static SmemOptIn opt[2];
+  cudaError_t e = opt[four].raise(reinterpret_cast<const void*>(kernel), UnitsShape<8>::smem(kMaxUnitTokens, 8));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C, (unsigned)(c.B * c.Hkv * p.row_tiles));
+  cfg.blockDim = dim3(four ? UnitsShape<4>::kThreads : UnitsShape<8>::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  launch_begin(K_ATTEND_UNITS, s);
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  launch_end(K_ATTEND_UNITS, s);
+  return e;
+}
+
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
   AttendParams p;
   const rkv_cache& c = a.cache;
-  cudaError_t e = fill_params(a, p);
+  const int C = units_cluster(a);
+  cudaError_t e = fill_params(a, p, C > 0 ? kArRows : tile_rows(a.T, a.Hq / c.Hkv));
   if (e != cudaSuccess) return e;
   if (p.N > kMaxSms) p.N = kMaxSms;
+  if (C > 0) return launch_units(a, p, C, s);
   const int tile = tile_rows(a.T, p.G);
   const size_t rows = (size_t)2 * kMaxSms * tile;
   uint8_t* w = static_cast<uint8_t*>(a.ws);

@@ -37,6 +37,7 @@ enum KernelKind {
   K_SPARQ_KEYS_SYNC,
   K_ATTEND_ROWS,
   K_ATTEND_TILES,
+  K_ATTEND_UNITS,
   K_ATTEND_COMBINE,
   K_ATTEND_WEIGH,
   K_TREE_COMMIT,
