@@ -793,6 +793,10 @@ constexpr int kAtSoftRegs = 208, kAtIssueRegs = 88;
 static_assert(256 * kAtSoftRegs + 128 * kAtIssueRegs == 384 * 168, "the split must be what the block was launched with");
 constexpr int kAtEntry = 128 * 256;
 constexpr float kAtSlack = 8.f;
+// The tiled kernel's table: only the line's offsets; a run's lengths are read again.
+struct SlimRun : FlatRun {
+  int n, t;
+};
 template <bool kWide>
 struct TileShape {
   static constexpr int kRows = kWide ? 256 : 128;
@@ -809,16 +813,14 @@ struct TileShape {
     uint32_t sgroups[2];        // the same for the tile whose logits a slot holds
     uint32_t tmem_base;
     int abort_flag;
+    SlimRun first;  // the share's first run, worked out once
+    long long x0, x1;
     float2 ml_s[kWide ? 1 : 2][kWide ? 1 : 128];
   };
   static constexpr int kSmem = sizeof(Shared);
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
-// The tiled kernel's table: only the line's offsets; a run's lengths are read again.
-struct SlimRun : FlatRun {
-  int n, t;
-};
 template <int kRows, int kKeys>
 __device__ __forceinline__ int pieces_of(const AttendParams& p, int n, int t) {
   (void)p;
@@ -877,6 +879,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
     abort_flag = 0;
     fence_mbar_init();
   }
+  if (tid == 32) {
+    prefetch_map(&p.tmk);
+    prefetch_map(&p.tmv);
+  }
   if (warp == 9) {
     tmem_alloc(&sh.tmem_base, 512);
     tmem_relinquish();
@@ -889,10 +895,21 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
   tc_fence_after();
   grid_launch_dependents();
   const uint32_t tmem = sh.tmem_base;
-  const long long total = sh.base[p.B];
-  const int N = flat_ctas(total, p.N);
-  const bool works = (int)blockIdx.x < N;
-  const long long x0 = works ? flat_first(total, blockIdx.x, N) : 0, x1 = works ? flat_first(total, blockIdx.x + 1, N) : 0;
+  if (tid == 0) {  // one thread: twelve warps dividing at once took twice as long
+    const long long total = sh.base[p.B];
+    const int N = flat_ctas(total, p.N);
+    const bool works = (int)blockIdx.x < N;
+    sh.x0 = works ? flat_first(total, blockIdx.x, N) : 0;
+    sh.x1 = works ? flat_first(total, blockIdx.x + 1, N) : 0;
+    slim_run<R, kAtKeys>(p, sh.base, sh.x0, sh.x0, sh.x1, sh.first);
+  }
+  __syncthreads();
+  const long long x0 = sh.x0, x1 = sh.x1;
+  auto next_run = [&](long long x, SlimRun& r) {
+    if (x != x0 || x >= x1) return slim_run<R, kAtKeys>(p, sh.base, x, x0, x1, r);
+    r = sh.first;
+    return true;
+  };
   auto give_up = [&]() {
     flag_error(p.err, RKV_DEVERR_TIMEOUT);
     abort_flag = 1;
@@ -915,7 +932,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
       }
       return true;
     };
-    for (long long x = x0; ok && slim_run<R, kAtKeys>(p, sh.base, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+    for (long long x = x0; ok && next_run(x, r); x = r.x + (r.hi - r.lo)) {
       const int b = r.b, g = r.unit % p.Hkv, rt = r.unit / p.Hkv;
       const int n = r.n, nodes = r.t, rows = nodes * p.G, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
       const bool idle = kWide && slot == 1 && rows - rt * R <= 128;
@@ -1128,7 +1145,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
     const int pages = kAtKeys >> p.pshift, box = p.P * 128;  // pages of a tile, bytes of a box
     int before = 0;                                          // entries of the runs before
     bool ok = true;
-    for (long long x = x0; ok && slim_run<R, kAtKeys>(p, sh.base, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+    for (long long x = x0; ok && next_run(x, r); x = r.x + (r.hi - r.lo)) {
       const int b = r.b, g = r.unit % p.Hkv, n = r.n, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
       // lane j: page id of the tile's page j, -1: none; loaded a tile ahead and judged only
       // when it is used, so that the load's latency stays off the ring
@@ -1220,7 +1237,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
       if (lead) mbar_arrive(&s_b[slot]);
       __syncwarp();
     };
+    // O += P V once the slot's weights are there (handed over in two halves, the issuing
+    // warp waited twice and the other slot with it: 480 us against 410 for 64 nodes, 8 x 64K)
     auto mma_o = [&](int slot, int e, bool first, bool last, bool release) {
+      if (!(ok = wait(&p_b[slot], seen_p[slot]++))) return;
       tc_fence_after();
       const uint32_t d = tmem + slot * 256 + 128, pa = tmem + slot * 256, va = vlo + e * (kAtEntry >> 4);
 #pragma unroll
@@ -1229,7 +1249,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
       tc_commit_if(lead && release, &empty_b[e]);
       tc_commit_if(lead && last, &o_b[slot]);
     };
-    for (long long x = x0; ok && slim_run<R, kAtKeys>(p, sh.base, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+    for (long long x = x0; ok && next_run(x, r); x = r.x + (r.hi - r.lo)) {
       const int n = r.n, nodes = r.t, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
       const bool two = kWide && nodes * p.G - (r.unit / p.Hkv) * R > 128;  // slot 1 has rows
       // keys of a tile that may hold anything (behind the end, on a bad page) have weight 0,
@@ -1266,8 +1286,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
           if (!ok) break;
           clean_v(r.lo + i, ev, gr);
           const bool last = i + 1 == nt;
-          if (!(ok = wait(&p_b[0], seen_p[0]++))) break;
           mma_o(0, ev, i == 0, last, !two);
+          if (!ok) break;
           if (kWide) tc_commit_if(lead && last && !two, &o_b[1]);  // keeps an idle slot in step
           int en = 0;
           if (!last) {
@@ -1277,8 +1297,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
             mma_s(0, en, !two);
           }
           if (two) {
-            if (!(ok = wait(&p_b[1], seen_p[1]++))) break;
             mma_o(1, ev, i == 0, last, true);
+            if (!ok) break;
             if (!last) mma_s(1, en, true);
           }
         }
@@ -1305,8 +1325,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
           if (!ok) break;
           clean_v(r.lo + i, ev, gr[slot]);
           if (i + 1 < nt) gr[slot ^ 1] = gn;
-          if (!(ok = wait(&p_b[slot], seen_p[slot]++))) break;
           mma_o(slot, ev, i < 2, i + 2 >= nt, true);
+          if (!ok) break;
         }
       }
     }

@@ -165,6 +165,11 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* map, int x, i
       : "memory");
 }
 
+// Fetches a tensor map's descriptor ahead of the first copy that uses it.
+__device__ __forceinline__ void prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // The same, called by a whole converged warp with equal operands and issued where `issue`
 // holds: the operands then go through uniform registers once.  (With operands that differ
 // by lane the compiler serialises the lanes, about 100 clocks a box.)

@@ -27,21 +27,23 @@ __device__ __forceinline__ void flat_scan(long long* base, int B, Size size) {
   const int lane = threadIdx.x;
   if (lane < 32) {
     const int each = (B + 31) / 32;
-    long long s = 0;
+    long long s = 0, only = 0;
     for (int j = 0; j < each; ++j)
-      if (lane * each + j < B) s += size(lane * each + j);
+      if (lane * each + j < B) s += (only = size(lane * each + j));
     long long incl = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+      if (o < B) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
     }
     long long at = incl - s;
     for (int j = 0; j < each; ++j) {
       const int b = lane * each + j;
       if (b < B) {
         base[b] = at;
-        at += size(b);
+        at += each == 1 ? only : size(b);
         if (b == B - 1) base[B] = at;
       }
     }
