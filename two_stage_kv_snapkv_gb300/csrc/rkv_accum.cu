@@ -18,6 +18,7 @@ namespace {
 // read, 4 KB for a 16-key chunk, and every position has one writer: no atomics, the
 // same sums in the same order every time.
 constexpr int kRwKeys = 16;
+constexpr int kRwPad = 16;  // what a run costs, in chunks
 constexpr int kRwStageBytes = 4096;
 constexpr int kRwBlock = 64;  // query rows staged at a time, at most
 constexpr int kRwSmem = 1024 + 48 * kRwStageBytes + kRwBlock * 256;
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(RowsShape<kR16>::kWarps * 32, 1)
     for (int s = 0; s < kRwStages; ++s) mbar_init(&full_b[warp][s], 1);
   if (tid == 0) fence_mbar_init();
   flat_build(
-      ft, p.B, [&](int b) { return rows_cache_len(p, b); }, [&](int b) { return rows_of(p, b, rows_cache_len(p, b)); },
+      ft, p.B, kRwPad, [&](int b) { return rows_cache_len(p, b); }, [&](int b) { return rows_of(p, b, rows_cache_len(p, b)); },
       [&](int n, int m) { return m > 0 ? (n + kRwKeys - 1) / kRwKeys : 0; }, [&](int) { return p.Hkv; });
   const long long total = ft.base[p.B];
   const int N = flat_ctas(total, p.N);
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(RowsShape<kR16>::kWarps * 32, 1)
   bool dead = false;
   uint32_t skipped = 0;
   FlatRun r;
-  for (long long x = x0; flat_run(ft, p.B, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+  for (long long x = x0; flat_run(ft, p.B, x, x0, x1, r); x = r.next) {
     const int b = r.b, g = r.unit, n = ft.n[b], m = ft.t[b], rows = m * p.G;
     int ids = -1, ids_at = 0;  // page ids of this warp's chunks ids_at + 8 lane
     auto load_ids = [&](int c) {

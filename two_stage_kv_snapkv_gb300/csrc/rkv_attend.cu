@@ -31,6 +31,7 @@ constexpr int kArStageBytes = 4 * 2048;           // K, V: two 16 x 64 boxes eac
 constexpr int kArMergeRows = 4;                   // rows of every warp that meet at a time
 constexpr int kArMergeFloats = kArWarps * kArMergeRows * 128;
 constexpr int kArSmem = 1024 + kArWarps * kArStages * kArStageBytes + kArMergeFloats * 4;
+constexpr int kArPad = 16, kAtPad = 4;           // what a run costs, in chunks of 16 and tiles of 128 keys
 constexpr float kNoMax = -1e30f;                  // running maximum of a row that saw nothing
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWeighTokens = 2048;                // tokens of a weighing block, eight a thread
@@ -74,10 +75,14 @@ __device__ __forceinline__ int checked_nodes(const AttendParams& p, int b) {
   return t;
 }
 
+// Empty pieces of a unit: a run's start and end in chunks and tiles.
+template <int kKeys>
+__device__ __forceinline__ constexpr int pad_of() { return kKeys == kArKeys ? kArPad : kAtPad; }
+
 template <int kRows, int kKeys>
 __device__ __forceinline__ void build_table(const AttendParams& p, FlatTable& ft) {
   flat_build(
-      ft, p.B, [&](int b) { return checked_len(p, b); }, [&](int b) { return checked_nodes(p, b); },
+      ft, p.B, pad_of<kKeys>(), [&](int b) { return checked_len(p, b); }, [&](int b) { return checked_nodes(p, b); },
       [&](int n, int t) { return (n + kKeys - 1) / kKeys + (p.mask ? (t + kKeys - 1) / kKeys : 0); },
       [&](int t) { return p.Hkv * ((t * p.G + kRows - 1) / kRows); });
 }
@@ -253,7 +258,7 @@ __global__ void __launch_bounds__(kArThreads, 1) attend_rows_kernel(const __grid
   int fc = fr.lo + warp;
   auto settle = [&]() {  // the next chunk to fetch, past runs in which this warp has none left
     while (more && fc >= fr.hi) {
-      fx = fr.x + (fr.hi - fr.lo);
+      fx = fr.next;
       more = flat_run(ft, p.B, fx, x0, x1, fr);
       if (more) fc = fr.lo + warp;
     }
@@ -317,7 +322,7 @@ __global__ void __launch_bounds__(kArThreads, 1) attend_rows_kernel(const __grid
   const int qr = lane >> 2, qc = (lane & 3) * 2;  // fragment row and column pair
   FlatRun cr;
   RowTile tile;
-  for (long long x = x0; flat_run(ft, p.B, x, x0, x1, cr); x = cr.x + (cr.hi - cr.lo)) {
+  for (long long x = x0; flat_run(ft, p.B, x, x0, x1, cr); x = cr.next) {
     const int b = cr.b, g = cr.unit % p.Hkv, rt = cr.unit / p.Hkv;
     tile.start(p, b, g, rt, ft.n[b], ft.t[b]);
     const int rows = tile.rows;
@@ -609,8 +614,8 @@ __global__ void __launch_bounds__(UnitsShape<kWarps>::kThreads) attend_units_ker
 // when its share began before the unit.
 struct PartSlots {
   int c0, c1, late;
-  __device__ __forceinline__ PartSlots(long long ux, int per, long long total, int N)
-      : c0(flat_cta(ux, total, N)), c1(flat_cta(ux + per - 1, total, N)), late(flat_first(total, c0, N) < ux) {}
+  __device__ __forceinline__ PartSlots(long long ux, int per, int pad, long long total, int N)
+      : c0(flat_cta(ux + pad, total, N)), c1(flat_cta(ux + per - 1, total, N)), late(flat_first(total, c0, N) < ux) {}
   __device__ __forceinline__ size_t operator[](int c) const { return 2 * (size_t)c + (c == c0 ? late : 0); }
 };
 
@@ -650,7 +655,7 @@ __device__ __forceinline__ void combine_row(const AttendParams& p, const FlatTab
     if (lane == 0 && p.lse) p.lse[orow] = -INFINITY;
     return;
   }
-  const PartSlots ps(ft.base[b] + (long long)(rt * p.Hkv + g) * per, per, total, N);
+  const PartSlots ps(ft.base[b] + (long long)(rt * p.Hkv + g) * per, per, ft.pad, total, N);
   if (ps.c0 == ps.c1) return;  // final already
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = kNoMax, L = 0.f;
@@ -728,7 +733,7 @@ __global__ void __launch_bounds__(256, 4) attend_weigh_kernel(const __grid_const
     const int g = (int)((x - wbase[b]) / blocks), blk = (int)((x - wbase[b]) % blocks);
     const size_t unit = (size_t)b * p.Hkv + g;
     if (warp < p.G) {
-      const PartSlots ps(ft.base[b] + (long long)g * ft.per[b], ft.per[b], total, N);
+      const PartSlots ps(ft.base[b] + (long long)g * ft.per[b], ft.per[b], ft.pad, total, N);
       const float2 ml = ps.c0 == ps.c1 ? p.row_ml[unit * p.G + warp] : join_ml<kArRows>(p, ps, warp, lane);
       if (lane == 0) lse2[warp] = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;  // nothing read: weighs nothing
     }
@@ -814,6 +819,7 @@ struct TileShape {
     uint32_t tmem_base;
     int abort_flag;
     SlimRun first;  // the share's first run, worked out once
+    bool any;       // there is one
     long long x0, x1;
     float2 ml_s[kWide ? 1 : 2][kWide ? 1 : 128];
   };
@@ -821,32 +827,32 @@ struct TileShape {
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
+// Pieces of a unit, the empty ones included.
 template <int kRows, int kKeys>
 __device__ __forceinline__ int pieces_of(const AttendParams& p, int n, int t) {
-  (void)p;
-  return (n + kKeys - 1) / kKeys + (p.mask ? (t + kKeys - 1) / kKeys : 0);
+  const int real = (n + kKeys - 1) / kKeys + (p.mask ? (t + kKeys - 1) / kKeys : 0);
+  return real > 0 ? real + pad_of<kKeys>() : 0;
 }
 template <int kRows, int kKeys>
 __device__ __forceinline__ bool slim_run(const AttendParams& p, const long long* base, long long x, long long x0,
                                          long long x1, SlimRun& r) {
-  if (x >= x1) return false;
-  int lo = 0, hi = p.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (base[mid] <= x) lo = mid; else hi = mid - 1;
+  for (; x < x1; x = r.next) {
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (base[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    r.b = lo;
+    r.n = checked_len(p, lo);
+    r.t = checked_nodes(p, lo);
+    const int per = pieces_of<kRows, kKeys>(p, r.n, r.t);
+    const long long off = x - base[lo];
+    r.unit = off < (1LL << 31) ? (int)((uint32_t)off / (uint32_t)per) : (int)(off / per);
+    r.first = x == x0;
+    r.x = x;
+    if (flat_part(r, (int)(off - (long long)r.unit * per), x1 - x, per, pad_of<kKeys>())) return true;
   }
-  r.b = lo;
-  r.n = checked_len(p, lo);
-  r.t = checked_nodes(p, lo);
-  const int per = pieces_of<kRows, kKeys>(p, r.n, r.t);
-  const long long off = x - base[lo];
-  r.unit = off < (1LL << 31) ? (int)((uint32_t)off / (uint32_t)per) : (int)(off / per);
-  r.lo = (int)(off - (long long)r.unit * per);
-  r.hi = (int)min((long long)per, r.lo + (x1 - x));
-  r.whole = r.lo == 0 && r.hi == per;
-  r.first = x == x0;
-  r.x = x;
-  return true;
+  return false;
 }
 
 template <bool kWide>
@@ -901,14 +907,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
     const bool works = (int)blockIdx.x < N;
     sh.x0 = works ? flat_first(total, blockIdx.x, N) : 0;
     sh.x1 = works ? flat_first(total, blockIdx.x + 1, N) : 0;
-    slim_run<R, kAtKeys>(p, sh.base, sh.x0, sh.x0, sh.x1, sh.first);
+    sh.any = slim_run<R, kAtKeys>(p, sh.base, sh.x0, sh.x0, sh.x1, sh.first);
   }
   __syncthreads();
   const long long x0 = sh.x0, x1 = sh.x1;
   auto next_run = [&](long long x, SlimRun& r) {
-    if (x != x0 || x >= x1) return slim_run<R, kAtKeys>(p, sh.base, x, x0, x1, r);
+    if (x != x0) return slim_run<R, kAtKeys>(p, sh.base, x, x0, x1, r);
     r = sh.first;
-    return true;
+    return sh.any;
   };
   auto give_up = [&]() {
     flag_error(p.err, RKV_DEVERR_TIMEOUT);
@@ -932,7 +938,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
       }
       return true;
     };
-    for (long long x = x0; ok && next_run(x, r); x = r.x + (r.hi - r.lo)) {
+    for (long long x = x0; ok && next_run(x, r); x = r.next) {
       const int b = r.b, g = r.unit % p.Hkv, rt = r.unit / p.Hkv;
       const int n = r.n, nodes = r.t, rows = nodes * p.G, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
       const bool idle = kWide && slot == 1 && rows - rt * R <= 128;
@@ -1145,7 +1151,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
     const int pages = kAtKeys >> p.pshift, box = p.P * 128;  // pages of a tile, bytes of a box
     int before = 0;                                          // entries of the runs before
     bool ok = true;
-    for (long long x = x0; ok && next_run(x, r); x = r.x + (r.hi - r.lo)) {
+    for (long long x = x0; ok && next_run(x, r); x = r.next) {
       const int b = r.b, g = r.unit % p.Hkv, n = r.n, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
       // lane j: page id of the tile's page j, -1: none; loaded a tile ahead and judged only
       // when it is used, so that the load's latency stays off the ring
@@ -1249,7 +1255,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
       tc_commit_if(lead && release, &empty_b[e]);
       tc_commit_if(lead && last, &o_b[slot]);
     };
-    for (long long x = x0; ok && next_run(x, r); x = r.x + (r.hi - r.lo)) {
+    for (long long x = x0; ok && next_run(x, r); x = r.next) {
       const int n = r.n, nodes = r.t, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
       const bool two = kWide && nodes * p.G - (r.unit / p.Hkv) * R > 128;  // slot 1 has rows
       // keys of a tile that may hold anything (behind the end, on a bad page) have weight 0,

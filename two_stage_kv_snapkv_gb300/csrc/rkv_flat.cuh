@@ -4,8 +4,9 @@
 // of its `units(b)` units (KV heads, row tiles).  All units' pieces in order (b major)
 // form one line of `total` pieces and CTA i of N takes [i total / N, (i + 1) total / N):
 // the grid is sized without the lengths, and no CTA carries more than one piece above
-// the mean.  Each CTA rebuilds the table (one load a sequence and a warp scan, measured
-// well under a microsecond).
+// the mean.  A unit's first `pad` pieces are empty: they stand for what starting and ending
+// a run costs, so that a CTA with many short units gets fewer pieces.  Each CTA rebuilds
+// the table (one load a sequence and a warp scan, about a microsecond).
 #pragma once
 
 #include "rkv_device.cuh"
@@ -16,8 +17,9 @@ struct FlatTable {
   long long base[RKV_MAX_BATCH + 1];  // pieces before sequence b
   int n[RKV_MAX_BATCH];               // tokens of sequence b (0 when its length is not usable)
   int t[RKV_MAX_BATCH];               // query rows (nodes) of sequence b
-  int per[RKV_MAX_BATCH];             // pieces of each of its units
+  int per[RKV_MAX_BATCH];             // pieces of each of its units, the empty ones included
   int units[RKV_MAX_BATCH];           // its units
+  int pad;                            // empty pieces of a unit
 };
 
 // base[b] = sum of size(0 .. b - 1), base[B] the total: the first warp's scan; ends with a
@@ -51,15 +53,18 @@ __device__ __forceinline__ void flat_scan(long long* base, int B, Size size) {
   __syncthreads();
 }
 
-// len(b) -> tokens, rows(b) -> nodes, per(n, t) -> pieces a unit, units(t) -> units.
+// len(b) -> tokens, rows(b) -> nodes, per(n, t) -> pieces a unit (without the empty ones),
+// units(t) -> units.
 // Called by every thread of the block (at least 32); ends with a block barrier.
 template <class Len, class Rows, class Per, class Units>
-__device__ __forceinline__ void flat_build(FlatTable& ft, int B, Len len, Rows rows, Per per, Units units) {
+__device__ __forceinline__ void flat_build(FlatTable& ft, int B, int pad, Len len, Rows rows, Per per, Units units) {
   const int tid = threadIdx.x;
+  if (tid == 0) ft.pad = pad;
   for (int b = tid; b < B; b += blockDim.x) {
     ft.n[b] = len(b);
     ft.t[b] = rows(b);
-    ft.per[b] = per(ft.n[b], ft.t[b]);
+    const int real = per(ft.n[b], ft.t[b]);
+    ft.per[b] = real > 0 ? real + pad : 0;
     ft.units[b] = units(ft.t[b]);
   }
   __syncthreads();
@@ -93,23 +98,31 @@ __device__ __forceinline__ int flat_seq(const FlatTable& ft, int B, long long x)
 // Walks the pieces of a share a run at a time: a run is the share's part of one unit.
 struct FlatRun {
   int b, unit;           // sequence, unit inside it
-  int lo, hi;            // the run's pieces of the unit
+  int lo, hi;            // the run's pieces of the unit, without the empty ones; lo < hi
   int whole;             // the run is the whole unit
   int first;             // the run starts the share
-  long long x;           // the run's first piece
+  long long x, next;     // the run's first piece on the line, and the one behind its last
 };
+// Part [off, off + room) of a unit of `per` pieces as a run; false: only empty pieces.
+__device__ __forceinline__ bool flat_part(FlatRun& r, int off, long long room, int per, int pad) {
+  const int end = (int)min((long long)per, off + room);
+  r.next = r.x + (end - off);
+  r.lo = max(off - pad, 0);
+  r.hi = end - pad;
+  r.whole = r.lo == 0 && end == per;
+  return r.hi > r.lo;
+}
 __device__ __forceinline__ bool flat_run(const FlatTable& ft, int B, long long x, long long x0, long long x1, FlatRun& r) {
-  if (x >= x1) return false;
-  r.b = flat_seq(ft, B, x);
-  const int per = ft.per[r.b];
-  const long long off = x - ft.base[r.b];
-  r.unit = off < (1LL << 31) ? (int)((uint32_t)off / (uint32_t)per) : (int)(off / per);
-  r.lo = (int)(off - (long long)r.unit * per);
-  r.hi = (int)min((long long)per, r.lo + (x1 - x));
-  r.whole = r.lo == 0 && r.hi == per;
-  r.first = x == x0;
-  r.x = x;
-  return true;
+  for (; x < x1; x = r.next) {
+    r.b = flat_seq(ft, B, x);
+    const int per = ft.per[r.b];
+    const long long off = x - ft.base[r.b];
+    r.unit = off < (1LL << 31) ? (int)((uint32_t)off / (uint32_t)per) : (int)(off / per);
+    r.first = x == x0;
+    r.x = x;
+    if (flat_part(r, (int)(off - (long long)r.unit * per), x1 - x, per, ft.pad)) return true;
+  }
+  return false;
 }
 
 }  // namespace rkv
