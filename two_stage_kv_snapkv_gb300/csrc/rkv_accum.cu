@@ -309,8 +309,9 @@ struct TilesRun {
   int whole, first;
 };
 
-__device__ __forceinline__ bool tiles_run(const RowsParams& p, const TilesTable& tt, int nq, long long x, long long x0,
-                                          long long x1, TilesRun& r) {
+// The run that holds piece x, found from nothing (two 64-bit divisions and two searches).
+__device__ __forceinline__ bool tiles_find(const RowsParams& p, const TilesTable& tt, int nq, long long x, long long x0,
+                                           long long x1, TilesRun& r) {
   if (x >= x1) return false;
   int lo = 0, hi = p.B - 1;
   while (lo < hi) {
@@ -340,6 +341,30 @@ __device__ __forceinline__ bool tiles_run(const RowsParams& p, const TilesTable&
   return true;
 }
 
+// The run behind r: the next unit of the head, of the next head or sequence.
+__device__ __forceinline__ bool tiles_next(const RowsParams& p, const TilesTable& tt, int nq, long long x1, TilesRun& r) {
+  r.x += r.hi - r.lo;
+  if (r.x >= x1) return false;
+  if (++r.j * kAmKeys >= tt.n[r.b]) {
+    r.j = 0;
+    if (++r.g == p.Hkv) {
+      r.g = 0;
+      do ++r.b;
+      while (tt.m[r.b] == 0);  // there is one: pieces are left
+    }
+  }
+  const HeadShape h(tt.n[r.b], tt.m[r.b], nq, p.G);
+  r.f = h.first(r.j);
+  r.width = h.RT - r.f;
+  const int count = h.pieces(r.j);
+  r.lo = 0;
+  r.hi = (int)min((long long)count, x1 - r.x);
+  r.whole = r.hi == count;
+  r.first = 0;
+  r.ux = r.x;
+  return true;
+}
+
 __device__ __forceinline__ void tiles_table(const RowsParams& p, TilesTable& tt) {
   for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
     const int n = rows_cache_len(p, b);
@@ -364,7 +389,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
   __shared__ TilesTable tt;
   __shared__ uint64_t kfull[KS], kempty[KS], qfull[kAmQ], qempty[kAmQ], lfull[kAmQ];
   __shared__ uint64_t sfull[2][2], sempty[2][2], hsum;  // [buffer][key tile]
-  __shared__ float half_s[2][128];
+  __shared__ float half_s[2][2][128];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -419,6 +444,12 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
     }
     return true;
   };
+  auto wait_one = [&](uint64_t* bar, int phase) {  // a single lane's
+    if (mbar_wait_role(bar, (uint32_t)(phase & 1), &abort_flag)) return true;
+    flag_error(p.err, RKV_DEVERR_TIMEOUT);
+    abort_flag = 1;
+    return false;
+  };
   TilesRun r;
   int units = 0, tiles = 0;  // units and query tiles loaded (16), used (17), read (others)
   bool ok = true;
@@ -429,10 +460,10 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
     const int c0 = half * cols;  // this warp's columns
     const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kt * 128 + c0;
     const float sl = p.scale_log2;
-    for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+    for (bool more = tiles_find(p, tt, nq, x0, x0, x1, r); ok && more; more = tiles_next(p, tt, nq, x1, r)) {
       const int n = tt.n[r.b], m = tt.m[r.b], t = r.j * kAmKeys + key;
       float sum = 0.f;
-      int rt = r.f + r.lo % r.width;
+      int rt = r.f + (r.lo > 0 ? r.lo % r.width : 0);
       for (int o = r.lo; o < r.hi; ++o) {
         const int buf = tiles & 1, i0 = rt * nq;
         if (++rt == r.f + r.width) rt = r.f;
@@ -476,12 +507,12 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
         ++tiles;
       }
       if (!ok) break;
-      // the two halves of the columns meet
-      if (half) half_s[kt][tid & 127] = sum;
+      // the two halves of the columns meet (in turn in two places: one barrier a unit)
+      if (half) half_s[units & 1][kt][tid & 127] = sum;
       mbar_arrive(&hsum);
-      if (!(ok = wait(&hsum, 2 * units))) break;
+      if (!(ok = wait(&hsum, units))) break;
       if (!half) {
-        sum += half_s[kt][tid & 127];
+        sum += half_s[units & 1][kt][tid & 127];
         if (r.whole) {
           if (t < n) {
             const int phys = p.page_table[(size_t)r.b * p.max_pages + (t >> p.pshift)];
@@ -491,54 +522,58 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
           p.part[(2 * (size_t)blockIdx.x + (r.first ? 0 : 1)) * kAmKeys + key] = sum;
         }
       }
-      mbar_arrive(&hsum);  // half_s is free
-      if (!(ok = wait(&hsum, 2 * units + 1))) break;
       ++units;
     }
   } else {
     if (warp == 16) {
-    const bool lead = elect_lane();
-    for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
-      const int n = tt.n[r.b], s = units % KS;
-      // the unit's keys, a page a lane
-      const int pages = kAmKeys >> p.pshift, pg = r.j * pages + lane;
-      int phys = -1;
-      if (lane < pages && pg * p.P < n) {
-        phys = p.page_table[(size_t)r.b * p.max_pages + pg];
-        if (phys < 0 || phys >= p.num_phys) {
-          flag_error(p.err, RKV_DEVERR_PAGE_ID);
-          phys = -1;
-        }
-      }
-      if (units >= KS && !(ok = wait(&kempty[s], units / KS - 1))) break;
-      const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0), bar = smem_u32(&kfull[s]);
-      if (lead) {
-        if (have) mbar_arrive_expect_tx(&kfull[s], __popc(have) * p.P * 256);
-        else mbar_arrive(&kfull[s]);
-      }
-      __syncwarp();
+    if (elect_lane()) {  // one lane: a copy issued from converged code costs 90 clocks
+      const int pages = kAmKeys >> p.pshift, box = p.P * 128;
+      for (bool more = tiles_find(p, tt, nq, x0, x0, x1, r); ok && more; more = tiles_next(p, tt, nq, x1, r)) {
+        const int n = tt.n[r.b], s = units % KS;
+        // the unit's page ids: the table's rows are whole groups of eight
+        int ids[16];
+        const int* at = p.page_table + (size_t)r.b * p.max_pages + r.j * pages;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int ph = __shfl_sync(0xffffffffu, phys, j), row = j * p.P;  // of the unit's 256
-        const bool go = lead && ((have >> j) & 1u);
-        const uint32_t to = smem_u32(ks) + s * 65536 + (row >> 7) * 32768 + (row & 127) * 128;
-        tma_load_2d_if(go, to, &p.tmk, 0, (ph * p.Hkv + r.g) * p.P, bar);
-        tma_load_2d_if(go, to + 16384, &p.tmk, 64, (ph * p.Hkv + r.g) * p.P, bar);
-      }
-      ++units;
-      int h = r.lo / r.width, rt = r.f + r.lo - h * r.width;
-      for (int o = r.lo; o < r.hi; ++o) {
-        const int t = tiles % kAmQ;
-        if (tiles >= kAmQ && !(ok = wait(&qempty[t], tiles / kAmQ - 1))) break;
-        const int row = (r.b * p.Hq + r.g * p.G + h) * p.T + rt * nq;
-        if (lead) mbar_arrive_expect_tx(&qfull[t], nq * 256);
-        __syncwarp();
-        tma_load_2d_if(lead, smem_u32(qs) + t * QB, &p.tmq, 0, row, smem_u32(&qfull[t]));
-        tma_load_2d_if(lead, smem_u32(qs) + t * QB + QB / 2, &p.tmq, 64, row, smem_u32(&qfull[t]));
-        ++tiles;
-        if (++rt == r.f + r.width) {
-          rt = r.f;
-          ++h;
+        for (int q = 0; q < 4; ++q) {
+          int4 id = make_int4(-1, -1, -1, -1);
+          if (4 * q < pages && (r.j * pages + 4 * q) * p.P < n) id = *reinterpret_cast<const int4*>(at + 4 * q);
+          ids[4 * q] = id.x;
+          ids[4 * q + 1] = id.y;
+          ids[4 * q + 2] = id.z;
+          ids[4 * q + 3] = id.w;
+        }
+        uint32_t have = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (j < pages && (r.j * pages + j) * p.P < n) {
+            if (ids[j] >= 0 && ids[j] < p.num_phys) have |= 1u << j;
+            else flag_error(p.err, RKV_DEVERR_PAGE_ID);
+          }
+        if (units >= KS && !(ok = wait_one(&kempty[s], units / KS - 1))) break;
+        if (have) mbar_arrive_expect_tx(&kfull[s], __popc(have) * 2 * box);
+        else mbar_arrive(&kfull[s]);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if ((have >> j) & 1u) {
+            const int in = j * p.P, row = (ids[j] * p.Hkv + r.g) * p.P;  // row of the unit's 256, of the pool
+            uint8_t* to = ks + s * 65536 + (in >> 7) * 32768 + (in & 127) * 128;
+            tma_load_2d(to, &p.tmk, 0, row, &kfull[s]);
+            tma_load_2d(to + 16384, &p.tmk, 64, row, &kfull[s]);
+          }
+        ++units;
+        int h = r.lo > 0 ? r.lo / r.width : 0, rt = r.f + r.lo - h * r.width;
+        for (int o = r.lo; o < r.hi; ++o) {
+          const int t = tiles % kAmQ;
+          if (tiles >= kAmQ && !(ok = wait_one(&qempty[t], tiles / kAmQ - 1))) break;
+          const int row = (r.b * p.Hq + r.g * p.G + h) * p.T + rt * nq;
+          mbar_arrive_expect_tx(&qfull[t], nq * 256);
+          tma_load_2d(qs + t * QB, &p.tmq, 0, row, &qfull[t]);
+          tma_load_2d(qs + t * QB + QB / 2, &p.tmq, 64, row, &qfull[t]);
+          ++tiles;
+          if (++rt == r.f + r.width) {
+            rt = r.f;
+            ++h;
+          }
         }
       }
     }
@@ -547,7 +582,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
     const bool lead = elect_lane();
     const uint32_t klo = sw128_kmajor_lo(smem_u32(ks)), qlo = sw128_kmajor_lo(smem_u32(qs));
     const uint32_t onelo = plain_kmajor_lo(smem_u32(ones)), biaslo = plain_kmajor_lo(smem_u32(bias));
-    for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+    for (bool more = tiles_find(p, tt, nq, x0, x0, x1, r); ok && more; more = tiles_next(p, tt, nq, x1, r)) {
       const int s = units % KS;
       if (!(ok = wait(&kfull[s], units / KS))) break;
       ++units;
@@ -586,7 +621,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
     // one before it (of this warp) is still being written
     const float inv = 1.f / p.scale;
     int before = 0;  // tiles of the runs before
-    for (long long x = x0; ok && tiles_run(p, tt, nq, x, x0, x1, r); x = r.x + (r.hi - r.lo)) {
+    for (bool more = tiles_find(p, tt, nq, x0, x0, x1, r); ok && more; more = tiles_next(p, tt, nq, x1, r)) {
       const int m = tt.m[r.b];
       int o = r.lo + ((before + warp) & 1);  // warp 18 takes the even tiles of the CTA
       int h = o / r.width, rt = r.f + o - h * r.width;
@@ -639,7 +674,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
   tc_fence_before();
   __syncthreads();
   if (abort_flag) {
-    if (warp == 16 && lane == 0) {
+    if (warp == 16) {  // the lane that issued them; the others have none
       for (int i = max(0, tiles - kAmQ); i < tiles; ++i) mbar_wait(&qfull[i % kAmQ], (uint32_t)((i / kAmQ) & 1));
       for (int i = max(0, units - KS); i < units; ++i) mbar_wait(&kfull[i % KS], (uint32_t)((i / KS) & 1));
     }
@@ -664,7 +699,7 @@ __global__ void __launch_bounds__(kAmKeys) accum_join_kernel(const __grid_consta
   if (c >= N) return;
   const long long x0 = flat_first(total, c, N), x1 = flat_first(total, c + 1, N);
   TilesRun r;
-  tiles_run(p, tt, p.nq, x1 - 1, x0, total, r);
+  tiles_find(p, tt, p.nq, x1 - 1, x0, total, r);
   const long long end = r.x + (r.hi - r.lo);  // the unit's end
   if (r.ux < x0 || end <= x1) return;
   const int last = flat_cta(end - 1, total, N), t = r.j * kAmKeys + threadIdx.x;
@@ -891,9 +926,10 @@ size_t accum_rows_ws_bytes(int, int, int, int, int, int) { return (size_t)2 * kM
 cudaError_t launch_accum_rows(const AccumRowsArgs& a, cudaStream_t s) {
   const rkv_cache& c = a.cache;
   RowsParams p;
-  // up to 64 rows of a KV head are one staged block of accum_rows; rows picked by id are
-  // gathered, which only accum_rows does
-  const bool tiles = !a.row_ids && (long long)a.T * (a.Hq / c.Hkv) > kRwBlock;
+  // Up to two staged blocks of 64 rows of a KV head go to accum_rows (30 rows x 4 heads, 1 x
+  // 16K tokens: 26 us against 34 with the join; 32 x 4, 4 x 16K: 78 against 74; 48 x 4: 112
+  // against 75); so do rows picked by id, which only it gathers.
+  const bool tiles = !a.row_ids && (long long)a.T * (a.Hq / c.Hkv) > 2 * kRwBlock;
   p.nq = a.T > 64 ? 128 : 64;
   bool ok = encode_rows_map(&p.tmk, c.k_pages, (uint64_t)c.num_phys_pages * c.Hkv * c.page_size,
                             tiles ? (uint32_t)c.page_size : (uint32_t)kRwKeys);

@@ -170,18 +170,6 @@ __device__ __forceinline__ void prefetch_map(const void* map) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
-// The same, called by a whole converged warp with equal operands and issued where `issue`
-// holds: the operands then go through uniform registers once.  (With operands that differ
-// by lane the compiler serialises the lanes, about 100 clocks a box.)
-__device__ __forceinline__ void tma_load_2d_if(bool issue, uint32_t dst, const void* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n"
-      " @q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%2, {%3, %4}], [%5];\n}\n" ::"r"(
-          (uint32_t)issue),
-      "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-
 // 2^x by the special function unit's single instruction (PTX ex2.approx.ftz.f32):
 // relative error of a few ulps, results below 2^-126 flushed to zero.  Used where the
 // exponential is the inner loop's cost (the scoring epilogues, the attention's online
