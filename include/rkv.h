@@ -25,7 +25,7 @@
  *     with no side effect and a message in rkv_last_error().
  *   - A failed kernel launch returns RKV_ERR_CUDA.
  *   - Errors found on the device (a page id out of range, a sequence longer than
- *     its pages, a bounded wait that ran out) are OR-ed into cache->error_word as
+ *     its pages, a node id or count out of range, a bounded wait that ran out) are OR-ed into cache->error_word as
  *     RKV_DEVERR_* bits; the kernel skips the offending access and carries on.
  *     rkv_get_device_status reads and clears the word.
  *   - head_dim must be 128; page_size 16, 32 or 64; Hq a multiple of Hkv with
@@ -398,8 +398,9 @@ size_t rkv_tree_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, in
  *   out       : device [B][Hq][T][128] bf16.   lse : device [B][Hq][T] fp32 or NULL.
  * Logits, maxima, sums and the output's accumulation are fp32; the softmax weights enter
  * the product with V as bf16.  seq_len and tree_len are read on the device, so a captured
- * call can be replayed as the cache grows.  Calls whose work may overlap need workspaces
- * of their own.
+ * call can be replayed as the cache grows.  Calls of this and the following functions
+ * whose work may overlap need workspaces of their own; nothing in a workspace outlives its
+ * call.  scale lies in [1e-30, 1e30] here and below.
  */
 rkv_status rkv_tree_attention(const rkv_cache* cache, const rkv_bf16* q, const rkv_bf16* k_tree,
                               const rkv_bf16* v_tree, const uint32_t* tree_mask, int32_t Hq, int32_t T,

@@ -445,6 +445,28 @@ def test_evict_accum_flags_bad_lengths_and_pages(rkv):
             assert torch.equal(got[i], K[0][0, t])
 
 
+def test_evict_accum_in_place_skips_a_page_it_cannot_read(rkv):
+    cache, K, V, acc0 = _evict_case(rkv, [100], 2, 16, 48, False)
+    acc0[0, :, 32:48] += 2                             # the unreadable page's tokens are among the kept
+    kept = torch.full((1, 2, 40), -7, dtype=torch.int32, device="cuda")
+    acc = acc0.cuda()
+    ws = rkv.evict_workspace(1, 2, 40)
+    ws.fill_(255)                                      # NaN patterns, were they copied
+    bad = int(cache.page_table[0, 2])
+    cache.page_table[0, 2] = cache.num_phys_pages
+    rkv.rkv_evict_accum(cache, acc, [40], 4, kept, workspace=ws)
+    assert _status(rkv, cache) == rkv.DEVERR_PAGE_ID
+    cache.page_table[0, 2] = bad
+    for g in range(2):
+        want = C.keep_set(acc0[0, g], 100, 40, 4)
+        assert kept[0, g].tolist() == want
+        got = cache.token_kv(0, 32)[0][g].cpu()        # rows 32.. would go to the bad page
+        for i, t in enumerate(want[:32]):
+            if t // 16 != 2:
+                assert torch.equal(got[i], K[0][g, t])
+        assert torch.equal(acc[0, g, :40].cpu(), acc0[0, g][want])
+
+
 # ------------------------------------------------------------------ together
 def _together(rkv, lens, Hkv, G, P, rounds, seed, stream=None):
     """Speculative decoding with a heavy-hitter budget: a prompt's weights, then rounds of a
@@ -618,6 +640,26 @@ def test_another_stream_and_a_replayed_graph(rkv):
             C.check_lse(l1[i, h:h + 1].cpu(), l, Ew)
     assert cache.seq_len.tolist() == [700 + 12, 90 + 8]
     assert _status(rkv, cache) == 0
+
+
+def test_workspaces_made_by_the_calls_on_another_stream(rkv):
+    """Without a workspace argument each call makes its own; on a stream that is not the
+    current one its memory must not be handed out while the call still runs."""
+    cache, K, V = C.make_cache(rkv, [6000, 900], 2, 16, seed=65, room=10000)
+    g = C.gen(66)
+    q = C.randn(g, 2, 8, D)
+    qd = q.cuda()
+    side = torch.cuda.Stream()
+    outs = [torch.zeros(2, 8, D, dtype=torch.bfloat16, device="cuda") for _ in range(20)]
+    lse = torch.zeros(2, 8, device="cuda")
+    acc = rkv.accum_sums(cache)
+    torch.cuda.synchronize()
+    for o in outs:
+        rkv.rkv_decode_accum(cache, qd, o, acc, lse=lse, stream=side)
+        torch.full((8 << 20,), 255, dtype=torch.uint8, device="cuda")  # takes what was freed, on the current stream
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    _check_decode(outs[0], lse, acc, torch.zeros(2, 2, acc.shape[2]), K, V, q, steps=20)
 
 
 def test_a_long_cache_with_offsets_past_32_bits(rkv):

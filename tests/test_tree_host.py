@@ -51,7 +51,8 @@ def test_tree_attention_refusals(rkv):
         (dict(q=0x100008), "INVALID_ARG"), (dict(vt=0x300002), "INVALID_ARG"), (dict(mask=0x400002), "INVALID_ARG"),
         (dict(lse=0x700001), "INVALID_ARG"), (dict(tl=0x700002), "INVALID_ARG"),
         (dict(scale=0.0), "INVALID_ARG"), (dict(scale=-1.0), "INVALID_ARG"), (dict(scale=float("nan")), "INVALID_ARG"),
-        (dict(scale=float("inf")), "INVALID_ARG"), (dict(short=1), "WORKSPACE")])
+        (dict(scale=float("inf")), "INVALID_ARG"), (dict(scale=1e-38), "INVALID_ARG"), (dict(scale=1e31), "INVALID_ARG"),
+        (dict(short=1), "WORKSPACE")])
 
 
 def test_tree_commit_refusals(rkv):

@@ -850,18 +850,13 @@ __global__ void __launch_bounds__(128) evict_compact_kernel(const __grid_constan
       vv[j] = make_uint4(0, 0, 0, 0);
       if (!have[j]) continue;
       const int t = idx[q * P + r];
-      if (p.in_place && t != i) {
-        const size_t row = (unit * p.stage_stride + i) * 128 + piece * 8;
-        kv[j] = *reinterpret_cast<const uint4*>(p.stage_k + row);
-        vv[j] = *reinterpret_cast<const uint4*>(p.stage_v + row);
-      } else {
-        size_t row;
-        have[j] = evict_source(p, b, g, t, row);
-        if (have[j]) {
-          kv[j] = *reinterpret_cast<const uint4*>(p.src.k_pages + row + piece * 8);
-          vv[j] = *reinterpret_cast<const uint4*>(p.src.v_pages + row + piece * 8);
-        }
-      }
+      size_t row;
+      have[j] = evict_source(p, b, g, t, row);  // a row that cannot be read was not staged either
+      if (!have[j]) continue;
+      const bool moved = p.in_place && t != i;
+      if (moved) row = (unit * p.stage_stride + i) * 128;
+      kv[j] = *reinterpret_cast<const uint4*>((moved ? p.stage_k : p.src.k_pages) + row + piece * 8);
+      vv[j] = *reinterpret_cast<const uint4*>((moved ? p.stage_v : p.src.v_pages) + row + piece * 8);
     }
     float mx[8], mn[8];
 #pragma unroll

@@ -609,6 +609,12 @@ rkv_status rkv_decode_step_host(const rkv_cache* cache, const void* host_in, flo
   return cuda_status(e, "rkv_decode_step_host output copy");
 }
 
+// The softmax scale of the dense calls: their kernels multiply by it and by its inverse.
+static rkv_status check_scale(float scale) {
+  if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(RKV_ERR_INVALID_ARG, "scale must be in [1e-30, 1e30]");
+  return RKV_OK;
+}
+
 size_t rkv_tree_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t max_pages, int32_t page_size) {
   if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || max_pages < 1 || page_size < 1) return 0;
   return rkv::attend_ws_bytes(B, Hq, Hkv, T, max_pages, page_size, false);
@@ -630,7 +636,7 @@ rkv_status rkv_tree_attention(const rkv_cache* cache, const rkv_bf16* q, const r
     return fail(RKV_ERR_INVALID_ARG, "tree_mask, tree_len and lse must be 4-byte aligned");
   if (T < 1 || T > RKV_MAX_TREE) return fail(RKV_ERR_INVALID_ARG, "T=%d outside [1, %d]", T, RKV_MAX_TREE);
   if ((long long)cache->B * Hq * T >= (1LL << 31)) return fail(RKV_ERR_UNSUPPORTED, "B * Hq * T above 2^31");
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(RKV_ERR_INVALID_ARG, "scale must be positive");
+  if ((st = check_scale(scale)) != RKV_OK) return st;
   const size_t need = rkv::attend_ws_bytes(cache->B, Hq, cache->Hkv, T, cache->max_pages, cache->page_size, false);
   if (workspace_bytes < need)
     return fail(RKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
@@ -699,7 +705,7 @@ rkv_status rkv_decode_accum(const rkv_cache* cache, const rkv_bf16* q, int32_t H
     return fail(RKV_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
   if (!al4(lse)) return fail(RKV_ERR_INVALID_ARG, "lse must be 4-byte aligned");
   if ((st = check_acc(cache, acc, acc_stride, "acc")) != RKV_OK) return st;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(RKV_ERR_INVALID_ARG, "scale must be positive");
+  if ((st = check_scale(scale)) != RKV_OK) return st;
   const size_t need = rkv::attend_ws_bytes(cache->B, Hq, cache->Hkv, 1, cache->max_pages, cache->page_size, true);
   if (workspace_bytes < need)
     return fail(RKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
@@ -739,7 +745,7 @@ rkv_status rkv_accum_rows(const rkv_cache* cache, const rkv_bf16* q, const float
     return fail(RKV_ERR_INVALID_ARG, "ids_stride=%d outside [1, 2^20]", ids_stride);
   if ((long long)cache->B * Hq * T >= (1LL << 31)) return fail(RKV_ERR_UNSUPPORTED, "B * Hq * T above 2^31");
   if ((st = check_acc(cache, acc, acc_stride, "acc")) != RKV_OK) return st;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(RKV_ERR_INVALID_ARG, "scale must be positive");
+  if ((st = check_scale(scale)) != RKV_OK) return st;
   const size_t need = rkv::accum_rows_ws_bytes(cache->B, Hq, cache->Hkv, T, cache->max_pages, cache->page_size);
   if (workspace_bytes < need)
     return fail(RKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);

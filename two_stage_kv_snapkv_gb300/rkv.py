@@ -437,6 +437,13 @@ def _call_on(device, stream, fn, *args) -> None:
         _check(status)
 
 
+def _own_ws(workspace: torch.Tensor, stream) -> torch.Tensor:
+    """A workspace made for one call: kept from being handed out again while `stream` uses it."""
+    if stream is not None:
+        workspace.record_stream(stream)
+    return workspace
+
+
 def tree_workspace(B: int, Hq: int, Hkv: int, T: int, max_pages: int, page_size: int, device="cuda") -> torch.Tensor:
     n = _lib.rkv_tree_workspace_size(B, Hq, Hkv, T, max_pages, page_size)
     return torch.empty(n, dtype=torch.uint8, device=device)
@@ -461,7 +468,7 @@ def rkv_tree_attention(cache: PagedCache, q: torch.Tensor, k_tree: torch.Tensor,
             _arg(tree_len, "tree_len", (B,), torch.int32, dev), 1.0 / math.sqrt(d) if scale is None else scale,
             _arg(out, "out", (B, Hq, T, HEAD_DIM), bf16, dev), _arg(lse, "lse", (B, Hq, T), torch.float32, dev))
     if workspace is None:
-        workspace = tree_workspace(B, Hq, cache.Hkv, T, cache.max_pages, cache.page_size, dev)
+        workspace = _own_ws(tree_workspace(B, Hq, cache.Hkv, T, cache.max_pages, cache.page_size, dev), stream)
     _call_on(dev, stream, _lib.rkv_tree_attention, ctypes.byref(cache.struct), *args, _ws_arg(workspace, dev),
              workspace.numel())
 
@@ -505,7 +512,7 @@ def rkv_decode_accum(cache: PagedCache, q: torch.Tensor, out: torch.Tensor, acc:
             _arg(out, "out", (B, Hq, HEAD_DIM), torch.bfloat16, dev), _arg(lse, "lse", (B, Hq), torch.float32, dev),
             _acc_arg(acc, "acc", cache, dev), acc.shape[2])
     if workspace is None:
-        workspace = accum_workspace(B, Hq, cache.Hkv, cache.max_pages, cache.page_size, dev)
+        workspace = _own_ws(accum_workspace(B, Hq, cache.Hkv, cache.max_pages, cache.page_size, dev), stream)
     _call_on(dev, stream, _lib.rkv_decode_accum, ctypes.byref(cache.struct), *args, _ws_arg(workspace, dev),
              workspace.numel())
 
@@ -534,7 +541,7 @@ def rkv_accum_rows(cache: PagedCache, q: torch.Tensor, lse: torch.Tensor, acc: t
             _arg(row_ids, "row_ids", (B, ids), torch.int32, dev), ids, 1.0 / math.sqrt(d) if scale is None else scale,
             _acc_arg(acc, "acc", cache, dev), acc.shape[2])
     if workspace is None:
-        workspace = accum_rows_workspace(B, Hq, cache.Hkv, T, cache.max_pages, cache.page_size, dev)
+        workspace = _own_ws(accum_rows_workspace(B, Hq, cache.Hkv, T, cache.max_pages, cache.page_size, dev), stream)
     _call_on(dev, stream, _lib.rkv_accum_rows, ctypes.byref(cache.struct), *args, _ws_arg(workspace, dev),
              workspace.numel())
 
@@ -561,7 +568,8 @@ def rkv_evict_accum(cache: PagedCache, acc: torch.Tensor, keep: Sequence[int], r
     sums = _acc_arg(acc, "acc", cache, dev)
     to = _acc_arg(dst_acc, "dst_acc", cache, dev) if dst_acc is not None else None
     if workspace is None:
-        workspace = evict_workspace(cache.B, cache.Hkv, max(1, max(int(x) for x in keep)), dev, in_place=dst is None)
+        workspace = _own_ws(evict_workspace(cache.B, cache.Hkv, max(1, max(int(x) for x in keep)), dev,
+                                            in_place=dst is None), stream)
     _call_on(dev, stream, _lib.rkv_evict_accum, ctypes.byref(cache.struct), sums, acc.shape[2], _host_i32(keep),
              int(recent), kept, kept_idx.shape[2], ctypes.byref(dst.struct) if dst is not None else None, to,
              dst_acc.shape[2] if dst_acc is not None else 0, _ws_arg(workspace, dev), workspace.numel())
