@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
   static_assert(KS * 65536 + kAmQ * QB == 6 * 32768, "the rings fill the shared memory");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ TilesTable tt;
-  __shared__ uint64_t kfull[KS], kempty[KS], qfull[kAmQ], qempty[kAmQ], lfull[kAmQ];
+  __shared__ uint64_t kfull[KS], kempty[KS], qfull[kAmQ], qempty[kAmQ];
   __shared__ uint64_t sfull[2][2], sempty[2][2], hsum;  // [buffer][key tile]
   __shared__ float half_s[2][2][128];
   __shared__ uint32_t tmem_base;
@@ -409,9 +409,8 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
       mbar_init(&kempty[i], 1);
     }
     for (int i = 0; i < kAmQ; ++i) {
-      mbar_init(&qfull[i], 1);
+      mbar_init(&qfull[i], 1 + 32);  // the copy and the lanes that write the log-sum-exps
       mbar_init(&qempty[i], 1);
-      mbar_init(&lfull[i], 32);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sfull[i >> 1][i & 1], 1);
@@ -582,17 +581,20 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
     const bool lead = elect_lane();
     const uint32_t klo = sw128_kmajor_lo(smem_u32(ks)), qlo = sw128_kmajor_lo(smem_u32(qs));
     const uint32_t onelo = plain_kmajor_lo(smem_u32(ones)), biaslo = plain_kmajor_lo(smem_u32(bias));
+    // The waits stand where products are still queued: inside a unit a query tile is waited
+    // for before the second key tile of the one before it is issued.  (Not across units: the
+    // next unit's keys, and its query tiles behind them, wait for this unit's products.)
     for (bool more = tiles_find(p, tt, nq, x0, x0, x1, r); ok && more; more = tiles_next(p, tt, nq, x1, r)) {
       const int s = units % KS;
       if (!(ok = wait(&kfull[s], units / KS))) break;
       ++units;
+      if (!(ok = wait(&qfull[tiles % kAmQ], tiles / kAmQ))) break;
       for (int o = r.lo; o < r.hi; ++o) {
         const int t = tiles % kAmQ, d = tiles & 1;
-        if (!(ok = wait(&qfull[t], tiles / kAmQ))) break;
-        if (!(ok = wait(&lfull[t], tiles / kAmQ))) break;
         const uint32_t q = qlo + t * (QB >> 4);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
+          if (w == 1 && o + 1 < r.hi && !(ok = wait(&qfull[(tiles + 1) % kAmQ], (tiles + 1) / kAmQ))) break;
           if (tiles >= 2 && !(ok = wait(&sempty[d][w], tiles / 2 - 1))) break;
           tc_fence_after();
           const uint32_t to = tmem + d * 256 + w * 128, key = klo + s * (65536 >> 4) + w * (32768 >> 4);
@@ -663,7 +665,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
           if (row < nq) *reinterpret_cast<uint2*>(bias + t * kAmExtra + (row >> 3) * 256 + (row & 7) * 16) = w[e];
         }
         fence_proxy_async_smem();
-        mbar_arrive(&lfull[t]);
+        mbar_arrive(&qfull[t]);
       }
       before += r.hi - r.lo;
     }
