@@ -1142,84 +1142,92 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
   } else {
     setmaxnreg_dec<kAtIssueRegs>();
     if (warp == 8 || warp == 10) {
-    // warp 8 fetches K, warp 10 V, one lane each; entry of K_i / V_i among a run's 2 nt
-    // entries: wide K_i 2 i, V_i 2 i + 1; narrow K_0, then K_(i+1) and V_i for every i
-    if (elect_lane()) {
-      const bool v = warp == 10;
-      const CUtensorMap* map = v ? &p.tmv : &p.tmk;
-      const CUtensorMap* tmap = v ? &p.tmvt : &p.tmkt;
-      const int pages = kAtKeys >> p.pshift, box = p.P * 128;  // pages of a tile, bytes of a box
-      // one row tile: nobody reads the cache again (the wide form measured 267 us with this
-      // and 255 without, 63 nodes over the ragged batch; the narrow one 33 against 37)
-      const uint64_t policy = l2_policy(!kWide && p.T * p.G <= R);
-      int before = 0;                                          // entries of the runs before
-      bool ok = true;
-      for (long long x = x0; ok && next_run(x, r); x = r.next) {
-        const int b = r.b, g = r.unit % p.Hkv, n = r.n, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
-        // page ids of a tile (the table's rows are whole groups of eight), loaded a tile ahead
-        // and judged only when they are used, so that the load's latency stays off the ring
-        auto ids_of = [&](int tile, int4(&id)[2]) {
-          id[0] = id[1] = make_int4(-1, -1, -1, -1);
-          if (tile >= nc) return;
-          const int* at = p.page_table + (size_t)b * p.max_pages + tile * pages;
-          if (pages == 2) {
-            const int2 two = *reinterpret_cast<const int2*>(at);
-            id[0].x = two.x;
-            id[0].y = two.y;
-          } else {
-            id[0] = *reinterpret_cast<const int4*>(at);
-            if (pages == 8) id[1] = *reinterpret_cast<const int4*>(at + 4);
+    // warp 8 fetches K, warp 10 V; entry of K_i / V_i among a run's 2 nt entries:
+    // wide K_i 2 i, V_i 2 i + 1; narrow K_0, then K_(i+1) and V_i for every i
+    const bool v = warp == 10;
+    const CUtensorMap* map = v ? &p.tmv : &p.tmk;
+    const CUtensorMap* tmap = v ? &p.tmvt : &p.tmkt;
+    const bool lead = elect_lane();
+    const int pages = kAtKeys >> p.pshift, box = p.P * 128;  // pages of a tile, bytes of a box
+    // one row tile: nobody reads the cache again (the wide form measured 267 us with this
+    // and 255 without, 63 nodes over the ragged batch; the narrow one 33 against 37)
+    const uint64_t policy = l2_policy(!kWide && p.T * p.G <= R);
+    int before = 0;                                          // entries of the runs before
+    bool ok = true;
+    for (long long x = x0; ok && next_run(x, r); x = r.next) {
+      const int b = r.b, g = r.unit % p.Hkv, n = r.n, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
+      // lane j: page id of the tile's page j, -1: none; loaded a tile ahead and judged only
+      // when it is used, so that the load's latency stays off the ring
+      auto page_of = [&](int tile) {
+        const int pg = tile * pages + lane;
+        return tile < nc && lane < pages && pg * p.P < n ? p.page_table[(size_t)b * p.max_pages + pg] : -1;
+      };
+      int next = page_of(r.lo);
+      for (int i = 0; i < nt; ++i) {
+        const int tile = r.lo + i;
+        int phys = next;
+        next = i + 1 < nt ? page_of(tile + 1) : -1;
+        const int at = before + (kWide ? 2 * i + v : (v ? (i + 1 < nt ? 2 * i + 2 : 2 * nt - 1) : (i > 0 ? 2 * i - 1 : 0)));
+        const int e = at % E;
+        const bool late = at >= E && !mbar_wait_role(&empty_b[e], (uint32_t)((at / E - 1) & 1), &abort_flag);
+        if (__any_sync(0xffffffffu, late)) {
+          give_up();
+          ok = false;
+          break;
+        }
+        uint8_t* const st = ring + e * kAtEntry;
+        const uint32_t st32 = smem_u32(st), bar32 = smem_u32(&full_b[e]);
+        if (tile < nc) {
+          if (phys < 0 || phys >= p.num_phys) {
+            if (lane < pages && (tile * pages + lane) * p.P < n) flag_error(p.err, RKV_DEVERR_PAGE_ID);
+            phys = -1;
           }
-        };
-        int4 next[2];
-        ids_of(r.lo, next);
-        for (int i = 0; i < nt; ++i) {
-          const int tile = r.lo + i;
-          int ids[8] = {next[0].x, next[0].y, next[0].z, next[0].w, next[1].x, next[1].y, next[1].z, next[1].w};
-          if (i + 1 < nt) ids_of(tile + 1, next);
-          const int at = before + (kWide ? 2 * i + v : (v ? (i + 1 < nt ? 2 * i + 2 : 2 * nt - 1) : (i > 0 ? 2 * i - 1 : 0)));
-          const int e = at % E;
-          if (at >= E && !mbar_wait_role(&empty_b[e], (uint32_t)((at / E - 1) & 1), &abort_flag)) {
-            give_up();
-            ok = false;
-            break;
-          }
-          uint8_t* st = ring + e * kAtEntry;
-          uint64_t* bar = &full_b[e];
-          if (tile < nc) {
-            uint32_t have = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (j < pages && (tile * pages + j) * p.P < n) {
-                if (ids[j] >= 0 && ids[j] < p.num_phys) have |= 1u << j;
-                else flag_error(p.err, RKV_DEVERR_PAGE_ID);
-              }
+          const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0);
+          if (lead) {
             if (!v) {
               uint32_t gr = 0;  // a page is P / 16 groups
               for (int j = 0; j < pages; ++j)
                 if ((have >> j) & 1u) gr |= ((1u << (p.P >> 4)) - 1u) << (j * (p.P >> 4));
               groups[e] = gr;
             }
-            if (have) mbar_arrive_expect_tx(bar, __popc(have) * 2 * box);
-            else mbar_arrive(bar);
+            if (have) mbar_arrive_expect_tx(&full_b[e], __popc(have) * 2 * box);
+            else mbar_arrive(&full_b[e]);
+          }
+          __syncwarp();
+          int row[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) row[j] = (__shfl_sync(0xffffffffu, phys, j) * p.Hkv + g) * p.P;
+          if (kWide) {
+            // The wide form is bound by the products and the card's power: boxes issued from
+            // converged code, 90 clocks each, measured 406 us against 429 from one lane.
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              tma_load_2d_if(lead && ((have >> j) & 1u), st32 + j * box, map, 0, row[j], bar32);
+              tma_load_2d_if(lead && ((have >> j) & 1u), st32 + kAtEntry / 2 + j * box, map, 64, row[j], bar32);
+            }
+          } else if (lead) {  // the narrow one by the copies: 320 us from one lane against 364 (8 nodes, 8 x 64K)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               if ((have >> j) & 1u) {
-                const int row = (ids[j] * p.Hkv + g) * p.P;
-                tma_load_2d_hint(st + j * box, map, 0, row, bar, policy);
-                tma_load_2d_hint(st + kAtEntry / 2 + j * box, map, 64, row, bar, policy);
+                tma_load_2d_hint(st + j * box, map, 0, row[j], &full_b[e], policy);
+                tma_load_2d_hint(st + kAtEntry / 2 + j * box, map, 64, row[j], &full_b[e], policy);
               }
-          } else {
-            const int row = (b * p.Hkv + g) * p.T + (tile - nc) * kAtKeys;
-            if (!v) groups[e] = 0xffu;
-            mbar_arrive_expect_tx(bar, kAtEntry);
-            tma_load_2d(st, tmap, 0, row, bar);
-            tma_load_2d(st + kAtEntry / 2, tmap, 64, row, bar);
           }
-          loaded = at + 1;
+        } else {
+          const int row = (b * p.Hkv + g) * p.T + (tile - nc) * kAtKeys;
+          if (lead) {
+            if (!v) groups[e] = 0xffu;
+            mbar_arrive_expect_tx(&full_b[e], kAtEntry);
+          }
+          __syncwarp();
+          if (lead) {
+            tma_load_2d(st, tmap, 0, row, &full_b[e]);
+            tma_load_2d(st + kAtEntry / 2, tmap, 64, row, &full_b[e]);
+          }
         }
-        before += 2 * nt;
+        loaded = at + 1;
       }
+      before += 2 * nt;
     }
   } else if (warp == 9) {
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128), idesc_o = idesc_s | kIdescBNMajor;
@@ -1355,7 +1363,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
   tc_fence_before();
   __syncthreads();
   if (abort_flag) {
-    if (warp == 8 || warp == 10)  // the lane that issued them; the others have none
+    if ((warp == 8 || warp == 10) && lane == 0)
       for (int i = loaded > E ? loaded - E : 0; i < loaded; ++i) mbar_wait(&full_b[i % E], (uint32_t)((i / E) & 1));
     if (warp == 9 && lane == 0) {  // everything issued before this commit has completed when it arrives
       tc_commit(&o_b[0]);

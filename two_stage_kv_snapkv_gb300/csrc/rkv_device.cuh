@@ -165,6 +165,17 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* map, int x, i
       : "memory");
 }
 
+// The same, called by a whole converged warp with equal operands and issued where `issue`
+// holds.
+__device__ __forceinline__ void tma_load_2d_if(bool issue, uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n"
+      " @q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%2, {%3, %4}], [%5];\n}\n" ::"r"(
+          (uint32_t)issue),
+      "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
 // The same with an L2 policy: data that is read once gives way first, so that what is
 // written meanwhile for the next kernel stays in L2.
 __device__ __forceinline__ uint64_t l2_policy(bool read_once) {
