@@ -720,6 +720,8 @@ __global__ void __launch_bounds__(kAmKeys) accum_join_kernel(const __grid_consta
 
 // ---------------------------------------------------------------------------
 // evict
+constexpr int kSelectOne = 8192;  // positions that one CTA selects from by itself
+
 struct EvictParams {
   rkv_cache src, dst;
   int in_place;
@@ -745,7 +747,10 @@ __device__ __forceinline__ int evict_len(const EvictParams& p, int b) {
 // shared memory, not bytes.
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t skeys[];
-  __shared__ SelectSmem ss;
+  __shared__ union {
+    SelectSmem cluster;
+    TopkSmem<kSelectThreads> block;
+  } ss;
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -766,10 +771,25 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   if (k == 0) return;
   const float* acc = p.acc + (size_t)unit * p.acc_stride;
   // a NaN counts as the heaviest, and both zeros as one
-  cluster_select(Lp, k, [&](int t) {
+  auto load = [&](int t) {
     const float v = acc[t];
     return v != v ? __int_as_float(0x7fffffff) : v + 0.f;
-  }, out, skeys, ss);
+  };
+  if (C > 1) {
+    cluster_select(Lp, k, load, out, skeys, ss.cluster);
+    return;
+  }
+  // one CTA: the same select over the block, without the cluster's barriers
+  for (int i0 = tid; i0 < Lp; i0 += 8 * kSelectThreads) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = i0 + j * kSelectThreads < Lp ? load(i0 + j * kSelectThreads) : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i0 + j * kSelectThreads < Lp) skeys[i0 + j * kSelectThreads] = float_key(v[j]);
+  }
+  __syncthreads();
+  topk_adaptive_fn<kSelectThreads>(Lp, k, [&](int i) { return skeys[i]; }, ss.block, [&](int at, int i) { out[at] = i; });
 }
 
 // Row i of a unit's kept list in the source cache; null when its page id is out of range.
@@ -1033,10 +1053,11 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
     w += align256(rows * 256);
     p.stage_acc = reinterpret_cast<float*>(w);
   }
-  // select: about 4096 positions a CTA, clusters of up to 8 while the units leave SMs
-  // idle and of 2 once they cover them, wide enough for the slices to fit
+  // select: one CTA up to 8192 positions; about 4096 positions a CTA beyond, clusters of up to
+  // 8 while the units leave SMs idle and of 2 once they cover them, wide enough for the
+  // slices to fit
   const int units = c.B * c.Hkv, cap = c.max_pages * c.page_size;
-  int C = (cap + 4095) / 4096;
+  int C = cap <= kSelectOne ? 1 : (cap + 4095) / 4096;
   const int by_units = num_sms() / units > 2 ? num_sms() / units : 2;
   const int by_smem = (cap + kSelectSliceMax - 1) / kSelectSliceMax;
   C = C < by_units ? C : by_units;
