@@ -488,8 +488,9 @@ size_t rkv_evict_workspace_size(int32_t B, int32_t Hkv, int32_t max_keep, int32_
  *              destination has the source's B, Hkv and page_size, its pages are none of
  *              the source's, and dst_acc is not acc; the source is then left as it was.
  *              In place, no page may belong to two sequences.
- * Caches of more than 393216 tokens per sequence (max_pages * page_size) return
- * RKV_ERR_UNSUPPORTED.
+ * Positions are rewritten, so a key copy kept for rkv_decode_sparq (keys_t) starts again
+ * from zero afterwards.  Caches of more than 393216 tokens per sequence (max_pages *
+ * page_size) return RKV_ERR_UNSUPPORTED.
  */
 rkv_status rkv_evict_accum(const rkv_cache* cache, float* acc, int32_t acc_stride, const int32_t* keep,
                            int32_t recent, int32_t* kept_idx, int32_t kept_stride, const rkv_cache* dst,

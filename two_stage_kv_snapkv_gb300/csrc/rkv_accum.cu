@@ -529,150 +529,150 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
     }
   } else {
     if (warp == 16) {
-    if (elect_lane()) {  // one lane: a copy issued from converged code costs 90 clocks
-      const int pages = kAmKeys >> p.pshift, box = p.P * 128;
-      for (bool more = tiles_find(p, tt, nq, x0, x0, x1, r); ok && more; more = tiles_next(p, tt, nq, x1, r)) {
-        const int n = tt.n[r.b], s = units % KS;
-        // the unit's page ids: the table's rows are whole groups of eight
-        int ids[16];
-        const int* at = p.page_table + (size_t)r.b * p.max_pages + r.j * pages;
+      if (elect_lane()) {  // one lane: a copy issued from converged code costs 90 clocks
+        const int pages = kAmKeys >> p.pshift, box = p.P * 128;
+        for (bool more = tiles_find(p, tt, nq, x0, x0, x1, r); ok && more; more = tiles_next(p, tt, nq, x1, r)) {
+          const int n = tt.n[r.b], s = units % KS;
+          // the unit's page ids: the table's rows are whole groups of eight
+          int ids[16];
+          const int* at = p.page_table + (size_t)r.b * p.max_pages + r.j * pages;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          int4 id = make_int4(-1, -1, -1, -1);
-          if (4 * q < pages && (r.j * pages + 4 * q) * p.P < n) id = *reinterpret_cast<const int4*>(at + 4 * q);
-          ids[4 * q] = id.x;
-          ids[4 * q + 1] = id.y;
-          ids[4 * q + 2] = id.z;
-          ids[4 * q + 3] = id.w;
+          for (int q = 0; q < 4; ++q) {
+            int4 id = make_int4(-1, -1, -1, -1);
+            if (4 * q < pages && (r.j * pages + 4 * q) * p.P < n) id = *reinterpret_cast<const int4*>(at + 4 * q);
+            ids[4 * q] = id.x;
+            ids[4 * q + 1] = id.y;
+            ids[4 * q + 2] = id.z;
+            ids[4 * q + 3] = id.w;
+          }
+          uint32_t have = 0;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (j < pages && (r.j * pages + j) * p.P < n) {
+              if (ids[j] >= 0 && ids[j] < p.num_phys) have |= 1u << j;
+              else flag_error(p.err, RKV_DEVERR_PAGE_ID);
+            }
+          if (units >= KS && !(ok = wait_one(&kempty[s], units / KS - 1))) break;
+          if (have) mbar_arrive_expect_tx(&kfull[s], __popc(have) * 2 * box);
+          else mbar_arrive(&kfull[s]);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if ((have >> j) & 1u) {
+              const int in = j * p.P, row = (ids[j] * p.Hkv + r.g) * p.P;  // row of the unit's 256, of the pool
+              uint8_t* to = ks + s * 65536 + (in >> 7) * 32768 + (in & 127) * 128;
+              tma_load_2d(to, &p.tmk, 0, row, &kfull[s]);
+              tma_load_2d(to + 16384, &p.tmk, 64, row, &kfull[s]);
+            }
+          ++units;
+          int h = r.lo > 0 ? r.lo / r.width : 0, rt = r.f + r.lo - h * r.width;
+          for (int o = r.lo; o < r.hi; ++o) {
+            const int t = tiles % kAmQ;
+            if (tiles >= kAmQ && !(ok = wait_one(&qempty[t], tiles / kAmQ - 1))) break;
+            const int row = (r.b * p.Hq + r.g * p.G + h) * p.T + rt * nq;
+            mbar_arrive_expect_tx(&qfull[t], nq * 256);
+            tma_load_2d(qs + t * QB, &p.tmq, 0, row, &qfull[t]);
+            tma_load_2d(qs + t * QB + QB / 2, &p.tmq, 64, row, &qfull[t]);
+            ++tiles;
+            if (++rt == r.f + r.width) {
+              rt = r.f;
+              ++h;
+            }
+          }
         }
-        uint32_t have = 0;
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (j < pages && (r.j * pages + j) * p.P < n) {
-            if (ids[j] >= 0 && ids[j] < p.num_phys) have |= 1u << j;
-            else flag_error(p.err, RKV_DEVERR_PAGE_ID);
-          }
-        if (units >= KS && !(ok = wait_one(&kempty[s], units / KS - 1))) break;
-        if (have) mbar_arrive_expect_tx(&kfull[s], __popc(have) * 2 * box);
-        else mbar_arrive(&kfull[s]);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if ((have >> j) & 1u) {
-            const int in = j * p.P, row = (ids[j] * p.Hkv + r.g) * p.P;  // row of the unit's 256, of the pool
-            uint8_t* to = ks + s * 65536 + (in >> 7) * 32768 + (in & 127) * 128;
-            tma_load_2d(to, &p.tmk, 0, row, &kfull[s]);
-            tma_load_2d(to + 16384, &p.tmk, 64, row, &kfull[s]);
-          }
+      }
+    } else if (warp == 17) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, nq);
+      const bool lead = elect_lane();
+      const uint32_t klo = sw128_kmajor_lo(smem_u32(ks)), qlo = sw128_kmajor_lo(smem_u32(qs));
+      const uint32_t onelo = plain_kmajor_lo(smem_u32(ones)), biaslo = plain_kmajor_lo(smem_u32(bias));
+      // The waits stand where products are still queued: inside a unit a query tile is waited
+      // for before the second key tile of the one before it is issued.  (Not across units: the
+      // next unit's keys, and its query tiles behind them, wait for this unit's products.)
+      for (bool more = tiles_find(p, tt, nq, x0, x0, x1, r); ok && more; more = tiles_next(p, tt, nq, x1, r)) {
+        const int s = units % KS;
+        if (!(ok = wait(&kfull[s], units / KS))) break;
         ++units;
-        int h = r.lo > 0 ? r.lo / r.width : 0, rt = r.f + r.lo - h * r.width;
+        if (!(ok = wait(&qfull[tiles % kAmQ], tiles / kAmQ))) break;
         for (int o = r.lo; o < r.hi; ++o) {
-          const int t = tiles % kAmQ;
-          if (tiles >= kAmQ && !(ok = wait_one(&qempty[t], tiles / kAmQ - 1))) break;
-          const int row = (r.b * p.Hq + r.g * p.G + h) * p.T + rt * nq;
-          mbar_arrive_expect_tx(&qfull[t], nq * 256);
-          tma_load_2d(qs + t * QB, &p.tmq, 0, row, &qfull[t]);
-          tma_load_2d(qs + t * QB + QB / 2, &p.tmq, 64, row, &qfull[t]);
+          const int t = tiles % kAmQ, d = tiles & 1;
+          const uint32_t q = qlo + t * (QB >> 4);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (w == 1 && o + 1 < r.hi && !(ok = wait(&qfull[(tiles + 1) % kAmQ], (tiles + 1) / kAmQ))) break;
+            if (tiles >= 2 && !(ok = wait(&sempty[d][w], tiles / 2 - 1))) break;
+            tc_fence_after();
+            const uint32_t to = tmem + d * 256 + w * 128, key = klo + s * (65536 >> 4) + w * (32768 >> 4);
+            tc_mma_ss<false>(lead, to, key, q, idesc);
+#pragma unroll
+            for (int k = 1; k < 8; ++k) {
+              const uint32_t in = (k & 3) * 32;
+              tc_mma_ss<true>(lead, to, key + (((k >> 2) * 16384 + in) >> 4), q + (((k >> 2) * (QB / 2) + in) >> 4), idesc);
+            }
+            tc_mma_ss<true, kPlainDescHi>(lead, to, onelo, biaslo + t * (kAmExtra >> 4), idesc);
+            tc_commit_if(lead, &sfull[d][w]);
+          }
+          if (!ok) break;
+          tc_commit_if(lead, &qempty[t]);
+          tc_commit_if(lead && o + 1 == r.hi, &kempty[s]);
+          __syncwarp();
           ++tiles;
-          if (++rt == r.f + r.width) {
-            rt = r.f;
+        }
+      }
+      if (ok) {  // the last releases land before the CTA may exit
+        for (int i = max(0, tiles - kAmQ); i < tiles; ++i) mbar_wait(&qempty[i % kAmQ], (uint32_t)((i / kAmQ) & 1));
+        for (int i = max(0, units - KS); i < units; ++i) mbar_wait(&kempty[i % KS], (uint32_t)((i / KS) & 1));
+      }
+    } else {
+      // two warps take the query tiles in turn; a tile's log-sum-exps are loaded while the
+      // one before it (of this warp) is still being written
+      const float inv = 1.f / p.scale;
+      int before = 0;  // tiles of the runs before
+      for (bool more = tiles_find(p, tt, nq, x0, x0, x1, r); ok && more; more = tiles_next(p, tt, nq, x1, r)) {
+        const int m = tt.m[r.b];
+        int o = r.lo + ((before + warp) & 1);  // warp 18 takes the even tiles of the CTA
+        int h = o / r.width, rt = r.f + o - h * r.width;
+        auto load = [&](float(&v)[4]) {
+          const int i0 = rt * nq;
+          const float* src = p.lse + ((size_t)r.b * p.Hq + r.g * p.G + h) * p.T + i0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = o < r.hi && lane + 32 * e < min(nq, m - i0) ? src[lane + 32 * e] : -INFINITY;
+        };
+        float next[4];
+        load(next);
+        while (o < r.hi) {
+          const int tile = before + o - r.lo, t = tile % kAmQ;
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = next[e];
+          o += 2;
+          rt += 2;
+          while (rt >= r.f + r.width) {
+            rt -= r.width;
             ++h;
           }
-        }
-      }
-    }
-  } else if (warp == 17) {
-    constexpr uint32_t idesc = idesc_bf16_f32(128, nq);
-    const bool lead = elect_lane();
-    const uint32_t klo = sw128_kmajor_lo(smem_u32(ks)), qlo = sw128_kmajor_lo(smem_u32(qs));
-    const uint32_t onelo = plain_kmajor_lo(smem_u32(ones)), biaslo = plain_kmajor_lo(smem_u32(bias));
-    // The waits stand where products are still queued: inside a unit a query tile is waited
-    // for before the second key tile of the one before it is issued.  (Not across units: the
-    // next unit's keys, and its query tiles behind them, wait for this unit's products.)
-    for (bool more = tiles_find(p, tt, nq, x0, x0, x1, r); ok && more; more = tiles_next(p, tt, nq, x1, r)) {
-      const int s = units % KS;
-      if (!(ok = wait(&kfull[s], units / KS))) break;
-      ++units;
-      if (!(ok = wait(&qfull[tiles % kAmQ], tiles / kAmQ))) break;
-      for (int o = r.lo; o < r.hi; ++o) {
-        const int t = tiles % kAmQ, d = tiles & 1;
-        const uint32_t q = qlo + t * (QB >> 4);
+          load(next);
+          // -lse / scale in three bf16 terms (a row that weighs nothing: a huge negative one)
+          uint2 w[4];
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (w == 1 && o + 1 < r.hi && !(ok = wait(&qfull[(tiles + 1) % kAmQ], (tiles + 1) / kAmQ))) break;
-          if (tiles >= 2 && !(ok = wait(&sempty[d][w], tiles / 2 - 1))) break;
-          tc_fence_after();
-          const uint32_t to = tmem + d * 256 + w * 128, key = klo + s * (65536 >> 4) + w * (32768 >> 4);
-          tc_mma_ss<false>(lead, to, key, q, idesc);
-#pragma unroll
-          for (int k = 1; k < 8; ++k) {
-            const uint32_t in = (k & 3) * 32;
-            tc_mma_ss<true>(lead, to, key + (((k >> 2) * 16384 + in) >> 4), q + (((k >> 2) * (QB / 2) + in) >> 4), idesc);
+          for (int e = 0; e < 4; ++e) {
+            float a = v[e] == -INFINITY ? -1e30f : -v[e] * inv;
+            a = a > 1e30f ? 1e30f : (a < -1e30f ? -1e30f : a);  // a NaN stays one
+            const float hi = __bfloat162float(__float2bfloat16_rn(a)), r1 = a - hi;
+            const float mid = __bfloat162float(__float2bfloat16_rn(r1));
+            w[e] = make_uint2(pack_bf16x2(hi, mid), pack_bf16x2(r1 - mid, 0.f));
           }
-          tc_mma_ss<true, kPlainDescHi>(lead, to, onelo, biaslo + t * (kAmExtra >> 4), idesc);
-          tc_commit_if(lead, &sfull[d][w]);
+          if (tile >= kAmQ && !(ok = wait(&qempty[t], tile / kAmQ - 1))) break;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = lane + 32 * e;
+            if (row < nq) *reinterpret_cast<uint2*>(bias + t * kAmExtra + (row >> 3) * 256 + (row & 7) * 16) = w[e];
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&qfull[t]);
         }
-        if (!ok) break;
-        tc_commit_if(lead, &qempty[t]);
-        tc_commit_if(lead && o + 1 == r.hi, &kempty[s]);
-        __syncwarp();
-        ++tiles;
+        before += r.hi - r.lo;
       }
-    }
-    if (ok) {  // the last releases land before the CTA may exit
-      for (int i = max(0, tiles - kAmQ); i < tiles; ++i) mbar_wait(&qempty[i % kAmQ], (uint32_t)((i / kAmQ) & 1));
-      for (int i = max(0, units - KS); i < units; ++i) mbar_wait(&kempty[i % KS], (uint32_t)((i / KS) & 1));
-    }
-  } else {
-    // two warps take the query tiles in turn; a tile's log-sum-exps are loaded while the
-    // one before it (of this warp) is still being written
-    const float inv = 1.f / p.scale;
-    int before = 0;  // tiles of the runs before
-    for (bool more = tiles_find(p, tt, nq, x0, x0, x1, r); ok && more; more = tiles_next(p, tt, nq, x1, r)) {
-      const int m = tt.m[r.b];
-      int o = r.lo + ((before + warp) & 1);  // warp 18 takes the even tiles of the CTA
-      int h = o / r.width, rt = r.f + o - h * r.width;
-      auto load = [&](float(&v)[4]) {
-        const int i0 = rt * nq;
-        const float* src = p.lse + ((size_t)r.b * p.Hq + r.g * p.G + h) * p.T + i0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          v[e] = o < r.hi && lane + 32 * e < min(nq, m - i0) ? src[lane + 32 * e] : -INFINITY;
-      };
-      float next[4];
-      load(next);
-      while (o < r.hi) {
-        const int tile = before + o - r.lo, t = tile % kAmQ;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = next[e];
-        o += 2;
-        rt += 2;
-        while (rt >= r.f + r.width) {
-          rt -= r.width;
-          ++h;
-        }
-        load(next);
-        // -lse / scale in three bf16 terms (a row that weighs nothing: a huge negative one)
-        uint2 w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float a = v[e] == -INFINITY ? -1e30f : -v[e] * inv;
-          a = a > 1e30f ? 1e30f : (a < -1e30f ? -1e30f : a);  // a NaN stays one
-          const float hi = __bfloat162float(__float2bfloat16_rn(a)), r1 = a - hi;
-          const float mid = __bfloat162float(__float2bfloat16_rn(r1));
-          w[e] = make_uint2(pack_bf16x2(hi, mid), pack_bf16x2(r1 - mid, 0.f));
-        }
-        if (tile >= kAmQ && !(ok = wait(&qempty[t], tile / kAmQ - 1))) break;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = lane + 32 * e;
-          if (row < nq) *reinterpret_cast<uint2*>(bias + t * kAmExtra + (row >> 3) * 256 + (row & 7) * 16) = w[e];
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&qfull[t]);
-      }
-      before += r.hi - r.lo;
-    }
     }
   }
 

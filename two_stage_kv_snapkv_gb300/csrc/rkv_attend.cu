@@ -1149,221 +1149,221 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
   } else {
     setmaxnreg_dec<kAtIssueRegs>();
     if (warp == 8 || warp == 10) {
-    // warp 8 fetches K, warp 10 V; entry of K_i / V_i among a run's 2 nt entries:
-    // wide K_i 2 i, V_i 2 i + 1; narrow K_0, then K_(i+1) and V_i for every i
-    const bool v = warp == 10;
-    const CUtensorMap* map = v ? &p.tmv : &p.tmk;
-    const CUtensorMap* tmap = v ? &p.tmvt : &p.tmkt;
-    const bool lead = elect_lane();
-    const int pages = kAtKeys >> p.pshift, box = p.P * 128;  // pages of a tile, bytes of a box
-    // one row tile: nobody reads the cache again (the wide form measured 267 us with this
-    // and 255 without, 63 nodes over the ragged batch; the narrow one 33 against 37)
-    const uint64_t policy = l2_policy(!kWide && p.T * p.G <= R);
-    int before = 0;                                          // entries of the runs before
-    bool ok = true;
-    for (long long x = x0; ok && next_run(x, r); x = r.next) {
-      const int b = r.b, g = r.unit % p.Hkv, n = r.n, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
-      // lane j: page id of the tile's page j, -1: none; loaded a tile ahead and judged only
-      // when it is used, so that the load's latency stays off the ring
-      auto page_of = [&](int tile) {
-        const int pg = tile * pages + lane;
-        return tile < nc && lane < pages && pg * p.P < n ? p.page_table[(size_t)b * p.max_pages + pg] : -1;
-      };
-      int next = page_of(r.lo);
-      for (int i = 0; i < nt; ++i) {
-        const int tile = r.lo + i;
-        int phys = next;
-        next = i + 1 < nt ? page_of(tile + 1) : -1;
-        const int at = before + (kWide ? 2 * i + v : (v ? (i + 1 < nt ? 2 * i + 2 : 2 * nt - 1) : (i > 0 ? 2 * i - 1 : 0)));
-        const int e = at % E;
-        const bool late = at >= E && !mbar_wait_role(&empty_b[e], (uint32_t)((at / E - 1) & 1), &abort_flag);
+      // warp 8 fetches K, warp 10 V; entry of K_i / V_i among a run's 2 nt entries:
+      // wide K_i 2 i, V_i 2 i + 1; narrow K_0, then K_(i+1) and V_i for every i
+      const bool v = warp == 10;
+      const CUtensorMap* map = v ? &p.tmv : &p.tmk;
+      const CUtensorMap* tmap = v ? &p.tmvt : &p.tmkt;
+      const bool lead = elect_lane();
+      const int pages = kAtKeys >> p.pshift, box = p.P * 128;  // pages of a tile, bytes of a box
+      // one row tile: nobody reads the cache again (the wide form measured 267 us with this
+      // and 255 without, 63 nodes over the ragged batch; the narrow one 33 against 37)
+      const uint64_t policy = l2_policy(!kWide && p.T * p.G <= R);
+      int before = 0;                                          // entries of the runs before
+      bool ok = true;
+      for (long long x = x0; ok && next_run(x, r); x = r.next) {
+        const int b = r.b, g = r.unit % p.Hkv, n = r.n, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
+        // lane j: page id of the tile's page j, -1: none; loaded a tile ahead and judged only
+        // when it is used, so that the load's latency stays off the ring
+        auto page_of = [&](int tile) {
+          const int pg = tile * pages + lane;
+          return tile < nc && lane < pages && pg * p.P < n ? p.page_table[(size_t)b * p.max_pages + pg] : -1;
+        };
+        int next = page_of(r.lo);
+        for (int i = 0; i < nt; ++i) {
+          const int tile = r.lo + i;
+          int phys = next;
+          next = i + 1 < nt ? page_of(tile + 1) : -1;
+          const int at = before + (kWide ? 2 * i + v : (v ? (i + 1 < nt ? 2 * i + 2 : 2 * nt - 1) : (i > 0 ? 2 * i - 1 : 0)));
+          const int e = at % E;
+          const bool late = at >= E && !mbar_wait_role(&empty_b[e], (uint32_t)((at / E - 1) & 1), &abort_flag);
+          if (__any_sync(0xffffffffu, late)) {
+            give_up();
+            ok = false;
+            break;
+          }
+          uint8_t* const st = ring + e * kAtEntry;
+          const uint32_t st32 = smem_u32(st), bar32 = smem_u32(&full_b[e]);
+          if (tile < nc) {
+            if (phys < 0 || phys >= p.num_phys) {
+              if (lane < pages && (tile * pages + lane) * p.P < n) flag_error(p.err, RKV_DEVERR_PAGE_ID);
+              phys = -1;
+            }
+            const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0);
+            if (lead) {
+              if (!v) {
+                uint32_t gr = 0;  // a page is P / 16 groups
+                for (int j = 0; j < pages; ++j)
+                  if ((have >> j) & 1u) gr |= ((1u << (p.P >> 4)) - 1u) << (j * (p.P >> 4));
+                groups[e] = gr;
+              }
+              if (have) mbar_arrive_expect_tx(&full_b[e], __popc(have) * 2 * box);
+              else mbar_arrive(&full_b[e]);
+            }
+            __syncwarp();
+            int row[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) row[j] = (__shfl_sync(0xffffffffu, phys, j) * p.Hkv + g) * p.P;
+            if (kWide) {
+              // The wide form is bound by the products and the card's power: boxes issued from
+              // converged code, 90 clocks each, measured 406 us against 429 from one lane.
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                tma_load_2d_if(lead && ((have >> j) & 1u), st32 + j * box, map, 0, row[j], bar32);
+                tma_load_2d_if(lead && ((have >> j) & 1u), st32 + kAtEntry / 2 + j * box, map, 64, row[j], bar32);
+              }
+            } else if (lead) {  // the narrow one by the copies: 320 us from one lane against 364 (8 nodes, 8 x 64K)
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if ((have >> j) & 1u) {
+                  tma_load_2d_hint(st + j * box, map, 0, row[j], &full_b[e], policy);
+                  tma_load_2d_hint(st + kAtEntry / 2 + j * box, map, 64, row[j], &full_b[e], policy);
+                }
+            }
+          } else {
+            const int row = (b * p.Hkv + g) * p.T + (tile - nc) * kAtKeys;
+            if (lead) {
+              if (!v) groups[e] = 0xffu;
+              mbar_arrive_expect_tx(&full_b[e], kAtEntry);
+            }
+            __syncwarp();
+            if (lead) {
+              tma_load_2d(st, tmap, 0, row, &full_b[e]);
+              tma_load_2d(st + kAtEntry / 2, tmap, 64, row, &full_b[e]);
+            }
+          }
+          loaded = at + 1;
+        }
+        before += 2 * nt;
+      }
+    } else if (warp == 9) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128), idesc_o = idesc_s | kIdescBNMajor;
+      const uint32_t q32 = smem_u32(qs), ring32 = smem_u32(ring);
+      int seen_p[2] = {0, 0}, runs[2] = {0, 0};
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int phase) {
+        const bool late = !mbar_wait_role(bar, (uint32_t)(phase & 1), &abort_flag);
         if (__any_sync(0xffffffffu, late)) {
           give_up();
-          ok = false;
-          break;
+          return false;
         }
-        uint8_t* const st = ring + e * kAtEntry;
-        const uint32_t st32 = smem_u32(st), bar32 = smem_u32(&full_b[e]);
-        if (tile < nc) {
-          if (phys < 0 || phys >= p.num_phys) {
-            if (lane < pages && (tile * pages + lane) * p.P < n) flag_error(p.err, RKV_DEVERR_PAGE_ID);
-            phys = -1;
-          }
-          const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0);
-          if (lead) {
-            if (!v) {
-              uint32_t gr = 0;  // a page is P / 16 groups
-              for (int j = 0; j < pages; ++j)
-                if ((have >> j) & 1u) gr |= ((1u << (p.P >> 4)) - 1u) << (j * (p.P >> 4));
-              groups[e] = gr;
-            }
-            if (have) mbar_arrive_expect_tx(&full_b[e], __popc(have) * 2 * box);
-            else mbar_arrive(&full_b[e]);
-          }
-          __syncwarp();
-          int row[8];
+        return true;
+      };
+      const bool lead = elect_lane();
+      const uint32_t qlo = sw128_kmajor_lo(q32), klo = sw128_kmajor_lo(ring32), vlo = sw128_nmajor_lo(ring32, kAtEntry / 2);
+      // S of `slot` from the K entry e (its copy has landed)
+      auto mma_s = [&](int slot, int e, bool release) {
+        tc_fence_after();
+        if (lead) sgroups[slot] = groups[e];
+        const uint32_t d = tmem + slot * 256, qa = qlo + (kWide ? slot * (128 * 256 >> 4) : 0), ka = klo + e * (kAtEntry >> 4);
+        tc_mma_ss<false>(lead, d, qa, ka, idesc_s);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) row[j] = (__shfl_sync(0xffffffffu, phys, j) * p.Hkv + g) * p.P;
-          if (kWide) {
-            // The wide form is bound by the products and the card's power: boxes issued from
-            // converged code, 90 clocks each, measured 406 us against 429 from one lane.
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              tma_load_2d_if(lead && ((have >> j) & 1u), st32 + j * box, map, 0, row[j], bar32);
-              tma_load_2d_if(lead && ((have >> j) & 1u), st32 + kAtEntry / 2 + j * box, map, 64, row[j], bar32);
-            }
-          } else if (lead) {  // the narrow one by the copies: 320 us from one lane against 364 (8 nodes, 8 x 64K)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if ((have >> j) & 1u) {
-                tma_load_2d_hint(st + j * box, map, 0, row[j], &full_b[e], policy);
-                tma_load_2d_hint(st + kAtEntry / 2 + j * box, map, 64, row[j], &full_b[e], policy);
-              }
-          }
-        } else {
-          const int row = (b * p.Hkv + g) * p.T + (tile - nc) * kAtKeys;
-          if (lead) {
-            if (!v) groups[e] = 0xffu;
-            mbar_arrive_expect_tx(&full_b[e], kAtEntry);
-          }
-          __syncwarp();
-          if (lead) {
-            tma_load_2d(st, tmap, 0, row, &full_b[e]);
-            tma_load_2d(st + kAtEntry / 2, tmap, 64, row, &full_b[e]);
-          }
+        for (int k = 1; k < 8; ++k) {
+          const uint32_t off = ((k >> 2) * (kAtEntry / 2) + (k & 3) * 32) >> 4;
+          tc_mma_ss<true>(lead, d, qa + off, ka + off, idesc_s);
         }
-        loaded = at + 1;
-      }
-      before += 2 * nt;
-    }
-  } else if (warp == 9) {
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128), idesc_o = idesc_s | kIdescBNMajor;
-    const uint32_t q32 = smem_u32(qs), ring32 = smem_u32(ring);
-    int seen_p[2] = {0, 0}, runs[2] = {0, 0};
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, int phase) {
-      const bool late = !mbar_wait_role(bar, (uint32_t)(phase & 1), &abort_flag);
-      if (__any_sync(0xffffffffu, late)) {
-        give_up();
-        return false;
-      }
-      return true;
-    };
-    const bool lead = elect_lane();
-    const uint32_t qlo = sw128_kmajor_lo(q32), klo = sw128_kmajor_lo(ring32), vlo = sw128_nmajor_lo(ring32, kAtEntry / 2);
-    // S of `slot` from the K entry e (its copy has landed)
-    auto mma_s = [&](int slot, int e, bool release) {
-      tc_fence_after();
-      if (lead) sgroups[slot] = groups[e];
-      const uint32_t d = tmem + slot * 256, qa = qlo + (kWide ? slot * (128 * 256 >> 4) : 0), ka = klo + e * (kAtEntry >> 4);
-      tc_mma_ss<false>(lead, d, qa, ka, idesc_s);
-#pragma unroll
-      for (int k = 1; k < 8; ++k) {
-        const uint32_t off = ((k >> 2) * (kAtEntry / 2) + (k & 3) * 32) >> 4;
-        tc_mma_ss<true>(lead, d, qa + off, ka + off, idesc_s);
-      }
-      tc_commit_if(lead && release, &empty_b[e]);
-      tc_commit_if(lead, &s_b[slot]);
-      if (lead) mbar_arrive(&s_b[slot]);
-      __syncwarp();
-    };
-    // O += P V once the slot's weights are there (handed over in two halves, the issuing
-    // warp waited twice and the other slot with it: 480 us against 410 for 64 nodes, 8 x 64K)
-    auto mma_o = [&](int slot, int e, bool first, bool last, bool release) {
-      if (!(ok = wait(&p_b[slot], seen_p[slot]++))) return;
-      tc_fence_after();
-      const uint32_t d = tmem + slot * 256 + 128, pa = tmem + slot * 256, va = vlo + e * (kAtEntry >> 4);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        tc_mma_ts(lead, d, pa + k * 8, va + (k * 2048 >> 4), idesc_o, (first && k == 0) ? 0u : 1u);
-      tc_commit_if(lead && release, &empty_b[e]);
-      tc_commit_if(lead && last, &o_b[slot]);
-    };
-    for (long long x = x0; ok && next_run(x, r); x = r.next) {
-      const int n = r.n, nodes = r.t, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
-      const bool two = kWide && nodes * p.G - (r.unit / p.Hkv) * R > 128;  // slot 1 has rows
-      // keys of a tile that may hold anything (behind the end, on a bad page) have weight 0,
-      // and 0 x NaN is not 0: their V rows are cleared first
-      auto clean_v = [&](int tile, int e, uint32_t gr) {
-        const int left = tile < nc ? n - tile * kAtKeys : nodes - (tile - nc) * kAtKeys;
-        if (left >= kAtKeys && gr == 0xffu) return;
-        for (int i = lane; i < 128 * 16; i += 32) {
-          const int row = i >> 4;
-          if (row < left && ((gr >> (row >> 4)) & 1u)) continue;
-          *reinterpret_cast<uint4*>(ring + e * kAtEntry + ((i >> 3) & 1) * (kAtEntry / 2) + row * 128 + (i & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
+        tc_commit_if(lead && release, &empty_b[e]);
+        tc_commit_if(lead, &s_b[slot]);
+        if (lead) mbar_arrive(&s_b[slot]);
         __syncwarp();
       };
-      auto take = [&]() {  // the next ring entry, landed
-        const int e = loaded % E;
-        ok = wait(&full_b[e], loaded / E);
-        ++loaded;
-        return e;
+      // O += P V once the slot's weights are there (handed over in two halves, the issuing
+      // warp waited twice and the other slot with it: 480 us against 410 for 64 nodes, 8 x 64K)
+      auto mma_o = [&](int slot, int e, bool first, bool last, bool release) {
+        if (!(ok = wait(&p_b[slot], seen_p[slot]++))) return;
+        tc_fence_after();
+        const uint32_t d = tmem + slot * 256 + 128, pa = tmem + slot * 256, va = vlo + e * (kAtEntry >> 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc_mma_ts(lead, d, pa + k * 8, va + (k * 2048 >> 4), idesc_o, (first && k == 0) ? 0u : 1u);
+        tc_commit_if(lead && release, &empty_b[e]);
+        tc_commit_if(lead && last, &o_b[slot]);
       };
-      ok = wait(&q_b[0], runs[0]++);
-      if (kWide && ok) ok = wait(&q_b[1], runs[1]++);
-      if (!ok) break;
-      if (kWide) {
-        int ek = take();
+      for (long long x = x0; ok && next_run(x, r); x = r.next) {
+        const int n = r.n, nodes = r.t, nc = (n + kAtKeys - 1) / kAtKeys, nt = r.hi - r.lo;
+        const bool two = kWide && nodes * p.G - (r.unit / p.Hkv) * R > 128;  // slot 1 has rows
+        // keys of a tile that may hold anything (behind the end, on a bad page) have weight 0,
+        // and 0 x NaN is not 0: their V rows are cleared first
+        auto clean_v = [&](int tile, int e, uint32_t gr) {
+          const int left = tile < nc ? n - tile * kAtKeys : nodes - (tile - nc) * kAtKeys;
+          if (left >= kAtKeys && gr == 0xffu) return;
+          for (int i = lane; i < 128 * 16; i += 32) {
+            const int row = i >> 4;
+            if (row < left && ((gr >> (row >> 4)) & 1u)) continue;
+            *reinterpret_cast<uint4*>(ring + e * kAtEntry + ((i >> 3) & 1) * (kAtEntry / 2) + row * 128 + (i & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        };
+        auto take = [&]() {  // the next ring entry, landed
+          const int e = loaded % E;
+          ok = wait(&full_b[e], loaded / E);
+          ++loaded;
+          return e;
+        };
+        ok = wait(&q_b[0], runs[0]++);
+        if (kWide && ok) ok = wait(&q_b[1], runs[1]++);
         if (!ok) break;
-        uint32_t gr = groups[ek];
-        mma_s(0, ek, !two);
-        if (two) mma_s(1, ek, true);
-        for (int i = 0; i < nt; ++i) {
-          const int ev = take();
+        if (kWide) {
+          int ek = take();
           if (!ok) break;
-          clean_v(r.lo + i, ev, gr);
-          const bool last = i + 1 == nt;
-          mma_o(0, ev, i == 0, last, !two);
-          if (!ok) break;
-          if (kWide) tc_commit_if(lead && last && !two, &o_b[1]);  // keeps an idle slot in step
-          int en = 0;
-          if (!last) {
-            en = take();
+          uint32_t gr = groups[ek];
+          mma_s(0, ek, !two);
+          if (two) mma_s(1, ek, true);
+          for (int i = 0; i < nt; ++i) {
+            const int ev = take();
             if (!ok) break;
-            gr = groups[en];
-            mma_s(0, en, !two);
-          }
-          if (two) {
-            mma_o(1, ev, i == 0, last, true);
+            clean_v(r.lo + i, ev, gr);
+            const bool last = i + 1 == nt;
+            mma_o(0, ev, i == 0, last, !two);
             if (!ok) break;
-            if (!last) mma_s(1, en, true);
+            if (kWide) tc_commit_if(lead && last && !two, &o_b[1]);  // keeps an idle slot in step
+            int en = 0;
+            if (!last) {
+              en = take();
+              if (!ok) break;
+              gr = groups[en];
+              mma_s(0, en, !two);
+            }
+            if (two) {
+              mma_o(1, ev, i == 0, last, true);
+              if (!ok) break;
+              if (!last) mma_s(1, en, true);
+            }
           }
-        }
-      } else {
-        uint32_t gr[2];
-        const int e0 = take();
-        if (!ok) break;
-        gr[0] = groups[e0];
-        mma_s(0, e0, true);
-        for (int i = 0; i < nt; ++i) {
-          // order of the entries: K_0, then K_(i+1) and V_i for every i
-          const int slot = i & 1;
-          int en = 0;
-          uint32_t gn = 0;
-          if (i + 1 < nt) {
-            en = take();
+        } else {
+          uint32_t gr[2];
+          const int e0 = take();
+          if (!ok) break;
+          gr[0] = groups[e0];
+          mma_s(0, e0, true);
+          for (int i = 0; i < nt; ++i) {
+            // order of the entries: K_0, then K_(i+1) and V_i for every i
+            const int slot = i & 1;
+            int en = 0;
+            uint32_t gn = 0;
+            if (i + 1 < nt) {
+              en = take();
+              if (!ok) break;
+              gn = groups[en];
+              if (i == 0) mma_s(1, en, true);
+            }
+            // tile i + 1's logits go where tile i - 1's weights lay: its product was issued before
+            if (i + 1 < nt && i > 0) mma_s(slot ^ 1, en, true);
+            const int ev = take();
             if (!ok) break;
-            gn = groups[en];
-            if (i == 0) mma_s(1, en, true);
+            clean_v(r.lo + i, ev, gr[slot]);
+            if (i + 1 < nt) gr[slot ^ 1] = gn;
+            mma_o(slot, ev, i < 2, i + 2 >= nt, true);
+            if (!ok) break;
           }
-          // tile i + 1's logits go where tile i - 1's weights lay: its product was issued before
-          if (i + 1 < nt && i > 0) mma_s(slot ^ 1, en, true);
-          const int ev = take();
-          if (!ok) break;
-          clean_v(r.lo + i, ev, gr[slot]);
-          if (i + 1 < nt) gr[slot ^ 1] = gn;
-          mma_o(slot, ev, i < 2, i + 2 >= nt, true);
-          if (!ok) break;
         }
       }
+      // the last entries' releases land before the CTA may exit
+      if (ok)
+        for (int i = loaded > E ? loaded - E : 0; i < loaded; ++i) mbar_wait(&empty_b[i % E], (uint32_t)((i / E) & 1));
     }
-    // the last entries' releases land before the CTA may exit
-    if (ok)
-      for (int i = loaded > E ? loaded - E : 0; i < loaded; ++i) mbar_wait(&empty_b[i % E], (uint32_t)((i / E) & 1));
-  }
   }
 
   // teardown: after a timeout, wait (bounded) for the copies and products still in flight
