@@ -10,6 +10,7 @@
 #include <stdint.h>
 
 #include "rkv.h"
+#include "rkv_bins.h"
 
 namespace rkv {
 
@@ -419,7 +420,6 @@ __device__ __forceinline__ void flag_error(int32_t* word, int32_t bit) {
 // shared-memory reads then hit distinct banks, a run of equal keys adds to the
 // histogram once, and the compaction is one pass with one block scan.  `key(i)` is
 // called several times for each i in [0, n); every thread of the block calls this.
-constexpr int kTkBins = 1024;
 constexpr int kTkCand = 32;
 constexpr int kTkCandFlat = 64;  // the candidate cap of topk_flat (two ranking warps)
 template <int NT, int NBINS = kTkBins>
@@ -469,8 +469,7 @@ __device__ void topk_adaptive_fn(int n, int k, KeyFn key, TopkSmem<NT>& ts, Take
   // 2. shrink [lo, hi]; `need` of the `nin` keys inside it are taken
   int need = k, nin = n;
   while (nin > kTkCand && lo != hi) {
-    const uint32_t range = hi - lo;
-    const int shift = range < (uint32_t)kTkBins ? 0 : (32 - __clz(range)) - 10;  // (range >> shift) < 1024
+    const int shift = tk_shift(hi - lo);
     for (int i = tid; i < kTkBins; i += NT) ts.hist[i] = 0u;
     __syncthreads();
     int run_bin = -1, run = 0;
@@ -529,7 +528,7 @@ __device__ void topk_adaptive_fn(int n, int k, KeyFn key, TopkSmem<NT>& ts, Take
     }
     __syncthreads();
     const uint32_t nlo = lo + ((uint32_t)ts.bstar << shift);
-    hi = shift == 0 ? nlo : min(hi, nlo + ((1u << shift) - 1u));
+    hi = tk_upper(nlo, hi, shift);
     lo = nlo;
     need = ts.need;
     nin = ts.nb;
@@ -716,8 +715,7 @@ __device__ void topk_flat(const uint32_t* keys, int n, int k, TopkSmem<NT>& ts, 
       __syncthreads();
     }
     cleared = false;
-    const uint32_t range = hi - lo;
-    const int shift = range < (uint32_t)kTkBins ? 0 : (32 - __clz(range)) - 10;
+    const int shift = tk_shift(hi - lo);
 #pragma unroll 1
     for (int q = 0; q < Q; ++q) {
       const uint4 v = k4[q];
@@ -768,7 +766,7 @@ __device__ void topk_flat(const uint32_t* keys, int n, int k, TopkSmem<NT>& ts, 
     }
     __syncthreads();
     const uint32_t nlo = lo + ((uint32_t)ts.bstar << shift);
-    hi = shift == 0 ? nlo : min(hi, nlo + ((1u << shift) - 1u));
+    hi = tk_upper(nlo, hi, shift);
     lo = nlo;
     need = ts.need;
     nin = ts.nb;

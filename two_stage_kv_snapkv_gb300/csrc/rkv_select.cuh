@@ -97,8 +97,7 @@ __device__ __forceinline__ void cluster_select(int Lp, int k, LoadFn load, int32
 
   int need = k, nin = Lp;
   while (nin > kTkCand && lo != hi) {
-    const uint32_t range = hi - lo;
-    const int shift = range < (uint32_t)kTkBins ? 0 : (32 - __clz(range)) - 10;
+    const int shift = tk_shift(hi - lo);
     for (int i = tid; i < kTkBins; i += NT) ss.hist[i] = 0u;
     __syncthreads();
     int run_bin = -1, run = 0;
@@ -151,7 +150,7 @@ __device__ __forceinline__ void cluster_select(int Lp, int k, LoadFn load, int32
     }
     cluster.sync();  // every CTA has read every histogram (they are cleared next round)
     const uint32_t nlo = lo + ((uint32_t)ss.bstar << shift);
-    hi = shift == 0 ? nlo : min(hi, nlo + ((1u << shift) - 1u));
+    hi = tk_upper(nlo, hi, shift);
     lo = nlo;
     need = ss.need;
     nin = ss.nb;
