@@ -1,0 +1,27 @@
+"""Rules that the kernels' sources keep and that no run of them shows reliably (no GPU)."""
+import glob
+import os
+import re
+
+from two_stage_kv_snapkv_gb300 import build_lib
+
+
+def _sources():
+    for path in sorted(glob.glob(os.path.join(build_lib.CSRC, "*.cu"))):
+        with open(path) as f:
+            yield os.path.basename(path), re.sub(r"//[^\n]*", "", f.read())
+
+
+def test_barriers_are_fenced_by_the_threads_that_initialise_them():
+    # fence.mbarrier_init orders the executing thread's own mbarrier.init before the copies
+    # that complete on it: between an init and its fence no branch may change the threads
+    seen = 0
+    for name, text in _sources():
+        for m in re.finditer(r"\bmbar_init\(", text):
+            fence = text.find("fence_mbar_init();", m.end())
+            line = text.count("\n", 0, m.start()) + 1
+            assert fence >= 0, f"{name}:{line}: no fence behind the initialisation"
+            between = text[m.end():fence]
+            assert not re.search(r"\bif \(|\breturn\b|__global__", between), f"{name}:{line}: fenced by other threads"
+            seen += 1
+    assert seen > 10

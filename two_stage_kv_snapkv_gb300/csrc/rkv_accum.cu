@@ -82,9 +82,10 @@ __global__ void __launch_bounds__(RowsShape<kR16>::kWarps * 32, 1)
   uint8_t* base = align1024(smem);
   uint8_t* ring = base + warp * kRwStages * kRwStageBytes;
   uint8_t* qs = base + kRwWarps * kRwStages * kRwStageBytes;
-  if (lane == 0)
+  if (lane == 0) {
     for (int s = 0; s < kRwStages; ++s) mbar_init(&full_b[warp][s], 1);
-  if (tid == 0) fence_mbar_init();
+    fence_mbar_init();
+  }
   flat_build(
       ft, p.B, kRwPad, [&](int b) { return rows_cache_len(p, b); }, [&](int b) { return rows_of(p, b, rows_cache_len(p, b)); },
       [&](int n, int m) { return m > 0 ? (n + kRwKeys - 1) / kRwKeys : 0; }, [&](int) { return p.Hkv; });

@@ -242,9 +242,10 @@ __global__ void __launch_bounds__(kArThreads, 1) attend_rows_kernel(const __grid
   uint8_t* base = align1024(smem);
   uint8_t* ring = base + warp * kArStages * kArStageBytes;
   float* merge = reinterpret_cast<float*>(base + kArWarps * kArStages * kArStageBytes);
-  if (lane == 0)
+  if (lane == 0) {
     for (int s = 0; s < kArStages; ++s) mbar_init(&full_b[warp][s], 1);
-  if (tid == 0) fence_mbar_init();
+    fence_mbar_init();
+  }
   build_table<kArRows, kArKeys>(p, ft);
   grid_launch_dependents();
   const long long total = ft.base[p.B];
@@ -442,9 +443,10 @@ __global__ void __launch_bounds__(UnitsShape<kWarps>::kThreads) attend_units_ker
   float* zs = part_o + kArRows * 128;  // [G][tokens of this CTA]
   const int units = p.Hkv * p.row_tiles, b = blockIdx.y / units, unit = blockIdx.y % units;
   const int g = unit % p.Hkv, rt = unit / p.Hkv;
-  if (lane == 0)
+  if (lane == 0) {
     for (int s = 0; s < kAuStages; ++s) mbar_init(&full_b[warp][s], 1);
-  if (tid == 0) fence_mbar_init();
+    fence_mbar_init();
+  }
   __syncwarp();
   const int n = checked_len(p, b), nodes = checked_nodes(p, b);
   const int live = min(kArRows, nodes * p.G - rt * kArRows);
