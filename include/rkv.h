@@ -400,7 +400,9 @@ size_t rkv_tree_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, in
  * the product with V as bf16.  seq_len and tree_len are read on the device, so a captured
  * call can be replayed as the cache grows.  Calls of this and the following functions
  * whose work may overlap need workspaces of their own; nothing in a workspace outlives its
- * call.  scale lies in [1e-30, 1e30] here and below.
+ * call.  scale lies in [1e-30, 1e30] here and below, and logits (times log2 e, 1.45) must be
+ * finite in fp32; a logit is rounded to 2^-22 of its magnitude, and equal ones weigh the
+ * same however large they are.
  */
 rkv_status rkv_tree_attention(const rkv_cache* cache, const rkv_bf16* q, const rkv_bf16* k_tree,
                               const rkv_bf16* v_tree, const uint32_t* tree_mask, int32_t Hq, int32_t T,

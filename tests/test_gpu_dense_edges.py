@@ -55,3 +55,91 @@ def test_evict_with_more_nan_weights_than_kept(rkv, n, nans, keep, recent, room,
         assert kept[0, h].tolist() == want + [-7], f"g{h}"
         assert torch.equal(got.token_kv(0, keep)[0][h].cpu(), K[0][h][want])
         assert torch.equal(sums[0, h, :keep].cpu().view(torch.int32), acc0[0, h][want].view(torch.int32))
+
+
+# ------------------------------------------------------------------ scales at the ends of their range
+def _whole(g, *shape, sign):
+    """Whole numbers: channels 1 .. 16 of -1, 0, 1 and one of 8 (its sign `sign`), so that
+    every q . k is exact in fp32, lies in +-[48, 80] and often ties."""
+    x = torch.zeros(*shape, D)
+    x[..., 1:17] = torch.randint(-1, 2, (*shape, 16), generator=g).float()
+    x[..., 0] = 8 * sign
+    return x.to(torch.bfloat16)
+
+
+def _attend_whole(q, K, V, shown, scale):
+    """(out, lse, weights) in fp64.  The logits of different q . k differ by `scale` at least and
+    equal ones are equal to the bit, so only the fp32 rounding of scale, log2(e) and their
+    products enters, not the weights' ratios."""
+    z = (q.double() @ K.double().T) * float(torch.tensor(scale))
+    z = z.masked_fill(~shown, -math.inf)
+    lse = torch.logsumexp(z, 1)
+    top = z.max(1, keepdim=True).values.clamp_min(-1e300)
+    w = torch.exp(z - top)
+    w = w / w.sum(1, keepdim=True).clamp_min(1e-300)
+    return w @ V.double(), lse, w
+
+
+def _check_whole(out, lse, ref, rlse, w, V, scale, what):
+    # a logit's difference to the largest (at most 32 scale) is off by 2^-22 of the largest
+    # logit (80 scale): below scale 1 / 16 that is a weight's error, from 60 on every weight is 0
+    # or a tie.  Between them the test has no scale.  Then a rounding of the weights and one
+    # of the output, 2^-8 each (dense_check).
+    Ew = 2.0 ** -22 * 80 * scale + 2.0 ** -16 if scale < 1 else 2.0 ** -16
+    C.check_out(out, ref, w, V, Ew, what)
+    C.check_lse(lse, rlse, Ew, what)
+
+
+SCALES = [1e-30, 1e-20, 1e-3, 1e3, 3e5, 1e7, 1e9, 1e20, 1e30]
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("T,G,room", [(3, 4, 0), (3, 4, 40000), (20, 4, 40000), (70, 4, 40000)])
+def test_tree_attention_over_the_range_of_scales(rkv, T, G, room, scale, sign):
+    # clusters; 16-row tiles; 128 rows; 256 rows
+    g = C.gen(91)
+    lens, Hkv, P = [700, 0, 130], 1, 16
+    cache, K, V = C.make_cache(rkv, lens, Hkv, P, seed=90, room=room)
+    q, kt, vt = _whole(g, 3, Hkv * G, T, sign=1), _whole(g, 3, Hkv, T, sign=sign), C.randn(g, 3, Hkv, T, D)
+    for b, n in enumerate(lens):
+        K[b] = _whole(g, Hkv, n, sign=sign)
+        C.put_rows(cache, b, K[b], V[b])
+    sees = torch.rand(3, T, T, generator=g) < 0.5
+    sees[:, 0] = False                                     # sequence 1's first node sees nothing
+    out = torch.full((3, Hkv * G, T, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((3, Hkv * G, T), 7.0, device="cuda")
+    rkv.rkv_tree_attention(cache, q.cuda(), kt.cuda(), vt.cuda(), C.mask_words(sees).cuda(), out, lse=lse, scale=scale)
+    assert _status(rkv, cache) == 0
+    for b, n in enumerate(lens):
+        shown = torch.cat([torch.ones(T, n, dtype=torch.bool), sees[b]], 1)
+        k, v = torch.cat([K[b][0], kt[b, 0]]), torch.cat([V[b][0], vt[b, 0]])
+        for h in range(Hkv * G):
+            ref, rlse, w = _attend_whole(q[b, h], k, v, shown, scale)
+            _check_whole(out[b, h].cpu(), lse[b, h].cpu(), ref, rlse, w, v, scale, f"b{b} h{h}")
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("room", [0, 40000])
+def test_decode_accum_over_the_range_of_scales(rkv, room, scale, sign):
+    g = C.gen(93)
+    lens, Hkv, G, P = [900, 1, 33], 2, 2, 16
+    cache, K, V = C.make_cache(rkv, lens, Hkv, P, seed=92, room=room)
+    for b, n in enumerate(lens):
+        K[b] = _whole(g, Hkv, n, sign=sign)
+        C.put_rows(cache, b, K[b], V[b])
+    q = _whole(g, 3, Hkv * G, sign=1)
+    out = torch.zeros(3, Hkv * G, D, dtype=torch.bfloat16, device="cuda")
+    lse, acc = torch.zeros(3, Hkv * G, device="cuda"), rkv.accum_sums(cache)
+    rkv.rkv_decode_accum(cache, q.cuda(), out, acc, lse=lse, scale=scale)
+    assert _status(rkv, cache) == 0
+    Ew = 2.0 ** -22 * 80 * scale + 2.0 ** -16 if scale < 1 else 2.0 ** -16
+    for b, n in enumerate(lens):
+        want = torch.zeros(Hkv, n).double()
+        for h in range(Hkv * G):
+            ref, rlse, w = _attend_whole(q[b, h:h + 1], K[b][h // G], V[b][h // G], torch.ones(1, n, dtype=torch.bool), scale)
+            _check_whole(out[b, h:h + 1].cpu(), lse[b, h:h + 1].cpu(), ref, rlse, w, V[b][h // G], scale, f"b{b} h{h}")
+            want[h // G] += w[0]
+        got = acc[b, :, :n].cpu().double()
+        assert ((got - want).abs() <= want * (math.exp(Ew) - 1 + 2.0 ** -20)).all(), f"b{b}"

@@ -34,7 +34,9 @@ constexpr int kArMergeRows = 4;                   // rows of every warp that mee
 constexpr int kArMergeFloats = kArWarps * kArMergeRows * 128;
 constexpr int kArSmem = 1024 + kArWarps * kArStages * kArStageBytes + kArMergeFloats * 4;
 constexpr int kArPad = 16, kAtPad = 4;           // what a run costs, in chunks of 16 and tiles of 128 keys
-constexpr float kNoMax = -1e30f;                  // running maximum of a row that saw nothing
+// Running maximum of a row that saw nothing: no logit lies below it, and differences with
+// it are never inf - inf.
+constexpr float kNoMax = -3.402823466e+38f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWeighTokens = 2048;                // tokens of a weighing block, eight a thread
 
@@ -94,6 +96,9 @@ __device__ __forceinline__ size_t out_row(const AttendParams& p, int b, int g, i
   return ((size_t)b * p.Hq + g * p.G + (r & (p.G - 1))) * p.T + (r >> p.gshift);
 }
 
+// What turns base-2 logits into weights, 2^(z - m) / l: not 2^(z - log-sum-exp), whose sum
+// m + log2 l keeps nothing of l once m is past 2^24.  Nothing read: weighs nothing.
+__device__ __forceinline__ float2 norm_of(float m, float l) { return make_float2(m, l > 0.f ? 1.f / l : 0.f); }
 __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY; }
 
 // A warp's share of a 16-row tile: the queries as A fragments (eight steps of 16
@@ -433,7 +438,7 @@ __global__ void __launch_bounds__(UnitsShape<kWarps>::kThreads) attend_units_ker
   __shared__ uint64_t full_b[kWarps][kAuStages];
   __shared__ float wm[kWarps][kArRows], wl[kWarps][kArRows];
   __shared__ float2 part_ml[kArRows];  // this CTA's (m, l), read by the cluster
-  __shared__ float lse2[8];
+  __shared__ float2 norm[8];  // a head's maximum and 1 / sum
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   uint8_t* base = align1024(smem);
@@ -600,7 +605,7 @@ __global__ void __launch_bounds__(UnitsShape<kWarps>::kThreads) attend_units_ker
         float L = ml.y * ex2_approx(ml.x - M);
 #pragma unroll
         for (int o = 4; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        if (lane == 0) lse2[h] = L > 0.f ? M + log2f(L) : INFINITY;  // nothing read: weighs nothing
+        if (lane == 0) norm[h] = norm_of(M, L);
       }
     }
     __syncthreads();
@@ -608,7 +613,7 @@ __global__ void __launch_bounds__(UnitsShape<kWarps>::kThreads) attend_units_ker
     for (int t = tid; t < tokens; t += Sh::kThreads) {
       if (lo * kArKeys + t >= n) break;
       float w = 0.f;
-      for (int h = 0; h < p.G; ++h) w += ex2_approx(zs[h * tokens + t] - lse2[h]);
+      for (int h = 0; h < p.G; ++h) w += ex2_approx(zs[h * tokens + t] - norm[h].x) * norm[h].y;
       a[t] += w;
     }
   }
@@ -715,7 +720,7 @@ __global__ void __launch_bounds__(256, 4) attend_combine_kernel(const __grid_con
 // heads' (m, l) for itself.  The logits were written a moment ago and mostly lie in L2.
 __global__ void __launch_bounds__(256, 4) attend_weigh_kernel(const __grid_constant__ AttendParams p) {
   __shared__ FlatTable ft;
-  __shared__ float lse2[8];
+  __shared__ float2 norm[8];  // a head's maximum and 1 / sum
   __shared__ long long wbase[RKV_MAX_BATCH + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   build_table<kArRows, kArKeys>(p, ft);
@@ -741,7 +746,7 @@ __global__ void __launch_bounds__(256, 4) attend_weigh_kernel(const __grid_const
     if (warp < p.G) {
       const PartSlots ps(ft.base[b] + (long long)g * ft.per[b], ft.per[b], ft.pad, total, N);
       const float2 ml = ps.c0 == ps.c1 ? p.row_ml[unit * p.G + warp] : join_ml<kArRows>(p, ps, warp, lane);
-      if (lane == 0) lse2[warp] = ml.y > 0.f ? ml.x + log2f(ml.y) : INFINITY;  // nothing read: weighs nothing
+      if (lane == 0) norm[warp] = norm_of(ml.x, ml.y);
     }
     __syncthreads();
     // two quads of tokens a thread; positions behind n hold -inf up to the chunk's end and
@@ -751,15 +756,15 @@ __global__ void __launch_bounds__(256, 4) attend_weigh_kernel(const __grid_const
     const float* zu = p.z + unit * p.G * p.zstride;
 #pragma unroll 4
     for (int h = 0; h < p.G; ++h) {
-      const float base = lse2[h];
+      const float base = norm[h].x, inv = norm[h].y;
 #pragma unroll
       for (int q = 0; q < 2; ++q)
         if (t[q] < n) {
           const float4 z = *reinterpret_cast<const float4*>(zu + (size_t)h * p.zstride + t[q]);
-          w[q].x += ex2_approx(z.x - base);
-          w[q].y += ex2_approx(z.y - base);
-          w[q].z += ex2_approx(z.z - base);
-          w[q].w += ex2_approx(z.w - base);
+          w[q].x += ex2_approx(z.x - base) * inv;
+          w[q].y += ex2_approx(z.y - base) * inv;
+          w[q].z += ex2_approx(z.z - base) * inv;
+          w[q].w += ex2_approx(z.w - base) * inv;
         }
     }
     float* a = p.acc + unit * p.acc_stride;
@@ -770,7 +775,7 @@ __global__ void __launch_bounds__(256, 4) attend_weigh_kernel(const __grid_const
       for (int i = 0; i < 4; ++i)
         if (t[q] + i < n) a[t[q] + i] += e[i];
     }
-    __syncthreads();  // lse2 is free
+    __syncthreads();  // norm is free
   }
 }
 
@@ -807,6 +812,10 @@ constexpr int kAtSoftRegs = 208, kAtIssueRegs = 88;
 static_assert(256 * kAtSoftRegs + 128 * kAtIssueRegs == 384 * 168, "the split must be what the block was launched with");
 constexpr int kAtEntry = 128 * 256;
 constexpr float kAtSlack = 8.f;
+// Base-2 logits beyond this are rounded before the maximum comes off: z scale is taken as
+// one fused multiply-add with the rounded maximum, whose rounding (half of 2^-23 of it) then
+// scales a row's weights by 2^1 at most, and cancels; from 2^31 on it would be all of them.
+constexpr float kAtFused = 16777216.f;
 // The tiled kernel's table: only the line's offsets; a run's lengths are read again.
 struct SlimRun : FlatRun {
   int n, t;
@@ -1037,6 +1046,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
               tc_st32_wait(mine + 128 + c * 32, o);
             }
           }
+          float mul = sl;
+          if (fabsf(mx) > kAtFused && mx != -INFINITY) {
+            mul = 1.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[c][j] = __float_as_uint(__uint_as_float(v[c][j]) * sl);
+          }
           float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -1044,8 +1061,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const int cc = c * 2 + (j >> 4), jj = (j & 15) * 2;
-              const float ax = ex2_approx(fmaf(__uint_as_float(v[cc][jj]), sl, -m));
-              const float ay = ex2_approx(fmaf(__uint_as_float(v[cc][jj + 1]), sl, -m));
+              const float ax = ex2_approx(fmaf(__uint_as_float(v[cc][jj]), mul, -m));
+              const float ay = ex2_approx(fmaf(__uint_as_float(v[cc][jj + 1]), mul, -m));
               (j & 1 ? u0 : s0) += ax;
               (j & 1 ? u1 : s1) += ay;
               // bf16 weights (off by at most 2^-8 of each, as V is); their sum stays unrounded
