@@ -812,10 +812,12 @@ constexpr int kAtSoftRegs = 208, kAtIssueRegs = 88;
 static_assert(256 * kAtSoftRegs + 128 * kAtIssueRegs == 384 * 168, "the split must be what the block was launched with");
 constexpr int kAtEntry = 128 * 256;
 constexpr float kAtSlack = 8.f;
-// Base-2 logits beyond this are rounded before the maximum comes off: z scale is taken as
-// one fused multiply-add with the rounded maximum, whose rounding (half of 2^-23 of it) then
-// scales a row's weights by 2^1 at most, and cancels; from 2^31 on it would be all of them.
-constexpr float kAtFused = 16777216.f;
+// A weight's exponent is z sl - m as one fused multiply-add, in which m is rounded and z sl is
+// not.  The difference, at most 2^-24 of m, is the same for the whole row and cancels, while
+// it is no more than 64.  A row whose maximum lies beyond this has distinct logits at least
+// 64 apart, so that only ties with the maximum count: it takes the power of two below sl,
+// whose product with the maximum is exact.
+constexpr float kAtFar = 1073741824.f;
 // The tiled kernel's table: only the line's offsets; a run's lengths are read again.
 struct SlimRun : FlatRun {
   int n, t;
@@ -985,6 +987,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
       }
       const int my = rt * R + (kWide ? slot * 128 : 0) + row;  // this thread's query row
       float m = kNoMax, l = 0.f;
+      float ref = m, ref_sl = sl;  // what the weights' exponents are taken with: z ref_sl - ref
+      auto set_ref = [&](float raw) {
+        const bool far = fabsf(m) > kAtFar && m != kNoMax;
+        ref_sl = far ? __uint_as_float(__float_as_uint(sl) & 0x7f800000u) : sl;
+        ref = far ? raw * ref_sl : m;
+      };
       if (!idle) {
         for (int i = kWide ? 0 : slot; i < nt; i += kWide ? 1 : 2) {
           if (!(ok = wait(&s_b[slot], seen_s++))) break;
@@ -1028,14 +1036,19 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
               mx1 = max3(mx1, __uint_as_float(v[c][j + 2]), __uint_as_float(v[c][j + 3]));
             }
           }
-          mx = fmaxf(mx, mx1) * sl;  // sl > 0
+          const float raw = fmaxf(mx, mx1);
+          mx = raw * sl;  // sl > 0
           const bool first = i < (kWide ? 1 : 2);
           if (first) {
             m = fmaxf(kNoMax, mx);
+            set_ref(raw);
           } else if (__any_sync(0xffffffffu, mx > m + kAtSlack)) {
             // this slot's earlier products are complete: its logits were issued after them
             const float to = fmaxf(m, mx), f = ex2_approx(m - to);
-            m = to;
+            if (mx > m) {
+              m = to;
+              set_ref(raw);
+            }
             l *= f;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -1046,14 +1059,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
               tc_st32_wait(mine + 128 + c * 32, o);
             }
           }
-          float mul = sl;
-          if (fabsf(mx) > kAtFused && mx != -INFINITY) {
-            mul = 1.f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[c][j] = __float_as_uint(__uint_as_float(v[c][j]) * sl);
-          }
           float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -1061,8 +1066,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const int cc = c * 2 + (j >> 4), jj = (j & 15) * 2;
-              const float ax = ex2_approx(fmaf(__uint_as_float(v[cc][jj]), mul, -m));
-              const float ay = ex2_approx(fmaf(__uint_as_float(v[cc][jj + 1]), mul, -m));
+              const float ax = ex2_approx(fmaf(__uint_as_float(v[cc][jj]), ref_sl, -ref));
+              const float ay = ex2_approx(fmaf(__uint_as_float(v[cc][jj + 1]), ref_sl, -ref));
               (j & 1 ? u0 : s0) += ax;
               (j & 1 ? u1 : s1) += ay;
               // bf16 weights (off by at most 2^-8 of each, as V is); their sum stays unrounded
