@@ -143,3 +143,38 @@ def test_decode_accum_over_the_range_of_scales(rkv, room, scale, sign):
             want[h // G] += w[0]
         got = acc[b, :, :n].cpu().double()
         assert ((got - want).abs() <= want * (math.exp(Ew) - 1 + 2.0 ** -20)).all(), f"b{b}"
+
+
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("T,G,m", [(8, 4, [8, 3]), (40, 4, [40, 9]), (150, 1, [150, 60])])
+def test_accum_rows_over_the_range_of_scales(rkv, T, G, m, scale):
+    # 16-row blocks; tensor cores with 64 and with 128 rows a tile.  q . k is 0 in the even rows and in
+    # [-80, -48] in the others, so that no weight overflows.
+    g = C.gen(95)
+    lens, Hkv, P = [400, 60], 2, 16
+    cache, K, V = C.make_cache(rkv, lens, Hkv, P, seed=94)
+    for b, n in enumerate(lens):
+        K[b] = _whole(g, Hkv, n, sign=-1)
+        C.put_rows(cache, b, K[b], V[b])
+    q = _whole(g, 2, Hkv * G, T, sign=1)
+    q[:, :, ::2] = 0
+    lse = torch.rand(2, Hkv * G, T, generator=g) * 4 + 6
+    lse[:, :, 1::5] = -math.inf                            # rows that saw nothing weigh nothing
+    lse[:, 0, 2] = math.inf
+    acc = rkv.accum_sums(cache)
+    rkv.rkv_accum_rows(cache, q.cuda(), lse.cuda(), acc, scale=scale,
+                       row_len=torch.tensor(m, dtype=torch.int32, device="cuda"))
+    assert _status(rkv, cache) == 0
+    # an exponent, of at most 80 scale + 10 before it is 0 all the same (from 120 on), is off by 2^-22
+    # of it for each of its roundings (scale log2 e, the product, lse log2 e or its three terms)
+    E = 4 * 2.0 ** -22 * min(80 * scale + 10, 130.0) + 2.0 ** -16
+    for b, n in enumerate(lens):
+        seen = torch.arange(n)[None] <= (n - m[b] + torch.arange(m[b]))[:, None]
+        for h in range(Hkv):
+            want = torch.zeros(n).double()
+            for i in range(h * G, (h + 1) * G):
+                z = (q[b, i, :m[b]].double() @ K[b][h].double().T) * float(torch.tensor(scale))
+                l = lse[b, i, :m[b]].double()[:, None]
+                want += torch.where(seen & (l != -math.inf), torch.exp(z - l), torch.zeros_like(z)).sum(0)
+            got = acc[b, h, :n].cpu().double()
+            assert ((got - want).abs() <= want * (math.exp(E) - 1) + 1e-37).all(), f"b{b} g{h}"

@@ -654,12 +654,14 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
             ++h;
           }
           load(next);
-          // -lse / scale in three bf16 terms (a row that weighs nothing: a huge negative one)
+          // -lse / scale in three bf16 terms.  At most 3e38, which bf16 holds: times the smallest
+          // scale that is 3e8, and no weight of a row that far off is but 0 or infinite.  A row
+          // that weighs nothing takes the lowest.
           uint2 w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float a = v[e] == -INFINITY ? -1e30f : -v[e] * inv;
-            a = a > 1e30f ? 1e30f : (a < -1e30f ? -1e30f : a);  // a NaN stays one
+            float a = v[e] == -INFINITY ? -3e38f : -v[e] * inv;
+            a = a > 3e38f ? 3e38f : (a < -3e38f ? -3e38f : a);  // a NaN stays one
             const float hi = __bfloat162float(__float2bfloat16_rn(a)), r1 = a - hi;
             const float mid = __bfloat162float(__float2bfloat16_rn(r1));
             w[e] = make_uint2(pack_bf16x2(hi, mid), pack_bf16x2(r1 - mid, 0.f));
