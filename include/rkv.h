@@ -385,7 +385,7 @@ size_t rkv_tree_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, in
  *           itself sets its own bit);
  *   out   = sum_j exp(z_j) v_j / sum_j exp(z_j),  lse = log sum_j exp(z_j).
  * A row that sees nothing (an empty cache and an empty mask row) gets out = 0 and
- * lse = -inf.  Rows t >= tree_len[b] of out and lse are left as they were.  The cache is
+ * lse = -inf; one with a NaN among its logits gets NaN for both.  Rows t >= tree_len[b] of out and lse are left as they were.  The cache is
  * read only: nothing is appended (rkv_tree_commit does that for the accepted path).
  *   q         : device [B][Hq][T][128] bf16; 1 <= T <= RKV_MAX_TREE.
  *   k_tree, v_tree : device [B][Hkv][T][128] bf16, the nodes' keys and values; rows

@@ -178,3 +178,67 @@ def test_accum_rows_over_the_range_of_scales(rkv, T, G, m, scale):
                 want += torch.where(seen & (l != -math.inf), torch.exp(z - l), torch.zeros_like(z)).sum(0)
             got = acc[b, h, :n].cpu().double()
             assert ((got - want).abs() <= want * (math.exp(E) - 1) + 1e-37).all(), f"b{b} g{h}"
+
+
+# ------------------------------------------------------------------ values that are not numbers
+@pytest.mark.parametrize("T,G,room", [(3, 4, 0), (3, 4, 40000), (20, 4, 40000), (70, 4, 40000)])
+def test_tree_attention_keeps_a_nan(rkv, T, G, room):
+    # a query with a NaN: its row is NaN, the log-sum-exp too, and no other row is
+    g = C.gen(97)
+    cache, K, V = C.make_cache(rkv, [700, 90], 1, 16, seed=96, room=room)
+    q, kt, vt = C.randn(g, 2, G, T, D), C.randn(g, 2, 1, T, D), C.randn(g, 2, 1, T, D)
+    sees = C.ancestors(2, T, g)
+    q[0, 1, T - 1, 77] = math.nan
+    K[1][0, 40, 3] = math.nan                              # and a cached key: every row of its sequence
+    C.put_rows(cache, 1, K[1], V[1])
+    out = torch.full((2, G, T, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((2, G, T), 7.0, device="cuda")
+    rkv.rkv_tree_attention(cache, q.cuda(), kt.cuda(), vt.cuda(), C.mask_words(sees).cuda(), out, lse=lse)
+    assert _status(rkv, cache) == 0
+    out, lse = out.cpu(), lse.cpu()
+    assert out[1].isnan().all() and lse[1].isnan().all()
+    assert out[0, 1, T - 1].isnan().all() and lse[0, 1, T - 1].isnan()
+    shown = torch.cat([torch.ones(T, 700, dtype=torch.bool), sees[0]], 1)
+    k, v = torch.cat([K[0][0], kt[0, 0]]), torch.cat([V[0][0], vt[0, 0]])
+    for h in range(G):
+        rows = [t for t in range(T) if (h, t) != (1, T - 1)]
+        ref, l, w, Ew = C.attend(q[0, h][rows], k, v, shown[rows])
+        C.check_out(out[0, h][rows], ref, w, v, Ew, f"h{h}")
+        C.check_lse(lse[0, h][rows], l, Ew, f"h{h}")
+
+
+@pytest.mark.parametrize("room", [0, 40000])
+def test_decode_accum_keeps_a_nan(rkv, room):
+    g = C.gen(99)
+    lens = [900, 65]
+    cache, K, V = C.make_cache(rkv, lens, 2, 16, seed=98, room=room)
+    K[0][1, 500, 9] = math.nan
+    C.put_rows(cache, 0, K[0], V[0])
+    q = C.randn(g, 2, 4, D)
+    q[1, 3, 0] = math.nan
+    out = torch.zeros(2, 4, D, dtype=torch.bfloat16, device="cuda")
+    lse, acc = torch.zeros(2, 4, device="cuda"), rkv.accum_sums(cache)
+    rkv.rkv_decode_accum(cache, q.cuda(), out, acc, lse=lse)
+    assert _status(rkv, cache) == 0
+    out, lse, acc = out.cpu(), lse.cpu(), acc.cpu()
+    nan = torch.tensor([[False, False, True, True], [False, False, False, True]])
+    assert torch.equal(lse.isnan(), nan) and torch.equal(out.isnan().all(-1), nan) and torch.equal(out.isnan().any(-1), nan)
+    for b, n in enumerate(lens):
+        assert acc[b, 1, :n].isnan().all() and (acc[b, :, n:] == 0).all()
+        w = [C.attend(q[b, h:h + 1], K[b][0], V[b][0], torch.ones(1, n, dtype=torch.bool)) for h in range(2)]
+        want, Ew = w[0][2][0] + w[1][2][0], max(w[0][3], w[1][3])
+        assert ((acc[b, 0, :n].double() - want).abs() <= want * (math.exp(Ew) - 1 + 2.0 ** -20)).all()
+
+
+@pytest.mark.parametrize("T,G", [(8, 4), (40, 4), (150, 1)])
+def test_accum_rows_keeps_a_nan(rkv, T, G):
+    # a row whose log-sum-exp is NaN makes what it sees NaN, and nothing else
+    g = C.gen(101)
+    cache, K, V = C.make_cache(rkv, [300], 2, 16, seed=100)
+    q, lse = C.randn(g, 1, 2 * G, T, D), torch.full((1, 2 * G, T), 7.0)
+    lse[0, 0, T // 2] = math.nan
+    acc = rkv.accum_sums(cache)
+    rkv.rkv_accum_rows(cache, q.cuda(), lse.cuda(), acc)
+    assert _status(rkv, cache) == 0
+    seen = 300 - T + T // 2 + 1
+    assert acc[0, 0, :seen].isnan().all() and not acc[0, 0, seen:].isnan().any() and not acc[0, 1].isnan().any()

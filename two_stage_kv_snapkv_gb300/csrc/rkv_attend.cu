@@ -96,10 +96,13 @@ __device__ __forceinline__ size_t out_row(const AttendParams& p, int b, int g, i
   return ((size_t)b * p.Hq + g * p.G + (r & (p.G - 1))) * p.T + (r >> p.gshift);
 }
 
+// A row's results from its maximum m and sum l.  l = 0: it saw nothing, and nothing is what it
+// weighs; a NaN among its logits has left l a NaN, which stays one.
+__device__ __forceinline__ float inverse_of(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
 // What turns base-2 logits into weights, 2^(z - m) / l: not 2^(z - log-sum-exp), whose sum
-// m + log2 l keeps nothing of l once m is past 2^24.  Nothing read: weighs nothing.
-__device__ __forceinline__ float2 norm_of(float m, float l) { return make_float2(m, l > 0.f ? 1.f / l : 0.f); }
-__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY; }
+// m + log2 l keeps nothing of l once m is past 2^24.
+__device__ __forceinline__ float2 norm_of(float m, float l) { return make_float2(m, inverse_of(l)); }
 
 // A warp's share of a 16-row tile: the queries as A fragments (eight steps of 16
 // channels), the running maximum, sum and fp32 output of fragment rows r0 = lane / 4 and
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(kArThreads, 1) attend_rows_kernel(const __grid
           ay += v.y * f;
         }
         if (cr.whole) {
-          const float inv = L > 0.f ? 1.f / L : 0.f;
+          const float inv = inverse_of(L);
           const size_t orow = out_row(p, b, g, r);
           *reinterpret_cast<uint32_t*>(p.out + orow * 128 + d) = pack_bf16x2(ax * inv, ay * inv);
           if (d == 0) {
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__(UnitsShape<kWarps>::kThreads) attend_units_ker
         ax += v[c].x * f;
         ay += v[c].y * f;
       }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = inverse_of(L);
     const size_t orow = out_row(p, b, g, rt * kArRows + row);
     *reinterpret_cast<uint32_t*>(p.out + orow * 128 + d) = pack_bf16x2(ax * inv, ay * inv);
     if (d == 0 && p.lse) p.lse[orow] = lse_of(M, L);
@@ -698,7 +701,7 @@ __device__ __forceinline__ void combine_row(const AttendParams& p, const FlatTab
       o.w += v[j].w * w;
     }
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = inverse_of(L);
   *out = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
   if (lane == 0 && p.lse) p.lse[orow] = lse_of(M, L);
 }
@@ -1103,7 +1106,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
       tc_fence_after();
       if (!idle) {
         const bool live = my < rows;
-        const float inv = r.whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+        const float inv = r.whole ? inverse_of(l) : 1.f;
         const size_t orow = live ? out_row(p, b, g, my) : 0;
         const size_t prow = (2 * (size_t)blockIdx.x + (r.first ? 0 : 1)) * R + (kWide ? slot * 128 : 0) + row;
         // kWide: all 128 channels of this slot's row; else 64 channels of both slots' O.  32
