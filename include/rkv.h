@@ -490,6 +490,8 @@ size_t rkv_evict_workspace_size(int32_t B, int32_t Hkv, int32_t max_keep, int32_
  *              destination has the source's B, Hkv and page_size, its pages are none of
  *              the source's, and dst_acc is not acc; the source is then left as it was.
  *              In place, no page may belong to two sequences.
+ * A sequence whose seq_len is negative or beyond its pages sets RKV_DEVERR_CAPACITY and is
+ * left as it was in place; a destination's sequence becomes empty, with its sums at zero.
  * Positions are rewritten, so a key copy kept for rkv_decode_sparq (keys_t) starts again
  * from zero afterwards.  Caches of more than 393216 tokens per sequence (max_pages *
  * page_size) return RKV_ERR_UNSUPPORTED.

@@ -242,3 +242,29 @@ def test_accum_rows_keeps_a_nan(rkv, T, G):
     assert _status(rkv, cache) == 0
     seen = 300 - T + T // 2 + 1
     assert acc[0, 0, :seen].isnan().all() and not acc[0, 0, seen:].isnan().any() and not acc[0, 1].isnan().any()
+
+
+# ------------------------------------------------------------------ eviction: lengths that cannot be used
+@pytest.mark.parametrize("room", [0, 9000])
+@pytest.mark.parametrize("bad", [-3, None])
+def test_evict_in_place_leaves_a_sequence_of_unusable_length(rkv, bad, room):
+    lens, P = [100, 90, 40], 16
+    cache, K, V = C.make_cache(rkv, lens, 2, P, seed=103, room=room)
+    acc0 = torch.rand(3, 2, cache.max_pages * P, generator=C.gen(104))
+    acc, kept = acc0.cuda(), torch.full((3, 2, 30), -7, dtype=torch.int32, device="cuda")
+    cache.seq_len[0] = cache.max_pages * P + 1 if bad is None else bad
+    bits = lambda t: t.cpu().view(torch.int16)  # noqa: E731
+    at = cache.page_table[0].long()
+    before = [bits(t) for t in (cache.k_pages[at], cache.v_pages[at], cache.kmax[0], cache.kmin[0])]
+    length = int(cache.seq_len[0])
+    rkv.rkv_evict_accum(cache, acc, [30, 30, 30], 5, kept)
+    assert _status(rkv, cache) == rkv.DEVERR_CAPACITY
+    assert cache.seq_len.tolist() == [length, 30, 30]
+    after = [bits(t) for t in (cache.k_pages[at], cache.v_pages[at], cache.kmax[0], cache.kmin[0])]
+    assert all(torch.equal(x, y) for x, y in zip(before, after))
+    assert torch.equal(acc[0].cpu(), acc0[0]) and (kept[0] == -7).all()
+    for b in (1, 2):
+        for h in range(2):
+            want = C.keep_set(acc0[b, h], lens[b], 30, 5)
+            assert kept[b, h].tolist() == want
+            assert torch.equal(cache.token_kv(b, 30)[0][h].cpu(), K[b][h][want])

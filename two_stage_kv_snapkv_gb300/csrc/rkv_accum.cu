@@ -735,7 +735,7 @@ struct EvictParams {
   float* dst_acc;
   int acc_stride, dst_acc_stride, recent, kept_stride, stage_stride;
   int32_t* kept;        // [B][Hkv][kept_stride]
-  int32_t* count;       // [B] tokens kept (workspace)
+  int32_t* count;       // [B] tokens kept (workspace); -1: not touched
   rkv_bf16* stage_k;    // in place: [B][Hkv][stage_stride][128], else null
   rkv_bf16* stage_v;
   float* stage_acc;     // [B][Hkv][stage_stride]
@@ -764,8 +764,9 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   const int n = evict_len(p, b), keep = p.keep[b];
   int32_t* out = p.kept + (size_t)unit * p.kept_stride;
   if (rank == 0 && tid == 0 && unit % p.src.Hkv == 0) {
-    if (n != p.src.seq_len[b]) flag_error(p.src.error_word, RKV_DEVERR_CAPACITY);
-    p.count[b] = min(n, keep);
+    const bool usable = n == p.src.seq_len[b];
+    if (!usable) flag_error(p.src.error_word, RKV_DEVERR_CAPACITY);
+    p.count[b] = usable || !p.in_place ? min(n, keep) : -1;  // in place: left as it is
   }
   if (n <= keep) {  // the same branch in every CTA of the cluster
     for (int i = rank * kSelectThreads + tid; i < n; i += C * kSelectThreads) out[i] = i;
@@ -851,6 +852,7 @@ __global__ void __launch_bounds__(128) evict_compact_kernel(const __grid_constan
   const size_t unit = (size_t)b * p.src.Hkv + g;
   const int n = p.count[b];
   const int pg0 = blockIdx.x * p.cgroup;
+  if (n < 0) return;
   if (blockIdx.x == 0 && g == 0 && tid == 0) p.dst.seq_len[b] = n;
   // the weights behind the kept ones start again at zero
   for (int t = n + blockIdx.x * 128 + tid; t < p.dst_acc_stride; t += gridDim.x * 128)
