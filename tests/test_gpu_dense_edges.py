@@ -268,3 +268,33 @@ def test_evict_in_place_leaves_a_sequence_of_unusable_length(rkv, bad, room):
             want = C.keep_set(acc0[b, h], lens[b], 30, 5)
             assert kept[b, h].tolist() == want
             assert torch.equal(cache.token_kv(b, 30)[0][h].cpu(), K[b][h][want])
+
+
+# ------------------------------------------------------------------ workspaces on another stream
+def test_a_workspace_is_not_memory_that_the_current_stream_still_writes(rkv):
+    """The reverse of a workspace handed out too early: what the current stream is still writing
+    to has been freed on the host, and a call on another stream makes its workspace."""
+    lens = [6000, 900]
+    cache, K, V = C.make_cache(rkv, lens, 2, 16, seed=105, room=10000)
+    q = C.randn(C.gen(106), 2, 8, D)
+    qd = q.cuda()
+    side = torch.cuda.Stream()
+    acc, lse = rkv.accum_sums(cache), torch.zeros(2, 8, device="cuda")
+    outs = [torch.zeros(2, 8, D, dtype=torch.bfloat16, device="cuda") for _ in range(6)]
+    size = rkv.accum_workspace(2, 8, 2, cache.max_pages, 16).numel()
+    torch.cuda.synchronize()
+    for o in outs:
+        was = torch.empty(size, dtype=torch.uint8, device="cuda")
+        for _ in range(60):
+            was.fill_(255)
+        del was
+        rkv.rkv_decode_accum(cache, qd, o, acc, lse=lse, stream=side)
+    torch.cuda.synchronize()
+    assert _status(rkv, cache) == 0
+    for o in outs:
+        assert torch.equal(o, outs[0])
+    for b, n in enumerate(lens):
+        for h in range(8):
+            ref, l, w, Ew = C.attend(q[b, h:h + 1], K[b][h // 4], V[b][h // 4], torch.ones(1, n, dtype=torch.bool))
+            C.check_out(outs[0][b, h:h + 1].cpu(), ref, w, V[b][h // 4], Ew, f"b{b} h{h}")
+            C.check_lse(lse[b, h:h + 1].cpu(), l, Ew, f"b{b} h{h}")

@@ -181,6 +181,15 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _made_for(stream, make, *args, **kw) -> torch.Tensor:
+    """A workspace for one call, from the memory of the stream that the call runs on: nothing
+    queued on another stream still uses it, and nothing else gets it before the call is done."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 @functools.lru_cache(maxsize=256)
 def _host_i32_cached(values: tuple):
     return (ctypes.c_int32 * len(values))(*values)
@@ -281,7 +290,7 @@ def rkv_prefill_evict(q_win: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pro
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
-        workspace = prefill_workspace(B, Hq, cache.Hkv, w, Lmax, q_win.device)
+        workspace = _made_for(stream, prefill_workspace, B, Hq, cache.Hkv, w, Lmax, q_win.device)
     _check(_lib.rkv_prefill_evict(_ptr(q_win), _ptr(k), _ptr(v), B, Hq, w, Lmax, _host_i32(prompt_len),
                                   _host_i32(keep1), _host_i32(pool_kernel), scale, ctypes.byref(cache.struct),
                                   _ptr(kept_idx), kept_idx.shape[-1], _ptr(pooled_scores), _ptr(workspace),
@@ -305,7 +314,7 @@ def rkv_prefill_chunk(q_win: torch.Tensor, k_chunk: torch.Tensor, v_chunk: torch
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
         total = max(int(h) + int(m) for h, m in zip(held_len, chunk_len))
-        workspace = prefill_chunk_workspace(B, Hq, cache.Hkv, w, total, q_win.device)
+        workspace = _made_for(stream, prefill_chunk_workspace, B, Hq, cache.Hkv, w, total, q_win.device)
     _check(_lib.rkv_prefill_chunk(_ptr(q_win), _ptr(k_chunk), _ptr(v_chunk), B, Hq, w, chunk_max,
                                   _host_i32(chunk_len), _host_i32(held_len), _host_i32(keep1),
                                   _host_i32(pool_kernel), scale, ctypes.byref(cache.struct), _ptr(kept_idx),
@@ -327,7 +336,7 @@ def rkv_decode_hsa(cache: PagedCache, q: torch.Tensor, k1: Sequence[int], k2: Se
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
-        workspace = decode_workspace(B, Hq, cache.Hkv, cache.max_pages, q.device)
+        workspace = _made_for(stream, decode_workspace, B, Hq, cache.Hkv, cache.max_pages, q.device)
     stride = sel_pages.shape[-1] if sel_pages is not None else 0
     _check(_lib.rkv_decode_hsa(ctypes.byref(cache.struct), _ptr(q), Hq, _host_i32(k1), _host_i32(k2), scale,
                                _ptr(out), _ptr(sel_channels), _ptr(sel_pages), stride, _ptr(workspace),
@@ -343,7 +352,7 @@ def rkv_decode_step(cache: PagedCache, q: torch.Tensor, k_new: torch.Tensor, v_n
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
-        workspace = decode_workspace(B, Hq, cache.Hkv, cache.max_pages, q.device)
+        workspace = _made_for(stream, decode_workspace, B, Hq, cache.Hkv, cache.max_pages, q.device)
     stride = sel_pages.shape[-1] if sel_pages is not None else 0
     _check(_lib.rkv_decode_step(ctypes.byref(cache.struct), _ptr(q), _ptr(k_new), _ptr(v_new), Hq, _host_i32(k1),
                                 _host_i32(k2), scale, _ptr(out), _ptr(sel_channels), _ptr(sel_pages), stride,
@@ -392,7 +401,7 @@ def rkv_decode_sparq(cache: PagedCache, q: torch.Tensor, k1: Sequence[int], k_to
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
-        workspace = sparq_workspace(B, Hq, cache.Hkv, cache.max_pages, cache.page_size, q.device)
+        workspace = _made_for(stream, sparq_workspace, B, Hq, cache.Hkv, cache.max_pages, cache.page_size, q.device)
     stride = sel_tokens.shape[-1] if sel_tokens is not None else 0
     kt_bytes = keys_t.numel() * keys_t.element_size() if keys_t is not None else 0
     _check(_lib.rkv_decode_sparq(ctypes.byref(cache.struct), _ptr(q), Hq, _host_i32(k1), _host_i32(k_tokens), scale,
@@ -437,13 +446,6 @@ def _call_on(device, stream, fn, *args) -> None:
         _check(status)
 
 
-def _own_ws(workspace: torch.Tensor, stream) -> torch.Tensor:
-    """A workspace made for one call: kept from being handed out again while `stream` uses it."""
-    if stream is not None:
-        workspace.record_stream(stream)
-    return workspace
-
-
 def tree_workspace(B: int, Hq: int, Hkv: int, T: int, max_pages: int, page_size: int, device="cuda") -> torch.Tensor:
     n = _lib.rkv_tree_workspace_size(B, Hq, Hkv, T, max_pages, page_size)
     return torch.empty(n, dtype=torch.uint8, device=device)
@@ -468,7 +470,7 @@ def rkv_tree_attention(cache: PagedCache, q: torch.Tensor, k_tree: torch.Tensor,
             _arg(tree_len, "tree_len", (B,), torch.int32, dev), 1.0 / math.sqrt(d) if scale is None else scale,
             _arg(out, "out", (B, Hq, T, HEAD_DIM), bf16, dev), _arg(lse, "lse", (B, Hq, T), torch.float32, dev))
     if workspace is None:
-        workspace = _own_ws(tree_workspace(B, Hq, cache.Hkv, T, cache.max_pages, cache.page_size, dev), stream)
+        workspace = _made_for(stream, tree_workspace, B, Hq, cache.Hkv, T, cache.max_pages, cache.page_size, dev)
     _call_on(dev, stream, _lib.rkv_tree_attention, ctypes.byref(cache.struct), *args, _ws_arg(workspace, dev),
              workspace.numel())
 
@@ -512,7 +514,7 @@ def rkv_decode_accum(cache: PagedCache, q: torch.Tensor, out: torch.Tensor, acc:
             _arg(out, "out", (B, Hq, HEAD_DIM), torch.bfloat16, dev), _arg(lse, "lse", (B, Hq), torch.float32, dev),
             _acc_arg(acc, "acc", cache, dev), acc.shape[2])
     if workspace is None:
-        workspace = _own_ws(accum_workspace(B, Hq, cache.Hkv, cache.max_pages, cache.page_size, dev), stream)
+        workspace = _made_for(stream, accum_workspace, B, Hq, cache.Hkv, cache.max_pages, cache.page_size, dev)
     _call_on(dev, stream, _lib.rkv_decode_accum, ctypes.byref(cache.struct), *args, _ws_arg(workspace, dev),
              workspace.numel())
 
@@ -541,7 +543,7 @@ def rkv_accum_rows(cache: PagedCache, q: torch.Tensor, lse: torch.Tensor, acc: t
             _arg(row_ids, "row_ids", (B, ids), torch.int32, dev), ids, 1.0 / math.sqrt(d) if scale is None else scale,
             _acc_arg(acc, "acc", cache, dev), acc.shape[2])
     if workspace is None:
-        workspace = _own_ws(accum_rows_workspace(B, Hq, cache.Hkv, T, cache.max_pages, cache.page_size, dev), stream)
+        workspace = _made_for(stream, accum_rows_workspace, B, Hq, cache.Hkv, T, cache.max_pages, cache.page_size, dev)
     _call_on(dev, stream, _lib.rkv_accum_rows, ctypes.byref(cache.struct), *args, _ws_arg(workspace, dev),
              workspace.numel())
 
@@ -568,8 +570,8 @@ def rkv_evict_accum(cache: PagedCache, acc: torch.Tensor, keep: Sequence[int], r
     sums = _acc_arg(acc, "acc", cache, dev)
     to = _acc_arg(dst_acc, "dst_acc", cache, dev) if dst_acc is not None else None
     if workspace is None:
-        workspace = _own_ws(evict_workspace(cache.B, cache.Hkv, max(1, max(int(x) for x in keep)), dev,
-                                            in_place=dst is None), stream)
+        workspace = _made_for(stream, evict_workspace, cache.B, cache.Hkv, max(1, max(int(x) for x in keep)), dev,
+                              in_place=dst is None)
     _call_on(dev, stream, _lib.rkv_evict_accum, ctypes.byref(cache.struct), sums, acc.shape[2], _host_i32(keep),
              int(recent), kept, kept_idx.shape[2], ctypes.byref(dst.struct) if dst is not None else None, to,
              dst_acc.shape[2] if dst_acc is not None else 0, _ws_arg(workspace, dev), workspace.numel())
