@@ -145,6 +145,53 @@ def test_decode_accum_over_the_range_of_scales(rkv, room, scale, sign):
         assert ((got - want).abs() <= want * (math.exp(Ew) - 1 + 2.0 ** -20)).all(), f"b{b}"
 
 
+@pytest.mark.parametrize("late", [False, True])
+@pytest.mark.parametrize("T,G,room", [(3, 4, 0), (3, 4, 40000), (20, 4, 40000), (70, 4, 40000)])
+def test_tree_attention_whose_maxima_lie_far_apart(rkv, T, G, room, late):
+    """Rows of three kinds in every warp.  The first 256 keys have the logit -+2^40 scale or 0,
+    the same for all of them; one key behind them, if `late`, +-2^42 scale or 0.  The rest is
+    ordinary.  So a row's maximum stays far below or above the rest, or comes from far below
+    to the rest and from there to far above."""
+    n = 900
+    cache, K, V = C.make_cache(rkv, [n], 1, 16, seed=107, room=room)
+    g = C.gen(108)
+    K[0][0, :, 0] = 0
+    K[0][0, :256] = 0
+    K[0][0, :256, 0] = -2.0 ** 40
+    if late:
+        K[0][0, 700] = 0
+        K[0][0, 700, 0] = 2.0 ** 42
+    C.put_rows(cache, 0, K[0], V[0])
+    q, kt, vt = C.randn(g, 1, G, T, D), C.randn(g, 1, 1, T, D), C.randn(g, 1, 1, T, D)
+    kt[..., 0] = 0
+    kind = (torch.arange(G)[:, None] + torch.arange(T)[None]) % 3 - 1          # [G, T]: -1, 0, 1
+    q[0, :, :, 0] = kind.to(torch.bfloat16)
+    sees = C.ancestors(1, T, g)
+    out = torch.full((1, G, T, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((1, G, T), 7.0, device="cuda")
+    rkv.rkv_tree_attention(cache, q.cuda(), kt.cuda(), vt.cuda(), C.mask_words(sees).cuda(), out, lse=lse)
+    assert _status(rkv, cache) == 0
+    out, lse = out[0].cpu(), lse[0].cpu()
+    k, v = torch.cat([K[0][0], kt[0, 0]]), torch.cat([V[0][0], vt[0, 0]])
+    for h in range(G):
+        for t in range(T):
+            shown = torch.cat([torch.ones(n, dtype=torch.bool), sees[0, t]])
+            if kind[h, t] < 0:                             # the first keys alone, all the same
+                shown[256:] = False
+            elif kind[h, t] > 0:                           # all but the first, or the late one alone
+                shown[:256] = False
+                if late:
+                    shown[:] = False
+                    shown[700] = True
+            # the keys that count: their logits are exact where far, ordinary elsewhere
+            at = torch.nonzero(shown)[:, 0]
+            ref, l, w, Ew = C.attend(q[0, h, t:t + 1], k[at], v[at], torch.ones(1, len(at), dtype=torch.bool))
+            if kind[h, t] < 0 or (kind[h, t] > 0 and late):
+                Ew = 2.0 ** -16
+            C.check_out(out[h, t:t + 1], ref, w, v[at], Ew, f"h{h} t{t}")
+            C.check_lse(lse[h, t:t + 1], l, Ew, f"h{h} t{t}")
+
+
 @pytest.mark.parametrize("scale", SCALES)
 @pytest.mark.parametrize("T,G,m", [(8, 4, [8, 3]), (40, 4, [40, 9]), (150, 1, [150, 60])])
 def test_accum_rows_over_the_range_of_scales(rkv, T, G, m, scale):
