@@ -25,3 +25,19 @@ def test_barriers_are_fenced_by_the_threads_that_initialise_them():
             assert not re.search(r"\bif \(|\breturn\b|__global__", between), f"{name}:{line}: fenced by other threads"
             seen += 1
     assert seen > 10
+
+
+def test_products_given_up_are_waited_for_before_their_memory_is_freed():
+    # after a timeout a kernel that issues products between waits may hold one that no barrier
+    # phase counts: only a commit made behind the last one tells when all are done
+    for name, text in _sources():
+        if name not in ("rkv_attend.cu", "rkv_accum.cu"):
+            continue
+        stop = text.index("if (abort_flag) {")
+        free = text.index("tmem_dealloc(", stop)
+        branch = text[stop:free]
+        commit = branch.find("tc_commit_if(elect_lane(), &")
+        assert commit >= 0, f"{name}: no commit behind the last product"
+        bar = re.match(r"tc_commit_if\(elect_lane\(\), &([\w.]+)\)", branch[commit:]).group(1)
+        assert f"mbar_wait(&{bar}, 0)" in branch[commit:], f"{name}: the commit is not waited for"
+        assert text.count(f"mbar_init(&{bar}, 1)") == 1

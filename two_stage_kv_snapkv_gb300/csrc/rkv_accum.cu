@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ TilesTable tt;
   __shared__ uint64_t kfull[KS], kempty[KS], qfull[kAmQ], qempty[kAmQ];
-  __shared__ uint64_t sfull[2][2], sempty[2][2], hsum;  // [buffer][key tile]
+  __shared__ uint64_t sfull[2][2], sempty[2][2], hsum, drained;  // [buffer][key tile]
   __shared__ float half_s[2][2][128];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int abort_flag;
@@ -423,6 +423,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
       mbar_init(&sempty[i >> 1][i & 1], 256);
     }
     mbar_init(&hsum, 512);
+    mbar_init(&drained, 1);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -688,8 +689,10 @@ __global__ void __launch_bounds__(kAmThreads, 1) accum_tiles_kernel(const __grid
       for (int i = max(0, tiles - kAmQ); i < tiles; ++i) mbar_wait(&qfull[i % kAmQ], (uint32_t)((i / kAmQ) & 1));
       for (int i = max(0, units - KS); i < units; ++i) mbar_wait(&kfull[i % KS], (uint32_t)((i / KS) & 1));
     }
-    if (warp == 17 && lane == 0 && tiles > 0)
-      mbar_wait(&sfull[(tiles - 1) & 1][1], (uint32_t)(((tiles - 1) / 2) & 1));
+    if (warp == 17) {  // a tile given up between its two key tiles has one product that no phase counts
+      tc_commit_if(elect_lane(), &drained);
+      mbar_wait(&drained, 0);
+    }
     __syncthreads();
   }
   if (warp == 17) {

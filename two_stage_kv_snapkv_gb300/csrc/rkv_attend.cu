@@ -837,7 +837,7 @@ struct TileShape {
     uint8_t q[kQBytes];
     uint8_t ring[kEntries * kAtEntry];
     long long base[RKV_MAX_BATCH + 1];
-    uint64_t full[kEntries], empty[kEntries], s[2], p[2], o[2], qf[2], out[2], ml;
+    uint64_t full[kEntries], empty[kEntries], s[2], p[2], o[2], qf[2], out[2], ml, drained;
     uint32_t groups[kEntries];  // a K entry's 16-key groups that were loaded (page ids in range)
     uint32_t sgroups[2];        // the same for the tile whose logits a slot holds
     uint32_t tmem_base;
@@ -906,6 +906,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
       mbar_init(&sh.out[s], kWide ? 128 : 256);
     }
     mbar_init(ml_b, 256);
+    mbar_init(&sh.drained, 1);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -1399,11 +1400,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_tiles_kernel(const __gri
   if (abort_flag) {
     if ((warp == 8 || warp == 10) && lane == 0)
       for (int i = loaded > E ? loaded - E : 0; i < loaded; ++i) mbar_wait(&full_b[i % E], (uint32_t)((i / E) & 1));
-    if (warp == 9 && lane == 0) {  // everything issued before this commit has completed when it arrives
-      tc_commit(&o_b[0]);
-      const uint64_t t0 = global_ns();
-      while (global_ns() - t0 < 1000000ull) {
-      }
+    if (warp == 9) {  // everything this lane issued before the commit has completed when it arrives
+      tc_commit_if(elect_lane(), &sh.drained);
+      mbar_wait(&sh.drained, 0);
     }
     __syncthreads();
   }
