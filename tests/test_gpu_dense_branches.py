@@ -169,3 +169,88 @@ def test_the_same_call_twice_gives_the_same_bits(rkv):
         for other in runs[1:]:
             assert all(torch.equal(a, b) for a, b in zip(runs[0], other)), (lens, T)
         assert _status(rkv, cache) == 0
+
+
+def _round(rkv, seed, lens, T, G, P=16, room=20000):
+    """A cache of its own, what a round of decoding over it needs, and the round: tree, commit,
+    the path's weights, a prompt's weights, one token, eviction in place."""
+    Hkv, B = 2, len(lens)
+    g = C.gen(seed)
+    cache, _, _ = C.make_cache(rkv, lens, Hkv, P, seed=seed, room=room)
+    q, kt, vt = C.randn(g, B, Hkv * G, T, D).cuda(), C.randn(g, B, Hkv, T, D).cuda(), C.randn(g, B, Hkv, T, D).cuda()
+    mask = C.mask_words(C.ancestors(B, T, g)).cuda()
+    path = torch.randint(0, T, (B, 5), generator=g).to(torch.int32).cuda()
+    plen = torch.randint(1, 6, (B,), generator=g).to(torch.int32).cuda()
+    rows = 150
+    qr, lr = C.randn(g, B, Hkv * G, rows, D).cuda(), (torch.rand(B, Hkv * G, rows, generator=g) * 4 + 6).cuda()
+    few = torch.full((B,), rows - 7, dtype=torch.int32, device="cuda")
+    q1 = C.randn(g, B, Hkv * G, D).cuda()
+    out = torch.zeros(B, Hkv * G, T, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(B, Hkv * G, T, device="cuda")
+    one = torch.zeros(B, Hkv * G, D, dtype=torch.bfloat16, device="cuda")
+    acc = rkv.accum_sums(cache)
+    keep = [max(200, n - 3) for n in lens]
+    kept = torch.zeros(B, Hkv, max(keep), dtype=torch.int32, device="cuda")
+    size = (B, Hkv * G, Hkv)
+    ws = [rkv.tree_workspace(*size, T, cache.max_pages, P), rkv.accum_rows_workspace(*size, T, cache.max_pages, P),
+          rkv.accum_rows_workspace(*size, rows, cache.max_pages, P), rkv.accum_workspace(*size, cache.max_pages, P),
+          rkv.evict_workspace(B, Hkv, max(keep))]
+
+    def run():
+        rkv.rkv_tree_attention(cache, q, kt, vt, mask, out, lse=lse, workspace=ws[0])
+        rkv.rkv_tree_commit(cache, kt, vt, path, plen)
+        rkv.rkv_accum_rows(cache, q, lse, acc, row_len=plen, row_ids=path, workspace=ws[1])
+        rkv.rkv_accum_rows(cache, qr, lr, acc, row_len=few, workspace=ws[2])
+        rkv.rkv_decode_accum(cache, q1, one, acc, workspace=ws[3])
+        rkv.rkv_evict_accum(cache, acc, keep, 20, kept, workspace=ws[4])
+
+    def state():
+        assert _status(rkv, cache) == 0
+        return [t.cpu().view(torch.int16 if t.dtype == torch.bfloat16 else torch.int32).clone() for t in
+                (out, lse, one, acc, kept, cache.seq_len, cache.k_pages, cache.v_pages, cache.kmax, cache.kmin)]
+
+    return run, state
+
+
+SHAPES = [(201, [3000, 250, 900], 30, 4), (202, [2500], 70, 4), (203, [400, 700], 3, 4), (204, [5000, 300], 16, 8)]
+
+
+def test_calls_on_several_streams_at_once(rkv):
+    want = []
+    for shape in SHAPES:
+        run, state = _round(rkv, *shape)
+        for _ in range(4):
+            run()
+        want.append(state())
+    rounds = [_round(rkv, *shape) for shape in SHAPES]
+    streams = [torch.cuda.Stream() for _ in SHAPES]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for (run, _), s in zip(rounds, streams):
+            with torch.cuda.stream(s):
+                run()
+    torch.cuda.synchronize()
+    for i, (_, state) in enumerate(rounds):
+        for j, (a, b) in enumerate(zip(state(), want[i])):
+            assert torch.equal(a, b), f"shape {i}, tensor {j}"
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_a_round_with_its_eviction_captured_and_replayed(rkv, shape):
+    run, state = _round(rkv, *shape)
+    for _ in range(4):
+        run()
+    want = state()
+    run, state = _round(rkv, *shape)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            run()
+        for _ in range(3):
+            graph.replay()
+    torch.cuda.synchronize()
+    for j, (a, b) in enumerate(zip(state(), want)):
+        assert torch.equal(a, b), f"tensor {j}"
