@@ -747,8 +747,9 @@ def self_or_range(xs):
     return xs[0] if len(set(xs)) == 1 else f"{min(xs)}..{max(xs)}"
 
 
-# the headers every kernel source includes: part of each kernel's code
-KERNEL_HEADERS = ("two_stage_kv_snapkv_gb300/csrc/rkv_device.cuh", "two_stage_kv_snapkv_gb300/csrc/rkv_internal.h",
+# the headers kernel sources include: part of each kernel's code
+KERNEL_HEADERS = ("two_stage_kv_snapkv_gb300/csrc/rkv_device.cuh", "two_stage_kv_snapkv_gb300/csrc/rkv_bins.h",
+                  "two_stage_kv_snapkv_gb300/csrc/rkv_select.cuh", "two_stage_kv_snapkv_gb300/csrc/rkv_internal.h",
                   "include/rkv.h")
 
 

@@ -819,7 +819,8 @@ constexpr float kAtSlack = 8.f;
 // not.  The difference, at most 2^-24 of m, is the same for the whole row and cancels, while
 // it is no more than 64.  A row whose maximum lies beyond this has distinct logits at least
 // 64 apart, so that only ties with the maximum count: it takes the power of two below sl,
-// whose product with the maximum is exact.
+// whose product with the maximum is exact.  The choice is made where the maximum moves: 266 us
+// for the ragged batch of 63 nodes against 264 without it, 280 with a test in every tile.
 constexpr float kAtFar = 1073741824.f;
 // The tiled kernel's table: only the line's offsets; a run's lengths are read again.
 struct SlimRun : FlatRun {
