@@ -268,8 +268,9 @@ __global__ void __launch_bounds__(RowsShape<kR16>::kWarps * 32, 1)
 // for every key and, for row i, -lse_i / scale as three bf16 terms (24 bits), so the
 // accumulator is (z - lse) / scale and the sum a product, an exponential and an addition
 // per cell.  The three terms keep an lse to 2^-24, as its product with log2 e does in
-// accum_rows; the sums of 16K rows come out within 5e-7 of the 64-bit ones.  (Read from shared memory instead, 16 loads a warp and tile, the sums of a tile
-// took 2619 clocks beside running products, which use all of its bandwidth, and 1244 alone.)
+// accum_rows; the sums of 16K rows come out within 5e-7 of the 64-bit ones.  (Read from
+// shared memory instead, 16 loads a warp and tile, the sums of a tile took 2619 clocks
+// beside running products, which use all of its bandwidth, and 1244 alone.)
 // Per piece 2 x 128 x nq x 144 multiply-adds and 256 nq exponentials; at nq = 128 the
 // products take 1152 clocks of an SM and the exponentials 1024 at 32 a clock: two
 // accumulators a key tile keep both busy.  Measured: 16K rows x 32 heads 845 us, 1.3 PFLOP/s
