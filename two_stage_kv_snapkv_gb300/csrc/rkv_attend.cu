@@ -18,7 +18,7 @@
 // .. 32K (1.22 GB) 210 us.
 #include <cooperative_groups.h>
 
-#include "rkv_flat.cuh"
+#include "rkv_attend.cuh"
 #include "rkv_internal.h"
 
 namespace rkv {
@@ -34,10 +34,6 @@ constexpr int kArMergeRows = 4;                   // rows of every warp that mee
 constexpr int kArMergeFloats = kArWarps * kArMergeRows * 128;
 constexpr int kArSmem = 1024 + kArWarps * kArStages * kArStageBytes + kArMergeFloats * 4;
 constexpr int kArPad = 16, kAtPad = 4;           // what a run costs, in chunks of 16 and tiles of 128 keys
-// Running maximum of a row that saw nothing: no logit lies below it, and differences with
-// it are never inf - inf.
-constexpr float kNoMax = -3.402823466e+38f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWeighTokens = 2048;                // tokens of a weighing block, eight a thread
 
 struct AttendParams {
@@ -96,10 +92,6 @@ __device__ __forceinline__ size_t out_row(const AttendParams& p, int b, int g, i
   return ((size_t)b * p.Hq + g * p.G + (r & (p.G - 1))) * p.T + (r >> p.gshift);
 }
 
-// A row's results from its maximum m and sum l.  l = 0: it saw nothing, and nothing is what it
-// weighs; a NaN among its logits has left l a NaN, which stays one.
-__device__ __forceinline__ float inverse_of(float l) { return l == 0.f ? 0.f : 1.f / l; }
-__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
 // What turns base-2 logits into weights, 2^(z - m) / l: not 2^(z - log-sum-exp), whose sum
 // m + log2 l keeps nothing of l once m is past 2^24.
 __device__ __forceinline__ float2 norm_of(float m, float l) { return make_float2(m, inverse_of(l)); }
@@ -622,15 +614,6 @@ __global__ void __launch_bounds__(UnitsShape<kWarps>::kThreads) attend_units_ker
   }
   cluster.sync();  // no CTA leaves while another still reads its shared memory
 }
-
-// Where the parts of a split unit lie: CTA c's at slot 2 c, but the first CTA's at 2 c + 1
-// when its share began before the unit.
-struct PartSlots {
-  int c0, c1, late;
-  __device__ __forceinline__ PartSlots(long long ux, int per, int pad, long long total, int N)
-      : c0(flat_cta(ux + pad, total, N)), c1(flat_cta(ux + per - 1, total, N)), late(flat_first(total, c0, N) < ux) {}
-  __device__ __forceinline__ size_t operator[](int c) const { return 2 * (size_t)c + (c == c0 ? late : 0); }
-};
 
 // Final (m, l) of one row of a split unit: the lanes of a warp take its parts.
 template <int kRows>
