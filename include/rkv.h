@@ -59,7 +59,8 @@ typedef enum {
 #define RKV_DEVERR_CAPACITY  0x2  /* seq_len (+ appended tokens) beyond max_pages * page_size */
 #define RKV_DEVERR_TIMEOUT   0x4  /* a bounded wait on an mbarrier ran out */
 #define RKV_DEVERR_SEQ_LEN   0x8  /* device seq_len differs from the held_len the host passed */
-#define RKV_DEVERR_TREE      0x10 /* a tree_len, path_len, row_len or node id out of range */
+#define RKV_DEVERR_TREE      0x10 /* a tree_len, path_len, row_len, new_len or node id out of range */
+#define RKV_DEVERR_POOL      0x20 /* too few free pages, or a page count that cannot be */
 
 #define RKV_HEAD_DIM 128
 #define RKV_MAX_BATCH 256
@@ -502,6 +503,190 @@ rkv_status rkv_evict_accum(const rkv_cache* cache, float* acc, int32_t acc_strid
                            void* stream);
 
 /*
+ * The pages of a pool that no sequence holds, as a stack, and how many pages each sequence
+ * holds (all device memory, caller-owned).
+ *   free_pages : [num_phys_pages] int32, the free pages' ids in the first free_count entries,
+ *                the top of the stack last.
+ *   free_count : one int32.
+ *   held       : [B] int32, pages of sequence b: page_table[b][0 .. held[b]).
+ *   sync       : one int32, zero when the pool is created; every call leaves it at zero.
+ *   error_word : one int32 receiving RKV_DEVERR_* bits.
+ */
+typedef struct {
+  int32_t* free_pages;
+  int32_t* free_count;
+  int32_t* held;
+  int32_t* sync;
+  int32_t* error_word;
+  int32_t num_phys_pages;
+} rkv_page_pool;
+
+/*
+ * Page tables and slot maps from the sequences' lengths, on the device.  Sequence b is to
+ * hold ceil(len[b] / page_size) pages.  Those that hold more give their last ones back: they
+ * go on the stack in the order of the sequences and of their pages.  Then those that hold
+ * fewer take pages off its top, in the order of the sequences, into page_table[b][held[b]
+ * ..].  A length of 0 releases a sequence.  Sequences are served in order while the stack
+ * lasts: the first whose pages, with those of the takers before it, are more than there
+ * are, and every taker behind it, keep what they hold and set RKV_DEVERR_POOL.  A len[b]
+ * outside [0, max_pages * page_size] sets RKV_DEVERR_CAPACITY, a held[b] outside [0,
+ * max_pages] or a free_count outside [0, num_phys_pages] RKV_DEVERR_POOL; such a sequence
+ * (with a bad count, every one) keeps what it holds.  Entries of page_table behind a
+ * sequence's pages mean nothing and are left as they were, as are those of free_pages behind
+ * the stack's top.
+ *   page_table : device [B][max_pages] int32 (an rkv_cache's or rkv_cache8's); max_pages as
+ *                there.
+ *   len        : device [B] int32.
+ *   start      : device [B] int32, or NULL when no slots are wanted.  Sequence b, if it was
+ *                served, gets the slots of its positions [start[b], len[b]): page id *
+ *                page_size + place in the page, the row of one KV head's [page][place] where
+ *                the position's key and value go (none when start[b] >= len[b]).  A negative
+ *                start[b] sets RKV_DEVERR_CAPACITY and gets none.
+ *   slots      : device [slots_size] int32: the sequences' slots one behind the other; what
+ *                lies behind them is left as it was.  Those that do not fit set
+ *                RKV_DEVERR_CAPACITY and are not written.  -1 for a page whose id is out of
+ *                range (RKV_DEVERR_PAGE_ID).
+ *   first      : device [B + 1] int32: sequence b's slots are first[b] .. first[b + 1) - 1.
+ *   held_out, free_count_out : where the new counts go: pool->held and pool->free_count, or
+ *                copies that leave the old ones as they are.
+ */
+rkv_status rkv_reserve_pages(const rkv_page_pool* pool, int32_t* page_table, int32_t B, int32_t max_pages,
+                             int32_t page_size, const int32_t* len, const int32_t* start, int32_t* slots,
+                             int32_t slots_size, int32_t* first, int32_t* held_out, int32_t* free_count_out,
+                             void* stream);
+
+/* How rotary frequencies are slowed down for contexts beyond the one they were trained on. */
+#define RKV_ROTARY_PLAIN  0  /* f_i = base^(-2 i / rot_dim) */
+#define RKV_ROTARY_LINEAR 1  /* f_i / factor */
+#define RKV_ROTARY_TURNS  2  /* f_i (w + (1 - w) / factor), w = ramp(r), r = original_len f_i / 2 pi turns */
+#define RKV_ROTARY_LOGS   3  /* the same with w = ramp(log r); ramp(x) = (x - lo) / (hi - lo) in [0, 1], its ends
+                              * low and high turns */
+
+/* Rotary positions of one model: filled by rkv_rotary_init, read by rkv_rotary. */
+typedef struct {
+  uint64_t turns[RKV_HEAD_DIM / 2]; /* f_i / 2 pi as a fraction of 2^64: angles are exact modulo a turn */
+  float amplitude;                  /* factor of both sine and cosine */
+  int32_t rot_dim;                  /* rotated channels, the head's first */
+  int32_t interleaved;              /* pairs (2 i, 2 i + 1), else (i, i + rot_dim / 2) */
+} rkv_rotary_plan;
+
+/*
+ * Fills a plan.  rot_dim: a multiple of 16 in [16, 128]; base > 1; factor >= 1 (modes other
+ * than RKV_ROTARY_PLAIN); original_len >= 1 and 0 < low < high (the two ramps); amplitude
+ * finite and > 0.  Host only.
+ */
+rkv_status rkv_rotary_init(rkv_rotary_plan* plan, int32_t rot_dim, double base, int32_t interleaved,
+                           int32_t scaling, double factor, int32_t original_len, double low, double high,
+                           float amplitude);
+
+/*
+ * Rotary positions of a step's queries and keys ("RocketKV-adapted", "Evidence": positions
+ * are the tokens' true ones, not their rows in a compressed cache).  For each token at
+ * position p and each of its heads, with a_i = p f_i and the plan's amplitude s:
+ *   y_u = s (x_u cos a_i - x_v sin a_i),   y_v = s (x_v cos a_i + x_u sin a_i)
+ * over the plan's pairs (u, v); the channels from rot_dim on are copied.  inverse: the
+ * rotation by -a_i (with the same s), which is also the transpose, the gradient's way back.
+ *   q, k      : device bf16, token t of head h of sequence b at q + b q_strides[0] + h
+ *               q_strides[1] + t q_strides[2] (strides in elements, multiples of 8; 16-byte
+ *               aligned; 128 channels contiguous).  k may be NULL (then Hkv is 0).
+ *   q_out, k_out : the same with their own strides.  An output is its input (same address
+ *               and strides) or overlaps no input.
+ *   positions : device int32, [B][T] (per_token nonzero) or [B]: token t at positions[b] + t.
+ *               Any int32; a sum beyond 2^31 wraps.
+ * Angles are exact modulo a turn for every position; sines and cosines are fp32, and the
+ * result is rounded once.
+ */
+rkv_status rkv_rotary(const rkv_rotary_plan* plan, const rkv_bf16* q, const int64_t* q_strides, const rkv_bf16* k,
+                      const int64_t* k_strides, int32_t B, int32_t Hq, int32_t Hkv, int32_t T,
+                      const int32_t* positions, int32_t per_token, int32_t inverse, rkv_bf16* q_out,
+                      const int64_t* q_out_strides, rkv_bf16* k_out, const int64_t* k_out_strides, void* stream);
+
+/* Codes of an 8-bit cache. */
+#define RKV_Q8_E4M3 0  /* sign, 4 bits of exponent, 3 of mantissa; up to 448 */
+#define RKV_Q8_INT8 1  /* signed integers -127 .. 127 */
+
+/*
+ * The paged KV cache of one attention layer held in 8 bits (all device memory,
+ * caller-owned): value = code * scale, one scale for each page and KV head for K and one for V.
+ *   k_codes, v_codes : [num_phys_pages][Hkv][page_size][head_dim] bytes; pages, tables and
+ *                      lengths as in rkv_cache.
+ *   k_scale, v_scale : [num_phys_pages][Hkv] fp32, powers of two >= 2^-126: the smallest one
+ *                      that brings the block's largest magnitude into the codes' range
+ *                      (so that a code times its scale is a bf16 value, a block's codes move
+ *                      to a larger scale without a second error but where they leave the
+ *                      range at its small end, and nothing depends on rounded divisions).
+ *                      NaN, for both, in a page and head that was given a NaN or an infinity:
+ *                      every row that sees one of its tokens is NaN.
+ *   error_word       : one int32 receiving RKV_DEVERR_* bits.
+ *   sync             : [B] int32, zero when the cache is created; every call leaves it at zero.
+ * Limits as rkv_cache's.
+ */
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_scale;
+  float* v_scale;
+  int32_t* page_table;
+  int32_t* seq_len;
+  int32_t* error_word;
+  int32_t* sync;
+  int32_t B, Hkv, head_dim, page_size, max_pages, num_phys_pages, format;
+} rkv_cache8;
+
+/*
+ * New tokens enter the 8-bit cache: for each sequence the first new_len[b] rows of k_new and
+ * v_new go to positions seq_len[b], ..., and seq_len[b] += new_len[b].  A page that starts
+ * with this call gets the scale of its new rows; one that already holds tokens keeps the
+ * larger of its scale and theirs, and where that is theirs its codes are rounded to it.
+ * Codes are rounded to the nearest, ties to even.  Calls that write one cache are ordered by
+ * the caller (one stream).
+ *   k_new, v_new : device bf16, row t of KV head g of sequence b at k_new + b k_strides[0] +
+ *              g k_strides[1] + t k_strides[2] (strides in elements, multiples of 8; 16-byte
+ *              aligned; 128 channels contiguous).
+ *   T        : rows of k_new and v_new, 1 <= T <= 2^20.
+ *   new_len  : device [B] int32 in [0, T], or NULL for T everywhere.  A value outside sets
+ *              RKV_DEVERR_TREE, a sequence that would outgrow its pages RKV_DEVERR_CAPACITY;
+ *              that sequence is left unchanged.  A page id out of range sets
+ *              RKV_DEVERR_PAGE_ID and that page is not written.
+ */
+rkv_status rkv_q8_append(const rkv_cache8* cache, const rkv_bf16* k_new, const int64_t* k_strides,
+                         const rkv_bf16* v_new, const int64_t* v_strides, int32_t T, const int32_t* new_len,
+                         void* stream);
+
+/*
+ * A bf16 cache becomes an 8-bit one: every sequence's tokens, in their order (what
+ * rkv_prefill_evict or rkv_evict_accum kept, for instance), as rkv_q8_append would take them
+ * into an empty cache; cache->seq_len[b] = src->seq_len[b].  The source is read only.  Both
+ * have the same B, Hkv and page_size.  A sequence whose length is negative or beyond either
+ * side's pages sets RKV_DEVERR_CAPACITY (in cache->error_word) and becomes empty.
+ */
+rkv_status rkv_q8_load(const rkv_cache8* cache, const rkv_cache* src, void* stream);
+
+/* Bytes of workspace rkv_q8_attention needs. */
+size_t rkv_q8_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t max_pages, int32_t page_size);
+
+/*
+ * Attention of the last rows over the 8-bit cache: one decoded token, a chain of drafted ones,
+ * a prompt's chunk, whose keys and values are in the cache already (rkv_q8_append first).  The m = row_len[b] rows
+ * are the cache's last m positions, row i lying at position n - m + i (n = seq_len[b]) and seeing t <= n - m + i:
+ *   z_t = scale * q[b][h][i] . k_t,  out = sum_t exp(z_t) v_t / sum_t exp(z_t),  lse = log sum_t exp(z_t)
+ * with k_t, v_t the values that the codes stand for.  A row that sees nothing (n = 0, or
+ * i < m - n) gets out = 0 and lse = -inf; one with a NaN among its logits gets NaN for both.
+ * Rows i >= row_len[b] of out and lse are left as they were.
+ *   q       : device [B][Hq][T][128] bf16; 1 <= T <= 2^20.
+ *   row_len : device [B] int32 in [0, T], or NULL for T everywhere.  A value outside sets
+ *             RKV_DEVERR_TREE and counts as 0.
+ *   out     : device [B][Hq][T][128] bf16.   lse : device [B][Hq][T] fp32 or NULL.
+ * Logits, maxima, sums and the output's accumulation are fp32; queries, codes and softmax
+ * weights enter the products as fp16 (see rkv_q8_attend.cu for what that rounds).  Lengths
+ * are read on the device, so a captured call can be replayed as the cache grows; scale,
+ * workspaces and unreadable pages as for rkv_tree_attention.
+ */
+rkv_status rkv_q8_attention(const rkv_cache8* cache, const rkv_bf16* q, int32_t Hq, int32_t T,
+                            const int32_t* row_len, float scale, rkv_bf16* out, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
  * Exact-TopK recall of a page selection: a diagnostic, not a step of the method.
  * The summary page of "RocketKV: Accelerating Long-Context LLM Inference via
  * Two-Stage KV Cache Compression" measures RocketKV against the Exact-TopK
@@ -545,6 +730,9 @@ rkv_status rkv_get_device_status(const rkv_cache* cache, void* stream, int32_t* 
 
 /* Message of the last failed call on this thread ("" if none). */
 const char* rkv_last_error(void);
+
+/* The same for any device error word (a page pool's, an 8-bit cache's). */
+rkv_status rkv_read_device_error(int32_t* error_word, void* stream, int32_t* bits);
 
 /* Number of kernels this library has launched in this process. */
 int64_t rkv_launch_count(void);

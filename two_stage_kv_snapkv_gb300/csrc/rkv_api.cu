@@ -1,5 +1,6 @@
 // C ABI of librkv: argument validation, the adaptive ratio split, dispatch to the
 // kernel launchers, error reporting, launch counting and optional per-kernel timing.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -130,7 +131,8 @@ const char* kernel_name(int kind) {
       "hsa_topk",     "hsa_attend",   "hsa_combine",    "hsa_step",     "recall",
       "chunk_gather", "sparq_score",  "sparq_topk",     "sparq_attend", "wait_selftest",
       "sparq_keys_sync", "attend_rows", "attend_tiles", "attend_units", "attend_combine", "attend_weigh", "tree_commit",
-      "accum_rows", "accum_tiles", "accum_join", "evict_select", "evict_stage", "evict_compact"};
+      "accum_rows", "accum_tiles", "accum_join", "evict_select", "evict_stage", "evict_compact",
+      "reserve_pages", "rotary", "q8_append", "q8_load", "q8_rows", "q8_join"};
   return (kind >= 0 && kind < K_NUM_KINDS) ? names[kind] : nullptr;
 }
 
@@ -178,7 +180,7 @@ int num_sms() {
 }
 
 
-bool encode_rows_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
+static PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   // cuTensorMapEncodeTiled from the driver, looked up once per process
   static std::once_flag once;
   static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
@@ -189,14 +191,28 @@ bool encode_rows_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t b
         q == cudaDriverEntryPointSuccess)
       enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
   });
+  return enc;
+}
+
+// 128-byte wide boxes of rows of 128 elements, 128-byte swizzle.
+static bool encode_map(CUtensorMap* m, CUtensorMapDataType type, int bytes, const void* base, uint64_t rows,
+                       uint32_t box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
   if (!enc) return false;
   cuuint64_t dims[2] = {128, rows};
-  cuuint64_t strides[1] = {256};
-  cuuint32_t box[2] = {64, box_rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(128 * bytes)};
+  cuuint32_t box[2] = {(cuuint32_t)(128 / bytes), box_rows};
   cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_rows_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, box_rows);
+}
+bool encode_codes_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, rows, box_rows);
 }
 
 }  // namespace rkv
@@ -825,6 +841,249 @@ rkv_status rkv_evict_accum(const rkv_cache* cache, float* acc, int32_t acc_strid
   return cuda_status(rkv::launch_evict(a, static_cast<cudaStream_t>(stream)), "rkv_evict_accum launch");
 }
 
+// ------------------------------------------------------------------ pages and positions
+rkv_status rkv_reserve_pages(const rkv_page_pool* pool, int32_t* page_table, int32_t B, int32_t max_pages,
+                             int32_t page_size, const int32_t* len, const int32_t* start, int32_t* slots,
+                             int32_t slots_size, int32_t* first, int32_t* held_out, int32_t* free_count_out,
+                             void* stream) {
+  const NvtxRange nvtx_range("rkv_reserve_pages");
+  if (!pool) return fail(RKV_ERR_INVALID_ARG, "pool is NULL");
+  if (!pool->free_pages || !pool->free_count || !pool->held || !pool->sync || !pool->error_word || !page_table || !len ||
+      !held_out || !free_count_out)
+    return fail(RKV_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!al4(pool->free_pages) || !al4(pool->free_count) || !al4(pool->held) || !al4(pool->sync) ||
+      !al4(pool->error_word) || !al4(page_table) || !al4(len) || !al4(start) || !al4(slots) || !al4(first) ||
+      !al4(held_out) || !al4(free_count_out))
+    return fail(RKV_ERR_INVALID_ARG, "int32 pointers must be 4-byte aligned");
+  if (B < 1 || B > RKV_MAX_BATCH) return fail(RKV_ERR_INVALID_ARG, "B=%d outside [1, %d]", B, RKV_MAX_BATCH);
+  if (page_size != 16 && page_size != 32 && page_size != 64)
+    return fail(RKV_ERR_UNSUPPORTED, "page_size %d unsupported (16, 32 or 64)", page_size);
+  if (max_pages < 8 || max_pages % 8 != 0)
+    return fail(RKV_ERR_INVALID_ARG, "max_pages=%d must be a positive multiple of 8", max_pages);
+  if (max_pages > 16384) return fail(RKV_ERR_UNSUPPORTED, "max_pages=%d above 16384", max_pages);
+  if (pool->num_phys_pages < 1) return fail(RKV_ERR_INVALID_ARG, "num_phys_pages=%d", pool->num_phys_pages);
+  if ((long long)pool->num_phys_pages * page_size >= (1LL << 31))
+    return fail(RKV_ERR_UNSUPPORTED, "slots are 32-bit integers: num_phys_pages * page_size must be below 2^31");
+  if (start && (!slots || !first)) return fail(RKV_ERR_INVALID_ARG, "start is given without slots and first");
+  if (start && slots_size < 0) return fail(RKV_ERR_INVALID_ARG, "slots_size=%d", slots_size);
+  rkv::ReserveArgs a;
+  a.pool = *pool;
+  a.page_table = page_table;
+  a.B = B;
+  a.max_pages = max_pages;
+  a.page_size = page_size;
+  a.len = len;
+  a.start = start;
+  a.slots = slots;
+  a.slots_size = slots_size;
+  a.first = first;
+  a.held_out = held_out;
+  a.free_count_out = free_count_out;
+  return cuda_status(rkv::launch_reserve_pages(a, static_cast<cudaStream_t>(stream)), "rkv_reserve_pages launch");
+}
+
+rkv_status rkv_rotary_init(rkv_rotary_plan* plan, int32_t rot_dim, double base, int32_t interleaved, int32_t scaling,
+                           double factor, int32_t original_len, double low, double high, float amplitude) {
+  if (!plan) return fail(RKV_ERR_INVALID_ARG, "plan is NULL");
+  if (rot_dim < 16 || rot_dim > RKV_HEAD_DIM || rot_dim % 16 != 0)
+    return fail(RKV_ERR_UNSUPPORTED, "rot_dim=%d must be a multiple of 16 in [16, %d]", rot_dim, RKV_HEAD_DIM);
+  if (!(base > 1.0) || !std::isfinite(base)) return fail(RKV_ERR_INVALID_ARG, "base must be above 1");
+  if (scaling < RKV_ROTARY_PLAIN || scaling > RKV_ROTARY_LOGS)
+    return fail(RKV_ERR_INVALID_ARG, "scaling=%d is none of RKV_ROTARY_*", scaling);
+  if (scaling != RKV_ROTARY_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return fail(RKV_ERR_INVALID_ARG, "factor must be at least 1");
+  const bool ramps = scaling == RKV_ROTARY_TURNS || scaling == RKV_ROTARY_LOGS;
+  if (ramps && original_len < 1) return fail(RKV_ERR_INVALID_ARG, "original_len=%d", original_len);
+  if (ramps && (!(low > 0.0) || !(high > low) || !std::isfinite(high)))
+    return fail(RKV_ERR_INVALID_ARG, "the ramp needs 0 < low < high");
+  if (!(amplitude > 0.f) || !std::isfinite(amplitude)) return fail(RKV_ERR_INVALID_ARG, "amplitude must be positive");
+  const double two_pi = 6.283185307179586476925286766559;
+  for (int i = 0; i < RKV_HEAD_DIM / 2; ++i) {
+    plan->turns[i] = 0;
+    if (i >= rot_dim / 2) continue;
+    double f = std::pow(base, -2.0 * i / rot_dim);
+    if (scaling == RKV_ROTARY_LINEAR) f /= factor;
+    if (ramps) {
+      const double turns = original_len * f / two_pi;
+      double w = scaling == RKV_ROTARY_LOGS ? (std::log(turns) - std::log(low)) / (std::log(high) - std::log(low))
+                                            : (turns - low) / (high - low);
+      w = w < 0.0 ? 0.0 : (w > 1.0 ? 1.0 : w);
+      f *= w + (1.0 - w) / factor;
+    }
+    // f <= 1 rad, a sixth of a turn: the fraction fits 64 bits, and a double's 53 are kept
+    plan->turns[i] = (uint64_t)std::llrint(std::ldexp(f / two_pi, 64));
+  }
+  plan->amplitude = amplitude;
+  plan->rot_dim = rot_dim;
+  plan->interleaved = interleaved != 0;
+  return RKV_OK;
+}
+
+// Strides of [sequence][head][token] rows of 128 contiguous bf16 channels.
+static rkv_status check_strides(const int64_t* st, const char* what) {
+  if (!st) return fail(RKV_ERR_INVALID_ARG, "%s's strides are NULL", what);
+  for (int i = 0; i < 3; ++i)
+    if (st[i] < 0 || st[i] % 8 != 0)
+      return fail(RKV_ERR_INVALID_ARG, "%s's strides must be non-negative multiples of 8 elements", what);
+  return RKV_OK;
+}
+
+// Rows that are written: no two of them may share a channel.  True when, the dimensions of
+// more than one element taken by falling stride, each steps over all that the next ones span.
+static bool rows_apart(const int64_t* st, int B, int H, int T) {
+  int64_t s[3] = {st[0], st[1], st[2]}, n[3] = {B, H, T};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (s[j] > s[i]) {
+        std::swap(s[i], s[j]);
+        std::swap(n[i], n[j]);
+      }
+  int64_t span = RKV_HEAD_DIM;
+  for (int i = 2; i >= 0; --i) {
+    if (n[i] > 1 && s[i] < span) return false;
+    if (n[i] > 1) span += (n[i] - 1) * s[i];
+  }
+  return true;
+}
+
+rkv_status rkv_rotary(const rkv_rotary_plan* plan, const rkv_bf16* q, const int64_t* q_strides, const rkv_bf16* k,
+                      const int64_t* k_strides, int32_t B, int32_t Hq, int32_t Hkv, int32_t T,
+                      const int32_t* positions, int32_t per_token, int32_t inverse, rkv_bf16* q_out,
+                      const int64_t* q_out_strides, rkv_bf16* k_out, const int64_t* k_out_strides, void* stream) {
+  const NvtxRange nvtx_range("rkv_rotary");
+  if (!plan || !q || !q_out || !positions) return fail(RKV_ERR_INVALID_ARG, "a required pointer is NULL");
+  if ((k == nullptr) != (k_out == nullptr)) return fail(RKV_ERR_INVALID_ARG, "k and k_out must both be given, or neither");
+  if (plan->rot_dim < 16 || plan->rot_dim > RKV_HEAD_DIM || plan->rot_dim % 16 != 0)
+    return fail(RKV_ERR_INVALID_ARG, "the plan was not filled by rkv_rotary_init");
+  if (B < 1 || T < 1 || Hq < 1 || Hkv < (k ? 1 : 0)) return fail(RKV_ERR_INVALID_ARG, "sizes must be positive");
+  if ((long long)B * T >= (1LL << 31) || Hq > (1 << 16) || Hkv > (1 << 16))
+    return fail(RKV_ERR_UNSUPPORTED, "B * T must be below 2^31 and heads at most 65536");
+  if (!al16(q) || !al16(q_out) || !al16(k) || !al16(k_out))
+    return fail(RKV_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if (!al4(positions)) return fail(RKV_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+  rkv_status st;
+  if ((st = check_strides(q_strides, "q")) != RKV_OK || (st = check_strides(q_out_strides, "q_out")) != RKV_OK) return st;
+  if (k && ((st = check_strides(k_strides, "k")) != RKV_OK || (st = check_strides(k_out_strides, "k_out")) != RKV_OK))
+    return st;
+  if (!rows_apart(q_out_strides, B, Hq, T) || (k && !rows_apart(k_out_strides, B, Hkv, T)))
+    return fail(RKV_ERR_INVALID_ARG, "rows of an output overlap");
+  rkv::RotaryArgs a;
+  a.plan = *plan;
+  a.q = q;
+  a.k = k;
+  a.q_strides = q_strides;
+  a.k_strides = k_strides;
+  a.q_out_strides = q_out_strides;
+  a.k_out_strides = k_out_strides;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.T = T;
+  a.positions = positions;
+  a.per_token = per_token != 0;
+  a.inverse = inverse != 0;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  return cuda_status(rkv::launch_rotary(a, static_cast<cudaStream_t>(stream)), "rkv_rotary launch");
+}
+
+// ------------------------------------------------------------------ the 8-bit cache
+static rkv_status check_cache8(const rkv_cache8* c) {
+  if (!c) return fail(RKV_ERR_INVALID_ARG, "cache is NULL");
+  if (c->head_dim != RKV_HEAD_DIM) return fail(RKV_ERR_UNSUPPORTED, "head_dim %d unsupported (only 128)", c->head_dim);
+  if (c->format != RKV_Q8_E4M3 && c->format != RKV_Q8_INT8)
+    return fail(RKV_ERR_UNSUPPORTED, "format %d is none of RKV_Q8_*", c->format);
+  if (c->B < 1 || c->B > RKV_MAX_BATCH) return fail(RKV_ERR_INVALID_ARG, "B=%d outside [1, %d]", c->B, RKV_MAX_BATCH);
+  if (c->Hkv < 1) return fail(RKV_ERR_INVALID_ARG, "Hkv=%d", c->Hkv);
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64)
+    return fail(RKV_ERR_UNSUPPORTED, "page_size %d unsupported (16, 32 or 64)", c->page_size);
+  if (c->max_pages < 8 || c->max_pages % 8 != 0)
+    return fail(RKV_ERR_INVALID_ARG, "max_pages=%d must be a positive multiple of 8", c->max_pages);
+  if (c->max_pages > 16384) return fail(RKV_ERR_UNSUPPORTED, "max_pages=%d above 16384", c->max_pages);
+  if (c->num_phys_pages < 1) return fail(RKV_ERR_INVALID_ARG, "num_phys_pages=%d", c->num_phys_pages);
+  if ((long long)c->num_phys_pages * c->Hkv * c->page_size >= (1LL << 31))
+    return fail(RKV_ERR_UNSUPPORTED, "the page pools' rows are indexed with 32-bit integers (TMA coordinates)");
+  if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale || !c->page_table || !c->seq_len || !c->error_word ||
+      !c->sync)
+    return fail(RKV_ERR_INVALID_ARG, "a cache pointer is NULL");
+  if (!al16(c->k_codes) || !al16(c->v_codes) || !al16(c->page_table))
+    return fail(RKV_ERR_INVALID_ARG, "cache pointers must be 16-byte aligned");
+  if (!al4(c->k_scale) || !al4(c->v_scale) || !al4(c->seq_len) || !al4(c->error_word) || !al4(c->sync))
+    return fail(RKV_ERR_INVALID_ARG, "scales, seq_len, error_word and sync must be 4-byte aligned");
+  return RKV_OK;
+}
+
+rkv_status rkv_q8_append(const rkv_cache8* cache, const rkv_bf16* k_new, const int64_t* k_strides,
+                         const rkv_bf16* v_new, const int64_t* v_strides, int32_t T, const int32_t* new_len,
+                         void* stream) {
+  const NvtxRange nvtx_range("rkv_q8_append");
+  rkv_status st = check_cache8(cache);
+  if (st != RKV_OK) return st;
+  if (!k_new || !v_new) return fail(RKV_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!al16(k_new) || !al16(v_new)) return fail(RKV_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if (!al4(new_len)) return fail(RKV_ERR_INVALID_ARG, "new_len must be 4-byte aligned");
+  if (T < 1 || T > (1 << 20)) return fail(RKV_ERR_INVALID_ARG, "T=%d outside [1, 2^20]", T);
+  if ((st = check_strides(k_strides, "k_new")) != RKV_OK || (st = check_strides(v_strides, "v_new")) != RKV_OK) return st;
+  rkv::Q8AppendArgs a;
+  a.cache = *cache;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.k_strides = k_strides;
+  a.v_strides = v_strides;
+  a.T = T;
+  a.new_len = new_len;
+  return cuda_status(rkv::launch_q8_append(a, static_cast<cudaStream_t>(stream)), "rkv_q8_append launch");
+}
+
+rkv_status rkv_q8_load(const rkv_cache8* cache, const rkv_cache* src, void* stream) {
+  const NvtxRange nvtx_range("rkv_q8_load");
+  rkv_status st = check_cache8(cache);
+  if (st != RKV_OK || (st = check_cache(src)) != RKV_OK) return st;
+  if (src->B != cache->B || src->Hkv != cache->Hkv || src->page_size != cache->page_size)
+    return fail(RKV_ERR_INVALID_ARG, "the source differs from the cache in B, Hkv or page_size");
+  if (src->seq_len == cache->seq_len)
+    return fail(RKV_ERR_INVALID_ARG, "the source and the cache need lengths of their own");
+  rkv::Q8LoadArgs a;
+  a.cache = *cache;
+  a.src = *src;
+  return cuda_status(rkv::launch_q8_load(a, static_cast<cudaStream_t>(stream)), "rkv_q8_load launch");
+}
+
+size_t rkv_q8_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int32_t max_pages, int32_t page_size) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || max_pages < 1 || page_size < 1) return 0;
+  return rkv::q8_attend_ws_bytes(B, Hq, Hkv, T, max_pages, page_size);
+}
+
+rkv_status rkv_q8_attention(const rkv_cache8* cache, const rkv_bf16* q, int32_t Hq, int32_t T, const int32_t* row_len,
+                            float scale, rkv_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  const NvtxRange nvtx_range("rkv_q8_attention");
+  rkv_status st = check_cache8(cache);
+  if (st != RKV_OK) return st;
+  if ((st = check_heads(Hq, cache->Hkv)) != RKV_OK) return st;
+  if (!q || !out || !workspace) return fail(RKV_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!al16(q) || !al16(out) || !al16(workspace))
+    return fail(RKV_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if (!al4(row_len) || !al4(lse)) return fail(RKV_ERR_INVALID_ARG, "row_len and lse must be 4-byte aligned");
+  if (T < 1 || T > (1 << 20)) return fail(RKV_ERR_INVALID_ARG, "T=%d outside [1, 2^20]", T);
+  if ((long long)cache->B * Hq * T >= (1LL << 31)) return fail(RKV_ERR_UNSUPPORTED, "B * Hq * T above 2^31");
+  if ((st = check_scale(scale)) != RKV_OK) return st;
+  const size_t need = rkv::q8_attend_ws_bytes(cache->B, Hq, cache->Hkv, T, cache->max_pages, cache->page_size);
+  if (workspace_bytes < need)
+    return fail(RKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  rkv::Q8AttendArgs a;
+  a.cache = *cache;
+  a.q = q;
+  a.Hq = Hq;
+  a.T = T;
+  a.row_len = row_len;
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.ws = workspace;
+  return cuda_status(rkv::launch_q8_attend(a, static_cast<cudaStream_t>(stream)), "rkv_q8_attention launch");
+}
+
 rkv_status rkv_exact_topk_recall(const rkv_cache* cache, const rkv_bf16* q, int32_t Hq, const int32_t* sel_pages,
                                  int32_t sel_pages_stride, const int32_t* k_tokens, float scale, float* recall,
                                  float* mass, void* stream) {
@@ -871,20 +1130,26 @@ int32_t rkv_decode_path(int32_t path) {
   return g_decode_path.load();
 }
 
-rkv_status rkv_get_device_status(const rkv_cache* cache, void* stream, int32_t* bits) {
-  const NvtxRange nvtx_range("rkv_get_device_status");
-  if (!cache || !cache->error_word) return fail(RKV_ERR_INVALID_ARG, "cache or error_word is NULL");
+rkv_status rkv_read_device_error(int32_t* error_word, void* stream, int32_t* bits) {
+  const NvtxRange nvtx_range("rkv_read_device_error");
+  if (!error_word) return fail(RKV_ERR_INVALID_ARG, "error_word is NULL");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int32_t word = 0;
-  cudaError_t e = cudaMemcpyAsync(&word, cache->error_word, sizeof word, cudaMemcpyDeviceToHost, s);
+  cudaError_t e = cudaMemcpyAsync(&word, error_word, sizeof word, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && word != 0) e = cudaMemsetAsync(cache->error_word, 0, sizeof word, s);
+  if (e == cudaSuccess && word != 0) e = cudaMemsetAsync(error_word, 0, sizeof word, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return fail(RKV_ERR_CUDA, "rkv_get_device_status: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return fail(RKV_ERR_CUDA, "reading the device error word: %s", cudaGetErrorString(e));
   if (bits) *bits = word;
   if (word == 0) return RKV_OK;
   if (word & RKV_DEVERR_TIMEOUT) return fail(RKV_ERR_TIMEOUT, "a bounded device wait ran out (word 0x%x)", word);
   return fail(RKV_ERR_DEVICE_DATA, "device data error (word 0x%x)", word);
+}
+
+rkv_status rkv_get_device_status(const rkv_cache* cache, void* stream, int32_t* bits) {
+  const NvtxRange nvtx_range("rkv_get_device_status");
+  if (!cache || !cache->error_word) return fail(RKV_ERR_INVALID_ARG, "cache or error_word is NULL");
+  return rkv_read_device_error(cache->error_word, stream, bits);
 }
 
 const char* rkv_last_error(void) { return g_err.c_str(); }

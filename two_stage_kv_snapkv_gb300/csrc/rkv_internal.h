@@ -47,6 +47,12 @@ enum KernelKind {
   K_EVICT_SELECT,
   K_EVICT_STAGE,
   K_EVICT_COMPACT,
+  K_RESERVE_PAGES,
+  K_ROTARY,
+  K_Q8_APPEND,
+  K_Q8_LOAD,
+  K_Q8_ROWS,
+  K_Q8_JOIN,
   K_NUM_KINDS
 };
 const char* kernel_name(int kind);
@@ -103,6 +109,8 @@ void set_last_error(const char* msg);
 // 128-byte swizzle (a box row is 128 B; its 16-byte pieces are XOR-ed with row % 8).
 // False when the driver's encoder is unavailable or rejects the map.
 bool encode_rows_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows);
+// The same for a [rows][128] byte array: box_rows x 128-byte boxes.
+bool encode_codes_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows);
 
 // --------------------------------------------------------------- cache append
 cudaError_t launch_append(const rkv_cache& c, const rkv_bf16* k_new, const rkv_bf16* v_new,
@@ -239,6 +247,64 @@ struct EvictArgs {
 int evict_max_tokens();
 size_t evict_ws_bytes(int B, int Hkv, int max_keep, bool in_place);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
+
+// --------------------------------------------------------------- pages and positions
+struct ReserveArgs {
+  rkv_page_pool pool;
+  int32_t* page_table;
+  int B, max_pages, page_size;
+  const int32_t* len;    // device [B]
+  const int32_t* start;  // device [B], null: no slots
+  int32_t* slots;
+  int slots_size;
+  int32_t* first;  // device [B + 1]
+  int32_t* held_out;
+  int32_t* free_count_out;
+};
+cudaError_t launch_reserve_pages(const ReserveArgs& a, cudaStream_t s);
+
+struct RotaryArgs {
+  rkv_rotary_plan plan;
+  const rkv_bf16* q;
+  const rkv_bf16* k;  // may be null
+  const int64_t *q_strides, *k_strides, *q_out_strides, *k_out_strides;  // host [3]: sequence, head, token
+  int B, Hq, Hkv, T;
+  const int32_t* positions;  // device [B][T] or [B]
+  int per_token, inverse;
+  rkv_bf16* q_out;
+  rkv_bf16* k_out;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s);
+
+// --------------------------------------------------------------- the 8-bit cache
+struct Q8AppendArgs {
+  rkv_cache8 cache;
+  const rkv_bf16* k_new;
+  const rkv_bf16* v_new;
+  const int64_t *k_strides, *v_strides;  // host [3]: sequence, KV head, row
+  int T;
+  const int32_t* new_len;  // device [B] or null
+};
+cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s);
+
+struct Q8LoadArgs {
+  rkv_cache8 cache;
+  rkv_cache src;
+};
+cudaError_t launch_q8_load(const Q8LoadArgs& a, cudaStream_t s);
+
+struct Q8AttendArgs {
+  rkv_cache8 cache;
+  const rkv_bf16* q;  // [B][Hq][T][128]
+  int Hq, T;
+  const int32_t* row_len;  // device [B] or null
+  float scale;
+  rkv_bf16* out;
+  float* lse;  // may be null
+  void* ws;
+};
+size_t q8_attend_ws_bytes(int B, int Hq, int Hkv, int T, int max_pages, int page_size);
+cudaError_t launch_q8_attend(const Q8AttendArgs& a, cudaStream_t s);
 
 // --------------------------------------------------------------- diagnostics
 struct RecallArgs {

@@ -1,0 +1,199 @@
+// Page tables and slot maps from the sequences' lengths.
+//
+// need_b = ceil(len_b / P).  Sequences that hold more give their last pages back, those that
+// hold fewer take pages off the stack's top:
+//   take_b = max(need_b - held_b, 0),  give_b = max(held_b - need_b, 0),
+//   the i-th page taken of all comes from place count + sum(give) - 1 - i of the stack.
+// One launch: every CTA scans the at most 256 sequences for itself (a thread each) and then
+// works on its share of the taken pages and of the slots.  A place of the stack at or above
+// the old count is a page given back in this call and is read from its giver's table, so no
+// CTA waits for another's writes; what one CTA writes (table entries behind `held`, stack
+// places from `count` on) no other reads.  The counts are written by the CTA that finishes
+// last, when every one has read the old ones, so that they may be updated in place.
+#include "rkv_device.cuh"
+#include "rkv_internal.h"
+
+namespace rkv {
+namespace {
+
+constexpr int kRsThreads = 256;
+static_assert(kRsThreads >= RKV_MAX_BATCH, "a thread for every sequence");
+
+struct ReserveParams {
+  int32_t* free_pages;
+  const int32_t* free_count;
+  const int32_t* held;
+  int32_t* sync;
+  int32_t* err;
+  int32_t* page_table;
+  const int32_t* len;
+  const int32_t* start;  // null: no slots
+  int32_t* slots;
+  int32_t* first;
+  int32_t* held_out;
+  int32_t* count_out;
+  int B, max_pages, P, pshift, num_phys, slots_size;
+};
+
+struct ReserveTable {
+  int held[RKV_MAX_BATCH], need[RKV_MAX_BATCH], start[RKV_MAX_BATCH];
+  int take[RKV_MAX_BATCH + 1], give[RKV_MAX_BATCH + 1], slot[RKV_MAX_BATCH + 1];  // running sums
+  int warp_sum[kRsThreads / 32];
+  int last;
+};
+
+// sum[t] = values of the threads before t, sum[blockDim.x] the total.
+__device__ __forceinline__ int scan_into(ReserveTable& rt, int* sum, int x) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();  // warp_sum is free
+  if (lane == 31) rt.warp_sum[warp] = incl;
+  __syncthreads();
+  int before = 0;
+#pragma unroll
+  for (int w = 0; w < kRsThreads / 32; ++w) before += w < warp ? rt.warp_sum[w] : 0;
+  if (tid < RKV_MAX_BATCH) {
+    sum[tid] = before + incl - x;
+    if (tid == RKV_MAX_BATCH - 1) sum[RKV_MAX_BATCH] = before + incl;
+  }
+  return before + incl - x;
+}
+
+// The last sequence b with sum[b] <= x (sequences without a share have the next one's sum).
+__device__ __forceinline__ int holder(const int* sum, int B, int x) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sum[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kRsThreads) reserve_pages_kernel(const __grid_constant__ ReserveParams p) {
+  __shared__ ReserveTable rt;
+  const int tid = threadIdx.x, b = tid;
+  const bool lead = blockIdx.x == 0;
+  const int count = *p.free_count;
+  const bool stack_ok = count >= 0 && count <= p.num_phys;
+  int held = 0, need = 0, len = 0, start = 0, bad = 0;
+  bool ok = false;
+  if (b < p.B) {
+    held = p.held[b];
+    len = p.len[b];
+    start = p.start ? p.start[b] : 0;
+    ok = stack_ok;
+    if (!stack_ok || held < 0 || held > p.max_pages) {
+      bad |= RKV_DEVERR_POOL;
+      ok = false;
+    }
+    if (len < 0 || len > p.max_pages * p.P) {
+      bad |= RKV_DEVERR_CAPACITY;
+      ok = false;
+    }
+    if (start < 0) bad |= RKV_DEVERR_CAPACITY;
+    need = ok ? (len + p.P - 1) >> p.pshift : held;
+  }
+  scan_into(rt, rt.give, ok ? max(held - need, 0) : 0);
+  const int take = ok ? max(need - held, 0) : 0;
+  const int before = scan_into(rt, rt.take, take);
+  __syncthreads();
+  const int given = rt.give[RKV_MAX_BATCH], have = (stack_ok ? count : 0) + given;
+  if (take > 0 && before + take > have) {  // not served, nor is any taker behind it
+    bad |= RKV_DEVERR_POOL;
+    ok = false;
+    need = held;
+  }
+  __syncthreads();  // the first sums have been read
+  scan_into(rt, rt.take, ok ? take : 0);
+  scan_into(rt, rt.slot, ok && p.start && start >= 0 ? max(len - start, 0) : 0);
+  rt.held[b] = held;
+  rt.need[b] = need;
+  rt.start[b] = start;
+  __syncthreads();
+  const int taken = rt.take[RKV_MAX_BATCH], slots = rt.slot[RKV_MAX_BATCH];
+  if (lead) {
+    if (slots > p.slots_size) bad |= RKV_DEVERR_CAPACITY;
+    if (bad) flag_error(p.err, bad);
+    if (p.start && b <= p.B) p.first[b] = rt.slot[b];
+    if (p.start && tid == 0 && p.B == kRsThreads) p.first[p.B] = slots;
+  }
+
+  // the page on place x of the stack, pages given back on top of the old ones
+  auto stack_page = [&](int x) -> int {
+    if (x < count) return p.free_pages[x];
+    const int g = holder(rt.give, p.B, x - count);
+    return p.page_table[(size_t)g * p.max_pages + rt.need[g] + (x - count - rt.give[g])];
+  };
+  const int stride = gridDim.x * kRsThreads;
+  for (int i = blockIdx.x * kRsThreads + tid; i < taken; i += stride) {
+    const int s = holder(rt.take, p.B, i);
+    p.page_table[(size_t)s * p.max_pages + rt.held[s] + (i - rt.take[s])] = stack_page(have - 1 - i);
+  }
+  const int top = have - taken;  // pages given back that stay: the places [count, top)
+  for (int x = count + blockIdx.x * kRsThreads + tid; stack_ok && x < min(top, p.num_phys); x += stride)
+    p.free_pages[x] = stack_page(x);
+  const int live = min(slots, p.slots_size);
+  for (int x = blockIdx.x * kRsThreads + tid; x < live; x += stride) {
+    const int s = holder(rt.slot, p.B, x);
+    const int pos = rt.start[s] + (x - rt.slot[s]), j = pos >> p.pshift;
+    const int phys = j < rt.held[s] ? p.page_table[(size_t)s * p.max_pages + j]
+                                    : stack_page(have - 1 - (rt.take[s] + j - rt.held[s]));
+    const bool in = phys >= 0 && phys < p.num_phys;
+    if (!in) flag_error(p.err, RKV_DEVERR_PAGE_ID);
+    p.slots[x] = in ? phys * p.P + (pos & (p.P - 1)) : -1;
+  }
+
+  __syncthreads();  // every thread of this CTA has read the old counts
+  if (tid == 0) {
+    __threadfence();
+    rt.last = atomicAdd(p.sync, 1) == (int)gridDim.x - 1;
+  }
+  __syncthreads();
+  if (rt.last) {
+    if (b < p.B) p.held_out[b] = need;
+    if (tid == 0) {
+      *p.count_out = stack_ok ? top : count;
+      *p.sync = 0;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_reserve_pages(const ReserveArgs& a, cudaStream_t s) {
+  ReserveParams p;
+  p.free_pages = a.pool.free_pages;
+  p.free_count = a.pool.free_count;
+  p.held = a.pool.held;
+  p.sync = a.pool.sync;
+  p.err = a.pool.error_word;
+  p.page_table = a.page_table;
+  p.len = a.len;
+  p.start = a.start;
+  p.slots = a.slots;
+  p.first = a.first;
+  p.held_out = a.held_out;
+  p.count_out = a.free_count_out;
+  p.B = a.B;
+  p.max_pages = a.max_pages;
+  p.P = a.page_size;
+  p.pshift = log2_int(a.page_size);
+  p.num_phys = a.pool.num_phys_pages;
+  p.slots_size = a.start ? a.slots_size : 0;
+  const long long pages = (long long)a.B * a.max_pages < p.num_phys ? (long long)a.B * a.max_pages : p.num_phys;
+  const long long items = p.slots_size > pages ? p.slots_size : pages;
+  long long grid = (items + 4 * kRsThreads - 1) / (4 * kRsThreads);
+  const long long most = 4LL * num_sms();
+  if (grid > most) grid = most;
+  launch_begin(K_RESERVE_PAGES, s);
+  reserve_pages_kernel<<<(unsigned)grid, kRsThreads, 0, s>>>(p);
+  launch_end(K_RESERVE_PAGES, s);
+  return cudaGetLastError();
+}
+
+}  // namespace rkv

@@ -1,0 +1,632 @@
+// Attention of the last rows over the 8-bit cache.
+//
+// For sequence b with n tokens and m query rows of G heads a KV head, row i at position n - m +
+// i and seeing t <= n - m + i:
+//   z_t = scale q . k_t,  out = sum_t exp(z_t) v_t / sum_t exp(z_t),  lse = log sum_t exp(z_t)
+// where k_t = code * ks, v_t = code * vs with one power of two ks, vs for each page and KV head.
+//
+// Codes go to the tensor cores as fp16, which holds them exactly.  What else is rounded:
+//   queries   each row times a power of two that brings its largest magnitude to [2^8, 2^9):
+//             a bf16 number fits fp16's 11 bits, and only what lies 2^-33 below the row's
+//             largest is cut off at fp16's smallest step;
+//   weights   p = 2^(z - m) <= 2^8 enters the product with V times 2^7 vs / vref (vref: the
+//             largest vs so far, the output's unit): 11 bits, off by at most 2^-11 of each,
+//             down to 2^-21 of the output's unit, then by 2^-32 of it; their sum is fp32 and
+//             unrounded.
+// ks joins the logits behind the product and vs the weights, so neither costs a pass over codes.
+//
+// q8_rows: 8 or 16 query rows against 32-key chunks, keys and channels on the MMA's M.  A
+// chunk's codes are 8 KB for 2 x 32 x 128 x 8 (or 16) multiply-adds, so the cache's bytes bound
+// it: all units' chunks form one line that is split evenly over one CTA per SM; a CTA's
+// eight warps take a run's chunks in turn, each with its own three-stage TMA ring (192 KB in
+// flight per SM), its own running maximum, sum and fp32 output, and meet once per run.  The
+// parts of a split unit go to the workspace and q8_join joins them.
+#include "rkv_attend.cuh"
+#include "rkv_causal.cuh"
+#include "rkv_internal.h"
+#include "rkv_q8.cuh"
+
+namespace rkv {
+namespace {
+
+struct Q8Params {
+  CUtensorMap tmk, tmv;  // the codes as [rows][128] bytes, a page's (or half a 64-token page's) rows to a box
+  const rkv_bf16* q;     // [B][Hq][T][128]
+  const float *k_scale, *v_scale;
+  const int32_t* page_table;
+  const int32_t* seq_len;
+  const int32_t* row_len;  // null: T rows everywhere
+  int32_t* err;
+  rkv_bf16* out;
+  float* lse;      // may be null
+  float* part_o;   // [2 N][tile rows][128]
+  float2* part_ml; // [2 N][tile rows]
+  int B, Hq, Hkv, G, gshift, T, P, pshift, max_pages, num_phys, N;
+  float scale_log2;
+};
+
+constexpr int kQrWarps = 8;
+constexpr int kQrThreads = kQrWarps * 32;
+constexpr int kQrKeysShift = 5, kQrKeys = 1 << kQrKeysShift;
+constexpr int kQrStages = 3;
+constexpr int kQrStageBytes = 2 * kQrKeys * 128;
+constexpr int kQrPad = 8;                         // what a run costs, in chunks
+constexpr int kQrMergeRows = 4;                   // rows of every warp that meet at a time
+constexpr int kQrMergeStride = 132;               // floats
+constexpr int kQrSmem = 1024 + kQrWarps * kQrStages * kQrStageBytes + kQrWarps * kQrMergeRows * kQrMergeStride * 4;
+constexpr float kSlack = 8.f;        // a weight's exponent may lie this far above the maximum it refers to
+constexpr float kUnit = 128.f;       // 2^7: a weight of 2^8 becomes 2^15 in fp16
+constexpr float kLowestUnit = 3.009265538105056e-36f;  // 2^-118: 2^7 / vref stays finite
+
+template <int kRowsShift>
+using RowsLine = CausalLine<kRowsShift, kQrKeysShift, kQrPad>;
+
+__device__ __forceinline__ int checked_len(const Q8Params& p, int b) {
+  const int n = p.seq_len[b];
+  if (n < 0 || n > p.max_pages * p.P) {
+    flag_error(p.err, RKV_DEVERR_CAPACITY);
+    return 0;
+  }
+  return n;
+}
+__device__ __forceinline__ int checked_rows(const Q8Params& p, int b) {
+  const int m = p.row_len ? p.row_len[b] : p.T;
+  if (m < 0 || m > p.T) {
+    flag_error(p.err, RKV_DEVERR_TREE);
+    return 0;
+  }
+  return m;
+}
+__device__ __forceinline__ size_t out_row(const Q8Params& p, int b, int g, int r) {
+  return ((size_t)b * p.Hq + g * p.G + (r & (p.G - 1))) * p.T + (r >> p.gshift);
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // an 8 x 8 matrix of 16-bit values over the warp
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 .. 127
+
+// What a stage holds besides codes: the scales of its (at most two) pages and which of its 32
+// keys can be read.
+struct StageInfo {
+  float k[2], v[2];
+  uint32_t live;
+};
+
+// A warp's share of kN tiles of eight query rows.  Fragment rows are keys (first product) and
+// channels (second); a lane's query rows are the columns 2 (lane % 4) and the next of every
+// tile.  qb: the queries, step s of 16 channels: lane quarter c of a key's bytes 32 c + 4 s ..
+// + 3.  o: channels 16 (lane / 4) + 2 i and + 1 of them for i < 8, times kUnit / vref.
+template <int kFormat, int kN>
+struct RowTile8 {
+  uint32_t qb[kN][8][2];
+  float o[kN][8][4];
+  float m[kN][2], l[kN][2], factor[kN][2];  // factor: from the product to base-2 logits, without the key's scale
+  int lim[kN][2];                           // keys that the row sees
+  float vref;
+  int least;  // the fewest keys that a row sees
+
+  __device__ __forceinline__ void start(const Q8Params& p, int b, int g, int rt, int n, int rows_m) {
+    const int lane = threadIdx.x & 31, rows = rows_m * p.G, r0 = rt * kN * 8;
+#pragma unroll
+    for (int t = 0; t < kN; ++t) {
+      const int r = r0 + t * 8 + (lane >> 2);
+      uint4 x[4];
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + out_row(p, b, g, r) * 128) + (lane & 3) * 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = r < rows ? src[i] : make_uint4(0, 0, 0, 0);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7fff7fffu);
+      }
+      top = max(top & 0xffffu, top >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = max((int)(top >> 7) - 127, -100);  // the largest magnitude's exponent
+      const float up = power_of_two(8 - min(e, 127));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          qb[t][i * 2 + (j >> 1)][j & 1] = pack_f16x2(bf16_lo(w[j]) * up, bf16_hi(w[j]) * up);
+      }
+      // a row with an infinity or a NaN is NaN
+      const float f = top >= 0x7f80u ? __uint_as_float(0x7fffffffu) : p.scale_log2 * power_of_two(e - 8);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        factor[t][c] = __shfl_sync(0xffffffffu, f, ((lane & 3) * 2 + c) * 4);
+        const int rc = r0 + t * 8 + (lane & 3) * 2 + c;
+        lim[t][c] = rc < rows ? n - rows_m + (rc >> p.gshift) + 1 : n;
+        m[t][c] = kNoMax;
+        l[t][c] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[t][i][c] = 0.f;
+    }
+    vref = kLowestUnit;
+    least = n - rows_m + (r0 >> p.gshift) + 1;
+  }
+
+  __device__ __forceinline__ void scale_o(int t, float f0, float f1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      o[t][i][0] *= f0;
+      o[t][i][1] *= f1;
+      o[t][i][2] *= f0;
+      o[t][i][3] *= f1;
+    }
+  }
+
+  // The chunk whose first key is key0, K and V in st (their copies have landed).
+  __device__ __forceinline__ void step(uint8_t* st, const StageInfo& info, int key0) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c4 = lane & 3;
+    const uint32_t live = info.live;
+    if (live != ~0u) {  // a key that cannot be read may hold anything, and 0 x NaN is not 0
+      for (int i = lane; i < kQrKeys * 8; i += 32)
+        if (!((live >> (i >> 3)) & 1u)) *reinterpret_cast<uint4*>(st + kQrKeys * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+    float z[kN][2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint4 ka[2][2];  // keys r, r + 8; 32 bytes each
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          ka[h][i] = *reinterpret_cast<const uint4*>(st + (u * 16 + h * 8 + r) * 128 + (((c4 * 2 + i) ^ r) << 4));
+#pragma unroll
+      for (int t = 0; t < kN; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[t][u][e] = 0.f;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const uint4 &x0 = ka[0][s >> 2], &x1 = ka[1][s >> 2];
+        const uint32_t w0 = (s & 3) == 0 ? x0.x : ((s & 3) == 1 ? x0.y : ((s & 3) == 2 ? x0.z : x0.w));
+        const uint32_t w1 = (s & 3) == 0 ? x1.x : ((s & 3) == 1 ? x1.y : ((s & 3) == 2 ? x1.z : x1.w));
+        uint32_t a0, a1, a2, a3;
+        decode4<kFormat>(w0, a0, a2);
+        decode4<kFormat>(w1, a1, a3);
+#pragma unroll
+        for (int t = 0; t < kN; ++t) mma_f16(z[t][u], a0, a1, a2, a3, qb[t][s][0], qb[t][s][1]);
+      }
+    }
+    // base-2 logits, hidden ones -inf; e = 0, 1: key r, columns 0, 1; e = 2, 3: key r + 8
+    const bool all = live == ~0u && key0 + kQrKeys <= least;
+    bool over = false;
+#pragma unroll
+    for (int t = 0; t < kN; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          z[t][u][e] *= factor[t][e & 1] * info.k[u];
+          if (!all) {
+            const int key = u * 16 + (e >> 1) * 8 + r;
+            if (!((live >> key) & 1u) || key0 + key >= lim[t][e & 1]) z[t][u][e] = -INFINITY;
+          }
+          over |= z[t][u][e] > m[t][e & 1] + kSlack;
+        }
+    if (__any_sync(0xffffffffu, over)) {  // the maximum that the weights refer to moves
+#pragma unroll
+      for (int t = 0; t < kN; ++t) {
+        float f[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float x = fmaxf(fmaxf(z[t][0][c], z[t][0][c + 2]), fmaxf(z[t][1][c], z[t][1][c + 2]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float to = fmaxf(m[t][c], x);
+          f[c] = ex2_approx(m[t][c] - to);
+          m[t][c] = to;
+          l[t][c] *= f[c];
+        }
+        scale_o(t, f[0], f[1]);
+      }
+    }
+    // a page of NaN has NaN logits for whoever sees it; for the others its values are not there
+    const float v0 = info.v[0] >= 0.f ? info.v[0] : 0.f, v1 = info.v[1] >= 0.f ? info.v[1] : 0.f;
+    if (fmaxf(v0, v1) > vref) {  // the same in every lane
+      const float f = vref * inverse_scale(fmaxf(v0, v1));
+      vref = fmaxf(v0, v1);
+#pragma unroll
+      for (int t = 0; t < kN; ++t) scale_o(t, f, f);
+    }
+    const float unit = kUnit * inverse_scale(vref), up[2] = {v0 * unit, v1 * unit};
+    uint32_t pb[kN][2][2];  // the weights, columns of keys
+#pragma unroll
+    for (int t = 0; t < kN; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[e] = ex2_approx(z[t][u][e] - m[t][e & 1]);
+          l[t][e & 1] += w[e];  // this lane's keys; the eight lanes of a column add up at the end
+          w[e] *= up[u];
+        }
+        pb[t][u][0] = transpose8(pack_f16x2(w[0], w[1]));
+        pb[t][u][1] = transpose8(pack_f16x2(w[2], w[3]));
+      }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint4 va[4];  // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9; channels 16 r ..
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = c4 * 2 + (i & 1) + (i >> 1) * 8;
+        va[i] = *reinterpret_cast<const uint4*>(st + kQrKeys * 128 + (u * 16 + key) * 128 + ((r ^ (key & 7)) << 4));
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = w == 0 ? va[i].x : (w == 1 ? va[i].y : (w == 2 ? va[i].z : va[i].w));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // channels 4 w + 2 h, + 1
+          const uint32_t sel = h ? 0x7362 : 0x5140;
+          uint32_t a0, a1, a2, a3;
+          decode4<kFormat>(__byte_perm(x[0], x[1], sel), a0, a1);
+          decode4<kFormat>(__byte_perm(x[2], x[3], sel), a2, a3);
+#pragma unroll
+          for (int t = 0; t < kN; ++t) mma_f16(o[t][2 * w + h], a0, a1, a2, a3, pb[t][u][0], pb[t][u][1]);
+        }
+      }
+    }
+  }
+
+  // The eight lanes of a column add their sums up.
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int t = 0; t < kN; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[t][c] += __shfl_xor_sync(0xffffffffu, l[t][c], x);
+  }
+};
+
+template <int kFormat, int kN>
+__global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_constant__ Q8Params p) {
+  constexpr int kRows = kN * 8;
+  using Line = RowsLine<kN == 1 ? 3 : 4>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Line line;
+  __shared__ uint64_t full_b[kQrWarps][kQrStages];
+  __shared__ StageInfo info[kQrWarps][kQrStages];
+  __shared__ float wm[kQrWarps][kRows], wl[kQrWarps][kRows], wv[kQrWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* base = align1024(smem);
+  uint8_t* ring = base + warp * kQrStages * kQrStageBytes;
+  float* merge = reinterpret_cast<float*>(base + kQrWarps * kQrStages * kQrStageBytes);
+  if (lane == 0) {
+    for (int s = 0; s < kQrStages; ++s) mbar_init(&full_b[warp][s], 1);
+    fence_mbar_init();
+  }
+  line.build(p.B, p.Hkv, p.gshift, [&](int b) { return checked_len(p, b); }, [&](int b) { return checked_rows(p, b); });
+  grid_launch_dependents();
+  const long long total = line.base[p.B];
+  const int N = flat_ctas(total, p.N);
+  if ((int)blockIdx.x >= N) return;
+  const long long x0 = flat_first(total, blockIdx.x, N), x1 = flat_first(total, blockIdx.x + 1, N);
+  auto next_run = [&](long long x, typename Line::Run& r) { return line.next(p.B, p.Hkv, p.gshift, x, x0, x1, r); };
+
+  // this warp's chunks of a run: lo + warp, lo + warp + 8, ...  The fetch side walks the
+  // runs ahead of the compute side.
+  typename Line::Run fr;
+  bool more = next_run(x0, fr);
+  int fc = fr.lo + warp;
+  auto settle = [&]() {
+    while (more && fc >= fr.hi) {
+      more = next_run(fr.next, fr);
+      if (more) fc = fr.lo + warp;
+    }
+  };
+  settle();
+  // page ids and scales of this warp's next 32 chunks of the run, one chunk a lane
+  const int boxes = p.P < kQrKeys ? 2 : 1, box = kQrKeys / boxes;
+  int ids[2] = {-1, -1}, ids_at = 0;
+  float sk[2] = {0.f, 0.f}, sv[2] = {0.f, 0.f};
+  long long ids_x = -1;
+  const uint64_t policy = l2_policy(p.T * p.G <= kRows);  // one row tile: nobody reads the cache again
+  int fetched = 0, used = 0;
+  bool dead = false;
+  auto fetch = [&]() {
+    if (!more) return;
+    const int s = fetched % kQrStages;
+    if (ids_x != fr.x || fc >= ids_at + 32 * kQrWarps) {
+      ids_x = fr.x;
+      ids_at = fc;
+      const int c = fc + lane * kQrWarps;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int key = c * kQrKeys + h * box;
+        ids[h] = -1;
+        sk[h] = sv[h] = 0.f;
+        if (h < boxes && c < fr.hi && key < fr.n) {
+          const int id = p.page_table[(size_t)fr.b * p.max_pages + (key >> p.pshift)];
+          if (id >= 0 && id < p.num_phys) {
+            ids[h] = id;
+            sk[h] = p.k_scale[(size_t)id * p.Hkv + fr.g];
+            sv[h] = p.v_scale[(size_t)id * p.Hkv + fr.g];
+          } else {
+            flag_error(p.err, RKV_DEVERR_PAGE_ID);
+          }
+        }
+      }
+    }
+    const int from = (fc - ids_at) / kQrWarps, key0 = fc * kQrKeys;
+    const int id0 = __shfl_sync(0xffffffffu, ids[0], from), id1 = __shfl_sync(0xffffffffu, ids[1], from);
+    if (lane == from) {
+      StageInfo& si = info[warp][s];
+      const int left = fr.n - key0;
+      uint32_t live = left >= kQrKeys ? ~0u : (1u << left) - 1u;
+      if (boxes == 1) {
+        if (id0 < 0) live = 0u;
+      } else {
+        if (id0 < 0) live &= 0xffff0000u;
+        if (id1 < 0) live &= 0x0000ffffu;
+      }
+      si.live = live;
+      si.k[0] = sk[0];
+      si.v[0] = sv[0];
+      si.k[1] = boxes == 1 ? sk[0] : sk[1];
+      si.v[1] = boxes == 1 ? sv[0] : sv[1];
+    }
+    if (lane == 0) {
+      uint64_t* bar = &full_b[warp][s];
+      uint8_t* st = ring + s * kQrStageBytes;
+      const int loads = (id0 >= 0) + (id1 >= 0);
+      if (loads > 0) mbar_arrive_expect_tx(bar, loads * 2 * box * 128);
+      else mbar_arrive(bar);
+      if (id0 >= 0) {
+        const int row = (id0 * p.Hkv + fr.g) * p.P + (key0 & (p.P - 1));
+        tma_load_2d_hint(st, &p.tmk, 0, row, bar, policy);
+        tma_load_2d_hint(st + kQrKeys * 128, &p.tmv, 0, row, bar, policy);
+      }
+      if (id1 >= 0) {
+        const int row = (id1 * p.Hkv + fr.g) * p.P;
+        tma_load_2d_hint(st + box * 128, &p.tmk, 0, row, bar, policy);
+        tma_load_2d_hint(st + kQrKeys * 128 + box * 128, &p.tmv, 0, row, bar, policy);
+      }
+    }
+    ++fetched;
+    fc += kQrWarps;
+    settle();
+  };
+  for (int s = 0; s < kQrStages; ++s) fetch();
+  __syncwarp();
+
+  typename Line::Run cr;
+  RowTile8<kFormat, kN> tile;
+  for (long long x = x0; next_run(x, cr); x = cr.next) {
+    const int b = cr.b, g = cr.g, rt = cr.rt, rows = cr.m * p.G;
+    tile.start(p, b, g, rt, cr.n, cr.m);
+    for (int c = cr.lo + warp; c < cr.hi; c += kQrWarps) {
+      const int s = used % kQrStages;
+      const bool late = !dead && !mbar_wait(&full_b[warp][s], (uint32_t)((used / kQrStages) & 1));
+      if (__any_sync(0xffffffffu, late)) {
+        if (lane == 0) flag_error(p.err, RKV_DEVERR_TIMEOUT);
+        dead = true;
+      }
+      if (!dead && info[warp][s].live != 0u) tile.step(ring + s * kQrStageBytes, info[warp][s], c * kQrKeys);
+      ++used;
+      __syncwarp();  // every lane has read the stage
+      if (!dead) fetch();
+      __syncwarp();  // what the fetch noted is there
+    }
+
+    tile.finish();
+    const int r = lane >> 2, c4 = lane & 3;
+    if (r == 0) {
+#pragma unroll
+      for (int t = 0; t < kN; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          wm[warp][t * 8 + c4 * 2 + c] = tile.m[t][c];
+          wl[warp][t * 8 + c4 * 2 + c] = tile.l[t][c];
+        }
+      if (lane == 0) wv[warp] = tile.vref * (1.f / kUnit);
+    }
+    // the warps meet, four rows at a time: thread = (row, two channels)
+    const int live = min(kRows, rows - rt * kRows);
+    const size_t slot = 2 * (size_t)blockIdx.x + (cr.first ? 0 : 1);
+#pragma unroll
+    for (int quarter = 0; quarter < kRows / kQrMergeRows; ++quarter) {
+      if (quarter * kQrMergeRows >= live) break;
+      if ((c4 >> 1) == (quarter & 1)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float* dst = merge + (warp * kQrMergeRows + (c4 & 1) * 2 + c) * kQrMergeStride + r * 16;
+#pragma unroll
+          for (int i = 0; i < 8; i += 2)
+            *reinterpret_cast<float4*>(dst + 2 * i) =
+                make_float4(tile.o[quarter >> 1][i][c], tile.o[quarter >> 1][i][2 + c], tile.o[quarter >> 1][i + 1][c],
+                            tile.o[quarter >> 1][i + 1][2 + c]);
+        }
+      }
+      __syncthreads();
+      const int sub = tid >> 6, d = (tid & 63) * 2, row = quarter * kQrMergeRows + sub, rr = rt * kRows + row;
+      if (row < live) {
+        float M = kNoMax, L = 0.f, ax = 0.f, ay = 0.f;
+#pragma unroll
+        for (int w = 0; w < kQrWarps; ++w) M = fmaxf(M, wm[w][row]);
+#pragma unroll
+        for (int w = 0; w < kQrWarps; ++w) {
+          const float f = ex2_approx(wm[w][row] - M), fv = f * wv[w];
+          const float2 v = *reinterpret_cast<const float2*>(merge + (w * kQrMergeRows + sub) * kQrMergeStride + d);
+          L += wl[w][row] * f;
+          ax += v.x * fv;
+          ay += v.y * fv;
+        }
+        if (cr.whole) {
+          const float inv = inverse_of(L);
+          const size_t orow = out_row(p, b, g, rr);
+          *reinterpret_cast<uint32_t*>(p.out + orow * 128 + d) = pack_bf16x2(ax * inv, ay * inv);
+          if (d == 0 && p.lse) p.lse[orow] = lse_of(M, L);
+        } else {
+          *reinterpret_cast<float2*>(p.part_o + (slot * kRows + row) * 128 + d) = make_float2(ax, ay);
+          if (d == 0) p.part_ml[slot * kRows + row] = make_float2(M, L);
+        }
+      }
+      __syncthreads();  // the merge buffer (and, after the last rows, wm, wl and wv) are free
+    }
+  }
+  // after a timeout: wait (bounded) for what this warp still has in flight
+  if (dead)
+    for (int i = used; i < fetched; ++i) mbar_wait(&full_b[warp][i % kQrStages], (uint32_t)((i / kQrStages) & 1));
+}
+
+// Joins the parts of the split units, and gives the rows that see nothing their results: one
+// warp a row, four channels a lane, four parts' loads in flight.
+template <class Line>
+__global__ void __launch_bounds__(256, 4) q8_join_kernel(const __grid_constant__ Q8Params p) {
+  __shared__ Line line;
+  line.build(p.B, p.Hkv, p.gshift, [&](int b) { return checked_len(p, b); }, [&](int b) { return checked_rows(p, b); });
+  grid_dependency_wait();
+  constexpr int kRows = Line::kRows;
+  const int lane = threadIdx.x & 31;
+  const long long each = (long long)p.Hq * p.T, rows = each * p.B, total = line.base[p.B];
+  const int N = flat_ctas(total, p.N);
+  for (long long x = blockIdx.x * 8 + (threadIdx.x >> 5); x < rows; x += gridDim.x * 8) {
+    const int b = (int)(x / each), i = (int)(x - b * each), hq = i / p.T, t = i - hq * p.T;
+    if (t >= line.m[b]) continue;
+    const int g = hq / p.G, r = t * p.G + (hq & (p.G - 1)), rt = r / kRows, row = r % kRows;
+    const int per = Line::per(line.n[b], line.m[b], p.gshift, rt);
+    uint2* out = reinterpret_cast<uint2*>(p.out + (size_t)x * 128) + lane;
+    if (per == 0) {  // the whole tile sees nothing
+      *out = make_uint2(0u, 0u);
+      if (lane == 0 && p.lse) p.lse[x] = -INFINITY;
+      continue;
+    }
+    const PartSlots ps(line.at(b, p.Hkv, p.gshift, rt, g), per, Line::kPad, total, N);
+    if (ps.c0 == ps.c1) continue;  // final already
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = kNoMax, L = 0.f;
+    for (int c = ps.c0; c <= ps.c1; c += 4) {
+      float4 v[4];
+      float2 ml[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = c + j <= ps.c1;
+        const size_t at = ps[in ? c + j : c] * kRows + row;  // behind the last part: the first again, unweighted
+        ml[j] = p.part_ml[at];
+        v[j] = reinterpret_cast<const float4*>(p.part_o + at * 128)[lane];
+        if (!in) ml[j] = make_float2(kNoMax, 0.f);
+      }
+      const float to = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+      const float f = ex2_approx(M - to);
+      M = to;
+      L *= f;
+      o.x *= f;
+      o.y *= f;
+      o.z *= f;
+      o.w *= f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float w = c + j <= ps.c1 ? ex2_approx(ml[j].x - M) : 0.f;
+        L += ml[j].y * w;
+        o.x += v[j].x * w;
+        o.y += v[j].y * w;
+        o.z += v[j].z * w;
+        o.w += v[j].w * w;
+      }
+    }
+    const float inv = inverse_of(L);
+    *out = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (lane == 0 && p.lse) p.lse[x] = lse_of(M, L);
+  }
+}
+
+int tile_rows(int T, int G) { return (long long)T * G <= 8 ? 8 : 16; }
+
+cudaError_t fill_params(const Q8AttendArgs& a, Q8Params& p) {
+  const rkv_cache8& c = a.cache;
+  const uint64_t rows = (uint64_t)c.num_phys_pages * c.Hkv * c.page_size;
+  const uint32_t box = c.page_size < kQrKeys ? c.page_size : kQrKeys;
+  if (!encode_codes_map(&p.tmk, c.k_codes, rows, box) || !encode_codes_map(&p.tmv, c.v_codes, rows, box)) {
+    set_last_error("cuTensorMapEncodeTiled failed for the cache's codes");
+    return cudaErrorInvalidValue;
+  }
+  p.q = a.q;
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.page_table = c.page_table;
+  p.seq_len = c.seq_len;
+  p.row_len = a.row_len;
+  p.err = c.error_word;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.B = c.B;
+  p.Hq = a.Hq;
+  p.Hkv = c.Hkv;
+  p.G = a.Hq / c.Hkv;
+  p.gshift = log2_int(p.G);
+  p.T = a.T;
+  p.P = c.page_size;
+  p.pshift = log2_int(c.page_size);
+  p.max_pages = c.max_pages;
+  p.num_phys = c.num_phys_pages;
+  p.N = num_sms() < kMaxSms ? num_sms() : kMaxSms;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  return cudaSuccess;
+}
+
+template <int kFormat, int kN>
+cudaError_t launch_rows(const Q8Params& p, cudaStream_t s) {
+  static SmemOptIn opt;
+  cudaError_t e = opt.raise(reinterpret_cast<const void*>(q8_rows_kernel<kFormat, kN>), kQrSmem);
+  if (e != cudaSuccess) return e;
+  launch_begin(K_Q8_ROWS, s);
+  q8_rows_kernel<kFormat, kN><<<p.N, kQrThreads, kQrSmem, s>>>(p);
+  launch_end(K_Q8_ROWS, s);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t q8_attend_ws_bytes(int B, int Hq, int Hkv, int T, int max_pages, int page_size) {
+  const size_t rows = (size_t)2 * kMaxSms * tile_rows(T, Hq / Hkv > 0 ? Hq / Hkv : 1);
+  return align256(rows * 128 * 4) + align256(rows * 8);
+}
+
+cudaError_t launch_q8_attend(const Q8AttendArgs& a, cudaStream_t s) {
+  Q8Params p;
+  cudaError_t e = fill_params(a, p);
+  if (e != cudaSuccess) return e;
+  const int tile = tile_rows(a.T, p.G);
+  const size_t rows = (size_t)2 * kMaxSms * tile;
+  p.part_o = static_cast<float*>(a.ws);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(a.ws) + align256(rows * 128 * 4));
+  const bool int8 = a.cache.format == RKV_Q8_INT8;
+  if (tile == 8) e = int8 ? launch_rows<RKV_Q8_INT8, 1>(p, s) : launch_rows<RKV_Q8_E4M3, 1>(p, s);
+  else e = int8 ? launch_rows<RKV_Q8_INT8, 2>(p, s) : launch_rows<RKV_Q8_E4M3, 2>(p, s);
+  if (e != cudaSuccess) return e;
+  const long long jrows = ((long long)p.B * a.Hq * a.T + 7) / 8, jmost = 8LL * p.N;
+  const dim3 jgrid((unsigned)(jrows < jmost ? jrows : jmost));
+  return tile == 8 ? launch_dependent(q8_join_kernel<RowsLine<3>>, jgrid, 256, K_Q8_JOIN, s, p)
+                   : launch_dependent(q8_join_kernel<RowsLine<4>>, jgrid, 256, K_Q8_JOIN, s, p);
+}
+
+}  // namespace rkv

@@ -28,6 +28,7 @@ DEVERR_CAPACITY = 0x2
 DEVERR_TIMEOUT = 0x4
 DEVERR_SEQ_LEN = 0x8
 DEVERR_TREE = 0x10
+DEVERR_POOL = 0x20
 HEAD_DIM = 128
 MAX_BATCH = 256
 MAX_TREE = 256
@@ -61,6 +62,24 @@ class RkvCacheStruct(ctypes.Structure):
                 ("error_word", ctypes.c_void_p), ("step_sync", ctypes.c_void_p), ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("num_phys_pages", ctypes.c_int32)]
+
+
+class RkvPagePoolStruct(ctypes.Structure):
+    _fields_ = [("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("sync", ctypes.c_void_p), ("error_word", ctypes.c_void_p), ("num_phys_pages", ctypes.c_int32)]
+
+
+class RkvRotaryPlan(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_uint64 * (HEAD_DIM // 2)), ("amplitude", ctypes.c_float),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class RkvCache8Struct(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+                ("error_word", ctypes.c_void_p), ("sync", ctypes.c_void_p), ("B", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("num_phys_pages", ctypes.c_int32), ("format", ctypes.c_int32)]
 
 
 _vp, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
@@ -125,6 +144,27 @@ _lib.rkv_evict_workspace_size.argtypes = [_i32] * 4
 _lib.rkv_evict_workspace_size.restype = _sz
 _lib.rkv_evict_accum.argtypes = [_cachep, _vp, _i32, _i32p, _i32, _vp, _i32, _cachep, _vp, _i32, _vp, _sz, _vp]
 _lib.rkv_evict_accum.restype = _i32
+_i64p = ctypes.POINTER(ctypes.c_int64)
+_cache8p = ctypes.POINTER(RkvCache8Struct)
+_lib.rkv_reserve_pages.argtypes = [ctypes.POINTER(RkvPagePoolStruct), _vp, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp,
+                                   _vp, _vp, _vp]
+_lib.rkv_reserve_pages.restype = _i32
+_lib.rkv_rotary_init.argtypes = [ctypes.POINTER(RkvRotaryPlan), _i32, ctypes.c_double, _i32, _i32, ctypes.c_double, _i32,
+                                 ctypes.c_double, ctypes.c_double, _f32]
+_lib.rkv_rotary_init.restype = _i32
+_lib.rkv_rotary.argtypes = [ctypes.POINTER(RkvRotaryPlan), _vp, _i64p, _vp, _i64p, _i32, _i32, _i32, _i32, _vp, _i32,
+                            _i32, _vp, _i64p, _vp, _i64p, _vp]
+_lib.rkv_rotary.restype = _i32
+_lib.rkv_q8_append.argtypes = [_cache8p, _vp, _i64p, _vp, _i64p, _i32, _vp, _vp]
+_lib.rkv_q8_append.restype = _i32
+_lib.rkv_q8_load.argtypes = [_cache8p, _cachep, _vp]
+_lib.rkv_q8_load.restype = _i32
+_lib.rkv_q8_workspace_size.argtypes = [_i32] * 6
+_lib.rkv_q8_workspace_size.restype = _sz
+_lib.rkv_q8_attention.argtypes = [_cache8p, _vp, _i32, _i32, _vp, _f32, _vp, _vp, _vp, _sz, _vp]
+_lib.rkv_q8_attention.restype = _i32
+_lib.rkv_read_device_error.argtypes = [_vp, _vp, _i32p]
+_lib.rkv_read_device_error.restype = _i32
 _lib.rkv_exact_topk_recall.argtypes = [ctypes.POINTER(RkvCacheStruct), _vp, _i32, _vp, _i32, _i32p, _f32, _vp, _vp,
                                        _vp]
 _lib.rkv_exact_topk_recall.restype = _i32
@@ -153,7 +193,8 @@ EXPORTED = ["rkv_split_ratio", "rkv_split_ratio_mt", "rkv_prefill_workspace_size
             "rkv_decode_path", "rkv_step_host_staging_size", "rkv_decode_step_host", "rkv_sparq_workspace_size", "rkv_decode_sparq", "rkv_sparq_keys_size",
             "rkv_tree_workspace_size", "rkv_tree_attention", "rkv_tree_commit", "rkv_accum_workspace_size",
             "rkv_decode_accum", "rkv_accum_rows_workspace_size", "rkv_accum_rows", "rkv_evict_workspace_size",
-            "rkv_evict_accum", "rkv_exact_topk_recall", "rkv_selftest_bounded_wait", "rkv_get_device_status", "rkv_last_error",
+            "rkv_evict_accum", "rkv_reserve_pages", "rkv_rotary_init", "rkv_rotary", "rkv_q8_append", "rkv_q8_load",
+            "rkv_q8_workspace_size", "rkv_q8_attention", "rkv_read_device_error", "rkv_exact_topk_recall", "rkv_selftest_bounded_wait", "rkv_get_device_status", "rkv_last_error",
             "rkv_launch_count", "rkv_profile_enable", "rkv_profile_accumulate", "rkv_profile_release",
             "rkv_profile_reset", "rkv_profile_read"]
 
@@ -575,6 +616,219 @@ def rkv_evict_accum(cache: PagedCache, acc: torch.Tensor, keep: Sequence[int], r
     _call_on(dev, stream, _lib.rkv_evict_accum, ctypes.byref(cache.struct), sums, acc.shape[2], _host_i32(keep),
              int(recent), kept, kept_idx.shape[2], ctypes.byref(dst.struct) if dst is not None else None, to,
              dst_acc.shape[2] if dst_acc is not None else 0, _ws_arg(workspace, dev), workspace.numel())
+
+
+# ------------------------------------------------------------------ pages, positions
+def _count_arg(t: torch.Tensor, name: str, n: int, device) -> int:
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    return _arg(t, name, (n,), torch.int32, device)
+
+
+class PagePool:
+    """The pages that no sequence holds and how many each holds (see rkv_page_pool in rkv.h):
+    all pages free, or the stack, its count and the counts that are given."""
+
+    def __init__(self, num_phys_pages: int, B: int, device="cuda", free_pages: Optional[torch.Tensor] = None,
+                 free_count: Optional[torch.Tensor] = None, held: Optional[torch.Tensor] = None):
+        if free_pages is None:  # page 0 on top
+            free_pages = torch.arange(num_phys_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.free_pages = free_pages
+        dev = free_pages.device
+        if free_count is None:
+            free_count = torch.full((1,), num_phys_pages, dtype=torch.int32, device=dev)
+        self.free_count = free_count
+        self.held = torch.zeros(B, dtype=torch.int32, device=dev) if held is None else held
+        self.B, self.num_phys_pages = B, num_phys_pages
+        self.sync = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.error_word = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._struct = RkvPagePoolStruct(
+            _count_arg(self.free_pages, "free_pages", num_phys_pages, dev), _count_arg(self.free_count, "free_count", 1, dev),
+            _count_arg(self.held, "held", B, dev), self.sync.data_ptr(), self.error_word.data_ptr(), num_phys_pages)
+
+
+def rkv_reserve_pages(pool: PagePool, page_table: torch.Tensor, page_size: int, lens: torch.Tensor,
+                      start: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                      first: Optional[torch.Tensor] = None, held_out: Optional[torch.Tensor] = None,
+                      free_count_out: Optional[torch.Tensor] = None, stream=None):
+    """Bring every sequence of page_table (int32 [B, max_pages]) to the pages that lens (int32
+    [B]) needs, from and to the pool's stack.  With start (int32 [B]), slots (int32 [any
+    size]) and first (int32 [B + 1]): sequence b's positions start[b] .. lens[b] - 1 get
+    slots[first[b] : first[b + 1]], page id * page_size + place."""
+    dev = pool.free_pages.device
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: expected [B, max_pages], got {list(page_table.shape)}")
+    if start is not None and (slots is None or slots.dim() != 1):
+        raise ValueError("slots: expected one dimension")
+    B, pages = pool.B, page_table.shape[1]
+    held_out = pool.held if held_out is None else held_out
+    free_count_out = pool.free_count if free_count_out is None else free_count_out
+    size = slots.shape[0] if slots is not None else 0
+    args = (_arg(page_table, "page_table", (B, pages), torch.int32, dev), B, pages, page_size,
+            _count_arg(lens, "lens", B, dev), _arg(start, "start", (B,), torch.int32, dev),
+            _arg(slots, "slots", (size,), torch.int32, dev), size, _arg(first, "first", (B + 1,), torch.int32, dev),
+            _count_arg(held_out, "held_out", B, dev), _count_arg(free_count_out, "free_count_out", 1, dev))
+    _call_on(dev, stream, _lib.rkv_reserve_pages, ctypes.byref(pool._struct), *args)
+
+
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "turns": 2, "logs": 3}
+
+
+def rotary_plan(rot_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                factor: float = 1.0, original_len: int = 0, low: float = 1.0, high: float = 4.0,
+                amplitude: float = 1.0) -> RkvRotaryPlan:
+    """A model's rotary positions for rkv_rotary: frequencies base^(-2 i / rot_dim), scaled as
+    RKV_ROTARY_* in rkv.h say ("none", "linear", "turns", "logs")."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling: one of {sorted(ROTARY_SCALINGS)}, got {scaling!r}")
+    plan = RkvRotaryPlan()
+    _check(_lib.rkv_rotary_init(ctypes.byref(plan), rot_dim, base, int(interleaved), ROTARY_SCALINGS[scaling], factor,
+                                original_len, low, high, amplitude))
+    return plan
+
+
+def _rows_arg(t: Optional[torch.Tensor], name: str, shape: tuple, device) -> tuple:
+    """Address and strides of bf16 rows [sequence][head][token][128], whose channels are
+    contiguous and whose other strides are free (None: no rows)."""
+    if t is None:
+        return None, None
+    if t.shape != shape or t.dtype != torch.bfloat16 or t.device != device:
+        raise ValueError(f"{name}: expected torch.bfloat16 {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}: a row's {HEAD_DIM} channels must be contiguous")
+    return t.data_ptr(), (ctypes.c_int64 * 3)(*[t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)])
+
+
+def rkv_rotary(plan: RkvRotaryPlan, q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
+               q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, inverse: bool = False,
+               stream=None):
+    """Rotate queries (bf16 [B, Hq, T, 128]) and keys ([B, Hkv, T, 128] or None) to their
+    positions (int32 [B, T], or [B]: token t at positions[b] + t).  Rows may have any
+    strides that are multiples of 8 elements, so a slice of a fused projection's output is
+    read where it lies.  Without q_out and k_out in place.  inverse rotates back."""
+    if q.dim() != 4:
+        raise ValueError(f"q: expected [B, Hq, T, {HEAD_DIM}], got {list(q.shape)}")
+    if (k is None) != (k_out is None) and q_out is not None:
+        raise ValueError("k and k_out: both or neither")
+    B, Hq, T, _ = q.shape
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError(f"q: expected a CUDA tensor, got {dev}")
+    Hkv = k.shape[1] if k is not None and k.dim() == 4 else 0
+    q_out = q if q_out is None else q_out
+    k_out = k if k_out is None else k_out
+    per_token = positions.dim() == 2
+    qa, qs = _rows_arg(q, "q", (B, Hq, T, HEAD_DIM), dev)
+    ka, ks = _rows_arg(k, "k", (B, Hkv, T, HEAD_DIM), dev)
+    qo, qos = _rows_arg(q_out, "q_out", (B, Hq, T, HEAD_DIM), dev)
+    ko, kos = _rows_arg(k_out, "k_out", (B, Hkv, T, HEAD_DIM), dev)
+    at = _arg(positions, "positions", (B, T) if per_token else (B,), torch.int32, dev)
+    _call_on(dev, stream, _lib.rkv_rotary, ctypes.byref(plan), qa, qs, ka, ks, B, Hq, Hkv, T, at, int(per_token),
+             int(inverse), qo, qos, ko, kos)
+
+
+# ------------------------------------------------------------------ the 8-bit cache
+Q8_FORMATS = {"e4m3": (0, torch.float8_e4m3fn), "int8": (1, torch.int8)}
+
+
+class PagedCache8:
+    """Device memory of one layer's paged cache in 8 bits (see rkv_cache8 in rkv.h)."""
+
+    def __init__(self, B: int, Hkv: int, page_size: int, max_pages: int, device="cuda",
+                 page_table: Optional[torch.Tensor] = None, num_phys_pages: Optional[int] = None, fmt: str = "e4m3"):
+        if fmt not in Q8_FORMATS:
+            raise ValueError(f"fmt: one of {sorted(Q8_FORMATS)}, got {fmt!r}")
+        max_pages = (max_pages + 7) // 8 * 8
+        if page_table is None:
+            page_table = torch.arange(B * max_pages, dtype=torch.int32, device=device).view(B, max_pages)
+        if page_table.shape != (B, max_pages) or page_table.dtype != torch.int32:
+            raise ValueError(f"page_table: expected torch.int32 {[B, max_pages]}, got {page_table.dtype} {list(page_table.shape)}")
+        if num_phys_pages is None:
+            num_phys_pages = int(page_table.max().item()) + 1
+        self.B, self.Hkv, self.page_size, self.max_pages = B, Hkv, page_size, max_pages
+        self.num_phys_pages, self.fmt = num_phys_pages, fmt
+        self.page_table = page_table.to(device).contiguous()
+        code, dtype = Q8_FORMATS[fmt]
+        shape = (num_phys_pages, Hkv, page_size, HEAD_DIM)
+        self.k_codes = torch.empty(shape, dtype=dtype, device=device)
+        self.v_codes = torch.empty(shape, dtype=dtype, device=device)
+        self.k_scale = torch.empty((num_phys_pages, Hkv), dtype=torch.float32, device=device)
+        self.v_scale = torch.empty((num_phys_pages, Hkv), dtype=torch.float32, device=device)
+        self.seq_len = torch.zeros(B, dtype=torch.int32, device=device)
+        self.error_word = torch.zeros(1, dtype=torch.int32, device=device)
+        self.sync = torch.zeros(B, dtype=torch.int32, device=device)
+        self._struct = RkvCache8Struct(
+            self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+            self.page_table.data_ptr(), self.seq_len.data_ptr(), self.error_word.data_ptr(), self.sync.data_ptr(), B, Hkv,
+            HEAD_DIM, page_size, max_pages, num_phys_pages, code)
+
+    @property
+    def struct(self) -> RkvCache8Struct:
+        return self._struct
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in
+                   (self.k_codes, self.v_codes, self.k_scale, self.v_scale, self.page_table, self.seq_len))
+
+    def token_kv(self, b: int, n: Optional[int] = None):
+        """(K, V) of sequence b's first n tokens as fp32 values, [Hkv, n, 128] (gathered by torch; for checks)."""
+        if n is None:
+            n = int(self.seq_len[b].item())
+        npg = -(-n // self.page_size)
+        phys = self.page_table[b, :npg].long()
+        return tuple((c[phys].float() * s[phys][:, :, None, None]).permute(1, 0, 2, 3).reshape(self.Hkv, -1, HEAD_DIM)[:, :n]
+                     for c, s in ((self.k_codes, self.k_scale), (self.v_codes, self.v_scale)))
+
+
+def rkv_q8_append(cache: PagedCache8, k_new: torch.Tensor, v_new: torch.Tensor, new_len: Optional[torch.Tensor] = None,
+                  stream=None):
+    """The first new_len[b] (int32 [B] on the device; None: all T) rows of k_new and v_new
+    (bf16 [B, Hkv, T, 128], strides as for rkv_rotary) enter the cache, rounded to codes."""
+    if k_new.dim() != 4:
+        raise ValueError(f"k_new: expected [B, Hkv, T, {HEAD_DIM}], got {list(k_new.shape)}")
+    T, dev = k_new.shape[2], cache.k_codes.device
+    ka, ks = _rows_arg(k_new, "k_new", (cache.B, cache.Hkv, T, HEAD_DIM), dev)
+    va, vs = _rows_arg(v_new, "v_new", (cache.B, cache.Hkv, T, HEAD_DIM), dev)
+    _call_on(dev, stream, _lib.rkv_q8_append, ctypes.byref(cache.struct), ka, ks, va, vs, T,
+             _arg(new_len, "new_len", (cache.B,), torch.int32, dev))
+
+
+def rkv_q8_load(cache: PagedCache8, src: PagedCache, stream=None):
+    """cache becomes the bf16 cache src, every token rounded to codes."""
+    dev = cache.k_codes.device
+    if src.k_pages.device != dev:
+        raise ValueError("src lies on another device")
+    _call_on(dev, stream, _lib.rkv_q8_load, ctypes.byref(cache.struct), ctypes.byref(src.struct))
+
+
+def q8_workspace(B: int, Hq: int, Hkv: int, T: int, max_pages: int, page_size: int, device="cuda") -> torch.Tensor:
+    n = _lib.rkv_q8_workspace_size(B, Hq, Hkv, T, max_pages, page_size)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def rkv_q8_attention(cache: PagedCache8, q: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                     row_len: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of the cache's last row_len[b] (None: T) positions, whose queries are q (bf16
+    [B, Hq, T, 128]), over everything up to each: out bf16 [B, Hq, T, 128], lse fp32 [B, Hq, T]."""
+    if q.dim() != 4:
+        raise ValueError(f"q: expected [B, Hq, T, {HEAD_DIM}], got {list(q.shape)}")
+    B, Hq, T, d = q.shape
+    dev = cache.k_codes.device
+    args = (_arg(q, "q", (cache.B, Hq, T, HEAD_DIM), torch.bfloat16, dev), Hq, T,
+            _arg(row_len, "row_len", (B,), torch.int32, dev), 1.0 / math.sqrt(d) if scale is None else scale,
+            _arg(out, "out", (B, Hq, T, HEAD_DIM), torch.bfloat16, dev), _arg(lse, "lse", (B, Hq, T), torch.float32, dev))
+    if workspace is None:
+        workspace = _made_for(stream, q8_workspace, B, Hq, cache.Hkv, T, cache.max_pages, cache.page_size, dev)
+    _call_on(dev, stream, _lib.rkv_q8_attention, ctypes.byref(cache.struct), *args, _ws_arg(workspace, dev),
+             workspace.numel())
+
+
+def rkv_read_device_error(error_word: torch.Tensor, stream=None) -> tuple:
+    """(status, bits) of a PagePool's or PagedCache8's error word, which is cleared."""
+    bits = ctypes.c_int32(0)
+    st = _lib.rkv_read_device_error(ctypes.c_void_p(error_word.data_ptr()), _stream(stream), ctypes.byref(bits))
+    return st, bits.value
 
 
 def rkv_exact_topk_recall(cache: PagedCache, q: torch.Tensor, sel_pages: torch.Tensor, k_tokens: Sequence[int],
