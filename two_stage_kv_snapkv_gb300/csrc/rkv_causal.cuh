@@ -25,15 +25,16 @@ __device__ __forceinline__ long long floors_before(long long a, int sshift, int 
   return upto(x1) - upto(x0);
 }
 
+// A run and the rows that it belongs to: KV head, row tile, tokens and rows of its sequence.
+struct CausalRun : FlatRun {
+  int g, rt, n, m;
+};
+
 template <int kRowsShift, int kKeysShift, int kPadPieces>
 struct CausalLine {
   static constexpr int kKeys = 1 << kKeysShift, kPad = kPadPieces, kRows = 1 << kRowsShift;
   long long base[RKV_MAX_BATCH + 1];
-  int n[RKV_MAX_BATCH], m[RKV_MAX_BATCH];
 
-  struct Run : FlatRun {
-    int g, rt, n, m;
-  };
   static __device__ __forceinline__ int tiles(int m, int gshift) {
     const int sshift = kRowsShift - gshift;
     return (m + (1 << sshift) - 1) >> sshift;
@@ -58,18 +59,19 @@ struct CausalLine {
     if (k > last) sum += ((n + kKeys - 1) >> kKeysShift) + kPad;
     return sum;
   }
-  // len(b), rows(b); called by every thread, ends with a block barrier
+  // len(b), rows(b): tokens and rows of a sequence, asked for by the first warp; ends with a
+  // block barrier
   template <class Len, class Rows>
   __device__ __forceinline__ void build(int B, int Hkv, int gshift, Len len, Rows rows) {
-    for (int b = threadIdx.x; b < B; b += blockDim.x) {
-      n[b] = len(b);
-      m[b] = rows(b);
-    }
-    __syncthreads();
-    flat_scan(base, B, [&](int b) { return m[b] > 0 ? before(n[b], m[b], gshift, tiles(m[b], gshift)) * Hkv : 0LL; });
+    flat_scan(base, B, [&](int b) {
+      const int m = rows(b);
+      return m > 0 ? before(len(b), m, gshift, tiles(m, gshift)) * Hkv : 0LL;
+    });
   }
   // the next run of a share at or behind x
-  __device__ __forceinline__ bool next(int B, int Hkv, int gshift, long long x, long long x0, long long x1, Run& r) const {
+  template <class Len, class Rows>
+  __device__ __forceinline__ bool next(int B, int Hkv, int gshift, Len len, Rows rows, long long x, long long x0,
+                                       long long x1, CausalRun& r) const {
     for (; x < x1; x = r.next) {
       int lo = 0, hi = B - 1;
       while (lo < hi) {
@@ -77,8 +79,8 @@ struct CausalLine {
         if (base[mid] <= x) lo = mid; else hi = mid - 1;
       }
       r.b = lo;
-      r.n = n[lo];
-      r.m = m[lo];
+      r.n = len(lo);
+      r.m = rows(lo);
       const long long off = x - base[lo];
       int a = 0, z = tiles(r.m, gshift) - 1;
       while (a < z) {  // the last tile whose pieces begin at or before off
@@ -96,9 +98,30 @@ struct CausalLine {
     }
     return false;
   }
-  // where unit (b, tile i, KV head g) begins on the line
+  // where unit (b, tile i, KV head g) of a sequence of n tokens and m rows begins on the line
+  __device__ __forceinline__ long long at(int b, int n, int m, int Hkv, int gshift, int i, int g) const {
+    return base[b] + before(n, m, gshift, i) * Hkv + (long long)g * per(n, m, gshift, i);
+  }
+};
+
+// The same with the sequences' lengths beside it, read once.
+template <class Line>
+struct LineLengths : Line {
+  int n[RKV_MAX_BATCH], m[RKV_MAX_BATCH];
+  template <class Len, class Rows>
+  __device__ __forceinline__ void build(int B, int Hkv, int gshift, Len len, Rows rows) {
+    for (int b = threadIdx.x; b < B; b += blockDim.x) {
+      n[b] = len(b);
+      m[b] = rows(b);
+    }
+    __syncthreads();
+    Line::build(B, Hkv, gshift, [&](int b) { return n[b]; }, [&](int b) { return m[b]; });
+  }
+  __device__ __forceinline__ bool next(int B, int Hkv, int gshift, long long x, long long x0, long long x1, CausalRun& r) const {
+    return Line::next(B, Hkv, gshift, [&](int b) { return n[b]; }, [&](int b) { return m[b]; }, x, x0, x1, r);
+  }
   __device__ __forceinline__ long long at(int b, int Hkv, int gshift, int i, int g) const {
-    return base[b] + before(n[b], m[b], gshift, i) * Hkv + (long long)g * per(n[b], m[b], gshift, i);
+    return Line::at(b, n[b], m[b], Hkv, gshift, i, g);
   }
 };
 

@@ -52,6 +52,7 @@ enum KernelKind {
   K_Q8_APPEND,
   K_Q8_LOAD,
   K_Q8_ROWS,
+  K_Q8_TILES,
   K_Q8_JOIN,
   K_NUM_KINDS
 };

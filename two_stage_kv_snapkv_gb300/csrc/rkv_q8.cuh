@@ -30,6 +30,25 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) 
   }
 }
 
+// The same times a power of two f (which an INT8 code costs nothing for).
+template <int kFormat>
+__device__ __forceinline__ void decode4_times(uint32_t w, __half2 f, __half2 bias_f, uint32_t& lo, uint32_t& hi) {
+  __half2 x, y;
+  if (kFormat == RKV_Q8_E4M3) {
+    uint32_t a, b;
+    decode4<kFormat>(w, a, b);
+    x = __hmul2(*reinterpret_cast<__half2*>(&a), f);
+    y = __hmul2(*reinterpret_cast<__half2*>(&b), f);
+  } else {
+    const uint32_t u = w ^ 0x80808080u;
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    x = __hfma2(*reinterpret_cast<__half2*>(&a), f, bias_f);  // bias_f = -1152 f
+    y = __hfma2(*reinterpret_cast<__half2*>(&b), f, bias_f);
+  }
+  lo = *reinterpret_cast<uint32_t*>(&x);
+  hi = *reinterpret_cast<uint32_t*>(&y);
+}
+
 // Four values, divided by the scale already and in the codes' range, as codes: nearest, ties
 // to even.
 template <int kFormat>

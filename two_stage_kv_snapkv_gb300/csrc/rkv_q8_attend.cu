@@ -21,29 +21,10 @@
 // eight warps take a run's chunks in turn, each with its own three-stage TMA ring (192 KB in
 // flight per SM), its own running maximum, sum and fp32 output, and meet once per run.  The
 // parts of a split unit go to the workspace and q8_join joins them.
-#include "rkv_attend.cuh"
-#include "rkv_causal.cuh"
-#include "rkv_internal.h"
-#include "rkv_q8.cuh"
+#include "rkv_q8_attend.cuh"
 
 namespace rkv {
 namespace {
-
-struct Q8Params {
-  CUtensorMap tmk, tmv;  // the codes as [rows][128] bytes, a page's (or half a 64-token page's) rows to a box
-  const rkv_bf16* q;     // [B][Hq][T][128]
-  const float *k_scale, *v_scale;
-  const int32_t* page_table;
-  const int32_t* seq_len;
-  const int32_t* row_len;  // null: T rows everywhere
-  int32_t* err;
-  rkv_bf16* out;
-  float* lse;      // may be null
-  float* part_o;   // [2 N][tile rows][128]
-  float2* part_ml; // [2 N][tile rows]
-  int B, Hq, Hkv, G, gshift, T, P, pshift, max_pages, num_phys, N;
-  float scale_log2;
-};
 
 constexpr int kQrWarps = 8;
 constexpr int kQrThreads = kQrWarps * 32;
@@ -54,32 +35,10 @@ constexpr int kQrPad = 8;                         // what a run costs, in chunks
 constexpr int kQrMergeRows = 4;                   // rows of every warp that meet at a time
 constexpr int kQrMergeStride = 132;               // floats
 constexpr int kQrSmem = 1024 + kQrWarps * kQrStages * kQrStageBytes + kQrWarps * kQrMergeRows * kQrMergeStride * 4;
-constexpr float kSlack = 8.f;        // a weight's exponent may lie this far above the maximum it refers to
-constexpr float kUnit = 128.f;       // 2^7: a weight of 2^8 becomes 2^15 in fp16
 constexpr float kLowestUnit = 3.009265538105056e-36f;  // 2^-118: 2^7 / vref stays finite
 
 template <int kRowsShift>
 using RowsLine = CausalLine<kRowsShift, kQrKeysShift, kQrPad>;
-
-__device__ __forceinline__ int checked_len(const Q8Params& p, int b) {
-  const int n = p.seq_len[b];
-  if (n < 0 || n > p.max_pages * p.P) {
-    flag_error(p.err, RKV_DEVERR_CAPACITY);
-    return 0;
-  }
-  return n;
-}
-__device__ __forceinline__ int checked_rows(const Q8Params& p, int b) {
-  const int m = p.row_len ? p.row_len[b] : p.T;
-  if (m < 0 || m > p.T) {
-    flag_error(p.err, RKV_DEVERR_TREE);
-    return 0;
-  }
-  return m;
-}
-__device__ __forceinline__ size_t out_row(const Q8Params& p, int b, int g, int r) {
-  return ((size_t)b * p.Hq + g * p.G + (r & (p.G - 1))) * p.T + (r >> p.gshift);
-}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -94,12 +53,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // an 8 x 8 matrix
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 .. 127
-
 // What a stage holds besides codes: the scales of its (at most two) pages and which of its 32
 // keys can be read.
 struct StageInfo {
@@ -310,7 +263,7 @@ struct RowTile8 {
 template <int kFormat, int kN>
 __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_constant__ Q8Params p) {
   constexpr int kRows = kN * 8;
-  using Line = RowsLine<kN == 1 ? 3 : 4>;
+  using Line = LineLengths<RowsLine<kN == 1 ? 3 : 4>>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Line line;
   __shared__ uint64_t full_b[kQrWarps][kQrStages];
@@ -330,11 +283,11 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
   const int N = flat_ctas(total, p.N);
   if ((int)blockIdx.x >= N) return;
   const long long x0 = flat_first(total, blockIdx.x, N), x1 = flat_first(total, blockIdx.x + 1, N);
-  auto next_run = [&](long long x, typename Line::Run& r) { return line.next(p.B, p.Hkv, p.gshift, x, x0, x1, r); };
+  auto next_run = [&](long long x, CausalRun& r) { return line.next(p.B, p.Hkv, p.gshift, x, x0, x1, r); };
 
   // this warp's chunks of a run: lo + warp, lo + warp + 8, ...  The fetch side walks the
   // runs ahead of the compute side.
-  typename Line::Run fr;
+  CausalRun fr;
   bool more = next_run(x0, fr);
   int fc = fr.lo + warp;
   auto settle = [&]() {
@@ -418,7 +371,7 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
   for (int s = 0; s < kQrStages; ++s) fetch();
   __syncwarp();
 
-  typename Line::Run cr;
+  CausalRun cr;
   RowTile8<kFormat, kN> tile;
   for (long long x = x0; next_run(x, cr); x = cr.next) {
     const int b = cr.b, g = cr.g, rt = cr.rt, rows = cr.m * p.G;
@@ -502,7 +455,7 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
 // warp a row, four channels a lane, four parts' loads in flight.
 template <class Line>
 __global__ void __launch_bounds__(256, 4) q8_join_kernel(const __grid_constant__ Q8Params p) {
-  __shared__ Line line;
+  __shared__ LineLengths<Line> line;
   line.build(p.B, p.Hkv, p.gshift, [&](int b) { return checked_len(p, b); }, [&](int b) { return checked_rows(p, b); });
   grid_dependency_wait();
   constexpr int kRows = Line::kRows;
@@ -559,12 +512,16 @@ __global__ void __launch_bounds__(256, 4) q8_join_kernel(const __grid_constant__
   }
 }
 
-int tile_rows(int T, int G) { return (long long)T * G <= 8 ? 8 : 16; }
+// How many rows of a unit share a pass over the cache: 8 or 16 (mma.sync), 128 or 256 (tcgen05).
+int tile_rows(int T, int G) {
+  const long long rows = (long long)T * G;
+  return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 128 ? 128 : 256));
+}
 
-cudaError_t fill_params(const Q8AttendArgs& a, Q8Params& p) {
+cudaError_t fill_params(const Q8AttendArgs& a, Q8Params& p, int tile) {
   const rkv_cache8& c = a.cache;
   const uint64_t rows = (uint64_t)c.num_phys_pages * c.Hkv * c.page_size;
-  const uint32_t box = c.page_size < kQrKeys ? c.page_size : kQrKeys;
+  const uint32_t box = tile > 16 || c.page_size < kQrKeys ? c.page_size : kQrKeys;
   if (!encode_codes_map(&p.tmk, c.k_codes, rows, box) || !encode_codes_map(&p.tmv, c.v_codes, rows, box)) {
     set_last_error("cuTensorMapEncodeTiled failed for the cache's codes");
     return cudaErrorInvalidValue;
@@ -613,20 +570,34 @@ size_t q8_attend_ws_bytes(int B, int Hq, int Hkv, int T, int max_pages, int page
 
 cudaError_t launch_q8_attend(const Q8AttendArgs& a, cudaStream_t s) {
   Q8Params p;
-  cudaError_t e = fill_params(a, p);
+  const int tile = tile_rows(a.T, a.Hq / a.cache.Hkv);
+  cudaError_t e = fill_params(a, p, tile);
   if (e != cudaSuccess) return e;
-  const int tile = tile_rows(a.T, p.G);
   const size_t rows = (size_t)2 * kMaxSms * tile;
   p.part_o = static_cast<float*>(a.ws);
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(a.ws) + align256(rows * 128 * 4));
   const bool int8 = a.cache.format == RKV_Q8_INT8;
-  if (tile == 8) e = int8 ? launch_rows<RKV_Q8_INT8, 1>(p, s) : launch_rows<RKV_Q8_E4M3, 1>(p, s);
-  else e = int8 ? launch_rows<RKV_Q8_INT8, 2>(p, s) : launch_rows<RKV_Q8_E4M3, 2>(p, s);
+  void (*join)(Q8Params);
+  switch (tile) {
+    case 8:
+      e = int8 ? launch_rows<RKV_Q8_INT8, 1>(p, s) : launch_rows<RKV_Q8_E4M3, 1>(p, s);
+      join = q8_join_kernel<RowsLine<3>>;
+      break;
+    case 16:
+      e = int8 ? launch_rows<RKV_Q8_INT8, 2>(p, s) : launch_rows<RKV_Q8_E4M3, 2>(p, s);
+      join = q8_join_kernel<RowsLine<4>>;
+      break;
+    case 128:
+      e = launch_q8_tiles(p, false, int8, s);
+      join = q8_join_kernel<TileLine<7>>;
+      break;
+    default:
+      e = launch_q8_tiles(p, true, int8, s);
+      join = q8_join_kernel<TileLine<8>>;
+  }
   if (e != cudaSuccess) return e;
   const long long jrows = ((long long)p.B * a.Hq * a.T + 7) / 8, jmost = 8LL * p.N;
-  const dim3 jgrid((unsigned)(jrows < jmost ? jrows : jmost));
-  return tile == 8 ? launch_dependent(q8_join_kernel<RowsLine<3>>, jgrid, 256, K_Q8_JOIN, s, p)
-                   : launch_dependent(q8_join_kernel<RowsLine<4>>, jgrid, 256, K_Q8_JOIN, s, p);
+  return launch_dependent(join, dim3((unsigned)(jrows < jmost ? jrows : jmost)), 256, K_Q8_JOIN, s, p);
 }
 
 }  // namespace rkv

@@ -1,0 +1,711 @@
+// Attention over the 8-bit cache for many query rows, on the fifth-generation tensor cores
+// (formulas and what is rounded: rkv_q8_attend.cu).
+//
+// Two row slots of 128 rows work in turn on 128-key tiles: while a slot's four warps turn its
+// logits into weights, the tensor cores run the other slot's products.
+//   S = Q K^T   128 x 128 x 128, fp16, both operands in shared memory, S in TMEM;
+//   P           fp16, written back over S's columns (thread = row = TMEM lane);
+//   O += P V    128 x 128 x 128, P from TMEM, V from shared memory, O in TMEM.
+// kWide: a unit's tile is 256 rows, the slots hold different rows and both use every key
+// tile.  Otherwise the tile is 128 rows and the slots take alternate key tiles of the same
+// rows, each with its own maximum, sum and O, and join them at the end of a run.
+//
+// TMA brings a tile's codes (16 KB of K, 16 KB of V) and four warps write them out as fp16
+// operands, 32 KB each, times 2^(page's exponent - tile's): K's tile exponent is its pages'
+// largest and joins the logits, V's is the largest of the run so far, the unit of O (where
+// it grows, O is scaled down with the maximum's move).  A code times such a factor is exact
+// but where it falls below fp16's smallest step, 2^-33 of the largest.
+//   warps 0-3, 4-7: softmax of slot 0, 1;  8, 10: TMA of K, V;  9: MMA issue;  11: idle;
+//   12-15: codes to fp16.
+// Order and phases of both rings are the same formula in every role.  Every wait is bounded;
+// one that runs out flags RKV_DEVERR_TIMEOUT and stops every role.
+#include "rkv_q8_attend.cuh"
+
+namespace rkv {
+namespace {
+
+constexpr int kQtKeys = 1 << kQtKeysShift;
+constexpr int kQtThreads = 512;
+// Registers: 512 threads start with 128 each; the softmax warps take 192, the third
+// warpgroup (TMA, MMA) 56 and the fourth 72: 256 x 192 + 128 x 56 + 128 x 72 = 512 x 128.
+constexpr int kQtSoftRegs = 192, kQtIssueRegs = 56, kQtCodeRegs = 72;
+static_assert(256 * kQtSoftRegs + 128 * (kQtIssueRegs + kQtCodeRegs) == 512 * 128,
+              "the split must be what the block was launched with");
+constexpr int kQtTile = kQtKeys * 256, kQtCodes = kQtKeys * 128;
+constexpr int kQtInfos = 8;     // tiles between the TMA and the softmax: at most six
+constexpr int kNoFactor = 255;  // a page of NaN: NaN keys, no values
+constexpr int kNoRow = -128;    // a query row with a NaN or an infinity
+// A row whose maximum lies beyond this has distinct logits at least 64 apart: its exponents
+// are taken with the power of two below the factor, whose product with the maximum is exact.
+constexpr float kQtFar = 1073741824.f;
+
+// A tile's scales: each 16-key group's exponent below the tile's, the tiles', and which
+// groups were loaded.
+struct TileInfo {
+  uint8_t k[8], v[8];
+  int16_t ek, ev;
+  uint32_t groups;
+};
+
+template <bool kWide>
+struct TileShape8 {
+  static constexpr int kRows = kWide ? 256 : 128;
+  static constexpr int kQBytes = kRows * 256;
+  static constexpr int kTiles = kWide ? 4 : 3, kCodeSlots = kWide ? 2 : 5;
+  using Line = TileLine<kWide ? 8 : 7>;
+  struct Shared {
+    uint8_t q[kQBytes];
+    uint8_t tiles[kTiles * kQtTile];
+    uint8_t codes[kCodeSlots * kQtCodes];
+    Line line;
+    uint64_t full_c[kCodeSlots], empty_c[kCodeSlots], full[kTiles], empty[kTiles], s[2], p[2], o[2], qf[2], out[2], ml, drained;
+    TileInfo info[kQtInfos];
+    CausalRun first;  // the share's first run, worked out once
+    long long x0, x1;
+    uint32_t tmem_base;
+    int abort_flag;
+    bool any;
+    int8_t row_exp[kRows];
+    float2 ml_s[kWide ? 1 : 2][kWide ? 1 : 128];
+  };
+  static constexpr int kSmem = sizeof(Shared);
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+};
+
+// The j-th of a run's 2 nt tiles of codes: K or V of which key tile.
+template <bool kWide>
+__device__ __forceinline__ void entry_of(int j, int nt, bool& v, int& i) {
+  if (kWide) {
+    v = j & 1;
+    i = j >> 1;
+  } else {  // K_0, then K_(i+1) and V_i for every i
+    v = j == 2 * nt - 1 || (j > 0 && !(j & 1));
+    i = j == 2 * nt - 1 ? nt - 1 : (v ? (j >> 1) - 1 : (j + 1) >> 1);
+  }
+}
+template <bool kWide>
+__device__ __forceinline__ int place_of(bool v, int i, int nt) {
+  if (kWide) return 2 * i + v;
+  return v ? (i + 1 < nt ? 2 * i + 2 : 2 * nt - 1) : (i > 0 ? 2 * i - 1 : 0);
+}
+
+// 2^-d as a pair of fp16 numbers, d <= 24.
+__device__ __forceinline__ __half2 half_power(int d) {
+  const uint32_t h = d < 15 ? (uint32_t)(15 - d) << 10 : 1u << (24 - d);
+  const uint32_t hh = h | (h << 16);
+  return *reinterpret_cast<const __half2*>(&hh);
+}
+
+template <int kFormat, bool kWide>
+__global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_constant__ Q8Params p) {
+  using Sh = TileShape8<kWide>;
+  constexpr int E = Sh::kTiles, C = Sh::kCodeSlots, R = Sh::kRows;
+  extern __shared__ __align__(1024) uint8_t dyn_smem[];
+  typename Sh::Shared& sh = *reinterpret_cast<typename Sh::Shared*>(dyn_smem);
+  volatile int& abort_flag = *const_cast<volatile int*>(&sh.abort_flag);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int e = 0; e < E; ++e) {
+      mbar_init(&sh.full[e], 4);   // the four warps that wrote it
+      mbar_init(&sh.empty[e], 1);
+    }
+    for (int c = 0; c < C; ++c) {
+      mbar_init(&sh.full_c[c], 1);
+      mbar_init(&sh.empty_c[c], 4);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh.s[s], 2);  // the issuing thread and its commit
+      mbar_init(&sh.p[s], 128);
+      mbar_init(&sh.o[s], 1);
+      mbar_init(&sh.qf[s], kWide ? 128 : 256);
+      mbar_init(&sh.out[s], kWide ? 128 : 256);
+    }
+    mbar_init(&sh.ml, 256);
+    mbar_init(&sh.drained, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (tid == 32) {
+    prefetch_map(&p.tmk);
+    prefetch_map(&p.tmv);
+  }
+  if (warp == 9) {
+    tmem_alloc(&sh.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  auto len_of = [&](int b) { return checked_len(p, b); };
+  auto rows_of = [&](int b) { return checked_rows(p, b); };
+  sh.line.build(p.B, p.Hkv, p.gshift, len_of, rows_of);  // ends with a block barrier
+  tc_fence_after();
+  grid_launch_dependents();
+  const uint32_t tmem = sh.tmem_base;
+  if (tid == 0) {
+    const long long total = sh.line.base[p.B];
+    const int N = flat_ctas(total, p.N);
+    const bool works = (int)blockIdx.x < N;
+    sh.x0 = works ? flat_first(total, blockIdx.x, N) : 0;
+    sh.x1 = works ? flat_first(total, blockIdx.x + 1, N) : 0;
+    sh.any = sh.line.next(p.B, p.Hkv, p.gshift, len_of, rows_of, sh.x0, sh.x0, sh.x1, sh.first);
+  }
+  __syncthreads();
+  const long long x0 = sh.x0, x1 = sh.x1;
+  auto next_run = [&](long long x, CausalRun& r) {
+    if (x != x0) return sh.line.next(p.B, p.Hkv, p.gshift, len_of, rows_of, x, x0, x1, r);
+    r = sh.first;
+    return sh.any;
+  };
+  auto give_up = [&]() {
+    flag_error(p.err, RKV_DEVERR_TIMEOUT);
+    abort_flag = 1;
+  };
+  // waits of a converged warp: all of its lanes go on, or none
+  auto wait = [&](uint64_t* bar, int phase) {
+    const bool late = !mbar_wait_role(bar, (uint32_t)(phase & 1), &abort_flag);
+    if (__any_sync(0xffffffffu, late)) {
+      give_up();
+      return false;
+    }
+    return true;
+  };
+  int loaded = 0;  // one past the last tile of codes asked for (warps 8, 10), of operands used (warp 9)
+  CausalRun r;
+
+  if (warp < 8) {
+    setmaxnreg_inc<kQtSoftRegs>();
+    const int slot = warp >> 2, row = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), mine = lanes + slot * 256;
+    int seen_s = 0, run = 0, done[2] = {0, 0}, tiles_before = 0;
+    bool ok = true;
+    for (long long x = x0; ok && next_run(x, r); x = r.next) {
+      const int b = r.b, g = r.g, rt = r.rt, n = r.n, rows = r.m * p.G, nt = r.hi - r.lo;
+      const bool idle = kWide && slot == 1 && rows - rt * R <= 128;
+      // the query rows as fp16, swizzled as TMA would store them, over the last run's staged outputs
+      if (run > 0 && !(ok = wait(&sh.out[kWide ? slot : 0], run - 1))) break;
+      {
+        constexpr int kPer = kWide ? 128 : 64;  // rows this slot's warps load
+        const int q0 = kWide ? 0 : slot * 64;
+        uint8_t* dst = sh.q + (kWide ? slot * (128 * 256) : 0);
+        const int piece = row & 15;
+        uint4 v[kPer / 8];  // all loads in flight together
+#pragma unroll
+        for (int j = 0; j < kPer / 8; ++j) {
+          const int rr = rt * R + (kWide ? slot * 128 : 0) + q0 + (row >> 4) + j * 8;
+          v[j] = make_uint4(0, 0, 0, 0);
+          if (rr < rows) v[j] = reinterpret_cast<const uint4*>(p.q + out_row(p, b, g, rr) * 128)[piece];
+        }
+#pragma unroll
+        for (int j = 0; j < kPer / 8; ++j) {
+          const int i = q0 + (row >> 4) + j * 8;
+          uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+          uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                  __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+          top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int e = max((int)(top >> 7) - 127, -100);  // the largest magnitude's exponent
+          const float up = power_of_two(8 - min(e, 127));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = pack_f16x2(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
+          *reinterpret_cast<uint4*>(dst + (piece >> 3) * (128 * 128) + i * 128 + (((piece & 7) ^ (i & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+          if (piece == 0) sh.row_exp[(kWide ? slot * 128 : 0) + i] = (int8_t)(top >= 0x7f80u ? kNoRow : e);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&sh.qf[kWide ? slot : 0]);
+      }
+      const int my = rt * R + (kWide ? slot * 128 : 0) + row;  // this thread's query row
+      // keys that it sees, and that the slot's first row does
+      const int lim = my < rows ? n - r.m + (my >> p.gshift) + 1 : n;
+      const int least = n - r.m + ((rt * R + (kWide ? slot * 128 : 0)) >> p.gshift) + 1;
+      float m = kNoMax, l = 0.f, factor = 0.f, ref = kNoMax;
+      bool far = false;
+      int unit = -126;  // O is in units of 2^unit
+      if (!idle) {
+        for (int i = kWide ? 0 : slot; i < nt; i += kWide ? 1 : 2) {
+          if (!(ok = wait(&sh.s[slot], seen_s++))) break;
+          tc_fence_after();
+          const bool first = i < (kWide ? 1 : 2);
+          if (first) {
+            const int e = sh.row_exp[(kWide ? slot * 128 : 0) + row];
+            factor = e == kNoRow ? __uint_as_float(0x7fffffffu) : p.scale_log2 * power_of_two(e - 8);
+          }
+          const TileInfo& ti = sh.info[(tiles_before + i) % kQtInfos];
+          const int key0 = (r.lo + i) * kQtKeys, left = n - key0, to_unit = ti.ev;
+          const uint32_t gr = ti.groups;
+          float sl = factor * power_of_two(ti.ek);
+          if (sl < kLowestScale) sl = kLowestScale;  // 0 x -inf is not -inf; a NaN stays
+          const bool all = left >= kQtKeys && gr == 0xffu && key0 + kQtKeys <= least;
+          uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+          if (!all) {
+            const int mine_left = min(left, lim - key0);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int k = mine_left - w * 32;
+              see[w] = k >= 32 ? ~0u : (k <= 0 ? 0u : (1u << k) - 1u);
+              if (!((gr >> (2 * w)) & 1u)) see[w] &= 0xffff0000u;
+              if (!((gr >> (2 * w + 1)) & 1u)) see[w] &= 0x0000ffffu;
+            }
+          }
+          uint32_t v[4][32];
+          float mx = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tc_ld32(mine + c * 32, v[c]);
+          tc_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tc_ld_done(v[c]);
+            if (!all) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((see[c] >> j) & 1u)) v[c][j] = 0xff800000u;  // -inf
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              mx = max3(mx, __uint_as_float(v[c][j]), __uint_as_float(v[c][j + 1]));
+              mx1 = max3(mx1, __uint_as_float(v[c][j + 2]), __uint_as_float(v[c][j + 3]));
+            }
+          }
+          const float raw = fmaxf(mx, mx1);
+          mx = raw * sl;  // sl > 0
+          auto set_ref = [&]() {
+            far = fabsf(m) > kQtFar && m != kNoMax;
+            ref = far ? raw * __uint_as_float(__float_as_uint(sl) & 0x7f800000u) : m;
+          };
+          if (first) {
+            m = fmaxf(kNoMax, mx);
+            set_ref();
+            unit = to_unit;
+          } else if (__any_sync(0xffffffffu, mx > m + kSlack || to_unit != unit)) {
+            // this slot's earlier products are complete: its logits were issued after them
+            const float to = fmaxf(m, mx), f = ex2_approx(m - to);
+            const float fo = f * power_of_two(max(unit - to_unit, -126));
+            unit = to_unit;
+            if (mx > m) {
+              m = to;
+              set_ref();
+            }
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tc_ld32_wait(mine + 128 + c * 32, o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fo);
+              tc_st32_wait(mine + 128 + c * 32, o);
+            }
+          }
+          const float by = far ? __uint_as_float(__float_as_uint(sl) & 0x7f800000u) : sl, sub = ref - 7.f;  // times kUnit
+          float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int cc = c * 2 + (j >> 4), jj = (j & 15) * 2;
+              const float ax = ex2_approx(fmaf(__uint_as_float(v[cc][jj]), by, -sub));
+              const float ay = ex2_approx(fmaf(__uint_as_float(v[cc][jj + 1]), by, -sub));
+              (j & 1 ? u0 : s0) += ax;
+              (j & 1 ? u1 : s1) += ay;
+              pk[j] = pack_f16x2(ax, ay);
+            }
+            tc_st32(mine + c * 32, pk);
+          }
+          tc_st_wait();
+          l += (s0 + s1) + (u0 + u1);
+          tc_fence_before();
+          mbar_arrive(&sh.p[slot]);
+        }
+      }
+      if (!ok) break;
+      tiles_before += nt;
+      l *= 1.f / kUnit;
+      float fo = power_of_two(max(unit - 7, -126));  // O's unit, with the weights'
+      // the run's end: out = O / l (whole unit) or the part (m, l, O)
+      const bool has[2] = {true, kWide ? true : nt > 1};
+      float f0 = fo, f1 = 0.f;
+      if (kWide) {
+        if (!(ok = wait(&sh.o[slot], done[slot]++))) break;
+      } else {
+        // both slots' sums, and their outputs' factors to the joint maximum
+        sh.ml_s[slot][row] = make_float2(m, l);
+        mbar_arrive(&sh.ml);
+        if (!(ok = wait(&sh.ml, run))) break;
+        if (!(ok = wait(&sh.o[0], done[0]++))) break;
+        if (has[1] && !(ok = wait(&sh.o[1], done[1]++))) break;
+        const float2 a = sh.ml_s[0][row], c = has[1] ? sh.ml_s[1][row] : make_float2(kNoMax, 0.f);
+        m = fmaxf(a.x, c.x);
+        f0 = ex2_approx(a.x - m);
+        f1 = ex2_approx(c.x - m);
+        l = a.y * f0 + c.y * f1;
+        // a slot's unit is that of its last tile
+        const int last0 = (nt - 1) & ~1, last1 = has[1] ? ((nt & 1) ? nt - 2 : nt - 1) : 0;
+        f0 *= power_of_two(max((int)sh.info[(tiles_before - nt + last0) % kQtInfos].ev - 7, -126));
+        if (has[1]) f1 *= power_of_two(max((int)sh.info[(tiles_before - nt + last1) % kQtInfos].ev - 7, -126));
+      }
+      ++run;
+      tc_fence_after();
+      if (!idle) {
+        const bool live = my < rows;
+        const float inv = r.whole ? inverse_of(l) : 1.f;
+        f0 *= inv;
+        f1 *= inv;
+        const size_t orow = live ? out_row(p, b, g, my) : 0;
+        const size_t prow = (2 * (size_t)blockIdx.x + (r.first ? 0 : 1)) * R + (kWide ? slot * 128 : 0) + row;
+        // kWide: all 128 channels of this slot's row; else 64 channels of both slots' O.  32
+        // channels of the warp's 32 rows at a time go through the query tile's memory (its
+        // products are done), so that the stores are whole 128-byte (bf16: 64-byte) pieces
+        // of rows and not 16 bytes of 32 rows each.
+        constexpr int kChunks = kWide ? 4 : 2;
+        uint8_t* const stage = sh.q + slot * (kWide ? 32768 : 16384) + (warp & 3) * 4096;
+        const int row0 = rt * R + (kWide ? slot * 128 : 0) + (warp & 3) * 32;  // the warp's first query row
+        const size_t prow0 = prow - lane;
+#pragma unroll 1
+        for (int cc = 0; cc < kChunks; ++cc) {
+          const int c = kWide ? cc : slot * 2 + cc;
+          uint32_t o[32];
+          tc_ld32_wait(kWide ? mine + 128 + c * 32 : lanes + 128 + c * 32, o);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
+          if (!kWide && has[1]) {
+            uint32_t o1[32];
+            tc_ld32_wait(lanes + 256 + 128 + c * 32, o1);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j])));
+          }
+          __syncwarp();  // the staged piece before this one is read
+          if (r.whole) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16x2(__uint_as_float(o[j * 8 + 2 * e]), __uint_as_float(o[j * 8 + 2 * e + 1]));
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int i = k * 8 + (lane >> 2), j = lane & 3;
+              const uint4 w = *reinterpret_cast<const uint4*>(stage + i * 64 + ((j ^ ((i >> 1) & 3)) << 4));
+              if (row0 + i < rows) reinterpret_cast<uint4*>(p.out + out_row(p, b, g, row0 + i) * 128 + c * 32)[j] = w;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                  make_uint4(o[j * 4], o[j * 4 + 1], o[j * 4 + 2], o[j * 4 + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int i = k * 4 + (lane >> 3), j = lane & 7;
+              const uint4 w = *reinterpret_cast<const uint4*>(stage + i * 128 + ((j ^ (i & 7)) << 4));
+              if (row0 + i < rows) reinterpret_cast<uint4*>(p.part_o + (prow0 + i) * 128 + c * 32)[j] = w;
+            }
+          }
+        }
+        if (live && (kWide || slot == 0)) {
+          if (!r.whole) p.part_ml[prow] = make_float2(m, l);
+          else if (p.lse) p.lse[orow] = lse_of(m, l);
+        }
+        tc_fence_before();  // O is read before the next run's queries let its products start
+      }
+      mbar_arrive(&sh.out[kWide ? slot : 0]);  // this thread has read what it staged
+    }
+  } else if (warp < 12) {
+    setmaxnreg_dec<kQtIssueRegs>();
+    if (warp == 8 || warp == 10) {
+      const bool v = warp == 10;
+      const CUtensorMap* map = v ? &p.tmv : &p.tmk;
+      const bool lead = elect_lane();
+      const int pages = kQtKeys >> p.pshift, box = p.P * 128, per_page = p.P >> 4;  // of a tile; bytes; 16-key groups
+      const uint64_t policy = l2_policy(!kWide && (long long)p.T * p.G <= R);  // one row tile: read once
+      int before = 0, tiles_before = 0;
+      bool ok = true;
+      for (long long x = x0; ok && next_run(x, r); x = r.next) {
+        const int b = r.b, g = r.g, n = r.n, nt = r.hi - r.lo;
+        // lane j: the tile's page j, and its scales (warp 8); loaded a tile ahead, so that the
+        // loads' latency stays off the ring
+        auto page_of = [&](int tile) {
+          const int pg = tile * pages + lane;
+          return lane < pages && pg * p.P < n ? p.page_table[(size_t)b * p.max_pages + pg] : -1;
+        };
+        auto scales_of = [&](int phys, float& sk, float& sv) {
+          sk = sv = 0.f;
+          if (!v && phys >= 0 && phys < p.num_phys) {
+            sk = p.k_scale[(size_t)phys * p.Hkv + g];
+            sv = p.v_scale[(size_t)phys * p.Hkv + g];
+          }
+        };
+        int next = page_of(r.lo), after = nt > 1 ? page_of(r.lo + 1) : -1, unit = -126;
+        float nk, nv;
+        scales_of(next, nk, nv);
+        for (int i = 0; i < nt; ++i) {
+          const int tile = r.lo + i;
+          int phys = next;
+          const float sk = nk, sv = nv;
+          next = after;
+          after = i + 2 < nt ? page_of(tile + 2) : -1;
+          scales_of(next, nk, nv);
+          const int at = before + place_of<kWide>(v, i, nt), c = at % C;
+          if (at >= C && !(ok = wait(&sh.empty_c[c], at / C - 1))) break;
+          const bool mine = lane < pages && (tile * pages + lane) * p.P < n;
+          if (phys < 0 || phys >= p.num_phys) {
+            if (mine) flag_error(p.err, RKV_DEVERR_PAGE_ID);
+            phys = -1;
+          }
+          const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0);
+          if (!v) {
+            // exponents; 255: NaN (a scale is positive)
+            const int xk = (int)(__float_as_uint(sk) >> 23) & 255, xv = (int)(__float_as_uint(sv) >> 23) & 255;
+            const bool in = phys >= 0;
+            const int ek = __reduce_max_sync(0xffffffffu, in && xk < 255 ? xk : 1) - 127;
+            unit = max(unit, __reduce_max_sync(0xffffffffu, in && xv < 255 ? xv : 1) - 127);
+            TileInfo& ti = sh.info[(tiles_before + i) % kQtInfos];
+            if (lane < pages)
+              for (int j = 0; j < per_page; ++j) {
+                ti.k[lane * per_page + j] = (uint8_t)(xk == 255 ? kNoFactor : min(max(ek - (xk - 127), 0), 254));
+                ti.v[lane * per_page + j] = (uint8_t)(xv == 255 ? kNoFactor : min(max(unit - (xv - 127), 0), 254));
+              }
+            if (lead) {
+              uint32_t gr = 0;
+              for (int j = 0; j < pages; ++j)
+                if ((have >> j) & 1u) gr |= ((1u << per_page) - 1u) << (j * per_page);
+              ti.groups = gr;
+              ti.ek = (int16_t)ek;
+              ti.ev = (int16_t)unit;
+            }
+            __syncwarp();
+          }
+          uint8_t* const st = sh.codes + c * kQtCodes;
+          if (lead) {
+            if (have) mbar_arrive_expect_tx(&sh.full_c[c], __popc(have) * box);
+            else mbar_arrive(&sh.full_c[c]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int row = (__shfl_sync(0xffffffffu, phys, j) * p.Hkv + g) * p.P;
+            if (lead && ((have >> j) & 1u)) tma_load_2d_hint(st + j * box, map, 0, row, &sh.full_c[c], policy);
+          }
+          loaded = at + 1;
+        }
+        before += 2 * nt;
+        tiles_before += nt;
+      }
+    } else if (warp == 9) {
+      constexpr uint32_t idesc_s = idesc_f16_f32(128, 128), idesc_o = idesc_s | kIdescBNMajor;
+      const uint32_t q32 = smem_u32(sh.q), ring32 = smem_u32(sh.tiles);
+      int seen_p[2] = {0, 0}, runs[2] = {0, 0};
+      bool ok = true;
+      const bool lead = elect_lane();
+      const uint32_t qlo = sw128_kmajor_lo(q32), klo = sw128_kmajor_lo(ring32), vlo = sw128_nmajor_lo(ring32, kQtTile / 2);
+      // S of `slot` from the K operand e
+      auto mma_s = [&](int slot, int e, bool release) {
+        tc_fence_after();
+        const uint32_t d = tmem + slot * 256, qa = qlo + (kWide ? slot * (128 * 256 >> 4) : 0), ka = klo + e * (kQtTile >> 4);
+        tc_mma_ss<false>(lead, d, qa, ka, idesc_s);
+#pragma unroll
+        for (int k = 1; k < 8; ++k) {
+          const uint32_t off = ((k >> 2) * (kQtTile / 2) + (k & 3) * 32) >> 4;
+          tc_mma_ss<true>(lead, d, qa + off, ka + off, idesc_s);
+        }
+        tc_commit_if(lead && release, &sh.empty[e]);
+        tc_commit_if(lead, &sh.s[slot]);
+        if (lead) mbar_arrive(&sh.s[slot]);
+        __syncwarp();
+      };
+      // O += P V once the slot's weights are there
+      auto mma_o = [&](int slot, int e, bool first, bool last, bool release) {
+        if (!(ok = wait(&sh.p[slot], seen_p[slot]++))) return;
+        tc_fence_after();
+        const uint32_t d = tmem + slot * 256 + 128, pa = tmem + slot * 256, va = vlo + e * (kQtTile >> 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc_mma_ts(lead, d, pa + k * 8, va + (k * 2048 >> 4), idesc_o, (first && k == 0) ? 0u : 1u);
+        tc_commit_if(lead && release, &sh.empty[e]);
+        tc_commit_if(lead && last, &sh.o[slot]);
+      };
+      for (long long x = x0; ok && next_run(x, r); x = r.next) {
+        const int nt = r.hi - r.lo;
+        const bool two = kWide && r.m * p.G - r.rt * R > 128;  // slot 1 has rows
+        auto take = [&]() {  // the next operand, written
+          const int e = loaded % E;
+          ok = wait(&sh.full[e], loaded / E);
+          ++loaded;
+          return e;
+        };
+        ok = wait(&sh.qf[0], runs[0]++);
+        if (kWide && ok) ok = wait(&sh.qf[1], runs[1]++);
+        if (!ok) break;
+        if (kWide) {
+          int ek = take();
+          if (!ok) break;
+          mma_s(0, ek, !two);
+          if (two) mma_s(1, ek, true);
+          for (int i = 0; i < nt; ++i) {
+            const int ev = take();
+            if (!ok) break;
+            const bool last = i + 1 == nt;
+            mma_o(0, ev, i == 0, last, !two);
+            if (!ok) break;
+            tc_commit_if(lead && last && !two, &sh.o[1]);  // keeps an idle slot in step
+            int en = 0;
+            if (!last) {
+              en = take();
+              if (!ok) break;
+              mma_s(0, en, !two);
+            }
+            if (two) {
+              mma_o(1, ev, i == 0, last, true);
+              if (!ok) break;
+              if (!last) mma_s(1, en, true);
+            }
+          }
+        } else {
+          const int e0 = take();
+          if (!ok) break;
+          mma_s(0, e0, true);
+          for (int i = 0; i < nt; ++i) {
+            const int slot = i & 1;
+            if (i + 1 < nt) {
+              // tile i + 1's logits go where tile i - 1's weights lay: its product was issued before
+              const int en = take();
+              if (!ok) break;
+              mma_s(slot ^ 1, en, true);
+            }
+            const int ev = take();
+            if (!ok) break;
+            mma_o(slot, ev, i < 2, i + 2 >= nt, true);
+            if (!ok) break;
+          }
+        }
+      }
+      // the last operands' releases land before the CTA may exit
+      if (ok)
+        for (int i = loaded > E ? loaded - E : 0; i < loaded; ++i) mbar_wait(&sh.empty[i % E], (uint32_t)((i / E) & 1));
+    }
+  } else {
+    // codes to fp16: a warp's 32 keys of a tile, four keys of eight 16-code pieces at a time
+    setmaxnreg_dec<kQtCodeRegs>();
+    const int quarter = warp - 12, sub = lane >> 3, piece = lane & 7;
+    int before = 0, tiles_before = 0;
+    bool ok = true;
+    for (long long x = x0; ok && next_run(x, r); x = r.next) {
+      const int nt = r.hi - r.lo;
+      for (int j = 0; j < 2 * nt; ++j) {
+        bool v;
+        int i;
+        entry_of<kWide>(j, nt, v, i);
+        const int at = before + j, c = at % C, e = at % E;
+        if (!(ok = wait(&sh.full_c[c], at / C))) break;
+        const TileInfo& ti = sh.info[(tiles_before + i) % kQtInfos];
+        const int left = r.n - (r.lo + i) * kQtKeys;
+        const uint32_t gr = ti.groups;
+        const int d0 = v ? ti.v[quarter * 2] : ti.k[quarter * 2], d1 = v ? ti.v[quarter * 2 + 1] : ti.k[quarter * 2 + 1];
+        const uint8_t* const src = sh.codes + c * kQtCodes;
+        uint4 w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int row = quarter * 32 + k * 4 + sub;
+          w[k] = *reinterpret_cast<const uint4*>(src + row * 128 + ((piece ^ (row & 7)) << 4));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty_c[c]);  // the codes are in registers
+        if (at >= E && !(ok = wait(&sh.empty[e], at / E - 1))) break;
+        uint8_t* const dst = sh.tiles + e * kQtTile + (piece >> 2) * (kQtTile / 2);
+        auto put = [&](int row, const uint32_t (&a)[4], const uint32_t (&c4)[4]) {
+          const uint32_t sw = (uint32_t)(row & 7);
+          *reinterpret_cast<uint4*>(dst + row * 128 + ((((piece & 3) * 2) ^ sw) << 4)) = make_uint4(a[0], a[1], a[2], a[3]);
+          *reinterpret_cast<uint4*>(dst + row * 128 + ((((piece & 3) * 2 + 1) ^ sw) << 4)) =
+              make_uint4(c4[0], c4[1], c4[2], c4[3]);
+        };
+        // one branch for the whole tile: in the unrolled loop, a few of them cost 430 clocks a key row
+        if (max(d0, d1) <= 9 && (!v || (left >= kQtKeys && gr == 0xffu))) {
+          // a factor of 2^-9 keeps -1152 f an fp16 number
+          const __half2 f[2] = {half_power(d0), half_power(d1)};
+          const __half2 bias[2] = {__hmul2(f[0], __float2half2_rn(-1152.f)), __hmul2(f[1], __float2half2_rn(-1152.f))};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t a[4], c4[4];
+            decode4_times<kFormat>(w[k].x, f[k >> 2], bias[k >> 2], a[0], a[1]);
+            decode4_times<kFormat>(w[k].y, f[k >> 2], bias[k >> 2], a[2], a[3]);
+            decode4_times<kFormat>(w[k].z, f[k >> 2], bias[k >> 2], c4[0], c4[1]);
+            decode4_times<kFormat>(w[k].w, f[k >> 2], bias[k >> 2], c4[2], c4[3]);
+            put(quarter * 32 + k * 4 + sub, a, c4);
+          }
+        } else {
+          // scales far apart, a page of NaN, or values that are not there: those, and a page of
+          // NaN's (whoever sees it has NaN logits), may be anything, and 0 x NaN is not 0
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int d = h ? d1 : d0;
+            const __half2 f = d == kNoFactor ? __half2half2(__ushort_as_half(0x7fff)) : half_power(min(d, 14));
+            const __half2 f2 = half_power(d == kNoFactor ? 0 : min(max(d - 14, 0), 24));
+#pragma unroll
+            for (int k = h * 4; k < h * 4 + 4; ++k) {
+              const int row = quarter * 32 + k * 4 + sub;
+              const bool none = v && (row >= left || d == kNoFactor || !((gr >> (row >> 4)) & 1u));
+              uint32_t a[4], c4[4];
+              decode4<kFormat>(w[k].x, a[0], a[1]);
+              decode4<kFormat>(w[k].y, a[2], a[3]);
+              decode4<kFormat>(w[k].z, c4[0], c4[1]);
+              decode4<kFormat>(w[k].w, c4[2], c4[3]);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const __half2 x = __hmul2(__hmul2(*reinterpret_cast<__half2*>(&a[q]), f), f2);
+                const __half2 y = __hmul2(__hmul2(*reinterpret_cast<__half2*>(&c4[q]), f), f2);
+                a[q] = none ? 0u : *reinterpret_cast<const uint32_t*>(&x);
+                c4[q] = none ? 0u : *reinterpret_cast<const uint32_t*>(&y);
+              }
+              put(row, a, c4);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.full[e]);
+      }
+      before += 2 * nt;
+      tiles_before += nt;
+    }
+  }
+
+  // teardown: after a timeout, wait (bounded) for the copies and products still in flight
+  tc_fence_before();
+  __syncthreads();
+  if (abort_flag) {
+    if ((warp == 8 || warp == 10) && lane == 0)
+      for (int i = loaded > C ? loaded - C : 0; i < loaded; ++i) mbar_wait(&sh.full_c[i % C], (uint32_t)((i / C) & 1));
+    if (warp == 9) {  // everything this lane issued before the commit has completed when it arrives
+      tc_commit_if(elect_lane(), &sh.drained);
+      mbar_wait(&sh.drained, 0);
+    }
+    __syncthreads();
+  }
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int kFormat, bool kWide>
+cudaError_t launch(const Q8Params& p, cudaStream_t s) {
+  static SmemOptIn opt;
+  const int smem = TileShape8<kWide>::kSmem;
+  const cudaError_t e = opt.raise(reinterpret_cast<const void*>(q8_tiles_kernel<kFormat, kWide>), smem);
+  if (e != cudaSuccess) return e;
+  launch_begin(K_Q8_TILES, s);
+  q8_tiles_kernel<kFormat, kWide><<<p.N, kQtThreads, smem, s>>>(p);
+  launch_end(K_Q8_TILES, s);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_q8_tiles(const Q8Params& p, bool wide, bool int8, cudaStream_t s) {
+  if (wide) return int8 ? launch<RKV_Q8_INT8, true>(p, s) : launch<RKV_Q8_E4M3, true>(p, s);
+  return int8 ? launch<RKV_Q8_INT8, false>(p, s) : launch<RKV_Q8_E4M3, false>(p, s);
+}
+
+}  // namespace rkv
