@@ -10,13 +10,13 @@
 // tile.  Otherwise the tile is 128 rows and the slots take alternate key tiles of the same
 // rows, each with its own maximum, sum and O, and join them at the end of a run.
 //
-// TMA brings a tile's codes (16 KB of K, 16 KB of V) and four warps write them out as fp16
+// TMA brings a tile's codes (16 KB of K, 16 KB of V) and eight warps write them out as fp16
 // operands, 32 KB each, times 2^(page's exponent - tile's): K's tile exponent is its pages'
 // largest and joins the logits, V's is the largest of the run so far, the unit of O (where
 // it grows, O is scaled down with the maximum's move).  A code times such a factor is exact
 // but where it falls below fp16's smallest step, 2^-33 of the largest.
 //   warps 0-3, 4-7: softmax of slot 0, 1;  8, 10: TMA of K, V;  9: MMA issue;  11: idle;
-//   12-15: codes to fp16.
+//   12-15, 16-19: K's and V's codes to fp16.
 // Order and phases of both rings are the same formula in every role.  Every wait is bounded;
 // one that runs out flags RKV_DEVERR_TIMEOUT and stops every role.
 #include "rkv_q8_attend.cuh"
@@ -25,11 +25,11 @@ namespace rkv {
 namespace {
 
 constexpr int kQtKeys = 1 << kQtKeysShift;
-constexpr int kQtThreads = 512;
-// Registers: 512 threads start with 128 each; the softmax warps take 192, the third
-// warpgroup (TMA, MMA) 56 and the fourth 72: 256 x 192 + 128 x 56 + 128 x 72 = 512 x 128.
-constexpr int kQtSoftRegs = 192, kQtIssueRegs = 56, kQtCodeRegs = 72;
-static_assert(256 * kQtSoftRegs + 128 * (kQtIssueRegs + kQtCodeRegs) == 512 * 128,
+constexpr int kQtThreads = 640;
+// Registers: 640 threads start with 96 each; the softmax warps take 144, the third
+// warpgroup (TMA, MMA) 48 and the last two 72: 256 x 144 + 128 x 48 + 256 x 72 = 640 x 96.
+constexpr int kQtSoftRegs = 144, kQtIssueRegs = 48, kQtCodeRegs = 72;
+static_assert(256 * (kQtSoftRegs + kQtCodeRegs) + 128 * kQtIssueRegs == 640 * 96,
               "the split must be what the block was launched with");
 constexpr int kQtTile = kQtKeys * 256, kQtCodes = kQtKeys * 128;
 constexpr int kQtInfos = 8;     // tiles between the TMA and the softmax: at most six
@@ -39,11 +39,13 @@ constexpr int kNoRow = -128;    // a query row with a NaN or an infinity
 // are taken with the power of two below the factor, whose product with the maximum is exact.
 constexpr float kQtFar = 1073741824.f;
 
-// A tile's scales: each 16-key group's exponent below the tile's, the tiles', and which
-// groups were loaded.
+// A tile's scales, for K and for V from the warp that fetches its codes: each 16-key group's
+// exponent below `e`, and which groups were loaded.  e: K's tile's exponent; V's run's, up to
+// this tile, the unit of O (`unit`: the same from the warp of K, for the softmax, which does
+// not wait for V).
 struct TileInfo {
-  uint8_t k[8], v[8];
-  int16_t ek, ev;
+  uint8_t d[8];
+  int16_t e, unit;
   uint32_t groups;
 };
 
@@ -59,7 +61,7 @@ struct TileShape8 {
     uint8_t codes[kCodeSlots * kQtCodes];
     Line line;
     uint64_t full_c[kCodeSlots], empty_c[kCodeSlots], full[kTiles], empty[kTiles], s[2], p[2], o[2], qf[2], out[2], ml, drained;
-    TileInfo info[kQtInfos];
+    TileInfo info[2][kQtInfos];
     CausalRun first;  // the share's first run, worked out once
     long long x0, x1;
     uint32_t tmem_base;
@@ -72,21 +74,32 @@ struct TileShape8 {
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
-// The j-th of a run's 2 nt tiles of codes: K or V of which key tile.
-template <bool kWide>
-__device__ __forceinline__ void entry_of(int j, int nt, bool& v, int& i) {
-  if (kWide) {
-    v = j & 1;
-    i = j >> 1;
-  } else {  // K_0, then K_(i+1) and V_i for every i
-    v = j == 2 * nt - 1 || (j > 0 && !(j & 1));
-    i = j == 2 * nt - 1 ? nt - 1 : (v ? (j >> 1) - 1 : (j + 1) >> 1);
-  }
-}
+// Where K or V of key tile i lies among a run's 2 nt tiles of codes and operands: K_i then V_i
+// (kWide), or K_0, then K_(i+1) and V_i for every i.
 template <bool kWide>
 __device__ __forceinline__ int place_of(bool v, int i, int nt) {
   if (kWide) return 2 * i + v;
   return v ? (i + 1 < nt ? 2 * i + 2 : 2 * nt - 1) : (i > 0 ? 2 * i - 1 : 0);
+}
+
+// Two fp32 numbers in one 64-bit register, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pair_bits(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) { return pair_bits(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float pair_lo(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float pair_hi(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // 2^-d as a pair of fp16 numbers, d <= 24.
@@ -230,10 +243,10 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
             const int e = sh.row_exp[(kWide ? slot * 128 : 0) + row];
             factor = e == kNoRow ? __uint_as_float(0x7fffffffu) : p.scale_log2 * power_of_two(e - 8);
           }
-          const TileInfo& ti = sh.info[(tiles_before + i) % kQtInfos];
-          const int key0 = (r.lo + i) * kQtKeys, left = n - key0, to_unit = ti.ev;
+          const TileInfo& ti = sh.info[0][(tiles_before + i) % kQtInfos];
+          const int key0 = (r.lo + i) * kQtKeys, left = n - key0, to_unit = ti.unit;
           const uint32_t gr = ti.groups;
-          float sl = factor * power_of_two(ti.ek);
+          float sl = factor * power_of_two(ti.e);
           if (sl < kLowestScale) sl = kLowestScale;  // 0 x -inf is not -inf; a NaN stays
           const bool all = left >= kQtKeys && gr == 0xffu && key0 + kQtKeys <= least;
           uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
@@ -247,72 +260,88 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
               if (!((gr >> (2 * w + 1)) & 1u)) see[w] &= 0x0000ffffu;
             }
           }
-          uint32_t v[4][32];
-          float mx = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tc_ld32(mine + c * 32, v[c]);
-          tc_ld_wait();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tc_ld_done(v[c]);
+          auto hide = [&](uint32_t (&v)[32], int c) {
             if (!all) {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (!((see[c] >> j) & 1u)) v[c][j] = 0xff800000u;  // -inf
+                if (!((see[c] >> j) & 1u)) v[j] = 0xff800000u;  // -inf
             }
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              mx = max3(mx, __uint_as_float(v[c][j]), __uint_as_float(v[c][j + 1]));
-              mx1 = max3(mx1, __uint_as_float(v[c][j + 2]), __uint_as_float(v[c][j + 3]));
-            }
-          }
-          const float raw = fmaxf(mx, mx1);
-          mx = raw * sl;  // sl > 0
-          auto set_ref = [&]() {
-            far = fabsf(m) > kQtFar && m != kNoMax;
-            ref = far ? raw * __uint_as_float(__float_as_uint(sl) & 0x7f800000u) : m;
           };
-          if (first) {
-            m = fmaxf(kNoMax, mx);
-            set_ref();
-            unit = to_unit;
-          } else if (__any_sync(0xffffffffu, mx > m + kSlack || to_unit != unit)) {
-            // this slot's earlier products are complete: its logits were issued after them
-            const float to = fmaxf(m, mx), f = ex2_approx(m - to);
-            const float fo = f * power_of_two(max(unit - to_unit, -126));
-            unit = to_unit;
-            if (mx > m) {
-              m = to;
-              set_ref();
-            }
-            l *= f;
+          // The weights are taken with the maximum so far, without looking for a new one: as long
+          // as a row's 128 of them sum up to at most 2^8 (2^15 with their factor) none is beyond
+          // fp16, and a row whose maximum stays the same sums up to 2^7 at most.
+          uint32_t pk[2][32];
+          float sum;
+          for (bool moved = first;;) {
+            if (moved) {
+              float mx = -INFINITY, mx1 = -INFINITY;
 #pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t v[32];
+                tc_ld32_wait(mine + c * 32, v);
+                if (!all) {
+                  const uint32_t bits = c == 0 ? see[0] : (c == 1 ? see[1] : (c == 2 ? see[2] : see[3]));
+#pragma unroll
+                  for (int j = 0; j < 32; ++j)
+                    if (!((bits >> j) & 1u)) v[j] = 0xff800000u;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                  mx = max3(mx, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                  mx1 = max3(mx1, __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+                }
+              }
+              const float raw = fmaxf(mx, mx1);
+              mx = raw * sl;  // sl > 0
+              const float to = fmaxf(m, mx), f = ex2_approx(m - to);
+              if (first || mx > m) {
+                m = to;
+                far = fabsf(m) > kQtFar && m != kNoMax;
+                ref = far ? raw * __uint_as_float(__float_as_uint(sl) & 0x7f800000u) : m;
+              }
+              if (!first) {
+                // this slot's earlier products are complete: its logits were issued after them
+                const float fo = f * power_of_two(max(unit - to_unit, -126));
+                l *= f;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                  uint32_t o[32];
+                  tc_ld32_wait(mine + 128 + c * 32, o);
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fo);
+                  tc_st32_wait(mine + 128 + c * 32, o);
+                }
+              }
+              unit = to_unit;
+            }
+            const float by = far ? __uint_as_float(__float_as_uint(sl) & 0x7f800000u) : sl;
+            const uint64_t by2 = pair_of(by, by), sub2 = pair_of(7.f - ref, 7.f - ref);  // times kUnit
+            uint64_t s0 = pair_of(0.f, 0.f), s1 = s0;
+            uint32_t v[2][32];
+            tc_ld32(mine, v[0]);
+#pragma unroll
             for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tc_ld32_wait(mine + 128 + c * 32, o);
+              tc_ld_wait();
+              tc_ld_done(v[c & 1]);
+              if (c < 3) tc_ld32(mine + (c + 1) * 32, v[(c + 1) & 1]);
+              hide(v[c & 1], c);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fo);
-              tc_st32_wait(mine + 128 + c * 32, o);
+              for (int j = 0; j < 16; ++j) {
+                const uint64_t z = fma2(pair_bits(v[c & 1][2 * j], v[c & 1][2 * j + 1]), by2, sub2);
+                const float ax = ex2_approx(pair_lo(z)), ay = ex2_approx(pair_hi(z));
+                if (j & 1) s1 = add2(s1, pair_of(ax, ay)); else s0 = add2(s0, pair_of(ax, ay));
+                pk[c >> 1][(c & 1) * 16 + j] = pack_f16x2(ax, ay);
+              }
             }
+            s0 = add2(s0, s1);
+            sum = pair_lo(s0) + pair_hi(s0);
+            if (moved || !__any_sync(0xffffffffu, sum > 32768.f || to_unit != unit)) break;
+            moved = true;
           }
-          const float by = far ? __uint_as_float(__float_as_uint(sl) & 0x7f800000u) : sl, sub = ref - 7.f;  // times kUnit
-          float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int cc = c * 2 + (j >> 4), jj = (j & 15) * 2;
-              const float ax = ex2_approx(fmaf(__uint_as_float(v[cc][jj]), by, -sub));
-              const float ay = ex2_approx(fmaf(__uint_as_float(v[cc][jj + 1]), by, -sub));
-              (j & 1 ? u0 : s0) += ax;
-              (j & 1 ? u1 : s1) += ay;
-              pk[j] = pack_f16x2(ax, ay);
-            }
-            tc_st32(mine + c * 32, pk);
-          }
+          tc_st32(mine, pk[0]);
+          tc_st32(mine + 32, pk[1]);
           tc_st_wait();
-          l += (s0 + s1) + (u0 + u1);
+          l += sum;
           tc_fence_before();
           mbar_arrive(&sh.p[slot]);
         }
@@ -340,8 +369,8 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         l = a.y * f0 + c.y * f1;
         // a slot's unit is that of its last tile
         const int last0 = (nt - 1) & ~1, last1 = has[1] ? ((nt & 1) ? nt - 2 : nt - 1) : 0;
-        f0 *= power_of_two(max((int)sh.info[(tiles_before - nt + last0) % kQtInfos].ev - 7, -126));
-        if (has[1]) f1 *= power_of_two(max((int)sh.info[(tiles_before - nt + last1) % kQtInfos].ev - 7, -126));
+        f0 *= power_of_two(max((int)sh.info[0][(tiles_before - nt + last0) % kQtInfos].unit - 7, -126));
+        if (has[1]) f1 *= power_of_two(max((int)sh.info[0][(tiles_before - nt + last1) % kQtInfos].unit - 7, -126));
       }
       ++run;
       tc_fence_after();
@@ -424,16 +453,16 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
       bool ok = true;
       for (long long x = x0; ok && next_run(x, r); x = r.next) {
         const int b = r.b, g = r.g, n = r.n, nt = r.hi - r.lo;
-        // lane j: the tile's page j, and its scales (warp 8); loaded a tile ahead, so that the
-        // loads' latency stays off the ring
+        // lane j: the tile's page j and its scales; loaded ahead, so that the loads' latency stays
+        // off the ring
         auto page_of = [&](int tile) {
           const int pg = tile * pages + lane;
           return lane < pages && pg * p.P < n ? p.page_table[(size_t)b * p.max_pages + pg] : -1;
         };
         auto scales_of = [&](int phys, float& sk, float& sv) {
           sk = sv = 0.f;
-          if (!v && phys >= 0 && phys < p.num_phys) {
-            sk = p.k_scale[(size_t)phys * p.Hkv + g];
+          if (phys >= 0 && phys < p.num_phys) {
+            if (!v) sk = p.k_scale[(size_t)phys * p.Hkv + g];
             sv = p.v_scale[(size_t)phys * p.Hkv + g];
           }
         };
@@ -455,28 +484,24 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
             phys = -1;
           }
           const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0);
-          if (!v) {
-            // exponents; 255: NaN (a scale is positive)
-            const int xk = (int)(__float_as_uint(sk) >> 23) & 255, xv = (int)(__float_as_uint(sv) >> 23) & 255;
-            const bool in = phys >= 0;
-            const int ek = __reduce_max_sync(0xffffffffu, in && xk < 255 ? xk : 1) - 127;
-            unit = max(unit, __reduce_max_sync(0xffffffffu, in && xv < 255 ? xv : 1) - 127);
-            TileInfo& ti = sh.info[(tiles_before + i) % kQtInfos];
-            if (lane < pages)
-              for (int j = 0; j < per_page; ++j) {
-                ti.k[lane * per_page + j] = (uint8_t)(xk == 255 ? kNoFactor : min(max(ek - (xk - 127), 0), 254));
-                ti.v[lane * per_page + j] = (uint8_t)(xv == 255 ? kNoFactor : min(max(unit - (xv - 127), 0), 254));
-              }
-            if (lead) {
-              uint32_t gr = 0;
-              for (int j = 0; j < pages; ++j)
-                if ((have >> j) & 1u) gr |= ((1u << per_page) - 1u) << (j * per_page);
-              ti.groups = gr;
-              ti.ek = (int16_t)ek;
-              ti.ev = (int16_t)unit;
-            }
-            __syncwarp();
+          // exponents; 255: NaN (a scale is positive)
+          const int xk = (int)(__float_as_uint(sk) >> 23) & 255, xv = (int)(__float_as_uint(sv) >> 23) & 255;
+          unit = max(unit, __reduce_max_sync(0xffffffffu, phys >= 0 && xv < 255 ? xv : 1) - 127);
+          const int ek = __reduce_max_sync(0xffffffffu, phys >= 0 && xk < 255 ? xk : 1) - 127;
+          TileInfo& ti = sh.info[v][(tiles_before + i) % kQtInfos];
+          const int mx = v ? xv : xk, me = v ? unit : ek;
+          if (lane < pages)
+            for (int j = 0; j < per_page; ++j)
+              ti.d[lane * per_page + j] = (uint8_t)(mx == 255 ? kNoFactor : min(max(me - (mx - 127), 0), 254));
+          if (lead) {
+            uint32_t gr = 0;
+            for (int j = 0; j < pages; ++j)
+              if ((have >> j) & 1u) gr |= ((1u << per_page) - 1u) << (j * per_page);
+            ti.groups = gr;
+            ti.e = (int16_t)me;
+            ti.unit = (int16_t)unit;
           }
+          __syncwarp();
           uint8_t* const st = sh.codes + c * kQtCodes;
           if (lead) {
             if (have) mbar_arrive_expect_tx(&sh.full_c[c], __popc(have) * box);
@@ -586,23 +611,22 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         for (int i = loaded > E ? loaded - E : 0; i < loaded; ++i) mbar_wait(&sh.empty[i % E], (uint32_t)((i / E) & 1));
     }
   } else {
-    // codes to fp16: a warp's 32 keys of a tile, four keys of eight 16-code pieces at a time
+    // codes to fp16, K's (warps 12-15) and V's: a warp's 32 keys of a tile, four keys of eight
+    // 16-code pieces at a time
     setmaxnreg_dec<kQtCodeRegs>();
-    const int quarter = warp - 12, sub = lane >> 3, piece = lane & 7;
+    const bool v = warp >= 16;
+    const int quarter = warp & 3, sub = lane >> 3, piece = lane & 7;
     int before = 0, tiles_before = 0;
     bool ok = true;
     for (long long x = x0; ok && next_run(x, r); x = r.next) {
       const int nt = r.hi - r.lo;
-      for (int j = 0; j < 2 * nt; ++j) {
-        bool v;
-        int i;
-        entry_of<kWide>(j, nt, v, i);
-        const int at = before + j, c = at % C, e = at % E;
+      for (int i = 0; i < nt; ++i) {
+        const int at = before + place_of<kWide>(v, i, nt), c = at % C, e = at % E;
         if (!(ok = wait(&sh.full_c[c], at / C))) break;
-        const TileInfo& ti = sh.info[(tiles_before + i) % kQtInfos];
+        const TileInfo& ti = sh.info[v][(tiles_before + i) % kQtInfos];
         const int left = r.n - (r.lo + i) * kQtKeys;
         const uint32_t gr = ti.groups;
-        const int d0 = v ? ti.v[quarter * 2] : ti.k[quarter * 2], d1 = v ? ti.v[quarter * 2 + 1] : ti.k[quarter * 2 + 1];
+        const int d0 = ti.d[quarter * 2], d1 = ti.d[quarter * 2 + 1];
         const uint8_t* const src = sh.codes + c * kQtCodes;
         uint4 w[8];
 #pragma unroll
