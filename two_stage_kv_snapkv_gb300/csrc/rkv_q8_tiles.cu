@@ -1,10 +1,10 @@
 // Attention over the 8-bit cache for many query rows, on the fifth-generation tensor cores
 // (formulas and what is rounded: rkv_q8_attend.cu).
 //
-// Two row slots of 128 rows work in turn on 128-key tiles: while a slot's four warps turn its
+// Two row slots of 128 rows work in turn on 128-key tiles: while a slot's eight warps turn its
 // logits into weights, the tensor cores run the other slot's products.
 //   S = Q K^T   128 x 128 x 128, fp16, both operands in shared memory, S in TMEM;
-//   P           fp16, written back over S's columns (thread = row = TMEM lane);
+//   P           fp16, written back over S's columns (TMEM lane = row; two threads a row, 64 keys each);
 //   O += P V    128 x 128 x 128, P from TMEM, V from shared memory, O in TMEM.
 // kWide: a unit's tile is 256 rows, the slots hold different rows and both use every key
 // tile.  Otherwise the tile is 128 rows and the slots take alternate key tiles of the same
@@ -15,8 +15,8 @@
 // largest and joins the logits, V's is the largest of the run so far, the unit of O (where
 // it grows, O is scaled down with the maximum's move).  A code times such a factor is exact
 // but where it falls below fp16's smallest step, 2^-33 of the largest.
-//   warps 0-3, 4-7: softmax of slot 0, 1;  8, 10: TMA of K, V;  9: MMA issue;  11: idle;
-//   12-15, 16-19: K's and V's codes to fp16.
+//   warps 0-7, 8-15: softmax of slot 0, 1 (four warps to 64 keys);  16, 18: TMA of K, V;  17:
+//   MMA issue;  19: idle;  20-23, 24-27: K's and V's codes to fp16.
 // Order and phases of both rings are the same formula in every role.  Every wait is bounded;
 // one that runs out flags RKV_DEVERR_TIMEOUT and stops every role.
 #include "rkv_q8_attend.cuh"
@@ -25,11 +25,11 @@ namespace rkv {
 namespace {
 
 constexpr int kQtKeys = 1 << kQtKeysShift;
-constexpr int kQtThreads = 640;
-// Registers: 640 threads start with 96 each; the softmax warps take 144, the third
-// warpgroup (TMA, MMA) 48 and the last two 72: 256 x 144 + 128 x 48 + 256 x 72 = 640 x 96.
-constexpr int kQtSoftRegs = 144, kQtIssueRegs = 48, kQtCodeRegs = 72;
-static_assert(256 * (kQtSoftRegs + kQtCodeRegs) + 128 * kQtIssueRegs == 640 * 96,
+constexpr int kQtThreads = 896;
+// Registers: 896 threads start with 72 each; the softmax warps take 80, the fifth warpgroup
+// (TMA, MMA) 56 and the last two 64: 512 x 80 + 128 x 56 + 256 x 64 = 896 x 72.
+constexpr int kQtSoftRegs = 80, kQtIssueRegs = 56, kQtCodeRegs = 64;
+static_assert(512 * kQtSoftRegs + 128 * kQtIssueRegs + 256 * kQtCodeRegs == 896 * 72,
               "the split must be what the block was launched with");
 constexpr int kQtTile = kQtKeys * 256, kQtCodes = kQtKeys * 128;
 constexpr int kQtInfos = 8;     // tiles between the TMA and the softmax: at most six
@@ -53,7 +53,7 @@ template <bool kWide>
 struct TileShape8 {
   static constexpr int kRows = kWide ? 256 : 128;
   static constexpr int kQBytes = kRows * 256;
-  static constexpr int kTiles = kWide ? 4 : 3, kCodeSlots = kWide ? 2 : 5;
+  static constexpr int kTiles = 3, kCodeSlots = kWide ? 4 : 5;
   using Line = TileLine<kWide ? 8 : 7>;
   struct Shared {
     uint8_t q[kQBytes];
@@ -68,7 +68,7 @@ struct TileShape8 {
     int abort_flag;
     bool any;
     int8_t row_exp[kRows];
-    float2 ml_s[kWide ? 1 : 2][kWide ? 1 : 128];
+    float2 ml_s[kWide ? 1 : 4][kWide ? 1 : 128];
   };
   static constexpr int kSmem = sizeof(Shared);
   static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -128,12 +128,12 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh.s[s], 2);  // the issuing thread and its commit
-      mbar_init(&sh.p[s], 128);
+      mbar_init(&sh.p[s], 8);  // a lane of each warp
       mbar_init(&sh.o[s], 1);
-      mbar_init(&sh.qf[s], kWide ? 128 : 256);
-      mbar_init(&sh.out[s], kWide ? 128 : 256);
+      mbar_init(&sh.qf[s], kWide ? 8 : 16);
+      mbar_init(&sh.out[s], kWide ? 8 : 16);
     }
-    mbar_init(&sh.ml, 256);
+    mbar_init(&sh.ml, 16);
     mbar_init(&sh.drained, 1);
     abort_flag = 0;
     fence_mbar_init();
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
     prefetch_map(&p.tmk);
     prefetch_map(&p.tmv);
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(&sh.tmem_base, 512);
     tmem_relinquish();
   }
@@ -181,15 +181,33 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
     }
     return true;
   };
-  int loaded = 0;  // one past the last tile of codes asked for (warps 8, 10), of operands used (warp 9)
+  // every lane of the warp is done with something: one arrival (32 of them on one barrier are
+  // 32 turns)
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  int loaded = 0;  // one past the last tile of codes asked for (warps 16, 18), of operands used (warp 17)
   CausalRun r;
 
-  if (warp < 8) {
+  if (warp < 16) {
     setmaxnreg_inc<kQtSoftRegs>();
-    const int slot = warp >> 2, row = tid & 127;
-    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), mine = lanes + slot * 256;
+    const int slot = warp >> 3, half = (warp >> 2) & 1, row = tid & 127, pr = slot * 4 + (warp & 3);
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), mine = lanes + slot * 256, keys = mine + half * 64;
     int seen_s = 0, run = 0, done[2] = {0, 0}, tiles_before = 0;
     bool ok = true;
+    // The two warps that share 32 rows meet: whether either says yes.  A hardware barrier of
+    // their own (the wait on a shared-memory one took 250 clocks a tile); a warp that gives up
+    // arrives once more on its way out, so that the other one is never left waiting.
+    auto vote = [&](bool yes) {
+      uint32_t any;
+      asm volatile(
+          "{\n .reg .pred a, b;\n setp.ne.b32 a, %1, 0;\n barrier.cta.red.or.pred b, %2, 64, a;\n selp.u32 %0, 1, 0, b;\n}\n"
+          : "=r"(any)
+          : "r"((uint32_t)yes), "r"(pr + 1)
+          : "memory");
+      return any != 0;
+    };
     for (long long x = x0; ok && next_run(x, r); x = r.next) {
       const int b = r.b, g = r.g, rt = r.rt, n = r.n, rows = r.m * p.G, nt = r.hi - r.lo;
       const bool idle = kWide && slot == 1 && rows - rt * R <= 128;
@@ -197,19 +215,19 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
       if (run > 0 && !(ok = wait(&sh.out[kWide ? slot : 0], run - 1))) break;
       {
         constexpr int kPer = kWide ? 128 : 64;  // rows this slot's warps load
-        const int q0 = kWide ? 0 : slot * 64;
+        const int q0 = kWide ? 0 : slot * 64, t = tid & 255;
         uint8_t* dst = sh.q + (kWide ? slot * (128 * 256) : 0);
-        const int piece = row & 15;
-        uint4 v[kPer / 8];  // all loads in flight together
+        const int piece = t & 15;
+        uint4 v[kPer / 16];  // all loads in flight together
 #pragma unroll
-        for (int j = 0; j < kPer / 8; ++j) {
-          const int rr = rt * R + (kWide ? slot * 128 : 0) + q0 + (row >> 4) + j * 8;
+        for (int j = 0; j < kPer / 16; ++j) {
+          const int rr = rt * R + (kWide ? slot * 128 : 0) + q0 + (t >> 4) + j * 16;
           v[j] = make_uint4(0, 0, 0, 0);
           if (rr < rows) v[j] = reinterpret_cast<const uint4*>(p.q + out_row(p, b, g, rr) * 128)[piece];
         }
 #pragma unroll
-        for (int j = 0; j < kPer / 8; ++j) {
-          const int i = q0 + (row >> 4) + j * 8;
+        for (int j = 0; j < kPer / 16; ++j) {
+          const int i = q0 + (t >> 4) + j * 16;
           uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
           uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
                                   __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
@@ -225,7 +243,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
           if (piece == 0) sh.row_exp[(kWide ? slot * 128 : 0) + i] = (int8_t)(top >= 0x7f80u ? kNoRow : e);
         }
         fence_proxy_async_smem();
-        mbar_arrive(&sh.qf[kWide ? slot : 0]);
+        arrive(&sh.qf[kWide ? slot : 0]);
       }
       const int my = rt * R + (kWide ? slot * 128 : 0) + row;  // this thread's query row
       // keys that it sees, and that the slot's first row does
@@ -244,54 +262,45 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
             factor = e == kNoRow ? __uint_as_float(0x7fffffffu) : p.scale_log2 * power_of_two(e - 8);
           }
           const TileInfo& ti = sh.info[0][(tiles_before + i) % kQtInfos];
-          const int key0 = (r.lo + i) * kQtKeys, left = n - key0, to_unit = ti.unit;
+          const int key0 = (r.lo + i) * kQtKeys, to_unit = ti.unit;
           const uint32_t gr = ti.groups;
           float sl = factor * power_of_two(ti.e);
           if (sl < kLowestScale) sl = kLowestScale;  // 0 x -inf is not -inf; a NaN stays
-          const bool all = left >= kQtKeys && gr == 0xffu && key0 + kQtKeys <= least;
-          uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+          const bool all = gr == 0xffu && key0 + kQtKeys <= min(least, n);
+          uint32_t see[2] = {~0u, ~0u};  // of this thread's 64 keys
           if (!all) {
-            const int mine_left = min(left, lim - key0);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int k = mine_left - w * 32;
+            for (int w = 0; w < 2; ++w) {
+              const int k = min(n, lim) - key0 - half * 64 - w * 32;
               see[w] = k >= 32 ? ~0u : (k <= 0 ? 0u : (1u << k) - 1u);
-              if (!((gr >> (2 * w)) & 1u)) see[w] &= 0xffff0000u;
-              if (!((gr >> (2 * w + 1)) & 1u)) see[w] &= 0x0000ffffu;
+              if (!((gr >> (half * 4 + 2 * w)) & 1u)) see[w] &= 0xffff0000u;
+              if (!((gr >> (half * 4 + 2 * w + 1)) & 1u)) see[w] &= 0x0000ffffu;
             }
           }
-          auto hide = [&](uint32_t (&v)[32], int c) {
-            if (!all) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!((see[c] >> j) & 1u)) v[j] = 0xff800000u;  // -inf
-            }
-          };
           // The weights are taken with the maximum so far, without looking for a new one: as long
-          // as a row's 128 of them sum up to at most 2^8 (2^15 with their factor) none is beyond
-          // fp16, and a row whose maximum stays the same sums up to 2^7 at most.
-          uint32_t pk[2][32];
+          // as 64 of a row's sum up to at most 2^8 (2^15 with their factor) none is beyond fp16,
+          // and while the maximum stays the same they sum up to 2^6 at most.
+          uint32_t pk[32];
           float sum;
           for (bool moved = first;;) {
             if (moved) {
-              float mx = -INFINITY, mx1 = -INFINITY;
+              // the maximum of all 128 logits, by both threads of the row
+              float mx = -INFINITY;
 #pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                uint32_t v[32];
-                tc_ld32_wait(mine + c * 32, v);
+              for (int c = 0; c < 8; ++c) {
+                uint32_t v[16];
+                tc_ld16_wait(mine + c * 16, v);
                 if (!all) {
-                  const uint32_t bits = c == 0 ? see[0] : (c == 1 ? see[1] : (c == 2 ? see[2] : see[3]));
+                  const int k = min(n, lim) - key0 - c * 16;
+                  const uint32_t bits = ((gr >> c) & 1u) ? (k >= 16 ? ~0u : (k <= 0 ? 0u : (1u << k) - 1u)) : 0u;
 #pragma unroll
-                  for (int j = 0; j < 32; ++j)
-                    if (!((bits >> j) & 1u)) v[j] = 0xff800000u;
+                  for (int j = 0; j < 16; ++j)
+                    if (!((bits >> j) & 1u)) v[j] = 0xff800000u;  // -inf
                 }
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                  mx = max3(mx, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-                  mx1 = max3(mx1, __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
-                }
+                for (int j = 0; j < 16; j += 2) mx = max3(mx, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
               }
-              const float raw = fmaxf(mx, mx1);
+              const float raw = mx;
               mx = raw * sl;  // sl > 0
               const float to = fmaxf(m, mx), f = ex2_approx(m - to);
               if (first || mx > m) {
@@ -305,11 +314,11 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
                 l *= f;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-                  uint32_t o[32];
-                  tc_ld32_wait(mine + 128 + c * 32, o);
+                  uint32_t o[16];
+                  tc_ld16_wait(mine + 128 + half * 64 + c * 16, o);
 #pragma unroll
-                  for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fo);
-                  tc_st32_wait(mine + 128 + c * 32, o);
+                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fo);
+                  tc_st16_wait(mine + 128 + half * 64 + c * 16, o);
                 }
               }
               unit = to_unit;
@@ -317,56 +326,66 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
             const float by = far ? __uint_as_float(__float_as_uint(sl) & 0x7f800000u) : sl;
             const uint64_t by2 = pair_of(by, by), sub2 = pair_of(7.f - ref, 7.f - ref);  // times kUnit
             uint64_t s0 = pair_of(0.f, 0.f), s1 = s0;
-            uint32_t v[2][32];
-            tc_ld32(mine, v[0]);
+            uint32_t v[2][16];
+            tc_ld16(keys, v[0]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               tc_ld_wait();
-              tc_ld_done(v[c & 1]);
-              if (c < 3) tc_ld32(mine + (c + 1) * 32, v[(c + 1) & 1]);
-              hide(v[c & 1], c);
+              tc_ld16_done(v[c & 1]);
+              if (c < 3) tc_ld16(keys + (c + 1) * 16, v[(c + 1) & 1]);
+              if (!all) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
+                for (int j = 0; j < 16; ++j)
+                  if (!((see[c >> 1] >> ((c & 1) * 16 + j)) & 1u)) v[c & 1][j] = 0xff800000u;
+              }
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
                 const uint64_t z = fma2(pair_bits(v[c & 1][2 * j], v[c & 1][2 * j + 1]), by2, sub2);
                 const float ax = ex2_approx(pair_lo(z)), ay = ex2_approx(pair_hi(z));
                 if (j & 1) s1 = add2(s1, pair_of(ax, ay)); else s0 = add2(s0, pair_of(ax, ay));
-                pk[c >> 1][(c & 1) * 16 + j] = pack_f16x2(ax, ay);
+                pk[c * 8 + j] = pack_f16x2(ax, ay);
               }
             }
             s0 = add2(s0, s1);
             sum = pair_lo(s0) + pair_hi(s0);
-            if (moved || !__any_sync(0xffffffffu, sum > 32768.f || to_unit != unit)) break;
+            // in the second round: neither thread of the row writes over logits that the other
+            // still looks for their maximum in
+            if (!vote(!moved && (sum > 32768.f || to_unit != unit))) break;
             moved = true;
           }
-          tc_st32(mine, pk[0]);
-          tc_st32(mine + 32, pk[1]);
+          tc_st32(keys, pk);
           tc_st_wait();
           l += sum;
           tc_fence_before();
-          mbar_arrive(&sh.p[slot]);
+          arrive(&sh.p[slot]);
         }
       }
       if (!ok) break;
       tiles_before += nt;
       l *= 1.f / kUnit;
-      float fo = power_of_two(max(unit - 7, -126));  // O's unit, with the weights'
       // the run's end: out = O / l (whole unit) or the part (m, l, O)
       const bool has[2] = {true, kWide ? true : nt > 1};
-      float f0 = fo, f1 = 0.f;
+      float f0 = power_of_two(max(unit - 7, -126)), f1 = 0.f;  // O's unit, with the weights'
       if (kWide) {
         if (!(ok = wait(&sh.o[slot], done[slot]++))) break;
+        // the other thread's sum, through the query tile's upper half (its products are done)
+        float* const sums = reinterpret_cast<float*>(sh.q + slot * 32768 + 16384);
+        sums[half * 128 + row] = l;
+        vote(false);
+        l += sums[(half ^ 1) * 128 + row];
       } else {
         // both slots' sums, and their outputs' factors to the joint maximum
-        sh.ml_s[slot][row] = make_float2(m, l);
-        mbar_arrive(&sh.ml);
+        sh.ml_s[slot * 2 + half][row] = make_float2(m, l);
+        arrive(&sh.ml);
         if (!(ok = wait(&sh.ml, run))) break;
         if (!(ok = wait(&sh.o[0], done[0]++))) break;
         if (has[1] && !(ok = wait(&sh.o[1], done[1]++))) break;
-        const float2 a = sh.ml_s[0][row], c = has[1] ? sh.ml_s[1][row] : make_float2(kNoMax, 0.f);
+        const float2 a = sh.ml_s[0][row], c = has[1] ? sh.ml_s[2][row] : make_float2(kNoMax, 0.f);
+        const float la = a.y + sh.ml_s[1][row].y, lc = has[1] ? c.y + sh.ml_s[3][row].y : 0.f;
         m = fmaxf(a.x, c.x);
         f0 = ex2_approx(a.x - m);
         f1 = ex2_approx(c.x - m);
-        l = a.y * f0 + c.y * f1;
+        l = la * f0 + lc * f1;
         // a slot's unit is that of its last tile
         const int last0 = (nt - 1) & ~1, last1 = has[1] ? ((nt & 1) ? nt - 2 : nt - 1) : 0;
         f0 *= power_of_two(max((int)sh.info[0][(tiles_before - nt + last0) % kQtInfos].unit - 7, -126));
@@ -381,70 +400,70 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         f1 *= inv;
         const size_t orow = live ? out_row(p, b, g, my) : 0;
         const size_t prow = (2 * (size_t)blockIdx.x + (r.first ? 0 : 1)) * R + (kWide ? slot * 128 : 0) + row;
-        // kWide: all 128 channels of this slot's row; else 64 channels of both slots' O.  32
-        // channels of the warp's 32 rows at a time go through the query tile's memory (its
-        // products are done), so that the stores are whole 128-byte (bf16: 64-byte) pieces
-        // of rows and not 16 bytes of 32 rows each.
+        // kWide: 64 channels of this slot's row; else 32 channels of both slots' O.  16 channels
+        // of the warp's 32 rows at a time go through the query tile's memory, so that the stores
+        // are 64-byte (bf16: 32-byte) pieces of rows and not 16 bytes of 32 rows each.
         constexpr int kChunks = kWide ? 4 : 2;
-        uint8_t* const stage = sh.q + slot * (kWide ? 32768 : 16384) + (warp & 3) * 4096;
+        uint8_t* const stage = kWide ? sh.q + slot * 32768 + (warp & 7) * 2048 : sh.q + warp * 2048;
         const int row0 = rt * R + (kWide ? slot * 128 : 0) + (warp & 3) * 32;  // the warp's first query row
         const size_t prow0 = prow - lane;
 #pragma unroll 1
         for (int cc = 0; cc < kChunks; ++cc) {
-          const int c = kWide ? cc : slot * 2 + cc;
-          uint32_t o[32];
-          tc_ld32_wait(kWide ? mine + 128 + c * 32 : lanes + 128 + c * 32, o);
+          const int c = kWide ? half * 4 + cc : (slot * 2 + half) * 2 + cc;
+          uint32_t o[16];
+          tc_ld16_wait(kWide ? mine + 128 + c * 16 : lanes + 128 + c * 16, o);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
+          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
           if (!kWide && has[1]) {
-            uint32_t o1[32];
-            tc_ld32_wait(lanes + 256 + 128 + c * 32, o1);
+            uint32_t o1[16];
+            tc_ld16_wait(lanes + 256 + 128 + c * 16, o1);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j])));
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j])));
           }
           __syncwarp();  // the staged piece before this one is read
           if (r.whole) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 w[e] = pack_bf16x2(__uint_as_float(o[j * 8 + 2 * e]), __uint_as_float(o[j * 8 + 2 * e + 1]));
-              *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(stage + lane * 32 + ((j ^ ((lane >> 2) & 1)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int i = k * 16 + (lane >> 1), j = lane & 1;
+              const uint4 w = *reinterpret_cast<const uint4*>(stage + i * 32 + ((j ^ ((i >> 2) & 1)) << 4));
+              if (row0 + i < rows) reinterpret_cast<uint4*>(p.out + out_row(p, b, g, row0 + i) * 128 + c * 16)[j] = w;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(o[j * 4], o[j * 4 + 1], o[j * 4 + 2], o[j * 4 + 3]);
             __syncwarp();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int i = k * 8 + (lane >> 2), j = lane & 3;
               const uint4 w = *reinterpret_cast<const uint4*>(stage + i * 64 + ((j ^ ((i >> 1) & 3)) << 4));
-              if (row0 + i < rows) reinterpret_cast<uint4*>(p.out + out_row(p, b, g, row0 + i) * 128 + c * 32)[j] = w;
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                  make_uint4(o[j * 4], o[j * 4 + 1], o[j * 4 + 2], o[j * 4 + 3]);
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int i = k * 4 + (lane >> 3), j = lane & 7;
-              const uint4 w = *reinterpret_cast<const uint4*>(stage + i * 128 + ((j ^ (i & 7)) << 4));
-              if (row0 + i < rows) reinterpret_cast<uint4*>(p.part_o + (prow0 + i) * 128 + c * 32)[j] = w;
+              if (row0 + i < rows) reinterpret_cast<uint4*>(p.part_o + (prow0 + i) * 128 + c * 16)[j] = w;
             }
           }
         }
-        if (live && (kWide || slot == 0)) {
+        if (live && half == 0 && (kWide || slot == 0)) {
           if (!r.whole) p.part_ml[prow] = make_float2(m, l);
           else if (p.lse) p.lse[orow] = lse_of(m, l);
         }
         tc_fence_before();  // O is read before the next run's queries let its products start
       }
-      mbar_arrive(&sh.out[kWide ? slot : 0]);  // this thread has read what it staged
+      arrive(&sh.out[kWide ? slot : 0]);  // this thread has read what it staged
     }
-  } else if (warp < 12) {
+    if (!ok) asm volatile("barrier.cta.arrive %0, 64;\n" ::"r"(pr + 1) : "memory");
+  } else if (warp < 20) {
     setmaxnreg_dec<kQtIssueRegs>();
-    if (warp == 8 || warp == 10) {
-      const bool v = warp == 10;
+    if (warp == 16 || warp == 18) {
+      const bool v = warp == 18;
       const CUtensorMap* map = v ? &p.tmv : &p.tmk;
       const bool lead = elect_lane();
       const int pages = kQtKeys >> p.pshift, box = p.P * 128, per_page = p.P >> 4;  // of a tile; bytes; 16-key groups
@@ -518,7 +537,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         before += 2 * nt;
         tiles_before += nt;
       }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
       constexpr uint32_t idesc_s = idesc_f16_f32(128, 128), idesc_o = idesc_s | kIdescBNMajor;
       const uint32_t q32 = smem_u32(sh.q), ring32 = smem_u32(sh.tiles);
       int seen_p[2] = {0, 0}, runs[2] = {0, 0};
@@ -547,7 +566,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         const uint32_t d = tmem + slot * 256 + 128, pa = tmem + slot * 256, va = vlo + e * (kQtTile >> 4);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          tc_mma_ts(lead, d, pa + k * 8, va + (k * 2048 >> 4), idesc_o, (first && k == 0) ? 0u : 1u);
+          tc_mma_ts(lead, d, pa + (k >> 2) * 64 + (k & 3) * 8, va + (k * 2048 >> 4), idesc_o, (first && k == 0) ? 0u : 1u);
         tc_commit_if(lead && release, &sh.empty[e]);
         tc_commit_if(lead && last, &sh.o[slot]);
       };
@@ -611,10 +630,10 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         for (int i = loaded > E ? loaded - E : 0; i < loaded; ++i) mbar_wait(&sh.empty[i % E], (uint32_t)((i / E) & 1));
     }
   } else {
-    // codes to fp16, K's (warps 12-15) and V's: a warp's 32 keys of a tile, four keys of eight
+    // codes to fp16, K's (warps 20-23) and V's: a warp's 32 keys of a tile, four keys of eight
     // 16-code pieces at a time
     setmaxnreg_dec<kQtCodeRegs>();
-    const bool v = warp >= 16;
+    const bool v = warp >= 24;
     const int quarter = warp & 3, sub = lane >> 3, piece = lane & 7;
     int before = 0, tiles_before = 0;
     bool ok = true;
@@ -699,15 +718,15 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
   tc_fence_before();
   __syncthreads();
   if (abort_flag) {
-    if ((warp == 8 || warp == 10) && lane == 0)
+    if ((warp == 16 || warp == 18) && lane == 0)
       for (int i = loaded > C ? loaded - C : 0; i < loaded; ++i) mbar_wait(&sh.full_c[i % C], (uint32_t)((i / C) & 1));
-    if (warp == 9) {  // everything this lane issued before the commit has completed when it arrives
+    if (warp == 17) {  // everything this lane issued before the commit has completed when it arrives
       tc_commit_if(elect_lane(), &sh.drained);
       mbar_wait(&sh.drained, 0);
     }
     __syncthreads();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
