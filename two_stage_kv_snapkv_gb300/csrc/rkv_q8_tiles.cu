@@ -26,9 +26,9 @@ namespace {
 
 constexpr int kQtKeys = 1 << kQtKeysShift;
 constexpr int kQtThreads = 896;
-// Registers: 896 threads start with 72 each; the softmax warps take 80, the fifth warpgroup
-// (TMA, MMA) 56 and the last two 64: 512 x 80 + 128 x 56 + 256 x 64 = 896 x 72.
-constexpr int kQtSoftRegs = 80, kQtIssueRegs = 56, kQtCodeRegs = 64;
+// Registers: 896 threads start with 72 each; the softmax warps take 88, the fifth warpgroup
+// (TMA, MMA) 56 and the last two 48: 512 x 88 + 128 x 56 + 256 x 48 = 896 x 72.
+constexpr int kQtSoftRegs = 88, kQtIssueRegs = 56, kQtCodeRegs = 48;
 static_assert(512 * kQtSoftRegs + 128 * kQtIssueRegs + 256 * kQtCodeRegs == 896 * 72,
               "the split must be what the block was launched with");
 constexpr int kQtTile = kQtKeys * 256, kQtCodes = kQtKeys * 128;
@@ -647,14 +647,6 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         const uint32_t gr = ti.groups;
         const int d0 = ti.d[quarter * 2], d1 = ti.d[quarter * 2 + 1];
         const uint8_t* const src = sh.codes + c * kQtCodes;
-        uint4 w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int row = quarter * 32 + k * 4 + sub;
-          w[k] = *reinterpret_cast<const uint4*>(src + row * 128 + ((piece ^ (row & 7)) << 4));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty_c[c]);  // the codes are in registers
         if (at >= E && !(ok = wait(&sh.empty[e], at / E - 1))) break;
         uint8_t* const dst = sh.tiles + e * kQtTile + (piece >> 2) * (kQtTile / 2);
         auto put = [&](int row, const uint32_t (&a)[4], const uint32_t (&c4)[4]) {
@@ -664,30 +656,40 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
               make_uint4(c4[0], c4[1], c4[2], c4[3]);
         };
         // one branch for the whole tile: in the unrolled loop, a few of them cost 430 clocks a key row
-        if (max(d0, d1) <= 9 && (!v || (left >= kQtKeys && gr == 0xffu))) {
-          // a factor of 2^-9 keeps -1152 f an fp16 number
-          const __half2 f[2] = {half_power(d0), half_power(d1)};
-          const __half2 bias[2] = {__hmul2(f[0], __float2half2_rn(-1152.f)), __hmul2(f[1], __float2half2_rn(-1152.f))};
+        const bool plain = max(d0, d1) <= 9 && (!v || (left >= kQtKeys && gr == 0xffu));
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            uint32_t a[4], c4[4];
-            decode4_times<kFormat>(w[k].x, f[k >> 2], bias[k >> 2], a[0], a[1]);
-            decode4_times<kFormat>(w[k].y, f[k >> 2], bias[k >> 2], a[2], a[3]);
-            decode4_times<kFormat>(w[k].z, f[k >> 2], bias[k >> 2], c4[0], c4[1]);
-            decode4_times<kFormat>(w[k].w, f[k >> 2], bias[k >> 2], c4[2], c4[3]);
-            put(quarter * 32 + k * 4 + sub, a, c4);
+        for (int h = 0; h < 2; ++h) {  // the warp's two 16-key groups
+          const int d = h ? d1 : d0, row0 = quarter * 32 + h * 16 + sub;
+          uint4 w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = row0 + k * 4;
+            w[k] = *reinterpret_cast<const uint4*>(src + row * 128 + ((piece ^ (row & 7)) << 4));
           }
-        } else {
-          // scales far apart, a page of NaN, or values that are not there: those, and a page of
-          // NaN's (whoever sees it has NaN logits), may be anything, and 0 x NaN is not 0
+          if (h == 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.empty_c[c]);  // the codes are in registers
+          }
+          if (plain) {
+            // a factor of 2^-9 keeps -1152 f an fp16 number
+            const __half2 f = half_power(d), bias = __hmul2(f, __float2half2_rn(-1152.f));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int d = h ? d1 : d0;
+            for (int k = 0; k < 4; ++k) {
+              uint32_t a[4], c4[4];
+              decode4_times<kFormat>(w[k].x, f, bias, a[0], a[1]);
+              decode4_times<kFormat>(w[k].y, f, bias, a[2], a[3]);
+              decode4_times<kFormat>(w[k].z, f, bias, c4[0], c4[1]);
+              decode4_times<kFormat>(w[k].w, f, bias, c4[2], c4[3]);
+              put(row0 + k * 4, a, c4);
+            }
+          } else {
+            // scales far apart, a page of NaN, or values that are not there: those, and a page of
+            // NaN's (whoever sees it has NaN logits), may be anything, and 0 x NaN is not 0
             const __half2 f = d == kNoFactor ? __half2half2(__ushort_as_half(0x7fff)) : half_power(min(d, 14));
             const __half2 f2 = half_power(d == kNoFactor ? 0 : min(max(d - 14, 0), 24));
 #pragma unroll
-            for (int k = h * 4; k < h * 4 + 4; ++k) {
-              const int row = quarter * 32 + k * 4 + sub;
+            for (int k = 0; k < 4; ++k) {
+              const int row = row0 + k * 4;
               const bool none = v && (row >= left || d == kNoFactor || !((gr >> (row >> 4)) & 1u));
               uint32_t a[4], c4[4];
               decode4<kFormat>(w[k].x, a[0], a[1]);
