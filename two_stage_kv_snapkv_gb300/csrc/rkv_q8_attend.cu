@@ -15,12 +15,14 @@
 //             unrounded.
 // ks joins the logits behind the product and vs the weights, so neither costs a pass over codes.
 //
-// q8_rows: 8 or 16 query rows against 32-key chunks, keys and channels on the MMA's M.  A
-// chunk's codes are 8 KB for 2 x 32 x 128 x 8 (or 16) multiply-adds, so the cache's bytes bound
+// q8_rows: 8 to 32 query rows against 32-key chunks, keys and channels on the MMA's M.  A
+// chunk's codes are 8 KB for 2 x 32 x 128 multiply-adds a row, so the cache's bytes bound
 // it: all units' chunks form one line that is split evenly over one CTA per SM; a CTA's
 // eight warps take a run's chunks in turn, each with its own three-stage TMA ring (192 KB in
 // flight per SM), its own running maximum, sum and fp32 output, and meet once per run.  The
 // parts of a split unit go to the workspace and q8_join joins them.
+#include <type_traits>
+
 #include "rkv_q8_attend.cuh"
 
 namespace rkv {
@@ -60,20 +62,27 @@ struct StageInfo {
   uint32_t live;
 };
 
+// Queries of a run's rows as the MMA's B fragments, for row tiles whose registers are needed
+// elsewhere: [tile][pair of steps][lane], 16 bytes.
+template <int kN>
+using QueryTile = uint4[kN][4][32];
+
 // A warp's share of kN tiles of eight query rows.  Fragment rows are keys (first product) and
 // channels (second); a lane's query rows are the columns 2 (lane % 4) and the next of every
 // tile.  qb: the queries, step s of 16 channels: lane quarter c of a key's bytes 32 c + 4 s ..
 // + 3.  o: channels 16 (lane / 4) + 2 i and + 1 of them for i < 8, times kUnit / vref.
 template <int kFormat, int kN>
 struct RowTile8 {
-  uint32_t qb[kN][8][2];
+  static constexpr bool kShared = kN > 2;  // the queries lie in shared memory
+  uint32_t qb[kShared ? 1 : kN][8][2];
   float o[kN][8][4];
   float m[kN][2], l[kN][2], factor[kN][2];  // factor: from the product to base-2 logits, without the key's scale
   int lim[kN][2];                           // keys that the row sees
   float vref;
   int least;  // the fewest keys that a row sees
 
-  __device__ __forceinline__ void start(const Q8Params& p, int b, int g, int rt, int n, int rows_m) {
+  // qs, kShared: where the queries go, each warp those of the tiles warp, warp + 8, ..
+  __device__ __forceinline__ void start(const Q8Params& p, int b, int g, int rt, int n, int rows_m, uint4 (*qs)[4][32]) {
     const int lane = threadIdx.x & 31, rows = rows_m * p.G, r0 = rt * kN * 8;
 #pragma unroll
     for (int t = 0; t < kN; ++t) {
@@ -97,9 +106,17 @@ struct RowTile8 {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t h[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          qb[t][i * 2 + (j >> 1)][j & 1] = pack_f16x2(bf16_lo(w[j]) * up, bf16_hi(w[j]) * up);
+        for (int j = 0; j < 4; ++j) h[j] = pack_f16x2(bf16_lo(w[j]) * up, bf16_hi(w[j]) * up);
+        if constexpr (kShared) {
+          if ((int)(threadIdx.x >> 5) == t) qs[t][i][lane] = make_uint4(h[0], h[1], h[2], h[3]);
+        } else {
+          qb[t][i * 2][0] = h[0];
+          qb[t][i * 2][1] = h[1];
+          qb[t][i * 2 + 1][0] = h[2];
+          qb[t][i * 2 + 1][1] = h[3];
+        }
       }
       // a row with an infinity or a NaN is NaN
       const float f = top >= 0x7f80u ? __uint_as_float(0x7fffffffu) : p.scale_log2 * power_of_two(e - 8);
@@ -131,7 +148,7 @@ struct RowTile8 {
   }
 
   // The chunk whose first key is key0, K and V in st (their copies have landed).
-  __device__ __forceinline__ void step(uint8_t* st, const StageInfo& info, int key0) {
+  __device__ __forceinline__ void step(uint8_t* st, const StageInfo& info, int key0, const uint4 (*qs)[4][32]) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c4 = lane & 3;
     const uint32_t live = info.live;
     if (live != ~0u) {  // a key that cannot be read may hold anything, and 0 x NaN is not 0
@@ -142,27 +159,43 @@ struct RowTile8 {
     }
     float z[kN][2][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      uint4 ka[2][2];  // keys r, r + 8; 32 bytes each
+    for (int t = 0; t < kN; ++t)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          ka[h][i] = *reinterpret_cast<const uint4*>(st + (u * 16 + h * 8 + r) * 128 + (((c4 * 2 + i) ^ r) << 4));
-#pragma unroll
-      for (int t = 0; t < kN; ++t)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) z[t][u][e] = 0.f;
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const uint4 &x0 = ka[0][s >> 2], &x1 = ka[1][s >> 2];
-        const uint32_t w0 = (s & 3) == 0 ? x0.x : ((s & 3) == 1 ? x0.y : ((s & 3) == 2 ? x0.z : x0.w));
-        const uint32_t w1 = (s & 3) == 0 ? x1.x : ((s & 3) == 1 ? x1.y : ((s & 3) == 2 ? x1.z : x1.w));
-        uint32_t a0, a1, a2, a3;
-        decode4<kFormat>(w0, a0, a2);
-        decode4<kFormat>(w1, a1, a3);
+    for (int i = 0; i < 2; ++i) {  // a lane's 16 of a key's bytes at a time
+      uint4 ka[2][2];              // keys r, r + 8 of the chunk's two halves
 #pragma unroll
-        for (int t = 0; t < kN; ++t) mma_f16(z[t][u], a0, a1, a2, a3, qb[t][s][0], qb[t][s][1]);
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          ka[u][h] = *reinterpret_cast<const uint4*>(st + (u * 16 + h * 8 + r) * 128 + (((c4 * 2 + i) ^ r) << 4));
+#pragma unroll
+      for (int s2 = 0; s2 < 2; ++s2) {
+        uint4 qq[kN];
+#pragma unroll
+        for (int t = 0; t < kN; ++t) {
+          if constexpr (kShared) {
+            qq[t] = qs[t][i * 2 + s2][lane];
+          } else {
+            const int s = i * 4 + s2 * 2;
+            qq[t] = make_uint4(qb[t][s][0], qb[t][s][1], qb[t][s + 1][0], qb[t][s + 1][1]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t w0 = s2 ? (j ? ka[u][0].w : ka[u][0].z) : (j ? ka[u][0].y : ka[u][0].x);
+            const uint32_t w1 = s2 ? (j ? ka[u][1].w : ka[u][1].z) : (j ? ka[u][1].y : ka[u][1].x);
+            uint32_t a0, a1, a2, a3;
+            decode4<kFormat>(w0, a0, a2);
+            decode4<kFormat>(w1, a1, a3);
+#pragma unroll
+            for (int t = 0; t < kN; ++t) mma_f16(z[t][u], a0, a1, a2, a3, j ? qq[t].z : qq[t].x, j ? qq[t].w : qq[t].y);
+          }
       }
     }
     // base-2 logits, hidden ones -inf; e = 0, 1: key r, columns 0, 1; e = 2, 3: key r + 8
@@ -262,10 +295,12 @@ struct RowTile8 {
 
 template <int kFormat, int kN>
 __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_constant__ Q8Params p) {
-  constexpr int kRows = kN * 8;
-  using Line = LineLengths<RowsLine<kN == 1 ? 3 : 4>>;
+  constexpr int kRows = kN * 8, kPartRows = kN == 3 ? 32 : kRows;
+  // three tiles are a unit's only ones: their line is that of four
+  using Line = LineLengths<RowsLine<kN == 1 ? 3 : (kN == 2 ? 4 : 5)>>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Line line;
+  __shared__ typename std::conditional<(kN > 2), QueryTile<kN>, int>::type queries;
   __shared__ uint64_t full_b[kQrWarps][kQrStages];
   __shared__ StageInfo info[kQrWarps][kQrStages];
   __shared__ float wm[kQrWarps][kRows], wl[kQrWarps][kRows], wv[kQrWarps];
@@ -375,7 +410,10 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
   RowTile8<kFormat, kN> tile;
   for (long long x = x0; next_run(x, cr); x = cr.next) {
     const int b = cr.b, g = cr.g, rt = cr.rt, rows = cr.m * p.G;
-    tile.start(p, b, g, rt, cr.n, cr.m);
+    uint4 (*qs)[4][32] = nullptr;
+    if constexpr (kN > 2) qs = queries;
+    tile.start(p, b, g, rt, cr.n, cr.m, qs);
+    if (kN > 2) __syncthreads();  // the queries are there (the last run's were used up before its warps met)
     for (int c = cr.lo + warp; c < cr.hi; c += kQrWarps) {
       const int s = used % kQrStages;
       const bool late = !dead && !mbar_wait(&full_b[warp][s], (uint32_t)((used / kQrStages) & 1));
@@ -383,7 +421,7 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
         if (lane == 0) flag_error(p.err, RKV_DEVERR_TIMEOUT);
         dead = true;
       }
-      if (!dead && info[warp][s].live != 0u) tile.step(ring + s * kQrStageBytes, info[warp][s], c * kQrKeys);
+      if (!dead && info[warp][s].live != 0u) tile.step(ring + s * kQrStageBytes, info[warp][s], c * kQrKeys, qs);
       ++used;
       __syncwarp();  // every lane has read the stage
       if (!dead) fetch();
@@ -439,8 +477,8 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
           *reinterpret_cast<uint32_t*>(p.out + orow * 128 + d) = pack_bf16x2(ax * inv, ay * inv);
           if (d == 0 && p.lse) p.lse[orow] = lse_of(M, L);
         } else {
-          *reinterpret_cast<float2*>(p.part_o + (slot * kRows + row) * 128 + d) = make_float2(ax, ay);
-          if (d == 0) p.part_ml[slot * kRows + row] = make_float2(M, L);
+          *reinterpret_cast<float2*>(p.part_o + (slot * kPartRows + row) * 128 + d) = make_float2(ax, ay);
+          if (d == 0) p.part_ml[slot * kPartRows + row] = make_float2(M, L);
         }
       }
       __syncthreads();  // the merge buffer (and, after the last rows, wm, wl and wv) are free
@@ -512,16 +550,20 @@ __global__ void __launch_bounds__(256, 4) q8_join_kernel(const __grid_constant__
   }
 }
 
-// How many rows of a unit share a pass over the cache: 8 or 16 (mma.sync), 128 or 256 (tcgen05).
+// How many rows of a unit share a pass over the cache: 8, 16, 24 or 32 (mma.sync), 128 or 256
+// (tcgen05).
 int tile_rows(int T, int G) {
   const long long rows = (long long)T * G;
-  return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 128 ? 128 : 256));
+  return rows <= 32 ? (int)(rows + 7) / 8 * 8 : (rows <= 128 ? 128 : 256);
 }
+
+// Rows of a part in the workspace: a power of two.
+int part_rows(int tile) { return tile == 24 ? 32 : tile; }
 
 cudaError_t fill_params(const Q8AttendArgs& a, Q8Params& p, int tile) {
   const rkv_cache8& c = a.cache;
   const uint64_t rows = (uint64_t)c.num_phys_pages * c.Hkv * c.page_size;
-  const uint32_t box = tile > 16 || c.page_size < kQrKeys ? c.page_size : kQrKeys;
+  const uint32_t box = tile > 32 || c.page_size < kQrKeys ? c.page_size : kQrKeys;
   if (!encode_codes_map(&p.tmk, c.k_codes, rows, box) || !encode_codes_map(&p.tmv, c.v_codes, rows, box)) {
     set_last_error("cuTensorMapEncodeTiled failed for the cache's codes");
     return cudaErrorInvalidValue;
@@ -564,7 +606,7 @@ cudaError_t launch_rows(const Q8Params& p, cudaStream_t s) {
 }  // namespace
 
 size_t q8_attend_ws_bytes(int B, int Hq, int Hkv, int T, int max_pages, int page_size) {
-  const size_t rows = (size_t)2 * kMaxSms * tile_rows(T, Hq / Hkv > 0 ? Hq / Hkv : 1);
+  const size_t rows = (size_t)2 * kMaxSms * part_rows(tile_rows(T, Hq / Hkv > 0 ? Hq / Hkv : 1));
   return align256(rows * 128 * 4) + align256(rows * 8);
 }
 
@@ -573,7 +615,7 @@ cudaError_t launch_q8_attend(const Q8AttendArgs& a, cudaStream_t s) {
   const int tile = tile_rows(a.T, a.Hq / a.cache.Hkv);
   cudaError_t e = fill_params(a, p, tile);
   if (e != cudaSuccess) return e;
-  const size_t rows = (size_t)2 * kMaxSms * tile;
+  const size_t rows = (size_t)2 * kMaxSms * part_rows(tile);
   p.part_o = static_cast<float*>(a.ws);
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(a.ws) + align256(rows * 128 * 4));
   const bool int8 = a.cache.format == RKV_Q8_INT8;
@@ -586,6 +628,14 @@ cudaError_t launch_q8_attend(const Q8AttendArgs& a, cudaStream_t s) {
     case 16:
       e = int8 ? launch_rows<RKV_Q8_INT8, 2>(p, s) : launch_rows<RKV_Q8_E4M3, 2>(p, s);
       join = q8_join_kernel<RowsLine<4>>;
+      break;
+    case 24:
+      e = int8 ? launch_rows<RKV_Q8_INT8, 3>(p, s) : launch_rows<RKV_Q8_E4M3, 3>(p, s);
+      join = q8_join_kernel<RowsLine<5>>;
+      break;
+    case 32:
+      e = int8 ? launch_rows<RKV_Q8_INT8, 4>(p, s) : launch_rows<RKV_Q8_E4M3, 4>(p, s);
+      join = q8_join_kernel<RowsLine<5>>;
       break;
     case 128:
       e = launch_q8_tiles(p, false, int8, s);

@@ -635,6 +635,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
     setmaxnreg_dec<kQtCodeRegs>();
     const bool v = warp >= 24;
     const int quarter = warp & 3, sub = lane >> 3, piece = lane & 7;
+    const uint32_t from = (uint32_t)((piece ^ sub) << 4), place_a = (uint32_t)((((piece & 3) * 2) ^ sub) << 4);
     int before = 0, tiles_before = 0;
     bool ok = true;
     for (long long x = x0; ok && next_run(x, r); x = r.next) {
@@ -646,14 +647,14 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         const int left = r.n - (r.lo + i) * kQtKeys;
         const uint32_t gr = ti.groups;
         const int d0 = ti.d[quarter * 2], d1 = ti.d[quarter * 2 + 1];
-        const uint8_t* const src = sh.codes + c * kQtCodes;
+        const uint8_t* const src = sh.codes + c * kQtCodes + (quarter * 32 + sub) * 128;
         if (at >= E && !(ok = wait(&sh.empty[e], at / E - 1))) break;
-        uint8_t* const dst = sh.tiles + e * kQtTile + (piece >> 2) * (kQtTile / 2);
-        auto put = [&](int row, const uint32_t (&a)[4], const uint32_t (&c4)[4]) {
-          const uint32_t sw = (uint32_t)(row & 7);
-          *reinterpret_cast<uint4*>(dst + row * 128 + ((((piece & 3) * 2) ^ sw) << 4)) = make_uint4(a[0], a[1], a[2], a[3]);
-          *reinterpret_cast<uint4*>(dst + row * 128 + ((((piece & 3) * 2 + 1) ^ sw) << 4)) =
-              make_uint4(c4[0], c4[1], c4[2], c4[3]);
+        uint8_t* const dst = sh.tiles + e * kQtTile + (piece >> 2) * (kQtTile / 2) + (quarter * 32 + sub) * 128;
+        // row quarter * 32 + h * 16 + k * 4 + sub: row % 8 is sub or, for odd k, sub + 4
+        auto put = [&](int h, int k, const uint32_t (&a)[4], const uint32_t (&c4)[4]) {
+          const uint32_t at_a = (k & 1) ? place_a ^ 64u : place_a;  // the pieces' numbers XOR row % 8
+          *reinterpret_cast<uint4*>(dst + (h * 16 + k * 4) * 128 + at_a) = make_uint4(a[0], a[1], a[2], a[3]);
+          *reinterpret_cast<uint4*>(dst + (h * 16 + k * 4) * 128 + (at_a ^ 16u)) = make_uint4(c4[0], c4[1], c4[2], c4[3]);
         };
         // one branch for the whole tile: in the unrolled loop, a few of them cost 430 clocks a key row
         const bool plain = max(d0, d1) <= 9 && (!v || (left >= kQtKeys && gr == 0xffu));
@@ -663,14 +664,23 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
           uint4 w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int row = row0 + k * 4;
-            w[k] = *reinterpret_cast<const uint4*>(src + row * 128 + ((piece ^ (row & 7)) << 4));
+            w[k] = *reinterpret_cast<const uint4*>(src + (h * 16 + k * 4) * 128 + ((k & 1) ? from ^ 64u : from));
           }
           if (h == 1) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.empty_c[c]);  // the codes are in registers
           }
-          if (plain) {
+          if (kFormat == RKV_Q8_E4M3 && plain && d == 0) {  // most tiles' pages share one exponent
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t a[4], c4[4];
+              decode4<kFormat>(w[k].x, a[0], a[1]);
+              decode4<kFormat>(w[k].y, a[2], a[3]);
+              decode4<kFormat>(w[k].z, c4[0], c4[1]);
+              decode4<kFormat>(w[k].w, c4[2], c4[3]);
+              put(h, k, a, c4);
+            }
+          } else if (plain) {
             // a factor of 2^-9 keeps -1152 f an fp16 number
             const __half2 f = half_power(d), bias = __hmul2(f, __float2half2_rn(-1152.f));
 #pragma unroll
@@ -680,7 +690,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
               decode4_times<kFormat>(w[k].y, f, bias, a[2], a[3]);
               decode4_times<kFormat>(w[k].z, f, bias, c4[0], c4[1]);
               decode4_times<kFormat>(w[k].w, f, bias, c4[2], c4[3]);
-              put(row0 + k * 4, a, c4);
+              put(h, k, a, c4);
             }
           } else {
             // scales far apart, a page of NaN, or values that are not there: those, and a page of
@@ -703,7 +713,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
                 a[q] = none ? 0u : *reinterpret_cast<const uint32_t*>(&x);
                 c4[q] = none ? 0u : *reinterpret_cast<const uint32_t*>(&y);
               }
-              put(row, a, c4);
+              put(h, k, a, c4);
             }
           }
         }
