@@ -15,7 +15,7 @@
 //             unrounded.
 // ks joins the logits behind the product and vs the weights, so neither costs a pass over codes.
 //
-// q8_rows: 8 to 32 query rows against 32-key chunks, keys and channels on the MMA's M.  A
+// q8_rows: 8 to 24 query rows against 32-key chunks, keys and channels on the MMA's M.  A
 // chunk's codes are 8 KB for 2 x 32 x 128 multiply-adds a row, so the cache's bytes bound
 // it: all units' chunks form one line that is split evenly over one CTA per SM; a CTA's
 // eight warps take a run's chunks in turn, each with its own three-stage TMA ring (192 KB in
@@ -550,11 +550,11 @@ __global__ void __launch_bounds__(256, 4) q8_join_kernel(const __grid_constant__
   }
 }
 
-// How many rows of a unit share a pass over the cache: 8, 16, 24 or 32 (mma.sync), 128 or 256
+// How many rows of a unit share a pass over the cache: 8, 16 or 24 (mma.sync), 128 or 256
 // (tcgen05).
 int tile_rows(int T, int G) {
   const long long rows = (long long)T * G;
-  return rows <= 32 ? (int)(rows + 7) / 8 * 8 : (rows <= 128 ? 128 : 256);
+  return rows <= 24 ? (int)(rows + 7) / 8 * 8 : (rows <= 128 ? 128 : 256);
 }
 
 // Rows of a part in the workspace: a power of two.
@@ -563,7 +563,7 @@ int part_rows(int tile) { return tile == 24 ? 32 : tile; }
 cudaError_t fill_params(const Q8AttendArgs& a, Q8Params& p, int tile) {
   const rkv_cache8& c = a.cache;
   const uint64_t rows = (uint64_t)c.num_phys_pages * c.Hkv * c.page_size;
-  const uint32_t box = tile > 32 || c.page_size < kQrKeys ? c.page_size : kQrKeys;
+  const uint32_t box = tile > 24 || c.page_size < kQrKeys ? c.page_size : kQrKeys;
   if (!encode_codes_map(&p.tmk, c.k_codes, rows, box) || !encode_codes_map(&p.tmv, c.v_codes, rows, box)) {
     set_last_error("cuTensorMapEncodeTiled failed for the cache's codes");
     return cudaErrorInvalidValue;
@@ -631,10 +631,6 @@ cudaError_t launch_q8_attend(const Q8AttendArgs& a, cudaStream_t s) {
       break;
     case 24:
       e = int8 ? launch_rows<RKV_Q8_INT8, 3>(p, s) : launch_rows<RKV_Q8_E4M3, 3>(p, s);
-      join = q8_join_kernel<RowsLine<5>>;
-      break;
-    case 32:
-      e = int8 ? launch_rows<RKV_Q8_INT8, 4>(p, s) : launch_rows<RKV_Q8_E4M3, 4>(p, s);
       join = q8_join_kernel<RowsLine<5>>;
       break;
     case 128:

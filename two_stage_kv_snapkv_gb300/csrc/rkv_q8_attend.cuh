@@ -53,7 +53,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 .. 127
 
-// More than 32 query rows a KV head, on the fifth-generation tensor cores: the parts of split
+// More than 24 query rows a KV head, on the fifth-generation tensor cores: the parts of split
 // units for q8_join, or the results.  wide: 256 rows to a tile, else 128.
 constexpr int kQtKeysShift = 7, kQtPad = 4;
 template <int kRowsShift>

@@ -16,8 +16,8 @@
 // it grows, O is scaled down with the maximum's move).  A code times such a factor is exact
 // but where it falls below fp16's smallest step, 2^-33 of the largest.
 //   warps 0-7, 8-15: softmax of slot 0, 1 (four warps to 64 keys);  16, 18: TMA of K, V;  17:
-//   MMA issue;  19: idle;  20-23, 24-27: K's and V's codes to fp16.
-// Order and phases of both rings are the same formula in every role.  Every wait is bounded;
+//   MMA issue;  19: the share's runs;  20-23, 24-27: K's and V's codes to fp16.
+// Every wait is bounded;
 // one that runs out flags RKV_DEVERR_TIMEOUT and stops every role.
 #include "rkv_q8_attend.cuh"
 
@@ -49,38 +49,42 @@ struct TileInfo {
   uint32_t groups;
 };
 
+// A run of the CTA's share, as warp 19 hands it to the others: worked out by every role, the
+// 64-bit arithmetic took registers from their loops over tiles.
+struct alignas(16) RunInfo {
+  int b, g, rt, n, m, lo, hi;
+  uint8_t whole, first, end, pad;
+};
+static_assert(sizeof(RunInfo) == 32, "read with two loads");
+constexpr int kQtRuns = 4;
+
 template <bool kWide>
 struct TileShape8 {
   static constexpr int kRows = kWide ? 256 : 128;
   static constexpr int kQBytes = kRows * 256;
-  static constexpr int kTiles = 3, kCodeSlots = kWide ? 4 : 5;
+  // K and V each have one operand and a ring of three tiles of codes (two: 282 us instead of
+  // 212 for 32 rows over 16 x 20000 tokens; a second operand in place of one: no change).  Each
+  // has one producer and one consumer that go through every slot's phases in order: a wait by
+  // parity cannot tell a phase from the one two before.
+  static constexpr int kCodes = 3;
   using Line = TileLine<kWide ? 8 : 7>;
   struct Shared {
     uint8_t q[kQBytes];
-    uint8_t tiles[kTiles * kQtTile];
-    uint8_t codes[kCodeSlots * kQtCodes];
+    uint8_t ops[2][kQtTile];
+    uint8_t codes[2][kCodes * kQtCodes];
     Line line;
-    uint64_t full_c[kCodeSlots], empty_c[kCodeSlots], full[kTiles], empty[kTiles], s[2], p[2], o[2], qf[2], out[2], ml, drained;
+    uint64_t full_c[2][kCodes], empty_c[2][kCodes], full[2], empty[2], s[2], p[2], o[2], qf[2], out[2], ml, drained;
     TileInfo info[2][kQtInfos];
-    CausalRun first;  // the share's first run, worked out once
-    long long x0, x1;
+    RunInfo runs[kQtRuns];
+    uint64_t full_r[kQtRuns], empty_r[kQtRuns];
     uint32_t tmem_base;
     int abort_flag;
-    bool any;
     int8_t row_exp[kRows];
     float2 ml_s[kWide ? 1 : 4][kWide ? 1 : 128];
   };
   static constexpr int kSmem = sizeof(Shared);
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
-
-// Where K or V of key tile i lies among a run's 2 nt tiles of codes and operands: K_i then V_i
-// (kWide), or K_0, then K_(i+1) and V_i for every i.
-template <bool kWide>
-__device__ __forceinline__ int place_of(bool v, int i, int nt) {
-  if (kWide) return 2 * i + v;
-  return v ? (i + 1 < nt ? 2 * i + 2 : 2 * nt - 1) : (i > 0 ? 2 * i - 1 : 0);
-}
 
 // Two fp32 numbers in one 64-bit register, and arithmetic on both at once.
 __device__ __forceinline__ uint64_t pair_bits(uint32_t lo, uint32_t hi) {
@@ -102,6 +106,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// A place in a ring: the slot and how often it was used before.
+template <int kSize>
+struct RingAt {
+  int slot = 0, use = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == kSize) {
+      slot = 0;
+      ++use;
+    }
+  }
+};
+
 // 2^-d as a pair of fp16 numbers, d <= 24.
 __device__ __forceinline__ __half2 half_power(int d) {
   const uint32_t h = d < 15 ? (uint32_t)(15 - d) << 10 : 1u << (24 - d);
@@ -112,19 +128,19 @@ __device__ __forceinline__ __half2 half_power(int d) {
 template <int kFormat, bool kWide>
 __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_constant__ Q8Params p) {
   using Sh = TileShape8<kWide>;
-  constexpr int E = Sh::kTiles, C = Sh::kCodeSlots, R = Sh::kRows;
+  constexpr int R = Sh::kRows;
   extern __shared__ __align__(1024) uint8_t dyn_smem[];
   typename Sh::Shared& sh = *reinterpret_cast<typename Sh::Shared*>(dyn_smem);
   volatile int& abort_flag = *const_cast<volatile int*>(&sh.abort_flag);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int e = 0; e < E; ++e) {
-      mbar_init(&sh.full[e], 4);   // the four warps that wrote it
-      mbar_init(&sh.empty[e], 1);
-    }
-    for (int c = 0; c < C; ++c) {
-      mbar_init(&sh.full_c[c], 1);
-      mbar_init(&sh.empty_c[c], 4);
+    for (int v = 0; v < 2; ++v) {
+      mbar_init(&sh.full[v], 4);  // the four warps that wrote it
+      mbar_init(&sh.empty[v], 1);
+      for (int c = 0; c < Sh::kCodes; ++c) {
+        mbar_init(&sh.full_c[v][c], 1);
+        mbar_init(&sh.empty_c[v][c], 4);
+      }
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh.s[s], 2);  // the issuing thread and its commit
@@ -135,6 +151,10 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
     }
     mbar_init(&sh.ml, 16);
     mbar_init(&sh.drained, 1);
+    for (int j = 0; j < kQtRuns; ++j) {
+      mbar_init(&sh.full_r[j], 1);
+      mbar_init(&sh.empty_r[j], kQtThreads / 32 - 1);
+    }
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -153,21 +173,6 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
   tc_fence_after();
   grid_launch_dependents();
   const uint32_t tmem = sh.tmem_base;
-  if (tid == 0) {
-    const long long total = sh.line.base[p.B];
-    const int N = flat_ctas(total, p.N);
-    const bool works = (int)blockIdx.x < N;
-    sh.x0 = works ? flat_first(total, blockIdx.x, N) : 0;
-    sh.x1 = works ? flat_first(total, blockIdx.x + 1, N) : 0;
-    sh.any = sh.line.next(p.B, p.Hkv, p.gshift, len_of, rows_of, sh.x0, sh.x0, sh.x1, sh.first);
-  }
-  __syncthreads();
-  const long long x0 = sh.x0, x1 = sh.x1;
-  auto next_run = [&](long long x, CausalRun& r) {
-    if (x != x0) return sh.line.next(p.B, p.Hkv, p.gshift, len_of, rows_of, x, x0, x1, r);
-    r = sh.first;
-    return sh.any;
-  };
   auto give_up = [&]() {
     flag_error(p.err, RKV_DEVERR_TIMEOUT);
     abort_flag = 1;
@@ -187,8 +192,18 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
-  int loaded = 0;  // one past the last tile of codes asked for (warps 16, 18), of operands used (warp 17)
-  CausalRun r;
+  // the next run of the share; false: there is none
+  int run_no = 0;
+  auto next_run = [&](RunInfo& r, bool& ok) {
+    const int k = run_no % kQtRuns;
+    if (!(ok = wait(&sh.full_r[k], run_no / kQtRuns))) return false;
+    r = sh.runs[k];
+    arrive(&sh.empty_r[k]);
+    ++run_no;
+    return !r.end;
+  };
+  int loaded = 0;  // tiles of codes asked for (warps 16, 18)
+  RunInfo r;
 
   if (warp < 16) {
     setmaxnreg_inc<kQtSoftRegs>();
@@ -208,7 +223,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
           : "memory");
       return any != 0;
     };
-    for (long long x = x0; ok && next_run(x, r); x = r.next) {
+    while (ok && next_run(r, ok)) {
       const int b = r.b, g = r.g, rt = r.rt, n = r.n, rows = r.m * p.G, nt = r.hi - r.lo;
       const bool idle = kWide && slot == 1 && rows - rt * R <= 128;
       // the query rows as fp16, swizzled as TMA would store them, over the last run's staged outputs
@@ -468,9 +483,9 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
       const bool lead = elect_lane();
       const int pages = kQtKeys >> p.pshift, box = p.P * 128, per_page = p.P >> 4;  // of a tile; bytes; 16-key groups
       const uint64_t policy = l2_policy(!kWide && (long long)p.T * p.G <= R);  // one row tile: read once
-      int before = 0, tiles_before = 0;
+      RingAt<Sh::kCodes> at;
       bool ok = true;
-      for (long long x = x0; ok && next_run(x, r); x = r.next) {
+      while (ok && next_run(r, ok)) {
         const int b = r.b, g = r.g, n = r.n, nt = r.hi - r.lo;
         // lane j: the tile's page j and its scales; loaded ahead, so that the loads' latency stays
         // off the ring
@@ -495,8 +510,8 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
           next = after;
           after = i + 2 < nt ? page_of(tile + 2) : -1;
           scales_of(next, nk, nv);
-          const int at = before + place_of<kWide>(v, i, nt), c = at % C;
-          if (at >= C && !(ok = wait(&sh.empty_c[c], at / C - 1))) break;
+          const int c = at.slot;
+          if (at.use > 0 && !(ok = wait(&sh.empty_c[v][c], at.use - 1))) break;
           const bool mine = lane < pages && (tile * pages + lane) * p.P < n;
           if (phys < 0 || phys >= p.num_phys) {
             if (mine) flag_error(p.err, RKV_DEVERR_PAGE_ID);
@@ -507,7 +522,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
           const int xk = (int)(__float_as_uint(sk) >> 23) & 255, xv = (int)(__float_as_uint(sv) >> 23) & 255;
           unit = max(unit, __reduce_max_sync(0xffffffffu, phys >= 0 && xv < 255 ? xv : 1) - 127);
           const int ek = __reduce_max_sync(0xffffffffu, phys >= 0 && xk < 255 ? xk : 1) - 127;
-          TileInfo& ti = sh.info[v][(tiles_before + i) % kQtInfos];
+          TileInfo& ti = sh.info[v][loaded % kQtInfos];
           const int mx = v ? xv : xk, me = v ? unit : ek;
           if (lane < pages)
             for (int j = 0; j < per_page; ++j)
@@ -521,113 +536,125 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
             ti.unit = (int16_t)unit;
           }
           __syncwarp();
-          uint8_t* const st = sh.codes + c * kQtCodes;
+          uint8_t* const st = sh.codes[v] + c * kQtCodes;
+          uint64_t* const bar = &sh.full_c[v][c];
           if (lead) {
-            if (have) mbar_arrive_expect_tx(&sh.full_c[c], __popc(have) * box);
-            else mbar_arrive(&sh.full_c[c]);
+            if (have) mbar_arrive_expect_tx(bar, __popc(have) * box);
+            else mbar_arrive(bar);
           }
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int row = (__shfl_sync(0xffffffffu, phys, j) * p.Hkv + g) * p.P;
-            if (lead && ((have >> j) & 1u)) tma_load_2d_hint(st + j * box, map, 0, row, &sh.full_c[c], policy);
+            if (lead && ((have >> j) & 1u)) tma_load_2d_hint(st + j * box, map, 0, row, bar, policy);
           }
-          loaded = at + 1;
+          ++loaded;
+          at.step();
         }
-        before += 2 * nt;
-        tiles_before += nt;
+      }
+    } else if (warp == 19) {
+      const long long total = sh.line.base[p.B];
+      const int N = flat_ctas(total, p.N);
+      const bool works = (int)blockIdx.x < N;
+      const long long x0 = works ? flat_first(total, blockIdx.x, N) : 0, x1 = works ? flat_first(total, blockIdx.x + 1, N) : 0;
+      CausalRun cr;
+      bool more = true;
+      for (long long x = x0; more; x = cr.next) {
+        more = sh.line.next(p.B, p.Hkv, p.gshift, len_of, rows_of, x, x0, x1, cr);
+        const int k = run_no % kQtRuns;
+        if (run_no >= kQtRuns && !wait(&sh.empty_r[k], run_no / kQtRuns - 1)) break;
+        if (lane == 0) {
+          RunInfo ri = {};
+          ri.end = !more;
+          if (more) ri = {cr.b, cr.g, cr.rt, cr.n, cr.m, cr.lo, cr.hi, (uint8_t)cr.whole, (uint8_t)cr.first, 0, 0};
+          sh.runs[k] = ri;
+          mbar_arrive(&sh.full_r[k]);
+        }
+        __syncwarp();
+        ++run_no;
       }
     } else if (warp == 17) {
       constexpr uint32_t idesc_s = idesc_f16_f32(128, 128), idesc_o = idesc_s | kIdescBNMajor;
-      const uint32_t q32 = smem_u32(sh.q), ring32 = smem_u32(sh.tiles);
-      int seen_p[2] = {0, 0}, runs[2] = {0, 0};
+      const uint32_t q32 = smem_u32(sh.q), k32 = smem_u32(sh.ops[0]), v32 = smem_u32(sh.ops[1]);
+      int seen_p[2] = {0, 0}, run = 0, taken[2] = {0, 0};
       bool ok = true;
       const bool lead = elect_lane();
-      const uint32_t qlo = sw128_kmajor_lo(q32), klo = sw128_kmajor_lo(ring32), vlo = sw128_nmajor_lo(ring32, kQtTile / 2);
-      // S of `slot` from the K operand e
-      auto mma_s = [&](int slot, int e, bool release) {
+      const uint32_t qlo = sw128_kmajor_lo(q32), klo = sw128_kmajor_lo(k32), vlo = sw128_nmajor_lo(v32, kQtTile / 2);
+      // S of `slot` from the K operand
+      auto mma_s = [&](int slot, bool release) {
         tc_fence_after();
-        const uint32_t d = tmem + slot * 256, qa = qlo + (kWide ? slot * (128 * 256 >> 4) : 0), ka = klo + e * (kQtTile >> 4);
+        uint32_t d = tmem + slot * 256, qa = qlo + (kWide ? slot * (128 * 256 >> 4) : 0), ka = klo;
+        // worked out anew each time: kept over the loop, the steps' addresses spill
+        asm volatile("" : "+r"(d), "+r"(qa), "+r"(ka));
         tc_mma_ss<false>(lead, d, qa, ka, idesc_s);
 #pragma unroll
         for (int k = 1; k < 8; ++k) {
           const uint32_t off = ((k >> 2) * (kQtTile / 2) + (k & 3) * 32) >> 4;
           tc_mma_ss<true>(lead, d, qa + off, ka + off, idesc_s);
         }
-        tc_commit_if(lead && release, &sh.empty[e]);
+        tc_commit_if(lead && release, &sh.empty[0]);
         tc_commit_if(lead, &sh.s[slot]);
         if (lead) mbar_arrive(&sh.s[slot]);
         __syncwarp();
       };
       // O += P V once the slot's weights are there
-      auto mma_o = [&](int slot, int e, bool first, bool last, bool release) {
+      auto mma_o = [&](int slot, bool first, bool last, bool release) {
         if (!(ok = wait(&sh.p[slot], seen_p[slot]++))) return;
         tc_fence_after();
-        const uint32_t d = tmem + slot * 256 + 128, pa = tmem + slot * 256, va = vlo + e * (kQtTile >> 4);
+        uint32_t d = tmem + slot * 256 + 128, pa = tmem + slot * 256, va = vlo;
+        asm volatile("" : "+r"(d), "+r"(pa), "+r"(va));
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           tc_mma_ts(lead, d, pa + (k >> 2) * 64 + (k & 3) * 8, va + (k * 2048 >> 4), idesc_o, (first && k == 0) ? 0u : 1u);
-        tc_commit_if(lead && release, &sh.empty[e]);
+        tc_commit_if(lead && release, &sh.empty[1]);
         tc_commit_if(lead && last, &sh.o[slot]);
       };
-      for (long long x = x0; ok && next_run(x, r); x = r.next) {
+      while (ok && next_run(r, ok)) {
         const int nt = r.hi - r.lo;
         const bool two = kWide && r.m * p.G - r.rt * R > 128;  // slot 1 has rows
-        auto take = [&]() {  // the next operand, written
-          const int e = loaded % E;
-          ok = wait(&sh.full[e], loaded / E);
-          ++loaded;
-          return e;
-        };
-        ok = wait(&sh.qf[0], runs[0]++);
-        if (kWide && ok) ok = wait(&sh.qf[1], runs[1]++);
+        auto take = [&](int v) { return ok = wait(&sh.full[v], taken[v]++); };  // K's or V's next operand, written
+        ok = wait(&sh.qf[0], run);
+        if (kWide && ok) ok = wait(&sh.qf[1], run);
         if (!ok) break;
+        ++run;
+        if (!take(0)) break;
+        mma_s(0, !two);
+        if (two) mma_s(1, true);
         if (kWide) {
-          int ek = take();
-          if (!ok) break;
-          mma_s(0, ek, !two);
-          if (two) mma_s(1, ek, true);
           for (int i = 0; i < nt; ++i) {
-            const int ev = take();
-            if (!ok) break;
+            if (!take(1)) break;
             const bool last = i + 1 == nt;
-            mma_o(0, ev, i == 0, last, !two);
+            mma_o(0, i == 0, last, !two);
             if (!ok) break;
             tc_commit_if(lead && last && !two, &sh.o[1]);  // keeps an idle slot in step
-            int en = 0;
             if (!last) {
-              en = take();
-              if (!ok) break;
-              mma_s(0, en, !two);
+              if (!take(0)) break;
+              mma_s(0, !two);
             }
             if (two) {
-              mma_o(1, ev, i == 0, last, true);
+              mma_o(1, i == 0, last, true);
               if (!ok) break;
-              if (!last) mma_s(1, en, true);
+              if (!last) mma_s(1, true);
             }
           }
         } else {
-          const int e0 = take();
-          if (!ok) break;
-          mma_s(0, e0, true);
           for (int i = 0; i < nt; ++i) {
             const int slot = i & 1;
             if (i + 1 < nt) {
               // tile i + 1's logits go where tile i - 1's weights lay: its product was issued before
-              const int en = take();
-              if (!ok) break;
-              mma_s(slot ^ 1, en, true);
+              if (!take(0)) break;
+              mma_s(slot ^ 1, true);
             }
-            const int ev = take();
-            if (!ok) break;
-            mma_o(slot, ev, i < 2, i + 2 >= nt, true);
+            if (!take(1)) break;
+            mma_o(slot, i < 2, i + 2 >= nt, true);
             if (!ok) break;
           }
         }
       }
       // the last operands' releases land before the CTA may exit
       if (ok)
-        for (int i = loaded > E ? loaded - E : 0; i < loaded; ++i) mbar_wait(&sh.empty[i % E], (uint32_t)((i / E) & 1));
+        for (int v = 0; v < 2; ++v)
+          if (taken[v] > 0) mbar_wait(&sh.empty[v], (uint32_t)((taken[v] - 1) & 1));
     }
   } else {
     // codes to fp16, K's (warps 20-23) and V's: a warp's 32 keys of a tile, four keys of eight
@@ -636,20 +663,21 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
     const bool v = warp >= 24;
     const int quarter = warp & 3, sub = lane >> 3, piece = lane & 7;
     const uint32_t from = (uint32_t)((piece ^ sub) << 4), place_a = (uint32_t)((((piece & 3) * 2) ^ sub) << 4);
-    int before = 0, tiles_before = 0;
+    RingAt<Sh::kCodes> at;
+    int tile_no = 0;
     bool ok = true;
-    for (long long x = x0; ok && next_run(x, r); x = r.next) {
+    while (ok && next_run(r, ok)) {
       const int nt = r.hi - r.lo;
       for (int i = 0; i < nt; ++i) {
-        const int at = before + place_of<kWide>(v, i, nt), c = at % C, e = at % E;
-        if (!(ok = wait(&sh.full_c[c], at / C))) break;
-        const TileInfo& ti = sh.info[v][(tiles_before + i) % kQtInfos];
+        const int c = at.slot;
+        if (!(ok = wait(&sh.full_c[v][c], at.use))) break;
+        const TileInfo& ti = sh.info[v][tile_no % kQtInfos];
         const int left = r.n - (r.lo + i) * kQtKeys;
         const uint32_t gr = ti.groups;
         const int d0 = ti.d[quarter * 2], d1 = ti.d[quarter * 2 + 1];
-        const uint8_t* const src = sh.codes + c * kQtCodes + (quarter * 32 + sub) * 128;
-        if (at >= E && !(ok = wait(&sh.empty[e], at / E - 1))) break;
-        uint8_t* const dst = sh.tiles + e * kQtTile + (piece >> 2) * (kQtTile / 2) + (quarter * 32 + sub) * 128;
+        const uint8_t* const src = sh.codes[v] + c * kQtCodes + (quarter * 32 + sub) * 128;
+        if (tile_no > 0 && !(ok = wait(&sh.empty[v], tile_no - 1))) break;
+        uint8_t* const dst = sh.ops[v] + (piece >> 2) * (kQtTile / 2) + (quarter * 32 + sub) * 128;
         // row quarter * 32 + h * 16 + k * 4 + sub: row % 8 is sub or, for odd k, sub + 4
         auto put = [&](int h, int k, const uint32_t (&a)[4], const uint32_t (&c4)[4]) {
           const uint32_t at_a = (k & 1) ? place_a ^ 64u : place_a;  // the pieces' numbers XOR row % 8
@@ -668,7 +696,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
           }
           if (h == 1) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.empty_c[c]);  // the codes are in registers
+            if (lane == 0) mbar_arrive(&sh.empty_c[v][c]);  // the codes are in registers
           }
           if (kFormat == RKV_Q8_E4M3 && plain && d == 0) {  // most tiles' pages share one exponent
 #pragma unroll
@@ -719,10 +747,10 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.full[e]);
+        if (lane == 0) mbar_arrive(&sh.full[v]);
+        at.step();
+        ++tile_no;
       }
-      before += 2 * nt;
-      tiles_before += nt;
     }
   }
 
@@ -730,8 +758,11 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
   tc_fence_before();
   __syncthreads();
   if (abort_flag) {
-    if ((warp == 16 || warp == 18) && lane == 0)
-      for (int i = loaded > C ? loaded - C : 0; i < loaded; ++i) mbar_wait(&sh.full_c[i % C], (uint32_t)((i / C) & 1));
+    if ((warp == 16 || warp == 18) && lane == 0) {
+      constexpr int C = Sh::kCodes;
+      const int v = warp == 18;
+      for (int i = max(loaded - C, 0); i < loaded; ++i) mbar_wait(&sh.full_c[v][i % C], (uint32_t)((i / C) & 1));
+    }
     if (warp == 17) {  // everything this lane issued before the commit has completed when it arrives
       tc_commit_if(elect_lane(), &sh.drained);
       mbar_wait(&sh.drained, 0);
