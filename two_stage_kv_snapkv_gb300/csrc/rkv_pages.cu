@@ -10,6 +10,8 @@
 // CTA waits for another's writes; what one CTA writes (table entries behind `held`, stack
 // places from `count` on) no other reads.  The counts are written by the CTA that finishes
 // last, when every one has read the old ones, so that they may be updated in place.
+#include <algorithm>
+
 #include "rkv_device.cuh"
 #include "rkv_internal.h"
 
@@ -17,6 +19,8 @@ namespace rkv {
 namespace {
 
 constexpr int kRsThreads = 256;
+constexpr int kRsSlots = 8;  // of a thread at a time
+constexpr int kRsCtas = 4;   // of an SM
 static_assert(kRsThreads >= RKV_MAX_BATCH, "a thread for every sequence");
 
 struct ReserveParams {
@@ -32,7 +36,7 @@ struct ReserveParams {
   int32_t* first;
   int32_t* held_out;
   int32_t* count_out;
-  int B, max_pages, P, pshift, num_phys, slots_size;
+  int B, max_pages, P, pshift, num_phys, slots_size, wide_stores;
 };
 
 struct ReserveTable {
@@ -74,7 +78,7 @@ __device__ __forceinline__ int holder(const int* sum, int B, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kRsThreads) reserve_pages_kernel(const __grid_constant__ ReserveParams p) {
+__global__ void __launch_bounds__(kRsThreads, kRsCtas) reserve_pages_kernel(const __grid_constant__ ReserveParams p) {
   __shared__ ReserveTable rt;
   const int tid = threadIdx.x, b = tid;
   const bool lead = blockIdx.x == 0;
@@ -137,15 +141,52 @@ __global__ void __launch_bounds__(kRsThreads) reserve_pages_kernel(const __grid_
   const int top = have - taken;  // pages given back that stay: the places [count, top)
   for (int x = count + blockIdx.x * kRsThreads + tid; stack_ok && x < min(top, p.num_phys); x += stride)
     p.free_pages[x] = stack_page(x);
+  // Slots.  The page that holds position pos of sequence s, -1 when its id is out of range.
   const int live = min(slots, p.slots_size);
-  for (int x = blockIdx.x * kRsThreads + tid; x < live; x += stride) {
-    const int s = holder(rt.slot, p.B, x);
-    const int pos = rt.start[s] + (x - rt.slot[s]), j = pos >> p.pshift;
+  auto page_of = [&](int s, int j) -> int {
     const int phys = j < rt.held[s] ? p.page_table[(size_t)s * p.max_pages + j]
                                     : stack_page(have - 1 - (rt.take[s] + j - rt.held[s]));
-    const bool in = phys >= 0 && phys < p.num_phys;
-    if (!in) flag_error(p.err, RKV_DEVERR_PAGE_ID);
-    p.slots[x] = in ? phys * p.P + (pos & (p.P - 1)) : -1;
+    if (phys >= 0 && phys < p.num_phys) return phys;
+    flag_error(p.err, RKV_DEVERR_PAGE_ID);
+    return -1;
+  };
+  if (live <= stride) {  // a thread for each
+    const int x = blockIdx.x * kRsThreads + tid;
+    if (x < live) {
+      const int s = holder(rt.slot, p.B, x), pos = rt.start[s] + (x - rt.slot[s]), phys = page_of(s, pos >> p.pshift);
+      p.slots[x] = phys >= 0 ? phys * p.P + (pos & (p.P - 1)) : -1;
+    }
+  } else {  // eight neighbours a thread: one search for the sequence, one or two pages looked up
+    for (int x = (blockIdx.x * kRsThreads + tid) * kRsSlots; x < live; x += stride * kRsSlots) {
+      int s = holder(rt.slot, p.B, x), out[kRsSlots];
+      if (x + kRsSlots <= min(live, rt.slot[s + 1])) {  // of one sequence, and so of two pages at most
+        const int pos = rt.start[s] + (x - rt.slot[s]), j = pos >> p.pshift, k = (pos + kRsSlots - 1) >> p.pshift;
+        const int one = page_of(s, j), two = k != j ? page_of(s, k) : one;
+#pragma unroll
+        for (int e = 0; e < kRsSlots; ++e) {
+          const int phys = (pos + e) >> p.pshift == j ? one : two;
+          out[e] = phys >= 0 ? phys * p.P + ((pos + e) & (p.P - 1)) : -1;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < kRsSlots; ++e) {
+          out[e] = 0;
+          if (x + e >= live) continue;
+          while (x + e >= rt.slot[s + 1]) ++s;
+          const int pos = rt.start[s] + (x + e - rt.slot[s]), phys = page_of(s, pos >> p.pshift);
+          out[e] = phys >= 0 ? phys * p.P + (pos & (p.P - 1)) : -1;
+        }
+      }
+      if (p.wide_stores && x + kRsSlots <= live) {
+#pragma unroll
+        for (int e = 0; e < kRsSlots; e += 4)
+          *reinterpret_cast<int4*>(p.slots + x + e) = make_int4(out[e], out[e + 1], out[e + 2], out[e + 3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kRsSlots; ++e)
+          if (x + e < live) p.slots[x + e] = out[e];
+      }
+    }
   }
 
   __syncthreads();  // every thread of this CTA has read the old counts
@@ -185,13 +226,13 @@ cudaError_t launch_reserve_pages(const ReserveArgs& a, cudaStream_t s) {
   p.pshift = log2_int(a.page_size);
   p.num_phys = a.pool.num_phys_pages;
   p.slots_size = a.start ? a.slots_size : 0;
+  p.wide_stores = (reinterpret_cast<uintptr_t>(a.slots) & 15u) == 0;
   const long long pages = (long long)a.B * a.max_pages < p.num_phys ? (long long)a.B * a.max_pages : p.num_phys;
-  const long long items = p.slots_size > pages ? p.slots_size : pages;
-  long long grid = (items + 4 * kRsThreads - 1) / (4 * kRsThreads);
-  const long long most = 4LL * num_sms();
-  if (grid > most) grid = most;
+  // a thread for every eight slots, or every four pages that could be taken
+  const long long items = std::max((long long)p.slots_size / kRsSlots, pages / 4) + 1;
+  const unsigned grid = (unsigned)std::min((items + kRsThreads - 1) / kRsThreads, (long long)kRsCtas * num_sms());
   launch_begin(K_RESERVE_PAGES, s);
-  reserve_pages_kernel<<<(unsigned)grid, kRsThreads, 0, s>>>(p);
+  reserve_pages_kernel<<<grid, kRsThreads, 0, s>>>(p);
   launch_end(K_RESERVE_PAGES, s);
   return cudaGetLastError();
 }

@@ -171,6 +171,7 @@ struct NewRows {  // row r of the page whose first row is new row `at` (which ma
 // length on.
 constexpr int kWrWarps = 8;
 constexpr int kWrSmall = 16;
+constexpr int kWrCtas = 2;  // of an SM, all resident: 16 loads in flight a lane take 128 registers
 
 template <int kFormat>
 __global__ void __launch_bounds__(kWrWarps * 32) q8_append_small_kernel(const __grid_constant__ Q8WriteParams p) {
@@ -206,7 +207,7 @@ struct WriteLine {
 };
 
 template <int kFormat, int kPieces, bool kLoad>
-__global__ void __launch_bounds__(kWrWarps * 32) q8_write_kernel(const __grid_constant__ Q8WriteParams p) {
+__global__ void __launch_bounds__(kWrWarps * 32, kWrCtas) q8_write_kernel(const __grid_constant__ Q8WriteParams p) {
   constexpr int kPages = kWrWarps / kPieces;  // pages of a CTA at a time
   __shared__ WriteLine line;
   const int tid = threadIdx.x, warp = tid >> 5, slot = warp / kPieces;
@@ -306,7 +307,7 @@ template <int kFormat, bool kLoad>
 cudaError_t launch_line(const Q8WriteParams& p, long long most_pages, int kind, cudaStream_t s) {
   const int pieces = p.P / 16;
   const long long units = (long long)p.B * p.Hkv * most_pages, ctas = (units * pieces + kWrWarps - 1) / kWrWarps;
-  const long long most = 3LL * num_sms();
+  const long long most = (long long)kWrCtas * num_sms();
   const unsigned grid = (unsigned)(ctas < most ? ctas : most);
   void (*kernel)(Q8WriteParams) = pieces == 1   ? q8_write_kernel<kFormat, 1, kLoad>
                                   : pieces == 2 ? q8_write_kernel<kFormat, 2, kLoad>

@@ -144,7 +144,6 @@ _lib.rkv_evict_workspace_size.argtypes = [_i32] * 4
 _lib.rkv_evict_workspace_size.restype = _sz
 _lib.rkv_evict_accum.argtypes = [_cachep, _vp, _i32, _i32p, _i32, _vp, _i32, _cachep, _vp, _i32, _vp, _sz, _vp]
 _lib.rkv_evict_accum.restype = _i32
-_i64p = ctypes.POINTER(ctypes.c_int64)
 _cache8p = ctypes.POINTER(RkvCache8Struct)
 _lib.rkv_reserve_pages.argtypes = [ctypes.POINTER(RkvPagePoolStruct), _vp, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp,
                                    _vp, _vp, _vp]
@@ -152,10 +151,10 @@ _lib.rkv_reserve_pages.restype = _i32
 _lib.rkv_rotary_init.argtypes = [ctypes.POINTER(RkvRotaryPlan), _i32, ctypes.c_double, _i32, _i32, ctypes.c_double, _i32,
                                  ctypes.c_double, ctypes.c_double, _f32]
 _lib.rkv_rotary_init.restype = _i32
-_lib.rkv_rotary.argtypes = [ctypes.POINTER(RkvRotaryPlan), _vp, _i64p, _vp, _i64p, _i32, _i32, _i32, _i32, _vp, _i32,
-                            _i32, _vp, _i64p, _vp, _i64p, _vp]
+_lib.rkv_rotary.argtypes = [ctypes.POINTER(RkvRotaryPlan), _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32,
+                            _i32, _vp, _vp, _vp, _vp, _vp]
 _lib.rkv_rotary.restype = _i32
-_lib.rkv_q8_append.argtypes = [_cache8p, _vp, _i64p, _vp, _i64p, _i32, _vp, _vp]
+_lib.rkv_q8_append.argtypes = [_cache8p, _vp, _vp, _vp, _vp, _i32, _vp, _vp]
 _lib.rkv_q8_append.restype = _i32
 _lib.rkv_q8_load.argtypes = [_cache8p, _cachep, _vp]
 _lib.rkv_q8_load.restype = _i32
@@ -456,7 +455,7 @@ def _arg(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype,
     (None stays None)."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name}: expected {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensors passed to librkv must be contiguous")
@@ -470,9 +469,9 @@ def _acc_arg(acc: torch.Tensor, name: str, cache: "PagedCache", device) -> int:
 
 
 def _ws_arg(workspace: torch.Tensor, device) -> int:
-    if workspace.dtype != torch.uint8:
-        raise ValueError(f"workspace: expected torch.uint8, got {workspace.dtype}")
-    return _arg(workspace, "workspace", workspace.shape, torch.uint8, device)
+    if workspace.dtype is not torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected contiguous torch.uint8 on {device}, got {workspace.dtype} on {workspace.device}")
+    return workspace.data_ptr()
 
 
 def _call_on(device, stream, fn, *args) -> None:
@@ -687,16 +686,25 @@ def rotary_plan(rot_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: boo
     return plan
 
 
+@functools.lru_cache(maxsize=1024)
+def _row_strides(shape: tuple, stride: tuple) -> tuple:
+    """(address, array) of the strides that the library takes for rows [sequence][head][token][128]
+    (strides of a dimension of one mean nothing)."""
+    a = (ctypes.c_int64 * 3)(*[stride[i] if shape[i] > 1 else 0 for i in range(3)])
+    return ctypes.addressof(a), a
+
+
 def _rows_arg(t: Optional[torch.Tensor], name: str, shape: tuple, device) -> tuple:
-    """Address and strides of bf16 rows [sequence][head][token][128], whose channels are
-    contiguous and whose other strides are free (None: no rows)."""
+    """Address and strides (held by the second value) of bf16 rows [sequence][head][token][128],
+    whose channels are contiguous and whose other strides are free (None: no rows)."""
     if t is None:
-        return None, None
-    if t.shape != shape or t.dtype != torch.bfloat16 or t.device != device:
+        return None, (None, None)
+    if t.shape != shape or t.dtype is not torch.bfloat16 or t.device != device:
         raise ValueError(f"{name}: expected torch.bfloat16 {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
-    if t.stride(3) != 1:
+    stride = t.stride()
+    if stride[3] != 1:
         raise ValueError(f"{name}: a row's {HEAD_DIM} channels must be contiguous")
-    return t.data_ptr(), (ctypes.c_int64 * 3)(*[t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)])
+    return t.data_ptr(), _row_strides(shape, stride)
 
 
 def rkv_rotary(plan: RkvRotaryPlan, q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
@@ -723,8 +731,8 @@ def rkv_rotary(plan: RkvRotaryPlan, q: torch.Tensor, k: Optional[torch.Tensor], 
     qo, qos = _rows_arg(q_out, "q_out", (B, Hq, T, HEAD_DIM), dev)
     ko, kos = _rows_arg(k_out, "k_out", (B, Hkv, T, HEAD_DIM), dev)
     at = _arg(positions, "positions", (B, T) if per_token else (B,), torch.int32, dev)
-    _call_on(dev, stream, _lib.rkv_rotary, ctypes.byref(plan), qa, qs, ka, ks, B, Hq, Hkv, T, at, int(per_token),
-             int(inverse), qo, qos, ko, kos)
+    _call_on(dev, stream, _lib.rkv_rotary, ctypes.byref(plan), qa, qs[0], ka, ks[0], B, Hq, Hkv, T, at,
+             int(per_token), int(inverse), qo, qos[0], ko, kos[0])
 
 
 # ------------------------------------------------------------------ the 8-bit cache
@@ -789,7 +797,7 @@ def rkv_q8_append(cache: PagedCache8, k_new: torch.Tensor, v_new: torch.Tensor, 
     T, dev = k_new.shape[2], cache.k_codes.device
     ka, ks = _rows_arg(k_new, "k_new", (cache.B, cache.Hkv, T, HEAD_DIM), dev)
     va, vs = _rows_arg(v_new, "v_new", (cache.B, cache.Hkv, T, HEAD_DIM), dev)
-    _call_on(dev, stream, _lib.rkv_q8_append, ctypes.byref(cache.struct), ka, ks, va, vs, T,
+    _call_on(dev, stream, _lib.rkv_q8_append, ctypes.byref(cache.struct), ka, ks[0], va, vs[0], T,
              _arg(new_len, "new_len", (cache.B,), torch.int32, dev))
 
 
