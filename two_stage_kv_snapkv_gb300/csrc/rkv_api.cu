@@ -132,7 +132,7 @@ const char* kernel_name(int kind) {
       "chunk_gather", "sparq_score",  "sparq_topk",     "sparq_attend", "wait_selftest",
       "sparq_keys_sync", "attend_rows", "attend_tiles", "attend_units", "attend_combine", "attend_weigh", "tree_commit",
       "accum_rows", "accum_tiles", "accum_join", "evict_select", "evict_stage", "evict_compact",
-      "reserve_pages", "rotary", "q8_append", "q8_load", "q8_rows", "q8_tiles", "q8_join"};
+      "reserve_pages", "rotary", "q8_append", "q8_load", "q8_rows", "q8_tiles", "q8_units", "q8_join"};
   return (kind >= 0 && kind < K_NUM_KINDS) ? names[kind] : nullptr;
 }
 

@@ -53,6 +53,7 @@ enum KernelKind {
   K_Q8_LOAD,
   K_Q8_ROWS,
   K_Q8_TILES,
+  K_Q8_UNITS,
   K_Q8_JOIN,
   K_NUM_KINDS
 };

@@ -21,6 +21,8 @@
 // eight warps take a run's chunks in turn, each with its own three-stage TMA ring (192 KB in
 // flight per SM), its own running maximum, sum and fp32 output, and meet once per run.  The
 // parts of a split unit go to the workspace and q8_join joins them.
+#include <cooperative_groups.h>
+
 #include <type_traits>
 
 #include "rkv_q8_attend.cuh"
@@ -61,6 +63,43 @@ struct StageInfo {
   float k[2], v[2];
   uint32_t live;
 };
+
+// A chunk's copies: K and V of the 32 keys from key0 on, whose one or two pages are id0 and id1
+// (-1: none to read); from a whole warp.
+__device__ __forceinline__ void fetch_chunk(const Q8Params& p, uint8_t* st, uint64_t* bar, int id0, int id1, int g, int key0,
+                                            int box, uint64_t policy) {
+  if ((threadIdx.x & 31) != 0) return;
+  const int loads = (id0 >= 0) + (id1 >= 0);
+  if (loads > 0) mbar_arrive_expect_tx(bar, loads * 2 * box * 128);
+  else mbar_arrive(bar);
+  if (id0 >= 0) {
+    const int row = (id0 * p.Hkv + g) * p.P + (key0 & (p.P - 1));
+    tma_load_2d_hint(st, &p.tmk, 0, row, bar, policy);
+    tma_load_2d_hint(st + kQrKeys * 128, &p.tmv, 0, row, bar, policy);
+  }
+  if (id1 >= 0) {
+    const int row = (id1 * p.Hkv + g) * p.P;
+    tma_load_2d_hint(st + box * 128, &p.tmk, 0, row, bar, policy);
+    tma_load_2d_hint(st + kQrKeys * 128 + box * 128, &p.tmv, 0, row, bar, policy);
+  }
+}
+// What the chunk's stage holds besides; left: keys from the chunk's first to the last.  Behind
+// the copies: the scales may still be on their way.
+__device__ __forceinline__ void note_chunk(StageInfo& si, int id0, int id1, int left, int boxes, const float (&sk)[2],
+                                           const float (&sv)[2]) {
+  uint32_t live = left >= kQrKeys ? ~0u : (1u << left) - 1u;
+  if (boxes == 1) {
+    if (id0 < 0) live = 0u;
+  } else {
+    if (id0 < 0) live &= 0xffff0000u;
+    if (id1 < 0) live &= 0x0000ffffu;
+  }
+  si.live = live;
+  si.k[0] = sk[0];
+  si.v[0] = sv[0];
+  si.k[1] = boxes == 1 ? sk[0] : sk[1];
+  si.v[1] = boxes == 1 ? sv[0] : sv[1];
+}
 
 // Queries of a run's rows as the MMA's B fragments, for row tiles whose registers are needed
 // elsewhere: [tile][pair of steps][lane], 16 bytes.
@@ -366,39 +405,8 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
     }
     const int from = (fc - ids_at) / kQrWarps, key0 = fc * kQrKeys;
     const int id0 = __shfl_sync(0xffffffffu, ids[0], from), id1 = __shfl_sync(0xffffffffu, ids[1], from);
-    if (lane == from) {
-      StageInfo& si = info[warp][s];
-      const int left = fr.n - key0;
-      uint32_t live = left >= kQrKeys ? ~0u : (1u << left) - 1u;
-      if (boxes == 1) {
-        if (id0 < 0) live = 0u;
-      } else {
-        if (id0 < 0) live &= 0xffff0000u;
-        if (id1 < 0) live &= 0x0000ffffu;
-      }
-      si.live = live;
-      si.k[0] = sk[0];
-      si.v[0] = sv[0];
-      si.k[1] = boxes == 1 ? sk[0] : sk[1];
-      si.v[1] = boxes == 1 ? sv[0] : sv[1];
-    }
-    if (lane == 0) {
-      uint64_t* bar = &full_b[warp][s];
-      uint8_t* st = ring + s * kQrStageBytes;
-      const int loads = (id0 >= 0) + (id1 >= 0);
-      if (loads > 0) mbar_arrive_expect_tx(bar, loads * 2 * box * 128);
-      else mbar_arrive(bar);
-      if (id0 >= 0) {
-        const int row = (id0 * p.Hkv + fr.g) * p.P + (key0 & (p.P - 1));
-        tma_load_2d_hint(st, &p.tmk, 0, row, bar, policy);
-        tma_load_2d_hint(st + kQrKeys * 128, &p.tmv, 0, row, bar, policy);
-      }
-      if (id1 >= 0) {
-        const int row = (id1 * p.Hkv + fr.g) * p.P;
-        tma_load_2d_hint(st + box * 128, &p.tmk, 0, row, bar, policy);
-        tma_load_2d_hint(st + kQrKeys * 128 + box * 128, &p.tmv, 0, row, bar, policy);
-      }
-    }
+    fetch_chunk(p, ring + s * kQrStageBytes, &full_b[warp][s], id0, id1, fr.g, key0, box, policy);
+    if (lane == from) note_chunk(info[warp][s], id0, id1, fr.n - key0, boxes, sk, sv);
     ++fetched;
     fc += kQrWarps;
     settle();
@@ -487,6 +495,179 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
   // after a timeout: wait (bounded) for what this warp still has in flight
   if (dead)
     for (int i = used; i < fetched; ++i) mbar_wait(&full_b[warp][i % kQrStages], (uint32_t)((i / kQrStages) & 1));
+}
+
+// ---------------------------------------------------------------------------
+// q8_units: the same tile for small caches, where launches and latencies count: one cluster
+// of C CTAs per (sequence, KV head), each with an equal part of the chunks, two stages a warp.
+// The parts meet through distributed shared memory, so there is one launch and no workspace.
+constexpr int kQuStages = 2;
+template <int kN>
+struct UnitsShape8 {
+  static constexpr int kRows = kN * 8;
+  static constexpr int kRing = kQrWarps * kQuStages * kQrStageBytes;  // then the warps' outputs
+  static constexpr int kPart = kRows * kQrMergeStride * 4;            // the CTA's output
+  static_assert(kQrWarps * kPart <= kRing, "the warps' outputs take the ring's place");
+  static constexpr int kSmem = 1024 + kRing + kPart;
+};
+
+template <int kFormat, int kN>
+__global__ void __launch_bounds__(kQrThreads, 1) q8_units_kernel(const __grid_constant__ Q8Params p) {
+  using Sh = UnitsShape8<kN>;
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  constexpr int kRows = Sh::kRows;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ typename std::conditional<(kN > 2), QueryTile<kN>, int>::type queries;
+  __shared__ uint64_t full_b[kQrWarps][kQuStages];
+  __shared__ StageInfo info[kQrWarps][kQuStages];
+  __shared__ float wm[kQrWarps][kRows], wl[kQrWarps][kRows], wv[kQrWarps];
+  __shared__ float2 part_ml[kRows];  // this CTA's (m, l), read by the cluster
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  uint8_t* base = align1024(smem);
+  uint8_t* ring = base + warp * kQuStages * kQrStageBytes;
+  float* merge = reinterpret_cast<float*>(base);
+  float* part_o = reinterpret_cast<float*>(base + Sh::kRing);
+  const int b = blockIdx.y / p.Hkv, g = blockIdx.y % p.Hkv;
+  if (lane == 0) {
+    for (int s = 0; s < kQuStages; ++s) mbar_init(&full_b[warp][s], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  const int n = checked_len(p, b), m = checked_rows(p, b), rows = m * p.G;
+  if (rows == 0) return;  // the same in every CTA of the cluster
+  const int chunks = (n + kQrKeys - 1) / kQrKeys;
+  const int lo = (int)((long long)chunks * rank / C), hi = (int)((long long)chunks * (rank + 1) / C);
+  // page ids and scales of this warp's next 32 chunks, one chunk a lane
+  const int boxes = p.P < kQrKeys ? 2 : 1, box = kQrKeys / boxes;
+  int ids[2] = {-1, -1}, ids_at = 0, fetched = 0, used = 0, fc = lo + warp;
+  float sk[2] = {0.f, 0.f}, sv[2] = {0.f, 0.f};
+  bool dead = false;
+  auto fetch = [&]() {
+    if (fc >= hi) return;
+    const int s = fetched % kQuStages;
+    if (fetched % 32 == 0) {
+      ids_at = fc;
+      const int c = fc + lane * kQrWarps;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int key = c * kQrKeys + h * box;
+        ids[h] = -1;
+        sk[h] = sv[h] = 0.f;
+        if (h < boxes && c < hi && key < n) {
+          const int id = p.page_table[(size_t)b * p.max_pages + (key >> p.pshift)];
+          if (id >= 0 && id < p.num_phys) {
+            ids[h] = id;
+            sk[h] = p.k_scale[(size_t)id * p.Hkv + g];
+            sv[h] = p.v_scale[(size_t)id * p.Hkv + g];
+          } else {
+            flag_error(p.err, RKV_DEVERR_PAGE_ID);
+          }
+        }
+      }
+    }
+    const int from = (fc - ids_at) / kQrWarps, key0 = fc * kQrKeys;
+    const int id0 = __shfl_sync(0xffffffffu, ids[0], from), id1 = __shfl_sync(0xffffffffu, ids[1], from);
+    fetch_chunk(p, ring + s * kQrStageBytes, &full_b[warp][s], id0, id1, g, key0, box, l2_policy(false));
+    if (lane == from) note_chunk(info[warp][s], id0, id1, n - key0, boxes, sk, sv);
+    ++fetched;
+    fc += kQrWarps;
+  };
+  for (int s = 0; s < kQuStages; ++s) fetch();
+  RowTile8<kFormat, kN> tile;
+  uint4 (*qs)[4][32] = nullptr;
+  if constexpr (kN > 2) qs = queries;
+  tile.start(p, b, g, 0, n, m, qs);
+  if (kN > 2) __syncthreads();
+  __syncwarp();
+  for (int c = lo + warp; c < hi; c += kQrWarps) {
+    const int s = used % kQuStages;
+    const bool late = !dead && !mbar_wait(&full_b[warp][s], (uint32_t)((used / kQuStages) & 1));
+    if (__any_sync(0xffffffffu, late)) {
+      if (lane == 0) flag_error(p.err, RKV_DEVERR_TIMEOUT);
+      dead = true;
+    }
+    if (!dead && info[warp][s].live != 0u) tile.step(ring + s * kQrStageBytes, info[warp][s], c * kQrKeys, qs);
+    ++used;
+    __syncwarp();  // every lane has read the stage
+    if (!dead) fetch();
+    __syncwarp();  // what the fetch noted is there
+  }
+  if (dead)
+    for (int i = used; i < fetched; ++i) mbar_wait(&full_b[warp][i % kQuStages], (uint32_t)((i / kQuStages) & 1));
+  tile.finish();
+  const int r = lane >> 2, c4 = lane & 3;
+  if (r == 0) {
+#pragma unroll
+    for (int t = 0; t < kN; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        wm[warp][t * 8 + c4 * 2 + c] = tile.m[t][c];
+        wl[warp][t * 8 + c4 * 2 + c] = tile.l[t][c];
+      }
+    if (lane == 0) wv[warp] = tile.vref * (1.f / kUnit);
+  }
+  __syncthreads();  // every warp is done with its ring: the outputs take its place
+#pragma unroll
+  for (int t = 0; t < kN; ++t)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (t * 8 + c4 * 2 + c < rows) {
+        float* dst = merge + (warp * kRows + t * 8 + c4 * 2 + c) * kQrMergeStride + r * 16;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2)
+          *reinterpret_cast<float4*>(dst + 2 * i) =
+              make_float4(tile.o[t][i][c], tile.o[t][i][2 + c], tile.o[t][i + 1][c], tile.o[t][i + 1][2 + c]);
+      }
+  __syncthreads();
+  for (int i = tid; i < rows * 64; i += kQrThreads) {
+    const int row = i >> 6, d = (i & 63) * 2;
+    float M = kNoMax, L = 0.f, ax = 0.f, ay = 0.f;
+#pragma unroll
+    for (int w = 0; w < kQrWarps; ++w) M = fmaxf(M, wm[w][row]);
+#pragma unroll
+    for (int w = 0; w < kQrWarps; ++w) {
+      const float f = ex2_approx(wm[w][row] - M), fv = f * wv[w];
+      const float2 v = *reinterpret_cast<const float2*>(merge + (w * kRows + row) * kQrMergeStride + d);
+      L += wl[w][row] * f;
+      ax += v.x * fv;
+      ay += v.y * fv;
+    }
+    *reinterpret_cast<float2*>(part_o + row * kQrMergeStride + d) = make_float2(ax, ay);
+    if (d == 0) part_ml[row] = make_float2(M, L);
+  }
+  cluster.sync();  // every CTA's part is in place
+  // rows of the output in turn over the cluster: thread = (row, two channels), eight parts'
+  // reads in flight
+  for (int i = tid; i < rows * 64; i += kQrThreads) {
+    const int row = i >> 6, d = (i & 63) * 2;
+    if (row % C != rank) continue;
+    float2 ml[8], v[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < C) {
+        ml[c] = *cluster.map_shared_rank(&part_ml[row], c);
+        v[c] = *cluster.map_shared_rank(reinterpret_cast<float2*>(part_o + row * kQrMergeStride + d), c);
+      }
+    float M = kNoMax, L = 0.f, ax = 0.f, ay = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < C) M = fmaxf(M, ml[c].x);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < C) {
+        const float f = ex2_approx(ml[c].x - M);
+        L += ml[c].y * f;
+        ax += v[c].x * f;
+        ay += v[c].y * f;
+      }
+    const float inv = inverse_of(L);
+    const size_t orow = out_row(p, b, g, row);
+    *reinterpret_cast<uint32_t*>(p.out + orow * 128 + d) = pack_bf16x2(ax * inv, ay * inv);
+    if (d == 0 && p.lse) p.lse[orow] = lse_of(M, L);
+  }
+  cluster.sync();  // no CTA leaves while another still reads its shared memory
 }
 
 // Joins the parts of the split units, and gives the rows that see nothing their results: one
@@ -603,6 +784,46 @@ cudaError_t launch_rows(const Q8Params& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// Whether q8_units takes the call, with clusters of how many CTAs (0: it does not).  The host
+// knows the caches' capacity, not their lengths.  One wave of CTAs (an SM each) against the line
+// split over all SMs and its join, one token, 8 KV heads, us: 1 x 515 tokens 5.7 (C = 8)
+// against 8.9, 1 x 2563 6.9 against 9.8, 1 x 8000 10.3 against 11.2, 1 x 16000 14.9 against
+// 13.4; 2 x 4000 10.2 (C = 4: only about nine clusters of eight lie on the SMs at a time)
+// against 10.2; 4 x 8000 15.2 (C = 4) against 19.3; 8 x 4000 15.1 (C = 2) against 19.2; 16 x
+// 3000 21.3 (C = 1) against 23.9.  So up to 1024 tokens a CTA, and three times that where the
+// CTAs are most of the SMs.
+int units_cluster(const Q8AttendArgs& a, int tile) {
+  const rkv_cache8& c = a.cache;
+  const long long units = (long long)c.B * c.Hkv;
+  if (tile > 24 || units > 152) return 0;
+  const int C = units <= 9 ? 8 : (units <= 36 ? 4 : (units <= 76 ? 2 : 1));
+  return c.max_pages * c.page_size <= C * (units * C >= 120 ? 3000 : 1024) ? C : 0;
+}
+
+template <int kFormat, int kN>
+cudaError_t launch_units(const Q8Params& p, int C, cudaStream_t s) {
+  static SmemOptIn opt;
+  const int smem = UnitsShape8<kN>::kSmem;
+  cudaError_t e = opt.raise(reinterpret_cast<const void*>(q8_units_kernel<kFormat, kN>), smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C, (unsigned)(p.B * p.Hkv));
+  cfg.blockDim = dim3(kQrThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  launch_begin(K_Q8_UNITS, s);
+  e = cudaLaunchKernelEx(&cfg, q8_units_kernel<kFormat, kN>, p);
+  launch_end(K_Q8_UNITS, s);
+  return e;
+}
+
 }  // namespace
 
 size_t q8_attend_ws_bytes(int B, int Hq, int Hkv, int T, int max_pages, int page_size) {
@@ -619,6 +840,11 @@ cudaError_t launch_q8_attend(const Q8AttendArgs& a, cudaStream_t s) {
   p.part_o = static_cast<float*>(a.ws);
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(a.ws) + align256(rows * 128 * 4));
   const bool int8 = a.cache.format == RKV_Q8_INT8;
+  if (const int C = units_cluster(a, tile)) {
+    if (tile == 8) return int8 ? launch_units<RKV_Q8_INT8, 1>(p, C, s) : launch_units<RKV_Q8_E4M3, 1>(p, C, s);
+    if (tile == 16) return int8 ? launch_units<RKV_Q8_INT8, 2>(p, C, s) : launch_units<RKV_Q8_E4M3, 2>(p, C, s);
+    return int8 ? launch_units<RKV_Q8_INT8, 3>(p, C, s) : launch_units<RKV_Q8_E4M3, 3>(p, C, s);
+  }
   void (*join)(Q8Params);
   switch (tile) {
     case 8:
