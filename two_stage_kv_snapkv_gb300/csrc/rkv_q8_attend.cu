@@ -30,14 +30,13 @@
 namespace rkv {
 namespace {
 
-constexpr int kQrWarps = 8;
-constexpr int kQrThreads = kQrWarps * 32;
 constexpr int kQrKeysShift = 5, kQrKeys = 1 << kQrKeysShift;
-constexpr int kQrStages = 3;
 constexpr int kQrStageBytes = 2 * kQrKeys * 128;
 constexpr int kQrPad = 8;                         // what a run costs, in chunks
-constexpr int kQrMergeRows = 4;                   // rows of every warp that meet at a time
 constexpr int kQrMergeStride = 132;               // floats
+constexpr int kQrWarps = 8, kQrThreads = kQrWarps * 32;
+constexpr int kQrStages = 3;
+constexpr int kQrMergeRows = 4;                   // rows of every warp that meet at a time
 constexpr int kQrSmem = 1024 + kQrWarps * kQrStages * kQrStageBytes + kQrWarps * kQrMergeRows * kQrMergeStride * 4;
 constexpr float kLowestUnit = 3.009265538105056e-36f;  // 2^-118: 2^7 / vref stays finite
 
@@ -110,9 +109,9 @@ using QueryTile = uint4[kN][4][32];
 // channels (second); a lane's query rows are the columns 2 (lane % 4) and the next of every
 // tile.  qb: the queries, step s of 16 channels: lane quarter c of a key's bytes 32 c + 4 s ..
 // + 3.  o: channels 16 (lane / 4) + 2 i and + 1 of them for i < 8, times kUnit / vref.
-template <int kFormat, int kN>
+// kShared: the queries lie in shared memory.
+template <int kFormat, int kN, bool kShared>
 struct RowTile8 {
-  static constexpr bool kShared = kN > 2;  // the queries lie in shared memory
   uint32_t qb[kShared ? 1 : kN][8][2];
   float o[kN][8][4];
   float m[kN][2], l[kN][2], factor[kN][2];  // factor: from the product to base-2 logits, without the key's scale
@@ -120,7 +119,7 @@ struct RowTile8 {
   float vref;
   int least;  // the fewest keys that a row sees
 
-  // qs, kShared: where the queries go, each warp those of the tiles warp, warp + 8, ..
+  // qs, kShared: where the queries go, warp t those of tile t
   __device__ __forceinline__ void start(const Q8Params& p, int b, int g, int rt, int n, int rows_m, uint4 (*qs)[4][32]) {
     const int lane = threadIdx.x & 31, rows = rows_m * p.G, r0 = rt * kN * 8;
 #pragma unroll
@@ -334,12 +333,13 @@ struct RowTile8 {
 
 template <int kFormat, int kN>
 __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_constant__ Q8Params p) {
+  constexpr bool kShared = kN > 2;
   constexpr int kRows = kN * 8, kPartRows = kN == 3 ? 32 : kRows;
   // three tiles are a unit's only ones: their line is that of four
   using Line = LineLengths<RowsLine<kN == 1 ? 3 : (kN == 2 ? 4 : 5)>>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Line line;
-  __shared__ typename std::conditional<(kN > 2), QueryTile<kN>, int>::type queries;
+  __shared__ typename std::conditional<kShared, QueryTile<kN>, int>::type queries;
   __shared__ uint64_t full_b[kQrWarps][kQrStages];
   __shared__ StageInfo info[kQrWarps][kQrStages];
   __shared__ float wm[kQrWarps][kRows], wl[kQrWarps][kRows], wv[kQrWarps];
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
   const long long x0 = flat_first(total, blockIdx.x, N), x1 = flat_first(total, blockIdx.x + 1, N);
   auto next_run = [&](long long x, CausalRun& r) { return line.next(p.B, p.Hkv, p.gshift, x, x0, x1, r); };
 
-  // this warp's chunks of a run: lo + warp, lo + warp + 8, ...  The fetch side walks the
+  // this warp's chunks of a run: lo + warp, lo + warp + kQrWarps, ...  The fetch side walks the
   // runs ahead of the compute side.
   CausalRun fr;
   bool more = next_run(x0, fr);
@@ -415,13 +415,13 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
   __syncwarp();
 
   CausalRun cr;
-  RowTile8<kFormat, kN> tile;
+  RowTile8<kFormat, kN, kShared> tile;
   for (long long x = x0; next_run(x, cr); x = cr.next) {
     const int b = cr.b, g = cr.g, rt = cr.rt, rows = cr.m * p.G;
     uint4 (*qs)[4][32] = nullptr;
-    if constexpr (kN > 2) qs = queries;
+    if constexpr (kShared) qs = queries;
     tile.start(p, b, g, rt, cr.n, cr.m, qs);
-    if (kN > 2) __syncthreads();  // the queries are there (the last run's were used up before its warps met)
+    if (kShared) __syncthreads();  // the queries are there (the last run's were used up before its warps met)
     for (int c = cr.lo + warp; c < cr.hi; c += kQrWarps) {
       const int s = used % kQrStages;
       const bool late = !dead && !mbar_wait(&full_b[warp][s], (uint32_t)((used / kQrStages) & 1));
@@ -448,26 +448,26 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
         }
       if (lane == 0) wv[warp] = tile.vref * (1.f / kUnit);
     }
-    // the warps meet, four rows at a time: thread = (row, two channels)
+    // the warps meet, a few rows at a time: thread = (row, two channels)
     const int live = min(kRows, rows - rt * kRows);
     const size_t slot = 2 * (size_t)blockIdx.x + (cr.first ? 0 : 1);
 #pragma unroll
-    for (int quarter = 0; quarter < kRows / kQrMergeRows; ++quarter) {
-      if (quarter * kQrMergeRows >= live) break;
-      if ((c4 >> 1) == (quarter & 1)) {
+    for (int q0 = 0; q0 < kRows; q0 += kQrMergeRows) {
+      if (q0 >= live) break;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float* dst = merge + (warp * kQrMergeRows + (c4 & 1) * 2 + c) * kQrMergeStride + r * 16;
+      for (int c = 0; c < 2; ++c) {
+        const int sub = c4 * 2 + c - (q0 & 7);  // this lane's row among those that meet
+        if (sub >= 0 && sub < kQrMergeRows) {
+          float* dst = merge + (warp * kQrMergeRows + sub) * kQrMergeStride + r * 16;
 #pragma unroll
           for (int i = 0; i < 8; i += 2)
-            *reinterpret_cast<float4*>(dst + 2 * i) =
-                make_float4(tile.o[quarter >> 1][i][c], tile.o[quarter >> 1][i][2 + c], tile.o[quarter >> 1][i + 1][c],
-                            tile.o[quarter >> 1][i + 1][2 + c]);
+            *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(tile.o[q0 >> 3][i][c], tile.o[q0 >> 3][i][2 + c],
+                                                                  tile.o[q0 >> 3][i + 1][c], tile.o[q0 >> 3][i + 1][2 + c]);
         }
       }
       __syncthreads();
-      const int sub = tid >> 6, d = (tid & 63) * 2, row = quarter * kQrMergeRows + sub, rr = rt * kRows + row;
-      if (row < live) {
+      const int sub = tid >> 6, d = (tid & 63) * 2, row = q0 + sub, rr = rt * kRows + row;
+      if (sub < kQrMergeRows && row < live) {
         float M = kNoMax, L = 0.f, ax = 0.f, ay = 0.f;
 #pragma unroll
         for (int w = 0; w < kQrWarps; ++w) M = fmaxf(M, wm[w][row]);
@@ -501,27 +501,30 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
 // q8_units: the same tile for small caches, where launches and latencies count: one cluster
 // of C CTAs per (sequence, KV head), each with an equal part of the chunks, two stages a warp.
 // The parts meet through distributed shared memory, so there is one launch and no workspace.
+// Twelve warps (a short cache's chunks in one round) where their 168 registers do.
 constexpr int kQuStages = 2;
 template <int kN>
 struct UnitsShape8 {
+  static constexpr int kWarps = kN == 3 ? 8 : 12, kThreads = kWarps * 32;
   static constexpr int kRows = kN * 8;
-  static constexpr int kRing = kQrWarps * kQuStages * kQrStageBytes;  // then the warps' outputs
+  static constexpr int kRing = kWarps * kQuStages * kQrStageBytes;  // then the warps' outputs
   static constexpr int kPart = kRows * kQrMergeStride * 4;            // the CTA's output
-  static_assert(kQrWarps * kPart <= kRing, "the warps' outputs take the ring's place");
+  static_assert(kWarps * kPart <= kRing, "the warps' outputs take the ring's place");
   static constexpr int kSmem = 1024 + kRing + kPart;
 };
 
 template <int kFormat, int kN>
-__global__ void __launch_bounds__(kQrThreads, 1) q8_units_kernel(const __grid_constant__ Q8Params p) {
+__global__ void __launch_bounds__(UnitsShape8<kN>::kThreads, 1) q8_units_kernel(const __grid_constant__ Q8Params p) {
   using Sh = UnitsShape8<kN>;
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
-  constexpr int kRows = Sh::kRows;
+  constexpr bool kShared = kN > 1;  // twelve warps leave 168 registers
+  constexpr int kWarps = Sh::kWarps, kRows = Sh::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ typename std::conditional<(kN > 2), QueryTile<kN>, int>::type queries;
-  __shared__ uint64_t full_b[kQrWarps][kQuStages];
-  __shared__ StageInfo info[kQrWarps][kQuStages];
-  __shared__ float wm[kQrWarps][kRows], wl[kQrWarps][kRows], wv[kQrWarps];
+  __shared__ typename std::conditional<kShared, QueryTile<kN>, int>::type queries;
+  __shared__ uint64_t full_b[kWarps][kQuStages];
+  __shared__ StageInfo info[kWarps][kQuStages];
+  __shared__ float wm[kWarps][kRows], wl[kWarps][kRows], wv[kWarps];
   __shared__ float2 part_ml[kRows];  // this CTA's (m, l), read by the cluster
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_units_kernel(const __grid_co
     const int s = fetched % kQuStages;
     if (fetched % 32 == 0) {
       ids_at = fc;
-      const int c = fc + lane * kQrWarps;
+      const int c = fc + lane * kWarps;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int key = c * kQrKeys + h * box;
@@ -567,21 +570,21 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_units_kernel(const __grid_co
         }
       }
     }
-    const int from = (fc - ids_at) / kQrWarps, key0 = fc * kQrKeys;
+    const int from = (fc - ids_at) / kWarps, key0 = fc * kQrKeys;
     const int id0 = __shfl_sync(0xffffffffu, ids[0], from), id1 = __shfl_sync(0xffffffffu, ids[1], from);
     fetch_chunk(p, ring + s * kQrStageBytes, &full_b[warp][s], id0, id1, g, key0, box, l2_policy(false));
     if (lane == from) note_chunk(info[warp][s], id0, id1, n - key0, boxes, sk, sv);
     ++fetched;
-    fc += kQrWarps;
+    fc += kWarps;
   };
   for (int s = 0; s < kQuStages; ++s) fetch();
-  RowTile8<kFormat, kN> tile;
+  RowTile8<kFormat, kN, kShared> tile;
   uint4 (*qs)[4][32] = nullptr;
-  if constexpr (kN > 2) qs = queries;
+  if constexpr (kShared) qs = queries;
   tile.start(p, b, g, 0, n, m, qs);
-  if (kN > 2) __syncthreads();
+  if (kShared) __syncthreads();
   __syncwarp();
-  for (int c = lo + warp; c < hi; c += kQrWarps) {
+  for (int c = lo + warp; c < hi; c += kWarps) {
     const int s = used % kQuStages;
     const bool late = !dead && !mbar_wait(&full_b[warp][s], (uint32_t)((used / kQuStages) & 1));
     if (__any_sync(0xffffffffu, late)) {
@@ -621,13 +624,13 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_units_kernel(const __grid_co
               make_float4(tile.o[t][i][c], tile.o[t][i][2 + c], tile.o[t][i + 1][c], tile.o[t][i + 1][2 + c]);
       }
   __syncthreads();
-  for (int i = tid; i < rows * 64; i += kQrThreads) {
+  for (int i = tid; i < rows * 64; i += Sh::kThreads) {
     const int row = i >> 6, d = (i & 63) * 2;
     float M = kNoMax, L = 0.f, ax = 0.f, ay = 0.f;
 #pragma unroll
-    for (int w = 0; w < kQrWarps; ++w) M = fmaxf(M, wm[w][row]);
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w][row]);
 #pragma unroll
-    for (int w = 0; w < kQrWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       const float f = ex2_approx(wm[w][row] - M), fv = f * wv[w];
       const float2 v = *reinterpret_cast<const float2*>(merge + (w * kRows + row) * kQrMergeStride + d);
       L += wl[w][row] * f;
@@ -640,7 +643,7 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_units_kernel(const __grid_co
   cluster.sync();  // every CTA's part is in place
   // rows of the output in turn over the cluster: thread = (row, two channels), eight parts'
   // reads in flight
-  for (int i = tid; i < rows * 64; i += kQrThreads) {
+  for (int i = tid; i < rows * 64; i += Sh::kThreads) {
     const int row = i >> 6, d = (i & 63) * 2;
     if (row % C != rank) continue;
     float2 ml[8], v[8];
@@ -808,7 +811,7 @@ cudaError_t launch_units(const Q8Params& p, int C, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, (unsigned)(p.B * p.Hkv));
-  cfg.blockDim = dim3(kQrThreads);
+  cfg.blockDim = dim3(UnitsShape8<kN>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
