@@ -481,17 +481,19 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
       const bool v = warp == 18;
       const CUtensorMap* map = v ? &p.tmv : &p.tmk;
       const bool lead = elect_lane();
-      const int pages = kQtKeys >> p.pshift, box = p.P * 128, per_page = p.P >> 4;  // of a tile; bytes; 16-key groups
+      const int pages = kQtKeys >> p.pshift, box = p.P * 128, gs = p.pshift - 4;  // of a tile; bytes; 2^gs 16-key groups a page
       const uint64_t policy = l2_policy(!kWide && (long long)p.T * p.G <= R);  // one row tile: read once
       RingAt<Sh::kCodes> at;
       bool ok = true;
       while (ok && next_run(r, ok)) {
         const int b = r.b, g = r.g, n = r.n, nt = r.hi - r.lo;
-        // lane j: the tile's page j and its scales; loaded ahead, so that the loads' latency stays
-        // off the ring
-        auto page_of = [&](int tile) {
+        // Page ids and scales of 32 pages (4 to 16 tiles), one a lane, and of the 32 behind them
+        // on their way: a tile's own loads, one behind the other, took 2700 clocks of the 3000 a
+        // tile of the narrow form.
+        const int batch = 32 / pages;  // tiles
+        auto page_at = [&](int tile) {  // of this lane, in the batch that begins with `tile`
           const int pg = tile * pages + lane;
-          return lane < pages && pg * p.P < n ? p.page_table[(size_t)b * p.max_pages + pg] : -1;
+          return pg * p.P < min(n, r.hi * kQtKeys) ? p.page_table[(size_t)b * p.max_pages + pg] : -1;
         };
         auto scales_of = [&](int phys, float& sk, float& sv) {
           sk = sv = 0.f;
@@ -500,19 +502,27 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
             sv = p.v_scale[(size_t)phys * p.Hkv + g];
           }
         };
-        int next = page_of(r.lo), after = nt > 1 ? page_of(r.lo + 1) : -1, unit = -126;
-        float nk, nv;
-        scales_of(next, nk, nv);
+        int ids = page_at(r.lo), next_ids = page_at(r.lo + batch), unit = -126, in = 0;  // in: tiles of the batch behind us
+        float ks, vs, next_ks = 0.f, next_vs = 0.f;
+        scales_of(ids, ks, vs);
         for (int i = 0; i < nt; ++i) {
           const int tile = r.lo + i;
-          int phys = next;
-          const float sk = nk, sv = nv;
-          next = after;
-          after = i + 2 < nt ? page_of(tile + 2) : -1;
-          scales_of(next, nk, nv);
+          if (in == batch) {
+            in = 0;
+            ids = next_ids;
+            ks = next_ks;
+            vs = next_vs;
+            next_ids = page_at(tile + batch);
+          }
+          if (in == batch - 1) scales_of(next_ids, next_ks, next_vs);
+          const int from = in * pages + (lane & (pages - 1));
+          int phys = __shfl_sync(0xffffffffu, ids, from);
+          const float sk = __shfl_sync(0xffffffffu, ks, from), sv = __shfl_sync(0xffffffffu, vs, from);
+          ++in;
           const int c = at.slot;
           if (at.use > 0 && !(ok = wait(&sh.empty_c[v][c], at.use - 1))) break;
           const bool mine = lane < pages && (tile * pages + lane) * p.P < n;
+          if (!mine) phys = -1;
           if (phys < 0 || phys >= p.num_phys) {
             if (mine) flag_error(p.err, RKV_DEVERR_PAGE_ID);
             phys = -1;
@@ -524,13 +534,11 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
           const int ek = __reduce_max_sync(0xffffffffu, phys >= 0 && xk < 255 ? xk : 1) - 127;
           TileInfo& ti = sh.info[v][loaded % kQtInfos];
           const int mx = v ? xv : xk, me = v ? unit : ek;
-          if (lane < pages)
-            for (int j = 0; j < per_page; ++j)
-              ti.d[lane * per_page + j] = (uint8_t)(mx == 255 ? kNoFactor : min(max(me - (mx - 127), 0), 254));
+          // lanes 0 .. 7: the 16-key groups
+          const int below = mx == 255 ? kNoFactor : min(max(me - (mx - 127), 0), 254), d = __shfl_sync(0xffffffffu, below, lane >> gs);
+          const uint32_t gr = __ballot_sync(0xffffffffu, lane < 8 && ((have >> (lane >> gs)) & 1u));
+          if (lane < 8) ti.d[lane] = (uint8_t)d;
           if (lead) {
-            uint32_t gr = 0;
-            for (int j = 0; j < pages; ++j)
-              if ((have >> j) & 1u) gr |= ((1u << per_page) - 1u) << (j * per_page);
             ti.groups = gr;
             ti.e = (int16_t)me;
             ti.unit = (int16_t)unit;
