@@ -666,11 +666,14 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
     }
   } else {
     // codes to fp16, K's (warps 20-23) and V's: a warp's 32 keys of a tile, four keys of eight
-    // 16-code pieces at a time
+    // 16-code pieces at a time.
     setmaxnreg_dec<kQtCodeRegs>();
     const bool v = warp >= 24;
-    const int quarter = warp & 3, sub = lane >> 3, piece = lane & 7;
-    const uint32_t from = (uint32_t)((piece ^ sub) << 4), place_a = (uint32_t)((((piece & 3) * 2) ^ sub) << 4);
+    // Eight lanes of a 16-byte access (its turn at the banks) have four pieces of the rows x and x
+    // ^ 5: the swizzle puts those of either load, and the even or odd pieces of either store, on
+    // different banks.  A warp takes rows 0, 5, 1, 4 of eight, then 2, 7, 3, 6 (two rows on).
+    const int quarter = warp & 3, piece = (lane & 3) | ((lane >> 4) << 2), row8 = ((lane >> 3) & 1) ^ (lane & 4 ? 5 : 0);
+    const uint32_t from = (uint32_t)((piece ^ row8) << 4), place_a = (uint32_t)((((piece & 3) * 2) ^ row8) << 4);
     RingAt<Sh::kCodes> at;
     int tile_no = 0;
     bool ok = true;
@@ -683,24 +686,24 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         const int left = r.n - (r.lo + i) * kQtKeys;
         const uint32_t gr = ti.groups;
         const int d0 = ti.d[quarter * 2], d1 = ti.d[quarter * 2 + 1];
-        const uint8_t* const src = sh.codes[v] + c * kQtCodes + (quarter * 32 + sub) * 128;
+        const uint8_t* const src = sh.codes[v] + c * kQtCodes + (quarter * 32 + row8) * 128;
         if (tile_no > 0 && !(ok = wait(&sh.empty[v], tile_no - 1))) break;
-        uint8_t* const dst = sh.ops[v] + (piece >> 2) * (kQtTile / 2) + (quarter * 32 + sub) * 128;
-        // row quarter * 32 + h * 16 + k * 4 + sub: row % 8 is sub or, for odd k, sub + 4
+        uint8_t* const dst = sh.ops[v] + (piece >> 2) * (kQtTile / 2) + (quarter * 32 + row8) * 128;
+        auto row_of = [](int h, int k) { return h * 16 + (k >> 1) * 8 + (k & 1) * 2; };  // and row8
         auto put = [&](int h, int k, const uint32_t (&a)[4], const uint32_t (&c4)[4]) {
-          const uint32_t at_a = (k & 1) ? place_a ^ 64u : place_a;  // the pieces' numbers XOR row % 8
-          *reinterpret_cast<uint4*>(dst + (h * 16 + k * 4) * 128 + at_a) = make_uint4(a[0], a[1], a[2], a[3]);
-          *reinterpret_cast<uint4*>(dst + (h * 16 + k * 4) * 128 + (at_a ^ 16u)) = make_uint4(c4[0], c4[1], c4[2], c4[3]);
+          const uint32_t at_a = (k & 1) ? place_a ^ 32u : place_a;  // the pieces' numbers XOR row % 8
+          *reinterpret_cast<uint4*>(dst + row_of(h, k) * 128 + at_a) = make_uint4(a[0], a[1], a[2], a[3]);
+          *reinterpret_cast<uint4*>(dst + row_of(h, k) * 128 + (at_a ^ 16u)) = make_uint4(c4[0], c4[1], c4[2], c4[3]);
         };
         // one branch for the whole tile: in the unrolled loop, a few of them cost 430 clocks a key row
         const bool plain = max(d0, d1) <= 9 && (!v || (left >= kQtKeys && gr == 0xffu));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // the warp's two 16-key groups
-          const int d = h ? d1 : d0, row0 = quarter * 32 + h * 16 + sub;
+          const int d = h ? d1 : d0;
           uint4 w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            w[k] = *reinterpret_cast<const uint4*>(src + (h * 16 + k * 4) * 128 + ((k & 1) ? from ^ 64u : from));
+            w[k] = *reinterpret_cast<const uint4*>(src + row_of(h, k) * 128 + ((k & 1) ? from ^ 32u : from));
           }
           if (h == 1) {
             __syncwarp();
@@ -735,7 +738,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
             const __half2 f2 = half_power(d == kNoFactor ? 0 : min(max(d - 14, 0), 24));
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int row = row0 + k * 4;
+              const int row = quarter * 32 + row8 + row_of(h, k);
               const bool none = v && (row >= left || d == kNoFactor || !((gr >> (row >> 4)) & 1u));
               uint32_t a[4], c4[4];
               decode4<kFormat>(w[k].x, a[0], a[1]);
