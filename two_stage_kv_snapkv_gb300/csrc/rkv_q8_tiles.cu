@@ -62,25 +62,23 @@ template <bool kWide>
 struct TileShape8 {
   static constexpr int kRows = kWide ? 256 : 128;
   static constexpr int kQBytes = kRows * 256;
-  // K and V each have one operand and a ring of three tiles of codes (two: 282 us instead of
-  // 212 for 32 rows over 16 x 20000 tokens; a second operand in place of one: no change).  Each
-  // has one producer and one consumer that go through every slot's phases in order: a wait by
-  // parity cannot tell a phase from the one two before.
-  static constexpr int kCodes = 3;
+  // K and V each have a ring of operands and one of codes, with one producer and one consumer
+  // that go through every slot's phases in order: a wait by parity cannot tell a phase from the
+  // one two before.
+  static constexpr int kOps = kWide ? 1 : 2, kCodes = kWide ? 3 : 2;
   using Line = TileLine<kWide ? 8 : 7>;
   struct Shared {
     uint8_t q[kQBytes];
-    uint8_t ops[2][kQtTile];
+    uint8_t ops[2][kOps * kQtTile];
     uint8_t codes[2][kCodes * kQtCodes];
     Line line;
-    uint64_t full_c[2][kCodes], empty_c[2][kCodes], full[2], empty[2], s[2], p[2], o[2], qf[2], out[2], ml, drained;
+    uint64_t full_c[2][kCodes], empty_c[2][kCodes], full[2][kOps], empty[2][kOps], s[2], p[2], o[2], qf[2], out[2], ml, drained;
     TileInfo info[2][kQtInfos];
     RunInfo runs[kQtRuns];
     uint64_t full_r[kQtRuns], empty_r[kQtRuns];
     uint32_t tmem_base;
     int abort_flag;
     int8_t row_exp[kRows];
-    float2 ml_s[kWide ? 1 : 4][kWide ? 1 : 128];
   };
   static constexpr int kSmem = sizeof(Shared);
   static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -135,8 +133,10 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int v = 0; v < 2; ++v) {
-      mbar_init(&sh.full[v], 4);  // the four warps that wrote it
-      mbar_init(&sh.empty[v], 1);
+      for (int e = 0; e < Sh::kOps; ++e) {
+        mbar_init(&sh.full[v][e], 4);  // the four warps that wrote it
+        mbar_init(&sh.empty[v][e], 1);
+      }
       for (int c = 0; c < Sh::kCodes; ++c) {
         mbar_init(&sh.full_c[v][c], 1);
         mbar_init(&sh.empty_c[v][c], 4);
@@ -389,14 +389,18 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         vote(false);
         l += sums[(half ^ 1) * 128 + row];
       } else {
-        // both slots' sums, and their outputs' factors to the joint maximum
-        sh.ml_s[slot * 2 + half][row] = make_float2(m, l);
-        arrive(&sh.ml);
-        if (!(ok = wait(&sh.ml, run))) break;
+        // both slots' maxima and sums, through the query tile's memory (its products are done),
+        // and their outputs' factors to the joint maximum
         if (!(ok = wait(&sh.o[0], done[0]++))) break;
         if (has[1] && !(ok = wait(&sh.o[1], done[1]++))) break;
-        const float2 a = sh.ml_s[0][row], c = has[1] ? sh.ml_s[2][row] : make_float2(kNoMax, 0.f);
-        const float la = a.y + sh.ml_s[1][row].y, lc = has[1] ? c.y + sh.ml_s[3][row].y : 0.f;
+        float2* const ml_s = reinterpret_cast<float2*>(sh.q);
+        ml_s[(slot * 2 + half) * 128 + row] = make_float2(m, l);
+        arrive(&sh.ml);
+        if (!(ok = wait(&sh.ml, 2 * run))) break;
+        const float2 a = ml_s[row], c = has[1] ? ml_s[256 + row] : make_float2(kNoMax, 0.f);
+        const float la = a.y + ml_s[128 + row].y, lc = has[1] ? c.y + ml_s[384 + row].y : 0.f;
+        arrive(&sh.ml);  // read, before outputs are staged there
+        if (!(ok = wait(&sh.ml, 2 * run + 1))) break;
         m = fmaxf(a.x, c.x);
         f0 = ex2_approx(a.x - m);
         f1 = ex2_approx(c.x - m);
@@ -584,14 +588,15 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
     } else if (warp == 17) {
       constexpr uint32_t idesc_s = idesc_f16_f32(128, 128), idesc_o = idesc_s | kIdescBNMajor;
       const uint32_t q32 = smem_u32(sh.q), k32 = smem_u32(sh.ops[0]), v32 = smem_u32(sh.ops[1]);
-      int seen_p[2] = {0, 0}, run = 0, taken[2] = {0, 0};
+      int seen_p[2] = {0, 0}, run = 0;
+      RingAt<Sh::kOps> kat, vat;
       bool ok = true;
       const bool lead = elect_lane();
       const uint32_t qlo = sw128_kmajor_lo(q32), klo = sw128_kmajor_lo(k32), vlo = sw128_nmajor_lo(v32, kQtTile / 2);
       // S of `slot` from the K operand
-      auto mma_s = [&](int slot, bool release) {
+      auto mma_s = [&](int slot, int e, bool release) {
         tc_fence_after();
-        uint32_t d = tmem + slot * 256, qa = qlo + (kWide ? slot * (128 * 256 >> 4) : 0), ka = klo;
+        uint32_t d = tmem + slot * 256, qa = qlo + (kWide ? slot * (128 * 256 >> 4) : 0), ka = klo + e * (kQtTile >> 4);
         // worked out anew each time: kept over the loop, the steps' addresses spill
         asm volatile("" : "+r"(d), "+r"(qa), "+r"(ka));
         tc_mma_ss<false>(lead, d, qa, ka, idesc_s);
@@ -600,49 +605,56 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
           const uint32_t off = ((k >> 2) * (kQtTile / 2) + (k & 3) * 32) >> 4;
           tc_mma_ss<true>(lead, d, qa + off, ka + off, idesc_s);
         }
-        tc_commit_if(lead && release, &sh.empty[0]);
+        tc_commit_if(lead && release, &sh.empty[0][e]);
         tc_commit_if(lead, &sh.s[slot]);
         if (lead) mbar_arrive(&sh.s[slot]);
         __syncwarp();
       };
       // O += P V once the slot's weights are there
-      auto mma_o = [&](int slot, bool first, bool last, bool release) {
+      auto mma_o = [&](int slot, int e, bool first, bool last, bool release) {
         if (!(ok = wait(&sh.p[slot], seen_p[slot]++))) return;
         tc_fence_after();
-        uint32_t d = tmem + slot * 256 + 128, pa = tmem + slot * 256, va = vlo;
+        uint32_t d = tmem + slot * 256 + 128, pa = tmem + slot * 256, va = vlo + e * (kQtTile >> 4);
         asm volatile("" : "+r"(d), "+r"(pa), "+r"(va));
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           tc_mma_ts(lead, d, pa + (k >> 2) * 64 + (k & 3) * 8, va + (k * 2048 >> 4), idesc_o, (first && k == 0) ? 0u : 1u);
-        tc_commit_if(lead && release, &sh.empty[1]);
+        tc_commit_if(lead && release, &sh.empty[1][e]);
         tc_commit_if(lead && last, &sh.o[slot]);
       };
       while (ok && next_run(r, ok)) {
         const int nt = r.hi - r.lo;
         const bool two = kWide && r.m * p.G - r.rt * R > 128;  // slot 1 has rows
-        auto take = [&](int v) { return ok = wait(&sh.full[v], taken[v]++); };  // K's or V's next operand, written
+        int ek = 0, ev = 0;
+        auto take = [&](int v) {  // K's or V's next operand, written
+          RingAt<Sh::kOps>& at = v ? vat : kat;
+          (v ? ev : ek) = at.slot;
+          ok = wait(&sh.full[v][at.slot], at.use);
+          at.step();
+          return ok;
+        };
         ok = wait(&sh.qf[0], run);
         if (kWide && ok) ok = wait(&sh.qf[1], run);
         if (!ok) break;
         ++run;
         if (!take(0)) break;
-        mma_s(0, !two);
-        if (two) mma_s(1, true);
+        mma_s(0, ek, !two);
+        if (two) mma_s(1, ek, true);
         if (kWide) {
           for (int i = 0; i < nt; ++i) {
             if (!take(1)) break;
             const bool last = i + 1 == nt;
-            mma_o(0, i == 0, last, !two);
+            mma_o(0, ev, i == 0, last, !two);
             if (!ok) break;
             tc_commit_if(lead && last && !two, &sh.o[1]);  // keeps an idle slot in step
             if (!last) {
               if (!take(0)) break;
-              mma_s(0, !two);
+              mma_s(0, ek, !two);
             }
             if (two) {
-              mma_o(1, i == 0, last, true);
+              mma_o(1, ev, i == 0, last, true);
               if (!ok) break;
-              if (!last) mma_s(1, true);
+              if (!last) mma_s(1, ek, true);
             }
           }
         } else {
@@ -651,10 +663,10 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
             if (i + 1 < nt) {
               // tile i + 1's logits go where tile i - 1's weights lay: its product was issued before
               if (!take(0)) break;
-              mma_s(slot ^ 1, true);
+              mma_s(slot ^ 1, ek, true);
             }
             if (!take(1)) break;
-            mma_o(slot, i < 2, i + 2 >= nt, true);
+            mma_o(slot, ev, i < 2, i + 2 >= nt, true);
             if (!ok) break;
           }
         }
@@ -662,7 +674,11 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
       // the last operands' releases land before the CTA may exit
       if (ok)
         for (int v = 0; v < 2; ++v)
-          if (taken[v] > 0) mbar_wait(&sh.empty[v], (uint32_t)((taken[v] - 1) & 1));
+          for (int e = 0; e < Sh::kOps; ++e) {  // the last use of each slot
+            const RingAt<Sh::kOps>& at = v ? vat : kat;
+            const int use = e < at.slot ? at.use : at.use - 1;
+            if (use >= 0) mbar_wait(&sh.empty[v][e], (uint32_t)(use & 1));
+          }
     }
   } else {
     // codes to fp16, K's (warps 20-23) and V's: a warp's 32 keys of a tile, four keys of eight
@@ -675,6 +691,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
     const int quarter = warp & 3, piece = (lane & 3) | ((lane >> 4) << 2), row8 = ((lane >> 3) & 1) ^ (lane & 4 ? 5 : 0);
     const uint32_t from = (uint32_t)((piece ^ row8) << 4), place_a = (uint32_t)((((piece & 3) * 2) ^ row8) << 4);
     RingAt<Sh::kCodes> at;
+    RingAt<Sh::kOps> to;
     int tile_no = 0;
     bool ok = true;
     while (ok && next_run(r, ok)) {
@@ -687,8 +704,8 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         const uint32_t gr = ti.groups;
         const int d0 = ti.d[quarter * 2], d1 = ti.d[quarter * 2 + 1];
         const uint8_t* const src = sh.codes[v] + c * kQtCodes + (quarter * 32 + row8) * 128;
-        if (tile_no > 0 && !(ok = wait(&sh.empty[v], tile_no - 1))) break;
-        uint8_t* const dst = sh.ops[v] + (piece >> 2) * (kQtTile / 2) + (quarter * 32 + row8) * 128;
+        if (to.use > 0 && !(ok = wait(&sh.empty[v][to.slot], to.use - 1))) break;
+        uint8_t* const dst = sh.ops[v] + to.slot * kQtTile + (piece >> 2) * (kQtTile / 2) + (quarter * 32 + row8) * 128;
         auto row_of = [](int h, int k) { return h * 16 + (k >> 1) * 8 + (k & 1) * 2; };  // and row8
         auto put = [&](int h, int k, const uint32_t (&a)[4], const uint32_t (&c4)[4]) {
           const uint32_t at_a = (k & 1) ? place_a ^ 32u : place_a;  // the pieces' numbers XOR row % 8
@@ -758,8 +775,9 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.full[v]);
+        if (lane == 0) mbar_arrive(&sh.full[v][to.slot]);
         at.step();
+        to.step();
         ++tile_no;
       }
     }
