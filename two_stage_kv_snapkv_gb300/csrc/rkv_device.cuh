@@ -193,6 +193,16 @@ __device__ __forceinline__ void tma_load_2d_hint(void* dst, const void* map, int
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_2d_hint_if(bool issue, uint32_t dst, const void* map, int x, int y, uint32_t bar,
+                                                    uint64_t policy) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n"
+      " @q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%1], [%2, {%3, %4}], "
+      "[%5], %6;\n}\n" ::"r"((uint32_t)issue),
+      "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 // Fetches a tensor map's descriptor ahead of the first copy that uses it.
 __device__ __forceinline__ void prefetch_map(const void* map) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");

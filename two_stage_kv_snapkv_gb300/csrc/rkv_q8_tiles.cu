@@ -491,9 +491,9 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
       bool ok = true;
       while (ok && next_run(r, ok)) {
         const int b = r.b, g = r.g, n = r.n, nt = r.hi - r.lo;
-        // Page ids and scales of 32 pages (4 to 16 tiles), one a lane, and of the 32 behind them
-        // on their way: a tile's own loads, one behind the other, took 2700 clocks of the 3000 a
-        // tile of the narrow form.
+        // Page ids and scales of 32 pages (4 to 16 tiles), one a lane, with what follows from them,
+        // and of the 32 behind them on their way.  (Loaded a tile at a time, they took 2700 clocks
+        // of the narrow form's 3000 a tile; worked out a tile at a time, 1900 of its 2300.)
         const int batch = 32 / pages;  // tiles
         auto page_at = [&](int tile) {  // of this lane, in the batch that begins with `tile`
           const int pg = tile * pages + lane;
@@ -506,60 +506,58 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
             sv = p.v_scale[(size_t)phys * p.Hkv + g];
           }
         };
-        int ids = page_at(r.lo), next_ids = page_at(r.lo + batch), unit = -126, in = 0;  // in: tiles of the batch behind us
-        float ks, vs, next_ks = 0.f, next_vs = 0.f;
-        scales_of(ids, ks, vs);
+        int next_ids = page_at(r.lo), unit = -126, in = batch;  // in: tiles of the batch behind us
+        float next_ks, next_vs;
+        scales_of(next_ids, next_ks, next_vs);
+        int row = 0, x = 0, own_top = 0, v_top = 0;  // of this lane's page; the tops: its tile's exponents
+        uint32_t batch_have = 0;
         for (int i = 0; i < nt; ++i) {
           const int tile = r.lo + i;
           if (in == batch) {
             in = 0;
-            ids = next_ids;
-            ks = next_ks;
-            vs = next_vs;
+            const bool mine = (tile * pages + lane) * p.P < min(n, r.hi * kQtKeys);
+            const bool there = next_ids >= 0 && next_ids < p.num_phys;
+            if (mine && !there) flag_error(p.err, RKV_DEVERR_PAGE_ID);
+            batch_have = __ballot_sync(0xffffffffu, there);
+            row = (next_ids * p.Hkv + g) * p.P;
+            // exponents; 255: NaN (a scale is positive)
+            const int xk = (int)(__float_as_uint(next_ks) >> 23) & 255, xv = (int)(__float_as_uint(next_vs) >> 23) & 255;
+            x = v ? xv : xk;
+            own_top = there && x < 255 ? max(x, 1) : 1;
+            v_top = there && xv < 255 ? max(xv, 1) : 1;
+            for (int o = 1; o < pages; o <<= 1) {
+              own_top = max(own_top, __shfl_xor_sync(0xffffffffu, own_top, o));
+              v_top = max(v_top, __shfl_xor_sync(0xffffffffu, v_top, o));
+            }
             next_ids = page_at(tile + batch);
           }
           if (in == batch - 1) scales_of(next_ids, next_ks, next_vs);
-          const int from = in * pages + (lane & (pages - 1));
-          int phys = __shfl_sync(0xffffffffu, ids, from);
-          const float sk = __shfl_sync(0xffffffffu, ks, from), sv = __shfl_sync(0xffffffffu, vs, from);
+          const int first = in * pages;  // the tile's first lane
+          const uint32_t have = (batch_have >> first) & ((1u << pages) - 1u);
+          unit = max(unit, __shfl_sync(0xffffffffu, v_top, first) - 127);
+          const int e = v ? unit : __shfl_sync(0xffffffffu, own_top, first) - 127;
+          const int gx = __shfl_sync(0xffffffffu, x, first + ((lane & 7) >> gs));  // lanes 0 .. 7: the 16-key groups
+          const uint32_t gr = __ballot_sync(0xffffffffu, lane < 8 && ((have >> ((lane & 7) >> gs)) & 1u));
           ++in;
           const int c = at.slot;
           if (at.use > 0 && !(ok = wait(&sh.empty_c[v][c], at.use - 1))) break;
-          const bool mine = lane < pages && (tile * pages + lane) * p.P < n;
-          if (!mine) phys = -1;
-          if (phys < 0 || phys >= p.num_phys) {
-            if (mine) flag_error(p.err, RKV_DEVERR_PAGE_ID);
-            phys = -1;
-          }
-          const uint32_t have = __ballot_sync(0xffffffffu, phys >= 0);
-          // exponents; 255: NaN (a scale is positive)
-          const int xk = (int)(__float_as_uint(sk) >> 23) & 255, xv = (int)(__float_as_uint(sv) >> 23) & 255;
-          unit = max(unit, __reduce_max_sync(0xffffffffu, phys >= 0 && xv < 255 ? xv : 1) - 127);
-          const int ek = __reduce_max_sync(0xffffffffu, phys >= 0 && xk < 255 ? xk : 1) - 127;
           TileInfo& ti = sh.info[v][loaded % kQtInfos];
-          const int mx = v ? xv : xk, me = v ? unit : ek;
-          // lanes 0 .. 7: the 16-key groups
-          const int below = mx == 255 ? kNoFactor : min(max(me - (mx - 127), 0), 254), d = __shfl_sync(0xffffffffu, below, lane >> gs);
-          const uint32_t gr = __ballot_sync(0xffffffffu, lane < 8 && ((have >> (lane >> gs)) & 1u));
-          if (lane < 8) ti.d[lane] = (uint8_t)d;
+          if (lane < 8) ti.d[lane] = (uint8_t)(gx == 255 ? kNoFactor : min(max(e - (gx - 127), 0), 254));
           if (lead) {
             ti.groups = gr;
-            ti.e = (int16_t)me;
+            ti.e = (int16_t)e;
             ti.unit = (int16_t)unit;
           }
           __syncwarp();
-          uint8_t* const st = sh.codes[v] + c * kQtCodes;
-          uint64_t* const bar = &sh.full_c[v][c];
+          const uint32_t st = smem_u32(sh.codes[v] + c * kQtCodes), bar = smem_u32(&sh.full_c[v][c]);
           if (lead) {
-            if (have) mbar_arrive_expect_tx(bar, __popc(have) * box);
-            else mbar_arrive(bar);
+            if (have) mbar_arrive_expect_tx(&sh.full_c[v][c], __popc(have) * box);
+            else mbar_arrive(&sh.full_c[v][c]);
           }
           __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int row = (__shfl_sync(0xffffffffu, phys, j) * p.Hkv + g) * p.P;
-            if (lead && ((have >> j) & 1u)) tma_load_2d_hint(st + j * box, map, 0, row, bar, policy);
-          }
+          for (int j = 0; j < pages; ++j)
+            tma_load_2d_hint_if(lead && ((have >> j) & 1u), st + j * box, map, 0, __shfl_sync(0xffffffffu, row, first + j), bar,
+                                policy);
           ++loaded;
           at.step();
         }
