@@ -546,9 +546,10 @@ typedef struct {
  *                lies behind them is left as it was.  Those that do not fit set
  *                RKV_DEVERR_CAPACITY and are not written.  -1 for a page whose id is out of
  *                range (RKV_DEVERR_PAGE_ID).
- *   first      : device [B + 1] int32: sequence b's slots are first[b] .. first[b + 1) - 1.
+ *   first      : device [B + 1] int32: sequence b's slots are first[b] .. first[b + 1] - 1.
  *   held_out, free_count_out : where the new counts go: pool->held and pool->free_count, or
  *                copies that leave the old ones as they are.
+ * Calls on one pool, and calls that use its tables, are ordered by the caller (one stream).
  */
 rkv_status rkv_reserve_pages(const rkv_page_pool* pool, int32_t* page_table, int32_t B, int32_t max_pages,
                              int32_t page_size, const int32_t* len, const int32_t* start, int32_t* slots,
@@ -610,11 +611,11 @@ rkv_status rkv_rotary(const rkv_rotary_plan* plan, const rkv_bf16* q, const int6
  * caller-owned): value = code * scale, one scale for each page and KV head for K and one for V.
  *   k_codes, v_codes : [num_phys_pages][Hkv][page_size][head_dim] bytes; pages, tables and
  *                      lengths as in rkv_cache.
- *   k_scale, v_scale : [num_phys_pages][Hkv] fp32, powers of two >= 2^-126: the smallest one
- *                      that brings the block's largest magnitude into the codes' range
- *                      (so that a code times its scale is a bf16 value, a block's codes move
- *                      to a larger scale without a second error but where they leave the
- *                      range at its small end, and nothing depends on rounded divisions).
+ *   k_scale, v_scale : [num_phys_pages][Hkv] fp32, powers of two >= 2^-126 (rkv_q8_attention
+ *                      takes them for such): the smallest one that brings the block's largest
+ *                      magnitude into the codes' range.  A code times its scale is then a bf16
+ *                      value, and dividing by a scale is exact: a value is rounded once, and
+ *                      again only when its page's scale grows.
  *                      NaN, for both, in a page and head that was given a NaN or an infinity:
  *                      every row that sees one of its tokens is NaN.
  *   error_word       : one int32 receiving RKV_DEVERR_* bits.
@@ -657,8 +658,10 @@ rkv_status rkv_q8_append(const rkv_cache8* cache, const rkv_bf16* k_new, const i
  * A bf16 cache becomes an 8-bit one: every sequence's tokens, in their order (what
  * rkv_prefill_evict or rkv_evict_accum kept, for instance), as rkv_q8_append would take them
  * into an empty cache; cache->seq_len[b] = src->seq_len[b].  The source is read only.  Both
- * have the same B, Hkv and page_size.  A sequence whose length is negative or beyond either
- * side's pages sets RKV_DEVERR_CAPACITY (in cache->error_word) and becomes empty.
+ * have the same B, Hkv and page_size, and lengths of their own.  A sequence whose length is
+ * negative or beyond either side's pages sets RKV_DEVERR_CAPACITY (in cache->error_word) and
+ * becomes empty; a page of the source that cannot be read sets RKV_DEVERR_PAGE_ID and its
+ * scales are NaN.
  */
 rkv_status rkv_q8_load(const rkv_cache8* cache, const rkv_cache* src, void* stream);
 

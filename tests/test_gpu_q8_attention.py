@@ -83,6 +83,37 @@ def test_long_caches(rkv, T, n):
     _check(rkv, cache, K, V, _queries(2, 16, T, seed=n), sample=40)
 
 
+@pytest.mark.parametrize("T", [1, 3, 40])
+def test_the_longest_cache(rkv, T):
+    """2^20 positions, the most that a table holds."""
+    cache, K, V = C.filled(rkv, [1 << 20], 1, 64, "e4m3", seed=T)
+    assert cache.max_pages == 16384
+    _check(rkv, cache, K, V, _queries(1, 8, T, seed=T), sample=8)
+
+
+@pytest.mark.parametrize("T", [1, 5, 40, 300])
+def test_far_pages(rkv, T):
+    """Codes behind 2^31 bytes of their pools."""
+    H, P, phys, n = 8, 64, 40000, 700
+    pt = torch.arange(phys - 16, phys, dtype=torch.int32, device="cuda").view(1, 16)
+    cache = rkv.PagedCache8(1, H, P, 16, "cuda", page_table=pt, num_phys_pages=phys, fmt="int8")
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rkv.rkv_q8_append(cache, torch.randn(1, H, n, C.D, generator=g, device="cuda").bfloat16(),
+                      torch.randn(1, H, n, C.D, generator=g, device="cuda").bfloat16())
+    K, V = zip(*[[y.double() for y in cache.token_kv(0)]])
+    _check(rkv, cache, K, V, _queries(1, 2 * H, T, seed=T))
+
+
+@pytest.mark.parametrize("B,n", [(1, 3), (1, 900), (1, 8000), (3, 2000), (8, 1500), (19, 700), (20, 700)])
+@pytest.mark.parametrize("T", [1, 2, 6])
+def test_small_caches_by_clusters_of_every_size(rkv, B, n, T):
+    lens = [n - (n * b) // (2 * B) for b in range(B)]
+    if B > 2:
+        lens[1] = 0
+    cache, K, V = C.filled(rkv, lens, 8, 16, "e4m3" if T != 2 else "int8", seed=n)
+    _check(rkv, cache, K, V, _queries(B, 32, T, seed=n), [T - (b % 2) * (T // 2) for b in range(B)])
+
+
 @pytest.mark.parametrize("T", [1, 4, 70, 300])
 def test_every_row_a_whole_prompt(rkv, T):
     """n = m: the causal triangle from its first row on."""

@@ -227,3 +227,19 @@ def test_workspace_sizes(rkv):
     assert lib.rkv_q8_workspace_size(0, 8, 2, 1, 8, 16) == 0
     small, large = lib.rkv_q8_workspace_size(1, 8, 2, 1, 8, 16), lib.rkv_q8_workspace_size(1, 8, 2, 1000, 8, 16)
     assert 0 < small <= large
+
+
+def test_products_given_up_are_waited_for_in_the_tiles_of_codes():
+    # as for the other tensor-core kernels: after a timeout a commit behind the last product is
+    # waited for before TMEM is freed; and a warp that gives up frees its partner's barrier
+    import os
+    import re
+
+    from two_stage_kv_snapkv_gb300 import build_lib
+    text = open(os.path.join(build_lib.CSRC, "rkv_q8_tiles.cu")).read()
+    stop = text.index("if (abort_flag) {")
+    branch = text[stop:text.index("tmem_dealloc(", stop)]
+    assert "tc_commit_if(elect_lane(), &sh.drained);" in branch and "mbar_wait(&sh.drained, 0);" in branch
+    assert text.count("mbar_init(&sh.drained, 1)") == 1
+    reds, leave = text.count("barrier.cta.red"), re.search(r"if \(!ok\) asm volatile\(\"barrier\.cta\.arrive", text)
+    assert reds == 1 and leave
