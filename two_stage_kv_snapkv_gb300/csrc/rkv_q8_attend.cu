@@ -18,9 +18,10 @@
 // q8_rows: 8 to 24 query rows against 32-key chunks, keys and channels on the MMA's M.  A
 // chunk's codes are 8 KB for 2 x 32 x 128 multiply-adds a row, so the cache's bytes bound
 // it: all units' chunks form one line that is split evenly over one CTA per SM; a CTA's
-// eight warps take a run's chunks in turn, each with its own three-stage TMA ring (192 KB in
-// flight per SM), its own running maximum, sum and fp32 output, and meet once per run.  The
-// parts of a split unit go to the workspace and q8_join joins them.
+// eight warps take a run's chunks in turn, each with its own three-stage ring (192 KB in flight
+// per SM) that one of four more warps fills by TMA, its own running maximum, sum and fp32
+// output, and meet once per run.  The parts of a split unit go to the workspace and q8_join
+// joins them.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -34,7 +35,10 @@ constexpr int kQrKeysShift = 5, kQrKeys = 1 << kQrKeysShift;
 constexpr int kQrStageBytes = 2 * kQrKeys * 128;
 constexpr int kQrPad = 8;                         // what a run costs, in chunks
 constexpr int kQrMergeStride = 132;               // floats
-constexpr int kQrWarps = 8, kQrThreads = kQrWarps * 32;
+constexpr int kQrWarps = 8, kQrThreads = kQrWarps * 32 + 128;  // and four that fetch
+// Registers: 384 threads start with 168 each; 256 x 224 + 128 x 56 = 384 x 168.
+constexpr int kQrTileRegs = 224, kQrFetchRegs = 56;
+static_assert(256 * kQrTileRegs + 128 * kQrFetchRegs == 384 * 168, "the split must be what the block was launched with");
 constexpr int kQrStages = 3;
 constexpr int kQrMergeRows = 4;                   // rows of every warp that meet at a time
 constexpr int kQrSmem = 1024 + kQrWarps * kQrStages * kQrStageBytes + kQrWarps * kQrMergeRows * kQrMergeStride * 4;
@@ -340,17 +344,24 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Line line;
   __shared__ typename std::conditional<kShared, QueryTile<kN>, int>::type queries;
-  __shared__ uint64_t full_b[kQrWarps][kQrStages];
+  __shared__ uint64_t full_b[kQrWarps][kQrStages], empty_b[kQrWarps][kQrStages];
   __shared__ StageInfo info[kQrWarps][kQrStages];
   __shared__ float wm[kQrWarps][kRows], wl[kQrWarps][kRows], wv[kQrWarps];
+  __shared__ int stop_word;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int& stop = *const_cast<volatile int*>(&stop_word);
   uint8_t* base = align1024(smem);
-  uint8_t* ring = base + warp * kQrStages * kQrStageBytes;
   float* merge = reinterpret_cast<float*>(base + kQrWarps * kQrStages * kQrStageBytes);
-  if (lane == 0) {
-    for (int s = 0; s < kQrStages; ++s) mbar_init(&full_b[warp][s], 1);
+  if (tid == 0) {
+    for (int w = 0; w < kQrWarps; ++w)
+      for (int s = 0; s < kQrStages; ++s) {
+        mbar_init(&full_b[w][s], 2);  // the copies asked for, and the stage's scales
+        mbar_init(&empty_b[w][s], 1);
+      }
     fence_mbar_init();
+    stop = 0;
   }
+  // ends with a block barrier
   line.build(p.B, p.Hkv, p.gshift, [&](int b) { return checked_len(p, b); }, [&](int b) { return checked_rows(p, b); });
   grid_launch_dependents();
   const long long total = line.base[p.B];
@@ -358,62 +369,93 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
   if ((int)blockIdx.x >= N) return;
   const long long x0 = flat_first(total, blockIdx.x, N), x1 = flat_first(total, blockIdx.x + 1, N);
   auto next_run = [&](long long x, CausalRun& r) { return line.next(p.B, p.Hkv, p.gshift, x, x0, x1, r); };
-
-  // this warp's chunks of a run: lo + warp, lo + warp + kQrWarps, ...  The fetch side walks the
-  // runs ahead of the compute side.
-  CausalRun fr;
-  bool more = next_run(x0, fr);
-  int fc = fr.lo + warp;
-  auto settle = [&]() {
-    while (more && fc >= fr.hi) {
-      more = next_run(fr.next, fr);
-      if (more) fc = fr.lo + warp;
+  auto wait = [&](uint64_t* bar, int phase) {  // of a converged warp
+    const bool late = !mbar_wait_role(bar, (uint32_t)(phase & 1), &stop);
+    if (__any_sync(0xffffffffu, late)) {
+      if (lane == 0) flag_error(p.err, RKV_DEVERR_TIMEOUT);
+      stop = 1;
+      return false;
     }
+    return true;
   };
-  settle();
-  // page ids and scales of this warp's next 32 chunks of the run, one chunk a lane
-  const int boxes = p.P < kQrKeys ? 2 : 1, box = kQrKeys / boxes;
-  int ids[2] = {-1, -1}, ids_at = 0;
-  float sk[2] = {0.f, 0.f}, sv[2] = {0.f, 0.f};
-  long long ids_x = -1;
-  const uint64_t policy = l2_policy(p.T * p.G <= kRows);  // one row tile: nobody reads the cache again
-  int fetched = 0, used = 0;
-  bool dead = false;
-  auto fetch = [&]() {
-    if (!more) return;
-    const int s = fetched % kQrStages;
-    if (ids_x != fr.x || fc >= ids_at + 32 * kQrWarps) {
-      ids_x = fr.x;
-      ids_at = fc;
-      const int c = fc + lane * kQrWarps;
+
+  // A run's chunks: warp w of the eight has lo + w, lo + w + 8, ..
+  if (warp >= kQrWarps) {
+    // fetches for two of them: by themselves, each spent 700 of a chunk's 2500 to 4300 clocks on it
+    setmaxnreg_dec<kQrFetchRegs>();
+    const int w0 = (warp - kQrWarps) * 2;
+    const int boxes = p.P < kQrKeys ? 2 : 1, box = kQrKeys / boxes;
+    const uint64_t policy = l2_policy(p.T * p.G <= kRows);  // one row tile: nobody reads the cache again
+    int fetched[2] = {0, 0};
+    bool ok = true;
+    CausalRun r;
+    for (long long x = x0; ok && next_run(x, r); x = r.next) {
+      // page ids and scales of the two warps' next 16 chunks each, one chunk a lane, and those of
+      // the 16 behind them on their way
+      int ids[2], next_ids[2];
+      float sk[2], sv[2], next_sk[2], next_sv[2];
+      auto load_ids = [&](int k0, int (&id)[2]) {
+        const int c = r.lo + w0 + (lane & 1) + (k0 + (lane >> 1)) * kQrWarps;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int key = c * kQrKeys + h * box;
-        ids[h] = -1;
-        sk[h] = sv[h] = 0.f;
-        if (h < boxes && c < fr.hi && key < fr.n) {
-          const int id = p.page_table[(size_t)fr.b * p.max_pages + (key >> p.pshift)];
-          if (id >= 0 && id < p.num_phys) {
-            ids[h] = id;
-            sk[h] = p.k_scale[(size_t)id * p.Hkv + fr.g];
-            sv[h] = p.v_scale[(size_t)id * p.Hkv + fr.g];
-          } else {
+        for (int h = 0; h < 2; ++h) {
+          const int key = c * kQrKeys + h * box;
+          const bool in = h < boxes && c < r.hi && key < r.n;
+          id[h] = in ? p.page_table[(size_t)r.b * p.max_pages + (key >> p.pshift)] : -1;
+          if (in && (id[h] < 0 || id[h] >= p.num_phys)) {
             flag_error(p.err, RKV_DEVERR_PAGE_ID);
+            id[h] = -1;
           }
+        }
+      };
+      auto load_scales = [&](const int (&id)[2], float (&k)[2], float (&v)[2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          k[h] = id[h] >= 0 ? p.k_scale[(size_t)id[h] * p.Hkv + r.g] : 0.f;
+          v[h] = id[h] >= 0 ? p.v_scale[(size_t)id[h] * p.Hkv + r.g] : 0.f;
+        }
+      };
+      load_ids(0, next_ids);
+      load_scales(next_ids, next_sk, next_sv);
+      for (int k = 0; ok && r.lo + w0 + k * kQrWarps < r.hi; ++k) {
+        if ((k & 15) == 0) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ids[h] = next_ids[h];
+            sk[h] = next_sk[h];
+            sv[h] = next_sv[h];
+          }
+          load_ids(k + 16, next_ids);
+        }
+        if ((k & 15) == 14) load_scales(next_ids, next_sk, next_sv);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int c = r.lo + w0 + j + k * kQrWarps, from = (k & 15) * 2 + j;
+          if (c >= r.hi) continue;
+          const int s = fetched[j] % kQrStages, use = fetched[j] / kQrStages, w = w0 + j;
+          const int id0 = __shfl_sync(0xffffffffu, ids[0], from), id1 = __shfl_sync(0xffffffffu, ids[1], from);
+          if (use > 0 && !(ok = wait(&empty_b[w][s], use - 1))) break;
+          fetch_chunk(p, base + (w * kQrStages + s) * kQrStageBytes, &full_b[w][s], id0, id1, r.g, c * kQrKeys, box, policy);
+          if (lane == from) {
+            note_chunk(info[w][s], id0, id1, r.n - c * kQrKeys, boxes, sk, sv);
+            mbar_arrive(&full_b[w][s]);
+          }
+          __syncwarp();
+          ++fetched[j];
         }
       }
     }
-    const int from = (fc - ids_at) / kQrWarps, key0 = fc * kQrKeys;
-    const int id0 = __shfl_sync(0xffffffffu, ids[0], from), id1 = __shfl_sync(0xffffffffu, ids[1], from);
-    fetch_chunk(p, ring + s * kQrStageBytes, &full_b[warp][s], id0, id1, fr.g, key0, box, policy);
-    if (lane == from) note_chunk(info[warp][s], id0, id1, fr.n - key0, boxes, sk, sv);
-    ++fetched;
-    fc += kQrWarps;
-    settle();
-  };
-  for (int s = 0; s < kQrStages; ++s) fetch();
-  __syncwarp();
+    if (stop)  // after a timeout: wait (bounded) for what is still in flight
+      for (int j = 0; j < 2; ++j)
+        for (int i = max(fetched[j] - kQrStages, 0); i < fetched[j]; ++i)
+          mbar_wait(&full_b[w0 + j][i % kQrStages], (uint32_t)((i / kQrStages) & 1));
+    return;
+  }
 
+  setmaxnreg_inc<kQrTileRegs>();
+  uint8_t* const ring = base + warp * kQrStages * kQrStageBytes;
+  int used = 0;
+  bool ok = true;
+  auto meet = [&]() { asm volatile("barrier.cta.sync 1, %0;\n" ::"n"(kQrWarps * 32) : "memory"); };  // the eight warps
   CausalRun cr;
   RowTile8<kFormat, kN, kShared> tile;
   for (long long x = x0; next_run(x, cr); x = cr.next) {
@@ -421,19 +463,14 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
     uint4 (*qs)[4][32] = nullptr;
     if constexpr (kShared) qs = queries;
     tile.start(p, b, g, rt, cr.n, cr.m, qs);
-    if (kShared) __syncthreads();  // the queries are there (the last run's were used up before its warps met)
-    for (int c = cr.lo + warp; c < cr.hi; c += kQrWarps) {
+    if (kShared) meet();  // the queries are there (the last run's were used up before its warps met)
+    for (int c = cr.lo + warp; ok && c < cr.hi; c += kQrWarps) {
       const int s = used % kQrStages;
-      const bool late = !dead && !mbar_wait(&full_b[warp][s], (uint32_t)((used / kQrStages) & 1));
-      if (__any_sync(0xffffffffu, late)) {
-        if (lane == 0) flag_error(p.err, RKV_DEVERR_TIMEOUT);
-        dead = true;
-      }
-      if (!dead && info[warp][s].live != 0u) tile.step(ring + s * kQrStageBytes, info[warp][s], c * kQrKeys, qs);
+      if (!(ok = wait(&full_b[warp][s], used / kQrStages))) break;
+      if (info[warp][s].live != 0u) tile.step(ring + s * kQrStageBytes, info[warp][s], c * kQrKeys, qs);
       ++used;
       __syncwarp();  // every lane has read the stage
-      if (!dead) fetch();
-      __syncwarp();  // what the fetch noted is there
+      if (lane == 0) mbar_arrive(&empty_b[warp][s]);
     }
 
     tile.finish();
@@ -465,7 +502,7 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
                                                                   tile.o[q0 >> 3][i + 1][c], tile.o[q0 >> 3][i + 1][2 + c]);
         }
       }
-      __syncthreads();
+      meet();
       const int sub = tid >> 6, d = (tid & 63) * 2, row = q0 + sub, rr = rt * kRows + row;
       if (sub < kQrMergeRows && row < live) {
         float M = kNoMax, L = 0.f, ax = 0.f, ay = 0.f;
@@ -489,12 +526,9 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
           if (d == 0) p.part_ml[slot * kPartRows + row] = make_float2(M, L);
         }
       }
-      __syncthreads();  // the merge buffer (and, after the last rows, wm, wl and wv) are free
+      meet();  // the merge buffer (and, after the last rows, wm, wl and wv) are free
     }
   }
-  // after a timeout: wait (bounded) for what this warp still has in flight
-  if (dead)
-    for (int i = used; i < fetched; ++i) mbar_wait(&full_b[warp][i % kQrStages], (uint32_t)((i / kQrStages) & 1));
 }
 
 // ---------------------------------------------------------------------------
@@ -673,64 +707,78 @@ __global__ void __launch_bounds__(UnitsShape8<kN>::kThreads, 1) q8_units_kernel(
   cluster.sync();  // no CTA leaves while another still reads its shared memory
 }
 
-// Joins the parts of the split units, and gives the rows that see nothing their results: one
-// warp a row, four channels a lane, four parts' loads in flight.
+// Joins the parts of the split units, and gives the rows that see nothing their results.  A CTA
+// takes up to 32 rows of a unit, whose parts it finds once (a warp that did so for every row took
+// 25 us to find that 32768 rows were final), a warp a row, four channels a lane, four parts'
+// loads in flight.  tiles: of a unit, for the most rows that a sequence may have.
+template <class Line>
+struct JoinShape {
+  static constexpr int kRows = Line::kRows, kGroup = kRows < 32 ? kRows : 32, kGroups = kRows / kGroup;
+};
 template <class Line>
 __global__ void __launch_bounds__(256, 4) q8_join_kernel(const __grid_constant__ Q8Params p) {
+  using Sh = JoinShape<Line>;
+  constexpr int kRows = Sh::kRows;
   __shared__ LineLengths<Line> line;
   line.build(p.B, p.Hkv, p.gshift, [&](int b) { return checked_len(p, b); }, [&](int b) { return checked_rows(p, b); });
   grid_dependency_wait();
-  constexpr int kRows = Line::kRows;
-  const int lane = threadIdx.x & 31;
-  const long long each = (long long)p.Hq * p.T, rows = each * p.B, total = line.base[p.B];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long total = line.base[p.B], each = (long long)p.join_tiles * Sh::kGroups, items = each * p.B * p.Hkv;
   const int N = flat_ctas(total, p.N);
-  for (long long x = blockIdx.x * 8 + (threadIdx.x >> 5); x < rows; x += gridDim.x * 8) {
-    const int b = (int)(x / each), i = (int)(x - b * each), hq = i / p.T, t = i - hq * p.T;
-    if (t >= line.m[b]) continue;
-    const int g = hq / p.G, r = t * p.G + (hq & (p.G - 1)), rt = r / kRows, row = r % kRows;
-    const int per = Line::per(line.n[b], line.m[b], p.gshift, rt);
-    uint2* out = reinterpret_cast<uint2*>(p.out + (size_t)x * 128) + lane;
+  for (long long x = blockIdx.x; x < items; x += gridDim.x) {
+    const int unit = (int)(x / each), in = (int)(x - unit * each), rt = in / Sh::kGroups, b = unit / p.Hkv, g = unit % p.Hkv;
+    const int n = line.n[b], rows = line.m[b] * p.G, row0 = (in % Sh::kGroups) * Sh::kGroup;
+    if (rt * kRows + row0 >= rows) continue;
+    const int per = Line::per(n, line.m[b], p.gshift, rt), last = min(Sh::kGroup, rows - rt * kRows - row0);
     if (per == 0) {  // the whole tile sees nothing
-      *out = make_uint2(0u, 0u);
-      if (lane == 0 && p.lse) p.lse[x] = -INFINITY;
+      for (int i = warp; i < last; i += 8) {
+        const size_t orow = out_row(p, b, g, rt * kRows + row0 + i);
+        reinterpret_cast<uint2*>(p.out + orow * 128)[lane] = make_uint2(0u, 0u);
+        if (lane == 0 && p.lse) p.lse[orow] = -INFINITY;
+      }
       continue;
     }
     const PartSlots ps(line.at(b, p.Hkv, p.gshift, rt, g), per, Line::kPad, total, N);
     if (ps.c0 == ps.c1) continue;  // final already
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float M = kNoMax, L = 0.f;
-    for (int c = ps.c0; c <= ps.c1; c += 4) {
-      float4 v[4];
-      float2 ml[4];
+    for (int i = warp; i < last; i += 8) {
+      const int row = row0 + i;
+      const size_t orow = out_row(p, b, g, rt * kRows + row);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float M = kNoMax, L = 0.f;
+      for (int c = ps.c0; c <= ps.c1; c += 4) {
+        float4 v[4];
+        float2 ml[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = c + j <= ps.c1;
-        const size_t at = ps[in ? c + j : c] * kRows + row;  // behind the last part: the first again, unweighted
-        ml[j] = p.part_ml[at];
-        v[j] = reinterpret_cast<const float4*>(p.part_o + at * 128)[lane];
-        if (!in) ml[j] = make_float2(kNoMax, 0.f);
-      }
-      const float to = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
-      const float f = ex2_approx(M - to);
-      M = to;
-      L *= f;
-      o.x *= f;
-      o.y *= f;
-      o.z *= f;
-      o.w *= f;
+        for (int j = 0; j < 4; ++j) {
+          const bool in = c + j <= ps.c1;
+          const size_t at = ps[in ? c + j : c] * kRows + row;  // behind the last part: the first again, unweighted
+          ml[j] = p.part_ml[at];
+          v[j] = reinterpret_cast<const float4*>(p.part_o + at * 128)[lane];
+          if (!in) ml[j] = make_float2(kNoMax, 0.f);
+        }
+        const float to = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+        const float f = ex2_approx(M - to);
+        M = to;
+        L *= f;
+        o.x *= f;
+        o.y *= f;
+        o.z *= f;
+        o.w *= f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float w = c + j <= ps.c1 ? ex2_approx(ml[j].x - M) : 0.f;
-        L += ml[j].y * w;
-        o.x += v[j].x * w;
-        o.y += v[j].y * w;
-        o.z += v[j].z * w;
-        o.w += v[j].w * w;
+        for (int j = 0; j < 4; ++j) {
+          const float w = c + j <= ps.c1 ? ex2_approx(ml[j].x - M) : 0.f;
+          L += ml[j].y * w;
+          o.x += v[j].x * w;
+          o.y += v[j].y * w;
+          o.z += v[j].z * w;
+          o.w += v[j].w * w;
+        }
       }
+      const float inv = inverse_of(L);
+      reinterpret_cast<uint2*>(p.out + orow * 128)[lane] =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+      if (lane == 0 && p.lse) p.lse[orow] = lse_of(M, L);
     }
-    const float inv = inverse_of(L);
-    *out = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (lane == 0 && p.lse) p.lse[x] = lse_of(M, L);
   }
 }
 
@@ -842,6 +890,7 @@ cudaError_t launch_q8_attend(const Q8AttendArgs& a, cudaStream_t s) {
   const size_t rows = (size_t)2 * kMaxSms * part_rows(tile);
   p.part_o = static_cast<float*>(a.ws);
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(a.ws) + align256(rows * 128 * 4));
+  p.join_tiles = (int)(((long long)a.T * p.G + part_rows(tile) - 1) / part_rows(tile));
   const bool int8 = a.cache.format == RKV_Q8_INT8;
   if (const int C = units_cluster(a, tile)) {
     if (tile == 8) return int8 ? launch_units<RKV_Q8_INT8, 1>(p, C, s) : launch_units<RKV_Q8_E4M3, 1>(p, C, s);
@@ -871,8 +920,9 @@ cudaError_t launch_q8_attend(const Q8AttendArgs& a, cudaStream_t s) {
       join = q8_join_kernel<TileLine<8>>;
   }
   if (e != cudaSuccess) return e;
-  const long long jrows = ((long long)p.B * a.Hq * a.T + 7) / 8, jmost = 8LL * p.N;
-  return launch_dependent(join, dim3((unsigned)(jrows < jmost ? jrows : jmost)), 256, K_Q8_JOIN, s, p);
+  const int part = part_rows(tile), group = part < 32 ? part : 32;
+  const long long items = (long long)p.B * p.Hkv * p.join_tiles * (part / group), most = 8LL * p.N;
+  return launch_dependent(join, dim3((unsigned)(items < most ? items : most)), 256, K_Q8_JOIN, s, p);
 }
 
 }  // namespace rkv

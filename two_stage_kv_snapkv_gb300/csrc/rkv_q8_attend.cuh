@@ -21,6 +21,7 @@ struct Q8Params {
   float* part_o;   // [2 N][tile rows][128]
   float2* part_ml; // [2 N][tile rows]
   int B, Hq, Hkv, G, gshift, T, P, pshift, max_pages, num_phys, N;
+  int join_tiles;  // q8_join: row tiles of a unit with T rows
   float scale_log2;
 };
 
