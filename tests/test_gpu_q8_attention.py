@@ -187,6 +187,51 @@ def test_pages_of_nan_reach_who_sees_them_alone(rkv, T, P):
             assert ((out[b, h, idx].double() - ref).abs() <= 2.0 ** -6 * (torch.softmax(zz, 1) @ V[b][h // 4].abs()) + 1e-6).all()
 
 
+@pytest.mark.parametrize("which", ["k", "v", "kv"])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("T,n,P,at,room", [
+    (3, 306, 16, 304, 0),       # clusters; the page begins inside 32 keys that are taken together
+    (6, 308, 16, 304, 0),
+    (6, 322, 64, 320, 0),
+    (2, 305, 16, 304, 9000),    # the flat split on mma.sync: 8, 16 and 24 rows
+    (3, 306, 16, 304, 9000),
+    (6, 307, 16, 304, 9000),
+    (6, 321, 64, 320, 9000),
+    (32, 322, 16, 320, 0),      # 128-row tiles
+    (32, 322, 16, 304, 0),
+    (32, 322, 64, 320, 0),
+    (100, 322, 16, 320, 0),     # 256-row tiles
+    (100, 322, 16, 256, 0),
+    (300, 700, 16, 512, 0),
+])
+def test_pages_that_a_row_does_not_see(rkv, T, n, P, at, room, fmt, which):
+    """A page with 2^100 times its neighbours' scales has no part in the results of rows that end before it."""
+    cache, K, V = C.filled(rkv, [n], 2, P, fmt, seed=T, room=room)
+    ph = cache.page_table[0, at // P].long()
+    unit = float(cache.v_scale[cache.page_table[0, :at // P].long()].max())
+    for t, s in (("k", cache.k_scale), ("v", cache.v_scale)):
+        if t in which:
+            s[ph] *= 2.0 ** 100
+    q = _queries(1, 8, T, seed=T)
+    out, lse = _run(rkv, cache, q)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    pos = torch.arange(n - T, n, device="cuda")
+    idx = (pos < at).nonzero().flatten()
+    assert len(idx)
+    for h in range(8):
+        k, v = K[0][h // 4][:at], V[0][h // 4][:at]
+        qq = q[0, h, idx].double()
+        hidden = torch.arange(at, device="cuda")[None] > pos[idx][:, None]
+        z = (qq @ k.T * C.SCALE).masked_fill(hidden, -math.inf)
+        ref_l, w = torch.logsumexp(z, 1), torch.softmax(z, 1)
+        ref = w @ v
+        E = 132 * 2.0 ** -23 * C.SCALE * float((qq.abs() @ k.abs().T).max())
+        Ew = 2 * E + 2.0 ** -16 + n * 2.0 ** -30
+        tol = (2.0 ** -11 + Ew) * (w @ v.abs()) + 2.0 ** -8 * (1 + Ew) * ref.abs() + n * 2.0 ** -32 * 448 * unit
+        assert ((out[0, h, idx].double() - ref).abs() <= tol).all(), f"head {h}"
+        assert ((lse[0, h, idx].double() - ref_l).abs() <= Ew + 2.0 ** -22 * ref_l.abs()).all(), f"head {h}"
+
+
 @pytest.mark.parametrize("T", [1, 3, 40])
 def test_queries_with_a_nan_or_an_infinity(rkv, T):
     cache, K, V = C.filled(rkv, [200], 2, 16, "e4m3", seed=T)

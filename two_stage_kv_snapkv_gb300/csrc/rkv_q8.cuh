@@ -75,7 +75,7 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
   const int e = kFormat == RKV_Q8_E4M3 ? (int)((top + 0x1fffffu) >> 23) - 8 : (int)((top + 0x1ffffu) >> 23) - 6;
   return __uint_as_float((uint32_t)max(e, 1) << 23);
 }
-// 1 / scale, exact (0 < scale <= 2^121, a power of two).
+// 1 / scale, exact (0 < scale <= 2^122, a power of two).
 __device__ __forceinline__ float inverse_scale(float scale) {
   return __uint_as_float((254u << 23) - __float_as_uint(scale));
 }

@@ -10,7 +10,7 @@
 //             a bf16 number fits fp16's 11 bits, and only what lies 2^-33 below the row's
 //             largest is cut off at fp16's smallest step;
 //   weights   p = 2^(z - m) <= 2^8 enters the product with V times 2^7 vs / vref (vref: the
-//             largest vs so far, the output's unit): 11 bits, off by at most 2^-11 of each,
+//             largest vs that the row saw, its output's unit): 11 bits, off by at most 2^-11 of each,
 //             down to 2^-21 of the output's unit, then by 2^-32 of it; their sum is fp32 and
 //             unrounded.
 // ks joins the logits behind the product and vs the weights, so neither costs a pass over codes.
@@ -120,7 +120,10 @@ struct RowTile8 {
   float o[kN][8][4];
   float m[kN][2], l[kN][2], factor[kN][2];  // factor: from the product to base-2 logits, without the key's scale
   int lim[kN][2];                           // keys that the row sees
+  // The largest V scale so far, of the chunks that every row saw whole; from the first other one on
+  // (parted) each row has its own: own[2 tile + column][lane].
   float vref;
+  bool parted;
   int least;  // the fewest keys that a row sees
 
   // qs, kShared: where the queries go, warp t those of tile t
@@ -176,6 +179,7 @@ struct RowTile8 {
         for (int c = 0; c < 4; ++c) o[t][i][c] = 0.f;
     }
     vref = kLowestUnit;
+    parted = false;
     least = n - rows_m + (r0 >> p.gshift) + 1;
   }
 
@@ -190,10 +194,16 @@ struct RowTile8 {
   }
 
   // The chunk whose first key is key0, K and V in st (their copies have landed).
-  __device__ __forceinline__ void step(uint8_t* st, const StageInfo& info, int key0, const uint4 (*qs)[4][32]) {
+  __device__ __forceinline__ void step(uint8_t* st, const StageInfo& info, int key0, const uint4 (*qs)[4][32], float* own) {
+    if (info.live == ~0u && key0 + kQrKeys <= least) step_as<true>(st, info, key0, qs, own);
+    else step_as<false>(st, info, key0, qs, own);
+  }
+  // kPlain: every row sees all of its keys.
+  template <bool kPlain>
+  __device__ __forceinline__ void step_as(uint8_t* st, const StageInfo& info, int key0, const uint4 (*qs)[4][32], float* own) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c4 = lane & 3;
     const uint32_t live = info.live;
-    if (live != ~0u) {  // a key that cannot be read may hold anything, and 0 x NaN is not 0
+    if (!kPlain && live != ~0u) {  // a key that cannot be read may hold anything, and 0 x NaN is not 0
       for (int i = lane; i < kQrKeys * 8; i += 32)
         if (!((live >> (i >> 3)) & 1u)) *reinterpret_cast<uint4*>(st + kQrKeys * 128 + i * 16) = make_uint4(0, 0, 0, 0);
       fence_proxy_async_smem();
@@ -241,7 +251,7 @@ struct RowTile8 {
       }
     }
     // base-2 logits, hidden ones -inf; e = 0, 1: key r, columns 0, 1; e = 2, 3: key r + 8
-    const bool all = live == ~0u && key0 + kQrKeys <= least;
+    const bool inner = kPlain || key0 + kQrKeys <= least;
     bool over = false;
 #pragma unroll
     for (int t = 0; t < kN; ++t)
@@ -250,7 +260,7 @@ struct RowTile8 {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           z[t][u][e] *= factor[t][e & 1] * info.k[u];
-          if (!all) {
+          if (!kPlain) {
             const int key = u * 16 + (e >> 1) * 8 + r;
             if (!((live >> key) & 1u) || key0 + key >= lim[t][e & 1]) z[t][u][e] = -INFINITY;
           }
@@ -276,24 +286,44 @@ struct RowTile8 {
     }
     // a page of NaN has NaN logits for whoever sees it; for the others its values are not there
     const float v0 = info.v[0] >= 0.f ? info.v[0] : 0.f, v1 = info.v[1] >= 0.f ? info.v[1] : 0.f;
-    if (fmaxf(v0, v1) > vref) {  // the same in every lane
+    if (!inner) {
+#pragma unroll
+      for (int t = 0; t < kN; ++t) {
+        float f[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float& at = own[(2 * t + c) * 32 + lane];
+          const float was = parted ? at : vref;
+          const float to = fmaxf(was, fmaxf(key0 < lim[t][c] ? v0 : 0.f, key0 + 16 < lim[t][c] ? v1 : 0.f));
+          f[c] = was * inverse_scale(to);
+          at = to;
+        }
+        scale_o(t, f[0], f[1]);
+      }
+      parted = true;
+    } else if (fmaxf(v0, v1) > vref) {  // the same in every lane
       const float f = vref * inverse_scale(fmaxf(v0, v1));
       vref = fmaxf(v0, v1);
 #pragma unroll
       for (int t = 0; t < kN; ++t) scale_o(t, f, f);
     }
-    const float unit = kUnit * inverse_scale(vref), up[2] = {v0 * unit, v1 * unit};
+    const float unit = kUnit * inverse_scale(vref);
     uint32_t pb[kN][2][2];  // the weights, columns of keys
 #pragma unroll
     for (int t = 0; t < kN; ++t)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        float w[4];
+        float w[4], up[2];
+        up[0] = up[1] = (u ? v1 : v0) * unit;
+        if (!inner) {  // a page that the row does not see may lie above its unit
+#pragma unroll
+          for (int c = 0; c < 2; ++c) up[c] = fminf((u ? v1 : v0) * (kUnit * inverse_scale(own[(2 * t + c) * 32 + lane])), kUnit);
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           w[e] = ex2_approx(z[t][u][e] - m[t][e & 1]);
           l[t][e & 1] += w[e];  // this lane's keys; the eight lanes of a column add up at the end
-          w[e] *= up[u];
+          w[e] *= up[e & 1];
         }
         pb[t][u][0] = transpose8(pack_f16x2(w[0], w[1]));
         pb[t][u][1] = transpose8(pack_f16x2(w[2], w[3]));
@@ -324,6 +354,11 @@ struct RowTile8 {
     }
   }
 
+  // The unit of a row's output.
+  __device__ __forceinline__ float unit_of(int t, int c, const float* own) const {
+    return (parted ? own[(2 * t + c) * 32 + (threadIdx.x & 31)] : vref) * (1.f / kUnit);
+  }
+
   // The eight lanes of a column add their sums up.
   __device__ __forceinline__ void finish() {
 #pragma unroll
@@ -346,7 +381,7 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
   __shared__ typename std::conditional<kShared, QueryTile<kN>, int>::type queries;
   __shared__ uint64_t full_b[kQrWarps][kQrStages], empty_b[kQrWarps][kQrStages];
   __shared__ StageInfo info[kQrWarps][kQrStages];
-  __shared__ float wm[kQrWarps][kRows], wl[kQrWarps][kRows], wv[kQrWarps];
+  __shared__ float wm[kQrWarps][kRows], wl[kQrWarps][kRows], wv[kQrWarps][kRows];
   __shared__ int stop_word;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int& stop = *const_cast<volatile int*>(&stop_word);
@@ -453,6 +488,8 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
 
   setmaxnreg_inc<kQrTileRegs>();
   uint8_t* const ring = base + warp * kQrStages * kQrStageBytes;
+  float* const own = merge + warp * kQrMergeRows * kQrMergeStride;  // until the warps meet
+  static_assert(kN * 2 * 32 <= kQrMergeRows * kQrMergeStride, "the rows' units fit the merge buffer");
   int used = 0;
   bool ok = true;
   auto meet = [&]() { asm volatile("barrier.cta.sync 1, %0;\n" ::"n"(kQrWarps * 32) : "memory"); };  // the eight warps
@@ -467,7 +504,7 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
     for (int c = cr.lo + warp; ok && c < cr.hi; c += kQrWarps) {
       const int s = used % kQrStages;
       if (!(ok = wait(&full_b[warp][s], used / kQrStages))) break;
-      if (info[warp][s].live != 0u) tile.step(ring + s * kQrStageBytes, info[warp][s], c * kQrKeys, qs);
+      if (info[warp][s].live != 0u) tile.step(ring + s * kQrStageBytes, info[warp][s], c * kQrKeys, qs, own);
       ++used;
       __syncwarp();  // every lane has read the stage
       if (lane == 0) mbar_arrive(&empty_b[warp][s]);
@@ -482,9 +519,10 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
         for (int c = 0; c < 2; ++c) {
           wm[warp][t * 8 + c4 * 2 + c] = tile.m[t][c];
           wl[warp][t * 8 + c4 * 2 + c] = tile.l[t][c];
+          wv[warp][t * 8 + c4 * 2 + c] = tile.unit_of(t, c, own);
         }
-      if (lane == 0) wv[warp] = tile.vref * (1.f / kUnit);
     }
+    __syncwarp();  // the rows' units are read
     // the warps meet, a few rows at a time: thread = (row, two channels)
     const int live = min(kRows, rows - rt * kRows);
     const size_t slot = 2 * (size_t)blockIdx.x + (cr.first ? 0 : 1);
@@ -510,7 +548,7 @@ __global__ void __launch_bounds__(kQrThreads, 1) q8_rows_kernel(const __grid_con
         for (int w = 0; w < kQrWarps; ++w) M = fmaxf(M, wm[w][row]);
 #pragma unroll
         for (int w = 0; w < kQrWarps; ++w) {
-          const float f = ex2_approx(wm[w][row] - M), fv = f * wv[w];
+          const float f = ex2_approx(wm[w][row] - M), fv = f * wv[w][row];
           const float2 v = *reinterpret_cast<const float2*>(merge + (w * kQrMergeRows + sub) * kQrMergeStride + d);
           L += wl[w][row] * f;
           ax += v.x * fv;
@@ -544,7 +582,8 @@ struct UnitsShape8 {
   static constexpr int kRing = kWarps * kQuStages * kQrStageBytes;  // then the warps' outputs
   static constexpr int kPart = kRows * kQrMergeStride * 4;            // the CTA's output
   static_assert(kWarps * kPart <= kRing, "the warps' outputs take the ring's place");
-  static constexpr int kSmem = 1024 + kRing + kPart;
+  static constexpr int kOwn = kN * 2 * 32;                            // floats of a warp: its rows' units
+  static constexpr int kSmem = 1024 + kRing + kPart + kWarps * kOwn * 4;
 };
 
 template <int kFormat, int kN>
@@ -558,7 +597,7 @@ __global__ void __launch_bounds__(UnitsShape8<kN>::kThreads, 1) q8_units_kernel(
   __shared__ typename std::conditional<kShared, QueryTile<kN>, int>::type queries;
   __shared__ uint64_t full_b[kWarps][kQuStages];
   __shared__ StageInfo info[kWarps][kQuStages];
-  __shared__ float wm[kWarps][kRows], wl[kWarps][kRows], wv[kWarps];
+  __shared__ float wm[kWarps][kRows], wl[kWarps][kRows], wv[kWarps][kRows];
   __shared__ float2 part_ml[kRows];  // this CTA's (m, l), read by the cluster
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -566,6 +605,7 @@ __global__ void __launch_bounds__(UnitsShape8<kN>::kThreads, 1) q8_units_kernel(
   uint8_t* ring = base + warp * kQuStages * kQrStageBytes;
   float* merge = reinterpret_cast<float*>(base);
   float* part_o = reinterpret_cast<float*>(base + Sh::kRing);
+  float* const own = reinterpret_cast<float*>(base + Sh::kRing + Sh::kPart) + warp * Sh::kOwn;
   const int b = blockIdx.y / p.Hkv, g = blockIdx.y % p.Hkv;
   if (lane == 0) {
     for (int s = 0; s < kQuStages; ++s) mbar_init(&full_b[warp][s], 1);
@@ -625,7 +665,7 @@ __global__ void __launch_bounds__(UnitsShape8<kN>::kThreads, 1) q8_units_kernel(
       if (lane == 0) flag_error(p.err, RKV_DEVERR_TIMEOUT);
       dead = true;
     }
-    if (!dead && info[warp][s].live != 0u) tile.step(ring + s * kQrStageBytes, info[warp][s], c * kQrKeys, qs);
+    if (!dead && info[warp][s].live != 0u) tile.step(ring + s * kQrStageBytes, info[warp][s], c * kQrKeys, qs, own);
     ++used;
     __syncwarp();  // every lane has read the stage
     if (!dead) fetch();
@@ -642,8 +682,8 @@ __global__ void __launch_bounds__(UnitsShape8<kN>::kThreads, 1) q8_units_kernel(
       for (int c = 0; c < 2; ++c) {
         wm[warp][t * 8 + c4 * 2 + c] = tile.m[t][c];
         wl[warp][t * 8 + c4 * 2 + c] = tile.l[t][c];
+        wv[warp][t * 8 + c4 * 2 + c] = tile.unit_of(t, c, own);
       }
-    if (lane == 0) wv[warp] = tile.vref * (1.f / kUnit);
   }
   __syncthreads();  // every warp is done with its ring: the outputs take its place
 #pragma unroll
@@ -665,7 +705,7 @@ __global__ void __launch_bounds__(UnitsShape8<kN>::kThreads, 1) q8_units_kernel(
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w][row]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2_approx(wm[w][row] - M), fv = f * wv[w];
+      const float f = ex2_approx(wm[w][row] - M), fv = f * wv[w][row];
       const float2 v = *reinterpret_cast<const float2*>(merge + (w * kRows + row) * kQrMergeStride + d);
       L += wl[w][row] * f;
       ax += v.x * fv;

@@ -11,14 +11,20 @@
 // rows, each with its own maximum, sum and O, and join them at the end of a run.
 //
 // TMA brings a tile's codes (16 KB of K, 16 KB of V) and eight warps write them out as fp16
-// operands, 32 KB each, times 2^(page's exponent - tile's): K's tile exponent is its pages'
-// largest and joins the logits, V's is the largest of the run so far, the unit of O (where
-// it grows, O is scaled down with the maximum's move).  A code times such a factor is exact
-// but where it falls below fp16's smallest step, 2^-33 of the largest.
+// operands, 32 KB each.  In a tile that every row sees whole they are written times 2^(page's
+// exponent - tile's): K's tile exponent is its pages' largest and joins the logits, V's is the
+// largest of the run so far, the unit of O (where it grows, O is scaled down with the maximum's
+// move).  A code times such a factor is exact but where it falls below fp16's smallest step,
+// 2^-33 of the largest.  What a row does not see must have no part in that: in a run's last
+// tiles, which end beyond its first row's keys, the operands are the codes, K's scales meet
+// the logits and V's the weights (16 keys, a part of one page, at a time), and the unit is
+// each row's own.  (Scales at the softmax in every tile took 877 us where this takes 788.)
 //   warps 0-7, 8-15: softmax of slot 0, 1 (four warps to 64 keys);  16, 18: TMA of K, V;  17:
 //   MMA issue;  19: the share's runs;  20-23, 24-27: K's and V's codes to fp16.
 // Every wait is bounded;
 // one that runs out flags RKV_DEVERR_TIMEOUT and stops every role.
+#include <type_traits>
+
 #include "rkv_q8_attend.cuh"
 
 namespace rkv {
@@ -34,19 +40,17 @@ static_assert(512 * kQtSoftRegs + 128 * kQtIssueRegs + 256 * kQtCodeRegs == 896 
 constexpr int kQtTile = kQtKeys * 256, kQtCodes = kQtKeys * 128;
 constexpr int kQtInfos = 8;     // tiles between the TMA and the softmax: at most six
 constexpr int kNoFactor = 255;  // a page of NaN: NaN keys, no values
+constexpr int kFarUnits = 60;   // a weight so many powers of two below its row's unit is 0 in fp16
 constexpr int kNoRow = -128;    // a query row with a NaN or an infinity
 // A row whose maximum lies beyond this has distinct logits at least 64 apart: its exponents
 // are taken with the power of two below the factor, whose product with the maximum is exact.
 constexpr float kQtFar = 1073741824.f;
 
-// A tile's scales, for K and for V from the warp that fetches its codes: each 16-key group's
-// exponent below `e`, and which groups were loaded.  e: K's tile's exponent; V's run's, up to
-// this tile, the unit of O (`unit`: the same from the warp of K, for the softmax, which does
-// not wait for V).
-struct TileInfo {
-  uint8_t d[8];
-  int16_t e, unit;
-  uint32_t groups;
+// A tile's scales, for K and for V from the warp that fetches its codes.  A tile that every row
+// sees whole: each 16-key group's exponent below the tile's (`x`).  Else for K: the groups' biased
+// exponents, K's in `x` and V's in `vx`; for V: whether a group is of NaN (kNoFactor) or not (0).
+struct alignas(8) TileInfo {
+  uint8_t x[8], vx[8];
 };
 
 // A run of the CTA's share, as warp 19 hands it to the others: worked out by every role, the
@@ -74,6 +78,8 @@ struct TileShape8 {
     Line line;
     uint64_t full_c[2][kCodes], empty_c[2][kCodes], full[2][kOps], empty[2][kOps], s[2], p[2], o[2], qf[2], out[2], ml, drained;
     TileInfo info[2][kQtInfos];
+    uint8_t groups[2][kQtInfos];              // a tile's 16-key groups that were loaded
+    uint8_t e[kQtInfos], unit[kQtInfos];      // biased exponents: K's tile's, V's run's up to it (the unit of O)
     RunInfo runs[kQtRuns];
     uint64_t full_r[kQtRuns], empty_r[kQtRuns];
     uint32_t tmem_base;
@@ -261,11 +267,11 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         arrive(&sh.qf[kWide ? slot : 0]);
       }
       const int my = rt * R + (kWide ? slot * 128 : 0) + row;  // this thread's query row
-      // keys that it sees, and that the slot's first row does
+      // keys that it sees, and that the run's first row does
       const int lim = my < rows ? n - r.m + (my >> p.gshift) + 1 : n;
-      const int least = n - r.m + ((rt * R + (kWide ? slot * 128 : 0)) >> p.gshift) + 1;
+      const int least = n - r.m + ((rt * R) >> p.gshift) + 1;
       float m = kNoMax, l = 0.f, factor = 0.f, ref = kNoMax;
-      bool far = false;
+      auto is_far = [&]() { return fabsf(m) > kQtFar && m != kNoMax; };
       int unit = -126;  // O is in units of 2^unit
       if (!idle) {
         for (int i = kWide ? 0 : slot; i < nt; i += kWide ? 1 : 2) {
@@ -276,101 +282,142 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
             const int e = sh.row_exp[(kWide ? slot * 128 : 0) + row];
             factor = e == kNoRow ? __uint_as_float(0x7fffffffu) : p.scale_log2 * power_of_two(e - 8);
           }
-          const TileInfo& ti = sh.info[0][(tiles_before + i) % kQtInfos];
-          const int key0 = (r.lo + i) * kQtKeys, to_unit = ti.unit;
-          const uint32_t gr = ti.groups;
-          float sl = factor * power_of_two(ti.e);
-          if (sl < kLowestScale) sl = kLowestScale;  // 0 x -inf is not -inf; a NaN stays
-          const bool all = gr == 0xffu && key0 + kQtKeys <= min(least, n);
-          uint32_t see[2] = {~0u, ~0u};  // of this thread's 64 keys
-          if (!all) {
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              const int k = min(n, lim) - key0 - half * 64 - w * 32;
-              see[w] = k >= 32 ? ~0u : (k <= 0 ? 0u : (1u << k) - 1u);
-              if (!((gr >> (half * 4 + 2 * w)) & 1u)) see[w] &= 0xffff0000u;
-              if (!((gr >> (half * 4 + 2 * w + 1)) & 1u)) see[w] &= 0x0000ffffu;
-            }
-          }
+          const int at = (tiles_before + i) % kQtInfos, key0 = (r.lo + i) * kQtKeys;
+          const TileInfo& ti = sh.info[0][at];
+          const uint32_t gr = sh.groups[0][at];
+          // from the product to base-2 logits: 2^(x - 127) times the row's factor
+          auto factor_of = [&](uint32_t x) {
+            const float f = factor * __uint_as_float(x == kNoFactor ? 0x7fffffffu : x << 23);
+            return f < kLowestScale ? kLowestScale : f;  // 0 x -inf is not -inf; a NaN stays
+          };
+          auto power_part = [](float f) { return __uint_as_float(__float_as_uint(f) & 0x7f800000u); };
+          uint32_t pk[32];
           // The weights are taken with the maximum so far, without looking for a new one: as long
           // as 64 of a row's sum up to at most 2^8 (2^15 with their factor) none is beyond fp16,
           // and while the maximum stays the same they sum up to 2^6 at most.
-          uint32_t pk[32];
-          float sum;
-          for (bool moved = first;;) {
-            if (moved) {
-              // the maximum of all 128 logits, by both threads of the row
-              float mx = -INFINITY;
+          auto weigh = [&](auto plain_tile) {
+            constexpr bool kPlain = decltype(plain_tile)::value;
+            const float sl = kPlain ? factor_of(sh.e[at]) : 0.f;
+            int to_unit = max(unit, (int)sh.unit[at] - 127);
+            uint32_t see[2] = {~0u, ~0u};  // of this thread's 64 keys
+            if constexpr (!kPlain) {
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                const int k = min(n, lim) - key0 - half * 64 - w * 32;
+                see[w] = k >= 32 ? ~0u : (k <= 0 ? 0u : (1u << k) - 1u);
+                if (!((gr >> (half * 4 + 2 * w)) & 1u)) see[w] &= 0xffff0000u;
+                if (!((gr >> (half * 4 + 2 * w + 1)) & 1u)) see[w] &= 0x0000ffffu;
+              }
+              to_unit = unit;
 #pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
-                uint32_t v[16];
-                tc_ld16_wait(mine + c * 16, v);
-                if (!all) {
-                  const int k = min(n, lim) - key0 - c * 16;
-                  const uint32_t bits = ((gr >> c) & 1u) ? (k >= 16 ? ~0u : (k <= 0 ? 0u : (1u << k) - 1u)) : 0u;
+              for (int c = 0; c < 8; ++c)
+                if (((gr >> c) & 1u) && key0 + c * 16 < min(n, lim) && ti.vx[c] != kNoFactor)
+                  to_unit = max(to_unit, (int)ti.vx[c] - 127);
+            }
+            // the exponents of 16 keys' V below the row's unit (hidden ones may lie above it)
+            auto below = [&](int c) { return min(max(unit + 127 - (int)ti.vx[half * 4 + c], 0), kFarUnits); };
+            float sum;
+            for (bool moved = first;;) {
+              if (moved) {
+                // the maximum of all 128 logits, by both threads of the row; zp: without the part
+                // of the factor that is no power of two
+                float zp = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                  uint32_t v[16];
+                  float mx = -INFINITY, by = power_part(sl);
+                  tc_ld16_wait(mine + c * 16, v);
+                  if constexpr (!kPlain) {
+                    by = power_part(factor_of(ti.x[c] == kNoFactor ? 0u : ti.x[c]));
+                    const int k = min(n, lim) - key0 - c * 16;
+                    const uint32_t bits = ((gr >> c) & 1u) ? (k >= 16 ? ~0u : (k <= 0 ? 0u : (1u << k) - 1u)) : 0u;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                      if (!((bits >> j) & 1u)) v[j] = 0xff800000u;  // -inf
+                  }
+#pragma unroll
+                  for (int j = 0; j < 16; j += 2) mx = max3(mx, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                  zp = fmaxf(zp, mx * by);
+                }
+                const float mx = factor == factor ? zp * __uint_as_float((__float_as_uint(factor) & 0x7fffffu) | 0x3f800000u) : factor;
+                const float to = fmaxf(m, mx), f = ex2_approx(m - to);
+                if (first || mx > m) {
+                  m = to;
+                  ref = is_far() ? zp : m;
+                }
+                if (!first) {
+                  // this slot's earlier products are complete: its logits were issued after them
+                  const float fo = f * power_of_two(max(unit - to_unit, -126));
+                  l *= f;
+#pragma unroll 1
+                  for (int c = 0; c < 4; ++c) {
+                    uint32_t o[16];
+                    tc_ld16_wait(mine + 128 + half * 64 + c * 16, o);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fo);
+                    tc_st16_wait(mine + 128 + half * 64 + c * 16, o);
+                  }
+                }
+                unit = to_unit;
+              }
+              const bool far = is_far();
+              const float by = far ? power_part(sl) : sl, sub = 7.f - ref;  // times kUnit
+              uint64_t by2 = pair_of(by, by), sub2 = pair_of(sub, sub), back2 = 0, s0 = 0, s1 = 0, s = 0;
+              uint32_t v[2][16];
+              tc_ld16(keys, v[0]);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                tc_ld_wait();
+                tc_ld16_done(v[c & 1]);
+                if (c < 3) tc_ld16(keys + (c + 1) * 16, v[(c + 1) & 1]);
+                if constexpr (!kPlain) {
+                  const uint32_t bits = see[c >> 1] >> ((c & 1) * 16);
 #pragma unroll
                   for (int j = 0; j < 16; ++j)
-                    if (!((bits >> j) & 1u)) v[j] = 0xff800000u;  // -inf
+                    if (!((bits >> j) & 1u)) v[c & 1][j] = 0xff800000u;
+                  const float f = factor_of((bits & 0xffffu) ? ti.x[half * 4 + c] : 0u);  // none seen: a page of NaN does not matter
+                  const float g = far ? power_part(f) : f;
+                  by2 = pair_of(g, g);
+                  // V's scale goes into the exponent, and out of the sum again
+                  const int d = far ? 0 : below(c);
+                  const float sub_v = sub - (float)d, back = power_of_two(d);
+                  sub2 = pair_of(sub_v, sub_v);
+                  back2 = pair_of(back, back);
+                  s0 = s1 = 0;
                 }
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) mx = max3(mx, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                for (int j = 0; j < 8; ++j) {
+                  const uint64_t z = fma2(pair_bits(v[c & 1][2 * j], v[c & 1][2 * j + 1]), by2, sub2);
+                  const float ax = ex2_approx(pair_lo(z)), ay = ex2_approx(pair_hi(z));
+                  if (j & 1) s1 = add2(s1, pair_of(ax, ay)); else s0 = add2(s0, pair_of(ax, ay));
+                  pk[c * 8 + j] = pack_f16x2(ax, ay);
+                }
+                if constexpr (!kPlain) s = fma2(add2(s0, s1), back2, s);
               }
-              const float raw = mx;
-              mx = raw * sl;  // sl > 0
-              const float to = fmaxf(m, mx), f = ex2_approx(m - to);
-              if (first || mx > m) {
-                m = to;
-                far = fabsf(m) > kQtFar && m != kNoMax;
-                ref = far ? raw * __uint_as_float(__float_as_uint(sl) & 0x7f800000u) : m;
-              }
-              if (!first) {
-                // this slot's earlier products are complete: its logits were issued after them
-                const float fo = f * power_of_two(max(unit - to_unit, -126));
-                l *= f;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                  uint32_t o[16];
-                  tc_ld16_wait(mine + 128 + half * 64 + c * 16, o);
+              if constexpr (kPlain) s = add2(s0, s1);
+              sum = pair_lo(s) + pair_hi(s);
+              // in the second round: neither thread of the row writes over logits that the other
+              // still looks for their maximum in
+              if (!vote(!moved && (sum > 32768.f || to_unit != unit))) break;
+              moved = true;
+            }
+            if (!kPlain && is_far()) {  // the exponent had no room for V's scale
 #pragma unroll
-                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fo);
-                  tc_st16_wait(mine + 128 + half * 64 + c * 16, o);
+              for (int c = 0; c < 4; ++c) {
+                const float f = power_of_two(-below(c));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&pk[c * 8 + j]));
+                  pk[c * 8 + j] = pack_f16x2(w.x * f, w.y * f);
                 }
               }
-              unit = to_unit;
             }
-            const float by = far ? __uint_as_float(__float_as_uint(sl) & 0x7f800000u) : sl;
-            const uint64_t by2 = pair_of(by, by), sub2 = pair_of(7.f - ref, 7.f - ref);  // times kUnit
-            uint64_t s0 = pair_of(0.f, 0.f), s1 = s0;
-            uint32_t v[2][16];
-            tc_ld16(keys, v[0]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tc_ld_wait();
-              tc_ld16_done(v[c & 1]);
-              if (c < 3) tc_ld16(keys + (c + 1) * 16, v[(c + 1) & 1]);
-              if (!all) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (!((see[c >> 1] >> ((c & 1) * 16 + j)) & 1u)) v[c & 1][j] = 0xff800000u;
-              }
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const uint64_t z = fma2(pair_bits(v[c & 1][2 * j], v[c & 1][2 * j + 1]), by2, sub2);
-                const float ax = ex2_approx(pair_lo(z)), ay = ex2_approx(pair_hi(z));
-                if (j & 1) s1 = add2(s1, pair_of(ax, ay)); else s0 = add2(s0, pair_of(ax, ay));
-                pk[c * 8 + j] = pack_f16x2(ax, ay);
-              }
-            }
-            s0 = add2(s0, s1);
-            sum = pair_lo(s0) + pair_hi(s0);
-            // in the second round: neither thread of the row writes over logits that the other
-            // still looks for their maximum in
-            if (!vote(!moved && (sum > 32768.f || to_unit != unit))) break;
-            moved = true;
-          }
+            l += sum;
+          };
+          // a tile that every row sees whole, or another
+          if (gr == 0xffu && key0 + kQtKeys <= least) weigh(std::true_type{}); else weigh(std::false_type{});
           tc_st32(keys, pk);
           tc_st_wait();
-          l += sum;
           tc_fence_before();
           arrive(&sh.p[slot]);
         }
@@ -394,21 +441,22 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         if (!(ok = wait(&sh.o[0], done[0]++))) break;
         if (has[1] && !(ok = wait(&sh.o[1], done[1]++))) break;
         float2* const ml_s = reinterpret_cast<float2*>(sh.q);
+        int* const unit_s = reinterpret_cast<int*>(sh.q + 4096);
         ml_s[(slot * 2 + half) * 128 + row] = make_float2(m, l);
+        if (half == 0) unit_s[slot * 128 + row] = unit;
         arrive(&sh.ml);
         if (!(ok = wait(&sh.ml, 2 * run))) break;
         const float2 a = ml_s[row], c = has[1] ? ml_s[256 + row] : make_float2(kNoMax, 0.f);
         const float la = a.y + ml_s[128 + row].y, lc = has[1] ? c.y + ml_s[384 + row].y : 0.f;
+        const int ua = unit_s[row], uc = unit_s[128 + row];
         arrive(&sh.ml);  // read, before outputs are staged there
         if (!(ok = wait(&sh.ml, 2 * run + 1))) break;
         m = fmaxf(a.x, c.x);
         f0 = ex2_approx(a.x - m);
         f1 = ex2_approx(c.x - m);
         l = la * f0 + lc * f1;
-        // a slot's unit is that of its last tile
-        const int last0 = (nt - 1) & ~1, last1 = has[1] ? ((nt & 1) ? nt - 2 : nt - 1) : 0;
-        f0 *= power_of_two(max((int)sh.info[0][(tiles_before - nt + last0) % kQtInfos].unit - 7, -126));
-        if (has[1]) f1 *= power_of_two(max((int)sh.info[0][(tiles_before - nt + last1) % kQtInfos].unit - 7, -126));
+        f0 *= power_of_two(max(ua - 7, -126));
+        if (has[1]) f1 *= power_of_two(max(uc - 7, -126));
       }
       ++run;
       tc_fence_after();
@@ -490,7 +538,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
       RingAt<Sh::kCodes> at;
       bool ok = true;
       while (ok && next_run(r, ok)) {
-        const int b = r.b, g = r.g, n = r.n, nt = r.hi - r.lo;
+        const int b = r.b, g = r.g, n = r.n, nt = r.hi - r.lo, least = n - r.m + ((r.rt * R) >> p.gshift) + 1;
         // Page ids and scales of 32 pages (4 to 16 tiles), one a lane, with what follows from them,
         // and of the 32 behind them on their way.  (Loaded a tile at a time, they took 2700 clocks
         // of the narrow form's 3000 a tile; worked out a tile at a time, 1900 of its 2300.)
@@ -506,10 +554,10 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
             sv = p.v_scale[(size_t)phys * p.Hkv + g];
           }
         };
-        int next_ids = page_at(r.lo), unit = -126, in = batch;  // in: tiles of the batch behind us
+        int next_ids = page_at(r.lo), unit = 1, in = batch;  // in: tiles of the batch behind us
         float next_ks, next_vs;
         scales_of(next_ids, next_ks, next_vs);
-        int row = 0, x = 0, own_top = 0, v_top = 0;  // of this lane's page; the tops: its tile's exponents
+        int row = 0, xk = 0, xv = 0, own_top = 0, v_top = 0;  // of this lane's page; the tops: its tile's exponents
         uint32_t batch_have = 0;
         for (int i = 0; i < nt; ++i) {
           const int tile = r.lo + i;
@@ -521,8 +569,9 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
             batch_have = __ballot_sync(0xffffffffu, there);
             row = (next_ids * p.Hkv + g) * p.P;
             // exponents; 255: NaN (a scale is positive)
-            const int xk = (int)(__float_as_uint(next_ks) >> 23) & 255, xv = (int)(__float_as_uint(next_vs) >> 23) & 255;
-            x = v ? xv : xk;
+            xk = (int)(__float_as_uint(next_ks) >> 23) & 255;
+            xv = (int)(__float_as_uint(next_vs) >> 23) & 255;
+            const int x = v ? xv : xk;
             own_top = there && x < 255 ? max(x, 1) : 1;
             v_top = there && xv < 255 ? max(xv, 1) : 1;
             for (int o = 1; o < pages; o <<= 1) {
@@ -534,19 +583,28 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
           if (in == batch - 1) scales_of(next_ids, next_ks, next_vs);
           const int first = in * pages;  // the tile's first lane
           const uint32_t have = (batch_have >> first) & ((1u << pages) - 1u);
-          unit = max(unit, __shfl_sync(0xffffffffu, v_top, first) - 127);
-          const int e = v ? unit : __shfl_sync(0xffffffffu, own_top, first) - 127;
-          const int gx = __shfl_sync(0xffffffffu, x, first + ((lane & 7) >> gs));  // lanes 0 .. 7: the 16-key groups
+          const bool inner = (tile + 1) * kQtKeys <= least;  // every row sees it whole
+          const int top = __shfl_sync(0xffffffffu, v_top, first);
+          if (inner) unit = max(unit, top);
+          const int e = v ? unit : __shfl_sync(0xffffffffu, own_top, first), of = first + ((lane & 7) >> gs);
+          const int gk = __shfl_sync(0xffffffffu, xk, of), gv = __shfl_sync(0xffffffffu, xv, of);  // lanes 0 .. 7: the 16-key groups
           const uint32_t gr = __ballot_sync(0xffffffffu, lane < 8 && ((have >> ((lane & 7) >> gs)) & 1u));
+          const bool plain = inner && gr == 0xffu;
           ++in;
           const int c = at.slot;
           if (at.use > 0 && !(ok = wait(&sh.empty_c[v][c], at.use - 1))) break;
           TileInfo& ti = sh.info[v][loaded % kQtInfos];
-          if (lane < 8) ti.d[lane] = (uint8_t)(gx == 255 ? kNoFactor : min(max(e - (gx - 127), 0), 254));
+          if (lane < 8) {
+            const int gx = v ? gv : gk;
+            ti.x[lane] = (uint8_t)(gx == kNoFactor ? kNoFactor : (plain ? min(max(e - gx, 0), 254) : (v ? 0 : gx)));
+            ti.vx[lane] = (uint8_t)gv;
+          }
           if (lead) {
-            ti.groups = gr;
-            ti.e = (int16_t)e;
-            ti.unit = (int16_t)unit;
+            sh.groups[v][loaded % kQtInfos] = (uint8_t)gr;
+            if (!v) {
+              sh.e[loaded % kQtInfos] = (uint8_t)e;
+              sh.unit[loaded % kQtInfos] = (uint8_t)unit;
+            }
           }
           __syncwarp();
           const uint32_t st = smem_u32(sh.codes[v] + c * kQtCodes), bar = smem_u32(&sh.full_c[v][c]);
@@ -693,14 +751,15 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
     int tile_no = 0;
     bool ok = true;
     while (ok && next_run(r, ok)) {
-      const int nt = r.hi - r.lo;
+      const int nt = r.hi - r.lo, least = r.n - r.m + ((r.rt * R) >> p.gshift) + 1;
       for (int i = 0; i < nt; ++i) {
         const int c = at.slot;
         if (!(ok = wait(&sh.full_c[v][c], at.use))) break;
         const TileInfo& ti = sh.info[v][tile_no % kQtInfos];
         const int left = r.n - (r.lo + i) * kQtKeys;
-        const uint32_t gr = ti.groups;
-        const int d0 = ti.d[quarter * 2], d1 = ti.d[quarter * 2 + 1];
+        const uint32_t gr = sh.groups[v][tile_no % kQtInfos];
+        const bool codes = !v && (gr != 0xffu || (r.lo + i + 1) * kQtKeys > least);  // K's as they are
+        const int d0 = codes ? 0 : ti.x[quarter * 2], d1 = codes ? 0 : ti.x[quarter * 2 + 1];
         const uint8_t* const src = sh.codes[v] + c * kQtCodes + (quarter * 32 + row8) * 128;
         if (to.use > 0 && !(ok = wait(&sh.empty[v][to.slot], to.use - 1))) break;
         uint8_t* const dst = sh.ops[v] + to.slot * kQtTile + (piece >> 2) * (kQtTile / 2) + (quarter * 32 + row8) * 128;
