@@ -10,6 +10,9 @@
 // CTA waits for another's writes; what one CTA writes (table entries behind `held`, stack
 // places from `count` on) no other reads.  The counts are written by the CTA that finishes
 // last, when every one has read the old ones, so that they may be updated in place.
+// Bound by the chain of scans, searches and loads.  Measured: a step of 64 sequences 3.3 us; 128
+// prompts of up to 32000 tokens, all pages and slots (13.8 MB), 9.9 us (18.5 with a search for
+// every slot instead of one for eight).
 #include <algorithm>
 
 #include "rkv_device.cuh"

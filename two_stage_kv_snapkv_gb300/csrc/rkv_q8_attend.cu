@@ -21,7 +21,9 @@
 // eight warps take a run's chunks in turn, each with its own three-stage ring (192 KB in flight
 // per SM) that one of four more warps fills by TMA, its own running maximum, sum and fp32
 // output, and meet once per run.  The parts of a split unit go to the workspace and q8_join
-// joins them.
+// joins them.  Measured, 16 x 8K..32K tokens of 8 KV heads (601 MB): 4 query rows 92 us, 6.5 TB/s,
+// the rate of a plain copy 96 %; 20 rows 121 us (a chunk's chain of loads, products and
+// exponentials on two warps a scheduler, which issue in 37 % of the clocks).
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -748,17 +750,23 @@ __global__ void __launch_bounds__(UnitsShape8<kN>::kThreads, 1) q8_units_kernel(
 }
 
 // Joins the parts of the split units, and gives the rows that see nothing their results.  A CTA
-// takes up to 32 rows of a unit, whose parts it finds once (a warp that did so for every row took
-// 25 us to find that 32768 rows were final), a warp a row, four channels a lane, four parts'
-// loads in flight.  tiles: of a unit, for the most rows that a sequence may have.
-template <class Line>
+// takes a group of a unit's rows, whose parts it finds once (a warp that did so for every row took
+// 25 us to find that 32768 rows were final), a warp a row, four channels a lane.  tiles: of a
+// unit, for the most rows that a sequence may have.
+// kFew: the groups of 8 rows are no more than the CTAs that are resident together.  Their units
+// have many parts then, of which eight are in flight: 24 rows of 8 KV heads over 32000 tokens take
+// 24.6 us in all against 35.3 in groups of 32 with four parts in flight, of one head 29 against
+// 56.  With more units each CTA's table of the line costs more than that gives (80 rows of 128
+// heads and sequences over 2000 tokens each: 42 us in groups of 32, 50 of 8).
+template <class Line, bool kFew>
 struct JoinShape {
-  static constexpr int kRows = Line::kRows, kGroup = kRows < 32 ? kRows : 32, kGroups = kRows / kGroup;
+  static constexpr int kRows = Line::kRows, kGroup = kFew ? 8 : (kRows < 32 ? kRows : 32), kGroups = kRows / kGroup;
+  static constexpr int kParts = kFew ? 8 : 4, kCtas = kFew ? 2 : 4;
 };
-template <class Line>
-__global__ void __launch_bounds__(256, 4) q8_join_kernel(const __grid_constant__ Q8Params p) {
-  using Sh = JoinShape<Line>;
-  constexpr int kRows = Sh::kRows;
+template <class Line, bool kFew>
+__global__ void __launch_bounds__(256, JoinShape<Line, kFew>::kCtas) q8_join_kernel(const __grid_constant__ Q8Params p) {
+  using Sh = JoinShape<Line, kFew>;
+  constexpr int kRows = Sh::kRows, kJoinParts = Sh::kParts;
   __shared__ LineLengths<Line> line;
   line.build(p.B, p.Hkv, p.gshift, [&](int b) { return checked_len(p, b); }, [&](int b) { return checked_rows(p, b); });
   grid_dependency_wait();
@@ -785,18 +793,20 @@ __global__ void __launch_bounds__(256, 4) q8_join_kernel(const __grid_constant__
       const size_t orow = out_row(p, b, g, rt * kRows + row);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       float M = kNoMax, L = 0.f;
-      for (int c = ps.c0; c <= ps.c1; c += 4) {
-        float4 v[4];
-        float2 ml[4];
+      for (int c = ps.c0; c <= ps.c1; c += kJoinParts) {
+        float4 v[kJoinParts];
+        float2 ml[kJoinParts];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kJoinParts; ++j) {
           const bool in = c + j <= ps.c1;
           const size_t at = ps[in ? c + j : c] * kRows + row;  // behind the last part: the first again, unweighted
           ml[j] = p.part_ml[at];
           v[j] = reinterpret_cast<const float4*>(p.part_o + at * 128)[lane];
           if (!in) ml[j] = make_float2(kNoMax, 0.f);
         }
-        const float to = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+        float to = M;
+#pragma unroll
+        for (int j = 0; j < kJoinParts; ++j) to = fmaxf(to, ml[j].x);
         const float f = ex2_approx(M - to);
         M = to;
         L *= f;
@@ -805,7 +815,7 @@ __global__ void __launch_bounds__(256, 4) q8_join_kernel(const __grid_constant__
         o.z *= f;
         o.w *= f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kJoinParts; ++j) {
           const float w = c + j <= ps.c1 ? ex2_approx(ml[j].x - M) : 0.f;
           L += ml[j].y * w;
           o.x += v[j].x * w;
@@ -820,6 +830,15 @@ __global__ void __launch_bounds__(256, 4) q8_join_kernel(const __grid_constant__
       if (lane == 0 && p.lse) p.lse[orow] = lse_of(M, L);
     }
   }
+}
+
+template <class Line>
+cudaError_t launch_join(const Q8Params& p, cudaStream_t s) {
+  const long long tiles = (long long)p.B * p.Hkv * p.join_tiles;
+  const long long few = tiles * JoinShape<Line, true>::kGroups, many = tiles * JoinShape<Line, false>::kGroups;
+  const long long resident = (long long)JoinShape<Line, true>::kCtas * p.N, most = 8LL * p.N;
+  if (few <= resident) return launch_dependent(q8_join_kernel<Line, true>, dim3((unsigned)few), 256, K_Q8_JOIN, s, p);
+  return launch_dependent(q8_join_kernel<Line, false>, dim3((unsigned)(many < most ? many : most)), 256, K_Q8_JOIN, s, p);
 }
 
 // How many rows of a unit share a pass over the cache: 8, 16 or 24 (mma.sync), 128 or 256
@@ -877,18 +896,21 @@ cudaError_t launch_rows(const Q8Params& p, cudaStream_t s) {
 
 // Whether q8_units takes the call, with clusters of how many CTAs (0: it does not).  The host
 // knows the caches' capacity, not their lengths.  One wave of CTAs (an SM each) against the line
-// split over all SMs and its join, one token, 8 KV heads, us: 1 x 515 tokens 5.7 (C = 8)
-// against 8.9, 1 x 2563 6.9 against 9.8, 1 x 8000 10.3 against 11.2, 1 x 16000 14.9 against
-// 13.4; 2 x 4000 10.2 (C = 4: only about nine clusters of eight lie on the SMs at a time)
-// against 10.2; 4 x 8000 15.2 (C = 4) against 19.3; 8 x 4000 15.1 (C = 2) against 19.2; 16 x
-// 3000 21.3 (C = 1) against 23.9.  So up to 1024 tokens a CTA, and three times that where the
-// CTAs are most of the SMs.
+// split over all SMs and its join, 8 KV heads of 4 query heads, one token and six, us:
+//   1 x 2563 (C = 8)   6.5 against 10.1, 13.9 against 15.9
+//   1 x 8000 (C = 8)   9.5 against 11.3, 18.1 against 17.1;  1 x 16000  13.6 / 13.3, 25.0 / 19.7
+//   2 x 4000 (C = 4: only about nine clusters of eight lie on the SMs at a time)  9.5 / 10.9
+//   4 x 8000 (C = 4)  13.9 / 17.1, 26.5 / 28.5;  8 x 4000 (C = 2)  13.7 / 17.5, 26.4 / 29.3
+//   16 x 3000 (C = 1) 19.2 / 22.5, 34.5 / 38.0;  18 x 3000 (C = 1)  21.7 / 23.9, 35.3 / 40.2
+//   19 x 1500 (C = 1) 11.8 / 14.7, 22.3 / 21.8;  19 x 3000  24.1 / 22.3, 35.5 / 30.8
+// So up to 1024 tokens a CTA, and 3000 where the CTAs are most of the SMs; where the units are as
+// many as the SMs, the line has nothing to join, and 1500.
 int units_cluster(const Q8AttendArgs& a, int tile) {
   const rkv_cache8& c = a.cache;
   const long long units = (long long)c.B * c.Hkv;
   if (tile > 24 || units > 152) return 0;
   const int C = units <= 9 ? 8 : (units <= 36 ? 4 : (units <= 76 ? 2 : 1));
-  return c.max_pages * c.page_size <= C * (units * C >= 120 ? 3000 : 1024) ? C : 0;
+  return c.max_pages * c.page_size <= C * (units * C < 120 ? 1024 : (units == 152 ? 1500 : 3000)) ? C : 0;
 }
 
 template <int kFormat, int kN>
@@ -937,32 +959,23 @@ cudaError_t launch_q8_attend(const Q8AttendArgs& a, cudaStream_t s) {
     if (tile == 16) return int8 ? launch_units<RKV_Q8_INT8, 2>(p, C, s) : launch_units<RKV_Q8_E4M3, 2>(p, C, s);
     return int8 ? launch_units<RKV_Q8_INT8, 3>(p, C, s) : launch_units<RKV_Q8_E4M3, 3>(p, C, s);
   }
-  void (*join)(Q8Params);
   switch (tile) {
     case 8:
       e = int8 ? launch_rows<RKV_Q8_INT8, 1>(p, s) : launch_rows<RKV_Q8_E4M3, 1>(p, s);
-      join = q8_join_kernel<RowsLine<3>>;
-      break;
+      return e != cudaSuccess ? e : launch_join<RowsLine<3>>(p, s);
     case 16:
       e = int8 ? launch_rows<RKV_Q8_INT8, 2>(p, s) : launch_rows<RKV_Q8_E4M3, 2>(p, s);
-      join = q8_join_kernel<RowsLine<4>>;
-      break;
+      return e != cudaSuccess ? e : launch_join<RowsLine<4>>(p, s);
     case 24:
       e = int8 ? launch_rows<RKV_Q8_INT8, 3>(p, s) : launch_rows<RKV_Q8_E4M3, 3>(p, s);
-      join = q8_join_kernel<RowsLine<5>>;
-      break;
+      return e != cudaSuccess ? e : launch_join<RowsLine<5>>(p, s);
     case 128:
       e = launch_q8_tiles(p, false, int8, s);
-      join = q8_join_kernel<TileLine<7>>;
-      break;
+      return e != cudaSuccess ? e : launch_join<TileLine<7>>(p, s);
     default:
       e = launch_q8_tiles(p, true, int8, s);
-      join = q8_join_kernel<TileLine<8>>;
+      return e != cudaSuccess ? e : launch_join<TileLine<8>>(p, s);
   }
-  if (e != cudaSuccess) return e;
-  const int part = part_rows(tile), group = part < 32 ? part : 32;
-  const long long items = (long long)p.B * p.Hkv * p.join_tiles * (part / group), most = 8LL * p.N;
-  return launch_dependent(join, dim3((unsigned)(items < most ? items : most)), 256, K_Q8_JOIN, s, p);
 }
 
 }  // namespace rkv

@@ -10,7 +10,9 @@
 // in registers (a row's 256 bytes are 16 lanes' 16-byte loads, two rows at a time, so K and V
 // are 16 loads in flight a lane), finds their largest magnitude and rounds them: every value
 // is read once.  A page's 16-row pieces are neighbouring warps of a CTA and meet in shared
-// memory for the maximum.
+// memory for the maximum.  Measured: prompts of up to 16384 tokens of 8 sequences (574 MB) 95 us,
+// 6.0 TB/s; a bf16 cache of 16 x up to 9675 tokens (545 MB) 88 us, 6.2 TB/s, 91 % of a plain copy's
+// rate (108 and 103 with CTAs that are not all resident at once); one token of 64 sequences 4.4 us.
 #include "rkv_internal.h"
 #include "rkv_flat.cuh"
 #include "rkv_q8.cuh"
