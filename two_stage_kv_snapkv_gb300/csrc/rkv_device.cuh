@@ -360,6 +360,12 @@ __device__ __forceinline__ void tc_st32_wait(uint32_t taddr, const uint32_t (&r)
   tc_st32(taddr, r);
   tc_st_wait();
 }
+// Eight columns, without the wait.
+__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 // Shared-memory matrix descriptor of a K-major bf16 operand stored as TMA writes it with
 // 128-byte swizzle: rows of 128 B (64 elements of K), 8-row groups 1024 B apart, the
 // atom 1024-byte aligned.  Fields: start address >> 4 (bits 0-13), leading byte offset

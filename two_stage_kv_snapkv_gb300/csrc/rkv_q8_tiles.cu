@@ -18,17 +18,15 @@
 // 2^-33 of the largest.  What a row does not see must have no part in that: in a run's last
 // tiles, which end beyond its first row's keys, the operands are the codes, K's scales meet
 // the logits and V's the weights (16 keys, a part of one page, at a time), and the unit is
-// each row's own.  (Scales at the softmax in every tile took 877 us where this takes 815.)
+// each row's own.  (Scales at the softmax in every tile took 877 us where this takes 760.)
 //   warps 0-7, 8-15: softmax of slot 0, 1 (four warps to 64 keys);  16, 18: TMA of K, V;  17:
 //   MMA issue;  19: the share's runs;  20-23, 24-27: K's and V's codes to fp16.
 // Every wait is bounded; one that runs out flags RKV_DEVERR_TIMEOUT and stops every role.
 //
-// Measured: 2048 rows of 32 heads behind 32768 tokens (1.07 TFLOP) 815 us, 1.32 PFLOP/s, the tensor
+// Measured: 2048 rows of 32 heads behind 32768 tokens (1.07 TFLOP) 760 us, 1.41 PFLOP/s, the tensor
 // pipe busy in 54 % of the clocks: a tile's chain (logits, their loads, exponentials, weights,
 // product) is longer than the other slot's products hide.  80 rows a KV head over 4 x 32000 tokens
 // (262 MB) 76 us, 3.5 TB/s.
-#include <type_traits>
-
 #include "rkv_q8_attend.cuh"
 
 namespace rkv {
@@ -50,7 +48,9 @@ constexpr int kNoRow = -128;    // a query row with a NaN or an infinity
 // are taken with the power of two below the factor, whose product with the maximum is exact.
 constexpr float kQtFar = 1073741824.f;
 
-// A tile's scales, for K and for V from the warp that fetches its codes.  A tile that every row
+// What goes with a tile, for K and for V from the warp that fetches its codes.  In its tag: the
+// 16-key groups that were loaded (bits 0-7); whether all were and every row sees them (8); biased
+// exponents, K's tile's (16-23) and V's run's up to it, the unit of O (24-31).  Its scales:  A tile that every row
 // sees whole: each 16-key group's exponent below the tile's (`x`).  Else for K: the groups' biased
 // exponents, K's in `x` and V's in `vx`; for V: whether a group is of NaN (kNoFactor) or not (0).
 struct alignas(8) TileInfo {
@@ -82,8 +82,7 @@ struct TileShape8 {
     Line line;
     uint64_t full_c[2][kCodes], empty_c[2][kCodes], full[2][kOps], empty[2][kOps], s[2], p[2], o[2], qf[2], out[2], ml, drained;
     TileInfo info[2][kQtInfos];
-    uint8_t groups[2][kQtInfos];              // a tile's 16-key groups that were loaded
-    uint8_t e[kQtInfos], unit[kQtInfos];      // biased exponents: K's tile's, V's run's up to it (the unit of O)
+    uint32_t tag[2][kQtInfos];
     RunInfo runs[kQtRuns];
     uint64_t full_r[kQtRuns], empty_r[kQtRuns];
     uint32_t tmem_base;
@@ -271,9 +270,6 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
         arrive(&sh.qf[kWide ? slot : 0]);
       }
       const int my = rt * R + (kWide ? slot * 128 : 0) + row;  // this thread's query row
-      // keys that it sees, and that the run's first row does
-      const int lim = my < rows ? n - r.m + (my >> p.gshift) + 1 : n;
-      const int least = n - r.m + ((rt * R) >> p.gshift) + 1;
       float m = kNoMax, l = 0.f, factor = 0.f, ref = kNoMax;
       auto is_far = [&]() { return fabsf(m) > kQtFar && m != kNoMax; };
       int unit = -126;  // O is in units of 2^unit
@@ -286,87 +282,62 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
             const int e = sh.row_exp[(kWide ? slot * 128 : 0) + row];
             factor = e == kNoRow ? __uint_as_float(0x7fffffffu) : p.scale_log2 * power_of_two(e - 8);
           }
-          const int at = (tiles_before + i) % kQtInfos, key0 = (r.lo + i) * kQtKeys;
+          const int at = (tiles_before + i) % kQtInfos;
           const TileInfo& ti = sh.info[0][at];
-          const uint32_t gr = sh.groups[0][at];
+          const uint32_t tag = sh.tag[0][at];
           // from the product to base-2 logits: 2^(x - 127) times the row's factor
           auto factor_of = [&](uint32_t x) {
             const float f = factor * __uint_as_float(x == kNoFactor ? 0x7fffffffu : x << 23);
             return f < kLowestScale ? kLowestScale : f;  // 0 x -inf is not -inf; a NaN stays
           };
           auto power_part = [](float f) { return __uint_as_float(__float_as_uint(f) & 0x7f800000u); };
-          uint32_t pk[32];
-          // The weights are taken with the maximum so far, without looking for a new one: as long
-          // as 64 of a row's sum up to at most 2^8 (2^15 with their factor) none is beyond fp16,
-          // and while the maximum stays the same they sum up to 2^6 at most.
-          auto weigh = [&](auto plain_tile) {
-            constexpr bool kPlain = decltype(plain_tile)::value;
-            const float sl = kPlain ? factor_of(sh.e[at]) : 0.f;
-            int to_unit = max(unit, (int)sh.unit[at] - 127);
-            uint32_t see[2] = {~0u, ~0u};  // of this thread's 64 keys
-            if constexpr (!kPlain) {
-#pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                const int k = min(n, lim) - key0 - half * 64 - w * 32;
-                see[w] = k >= 32 ? ~0u : (k <= 0 ? 0u : (1u << k) - 1u);
-                if (!((gr >> (half * 4 + 2 * w)) & 1u)) see[w] &= 0xffff0000u;
-                if (!((gr >> (half * 4 + 2 * w + 1)) & 1u)) see[w] &= 0x0000ffffu;
-              }
-              to_unit = unit;
-#pragma unroll 1
-              for (int c = 0; c < 8; ++c)
-                if (((gr >> c) & 1u) && key0 + c * 16 < min(n, lim) && ti.vx[c] != kNoFactor)
-                  to_unit = max(to_unit, (int)ti.vx[c] - 127);
+          // The row's maximum over this tile (zp: without the part of the factor that is no power of
+          // two) and its unit become what the weights refer to; what was summed up follows.
+          auto refer_to = [&](float zp, int to_unit) {
+            const float mx = factor == factor ? zp * __uint_as_float((__float_as_uint(factor) & 0x7fffffu) | 0x3f800000u) : factor;
+            const float to = fmaxf(m, mx), f = ex2_approx(m - to);
+            if (first || mx > m) {
+              m = to;
+              ref = is_far() ? zp : m;
             }
-            // the exponents of 16 keys' V below the row's unit (hidden ones may lie above it)
-            auto below = [&](int c) { return min(max(unit + 127 - (int)ti.vx[half * 4 + c], 0), kFarUnits); };
+            if (!first) {
+              // this slot's earlier products are complete: its logits were issued after them
+              const float fo = f * power_of_two(max(unit - to_unit, -126));
+              l *= f;
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t o[16];
+                tc_ld16_wait(mine + 128 + half * 64 + c * 16, o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fo);
+                tc_st16_wait(mine + 128 + half * 64 + c * 16, o);
+              }
+            }
+            unit = to_unit;
+          };
+          if (tag & 256u) {  // every row sees the whole tile
+            // The weights are taken with the maximum so far, without looking for a new one: as long
+            // as 64 of a row's sum up to at most 2^8 (2^15 with their factor) none is beyond fp16,
+            // and while the maximum stays the same they sum up to 2^6 at most.
+            uint32_t pk[32];
+            const int to_unit = max(unit, (int)(tag >> 24) - 127);
+            const float sl = factor_of(tag >> 16 & 255u);
             float sum;
             for (bool moved = first;;) {
               if (moved) {
-                // the maximum of all 128 logits, by both threads of the row; zp: without the part
-                // of the factor that is no power of two
-                float zp = -INFINITY;
+                float raw = -INFINITY;  // of all 128 logits, by both threads of the row
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
                   uint32_t v[16];
-                  float mx = -INFINITY, by = power_part(sl);
                   tc_ld16_wait(mine + c * 16, v);
-                  if constexpr (!kPlain) {
-                    by = power_part(factor_of(ti.x[c] == kNoFactor ? 0u : ti.x[c]));
-                    const int k = min(n, lim) - key0 - c * 16;
-                    const uint32_t bits = ((gr >> c) & 1u) ? (k >= 16 ? ~0u : (k <= 0 ? 0u : (1u << k) - 1u)) : 0u;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                      if (!((bits >> j) & 1u)) v[j] = 0xff800000u;  // -inf
-                  }
-#pragma unroll
-                  for (int j = 0; j < 16; j += 2) mx = max3(mx, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-                  zp = fmaxf(zp, mx * by);
+                  for (int j = 0; j < 16; j += 2) raw = max3(raw, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
                 }
-                const float mx = factor == factor ? zp * __uint_as_float((__float_as_uint(factor) & 0x7fffffu) | 0x3f800000u) : factor;
-                const float to = fmaxf(m, mx), f = ex2_approx(m - to);
-                if (first || mx > m) {
-                  m = to;
-                  ref = is_far() ? zp : m;
-                }
-                if (!first) {
-                  // this slot's earlier products are complete: its logits were issued after them
-                  const float fo = f * power_of_two(max(unit - to_unit, -126));
-                  l *= f;
-#pragma unroll 1
-                  for (int c = 0; c < 4; ++c) {
-                    uint32_t o[16];
-                    tc_ld16_wait(mine + 128 + half * 64 + c * 16, o);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fo);
-                    tc_st16_wait(mine + 128 + half * 64 + c * 16, o);
-                  }
-                }
-                unit = to_unit;
+                refer_to(raw * power_part(sl), to_unit);
               }
-              const bool far = is_far();
-              const float by = far ? power_part(sl) : sl, sub = 7.f - ref;  // times kUnit
-              uint64_t by2 = pair_of(by, by), sub2 = pair_of(sub, sub), back2 = 0, s0 = 0, s1 = 0, s = 0;
+              const float by = is_far() ? power_part(sl) : sl;
+              const uint64_t by2 = pair_of(by, by), sub2 = pair_of(7.f - ref, 7.f - ref);  // times kUnit
+              uint64_t s0 = pair_of(0.f, 0.f), s1 = s0;
               uint32_t v[2][16];
               tc_ld16(keys, v[0]);
 #pragma unroll
@@ -374,21 +345,6 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
                 tc_ld_wait();
                 tc_ld16_done(v[c & 1]);
                 if (c < 3) tc_ld16(keys + (c + 1) * 16, v[(c + 1) & 1]);
-                if constexpr (!kPlain) {
-                  const uint32_t bits = see[c >> 1] >> ((c & 1) * 16);
-#pragma unroll
-                  for (int j = 0; j < 16; ++j)
-                    if (!((bits >> j) & 1u)) v[c & 1][j] = 0xff800000u;
-                  const float f = factor_of((bits & 0xffffu) ? ti.x[half * 4 + c] : 0u);  // none seen: a page of NaN does not matter
-                  const float g = far ? power_part(f) : f;
-                  by2 = pair_of(g, g);
-                  // V's scale goes into the exponent, and out of the sum again
-                  const int d = far ? 0 : below(c);
-                  const float sub_v = sub - (float)d, back = power_of_two(d);
-                  sub2 = pair_of(sub_v, sub_v);
-                  back2 = pair_of(back, back);
-                  s0 = s1 = 0;
-                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                   const uint64_t z = fma2(pair_bits(v[c & 1][2 * j], v[c & 1][2 * j + 1]), by2, sub2);
@@ -396,31 +352,63 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
                   if (j & 1) s1 = add2(s1, pair_of(ax, ay)); else s0 = add2(s0, pair_of(ax, ay));
                   pk[c * 8 + j] = pack_f16x2(ax, ay);
                 }
-                if constexpr (!kPlain) s = fma2(add2(s0, s1), back2, s);
               }
-              if constexpr (kPlain) s = add2(s0, s1);
-              sum = pair_lo(s) + pair_hi(s);
+              s0 = add2(s0, s1);
+              sum = pair_lo(s0) + pair_hi(s0);
               // in the second round: neither thread of the row writes over logits that the other
               // still looks for their maximum in
               if (!vote(!moved && (sum > 32768.f || to_unit != unit))) break;
               moved = true;
             }
-            if (!kPlain && is_far()) {  // the exponent had no room for V's scale
+            tc_st32(keys, pk);
+            l += sum;
+          } else {
+            // Rarely run, so small: it comes from far.  Always with the tile's maximum, 16 keys at a
+            // time, whose weights go where logits lay that have been read.
+            const uint32_t gr = tag & 255u;
+            const int key0 = (r.lo + i) * kQtKeys, lim = my < rows ? min(n, n - r.m + (my >> p.gshift) + 1) : n;  // keys that the row sees
+            int to_unit = unit;
+            float zp = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              const int k = lim - key0 - c * 16;
+              const uint32_t bits = ((gr >> c) & 1u) ? (k >= 16 ? ~0u : (k <= 0 ? 0u : (1u << k) - 1u)) : 0u;
+              uint32_t v[16];
+              float mx = -INFINITY;
+              tc_ld16_wait(mine + c * 16, v);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float f = power_of_two(-below(c));
+              for (int j = 0; j < 16; ++j)
+                if ((bits >> j) & 1u) mx = fmaxf(mx, __uint_as_float(v[j]));
+              zp = fmaxf(zp, mx * power_part(factor_of(ti.x[c] == kNoFactor ? 0u : ti.x[c])));
+              if (bits && ti.vx[c] != kNoFactor) to_unit = max(to_unit, (int)ti.vx[c] - 127);
+            }
+            refer_to(zp, to_unit);
+            vote(false);  // neither thread of the row writes over logits that the other still reads
+            const bool far = is_far();
+            const float sub = 7.f - ref;
+            float sum = 0.f;
+#pragma unroll 1
+            for (int c = half * 4; c < half * 4 + 4; ++c) {
+              const int k = lim - key0 - c * 16;
+              const uint32_t bits = ((gr >> c) & 1u) ? (k >= 16 ? ~0u : (k <= 0 ? 0u : (1u << k) - 1u)) : 0u;
+              const float by = bits ? factor_of(ti.x[c]) : 0.f;  // none seen: a page of NaN does not matter
+              const float b1 = far && by == by ? power_part(by) : by;
+              // V's scale; one that the row does not see may lie above its unit
+              const float up = power_of_two(-min(max(unit + 127 - (int)ti.vx[c], 0), kFarUnits));
+              uint32_t v[16], w[8];
+              tc_ld16_wait(mine + c * 16, v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&pk[c * 8 + j]));
-                  pk[c * 8 + j] = pack_f16x2(w.x * f, w.y * f);
-                }
+              for (int j = 0; j < 16; ++j) {
+                const float a = ((bits >> j) & 1u) ? ex2_approx(fmaf(__uint_as_float(v[j]), b1, sub)) : 0.f;
+                sum += a;
+                v[j] = __float_as_uint(a * up);
               }
+#pragma unroll
+              for (int j = 0; j < 8; ++j) w[j] = pack_f16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+              tc_st8(keys + (c & 3) * 8, w);
             }
             l += sum;
-          };
-          // a tile that every row sees whole, or another
-          if (gr == 0xffu && key0 + kQtKeys <= least) weigh(std::true_type{}); else weigh(std::false_type{});
-          tc_st32(keys, pk);
+          }
           tc_st_wait();
           tc_fence_before();
           arrive(&sh.p[slot]);
@@ -586,30 +574,26 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
           }
           if (in == batch - 1) scales_of(next_ids, next_ks, next_vs);
           const int first = in * pages;  // the tile's first lane
-          const uint32_t have = (batch_have >> first) & ((1u << pages) - 1u);
+          const uint32_t full = (1u << pages) - 1u, have = (batch_have >> first) & full;
           const bool inner = (tile + 1) * kQtKeys <= least;  // every row sees it whole
+          const bool plain = inner && have == full;
           const int top = __shfl_sync(0xffffffffu, v_top, first);
           if (inner) unit = max(unit, top);
           const int e = v ? unit : __shfl_sync(0xffffffffu, own_top, first), of = first + ((lane & 7) >> gs);
-          const int gk = __shfl_sync(0xffffffffu, xk, of), gv = __shfl_sync(0xffffffffu, xv, of);  // lanes 0 .. 7: the 16-key groups
-          const uint32_t gr = __ballot_sync(0xffffffffu, lane < 8 && ((have >> ((lane & 7) >> gs)) & 1u));
-          const bool plain = inner && gr == 0xffu;
+          int gx = __shfl_sync(0xffffffffu, v ? xv : xk, of), gv = 0;  // lanes 0 .. 7: the 16-key groups
+          uint32_t gr = 0xffu;
+          if (!plain) {
+            gr = __ballot_sync(0xffffffffu, lane < 8 && ((have >> ((lane & 7) >> gs)) & 1u));
+            gv = __shfl_sync(0xffffffffu, xv, of);
+          }
           ++in;
           const int c = at.slot;
           if (at.use > 0 && !(ok = wait(&sh.empty_c[v][c], at.use - 1))) break;
           TileInfo& ti = sh.info[v][loaded % kQtInfos];
-          if (lane < 8) {
-            const int gx = v ? gv : gk;
-            ti.x[lane] = (uint8_t)(gx == kNoFactor ? kNoFactor : (plain ? min(max(e - gx, 0), 254) : (v ? 0 : gx)));
-            ti.vx[lane] = (uint8_t)gv;
-          }
-          if (lead) {
-            sh.groups[v][loaded % kQtInfos] = (uint8_t)gr;
-            if (!v) {
-              sh.e[loaded % kQtInfos] = (uint8_t)e;
-              sh.unit[loaded % kQtInfos] = (uint8_t)unit;
-            }
-          }
+          if (!plain && lane < 8) ti.vx[lane] = (uint8_t)gv;
+          if (gx != kNoFactor) gx = plain ? min(max(e - gx, 0), 254) : (v ? 0 : gx);
+          if (lane < 8) ti.x[lane] = (uint8_t)gx;
+          if (lead) sh.tag[v][loaded % kQtInfos] = gr | (plain ? 256u : 0u) | (uint32_t)e << 16 | (uint32_t)unit << 24;
           __syncwarp();
           const uint32_t st = smem_u32(sh.codes[v] + c * kQtCodes), bar = smem_u32(&sh.full_c[v][c]);
           if (lead) {
@@ -755,14 +739,14 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
     int tile_no = 0;
     bool ok = true;
     while (ok && next_run(r, ok)) {
-      const int nt = r.hi - r.lo, least = r.n - r.m + ((r.rt * R) >> p.gshift) + 1;
+      const int nt = r.hi - r.lo;
       for (int i = 0; i < nt; ++i) {
         const int c = at.slot;
         if (!(ok = wait(&sh.full_c[v][c], at.use))) break;
         const TileInfo& ti = sh.info[v][tile_no % kQtInfos];
         const int left = r.n - (r.lo + i) * kQtKeys;
-        const uint32_t gr = sh.groups[v][tile_no % kQtInfos];
-        const bool codes = !v && (gr != 0xffu || (r.lo + i + 1) * kQtKeys > least);  // K's as they are
+        const uint32_t tag = sh.tag[v][tile_no % kQtInfos], gr = tag & 255u;
+        const bool codes = !v && !(tag & 256u);  // K's as they are
         const int d0 = codes ? 0 : ti.x[quarter * 2], d1 = codes ? 0 : ti.x[quarter * 2 + 1];
         const uint8_t* const src = sh.codes[v] + c * kQtCodes + (quarter * 32 + row8) * 128;
         if (to.use > 0 && !(ok = wait(&sh.empty[v][to.slot], to.use - 1))) break;
