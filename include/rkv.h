@@ -670,8 +670,9 @@ size_t rkv_q8_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int3
 
 /*
  * Attention of the last rows over the 8-bit cache: one decoded token, a chain of drafted ones,
- * a prompt's chunk, whose keys and values are in the cache already (rkv_q8_append first).  The m = row_len[b] rows
- * are the cache's last m positions, row i lying at position n - m + i (n = seq_len[b]) and seeing t <= n - m + i:
+ * a prompt's chunk, whose keys and values are in the cache already (rkv_q8_append first).
+ * The m = row_len[b] rows are the cache's last m positions, row i lying at position n - m + i
+ * (n = seq_len[b]) and seeing t <= n - m + i:
  *   z_t = scale * q[b][h][i] . k_t,  out = sum_t exp(z_t) v_t / sum_t exp(z_t),  lse = log sum_t exp(z_t)
  * with k_t, v_t the values that the codes stand for.  A row that sees nothing (n = 0, or
  * i < m - n) gets out = 0 and lse = -inf; one with a NaN among its logits gets NaN for both.
@@ -681,9 +682,10 @@ size_t rkv_q8_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t T, int3
  *             RKV_DEVERR_TREE and counts as 0.
  *   out     : device [B][Hq][T][128] bf16.   lse : device [B][Hq][T] fp32 or NULL.
  * Logits, maxima, sums and the output's accumulation are fp32; queries, codes and softmax
- * weights enter the products as fp16 (see rkv_q8_attend.cu for what that rounds).  Lengths
- * are read on the device, so a captured call can be replayed as the cache grows; scale,
- * workspaces and unreadable pages as for rkv_tree_attention.
+ * weights enter the products as fp16 (see rkv_q8_attend.cu for what that rounds).  The scales
+ * of pages that a row sees no key of have no part in its result.  Lengths are read on the
+ * device, so a captured call can be replayed as the cache grows; scale, workspaces and
+ * unreadable pages as for rkv_tree_attention.
  */
 rkv_status rkv_q8_attention(const rkv_cache8* cache, const rkv_bf16* q, int32_t Hq, int32_t T,
                             const int32_t* row_len, float scale, rkv_bf16* out, float* lse, void* workspace,

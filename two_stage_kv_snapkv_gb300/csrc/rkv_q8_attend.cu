@@ -22,8 +22,8 @@
 // per SM) that one of four more warps fills by TMA, its own running maximum, sum and fp32
 // output, and meet once per run.  The parts of a split unit go to the workspace and q8_join
 // joins them.  Measured, 16 x 8K..32K tokens of 8 KV heads (601 MB): 4 query rows 92 us, 6.5 TB/s,
-// the rate of a plain copy 96 %; 20 rows 121 us (a chunk's chain of loads, products and
-// exponentials on two warps a scheduler, which issue in 37 % of the clocks).
+// 96 % of a plain copy's rate; 20 rows 121 us (a chunk's chain of loads, products and
+// exponentials, on two warps a scheduler).
 #include <cooperative_groups.h>
 
 #include <type_traits>

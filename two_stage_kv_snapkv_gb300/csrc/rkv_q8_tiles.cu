@@ -50,9 +50,10 @@ constexpr float kQtFar = 1073741824.f;
 
 // What goes with a tile, for K and for V from the warp that fetches its codes.  In its tag: the
 // 16-key groups that were loaded (bits 0-7); whether all were and every row sees them (8); biased
-// exponents, K's tile's (16-23) and V's run's up to it, the unit of O (24-31).  Its scales:  A tile that every row
-// sees whole: each 16-key group's exponent below the tile's (`x`).  Else for K: the groups' biased
-// exponents, K's in `x` and V's in `vx`; for V: whether a group is of NaN (kNoFactor) or not (0).
+// exponents, K's tile's (16-23) and V's run's up to it, the unit of O (24-31).  Its scales: in a
+// tile that every row sees whole, each group's exponent below the tile's (`x`).  Else for K: the
+// groups' biased exponents, K's in `x` and V's in `vx`; for V: whether a group is of NaN
+// (kNoFactor) or not (0).
 struct alignas(8) TileInfo {
   uint8_t x[8], vx[8];
 };
