@@ -187,6 +187,23 @@ def test_pages_of_nan_reach_who_sees_them_alone(rkv, T, P):
             assert ((out[b, h, idx].double() - ref).abs() <= 2.0 ** -6 * (torch.softmax(zz, 1) @ V[b][h // 4].abs()) + 1e-6).all()
 
 
+@pytest.mark.parametrize("T", [1, 3, 6, 40, 200])
+@pytest.mark.parametrize("page", [2, 20])
+def test_pages_of_nan_among_logits_far_from_zero(rkv, T, page):
+    """Logits beyond 2^30 of either sign: a page of NaN makes every row that sees it NaN, none else."""
+    n, P = 330, 16
+    cache, K, V = C.filled(rkv, [n], 2, P, "e4m3", seed=T)
+    ph = cache.page_table[0, page].long()
+    cache.k_scale[ph] = math.nan
+    cache.v_scale[ph] = math.nan
+    q = _queries(1, 8, T, seed=T)
+    q[:, 1::2] = -q[:, ::2]
+    out, lse = _run(rkv, cache, q, scale=2.0 ** 34)
+    sees = torch.arange(T, device="cuda") + n - T >= page * P
+    assert torch.isnan(out[0, :, sees]).all() and torch.isnan(lse[0, :, sees]).all()
+    assert torch.isfinite(out[0, :, ~sees]).all() and torch.isfinite(lse[0, :, ~sees]).all()
+
+
 @pytest.mark.parametrize("which", ["k", "v", "kv"])
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("T,n,P,at,room", [
