@@ -24,9 +24,9 @@
 // Every wait is bounded; one that runs out flags RKV_DEVERR_TIMEOUT and stops every role.
 //
 // Measured: 2048 rows of 32 heads behind 32768 tokens (1.07 TFLOP) 760 us, 1.41 PFLOP/s, the tensor
-// pipe busy in 54 % of the clocks: a tile's chain (logits, their loads, exponentials, weights,
+// pipe busy in 55 % of the clocks: a tile's chain (logits, their loads, exponentials, weights,
 // product) is longer than the other slot's products hide.  80 rows a KV head over 4 x 32000 tokens
-// (262 MB) 76 us, 3.5 TB/s.
+// (262 MB) 77 us, 3.4 TB/s.
 #include "rkv_q8_attend.cuh"
 
 namespace rkv {
