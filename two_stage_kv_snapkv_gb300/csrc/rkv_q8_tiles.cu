@@ -18,15 +18,15 @@
 // 2^-33 of the largest.  What a row does not see must have no part in that: in a run's last
 // tiles, which end beyond its first row's keys, the operands are the codes, K's scales meet
 // the logits and V's the weights (16 keys, a part of one page, at a time), and the unit is
-// each row's own.  (Scales at the softmax in every tile took 877 us where this takes 760.)
+// each row's own.  (Scales at the softmax in every tile took 877 us where this form then took 817, now 716.)
 //   warps 0-7, 8-15: softmax of slot 0, 1 (four warps to 64 keys);  16, 18: TMA of K, V;  17:
 //   MMA issue;  19: the share's runs;  20-23, 24-27: K's and V's codes to fp16.
 // Every wait is bounded; one that runs out flags RKV_DEVERR_TIMEOUT and stops every role.
 //
-// Measured: 2048 rows of 32 heads behind 32768 tokens (1.07 TFLOP) 760 us, 1.41 PFLOP/s, the tensor
+// Measured: 2048 rows of 32 heads behind 32768 tokens (1.07 TFLOP) 716 us, 1.50 PFLOP/s, the tensor
 // pipe busy in 55 % of the clocks: a tile's chain (logits, their loads, exponentials, weights,
 // product) is longer than the other slot's products hide.  80 rows a KV head over 4 x 32000 tokens
-// (262 MB) 77 us, 3.4 TB/s.
+// (262 MB) 71 us, 3.7 TB/s.
 #include "rkv_q8_attend.cuh"
 
 namespace rkv {
@@ -34,9 +34,10 @@ namespace {
 
 constexpr int kQtKeys = 1 << kQtKeysShift;
 constexpr int kQtThreads = 896;
-// Registers: 896 threads start with 72 each; the softmax warps take 88, the fifth warpgroup
-// (TMA, MMA) 56 and the last two 48: 512 x 88 + 128 x 56 + 256 x 48 = 896 x 72.
-constexpr int kQtSoftRegs = 88, kQtIssueRegs = 56, kQtCodeRegs = 48;
+// Registers: 896 threads start with 72 each; the softmax warps take 80, the fifth warpgroup
+// (TMA, MMA) keeps its 72 and the last two give 16 away: 512 x 80 + 128 x 72 + 256 x 56 = 896 x
+// 72.  (With 88, 56 and 48 the last three spilled.)
+constexpr int kQtSoftRegs = 80, kQtIssueRegs = 72, kQtCodeRegs = 56;
 static_assert(512 * kQtSoftRegs + 128 * kQtIssueRegs + 256 * kQtCodeRegs == 896 * 72,
               "the split must be what the block was launched with");
 constexpr int kQtTile = kQtKeys * 256, kQtCodes = kQtKeys * 128;
@@ -521,7 +522,6 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
     }
     if (!ok) asm volatile("barrier.cta.arrive %0, 64;\n" ::"r"(pr + 1) : "memory");
   } else if (warp < 20) {
-    setmaxnreg_dec<kQtIssueRegs>();
     if (warp == 16 || warp == 18) {
       const bool v = warp == 18;
       const CUtensorMap* map = v ? &p.tmv : &p.tmk;
