@@ -18,15 +18,16 @@
 // 2^-33 of the largest.  What a row does not see must have no part in that: in a run's last
 // tiles, which end beyond its first row's keys, the operands are the codes, K's scales meet
 // the logits and V's the weights (16 keys, a part of one page, at a time), and the unit is
-// each row's own.  (Scales at the softmax in every tile took 877 us where this form then took 817, now 716.)
+// each row's own.  (Scales at the softmax in every tile took 877 us where two forms of tiles
+// first took 817; by now 716.)
 //   warps 0-7, 8-15: softmax of slot 0, 1 (four warps to 64 keys);  16, 18: TMA of K, V;  17:
 //   MMA issue;  19: the share's runs;  20-23, 24-27: K's and V's codes to fp16.
 // Every wait is bounded; one that runs out flags RKV_DEVERR_TIMEOUT and stops every role.
 //
 // Measured: 2048 rows of 32 heads behind 32768 tokens (1.07 TFLOP) 716 us, 1.50 PFLOP/s, the tensor
-// pipe busy in 55 % of the clocks: a tile's chain (logits, their loads, exponentials, weights,
+// pipe busy in 58 % of the clocks: a tile's chain (logits, their loads, exponentials, weights,
 // product) is longer than the other slot's products hide.  80 rows a KV head over 4 x 32000 tokens
-// (262 MB) 71 us, 3.7 TB/s.
+// (262 MB) 72 us, 3.6 TB/s.
 #include "rkv_q8_attend.cuh"
 
 namespace rkv {
