@@ -369,7 +369,8 @@ __global__ void __launch_bounds__(kQtThreads, 1) q8_tiles_kernel(const __grid_co
             // Rarely run, so small: it comes from far.  Always with the tile's maximum, 16 keys at a
             // time, whose weights go where logits lay that have been read.
             const uint32_t gr = tag & 255u;
-            const int key0 = (r.lo + i) * kQtKeys, lim = my < rows ? min(n, n - r.m + (my >> p.gshift) + 1) : n;  // keys that the row sees
+            const int key0 = (r.lo + i) * kQtKeys;
+            const int lim = my < rows ? min(n, n - r.m + (my >> p.gshift) + 1) : n;  // keys that the row sees
             int to_unit = unit;
             float zp = -INFINITY;
 #pragma unroll 1
